@@ -444,3 +444,12 @@ __all__ = [n for n in EXPORTS] + ["MoEError", "moe_shape", "make_shape", "load_l
                                    "MOE_GATE_TOPK_SOFTMAX", "MOE_GATE_SOFTMAX_TOPK",
                                    "MOE_GATE_SOFTMAX_TOPK_RENORM", "MOE_EXPERT_GELU",
                                    "MOE_EXPERT_SWIGLU"]
+
+from .decode import (DECODE_EXPORTS, MOED_MAX_ROWS, MOED_MAX_TOKENS, MoEDecodeLayer,  # noqa: E402
+                     Q4Weights, dequantize_q4, matvec_q4, moed_dequantize_q4, moed_forward,
+                     moed_forward_q4, moed_matvec_q4, moed_matvec_q4_workspace_size,
+                     moed_quantize_q4, moed_workspace_size, quantize_q4)
+
+__all__ += [n for n in DECODE_EXPORTS] + ["DECODE_EXPORTS", "MOED_MAX_ROWS", "MOED_MAX_TOKENS",
+                                          "MoEDecodeLayer", "Q4Weights", "dequantize_q4",
+                                          "matvec_q4", "quantize_q4"]

@@ -18,8 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "router.cu", "route_fused.cu", "dispatch_combine.cu", "ffn_gemm.cu",
-           "ffn_gemm_small.cu"]
-HEADERS = ["tc_common.cuh", "moe_internal.h", "route_topk.cuh"]
+           "ffn_gemm_small.cu", "decode_api.cu", "decode_route.cu", "decode_ffn.cu", "q4.cu"]
+HEADERS = ["tc_common.cuh", "moe_internal.h", "api_internal.h", "decode_internal.h", "route_topk.cuh"]
+INCLUDES = ["moe.h", "moe_decode.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,8 +43,8 @@ def _stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, "moe.h"),
-                                                                  os.path.abspath(__file__)]
+    deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS] + [os.path.join(INCLUDE, h) for h in INCLUDES]
+    deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -10,6 +10,7 @@
 
 #include <mutex>
 
+#include "api_internal.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -18,6 +19,7 @@ cudaError_t small_gemm_set_attributes();
 cudaError_t router_set_attributes();
 cudaError_t route_fused_set_attributes();
 cudaError_t dispatch_combine_set_attributes();
+cudaError_t decode_set_attributes();
 }  // namespace moe
 
 using namespace moe;
@@ -25,6 +27,10 @@ using namespace moe;
 namespace {
 
 thread_local char g_err[512] = "";
+
+}  // namespace
+
+namespace moe {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -38,6 +44,10 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(MOE_ERR_CUDA, "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
 }
 
+}  // namespace moe
+
+namespace {
+
 // ---------------------------------------------------------------- device --
 
 constexpr int kMaxDevices = 64;
@@ -48,6 +58,10 @@ struct DeviceInfo {
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
+
+namespace moe {
 
 int device_setup(int* sms) {
   int dev = 0;
@@ -69,6 +83,7 @@ int device_setup(int* sms) {
     if ((e = small_gemm_set_attributes()) != cudaSuccess) return cuda_fail(e, "gemm attributes");
     if ((e = dispatch_combine_set_attributes()) != cudaSuccess)
       return cuda_fail(e, "dispatch/combine attributes");
+    if ((e = decode_set_attributes()) != cudaSuccess) return cuda_fail(e, "decode attributes");
     if (!g_encode) {
       void* fn = nullptr;
       cudaDriverEntryPointQueryResult q;
@@ -84,16 +99,26 @@ int device_setup(int* sms) {
   return MOE_OK;
 }
 
+int encode_map_as(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle,
+                  const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                  const uint32_t* box, const char* what) {
+  uint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides_bytes, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+namespace {
+
 // bf16 tensor map, 128-byte swizzle, zero fill out of bounds.
 int encode_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                const uint64_t* strides_bytes, const uint32_t* box, const char* what) {
-  uint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base),
-                        dims, strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
-  return MOE_OK;
+  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank,
+                       dims, strides_bytes, box, what);
 }
 
 int map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
@@ -114,7 +139,9 @@ int map_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t 
 
 // ------------------------------------------------------------ validation --
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
+
+namespace moe {
 
 int check_shape(const moe_shape* s, bool need_ffn) {
   if (!s) return fail(MOE_ERR_INVALID_ARG, "shape is null");
@@ -135,12 +162,6 @@ int check_shape(const moe_shape* s, bool need_ffn) {
   return MOE_OK;
 }
 
-#define REQUIRE_PTR(p)                                                               \
-  do {                                                                               \
-    if (!(p)) return fail(MOE_ERR_INVALID_ARG, "%s is null", #p);                    \
-    if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
 int64_t capacity_of(const moe_shape* s) {
   const double cf = s->capacity_factor;
   if (!(cf > 0.0)) return -1;
@@ -150,6 +171,10 @@ int64_t capacity_of(const moe_shape* s) {
   if (c > tk) c = tk;
   return (int64_t)c;
 }
+
+}  // namespace moe
+
+namespace {
 
 // --------------------------------------------------------------- workspace --
 

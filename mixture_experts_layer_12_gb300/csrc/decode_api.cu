@@ -1,0 +1,369 @@
+// decode_api.cu -- the C ABI declared in include/moe_decode.h: argument
+// checks, workspace layout, tensor maps and the two launches of a call on the
+// caller's stream.  No allocation and no host synchronisation.
+#include "api_internal.h"
+#include "decode_internal.h"
+
+using namespace moe;
+
+namespace {
+
+size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+// Workspace: [control block | entries | column tickets | partial tiles |
+// expert outputs of whole items, fp32 | h].  The control block and the
+// tickets are cleared by the first kernel of every call.
+struct Layout {
+  size_t entries, col_tickets, parts, yfull, h, total;
+  int max_entries, row_cap;
+};
+
+int row_cap_of(int rows) { return rows >= kDecRows ? kDecRows : (rows + 7) / 8 * 8; }
+
+Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool layer) {
+  Layout L;
+  L.max_entries = max_entries;
+  L.row_cap = row_cap;
+  L.entries = kDecEntryOffset;
+  L.col_tickets = L.entries + up((size_t)max_entries * sizeof(DecEntry), 1024);
+  L.parts = L.col_tickets + (layer ? up((size_t)((H + kDecBN - 1) / kDecBN) * 4, 1024) : 0);
+  L.yfull = L.parts + (size_t)kDecMaxCtas * 2 * row_cap * kDecBN * 4;
+  L.h = L.yfull + (layer ? up((size_t)rows * H * 4, 1024) : 0);
+  L.total = L.h + (layer ? up((size_t)rows * F * 2, 1024) : 0);
+  return L;
+}
+
+Layout layer_layout(const moe_shape* s) {
+  const int n = s->T * s->k;
+  const int rows = n > 0 ? n : 1;
+  return layout_of(rows, row_cap_of(s->T > 0 ? s->T : 1), n < s->E ? (n > 0 ? n : 1) : s->E, s->H,
+                   s->F, true);
+}
+
+Layout matvec_layout(int rows, int n_segments) {
+  const int r = rows > 0 ? rows : 1;
+  // a segment with n rows has ceil(n / kDecRows) entries
+  const int ent = n_segments < r ? n_segments + r / kDecRows : r;
+  return layout_of(r, row_cap_of(r), ent, 0, 0, false);
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+int check_layer(const moe_shape* s) {
+  int rc = check_shape(s, true);
+  if (rc != MOE_OK) return rc;
+  if (s->T > MOED_MAX_TOKENS)
+    return fail(MOE_ERR_UNSUPPORTED, "T = %d: the decode operators take at most %d tokens", s->T,
+                MOED_MAX_TOKENS);
+  if ((int64_t)s->F * 2 > (int64_t)1 << 30 || (int64_t)s->H > (int64_t)1 << 30)
+    return fail(MOE_ERR_UNSUPPORTED, "H = %d, F = %d: too large", s->H, s->F);
+  return MOE_OK;
+}
+
+int check_group(int32_t group) {
+  if (group != 32 && group != 64 && group != 128)
+    return fail(MOE_ERR_UNSUPPORTED, "group = %d: need 32, 64 or 128", group);
+  return MOE_OK;
+}
+
+int check_q4(int32_t E, int32_t K, int32_t N, int32_t group) {
+  int rc = check_group(group);
+  if (rc != MOE_OK) return rc;
+  if (E < 1 || E > kMaxExperts)
+    return fail(MOE_ERR_UNSUPPORTED, "E = %d: need 1 <= E <= %d", E, kMaxExperts);
+  if (K < group || K % group != 0 || K > 1 << 24)
+    return fail(MOE_ERR_UNSUPPORTED, "K = %d: need a multiple of the group (%d), at most 2^24", K, group);
+  if (N < 8 || N % 8 != 0 || N > 1 << 24)
+    return fail(MOE_ERR_UNSUPPORTED, "N = %d: need N >= 8, N %% 8 == 0, at most 2^24", N);
+  // one thread per 64 weights, one block per 256 of them, on a 31-bit grid
+  if ((int64_t)E * (K / 8) * (N / 8) > (int64_t)1 << 38)
+    return fail(MOE_ERR_UNSUPPORTED, "E * K * N = %d * %d * %d: too large", E, K, N);
+  return MOE_OK;
+}
+
+// W [E, K, N] bf16 in boxes of 64 x 64
+int map_bf16(CUtensorMap* m, const void* w, int E, int K, int N, const char* what) {
+  const uint64_t dims[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)E};
+  const uint64_t strides[2] = {(uint64_t)N * 2, (uint64_t)K * N * 2};
+  const uint32_t box[3] = {64, kDecKC16, 1};
+  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, w, 3, dims,
+                       strides, box, what);
+}
+
+// codes [E, K/8, N] in boxes of 32 x 32 words, scales [E, K/group, N] in
+// boxes of 64 columns and one chunk's rows
+int map_q4(CUtensorMap* mw, CUtensorMap* ms, const void* codes, const void* scales, int E, int K,
+           int N, int group, const char* what) {
+  const uint64_t wd[3] = {(uint64_t)N, (uint64_t)K / 8, (uint64_t)E};
+  const uint64_t wst[2] = {(uint64_t)N * 4, (uint64_t)K / 8 * N * 4};
+  const uint32_t wb[3] = {32, kDecKC4 / 8, 1};
+  int rc = encode_map_as(mw, CU_TENSOR_MAP_DATA_TYPE_INT32, CU_TENSOR_MAP_SWIZZLE_128B, codes, 3, wd,
+                         wst, wb, what);
+  if (rc != MOE_OK) return rc;
+  const uint64_t sd[3] = {(uint64_t)N, (uint64_t)(K / group), (uint64_t)E};
+  const uint64_t sst[2] = {(uint64_t)N * 2, (uint64_t)(K / group) * N * 2};
+  const uint32_t sb[3] = {64, (uint32_t)(kDecKC4 / group), 1};
+  return encode_map_as(ms, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_NONE, scales, 3, sd,
+                       sst, sb, what);
+}
+
+int empty_call(void* ws, int32_t* counts, int32_t* offsets, int E, cudaStream_t st) {
+  cudaError_t e = launch_clear_status(static_cast<int*>(ws), st, true);
+  if (e == cudaSuccess && counts) e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)E, st);
+  if (e == cudaSuccess && offsets) e = cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (size_t)(E + 1), st);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "clearing an empty call's outputs");
+}
+
+struct Weights {
+  bool q4;
+  int group;
+  const void *w1, *s1, *w2, *s2;
+};
+
+int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint16_t* w_router,
+            const float* b_router, uint16_t* y, int32_t* ids, float* weights, int32_t* counts,
+            int32_t* offsets, int32_t* perm, int32_t* slot, void* ws, size_t ws_bytes,
+            void* stream) {
+  int rc;
+  REQUIRE_PTR(ws);
+  const Layout L = layer_layout(s);
+  if (ws_bytes < L.total)
+    return fail(MOE_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed (moed_workspace_size)",
+                ws_bytes, L.total);
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(offsets);
+  if (b_router && !aligned16(b_router)) return fail(MOE_ERR_INVALID_ARG, "b_router is not 16-byte aligned");
+  if (s->T > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(w_router);
+    REQUIRE_PTR(wt.w1);
+    REQUIRE_PTR(wt.w2);
+    if (wt.q4) {
+      REQUIRE_PTR(wt.s1);
+      REQUIRE_PTR(wt.s2);
+    }
+    REQUIRE_PTR(y);
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(weights);
+    REQUIRE_PTR(perm);
+    REQUIRE_PTR(slot);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  if (s->T == 0) return empty_call(ws, counts, offsets, s->E, st);
+
+  const bool swiglu = s->expert_act == MOE_EXPERT_SWIGLU;
+  const int N1 = swiglu ? 2 * s->F : s->F;
+  DecFfnMaps maps;
+  if (wt.q4) {
+    if ((rc = map_q4(&maps.w1, &maps.s1, wt.w1, wt.s1, s->E, s->H, N1, wt.group, "W1")) != MOE_OK) return rc;
+    if ((rc = map_q4(&maps.w2, &maps.s2, wt.w2, wt.s2, s->E, s->F, s->H, wt.group, "W2")) != MOE_OK) return rc;
+  } else {
+    if ((rc = map_bf16(&maps.w1, wt.w1, s->E, s->H, N1, "W1")) != MOE_OK) return rc;
+    if ((rc = map_bf16(&maps.w2, wt.w2, s->E, s->F, s->H, "W2")) != MOE_OK) return rc;
+    maps.s1 = maps.w1;  // not used
+    maps.s2 = maps.w2;
+  }
+
+  DecRouteArgs ra;
+  ra.x = x;
+  ra.w = w_router;
+  ra.bias = b_router;
+  ra.T = s->T;
+  ra.H = s->H;
+  ra.E = s->E;
+  ra.k = s->k;
+  ra.capacity = (int)capacity_of(s);
+  ra.gating = s->gating;
+  ra.ids = ids;
+  ra.weights = weights;
+  ra.counts = counts;
+  ra.offsets = offsets;
+  ra.perm = perm;
+  ra.slot = slot;
+  ra.ctrl = static_cast<int*>(ws);
+  ra.entries = at<DecEntry>(ws, L.entries);
+  ra.col_tickets = at<int>(ws, L.col_tickets);
+  ra.n_col_tickets = (s->H + kDecBN - 1) / kDecBN;
+  cudaError_t e = launch_decode_route(ra, st);
+  if (e != cudaSuccess) return cuda_fail(e, "decode route launch");
+
+  const int kc = wt.q4 ? kDecKC4 : kDecKC16;
+  const int cols1 = swiglu ? 64 : kDecBN;  // columns of h per item
+  DecFfnArgs fa = {};
+  fa.ctrl = static_cast<const int*>(ws);
+  fa.entries = ra.entries;
+  fa.max_entries = L.max_entries;
+  fa.barrier = at<unsigned>(ws, kDecBarrierOffset);
+  fa.item_tickets = at<unsigned>(ws, kDecTicketOffset);
+  fa.col_tickets = at<unsigned>(ws, L.col_tickets);
+  fa.parts = at<float>(ws, L.parts);
+  fa.row_cap = L.row_cap;
+  fa.yfull = at<float>(ws, L.yfull);
+  fa.h = at<uint16_t>(ws, L.h);
+  fa.x = x;
+  fa.perm = perm;
+  fa.slot = slot;
+  fa.gate = weights;
+  fa.y = y;
+  fa.T = s->T;
+  fa.k = s->k;
+  fa.act = swiglu ? kDecSwiGLU : kDecGelu;
+  fa.group = wt.group;
+  fa.K1 = s->H;
+  fa.N1 = s->F;
+  fa.nb1 = (s->F + cols1 - 1) / cols1;
+  fa.kc1 = (s->H + kc - 1) / kc;
+  fa.K2 = s->F;
+  fa.N2 = s->H;
+  fa.nb2 = (s->H + kDecBN - 1) / kDecBN;
+  fa.kc2 = (s->F + kc - 1) / kc;
+  fa.status = static_cast<int*>(ws);
+  fa.wait_limit_ns = kWaitLimitNs;
+  e = launch_decode_ffn(wt.q4, maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "decode expert launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moed_workspace_size(const moe_shape* s) {
+  if (check_layer(s) != MOE_OK) return 0;
+  return layer_layout(s).total;
+}
+
+int moed_forward(const moe_shape* s, const uint16_t* x, const uint16_t* w_router,
+                 const float* b_router, const uint16_t* w1, const uint16_t* w2, uint16_t* y,
+                 int32_t* ids, float* weights, int32_t* counts, int32_t* offsets, int32_t* perm,
+                 int32_t* slot, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_layer(s);
+  if (rc != MOE_OK) return rc;
+  const Weights wt{false, 0, w1, nullptr, w2, nullptr};
+  return forward(s, wt, x, w_router, b_router, y, ids, weights, counts, offsets, perm, slot, ws,
+                 ws_bytes, stream);
+}
+
+int moed_forward_q4(const moe_shape* s, int32_t group, const uint16_t* x, const uint16_t* w_router,
+                    const float* b_router, const uint32_t* w1_codes, const uint16_t* w1_scales,
+                    const uint32_t* w2_codes, const uint16_t* w2_scales, uint16_t* y, int32_t* ids,
+                    float* weights, int32_t* counts, int32_t* offsets, int32_t* perm,
+                    int32_t* slot, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_layer(s);
+  if (rc != MOE_OK) return rc;
+  if ((rc = check_group(group)) != MOE_OK) return rc;
+  if (s->H % group != 0 || s->F % group != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "H = %d, F = %d: need multiples of the group (%d)", s->H, s->F, group);
+  const Weights wt{true, group, w1_codes, w1_scales, w2_codes, w2_scales};
+  return forward(s, wt, x, w_router, b_router, y, ids, weights, counts, offsets, perm, slot, ws,
+                 ws_bytes, stream);
+}
+
+size_t moed_matvec_q4_workspace_size(int32_t rows, int32_t n_segments, int32_t K, int32_t N) {
+  if (rows < 0 || rows > MOED_MAX_ROWS || n_segments < 1 || n_segments > kMaxExperts || K < 32 || N < 8) {
+    fail(MOE_ERR_UNSUPPORTED, "rows = %d (0..%d), n_segments = %d (1..%d), K = %d, N = %d", rows,
+         MOED_MAX_ROWS, n_segments, kMaxExperts, K, N);
+    return 0;
+  }
+  return matvec_layout(rows, n_segments).total;
+}
+
+int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group, int32_t n_segments,
+                   const uint16_t* x, const uint32_t* codes, const uint16_t* scales,
+                   const int32_t* seg_offsets, uint16_t* y, void* ws, size_t ws_bytes,
+                   void* stream) {
+  int rc = check_q4(E, K, N, group);
+  if (rc != MOE_OK) return rc;
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %d < 0", rows);
+  if (rows > MOED_MAX_ROWS)
+    return fail(MOE_ERR_UNSUPPORTED, "rows = %d: at most %d", rows, MOED_MAX_ROWS);
+  if (n_segments < 1 || n_segments > kMaxExperts)
+    return fail(MOE_ERR_INVALID_ARG, "n_segments = %d, must be 1..%d", n_segments, kMaxExperts);
+  REQUIRE_PTR(ws);
+  const Layout L = matvec_layout(rows, n_segments);
+  if (ws_bytes < L.total)
+    return fail(MOE_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed (moed_matvec_q4_workspace_size)",
+                ws_bytes, L.total);
+  if (rows > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(codes);
+    REQUIRE_PTR(scales);
+    if (seg_offsets || n_segments != 1) REQUIRE_PTR(seg_offsets);  // null: one segment, all rows
+    REQUIRE_PTR(y);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  if (rows == 0) return empty_call(ws, nullptr, nullptr, 0, st);
+
+  DecFfnMaps maps;
+  if ((rc = map_q4(&maps.w1, &maps.s1, codes, scales, E, K, N, group, "W")) != MOE_OK) return rc;
+  maps.w2 = maps.w1;  // not used
+  maps.s2 = maps.s1;
+
+  DecPrepArgs pa;
+  pa.seg_offsets = seg_offsets;
+  pa.n_segments = n_segments;
+  pa.rows = rows;
+  pa.E = E;
+  pa.ctrl = static_cast<int*>(ws);
+  pa.entries = at<DecEntry>(ws, L.entries);
+  pa.max_entries = L.max_entries;
+  cudaError_t e = launch_decode_prep(pa, st);
+  if (e != cudaSuccess) return cuda_fail(e, "entry list launch");
+
+  DecFfnArgs fa = {};
+  fa.ctrl = static_cast<const int*>(ws);
+  fa.entries = pa.entries;
+  fa.max_entries = L.max_entries;
+  fa.barrier = at<unsigned>(ws, kDecBarrierOffset);
+  fa.item_tickets = at<unsigned>(ws, kDecTicketOffset);
+  fa.parts = at<float>(ws, L.parts);
+  fa.row_cap = L.row_cap;
+  fa.x = x;
+  fa.y = y;
+  fa.T = rows;
+  fa.k = 1;
+  fa.act = kDecNone;
+  fa.group = group;
+  fa.K1 = K;
+  fa.N1 = N;
+  fa.nb1 = (N + kDecBN - 1) / kDecBN;
+  fa.kc1 = (K + kDecKC4 - 1) / kDecKC4;
+  fa.status = static_cast<int*>(ws);
+  fa.wait_limit_ns = kWaitLimitNs;
+  e = launch_decode_ffn(true, maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "matrix-vector launch");
+}
+
+int moed_quantize_q4(int32_t E, int32_t K, int32_t N, int32_t group, const uint16_t* w,
+                     uint32_t* codes, uint16_t* scales, void* stream) {
+  int rc = check_q4(E, K, N, group);
+  if (rc != MOE_OK) return rc;
+  REQUIRE_PTR(w);
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  int sms = 0;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  cudaError_t e = launch_quantize_q4(E, K, N, group, w, codes, scales, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "quantize launch");
+}
+
+int moed_dequantize_q4(int32_t E, int32_t K, int32_t N, int32_t group, const uint32_t* codes,
+                       const uint16_t* scales, uint16_t* w, void* stream) {
+  int rc = check_q4(E, K, N, group);
+  if (rc != MOE_OK) return rc;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  REQUIRE_PTR(w);
+  int sms = 0;
+  if ((rc = device_setup(&sms)) != MOE_OK) return rc;
+  cudaError_t e = launch_dequantize_q4(E, K, N, group, codes, scales, w, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e, "dequantize launch");
+}
+
+}  // extern "C"

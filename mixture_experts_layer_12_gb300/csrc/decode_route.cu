@@ -1,0 +1,460 @@
+// decode_route.cu -- first kernel of the decode operators: the whole route
+// (logits, TopK, gate, dispatch) of at most 64 tokens by one cluster of 8
+// CTAs, and the entry list of the grouped products.
+//
+// "用Ascend C写一个MoE融合算子", section "1. Routing + Gating 合并" and listing
+// "Gather操作", as in route_fused.cu; what differs is the size.  A few tokens'
+// logits are a [T, H] x [H, E] product of at most a megabyte or two, far too
+// little to fill the GPU and bound by latency: one trip to memory, one
+// reduction, two cluster barriers.  The H axis is split over the 8 CTAs, so a
+// trip to memory brings all of W_router at once (16 SMs' worth of loads in
+// flight for E = 8, one load per thread); within a CTA the warps split the
+// remaining K steps and the experts.  The products are m16n8k16 tensor-core
+// ones with W_router as the M operand (ldmatrix.trans: E is contiguous) and
+// the tokens as N: bf16 products are exact in fp32, sums are fp32 in a fixed
+// order (warps of a CTA, then ranks 0..7).  The partial logits stay in shared
+// memory and are read through distributed shared memory by the rank that
+// owns the token (t mod 8), 8 lanes per token (route_topk.cuh).  Rank 0 then
+// holds every id and dispatches: at most 512 assignments, ranked within their
+// expert by warp match and a scan over the warps' chunks.
+#include "decode_internal.h"
+#include "route_topk.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int DR_THREADS = 256;
+constexpr int DR_WARPS = DR_THREADS / 32;
+constexpr int DR_RANKS = 8;
+constexpr int DR_MAX_ASSIGN = MOED_MAX_TOKENS * kMaxTopK;  // 512
+constexpr int DR_CHUNKS = DR_MAX_ASSIGN / 32;
+constexpr int DR_STAGE_BYTES = 128 * 1024;  // W_router and x rows staged at a time
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x2(uint32_t a, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void dsmem_st_u32(uint32_t cluster_saddr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_saddr), "r"(v) : "memory");
+}
+
+struct RouteLayout {
+  int ep;      // experts rounded up to 16
+  int tp;      // tokens rounded up to 8, 16, 32 or 64 (the kernel's token tiles)
+  int kb;      // K rows staged at a time (a multiple of 16)
+  int pw, px;  // row pitches of the staged W_router and x, bytes (odd multiples of 16)
+  int hs;      // H rows of a CTA
+  int wm;      // warps along the experts (the others split K)
+  size_t stage, part, total;
+};
+
+__host__ __device__ inline RouteLayout route_layout(int T, int H, int E) {
+  RouteLayout L;
+  L.ep = (E + 15) / 16 * 16;
+  L.tp = 8;
+  while (L.tp < T) L.tp *= 2;
+  L.hs = (H + DR_RANKS * 16 - 1) / (DR_RANKS * 16) * 16;
+  L.pw = L.ep * 2 + 16;
+  // kb rows of W_router (pw bytes) and of every token (2 kb + 16 bytes)
+  int kb = (DR_STAGE_BYTES - 16 * L.tp) / (L.pw + 2 * L.tp) / 16 * 16;
+  if (kb > L.hs) kb = L.hs;
+  if (kb < 16) kb = 16;
+  L.kb = kb;
+  L.px = kb * 2 + 16;
+  L.wm = 1;
+  while (L.wm < DR_WARPS && L.wm * 16 < L.ep) L.wm *= 2;
+  const size_t tiles = (size_t)kb * L.pw + (size_t)L.tp * L.px;
+  const size_t red = (size_t)(DR_WARPS / L.wm) * L.tp * L.ep * 4;  // reuses the tiles' space
+  L.stage = tiles > red ? tiles : red;
+  L.stage = (L.stage + 127) / 128 * 128;
+  L.part = (size_t)L.tp * L.ep * 4;
+  L.total = L.stage + L.part;
+  return L;
+}
+
+// NT: 8-token tiles; NCH: 32-expert chunks of the TopK lanes.
+template <int NT, int NCH>
+__global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1)
+    decode_route_kernel(const DecRouteArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_ids[DR_MAX_ASSIGN];
+  __shared__ int s_wc[DR_CHUNKS][kMaxExperts];
+  __shared__ int s_off[kMaxExperts + 1];
+  __shared__ int s_scan[2][DR_WARPS];
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const RouteLayout L = route_layout(a.T, a.H, a.E);
+  const int E = a.E, T = a.T, H = a.H, k = a.k;
+  uint8_t* sW = smem;
+  uint8_t* sX = smem + (size_t)L.kb * L.pw;
+  float* sRed = reinterpret_cast<float*>(smem);
+  float* sPart = reinterpret_cast<float*>(smem + L.stage);
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // the counters of the second kernel
+  for (int i = rank * DR_THREADS + tid; i < kDecCtrlInts + a.n_col_tickets;
+       i += DR_RANKS * DR_THREADS) {
+    if (i < kDecCtrlInts)
+      a.ctrl[i] = 0;
+    else
+      a.col_tickets[i - kDecCtrlInts] = 0;
+  }
+
+  // ---- partial logits of rows [h0, h1) of H
+  const int h0 = min(rank * L.hs, H), h1 = min(h0 + L.hs, H);
+  const int wm = warp & (L.wm - 1);        // expert tiles wm, wm + L.wm
+  const int wk = warp / L.wm;              // K steps wk, wk + nk, ...
+  const int nk = DR_WARPS / L.wm;
+  const int mt = L.ep / 16;
+  float acc[2][NT][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[m][n][r] = 0.f;
+
+  for (int hb = h0; hb < h1; hb += L.kb) {
+    const int rows = min(L.kb, h1 - hb);      // a multiple of 8
+    const int rows16 = (rows + 15) / 16 * 16;
+    if (hb != h0) __syncthreads();
+    if ((E & 7) == 0) {
+      const int ch = E / 8;
+      for (int i = tid; i < rows * ch; i += DR_THREADS) {
+        const int r = i / ch, c = i - r * ch;
+        cp_async16(smem_u32(sW + (size_t)r * L.pw + c * 16), a.w + (size_t)(hb + r) * E + c * 8);
+      }
+    } else {  // rows not 16-byte aligned
+      const uint16_t* src = a.w + (size_t)hb * E;
+      for (int i = tid; i < rows * E; i += DR_THREADS) {
+        const int r = i / E, c = i - r * E;
+        *reinterpret_cast<uint16_t*>(sW + (size_t)r * L.pw + c * 2) = __ldg(src + i);
+      }
+    }
+    const int xc = rows / 8;
+    for (int i = tid; i < T * xc; i += DR_THREADS) {
+      const int t = i / xc, c = i - t * xc;
+      cp_async16(smem_u32(sX + (size_t)t * L.px + c * 16), a.x + (size_t)t * H + hb + c * 8);
+    }
+    if (rows16 != rows) {  // zero the half step past the end in both operands
+      for (int i = tid; i < 8 * (L.ep / 8); i += DR_THREADS) {
+        const int r = rows + i / (L.ep / 8), c = i % (L.ep / 8);
+        *reinterpret_cast<uint4*>(sW + (size_t)r * L.pw + c * 16) = make_uint4(0, 0, 0, 0);
+      }
+      for (int t = tid; t < T; t += DR_THREADS)
+        *reinterpret_cast<uint4*>(sX + (size_t)t * L.px + rows * 2) = make_uint4(0, 0, 0, 0);
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    for (int ks = wk; ks < rows16 / 16; ks += nk) {
+      uint32_t b[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        ldsm_x2(smem_u32(sX + (size_t)(n * 8 + (lane & 7)) * L.px + ks * 32 + ((lane >> 3) & 1) * 16),
+                b[n][0], b[n][1]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int tile = wm + m * L.wm;
+        if (tile >= mt) break;
+        uint32_t w[4];
+        ldsm_x4_t(smem_u32(sW + (size_t)(ks * 16 + (lane >> 4) * 8 + (lane & 7)) * L.pw + tile * 32 +
+                           ((lane >> 3) & 1) * 16),
+                  w);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_bf16(acc[m][n], w, b[n][0], b[n][1]);
+      }
+    }
+  }
+  __syncthreads();
+  // sum over the warps that split K: [wk][token][expert]
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const int tile = wm + m * L.wm;
+    if (tile >= mt) break;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = tile * 16 + (lane >> 2) + (r >> 1) * 8;
+        const int t = n * 8 + (lane & 3) * 2 + (r & 1);
+        sRed[((size_t)wk * L.tp + t) * L.ep + e] = acc[m][n][r];
+      }
+  }
+  __syncthreads();
+  for (int i = tid; i < L.tp * L.ep; i += DR_THREADS) {
+    float v = 0.f;
+    for (int w = 0; w < nk; ++w) v += sRed[(size_t)w * L.tp * L.ep + i];
+    sPart[i] = v;
+  }
+  cluster_sync_all();
+
+  // ---- TopK and gate weights of the tokens this rank owns: t mod 8 = rank
+  {
+    const int grp = tid >> 3, g = tid & 7;
+    const int t = grp * DR_RANKS + rank;
+    if (t < T) {
+      const unsigned gmask = 0xFFu << (lane & 24);
+      float lv[NCH * 4];
+      uint32_t taken = 0;
+#pragma unroll
+      for (int cc = 0; cc < NCH; ++cc) {
+        const int e0 = (g + cc * kTopkGroup) * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e0 < L.ep) {
+          const uint32_t local = smem_u32(sPart + (size_t)t * L.ep + e0);
+          float4 p[DR_RANKS];
+#pragma unroll
+          for (int r = 0; r < DR_RANKS; ++r) p[r] = dsmem_ld_v4(dsmem_map(local, (uint32_t)r));
+#pragma unroll
+          for (int r = 0; r < DR_RANKS; ++r) {
+            s.x += p[r].x;
+            s.y += p[r].y;
+            s.z += p[r].z;
+            s.w += p[r].w;
+          }
+        }
+        const float v4[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = v4[i];
+          if (e0 + i < E) {
+            if (a.bias) v += __ldg(a.bias + e0 + i);
+            if (isnan(v)) v = -INFINITY;
+          } else {
+            v = -INFINITY;
+            taken |= 1u << (cc * 4 + i);
+          }
+          lv[cc * 4 + i] = v;
+        }
+      }
+      int id;
+      float w;
+      topk_gate_group<NCH>(lv, taken, g, gmask, k, E, a.gating, id, w);
+      if (g < k) {
+        a.ids[(size_t)t * k + g] = id;
+        a.weights[(size_t)t * k + g] = w;
+        dsmem_st_u32(dsmem_map(smem_u32(s_ids + t * k + g), 0), (uint32_t)id);
+      }
+    }
+  }
+  cluster_sync_all();
+  if (rank != 0) return;
+
+  // ---- dispatch of all T*k assignments, in (token, slot) order
+  const int n = T * k;
+  const int chunks = (n + 31) / 32;
+  for (int i = tid; i < chunks * kMaxExperts; i += DR_THREADS) (&s_wc[0][0])[i] = 0;
+  __syncthreads();
+  int my_e[2], below[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int c = warp + u * DR_WARPS;
+    my_e[u] = -1;
+    below[u] = 0;
+    if (c < chunks) {
+      const int i = c * 32 + lane;
+      int e = i < n ? s_ids[i] : -1;
+      if (e < 0 || e >= E) e = -1;
+      const unsigned m = __match_any_sync(0xffffffffu, e);
+      below[u] = __popc(m & ((1u << lane) - 1u));
+      if (e >= 0 && below[u] == 0) s_wc[c][e] = __popc(m);
+      my_e[u] = e;
+    }
+  }
+  __syncthreads();
+  int kept = 0;
+  if (tid < E) {
+    int run = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int v = s_wc[c][tid];
+      s_wc[c][tid] = run;
+      run += v;
+    }
+    kept = a.capacity >= 0 ? min(run, a.capacity) : run;
+  }
+  // exclusive scans over the experts of the kept rows and of the experts hit
+  const unsigned hit = __ballot_sync(0xffffffffu, kept > 0);
+  int incl = kept;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) {
+    s_scan[0][warp] = incl;
+    s_scan[1][warp] = __popc(hit);
+  }
+  __syncthreads();
+  int base = 0, hbase = 0, total = 0, htotal = 0;
+#pragma unroll
+  for (int w = 0; w < DR_WARPS; ++w) {
+    if (w < warp) {
+      base += s_scan[0][w];
+      hbase += s_scan[1][w];
+    }
+    total += s_scan[0][w];
+    htotal += s_scan[1][w];
+  }
+  if (tid < E) {
+    const int off = base + incl - kept;
+    s_off[tid] = off;
+    a.counts[tid] = kept;
+    a.offsets[tid] = off;
+    if (kept > 0)
+      a.entries[hbase + __popc(hit & ((1u << lane) - 1u))] = DecEntry{tid, off, kept, 0};
+  }
+  if (tid == 0) {
+    a.offsets[E] = total;
+    a.ctrl[kDecCountOffset / 4] = htotal;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int c = warp + u * DR_WARPS;
+    const int i = c * 32 + lane;
+    if (c >= chunks || i >= n) continue;
+    const int e = my_e[u];
+    const int pos = e >= 0 ? s_wc[c][e] + below[u] : -1;
+    if (pos >= 0 && (a.capacity < 0 || pos < a.capacity)) {
+      a.slot[i] = s_off[e] + pos;
+      a.perm[s_off[e] + pos] = i;
+    } else {
+      a.slot[i] = -1;
+    }
+  }
+  for (int i = total + tid; i < n; i += DR_THREADS) a.perm[i] = -1;
+}
+
+// Entries of the grouped products: segment i's rows in blocks of kDecRows.
+__global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
+  __shared__ int s_scan[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int i = tid; i < kDecCtrlInts; i += 256) a.ctrl[i] = 0;
+  int o0 = 0, n = 0;
+  if (tid < a.n_segments) {
+    // each row belongs to one entry at most: offsets are clamped, and a
+    // decreasing one gives an empty segment
+    o0 = a.seg_offsets ? min(max(__ldg(a.seg_offsets + tid), 0), a.rows) : 0;
+    const int o1 = a.seg_offsets ? min(max(__ldg(a.seg_offsets + tid + 1), 0), a.rows) : a.rows;
+    n = max(o1 - o0, 0);
+  }
+  const int blocks = (n + kDecRows - 1) / kDecRows;
+  int incl = blocks;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) base += s_scan[w];
+    total += s_scan[w];
+  }
+  int at = base + incl - blocks;
+  for (int b = 0; b < blocks && at < a.max_entries; ++b, ++at)
+    a.entries[at] = DecEntry{tid % a.E, o0 + b * kDecRows, min(kDecRows, n - b * kDecRows), 0};
+  if (tid == 0) a.ctrl[kDecCountOffset / 4] = min(total, a.max_entries);
+}
+
+template <int NT, int NCH>
+cudaError_t route_launch(const DecRouteArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(DR_RANKS, 1, 1);
+  cfg.blockDim = dim3(DR_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = route_layout(a.T, a.H, a.E).total;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  set_pdl_attr(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_route_kernel<NT, NCH>, a);
+}
+
+template <int NT>
+cudaError_t route_nt(const DecRouteArgs& a, cudaStream_t st) {
+  if (a.E <= 32) return route_launch<NT, 1>(a, st);
+  if (a.E <= 64) return route_launch<NT, 2>(a, st);
+  if (a.E <= 128) return route_launch<NT, 4>(a, st);
+  return route_launch<NT, 8>(a, st);
+}
+
+template <int NT>
+cudaError_t route_attr() {
+  // stage plus partial logits at the largest shapes: 128 KB + 64 KB
+  const int bytes = DR_STAGE_BYTES + MOED_MAX_TOKENS * kMaxExperts * 4;
+  cudaError_t e = cudaFuncSetAttribute(decode_route_kernel<NT, 1>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(decode_route_kernel<NT, 2>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(decode_route_kernel<NT, 4>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(decode_route_kernel<NT, 8>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_route(const DecRouteArgs& a, cudaStream_t st) {
+  const int nt = (a.T + 7) / 8;
+  if (nt <= 1) return route_nt<1>(a, st);
+  if (nt <= 2) return route_nt<2>(a, st);
+  if (nt <= 4) return route_nt<4>(a, st);
+  return route_nt<8>(a, st);
+}
+
+cudaError_t launch_decode_prep(const DecPrepArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  set_pdl_attr(attr[0]);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_prep_kernel, a);
+}
+
+cudaError_t decode_route_set_attributes() {
+  cudaError_t e = route_attr<1>();
+  if (e == cudaSuccess) e = route_attr<2>();
+  if (e == cudaSuccess) e = route_attr<4>();
+  if (e == cudaSuccess) e = route_attr<8>();
+  return e;
+}
+
+}  // namespace moe
