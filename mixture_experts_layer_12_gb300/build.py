@@ -18,8 +18,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "router.cu", "route_fused.cu", "dispatch_combine.cu", "ffn_gemm.cu",
-           "ffn_gemm_small.cu", "decode_api.cu", "decode_route.cu", "decode_ffn.cu", "q4.cu"]
-HEADERS = ["tc_common.cuh", "moe_internal.h", "api_internal.h", "decode_internal.h", "route_topk.cuh"]
+           "ffn_gemm_small.cu", "decode_api.cu", "decode_route.cu", "decode_ffn_bf16.cu",
+           "decode_ffn_q4_32.cu", "decode_ffn_q4_64.cu", "decode_ffn_q4_128.cu", "q4.cu"]
+HEADERS = ["tc_common.cuh", "moe_internal.h", "api_internal.h", "decode_internal.h", "decode_ffn.cuh",
+           "route_topk.cuh"]
 INCLUDES = ["moe.h", "moe_decode.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

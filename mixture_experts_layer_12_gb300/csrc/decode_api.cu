@@ -6,7 +6,29 @@
 
 using namespace moe;
 
+namespace moe {
+
+cudaError_t decode_set_attributes() {
+  cudaError_t e = decode_route_set_attributes();
+  if (e == cudaSuccess) e = decode_ffn_bf16_set_attributes();
+  if (e == cudaSuccess) e = decode_ffn_q4_32_set_attributes();
+  if (e == cudaSuccess) e = decode_ffn_q4_64_set_attributes();
+  if (e == cudaSuccess) e = decode_ffn_q4_128_set_attributes();
+  return e;
+}
+
+}  // namespace moe
+
 namespace {
+
+cudaError_t launch_decode_ffn(const DecFfnMaps& m, const DecFfnArgs& a, int ctas, cudaStream_t st) {
+  switch (a.group) {
+    case 0: return launch_decode_ffn_bf16(m, a, ctas, st);
+    case 32: return launch_decode_ffn_q4_32(m, a, ctas, st);
+    case 64: return launch_decode_ffn_q4_64(m, a, ctas, st);
+    default: return launch_decode_ffn_q4_128(m, a, ctas, st);
+  }
+}
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -14,7 +36,7 @@ size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // expert outputs of whole items, fp32 | h].  The control block and the
 // tickets are cleared by the first kernel of every call.
 struct Layout {
-  size_t entries, col_tickets, parts, yfull, h, total;
+  size_t entries, col_tickets, parts, parts2, yfull, h, total;
   int max_entries, row_cap;
 };
 
@@ -27,7 +49,9 @@ Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool laye
   L.entries = kDecEntryOffset;
   L.col_tickets = L.entries + up((size_t)max_entries * sizeof(DecEntry), 1024);
   L.parts = L.col_tickets + (layer ? up((size_t)((H + kDecBN - 1) / kDecBN) * 4, 1024) : 0);
-  L.yfull = L.parts + (size_t)kDecMaxCtas * 2 * row_cap * kDecBN * 4;
+  const size_t tiles = (size_t)kDecMaxCtas * 2 * row_cap * kDecBN * 4;
+  L.parts2 = L.parts + tiles;
+  L.yfull = L.parts2 + (layer ? tiles : 0);
   L.h = L.yfull + (layer ? up((size_t)rows * H * 4, 1024) : 0);
   L.total = L.h + (layer ? up((size_t)rows * F * 2, 1024) : 0);
   return L;
@@ -117,6 +141,14 @@ int empty_call(void* ws, int32_t* counts, int32_t* offsets, int E, cudaStream_t 
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "clearing an empty call's outputs");
 }
 
+// The streaming kernel counts a product's chunks, times its CTAs, in 32 bits.
+int check_chunks(int64_t entries, int64_t nb, int64_t kc) {
+  if (nb * kc > ((int64_t)1 << 32) / kDecMaxCtas || entries * nb * kc >= ((int64_t)1 << 32) / kDecMaxCtas)
+    return fail(MOE_ERR_UNSUPPORTED, "%lld x %lld x %lld weight tiles: too many", (long long)entries,
+                (long long)nb, (long long)kc);
+  return MOE_OK;
+}
+
 struct Weights {
   bool q4;
   int group;
@@ -169,6 +201,13 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
     maps.s2 = maps.w2;
   }
 
+  const int kc = wt.q4 ? kDecKC4 : kDecKC16;
+  const int cols1 = swiglu ? 64 : kDecBN;  // columns of h per item
+  const int nb1 = (s->F + cols1 - 1) / cols1, kc1 = (s->H + kc - 1) / kc;
+  const int nb2 = (s->H + kDecBN - 1) / kDecBN, kc2 = (s->F + kc - 1) / kc;
+  if ((rc = check_chunks(L.max_entries, nb1, kc1)) != MOE_OK) return rc;
+  if ((rc = check_chunks(L.max_entries, nb2, kc2)) != MOE_OK) return rc;
+
   DecRouteArgs ra;
   ra.x = x;
   ra.w = w_router;
@@ -192,8 +231,6 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   cudaError_t e = launch_decode_route(ra, st);
   if (e != cudaSuccess) return cuda_fail(e, "decode route launch");
 
-  const int kc = wt.q4 ? kDecKC4 : kDecKC16;
-  const int cols1 = swiglu ? 64 : kDecBN;  // columns of h per item
   DecFfnArgs fa = {};
   fa.ctrl = static_cast<const int*>(ws);
   fa.entries = ra.entries;
@@ -203,6 +240,7 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.col_tickets = at<unsigned>(ws, L.col_tickets);
   fa.parts = at<float>(ws, L.parts);
   fa.row_cap = L.row_cap;
+  fa.parts2 = at<float>(ws, L.parts2);
   fa.yfull = at<float>(ws, L.yfull);
   fa.h = at<uint16_t>(ws, L.h);
   fa.x = x;
@@ -216,15 +254,15 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.group = wt.group;
   fa.K1 = s->H;
   fa.N1 = s->F;
-  fa.nb1 = (s->F + cols1 - 1) / cols1;
-  fa.kc1 = (s->H + kc - 1) / kc;
+  fa.nb1 = nb1;
+  fa.kc1 = kc1;
   fa.K2 = s->F;
   fa.N2 = s->H;
-  fa.nb2 = (s->H + kDecBN - 1) / kDecBN;
-  fa.kc2 = (s->F + kc - 1) / kc;
+  fa.nb2 = nb2;
+  fa.kc2 = kc2;
   fa.status = static_cast<int*>(ws);
   fa.wait_limit_ns = kWaitLimitNs;
-  e = launch_decode_ffn(wt.q4, maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
+  e = launch_decode_ffn(maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "decode expert launch");
 }
 
@@ -300,6 +338,8 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   if ((rc = device_setup(&sms)) != MOE_OK) return rc;
   if (rows == 0) return empty_call(ws, nullptr, nullptr, 0, st);
 
+  const int nb = (N + kDecBN - 1) / kDecBN, kc = (K + kDecKC4 - 1) / kDecKC4;
+  if ((rc = check_chunks(L.max_entries, nb, kc)) != MOE_OK) return rc;
   DecFfnMaps maps;
   if ((rc = map_q4(&maps.w1, &maps.s1, codes, scales, E, K, N, group, "W")) != MOE_OK) return rc;
   maps.w2 = maps.w1;  // not used
@@ -332,11 +372,11 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   fa.group = group;
   fa.K1 = K;
   fa.N1 = N;
-  fa.nb1 = (N + kDecBN - 1) / kDecBN;
-  fa.kc1 = (K + kDecKC4 - 1) / kDecKC4;
+  fa.nb1 = nb;
+  fa.kc1 = kc;
   fa.status = static_cast<int*>(ws);
   fa.wait_limit_ns = kWaitLimitNs;
-  e = launch_decode_ffn(true, maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
+  e = launch_decode_ffn(maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "matrix-vector launch");
 }
 

@@ -1,4 +1,4 @@
-// decode_ffn.cu -- second kernel of the decode operators: the expert products
+// decode_ffn.cuh -- second kernel of the decode operators: the expert products
 // of a few rows, in one cooperative launch that streams every needed weight
 // once.
 //
@@ -41,20 +41,19 @@
 //     itself in; the last one sums every token's experts in slot order.
 // The grid barrier needs all CTAs resident, which the cooperative launch
 // guarantees; it and every other wait is bounded.
+#pragma once
+
 #include "decode_internal.h"
 #include "tc_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int DF_LOADERS = 3;     // 12 warps in all, 3 to a scheduler: 168 registers each
-constexpr int DF_CONSUMERS = 8;  // 4 across columns x 2 across K
-constexpr int DF_THREADS = 32 * (1 + DF_LOADERS + DF_CONSUMERS);
 constexpr int DF_WN = 4;         // consumer warps across the columns
 constexpr int DF_FIN = 32 * DF_WN;  // threads that write an item out
 constexpr int DF_W_BYTES = 16384;
 constexpr int DF_MAX_WSTAGES = 12;
-constexpr int DF_MAX_BSTAGES = 8;
+constexpr int DF_MAX_BSTAGES = 6;
 constexpr int DF_SMEM_LIMIT = 227 * 1024;
 
 // named barriers: consumers, writers of an item
@@ -125,22 +124,38 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t x) {
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same with a sum that begins at zero
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // codes i and i + 4 of a word (rows i and i + 4 of its 8) as a bf16 pair
-// c - 8, exactly: 0x4300 | c is 128 + c.
+// (c - 8) / 64, exactly (the scale is multiplied by 64).  A code at bits 0-3
+// or 4-7 of a half word is, read as bf16, c or 16 c times 2^-133 (the numbers
+// below 2^-125 are evenly spaced), so one masked word and one fused
+// multiply-add make a pair, and a word needs one shift: 9 instructions for 8
+// codes where (128 + c) - 136 takes 11, of which the shifts and masks run at
+// half rate (matrix-vector product 18.8 -> 17.9 us).
 template <int I>
 __device__ __forceinline__ uint32_t q4_pair(uint32_t v) {
-  uint32_t p;
-  asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(p) : "r"(v >> (4 * I)));
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&p),
-                                   __floats2bfloat162_rn(136.f, 136.f));
-  return *reinterpret_cast<const uint32_t*>(&d);
+  const uint32_t p = (I & 2 ? v >> 8 : v) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+      : "=r"(d)
+      : "r"(p), "r"(I & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(0xBE00BE00u));  // 2^123, 2^127; -8 / 64
+  return d;
 }
 
 // GELU(z) = 0.5 z (1 + erf(z / sqrt 2)) with erfc by Abramowitz & Stegun,
@@ -158,26 +173,69 @@ __device__ __forceinline__ float dec_gelu(float z) {
 }
 __device__ __forceinline__ float dec_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
+// 8 elements of h of row r of an entry, from the partial tiles of CTAs o0..o1
+// (in that order), activated and rounded to bf16.
+__device__ __forceinline__ uint4 sum_h_piece(const DecFfnArgs& p, int o0, int o1, int r, int kk,
+                                             bool swiglu) {
+  const int cl = swiglu ? kk & 63 : kk & 127;
+  const size_t tile = (size_t)p.row_cap * kDecBN;
+  float z[8], u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = u[i] = 0.f;
+#pragma unroll 2
+  for (int o = o0; o <= o1; ++o) {
+    const float4* s = reinterpret_cast<const float4*>(p.parts + (size_t)(o * 2 + (o == o0 ? 1 : 0)) * tile +
+                                                      r * kDecBN + cl);
+    const float4 a = __ldcg(s), b = __ldcg(s + 1);
+    z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
+    z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
+    if (swiglu) {
+      const float4 d = __ldcg(s + 16), e = __ldcg(s + 17);
+      u[0] += d.x; u[1] += d.y; u[2] += d.z; u[3] += d.w;
+      u[4] += e.x; u[5] += e.y; u[6] += e.z; u[7] += e.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = swiglu ? dec_silu(z[i]) * u[i] : dec_gelu(z[i]);
+  return make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                    pack_bf16x2(z[6], z[7]));
+}
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
 template <bool Q4, int NT>
 struct Cfg {
+  // consumer warps: KG groups of 4 across the columns; group i takes every
+  // KG-th chunk, so that a warp has a chunk's whole K to keep its pipes full
+  // between two waits.  With 64 rows the sums need the registers of 2 groups.
+  static constexpr int KG = Q4 && NT < 8 ? 3 : 2;
+  static constexpr int LOADERS = Q4 && NT == 8 ? 2 : 3;
+  static constexpr int CONSUMERS = DF_WN * KG;
+  static constexpr int THREADS = 32 * (1 + LOADERS + CONSUMERS);
   static constexpr int KC = Q4 ? kDecKC4 : kDecKC16;   // K rows of a chunk
   static constexpr int S_BYTES = Q4 ? 8 * 2 * 128 : 0; // scales: up to 8 groups x 2 boxes x 128 B
   static constexpr int W_STAGE = DF_W_BYTES + S_BYTES;
   static constexpr int B_TILE = KC * 16;               // 8 rows x KC bf16
   static constexpr int B_STAGE = B_TILE * NT;
-  static constexpr int B_STAGES = NT <= 2 ? 8 : Q4 && NT == 8 ? 3 : 4;
-  static constexpr int RED = DF_WN * 2 * NT * 4 * 32 * 4;  // cross-K sums
-  static constexpr int CTRL = 8 * 1024;
+  static constexpr int B_STAGES = !Q4 || NT == 1 ? 6 : KG;
+  static constexpr int RED = (KG - 1) * DF_WN * 2 * NT * 4 * 32 * 4;  // sums across the groups
+  static constexpr int CTRL = 12 * 1024;
   static constexpr int FIT = (DF_SMEM_LIMIT - 1024 - CTRL - RED - B_STAGE * B_STAGES) / W_STAGE;
-  static constexpr int W_STAGES = FIT < DF_MAX_WSTAGES ? FIT : DF_MAX_WSTAGES;
+  static constexpr int W_STAGES = (FIT < DF_MAX_WSTAGES ? FIT : DF_MAX_WSTAGES) / KG * KG;
   static constexpr size_t SMEM =
       1024 + (size_t)W_STAGES * W_STAGE + (size_t)B_STAGES * B_STAGE + RED + CTRL;
   static_assert(W_STAGES >= 4, "weight ring");
-  // a loader that has filled chunk q - DF_LOADERS knows chunk
-  // q - DF_LOADERS - B_STAGES to be consumed; its wait for q's stage tells
-  // phases apart by parity only if q - 2 B_STAGES is consumed too
-  static_assert(B_STAGES >= DF_LOADERS && B_STAGES <= DF_MAX_BSTAGES, "row ring");
   static_assert(SMEM <= DF_SMEM_LIMIT, "shared memory");
+  // A wait tells the phases of a barrier apart by parity only, so whoever
+  // waits for a stage's phase must know the one before it to be over.  A
+  // group finishes its chunks in order, but the groups (and the copies in
+  // flight) overtake each other: every stage therefore has one group and one
+  // loader of its own.
+  static_assert(W_STAGES % KG == 0 && B_STAGES % KG == 0 && B_STAGES % LOADERS == 0, "ring owners");
+  static_assert(B_STAGES <= DF_MAX_BSTAGES, "row ring");
 };
 
 struct Ctrl {
@@ -189,27 +247,120 @@ struct Ctrl {
   DecEntry ent[kDecMaxEntries];
   int2 owner[kDecMaxEntries];    // combine: CTAs of the column block's items
   uint16_t row_entry[MOED_MAX_ROWS];
+  int slot[MOED_MAX_ROWS];       // layer: [T, k]
+  float gate[MOED_MAX_ROWS];
 };
-static_assert(sizeof(Ctrl) <= 8 * 1024, "control area");
+static_assert(sizeof(Ctrl) <= 12 * 1024, "control area");
 
 // One product's chunks, in item order, dealt to the first G = min(CTAs, total)
 // CTAs: CTA c < G takes chunks [total c / G, total (c + 1) / G), at least one.
+// The host keeps total * CTAs below 2^32.
 struct Split {
-  long long total;
-  int G;
-  __device__ __forceinline__ Split(long long n, int ctas)
-      : total(n), G((int)min((long long)ctas, n)) {}
-  __device__ __forceinline__ long long start(int c) const { return c < G ? total * c / G : total; }
+  uint32_t total, G;
+  __device__ __forceinline__ Split(uint32_t n, uint32_t ctas) : total(n), G(min(ctas, n)) {}
+  __device__ __forceinline__ uint32_t start(uint32_t c) const {
+    return c < G ? total * c / G : total;
+  }
   // the CTA that holds chunk x: the largest c with total c / G < x + 1
-  __device__ __forceinline__ int owner(long long x) const {
+  __device__ __forceinline__ int owner(uint32_t x) const {
     return (int)(((x + 1) * G - 1) / total);
   }
 };
 
-template <bool Q4, int NT>
-__global__ void __launch_bounds__(DF_THREADS, 1)
+// A split item of the first product with at most this many rows is not put
+// together by the CTA that finishes it: the second product's row loaders add
+// its partial tiles when they read it.  That saves a ticket and a trip to
+// memory before the grid barrier, and costs every reader the sum and the
+// activation of the elements it reads, which a few rows' loaders have the time for.
+constexpr int kReaderRows = 2;
+
+// One chunk of 4-bit weights for a warp's 32 columns and the first NTA 8-row
+// tiles: acc += W^T x.  wl, bl: this lane's addresses in the stages (word row
+// 0 / 1 of a step by wofs); sl: its 4 columns' scales.  Everything is
+// unrolled and nothing branches, so that loads, unpacking and products of
+// different steps overlap.
+template <int NT, int NTA, int GRP>
+__device__ __forceinline__ void chunk_q4(float (&acc)[2][NT][4], uint32_t w0, const uint32_t (&wofs)[2],
+                                         uint32_t bl, uint32_t sl) {
+  constexpr int STEPS = GRP / 32;  // 32 rows of K each
+#pragma unroll
+  for (int grp = 0; grp < kDecKC4 / GRP; ++grp) {
+    float part[2][NTA][4];
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st) {
+      const uint32_t blk = (uint32_t)(grp * STEPS + st) >> 1, i = (uint32_t)(grp * STEPS + st) & 1;
+      uint32_t v[4];  // columns 4g .. 4g + 3 of 8 rows of K
+      lds128(w0 + blk * 1024 + wofs[i], v);
+      uint32_t b[NTA][4];
+#pragma unroll
+      for (int n = 0; n < NTA; ++n) lds128(bl + n * kDecKC4 * 16 + blk * 1024 + i * 512, b[n]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t va = v[2 * m], vb = v[2 * m + 1];
+        uint32_t a[8];
+        a[0] = q4_pair<0>(va);
+        a[1] = q4_pair<0>(vb);
+        a[2] = q4_pair<1>(va);
+        a[3] = q4_pair<1>(vb);
+        a[4] = q4_pair<2>(va);
+        a[5] = q4_pair<2>(vb);
+        a[6] = q4_pair<3>(va);
+        a[7] = q4_pair<3>(vb);
+#pragma unroll
+        for (int n = 0; n < NTA; ++n) {
+          if (st == 0)
+            mma_bf16_zero(part[m][n], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
+          else
+            mma_bf16(part[m][n], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
+          mma_bf16(part[m][n], a[4], a[5], a[6], a[7], b[n][2], b[n][3]);
+        }
+      }
+    }
+    uint32_t s01, s23;
+    lds64(sl + grp * 128, s01, s23);
+    const float s[4] = {64.f * bf16_lo(s01), 64.f * bf16_hi(s01), 64.f * bf16_lo(s23), 64.f * bf16_hi(s23)};
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NTA; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[m][n][r] = fmaf(s[2 * m + (r >> 1)], part[m][n][r], acc[m][n][r]);
+  }
+}
+
+// The same for a chunk of bf16 weights.
+template <int NT, int NTA>
+__device__ __forceinline__ void chunk_bf16(float (&acc)[2][NT][4], uint32_t w0,
+                                           const uint32_t (&wofs)[2], uint32_t bl) {
+#pragma unroll
+  for (int blk = 0; blk < kDecKC16 / 32; ++blk) {  // 32 rows of K
+    uint32_t a[2][2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) ldsm_x4_t(w0 + (blk * 32 + hf * 16) * 128 + wofs[m], a[m][hf]);
+#pragma unroll
+    for (int n = 0; n < NTA; ++n) {
+      uint32_t b[4];
+      lds128(bl + n * kDecKC16 * 16 + blk * 512, b);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        mma_bf16(acc[m][n], a[m][0][0], a[m][0][1], a[m][0][2], a[m][0][3], b[0], b[1]);
+        mma_bf16(acc[m][n], a[m][1][0], a[m][1][1], a[m][1][2], a[m][1][3], b[2], b[3]);
+      }
+    }
+  }
+}
+
+// GRP: rows per scale of 4-bit weights; 0: bf16 weights.
+template <int GRP, int NT>
+__global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     decode_ffn_kernel(const __grid_constant__ DecFfnMaps maps, const DecFfnArgs p) {
+  constexpr bool Q4 = GRP > 0;
   using C = Cfg<Q4, NT>;
+  constexpr int KG = C::KG;
+  constexpr int CTHREADS = 32 * C::CONSUMERS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -223,18 +374,26 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
   const int warp = tid >> 5;
   const int lane = tid & 31;
   const int cta = blockIdx.x;
-  const int G = gridDim.x;
+  const uint32_t G = gridDim.x;
   const bool layer = p.act != kDecNone;
   const bool swiglu = p.act == kDecSwiGLU;
 
+  if (tid == 64) {
+    tma_prefetch_desc(&maps.w1);
+    if (Q4) tma_prefetch_desc(&maps.s1);
+    if (layer) {
+      tma_prefetch_desc(&maps.w2);
+      if (Q4) tma_prefetch_desc(&maps.s2);
+    }
+  }
   if (tid == 0) {
     for (int i = 0; i < C::W_STAGES; ++i) {
       mbar_init(&c.wfull[i], 1);
-      mbar_init(&c.wempty[i], DF_CONSUMERS);
+      mbar_init(&c.wempty[i], DF_WN);
     }
     for (int i = 0; i < C::B_STAGES; ++i) {
       mbar_init(&c.bfull[i], 1);
-      mbar_init(&c.bempty[i], DF_CONSUMERS);
+      mbar_init(&c.bempty[i], DF_WN);
     }
     c.abort_flag = 0;
     fence_mbar_init();
@@ -243,10 +402,15 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
   pdl_wait();
   // the first kernel's list
   if (tid == 32) c.n_entries = min(__ldcg(p.ctrl + kDecCountOffset / 4), p.max_entries);
-  for (int i = tid; i < p.max_entries; i += DF_THREADS) {
+  for (int i = tid; i < p.max_entries; i += C::THREADS) {
     const int4 v = __ldcg(reinterpret_cast<const int4*>(p.entries) + i);
     c.ent[i] = DecEntry{v.x, v.y, v.z, v.w};
   }
+  if (layer)
+    for (int i = tid; i < p.T * p.k; i += C::THREADS) {
+      c.slot[i] = __ldcg(p.slot + i);
+      c.gate[i] = __ldcg(p.gate + i);
+    }
   __syncthreads();
   const int n_ent = c.n_entries;
   const WaitCtl wc{&c.abort_flag, p.status, p.wait_limit_ns};
@@ -254,7 +418,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
   if (n_ent == 0) {  // every assignment dropped: y = 0 (grouped products: nothing to write)
     if (layer) {
       const size_t n = (size_t)p.T * p.N2;  // N2 = H, a multiple of 8
-      for (size_t i = ((size_t)cta * DF_THREADS + tid) * 8; i < n; i += (size_t)G * DF_THREADS * 8)
+      for (size_t i = ((size_t)cta * C::THREADS + tid) * 8; i < n; i += (size_t)G * C::THREADS * 8)
         *reinterpret_cast<uint4*>(p.y + i) = make_uint4(0, 0, 0, 0);
     }
     return;
@@ -264,28 +428,22 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
   if (warp == 0) {
     // ------------------------------------------------ weight producer
     if (lane == 0) {
-      tma_prefetch_desc(&maps.w1);
-      if (Q4) tma_prefetch_desc(&maps.s1);
-      if (layer) {
-        tma_prefetch_desc(&maps.w2);
-        if (Q4) tma_prefetch_desc(&maps.s2);
-      }
       const uint64_t pol = l2_evict_first_policy();
-      const int srows = Q4 ? kDecKC4 / p.group : 0;  // scale rows of a chunk
+      constexpr int srows = Q4 ? kDecKC4 / (Q4 ? GRP : 1) : 0;  // scale rows of a chunk
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int ph = 0; ph < phases && ok; ++ph) {
         const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
-        const Split sp((long long)n_ent * NB * KCN, G);
+        const Split sp((uint32_t)n_ent * NB * KCN, G);
         const CUtensorMap* mw = ph ? &maps.w2 : &maps.w1;
         const CUtensorMap* ms = ph ? &maps.s2 : &maps.s1;
-        long long x = sp.start(cta);
-        const long long end = sp.start(cta + 1);
+        uint32_t x = sp.start(cta);
+        const uint32_t end = sp.start(cta + 1);
         while (x < end && ok) {
           const int item = (int)(x / KCN);
-          const int k0 = (int)(x - (long long)item * KCN);
-          const int k1 = (int)min((long long)KCN, k0 + (end - x));
+          const int k0 = (int)(x - (uint32_t)item * KCN);
+          const int k1 = (int)min((uint32_t)KCN, k0 + (end - x));
           const int ei = ph ? item % n_ent : item / NB;
           const int nb = ph ? item / n_ent : item % NB;
           const int e = c.ent[ei].expert;
@@ -335,23 +493,23 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp <= DF_LOADERS) {
+  } else if (warp <= C::LOADERS) {
     // ------------------------------------------------ row loaders
     const int lw = warp - 1;
-    const bool g32 = Q4 && p.group == 32;
+    constexpr bool g32 = GRP == 32;
     uint32_t q = 0;  // chunks of this CTA so far (both products)
     bool ok = true;
     for (int ph = 0; ph < phases && ok; ++ph) {
       const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
       const int K = ph ? p.K2 : p.K1;
-      const Split sp((long long)n_ent * NB * KCN, G);
-      long long x = sp.start(cta);
-      const long long end = sp.start(cta + 1);
+      const Split sp((uint32_t)n_ent * NB * KCN, G);
+      uint32_t x = sp.start(cta);
+      const uint32_t end = sp.start(cta + 1);
       if (ph == 1 && x < end) {  // every CTA's h must be there
         int got = 1;
         if (lane == 0) {
           const uint64_t t0 = global_timer_ns();
-          for (uint32_t it = 1; ld_acquire(p.barrier) < (unsigned)G; ++it) {
+          for (uint32_t it = 1; ld_acquire(p.barrier) < G; ++it) {
             if ((it & 63u) == 0) {
               if (c.abort_flag || global_timer_ns() - t0 > p.wait_limit_ns) {
                 if (!c.abort_flag) {
@@ -368,9 +526,10 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
       }
       while (x < end && ok) {
         const int item = (int)(x / KCN);
-        const int k0 = (int)(x - (long long)item * KCN);
-        const int k1 = (int)min((long long)KCN, k0 + (end - x));
-        const DecEntry en = c.ent[ph ? item % n_ent : item / NB];
+        const int k0 = (int)(x - (uint32_t)item * KCN);
+        const int k1 = (int)min((uint32_t)KCN, k0 + (end - x));
+        const int ei = ph ? item % n_ent : item / NB;
+        const DecEntry en = c.ent[ei];
         // source rows of this lane's two row numbers, lane and lane + 32
         const uint16_t* src = ph ? p.h : p.x;
         int r0 = en.row0 + lane, r1 = en.row0 + lane + 32;
@@ -380,19 +539,24 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
           if (lane + 32 < en.n) r1 = min(max(__ldg(p.perm + r1), 0), tk - 1) / p.k;
         }
         for (int kc = k0; kc < k1; ++kc, ++q) {
-          if (q % DF_LOADERS != (uint32_t)lw) continue;
+          if (q % C::LOADERS != (uint32_t)lw) continue;
           const uint32_t bs = q % C::B_STAGES;
           const uint32_t par = (q / C::B_STAGES) & 1;
-          if (!mbar_wait(&c.bempty[bs], par ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
           const uint32_t dst0 = smem_u32(sB + bs * C::B_STAGE);
           constexpr int PCS = C::KC / 8;       // 16-byte pieces of a row
           constexpr int RPP = 32 / PCS;        // rows per pass of the warp
           constexpr int UN = NT * 8 / RPP < 8 ? NT * 8 / RPP : 8;  // passes in flight together
           const int j = lane % PCS;
           const int kk = kc * C::KC + j * 8;
+          // this lane's elements of h: the CTAs that share their item
+          int o0 = 0, o1 = 0;
+          if (ph == 1 && en.n <= kReaderRows && kk < K) {
+            const int nb = swiglu ? kk >> 6 : kk >> 7;
+            const Split s1((uint32_t)n_ent * p.nb1 * p.kc1, G);
+            const uint32_t i0 = (uint32_t)(ei * p.nb1 + nb) * p.kc1;
+            o0 = s1.owner(i0);
+            o1 = s1.owner(i0 + p.kc1 - 1);
+          }
           for (int rb = 0; rb < en.n; rb += RPP * UN) {
             uint4 v[UN];
 #pragma unroll
@@ -400,8 +564,20 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
               const int r = rb + u * RPP + lane / PCS;
               const int sr = __shfl_sync(0xffffffffu, (rb + u * RPP) < 32 ? r0 : r1, r & 31);
               v[u] = make_uint4(0, 0, 0, 0);
-              if (r < en.n && kk < K)
+              if (r < en.n && kk < K && o0 == o1)
                 v[u] = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)sr * K + kk));
+            }
+            if (o0 != o1) {
+#pragma unroll
+              for (int u = 0; u < (kReaderRows + RPP - 1) / RPP; ++u) {
+                const int r = u * RPP + lane / PCS;
+                if (r < en.n) v[u] = sum_h_piece(p, o0, o1, r, kk, swiglu);
+              }
+            }
+            // the rows' loads are on their way before the stage is free
+            if (rb == 0 && !mbar_wait(&c.bempty[bs], par ^ 1u, wc)) {
+              ok = false;
+              break;
             }
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
@@ -428,6 +604,7 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
               }
             }
           }
+          if (!ok) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&c.bfull[bs]);
         }
@@ -436,53 +613,55 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
     }
   } else {
     // ------------------------------------------------ multiply, finish items
-    const int cw = warp - 1 - DF_LOADERS;
+    const int cw = warp - 1 - C::LOADERS;
     const int wn = cw & (DF_WN - 1);
     const int kg = cw / DF_WN;
     const int g = lane >> 2, t = lane & 3;
-    const int ctid = tid - 32 * (1 + DF_LOADERS);  // 0..255; < DF_FIN: kg = 0
-    int ws = 0, bs = 0;
+    const int ctid = tid - 32 * (1 + C::LOADERS);  // < DF_FIN: kg = 0
+    // this group's next chunk: its number q among the CTA's chunks (q mod KG =
+    // kg), its place in the rings and their parities
+    uint32_t q = (uint32_t)kg, qi = 0;
+    int ws = kg, bs = kg;
     uint32_t wpar = 0, bpar = 0;
+    static_assert(KG <= C::W_STAGES && KG <= C::B_STAGES, "a group steps over KG stages");
     bool ok = true;
+    if (layer)  // the entry of each row, for the combine
+      for (int i = ctid; i < n_ent; i += CTHREADS)
+        for (int r = 0; r < c.ent[i].n; ++r) c.row_entry[c.ent[i].row0 + r] = (uint16_t)i;
 
     for (int ph = 0; ph < phases && ok; ++ph) {
       const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
       const int N = ph ? p.N2 : p.N1;
-      const Split sp((long long)n_ent * NB * KCN, G);
+      const Split sp((uint32_t)n_ent * NB * KCN, G);
       const bool sg = ph == 0 && swiglu;
-      long long x = sp.start(cta);
-      const long long end = sp.start(cta + 1);
+      uint32_t x = sp.start(cta);
+      const uint32_t end = sp.start(cta + 1);
 
-      // tile column of m16 tile m, row g / row g + 8, and its place in a stage
-      //   plain:  columns 32 wn + 16 m + ..;  gated: tile 0 gate, tile 1 up,
-      //   both columns 16 wn + .. of their 64-column half
-      int tcol[2];
+      // this lane's place in a weight stage: tile columns 32 wn + ..
+      uint32_t wofs[2], sofs = 0;
+      if constexpr (Q4) {
+        // word row 2t + i of step i (4i + t with 32-row groups, whose rows
+        // must not mix): lane t holds 8 rows of K, the loaders order x alike
 #pragma unroll
-      for (int m = 0; m < 2; ++m) tcol[m] = sg ? m * 64 + 16 * wn : 32 * wn + 16 * m;
-      // bf16: ldmatrix rows of this lane; 4-bit: word offsets of this lane
-      uint32_t wofs[2][2];
-      uint32_t sofs[2];
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t row = GRP == 32 ? (uint32_t)(4 * i + t) : (uint32_t)(2 * t + i);
+          wofs[i] = (uint32_t)wn * 4096 + row * 128 + (((uint32_t)g ^ row) * 16);
+        }
+        sofs = (uint32_t)(wn >> 1) * (uint32_t)(kDecKC4 / (Q4 ? GRP : 1)) * 128 +
+               (uint32_t)((wn & 1) * 32 + 4 * g) * 2;
+      } else {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        sofs[m] = 0;
-        if constexpr (Q4) {
-          const uint32_t box = (uint32_t)(tcol[m] >> 5);
-          const uint32_t ch = (uint32_t)((tcol[m] & 31) >> 2) + (uint32_t)(g >> 1);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t row = p.group == 32 ? (uint32_t)(4 * i + t) : (uint32_t)(2 * t + i);
-            wofs[m][i] = box * 4096 + row * 128 + ((ch ^ row) * 16) + (uint32_t)(g & 1) * 8;
-          }
-          sofs[m] = (uint32_t)(tcol[m] >> 6) * (uint32_t)(kDecKC4 / p.group) * 128 +
-                    (uint32_t)((tcol[m] & 63) + 2 * g) * 2;
-        } else {
-          const uint32_t box = (uint32_t)(tcol[m] >> 6);
-          const uint32_t ch = (uint32_t)((tcol[m] & 63) >> 3) + (uint32_t)((lane >> 3) & 1);
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t ch = (uint32_t)((wn & 1) * 4 + m * 2) + (uint32_t)((lane >> 3) & 1);
           const uint32_t row = (uint32_t)((lane >> 4) * 8 + (lane & 7));
-          wofs[m][0] = box * 8192 + row * 128 + ((ch ^ (row & 7)) * 16);
-          wofs[m][1] = 0;
+          wofs[m] = (uint32_t)(wn >> 1) * 8192 + row * 128 + ((ch ^ (row & 7)) * 16);
         }
       }
+      // element (m, n, r) of this lane: tile column and row of the entry
+      auto col_of = [&](int m, int r) {
+        return 32 * wn + (Q4 ? 4 * g + 2 * m + (r >> 1) : 16 * m + g + 8 * (r >> 1));
+      };
+      auto row_of = [&](int n, int r) { return n * 8 + 2 * t + (r & 1); };
 
       int cur_nb = -1;  // second product: column block of the items done so far
       while (ok) {
@@ -492,34 +671,31 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
         if (ph == 1 && cur_nb >= 0 && nb != cur_nb) {
           // ---- this CTA's part of column block cur_nb is written: count in,
           // and combine the block if it is the last part
-          __threadfence();
-          named_sync(BAR_CONS, 32 * DF_CONSUMERS);
-          const long long b0 = (long long)cur_nb * n_ent * KCN;
-          if (ctid == 0) {
-            const int parts =
-                sp.owner(b0 + (long long)n_ent * KCN - 1) - sp.owner(b0) + 1;
-            c.last = atomicAdd(p.col_tickets + cur_nb, 1u) == (unsigned)(parts - 1);
+          const uint32_t b0 = (uint32_t)cur_nb * n_ent * KCN;
+          for (int i = ctid; i < n_ent; i += CTHREADS) {
+            const uint32_t i0 = b0 + (uint32_t)i * KCN;
+            c.owner[i] = make_int2(sp.owner(i0), sp.owner(i0 + KCN - 1));
           }
-          named_sync(BAR_CONS, 32 * DF_CONSUMERS);
-          if (c.last) {
+          named_sync(BAR_CONS, CTHREADS);
+          if (ctid == 0) {
+            const int parts = c.owner[n_ent - 1].y - c.owner[0].x + 1;
             __threadfence();
-            for (int i = ctid; i < n_ent; i += 32 * DF_CONSUMERS) {
-              const long long i0 = b0 + (long long)i * KCN;
-              c.owner[i] = make_int2(sp.owner(i0), sp.owner(i0 + KCN - 1));
-              const DecEntry en = c.ent[i];
-              for (int r = 0; r < en.n; ++r) c.row_entry[en.row0 + r] = (uint16_t)i;
-            }
-            named_sync(BAR_CONS, 32 * DF_CONSUMERS);
+            c.last = atomicAdd(p.col_tickets + cur_nb, 1u) == (unsigned)(parts - 1);
+            __threadfence();
+          }
+          named_sync(BAR_CONS, CTHREADS);
+          if (c.last) {
             const int col0 = cur_nb * kDecBN;
-            for (int i = ctid; i < p.T * (kDecBN / 2); i += 32 * DF_CONSUMERS) {
+            for (int i = ctid; i < p.T * (kDecBN / 2); i += CTHREADS) {
               const int tok = i / (kDecBN / 2);
               const int cl = (i % (kDecBN / 2)) * 2;
               if (col0 + cl >= N) continue;
               float y0 = 0.f, y1 = 0.f;
+#pragma unroll 4
               for (int j = 0; j < p.k; ++j) {
-                const int row = __ldcg(p.slot + tok * p.k + j);
+                const int row = c.slot[tok * p.k + j];
                 if (row < 0) continue;
-                const float w = __ldcg(p.gate + tok * p.k + j);
+                const float w = c.gate[tok * p.k + j];
                 const int ei = c.row_entry[row];
                 const int2 own = c.owner[ei];
                 float2 v;
@@ -528,9 +704,10 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
                 } else {
                   v = make_float2(0.f, 0.f);
                   const int rr = row - c.ent[ei].row0;
+#pragma unroll 4
                   for (int o = own.x; o <= own.y; ++o) {
                     const float2 u = __ldcg(reinterpret_cast<const float2*>(
-                        p.parts + ((size_t)(o * 2 + (o == own.x ? 1 : 0)) * p.row_cap + rr) * kDecBN +
+                        p.parts2 + ((size_t)(o * 2 + (o == own.x ? 1 : 0)) * p.row_cap + rr) * kDecBN +
                         cl));
                     v.x += u.x;
                     v.y += u.y;
@@ -545,8 +722,8 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
         }
         if (!more) break;
         cur_nb = nb;
-        const int k0 = (int)(x - (long long)item * KCN);
-        const int k1 = (int)min((long long)KCN, k0 + (end - x));
+        const int k0 = (int)(x - (uint32_t)item * KCN);
+        const int k1 = (int)min((uint32_t)KCN, k0 + (end - x));
         const DecEntry en = c.ent[ph ? item % n_ent : item / NB];
 
         float acc[2][NT][4];
@@ -557,145 +734,75 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[m][n][r] = 0.f;
 
-        for (int kc = k0; kc < k1; ++kc) {
+        for (; q < qi + (uint32_t)(k1 - k0); q += KG) {
           if (!mbar_wait(&c.wfull[ws], wpar, wc) || !mbar_wait(&c.bfull[bs], bpar, wc)) {
             ok = false;
             break;
           }
           const uint32_t w0 = smem_u32(sW + ws * DF_W_BYTES);
           const uint32_t b0 = smem_u32(sB + bs * C::B_STAGE) + (uint32_t)(t * 128 + ((g ^ (2 * t)) * 16));
-          if constexpr (Q4) {
-            const uint32_t s0 = smem_u32(sS + ws * C::S_BYTES);
-            float part[2][NT][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) part[m][n][r] = 0.f;
-#pragma unroll
-            for (int bb = 0; bb < 2; ++bb) {  // 64 rows of K
-              const uint32_t blk = (uint32_t)(kg * 2 + bb);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {   // 32 of them
-                uint32_t a[2][8];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  uint32_t va, vb;
-                  lds64(w0 + blk * 1024 + wofs[m][i], va, vb);
-                  a[m][0] = q4_pair<0>(va);
-                  a[m][1] = q4_pair<0>(vb);
-                  a[m][2] = q4_pair<1>(va);
-                  a[m][3] = q4_pair<1>(vb);
-                  a[m][4] = q4_pair<2>(va);
-                  a[m][5] = q4_pair<2>(vb);
-                  a[m][6] = q4_pair<3>(va);
-                  a[m][7] = q4_pair<3>(vb);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  if (n * 8 >= en.n) break;
-                  uint32_t b[4];
-                  lds128(b0 + n * C::B_TILE + blk * 1024 + i * 512, b);
-#pragma unroll
-                  for (int m = 0; m < 2; ++m) {
-                    mma_bf16(part[m][n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
-                    mma_bf16(part[m][n], a[m][4], a[m][5], a[m][6], a[m][7], b[2], b[3]);
-                  }
-                }
-                // end of a scale group: every 32, 64 or 128 rows
-                const bool flush = i == 1 ? (bb == 1 || p.group <= 64) : p.group == 32;
-                if (flush) {
-                  const uint32_t grp = (blk * 64 + (uint32_t)i * 32) / (uint32_t)p.group;
-#pragma unroll
-                  for (int m = 0; m < 2; ++m) {
-                    const uint32_t sv = lds32(s0 + grp * 128 + sofs[m]);
-                    const float sa = bf16_lo(sv), sb = bf16_hi(sv);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                      if (n * 8 >= en.n) break;
-                      acc[m][n][0] = fmaf(sa, part[m][n][0], acc[m][n][0]);
-                      acc[m][n][1] = fmaf(sa, part[m][n][1], acc[m][n][1]);
-                      acc[m][n][2] = fmaf(sb, part[m][n][2], acc[m][n][2]);
-                      acc[m][n][3] = fmaf(sb, part[m][n][3], acc[m][n][3]);
-#pragma unroll
-                      for (int r = 0; r < 4; ++r) part[m][n][r] = 0.f;
-                    }
-                  }
-                }
-              }
-            }
-          } else {
-            const uint32_t blk = (uint32_t)kg;  // 32 rows of K
-            uint32_t a[2][2][4];
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf)
-                ldsm_x4_t(w0 + (blk * 32 + hf * 16) * 128 + wofs[m][0], a[m][hf]);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (n * 8 >= en.n) break;
-              uint32_t b[4];
-              lds128(b0 + n * C::B_TILE + blk * 512, b);
-#pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                mma_bf16(acc[m][n], a[m][0][0], a[m][0][1], a[m][0][2], a[m][0][3], b[0], b[1]);
-                mma_bf16(acc[m][n], a[m][1][0], a[m][1][1], a[m][1][2], a[m][1][3], b[2], b[3]);
-              }
-            }
-          }
+          const auto chunk = [&](auto nta) {
+            constexpr int NTA = decltype(nta)::value;
+            if constexpr (Q4)
+              chunk_q4<NT, NTA, GRP>(acc, w0, wofs, b0, smem_u32(sS + ws * C::S_BYTES) + sofs);
+            else
+              chunk_bf16<NT, NTA>(acc, w0, wofs, b0);
+          };
+          if (NT == 1 || en.n <= 8)
+            chunk(Int<1>{});
+          else if (NT == 2 || en.n <= 16)
+            chunk(Int<NT < 2 ? NT : 2>{});
+          else if (NT == 4 || en.n <= 32)
+            chunk(Int<NT < 4 ? NT : 4>{});
+          else
+            chunk(Int<NT>{});
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&c.wempty[ws]);
             mbar_arrive(&c.bempty[bs]);
           }
-          if (++ws == C::W_STAGES) {
-            ws = 0;
+          if ((ws += KG) >= C::W_STAGES) {
+            ws -= C::W_STAGES;
             wpar ^= 1u;
           }
-          if (++bs == C::B_STAGES) {
-            bs = 0;
+          if ((bs += KG) >= C::B_STAGES) {
+            bs -= C::B_STAGES;
             bpar ^= 1u;
           }
         }
-        // ---- sum of the two K halves: the second half's warps hand over.  A
-        // wait that ran out in any warp ends the work of all of them here.
-        if (named_any(BAR_CONS, 32 * DF_CONSUMERS, !ok)) {
+        qi += (uint32_t)(k1 - k0);
+        // ---- sum over the warps that split K: the others hand over to kg = 0.
+        // A wait that ran out in any warp ends the work of all of them here.
+        if (kg > 0) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                sRed[(((kg - 1) * 2 * NT + m * NT + n) * 4 + r) * DF_FIN + wn * 32 + lane] = acc[m][n][r];
+        }
+        if (named_any(BAR_CONS, CTHREADS, !ok)) {
           ok = false;
           break;
         }
-        if (kg == 1) {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                sRed[((m * NT + n) * 4 + r) * DF_FIN + wn * 32 + lane] = acc[m][n][r];
-        }
-        named_sync(BAR_CONS, 32 * DF_CONSUMERS);
         if (kg == 0) {
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
+          for (int u = 0; u < KG - 1; ++u)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[m][n][r] += sRed[((m * NT + n) * 4 + r) * DF_FIN + wn * 32 + lane];
-
-          // element (m, n, r) of this lane: tile column and row of the entry
-          auto col_of = [&](int m, int r) {
-            return tcol[m] + (Q4 ? 2 * g + (r >> 1) : g + 8 * (r >> 1));
-          };
-          auto row_of = [&](int n, int r) { return n * 8 + 2 * t + (r & 1); };
-
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  acc[m][n][r] += sRed[((u * 2 * NT + m * NT + n) * 4 + r) * DF_FIN + wn * 32 + lane];
           const bool whole = k0 == 0 && k1 == KCN;
           bool write = whole;
           if (!whole) {
             // partial tile of this CTA: slot 0 if the item began in an
             // earlier CTA, else slot 1
-            float* mine = p.parts + (size_t)(cta * 2 + (k0 > 0 ? 0 : 1)) * p.row_cap * kDecBN;
+            float* mine = (ph ? p.parts2 : p.parts) +
+                          (size_t)(cta * 2 + (k0 > 0 ? 0 : 1)) * p.row_cap * kDecBN;
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -703,23 +810,17 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                   if (row_of(n, r) < en.n) mine[row_of(n, r) * kDecBN + col_of(m, r)] = acc[m][n][r];
-            if (ph == 0) {
-              const long long i0 = (long long)item * KCN;
-              __threadfence();
+            if (ph == 0 && (!layer || en.n > kReaderRows)) {
+              const uint32_t i0 = (uint32_t)item * KCN;
+              const int c0 = sp.owner(i0), c1 = sp.owner(i0 + KCN - 1);
               named_sync(BAR_FIN, DF_FIN);
-              int c0 = 0, c1 = 0;
               if (ctid == 0) {
-                c0 = sp.owner(i0);
-                c1 = sp.owner(i0 + KCN - 1);
-                c.last = atomicAdd(p.item_tickets + c0, 1u) == (unsigned)(c1 - c0)
-                             ? (c0 << 16 | c1) + 1
-                             : 0;
+                __threadfence();
+                c.last = atomicAdd(p.item_tickets + c0, 1u) == (unsigned)(c1 - c0);
+                __threadfence();
               }
               named_sync(BAR_FIN, DF_FIN);
               if (c.last) {
-                c0 = (c.last - 1) >> 16;
-                c1 = (c.last - 1) & 0xFFFF;
-                __threadfence();
                 write = true;
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
@@ -752,89 +853,96 @@ __global__ void __launch_bounds__(DF_THREADS, 1)
                   }
             } else {
               uint16_t* out = layer ? p.h : p.y;
+              if (sg) {  // gate columns meet up columns: warps 2, 3 hand over to 0, 1
+                named_sync(BAR_FIN, DF_FIN);  // sRed is read
+                if (wn >= 2) {
 #pragma unroll
-              for (int m = 0; m < 2; ++m) {
-                if (sg && m == 1) break;
+                  for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    const int col = nb * (sg ? 64 : kDecBN) + col_of(m, r);
-                    if (row_of(n, r) < en.n && col < N) {
-                      float v = acc[m][n][r];
-                      if (sg)
-                        v = dec_silu(v) * acc[1][n][r];
-                      else if (layer)
-                        v = dec_gelu(v);
-                      out[(size_t)(en.row0 + row_of(n, r)) * N + col] =
-                          (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+                      for (int r = 0; r < 4; ++r)
+                        sRed[((m * NT + n) * 4 + r) * 64 + (wn - 2) * 32 + lane] = acc[m][n][r];
+                }
+                named_sync(BAR_FIN, DF_FIN);
+              }
+              if (!sg || wn < 2) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                      const int col = nb * (sg ? 64 : kDecBN) + col_of(m, r);
+                      if (row_of(n, r) < en.n && col < N) {
+                        float v = acc[m][n][r];
+                        if (sg)
+                          v = dec_silu(v) * sRed[((m * NT + n) * 4 + r) * 64 + wn * 32 + lane];
+                        else if (layer)
+                          v = dec_gelu(v);
+                        out[(size_t)(en.row0 + row_of(n, r)) * N + col] =
+                            (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+                      }
                     }
-                  }
               }
             }
           }
         }
         x += k1 - k0;
+        // sRed is read (every consumer passes here once an item)
+        if (x < end) named_sync(BAR_CONS, CTHREADS);
       }
       if (ph == 0 && layer) {
         // this CTA's h is written: arrive at the grid barrier
-        __threadfence();
-        named_sync(BAR_CONS, 32 * DF_CONSUMERS);
-        if (ctid == 0) red_release(p.barrier, 1u);
+        named_sync(BAR_CONS, CTHREADS);
+        if (ctid == 0) {
+          __threadfence();
+          red_release(p.barrier, 1u);
+        }
       }
     }
   }
 }
 
-template <bool Q4, int NT>
+template <int GRP, int NT>
 cudaError_t ffn_launch(const DecFfnMaps& m, const DecFfnArgs& a, int ctas, cudaStream_t st) {
+  using C = Cfg<(GRP > 0), NT>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, 1, 1);
-  cfg.blockDim = dim3(DF_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<Q4, NT>::SMEM;
+  cfg.blockDim = dim3((unsigned)C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_ffn_kernel<Q4, NT>, m, a);
+  return cudaLaunchKernelEx(&cfg, decode_ffn_kernel<GRP, NT>, m, a);
 }
 
-template <bool Q4, int NT>
-cudaError_t ffn_attr() {
-  return cudaFuncSetAttribute(decode_ffn_kernel<Q4, NT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<Q4, NT>::SMEM);
-}
-
-template <bool Q4>
+template <int GRP>
 cudaError_t ffn_rows(const DecFfnMaps& m, const DecFfnArgs& a, int ctas, cudaStream_t st) {
-  if (a.row_cap <= 8) return ffn_launch<Q4, 1>(m, a, ctas, st);
-  if (a.row_cap <= 16) return ffn_launch<Q4, 2>(m, a, ctas, st);
-  if (a.row_cap <= 32) return ffn_launch<Q4, 4>(m, a, ctas, st);
-  return ffn_launch<Q4, 8>(m, a, ctas, st);
+  if (a.row_cap <= 8) return ffn_launch<GRP, 1>(m, a, ctas, st);
+  if (a.row_cap <= 16) return ffn_launch<GRP, 2>(m, a, ctas, st);
+  if (a.row_cap <= 32) return ffn_launch<GRP, 4>(m, a, ctas, st);
+  return ffn_launch<GRP, 8>(m, a, ctas, st);
 }
 
-}  // namespace
-
-cudaError_t launch_decode_ffn(bool q4, const DecFfnMaps& m, const DecFfnArgs& a, int ctas,
-                              cudaStream_t st) {
-  return q4 ? ffn_rows<true>(m, a, ctas, st) : ffn_rows<false>(m, a, ctas, st);
+template <int GRP, int NT>
+cudaError_t ffn_attr() {
+  return cudaFuncSetAttribute(decode_ffn_kernel<GRP, NT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Cfg<(GRP > 0), NT>::SMEM);
 }
 
-cudaError_t decode_route_set_attributes();
-
-cudaError_t decode_set_attributes() {
-  cudaError_t e = decode_route_set_attributes();
-  if (e == cudaSuccess) e = ffn_attr<false, 1>();
-  if (e == cudaSuccess) e = ffn_attr<false, 2>();
-  if (e == cudaSuccess) e = ffn_attr<false, 4>();
-  if (e == cudaSuccess) e = ffn_attr<false, 8>();
-  if (e == cudaSuccess) e = ffn_attr<true, 1>();
-  if (e == cudaSuccess) e = ffn_attr<true, 2>();
-  if (e == cudaSuccess) e = ffn_attr<true, 4>();
-  if (e == cudaSuccess) e = ffn_attr<true, 8>();
+template <int GRP>
+cudaError_t ffn_attrs() {
+  cudaError_t e = ffn_attr<GRP, 1>();
+  if (e == cudaSuccess) e = ffn_attr<GRP, 2>();
+  if (e == cudaSuccess) e = ffn_attr<GRP, 4>();
+  if (e == cudaSuccess) e = ffn_attr<GRP, 8>();
   return e;
 }
 
+}  // namespace
 }  // namespace moe

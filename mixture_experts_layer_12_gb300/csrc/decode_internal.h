@@ -72,7 +72,8 @@ struct DecFfnArgs {
   unsigned* barrier;
   unsigned* item_tickets;
   unsigned* col_tickets;
-  float* parts;          // [CTAs][2][row_cap][128] partial tiles of split items
+  float* parts;          // [CTAs][2][row_cap][128] partial tiles of the first product's split items
+  float* parts2;         // the second product's: the first's are still being read
   int row_cap;           // rows of an entry at most, rounded up to 8
   float* yfull;          // layer: [T*k, H] fp32 expert outputs of whole items
   uint16_t* h;           // layer: [T*k, F]
@@ -83,7 +84,7 @@ struct DecFfnArgs {
   uint16_t* y;
   int T, k;
   int act;               // kDec*
-  int group;             // 4-bit: rows per scale
+  int group;             // 4-bit: rows per scale; 0: bf16
   int K1, N1;            // first product: x [., K1] -> N1 columns of h (or y)
   int nb1, kc1;          // its column blocks and K chunks
   int K2, N2, nb2, kc2;  // second product (layer)
@@ -97,8 +98,18 @@ struct DecFfnMaps {
 constexpr int kDecBN = 128;    // columns of an item's weight tile
 constexpr int kDecKC16 = 64;   // K rows of a chunk, bf16 weights
 constexpr int kDecKC4 = 256;   // K rows of a chunk, 4-bit weights
-cudaError_t launch_decode_ffn(bool q4, const DecFfnMaps& m, const DecFfnArgs& a, int ctas,
-                              cudaStream_t st);
+// one translation unit per weight type (bf16; 4 bits with a scale per 32, 64
+// or 128 rows)
+#define DECODE_FFN_UNIT(name)                                                                    \
+  cudaError_t launch_decode_ffn_##name(const DecFfnMaps& m, const DecFfnArgs& a, int ctas,       \
+                                       cudaStream_t st);                                         \
+  cudaError_t decode_ffn_##name##_set_attributes();
+DECODE_FFN_UNIT(bf16)
+DECODE_FFN_UNIT(q4_32)
+DECODE_FFN_UNIT(q4_64)
+DECODE_FFN_UNIT(q4_128)
+#undef DECODE_FFN_UNIT
+cudaError_t decode_route_set_attributes();
 
 // ---- 4-bit weights
 cudaError_t launch_quantize_q4(int E, int K, int N, int group, const uint16_t* w, uint32_t* codes,
