@@ -26,7 +26,7 @@ constexpr int kDecMaxEntries = kMaxExperts + MOED_MAX_ROWS / kDecRows;
 // every call.  bytes: [status 64 | barrier 64 | item tickets | n_entries].
 constexpr size_t kDecBarrierOffset = 64;
 constexpr size_t kDecTicketOffset = 128;    // kDecMaxCtas ints (<= 152 * 4 = 608 bytes)
-constexpr size_t kDecCountOffset = 960;     // number of entries
+constexpr size_t kDecCountOffset = 960;     // number of entries, rows of the longest
 constexpr size_t kDecEntryOffset = 1024;    // entries, then the column tickets
 constexpr int kDecCtrlInts = 240;           // ints zeroed: everything before n_entries
 

@@ -102,7 +102,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   __shared__ int s_ids[DR_MAX_ASSIGN];
   __shared__ int s_wc[DR_CHUNKS][kMaxExperts];
   __shared__ int s_off[kMaxExperts + 1];
-  __shared__ int s_scan[2][DR_WARPS];
+  __shared__ int s_scan[3][DR_WARPS];
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -310,10 +310,13 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
     s_scan[0][warp] = incl;
     s_scan[1][warp] = __popc(hit);
   }
+  const int longest = __reduce_max_sync(0xffffffffu, kept);
+  if (lane == 0) s_scan[2][warp] = longest;
   __syncthreads();
-  int base = 0, hbase = 0, total = 0, htotal = 0;
+  int base = 0, hbase = 0, total = 0, htotal = 0, max_rows = 0;
 #pragma unroll
   for (int w = 0; w < DR_WARPS; ++w) {
+    max_rows = max(max_rows, s_scan[2][w]);
     if (w < warp) {
       base += s_scan[0][w];
       hbase += s_scan[1][w];
@@ -332,6 +335,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   if (tid == 0) {
     a.offsets[E] = total;
     a.ctrl[kDecCountOffset / 4] = htotal;
+    a.ctrl[kDecCountOffset / 4 + 1] = max_rows;
   }
   __syncthreads();
 #pragma unroll
@@ -353,7 +357,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
 
 // Entries of the grouped products: segment i's rows in blocks of kDecRows.
 __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
-  __shared__ int s_scan[8];
+  __shared__ int s_scan[8], s_rows[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   pdl_wait();
@@ -373,18 +377,26 @@ __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
     const int v = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += v;
   }
-  if (lane == 31) s_scan[warp] = incl;
+  const int longest = __reduce_max_sync(0xffffffffu, min(n, kDecRows));
+  if (lane == 31) {
+    s_scan[warp] = incl;
+    s_rows[warp] = longest;
+  }
   __syncthreads();
-  int base = 0, total = 0;
+  int base = 0, total = 0, max_rows = 0;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
     if (w < warp) base += s_scan[w];
     total += s_scan[w];
+    max_rows = max(max_rows, s_rows[w]);
   }
   int at = base + incl - blocks;
   for (int b = 0; b < blocks && at < a.max_entries; ++b, ++at)
     a.entries[at] = DecEntry{tid % a.E, o0 + b * kDecRows, min(kDecRows, n - b * kDecRows), 0};
-  if (tid == 0) a.ctrl[kDecCountOffset / 4] = min(total, a.max_entries);
+  if (tid == 0) {
+    a.ctrl[kDecCountOffset / 4] = min(total, a.max_entries);
+    a.ctrl[kDecCountOffset / 4 + 1] = max_rows;
+  }
 }
 
 template <int NT, int NCH>
