@@ -102,7 +102,7 @@ int device_setup(int* sms) {
 int encode_map_as(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle,
                   const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                   const uint32_t* box, const char* what) {
-  uint32_t estr[3] = {1, 1, 1};
+  uint32_t estr[5] = {1, 1, 1, 1, 1};
   CUresult r = g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides_bytes, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

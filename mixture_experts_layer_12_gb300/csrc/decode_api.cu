@@ -108,30 +108,27 @@ int check_q4(int32_t E, int32_t K, int32_t N, int32_t group) {
   return MOE_OK;
 }
 
-// W [E, K, N] bf16 in boxes of 64 x 64
-int map_bf16(CUtensorMap* m, const void* w, int E, int K, int N, const char* what) {
-  const uint64_t dims[3] = {(uint64_t)N, (uint64_t)K, (uint64_t)E};
-  const uint64_t strides[2] = {(uint64_t)N * 2, (uint64_t)K * N * 2};
-  const uint32_t box[3] = {64, kDecKC16, 1};
-  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, w, 3, dims,
-                       strides, box, what);
-}
-
-// codes [E, K/8, N] in boxes of 32 x 32 words, scales [E, K/group, N] in
-// boxes of 64 columns and one chunk's rows
-int map_q4(CUtensorMap* mw, CUtensorMap* ms, const void* codes, const void* scales, int E, int K,
-           int N, int group, const char* what) {
-  const uint64_t wd[3] = {(uint64_t)N, (uint64_t)K / 8, (uint64_t)E};
-  const uint64_t wst[2] = {(uint64_t)N * 4, (uint64_t)K / 8 * N * 4};
-  const uint32_t wb[3] = {32, kDecKC4 / 8, 1};
-  int rc = encode_map_as(mw, CU_TENSOR_MAP_DATA_TYPE_INT32, CU_TENSOR_MAP_SWIZZLE_128B, codes, 3, wd,
-                         wst, wb, what);
-  if (rc != MOE_OK) return rc;
-  const uint64_t sd[3] = {(uint64_t)N, (uint64_t)(K / group), (uint64_t)E};
-  const uint64_t sst[2] = {(uint64_t)N * 2, (uint64_t)(K / group) * N * 2};
-  const uint32_t sb[3] = {64, (uint32_t)(kDecKC4 / group), 1};
-  return encode_map_as(ms, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_NONE, scales, 3, sd,
-                       sst, sb, what);
+// The weights' tensor map (see DecFfnMaps): W [E, K, N] bf16, or words
+// [E, K/8, N]; `half`: columns of a gate / up half (N where there is none).
+int map_weights(CUtensorMap* m, int* blocked, const void* w, bool q4, int E, int K, int N, int half,
+                const char* what) {
+  const uint64_t rows = q4 ? K / 8 : K;
+  const uint64_t esize = q4 ? 4 : 2;
+  const uint64_t blk = 128 / esize;
+  const uint32_t box_rows = q4 ? kDecKC4 / 8 : kDecKC16;
+  const CUtensorMapDataType type = q4 ? CU_TENSOR_MAP_DATA_TYPE_INT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const bool gated = half != N;
+  *blocked = half % (int)blk == 0;
+  if (*blocked) {
+    const uint64_t dims[4] = {blk, rows, (uint64_t)N / blk, (uint64_t)E};
+    const uint64_t strides[3] = {(uint64_t)N * esize, 128, rows * N * esize};
+    const uint32_t box[4] = {(uint32_t)blk, box_rows, (uint32_t)((gated ? 64 : kDecBN) / blk), 1};
+    return encode_map_as(m, type, CU_TENSOR_MAP_SWIZZLE_128B, w, 4, dims, strides, box, what);
+  }
+  const uint64_t dims[3] = {(uint64_t)N, rows, (uint64_t)E};
+  const uint64_t strides[2] = {(uint64_t)N * esize, rows * N * esize};
+  const uint32_t box[3] = {(uint32_t)blk, box_rows, 1};
+  return encode_map_as(m, type, CU_TENSOR_MAP_SWIZZLE_128B, w, 3, dims, strides, box, what);
 }
 
 int empty_call(void* ws, int32_t* counts, int32_t* offsets, int E, cudaStream_t st) {
@@ -191,15 +188,9 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   const bool swiglu = s->expert_act == MOE_EXPERT_SWIGLU;
   const int N1 = swiglu ? 2 * s->F : s->F;
   DecFfnMaps maps;
-  if (wt.q4) {
-    if ((rc = map_q4(&maps.w1, &maps.s1, wt.w1, wt.s1, s->E, s->H, N1, wt.group, "W1")) != MOE_OK) return rc;
-    if ((rc = map_q4(&maps.w2, &maps.s2, wt.w2, wt.s2, s->E, s->F, s->H, wt.group, "W2")) != MOE_OK) return rc;
-  } else {
-    if ((rc = map_bf16(&maps.w1, wt.w1, s->E, s->H, N1, "W1")) != MOE_OK) return rc;
-    if ((rc = map_bf16(&maps.w2, wt.w2, s->E, s->F, s->H, "W2")) != MOE_OK) return rc;
-    maps.s1 = maps.w1;  // not used
-    maps.s2 = maps.w2;
-  }
+  int blocked1 = 0, blocked2 = 0;
+  if ((rc = map_weights(&maps.w1, &blocked1, wt.w1, wt.q4, s->E, s->H, N1, s->F, "W1")) != MOE_OK) return rc;
+  if ((rc = map_weights(&maps.w2, &blocked2, wt.w2, wt.q4, s->E, s->F, s->H, s->H, "W2")) != MOE_OK) return rc;
 
   const int kc = wt.q4 ? kDecKC4 : kDecKC16;
   const int cols1 = swiglu ? 64 : kDecBN;  // columns of h per item
@@ -243,6 +234,10 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.parts2 = at<float>(ws, L.parts2);
   fa.yfull = at<float>(ws, L.yfull);
   fa.h = at<uint16_t>(ws, L.h);
+  fa.s1 = static_cast<const uint16_t*>(wt.s1);
+  fa.s2 = static_cast<const uint16_t*>(wt.s2);
+  fa.blocked1 = blocked1;
+  fa.blocked2 = blocked2;
   fa.x = x;
   fa.perm = perm;
   fa.slot = slot;
@@ -341,9 +336,9 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   const int nb = (N + kDecBN - 1) / kDecBN, kc = (K + kDecKC4 - 1) / kDecKC4;
   if ((rc = check_chunks(L.max_entries, nb, kc)) != MOE_OK) return rc;
   DecFfnMaps maps;
-  if ((rc = map_q4(&maps.w1, &maps.s1, codes, scales, E, K, N, group, "W")) != MOE_OK) return rc;
+  int blocked = 0;
+  if ((rc = map_weights(&maps.w1, &blocked, codes, true, E, K, N, N, "W")) != MOE_OK) return rc;
   maps.w2 = maps.w1;  // not used
-  maps.s2 = maps.s1;
 
   DecPrepArgs pa;
   pa.seg_offsets = seg_offsets;
@@ -364,6 +359,8 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   fa.item_tickets = at<unsigned>(ws, kDecTicketOffset);
   fa.parts = at<float>(ws, L.parts);
   fa.row_cap = L.row_cap;
+  fa.s1 = scales;
+  fa.blocked1 = blocked;
   fa.x = x;
   fa.y = y;
   fa.T = rows;

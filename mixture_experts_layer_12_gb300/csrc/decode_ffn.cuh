@@ -100,6 +100,15 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(pol)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m, uint64_t* bar,
+                                                 int c0, int c1, int c2, int c3, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(pol)
+      : "memory");
+}
 __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   unsigned v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -253,7 +262,7 @@ struct Cfg {
   static constexpr int THREADS = 32 * (2 + CONSUMERS);
   static constexpr int KC = Q4 ? kDecKC4 : kDecKC16;    // K rows of a chunk
   static constexpr int PITCH = KC * 2 + 16;             // bytes of a row's chunk: no bank conflicts
-  static constexpr int S_BYTES = Q4 ? 8 * 2 * 128 : 0;  // scales: up to 8 groups x 2 boxes x 128 B
+  static constexpr int S_BYTES = Q4 ? 8 * 256 : 0;      // scales: up to 8 groups x 128 columns
   static constexpr int W_STAGE = DF_W_BYTES + S_BYTES;
   static constexpr int RED_GROUP = DF_FIN * 2 * NT * 4;    // floats a group hands over
   static constexpr int RED = KG * RED_GROUP * 4;
@@ -306,7 +315,7 @@ __device__ __forceinline__ void chunk_q4(float (&acc)[2][NT][4], uint32_t w0, co
 #pragma unroll
   for (int grp = 0; grp < kDecKC4 / GRP; ++grp) {
     uint32_t s01, s23;
-    lds64(sl + grp * 128, s01, s23);
+    lds64(sl + grp * 256, s01, s23);
     const float s[4] = {64.f * bf16_lo(s01), 64.f * bf16_hi(s01), 64.f * bf16_lo(s23), 64.f * bf16_hi(s23)};
 #pragma unroll
     for (int st = 0; st < STEPS; ++st) {
@@ -406,11 +415,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 
   if (tid == 64) {
     tma_prefetch_desc(&maps.w1);
-    if (Q4) tma_prefetch_desc(&maps.s1);
-    if (layer) {
-      tma_prefetch_desc(&maps.w2);
-      if (Q4) tma_prefetch_desc(&maps.s2);
-    }
+    if (layer) tma_prefetch_desc(&maps.w2);
   }
   if (tid == 0) {
     for (int i = 0; i < DF_MAX_STAGES; ++i) {
@@ -471,7 +476,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     // ------------------------------------------------ weights
     if (lane == 0) {
       const uint64_t pol = l2_evict_first_policy();
-      constexpr int srows = Q4 ? kDecKC4 / (Q4 ? GRP : 1) : 0;  // scale rows of a chunk
+      // A stage is 128 columns wide, in blocks of 128 bytes of a row.  The issue
+      // of one TMA load takes its thread ~150 clocks, so a chunk should be one
+      // load, or two where it has gate and up columns: blocks are a dimension
+      // of the tensor map where the columns divide into them.
+      constexpr int BLK = Q4 ? 32 : 64;            // columns of a block
+      constexpr int BLK_BYTES = Q4 ? 4096 : 8192;  // of a stage
+      constexpr int KROWS = C::KC / (Q4 ? 8 : 1);  // rows of a chunk in the weights' array
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
         const Split sp((uint32_t)n_ent * NB * KCN, G);
         const CUtensorMap* mw = ph ? &maps.w2 : &maps.w1;
-        const CUtensorMap* ms = ph ? &maps.s2 : &maps.s1;
+        const bool blocked = ph ? p.blocked2 : p.blocked1;
         uint32_t x = sp.start(cta);
         const uint32_t end = sp.start(cta + 1);
         while (x < end && ok) {
@@ -501,19 +512,15 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
             uint64_t* bar = &c.full[stage];
             uint8_t* dst = sW + stage * DF_W_BYTES;
-            if constexpr (Q4) {
-              mbar_arrive_expect_tx(bar, DF_W_BYTES + srows * 256);
-              tma_load_3d_hint(dst, mw, bar, ca, kc * 32, e, pol);
-              tma_load_3d_hint(dst + 4096, mw, bar, ca + 32, kc * 32, e, pol);
-              tma_load_3d_hint(dst + 8192, mw, bar, cb, kc * 32, e, pol);
-              tma_load_3d_hint(dst + 12288, mw, bar, cb + 32, kc * 32, e, pol);
-              uint8_t* ds = sS + stage * C::S_BYTES;
-              tma_load_3d_hint(ds, ms, bar, ca, kc * srows, e, pol);
-              tma_load_3d_hint(ds + srows * 128, ms, bar, cb, kc * srows, e, pol);
+            mbar_arrive_expect_tx(bar, DF_W_BYTES);
+            if (blocked) {
+              tma_load_4d_hint(dst, mw, bar, 0, kc * KROWS, ca / BLK, e, pol);
+              if (sg) tma_load_4d_hint(dst + DF_W_BYTES / 2, mw, bar, 0, kc * KROWS, cb / BLK, e, pol);
             } else {
-              mbar_arrive_expect_tx(bar, DF_W_BYTES);
-              tma_load_3d_hint(dst, mw, bar, ca, kc * 64, e, pol);
-              tma_load_3d_hint(dst + 8192, mw, bar, cb, kc * 64, e, pol);
+#pragma unroll
+              for (int i = 0; i < kDecBN / BLK; ++i)
+                tma_load_3d_hint(dst + i * BLK_BYTES, mw, bar,
+                                 (i < kDecBN / BLK / 2 ? ca : cb - 64) + i * BLK, kc * KROWS, e, pol);
             }
             ++issued;
             if (++stage == S) {
@@ -551,18 +558,40 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       uint32_t x = sp.start(cta);
       const uint32_t end = sp.start(cta + 1);
       const bool copies = ph == 0 || !reader;
+      const uint16_t* scales = ph ? p.s2 : p.s1;
+      const int N = ph ? p.N2 : p.N1;
+      const bool sg = ph == 0 && swiglu;
+      const int ncols = sg ? 2 * N : N;  // columns of W
       if (ph == 1 && copies && x < end) ok = grid_wait(p, G, c.abort_flag, lane);
       while (x < end && ok) {
         const int item = (int)(x / KCN);
         const int k0 = (int)(x - (uint32_t)item * KCN);
         const int k1 = (int)min((uint32_t)KCN, k0 + (end - x));
         const DecEntry en = c.ent[ph ? item % n_ent : item / NB];
+        const int nb = ph ? item / n_ent : item % NB;
         for (int kc = k0; kc < k1; ++kc) {
           if (!mbar_wait(&c.empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
           uint64_t* bar = &c.full[stage];
+          if constexpr (Q4) {
+            // the chunk's scales, [256 / GRP rows][128 columns]: 8 columns per
+            // copy, zeros past the end of K or of the columns
+            constexpr int SROWS = kDecKC4 / (Q4 ? GRP : 1);
+            const int c8 = (lane & 15) * 8;
+            const int col = sg ? nb * 64 + (c8 & 63) : nb * kDecBN + c8;
+            const bool in = col < N;
+            const uint32_t dst = smem_u32(sS + stage * C::S_BYTES) + (uint32_t)c8 * 2;
+#pragma unroll
+            for (int r = lane >> 4; r < SROWS; r += 2) {
+              const int sr = kc * SROWS + r;
+              const bool ok_row = in && sr * GRP < K;
+              const uint16_t* from = scales + ((size_t)en.expert * (K / GRP) + (ok_row ? sr : 0)) * ncols +
+                                     (ok_row ? col + (sg && c8 >= 64 ? N : 0) : 0);
+              cp_async16(dst + (uint32_t)r * 256, from, ok_row ? 16u : 0u);
+            }
+          }
           if (copies) {
             constexpr int RPP = 32 / PCS;  // rows per pass of the warp
             const int j = lane % PCS;
@@ -575,10 +604,11 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
               const int row = ph ? en.row0 + r : c.tok[en.row0 + r];
               cp_async16(dst + (uint32_t)(r * C::PITCH), s + (size_t)row * K, n);
             }
-            cp_async_arrive(bar);
-          } else {
-            if (lane == 0) mbar_arrive_n(bar, 32);
           }
+          if (Q4 || copies)
+            cp_async_arrive(bar);
+          else if (lane == 0)
+            mbar_arrive_n(bar, 32);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
@@ -625,8 +655,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         bofs[i] = row * 16;
       }
       bl = (uint32_t)(g * C::PITCH);
-      sofs = (uint32_t)(wn >> 1) * (uint32_t)(kDecKC4 / (Q4 ? GRP : 1)) * 128 +
-             (uint32_t)((wn & 1) * 32 + 4 * g) * 2;
+      sofs = (uint32_t)(wn * 32 + 4 * g) * 2;
     } else {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {

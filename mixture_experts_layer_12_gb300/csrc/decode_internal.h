@@ -77,6 +77,9 @@ struct DecFfnArgs {
   int row_cap;           // rows of an entry at most, rounded up to 8
   float* yfull;          // layer: [T*k, H] fp32 expert outputs of whole items
   uint16_t* h;           // layer: [T*k, F]
+  const uint16_t* s1;    // 4-bit: scales
+  const uint16_t* s2;
+  int blocked1, blocked2;  // the tensor maps have column blocks (see DecFfnMaps)
   const uint16_t* x;
   const int32_t* perm;   // layer
   const int32_t* slot;   // layer
@@ -91,9 +94,13 @@ struct DecFfnArgs {
   int* status;
   uint64_t wait_limit_ns;
 };
+// W [E, K, N] (4 bits: words [E, K/8, N]) with 128-byte swizzle.  Where the
+// columns divide into blocks of 128 bytes (64 bf16, 32 words), gate and up
+// separately: dimensions [E, blocks, K, block], a box of one expert, as many
+// blocks as a 128- (gated: 64-) column half takes and one chunk's rows.
+// Elsewhere: dimensions [E, K, N], a box of one block.
 struct DecFfnMaps {
-  CUtensorMap w1, w2;    // bf16: box {64, 64, 1}; codes: box {32, 32, 1}; 128-byte swizzle
-  CUtensorMap s1, s2;    // 4-bit: scales, box {64, 256 / group, 1}, no swizzle
+  CUtensorMap w1, w2;
 };
 constexpr int kDecBN = 128;    // columns of an item's weight tile
 constexpr int kDecKC16 = 64;   // K rows of a chunk, bf16 weights
