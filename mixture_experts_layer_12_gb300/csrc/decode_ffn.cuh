@@ -22,11 +22,11 @@
 //   * One warp issues TMA loads of weights into a ring of stages and runs ahead
 //     of everything: while the CTAs meet at the grid barrier between the two
 //     products, the ring already fills with W2.
-//   * One warp copies the rows' K chunk (x, then h) into the same stage with
+//   * Three warps copy the rows' K chunk (x, then h) into the same stage with
 //     cp.async.  With 150 KB of weights on their way to every SM any other
 //     access waits in the same queues for 2-3 us, so the rows have to be asked
-//     for as early as the weights are: three warps that loaded a chunk each
-//     and waited for it were what bound the kernel (a 4-bit chunk took 1400
+//     for as early as the weights are: warps that loaded a chunk each and
+//     waited for it were what bound the kernel (a 4-bit chunk took 1400
 //     clocks, 600 of them multiplying).
 //   * The consumer warps multiply: m16n8k16 products with the weights as M (32
 //     columns of W per warp) and the rows as N (8 at a time).  A weight is
@@ -63,13 +63,14 @@ constexpr int DF_MAX_STAGES = 12;
 constexpr int DF_SMEM = 227 * 1024;
 constexpr int DF_CACHE = 24 * 1024; // h kept whole by its readers: at most this much of it
 
-constexpr int KG = 2;  // consumer groups
+constexpr int DF_MAX_KG = 3;   // consumer groups at most
+constexpr int DF_LOADERS = 3;  // row loaders: 12 warps in all, 3 to a scheduler
 
 // named barriers: all consumers; the writers of an item (one per group); an
 // item's hand-over between the groups (one per writing group)
 constexpr int BAR_CONS = 1;
 constexpr int BAR_FIN = 2;
-constexpr int BAR_ITEM = BAR_FIN + KG;
+constexpr int BAR_ITEM = BAR_FIN + DF_MAX_KG;
 
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -255,18 +256,20 @@ template <bool Q4, int NT>
 struct Cfg {
   // consumer warps: KG groups of 4 across the columns; group i takes every
   // KG-th chunk, so that a warp has a chunk's whole K to keep its pipes full
-  // between two waits, and writes out every KG-th item while the other group
-  // goes on multiplying.  (2 groups unpack and multiply a 4-bit chunk in 615
-  // clocks, 3 in 600; one SM's share of the memory brings it in 700.)
+  // between two waits, and writes out every KG-th item while the others go on
+  // multiplying.  2 groups of 4 warps unpack and multiply a 4-bit chunk in 615
+  // clocks, 3 in 600, and one SM's share of the memory brings it in 700; the
+  // third group fills the pipes while another waits or writes.
+  static constexpr int KG = Q4 && NT <= 2 ? 3 : 2;
   static constexpr int CONSUMERS = DF_WN * KG;
-  static constexpr int THREADS = 32 * (2 + CONSUMERS);
+  static constexpr int THREADS = 32 * (1 + DF_LOADERS + CONSUMERS);
   static constexpr int KC = Q4 ? kDecKC4 : kDecKC16;    // K rows of a chunk
   static constexpr int PITCH = KC * 2 + 16;             // bytes of a row's chunk: no bank conflicts
   static constexpr int S_BYTES = Q4 ? 8 * 256 : 0;      // scales: up to 8 groups x 128 columns
   static constexpr int W_STAGE = DF_W_BYTES + S_BYTES;
   static constexpr int RED_GROUP = DF_FIN * 2 * NT * 4;    // floats a group hands over
-  static constexpr int RED = KG * RED_GROUP * 4;
-  static constexpr int CTRL = 16 * 1024;
+  static constexpr int RED = KG * (KG - 1) * RED_GROUP * 4;
+  static constexpr int CTRL = 18 * 1024;
   static constexpr int SPACE = DF_SMEM - 1024 - RED - CTRL;  // for the rings
   // reads of rows past an entry's last stay inside: RED and CTRL follow the rows
   static_assert(RED + CTRL >= 8 * PITCH, "room behind the rows");
@@ -278,15 +281,15 @@ struct Ctrl {
   int abort_flag;
   int n_entries;
   int max_rows;
-  int last[KG];
+  int last[DF_MAX_KG];
   DecEntry ent[kDecMaxEntries];
-  int2 owner[KG][kDecMaxEntries];     // combine: CTAs of the column block's items
+  int2 owner[DF_MAX_KG][kDecMaxEntries];     // combine: CTAs of the column block's items
   uint16_t row_entry[MOED_MAX_ROWS];  // layer: entry of a row
   int tok[MOED_MAX_ROWS];             // row of x of a dispatch row
   int slot[MOED_MAX_ROWS];            // layer: [T, k]
   float gate[MOED_MAX_ROWS];
 };
-static_assert(sizeof(Ctrl) <= 16 * 1024, "control area");
+static_assert(sizeof(Ctrl) <= 18 * 1024, "control area");
 
 // One product's chunks, in item order, dealt to the first G = min(CTAs, total)
 // CTAs: CTA c < G takes chunks [total c / G, total (c + 1) / G), at least one.
@@ -395,6 +398,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     decode_ffn_kernel(const __grid_constant__ DecFfnMaps maps, const DecFfnArgs p) {
   constexpr bool Q4 = GRP > 0;
   using C = Cfg<Q4, NT>;
+  constexpr int KG = C::KG;
   constexpr int CTHREADS = 32 * C::CONSUMERS;
   constexpr int PCS = C::KC / 8;  // 16-byte pieces of a row's chunk
   extern __shared__ uint8_t smem_raw[];
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < DF_MAX_STAGES; ++i) {
-      mbar_init(&c.full[i], 1 + 32);  // the weights' producer, the row loader's lanes
+      mbar_init(&c.full[i], 1 + 32 * DF_LOADERS);  // the weights' producer, the row loaders' lanes
       mbar_init(&c.empty[i], DF_WN);
     }
     c.abort_flag = 0;
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
       }
       // A CTA that gave up must not leave with copies in flight.  The barriers
-      // also count the row loader, so wait a bounded while for each stage that
+      // also count the row loaders, so wait a bounded while for each stage that
       // was issued and not seen full.
       if (!ok || *const_cast<volatile int*>(&c.abort_flag)) {
         for (int m = max(0, issued - S); m < issued; ++m) {
@@ -545,8 +549,11 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= DF_LOADERS) {
     // ------------------------------------------------ rows
+    // every loader takes every chunk: rows lw, lw + 3, ..; the last one the
+    // scales too (a row costs its warp ~150 clocks to ask for)
+    const int lw = warp - 1;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -575,10 +582,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             break;
           }
           uint64_t* bar = &c.full[stage];
-          if constexpr (Q4) {
+          bool any = false;
+          if (Q4 && lw == DF_LOADERS - 1) {
+            any = true;
             // the chunk's scales, [256 / GRP rows][128 columns]: 8 columns per
             // copy, zeros past the end of K or of the columns
-            constexpr int SROWS = kDecKC4 / (Q4 ? GRP : 1);
+            constexpr int GRP1 = Q4 ? GRP : 1;
+            constexpr int SROWS = kDecKC4 / GRP1;
             const int c8 = (lane & 15) * 8;
             const int col = sg ? nb * 64 + (c8 & 63) : nb * kDecBN + c8;
             const bool in = col < N;
@@ -586,13 +596,14 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 #pragma unroll
             for (int r = lane >> 4; r < SROWS; r += 2) {
               const int sr = kc * SROWS + r;
-              const bool ok_row = in && sr * GRP < K;
-              const uint16_t* from = scales + ((size_t)en.expert * (K / GRP) + (ok_row ? sr : 0)) * ncols +
+              const bool ok_row = in && sr * GRP1 < K;
+              const uint16_t* from = scales + ((size_t)en.expert * (K / GRP1) + (ok_row ? sr : 0)) * ncols +
                                      (ok_row ? col + (sg && c8 >= 64 ? N : 0) : 0);
               cp_async16(dst + (uint32_t)r * 256, from, ok_row ? 16u : 0u);
             }
           }
-          if (copies) {
+          if (copies && lw * (32 / PCS) < en.n) {
+            any = true;
             constexpr int RPP = 32 / PCS;  // rows per pass of the warp
             const int j = lane % PCS;
             const int kk = kc * C::KC + j * 8;
@@ -600,12 +611,12 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             const uint32_t n = kk < K ? 16u : 0u;   // zeros past the end of K
             const uint16_t* s = src + (kk < K ? kk : 0);
 #pragma unroll 4
-            for (int r = lane / PCS; r < en.n; r += RPP) {
+            for (int r = lw * RPP + lane / PCS; r < en.n; r += RPP * DF_LOADERS) {
               const int row = ph ? en.row0 + r : c.tok[en.row0 + r];
               cp_async16(dst + (uint32_t)(r * C::PITCH), s + (size_t)row * K, n);
             }
           }
-          if (Q4 || copies)
+          if (any)
             cp_async_arrive(bar);
           else if (lane == 0)
             mbar_arrive_n(bar, 32);
@@ -620,11 +631,11 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------ multiply, finish items
-    const int cw = warp - 2;
+    const int cw = warp - 1 - DF_LOADERS;
     const int wn = cw & (DF_WN - 1);
     const int kg = cw / DF_WN;
     const int g = lane >> 2, t = lane & 3;
-    const int ctid = tid - 64;
+    const int ctid = tid - 32 * (1 + DF_LOADERS);
     const int ftid = ctid & (DF_FIN - 1);  // among the group's threads
     // This group's next chunk: its number q among the CTA's chunks (q mod KG =
     // kg), its stage and that stage's parity.  A wait tells the phases of a
@@ -757,26 +768,29 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         qi += (uint32_t)(k1 - k0);
         x += (uint32_t)(k1 - k0);
 
-        // ---- one group sums both groups' parts and writes the item out.  The
-        // other hands over and goes on; it hands over again only after an item
-        // of its own, for which the first group has come to a barrier after
-        // this reading.
+        // ---- one group, in turn, sums all groups' parts and writes the item
+        // out; the others hand over and go on.  A group has a place for each
+        // of the KG - 1 items between two of its own: at its own item it meets
+        // the groups that wrote those, which have read them by then.
         const int writer = (int)(n_items % KG);
+        const int place = (int)(n_items % (KG - 1));
+        float* mine_red = sRed + (kg * (KG - 1) + place) * C::RED_GROUP;
         ++n_items;
         if (kg != writer) {
-          float* red = sRed + kg * C::RED_GROUP;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) red[((m * NT + n) * 4 + r) * DF_FIN + ftid] = acc[m][n][r];
+              for (int r = 0; r < 4; ++r) mine_red[((m * NT + n) * 4 + r) * DF_FIN + ftid] = acc[m][n][r];
           named_arrive(BAR_ITEM + writer, CTHREADS);
           continue;
         }
         named_sync(BAR_ITEM + writer, CTHREADS);
-        {
-          const float* red = sRed + (1 - kg) * C::RED_GROUP;
+#pragma unroll
+        for (int u = 1; u < KG; ++u) {
+          const int from = kg + u < KG ? kg + u : kg + u - KG;
+          const float* red = sRed + (from * (KG - 1) + place) * C::RED_GROUP;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -846,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             uint16_t* out = layer ? p.h : p.y;
             // gated: gate columns meet up columns, warps 2, 3 hand over to 0, 1
             // in this group's own space, which is free while it writes
-            float* red = sRed + kg * C::RED_GROUP;
+            float* red = sRed + kg * (KG - 1) * C::RED_GROUP;
             if (sg) {
               if (wn >= 2) {
 #pragma unroll
