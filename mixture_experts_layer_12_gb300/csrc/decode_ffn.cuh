@@ -66,8 +66,9 @@ constexpr int DF_CACHE = 24 * 1024; // h kept whole by its readers: at most this
 constexpr int DF_MAX_KG = 3;   // consumer groups at most
 constexpr int DF_LOADERS = 3;  // row loaders: 12 warps in all, 3 to a scheduler
 
-// named barriers: all consumers; the writers of an item (one per group); an
+// named barriers: set-up; all consumers; the writers of an item (one per group); an
 // item's hand-over between the groups (one per writing group)
+constexpr int BAR_SETUP = 0;
 constexpr int BAR_CONS = 1;
 constexpr int BAR_FIN = 2;
 constexpr int BAR_ITEM = BAR_FIN + DF_MAX_KG;
@@ -417,10 +418,6 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
   const bool layer = p.act != kDecNone;
   const bool swiglu = p.act == kDecSwiGLU;
 
-  if (tid == 64) {
-    tma_prefetch_desc(&maps.w1);
-    if (layer) tma_prefetch_desc(&maps.w2);
-  }
   if (tid == 0) {
     for (int i = 0; i < DF_MAX_STAGES; ++i) {
       mbar_init(&c.full[i], 1 + 32 * DF_LOADERS);  // the weights' producer, the row loaders' lanes
@@ -428,29 +425,37 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     }
     c.abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&maps.w1);
+    if (layer) tma_prefetch_desc(&maps.w2);
   }
   pdl_launch_dependents();
   pdl_wait();
-  // the first kernel's list and routing
-  if (tid == 32) {
+  // the first kernel's list, by the weights' warp, which goes on as soon as it
+  // has it; the routing by the others
+  if (warp == 0) {
     const int2 v = __ldcg(reinterpret_cast<const int2*>(p.ctrl + kDecCountOffset / 4));
-    c.n_entries = min(v.x, p.max_entries);
-    c.max_rows = min(v.y, p.row_cap);
-  }
-  for (int i = tid; i < p.T * p.k; i += C::THREADS) {
-    if (layer) {
-      c.slot[i] = __ldcg(p.slot + i);
-      c.gate[i] = __ldcg(p.gate + i);
-      c.tok[i] = min(max(__ldcg(p.perm + i), 0), p.T * p.k - 1) / p.k;
-    } else {
-      c.tok[i] = i;
+    for (int i = lane; i < p.max_entries; i += 32) {
+      const int4 e = __ldcg(reinterpret_cast<const int4*>(p.entries) + i);
+      c.ent[i] = DecEntry{e.x, e.y, e.z, e.w};
     }
+    if (lane == 0) {
+      c.n_entries = min(v.x, p.max_entries);
+      c.max_rows = min(v.y, p.row_cap);
+    }
+    __syncwarp();
+    named_arrive(BAR_SETUP, C::THREADS);
+  } else {
+    for (int i = tid - 32; i < p.T * p.k; i += C::THREADS - 32) {
+      if (layer) {
+        c.slot[i] = __ldcg(p.slot + i);
+        c.gate[i] = __ldcg(p.gate + i);
+        c.tok[i] = min(max(__ldcg(p.perm + i), 0), p.T * p.k - 1) / p.k;
+      } else {
+        c.tok[i] = i;
+      }
+    }
+    named_sync(BAR_SETUP, C::THREADS);
   }
-  for (int i = tid; i < p.max_entries; i += C::THREADS) {
-    const int4 v = __ldcg(reinterpret_cast<const int4*>(p.entries) + i);
-    c.ent[i] = DecEntry{v.x, v.y, v.z, v.w};
-  }
-  __syncthreads();
   const int n_ent = c.n_entries;
   const WaitCtl wc{&c.abort_flag, p.status, p.wait_limit_ns};
   if (n_ent == 0) {  // every assignment dropped: y = 0 (grouped products: nothing to write)
@@ -971,11 +976,12 @@ cudaError_t ffn_launch(const DecFfnMaps& m, const DecFfnArgs& a, int ctas, cudaS
   cfg.blockDim = dim3((unsigned)C::THREADS, 1, 1);
   cfg.dynamicSmemBytes = DF_SMEM;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  set_pdl_attr(attr[1]);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, decode_ffn_kernel<GRP, NT>, m, a);
 }
 

@@ -6,19 +6,24 @@
 // "Gather操作", as in route_fused.cu; what differs is the size.  A few tokens'
 // logits are a [T, H] x [H, E] product of at most a megabyte or two, far too
 // little to fill the GPU and bound by latency: one trip to memory, one
-// reduction, two cluster barriers.  The H axis is split over the 8 CTAs, so a
-// trip to memory brings all of W_router at once (16 SMs' worth of loads in
-// flight for E = 8, one load per thread); within a CTA the warps split the
+// reduction, two cluster barriers.  The H axis is split over the 8 CTAs, so
+// one trip to memory brings all of W_router; within a CTA the warps split the
 // remaining K steps and the experts.  The products are m16n8k16 tensor-core
 // ones with W_router as the M operand (ldmatrix.trans: E is contiguous) and
 // the tokens as N: bf16 products are exact in fp32, sums are fp32 in a fixed
-// order (warps of a CTA, then ranks 0..7).  The partial logits stay in shared
-// memory and are read through distributed shared memory by the rank that
-// owns the token (t mod 8), 8 lanes per token (route_topk.cuh).  Rank 0 then
-// holds every id and dispatches: at most 512 assignments, ranked within their
+// order (warps of a CTA, then ranks 0..7).  Every rank stores its partial
+// logits into the shared memory of the rank that owns the token (rank 0 owns
+// all of up to 8 tokens, else t mod 8), so that the owner reads its own
+// memory after the barrier.  A warp per token then takes the k largest, one
+// per round (two warp-wide integer reductions: the largest, then the lowest
+// index that has it).  This code runs once per launch and comes cold from
+// memory, so its size is its cost: the loops stay loops.  Rank 0 then holds
+// every id and dispatches: at most 512 assignments, ranked within their
 // expert by warp match and a scan over the warps' chunks.
+#include <math.h>
+
 #include "decode_internal.h"
-#include "route_topk.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 namespace {
@@ -28,7 +33,7 @@ constexpr int DR_WARPS = DR_THREADS / 32;
 constexpr int DR_RANKS = 8;
 constexpr int DR_MAX_ASSIGN = MOED_MAX_TOKENS * kMaxTopK;  // 512
 constexpr int DR_CHUNKS = DR_MAX_ASSIGN / 32;
-constexpr int DR_STAGE_BYTES = 128 * 1024;  // W_router and x rows staged at a time
+constexpr int DR_STAGE_BYTES = 112 * 1024;  // W_router and x rows staged at a time
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -87,15 +92,23 @@ __host__ __device__ inline RouteLayout route_layout(int T, int H, int E) {
   while (L.wm < DR_WARPS && L.wm * 16 < L.ep) L.wm *= 2;
   const size_t tiles = (size_t)kb * L.pw + (size_t)L.tp * L.px;
   const size_t red = (size_t)(DR_WARPS / L.wm) * L.tp * L.ep * 4;  // reuses the tiles' space
+  // partial logits of the tokens a rank owns, from all ranks
+  const size_t own = T <= DR_RANKS ? (size_t)L.tp : (size_t)(T + DR_RANKS - 1) / DR_RANKS;
   L.stage = tiles > red ? tiles : red;
   L.stage = (L.stage + 127) / 128 * 128;
-  L.part = (size_t)L.tp * L.ep * 4;
+  L.part = DR_RANKS * own * L.ep * 4;
   L.total = L.stage + L.part;
   return L;
 }
 
-// NT: 8-token tiles; NCH: 32-expert chunks of the TopK lanes.
-template <int NT, int NCH>
+// fp32 -> unsigned integers of the same order, none of them 0
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);  // -0 as +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// NT: 8-token tiles.
+template <int NT>
 __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1)
     decode_route_kernel(const DecRouteArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -103,6 +116,8 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   __shared__ int s_wc[DR_CHUNKS][kMaxExperts];
   __shared__ int s_off[kMaxExperts + 1];
   __shared__ int s_scan[3][DR_WARPS];
+  __shared__ float s_log[DR_WARPS][kMaxExperts];
+  __shared__ uint32_t s_key[DR_WARPS][kMaxExperts];
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -207,64 +222,95 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
       }
   }
   __syncthreads();
-  for (int i = tid; i < L.tp * L.ep; i += DR_THREADS) {
-    float v = 0.f;
-    for (int w = 0; w < nk; ++w) v += sRed[(size_t)w * L.tp * L.ep + i];
-    sPart[i] = v;
+  const bool one_owner = T <= DR_RANKS;
+  const int own = one_owner ? L.tp : (T + DR_RANKS - 1) / DR_RANKS;  // tokens of an owner
+  const uint32_t part0 = smem_u32(sPart);
+  for (int i = tid; i < T * (L.ep / 4); i += DR_THREADS) {
+    const int t = i / (L.ep / 4), c4 = i - t * (L.ep / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < nk; ++w) {
+      const float4 o = *reinterpret_cast<const float4*>(sRed + ((size_t)w * L.tp + t) * L.ep + c4 * 4);
+      v.x += o.x;
+      v.y += o.y;
+      v.z += o.z;
+      v.w += o.w;
+    }
+    const int owner = one_owner ? 0 : t % DR_RANKS, tl = one_owner ? t : t / DR_RANKS;
+    dsmem_st_v4(dsmem_map(part0 + (uint32_t)(((rank * own + tl) * L.ep + c4 * 4) * 4), (uint32_t)owner),
+                v.x, v.y, v.z, v.w);
   }
   cluster_sync_all();
 
-  // ---- TopK and gate weights of the tokens this rank owns: t mod 8 = rank
-  {
-    const int grp = tid >> 3, g = tid & 7;
-    const int t = grp * DR_RANKS + rank;
-    if (t < T) {
-      const unsigned gmask = 0xFFu << (lane & 24);
-      float lv[NCH * 4];
-      uint32_t taken = 0;
+  // ---- TopK and gate weights of the tokens this rank owns, a warp each
+  for (int tl = warp; tl < own; tl += DR_WARPS) {
+    const int t = one_owner ? tl : tl * DR_RANKS + rank;
+    if (t >= T || (one_owner && rank != 0)) break;
+    float* lg = s_log[warp];
+    uint32_t* key = s_key[warp];
+    for (int e = lane; e < E; e += 32) {
+      float v = 0.f;
 #pragma unroll
-      for (int cc = 0; cc < NCH; ++cc) {
-        const int e0 = (g + cc * kTopkGroup) * 4;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e0 < L.ep) {
-          const uint32_t local = smem_u32(sPart + (size_t)t * L.ep + e0);
-          float4 p[DR_RANKS];
-#pragma unroll
-          for (int r = 0; r < DR_RANKS; ++r) p[r] = dsmem_ld_v4(dsmem_map(local, (uint32_t)r));
-#pragma unroll
-          for (int r = 0; r < DR_RANKS; ++r) {
-            s.x += p[r].x;
-            s.y += p[r].y;
-            s.z += p[r].z;
-            s.w += p[r].w;
-          }
-        }
-        const float v4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = v4[i];
-          if (e0 + i < E) {
-            if (a.bias) v += __ldg(a.bias + e0 + i);
-            if (isnan(v)) v = -INFINITY;
-          } else {
-            v = -INFINITY;
-            taken |= 1u << (cc * 4 + i);
-          }
-          lv[cc * 4 + i] = v;
-        }
-      }
-      int id;
-      float w;
-      topk_gate_group<NCH>(lv, taken, g, gmask, k, E, a.gating, id, w);
-      if (g < k) {
-        a.ids[(size_t)t * k + g] = id;
-        a.weights[(size_t)t * k + g] = w;
-        dsmem_st_u32(dsmem_map(smem_u32(s_ids + t * k + g), 0), (uint32_t)id);
-      }
+      for (int r = 0; r < DR_RANKS; ++r) v += sPart[((size_t)r * own + tl) * L.ep + e];
+      if (a.bias) v += __ldg(a.bias + e);
+      if (isnan(v)) v = -INFINITY;
+      lg[e] = v;
+      key[e] = order_key(v);
     }
+    int id = 0;
+    float top = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) {
+      // each lane's largest untaken (its lowest index: strictly larger
+      // replaces), then the warp's, then the lowest index that has it
+      uint32_t bk = 0;
+      int be = kMaxExperts;
+#pragma unroll 1
+      for (int e = lane; e < E; e += 32) {
+        const uint32_t u = key[e];
+        if (u > bk) {
+          bk = u;
+          be = e;
+        }
+      }
+      const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
+      const int e = __reduce_min_sync(0xffffffffu, bk == m ? be : kMaxExperts);
+      if (lane == (e & 31)) key[e] = 0;  // taken
+      if (lane == j) {
+        id = e;
+        top = lg[e];
+      }
+      __syncwarp();
+    }
+    const float mx = __shfl_sync(0xffffffffu, top, 0);
+    float ex = lane < k ? expf(top - mx) : 0.f;
+    if (a.gating != MOE_GATE_TOPK_SOFTMAX) {  // softmax over all E first
+      float zall = 0.f;
+      for (int e = lane; e < E; e += 32) zall += expf(lg[e] - mx);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) zall += __shfl_xor_sync(0xffffffffu, zall, off);
+      ex /= zall;
+    }
+    float z = ex;
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+    if (a.gating != MOE_GATE_SOFTMAX_TOPK) ex /= z;
+    if (lane < k) {
+      a.ids[(size_t)t * k + lane] = id;
+      a.weights[(size_t)t * k + lane] = ex;
+      if (one_owner)
+        s_ids[t * k + lane] = id;
+      else
+        dsmem_st_u32(dsmem_map(smem_u32(s_ids + t * k + lane), 0), (uint32_t)id);
+    }
+    __syncwarp();
   }
-  cluster_sync_all();
-  if (rank != 0) return;
+  if (one_owner) {
+    if (rank != 0) return;  // nothing of these ranks is read any more
+    __syncthreads();
+  } else {
+    cluster_sync_all();
+    if (rank != 0) return;
+  }
 
   // ---- dispatch of all T*k assignments, in (token, slot) order
   const int n = T * k;
@@ -399,7 +445,7 @@ __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
   }
 }
 
-template <int NT, int NCH>
+template <int NT>
 cudaError_t route_launch(const DecRouteArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(DR_RANKS, 1, 1);
@@ -410,43 +456,24 @@ cudaError_t route_launch(const DecRouteArgs& a, cudaStream_t st) {
   set_pdl_attr(attr[0]);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_route_kernel<NT, NCH>, a);
-}
-
-template <int NT>
-cudaError_t route_nt(const DecRouteArgs& a, cudaStream_t st) {
-  if (a.E <= 32) return route_launch<NT, 1>(a, st);
-  if (a.E <= 64) return route_launch<NT, 2>(a, st);
-  if (a.E <= 128) return route_launch<NT, 4>(a, st);
-  return route_launch<NT, 8>(a, st);
+  return cudaLaunchKernelEx(&cfg, decode_route_kernel<NT>, a);
 }
 
 template <int NT>
 cudaError_t route_attr() {
-  // stage plus partial logits at the largest shapes: 128 KB + 64 KB
-  const int bytes = DR_STAGE_BYTES + MOED_MAX_TOKENS * kMaxExperts * 4;
-  cudaError_t e = cudaFuncSetAttribute(decode_route_kernel<NT, 1>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_route_kernel<NT, 2>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_route_kernel<NT, 4>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decode_route_kernel<NT, 8>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e;
+  // stage plus partial logits at the largest shapes: 112 KB + 64 KB
+  return cudaFuncSetAttribute(decode_route_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              DR_STAGE_BYTES + MOED_MAX_TOKENS * kMaxExperts * 4);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_route(const DecRouteArgs& a, cudaStream_t st) {
   const int nt = (a.T + 7) / 8;
-  if (nt <= 1) return route_nt<1>(a, st);
-  if (nt <= 2) return route_nt<2>(a, st);
-  if (nt <= 4) return route_nt<4>(a, st);
-  return route_nt<8>(a, st);
+  if (nt <= 1) return route_launch<1>(a, st);
+  if (nt <= 2) return route_launch<2>(a, st);
+  if (nt <= 4) return route_launch<4>(a, st);
+  return route_launch<8>(a, st);
 }
 
 cudaError_t launch_decode_prep(const DecPrepArgs& a, cudaStream_t st) {
