@@ -116,6 +116,13 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// counts in on a ticket: earlier writes of the CTA (a barrier before it) are
+// visible to whoever sees the count, and theirs to this CTA
+__device__ __forceinline__ unsigned atom_acq_rel(unsigned* p) {
+  unsigned v;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ void red_release(unsigned* p, unsigned v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -195,32 +202,57 @@ __device__ __forceinline__ float dec_gelu(float z) {
 }
 __device__ __forceinline__ float dec_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
-// 8 elements of h of row r of an entry, from the partial tiles of CTAs o0..o1
-// (in that order), activated and rounded to bf16.
-__device__ __forceinline__ uint4 sum_h_piece(const DecFfnArgs& p, int o0, int o1, int r, int kk,
-                                             bool swiglu) {
-  const int cl = swiglu ? kk & 63 : kk & 127;
+__device__ __forceinline__ void add4(float4& a, const float4 b) {
+  a.x += b.x;
+  a.y += b.y;
+  a.z += b.z;
+  a.w += b.w;
+}
+
+// 8 elements of h, rounded to bf16, from x W1 (or the gate's, and the up
+// projection's)
+__device__ __forceinline__ uint4 activated(const float4 (&z)[2], const float4 (&u)[2], bool swiglu) {
+  const float a[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
+  const float b[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+  float h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = swiglu ? dec_silu(a[i]) * b[i] : dec_gelu(a[i]);
+  return make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]),
+                    pack_bf16x2(h[6], h[7]));
+}
+
+// A shared item of the first product, put together by one group (128 threads):
+// the sum of the partial tiles of CTAs c0..c1 in that order, 4 columns of a row
+// per thread and step.
+__device__ __forceinline__ void finish_item(const DecFfnArgs& p, const DecEntry& en, int nb, int c0, int c1,
+                                            int ftid) {
+  const bool swiglu = p.act == kDecSwiGLU;
+  const int cols = swiglu ? 64 : kDecBN;
   const size_t tile = (size_t)p.row_cap * kDecBN;
-  float z[8], u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = u[i] = 0.f;
-#pragma unroll 2
-  for (int o = o0; o <= o1; ++o) {
-    const float4* s = reinterpret_cast<const float4*>(p.parts + (size_t)(o * 2 + (o == o0 ? 1 : 0)) * tile +
-                                                      r * kDecBN + cl);
-    const float4 a = __ldcg(s), b = __ldcg(s + 1);
-    z[0] += a.x; z[1] += a.y; z[2] += a.z; z[3] += a.w;
-    z[4] += b.x; z[5] += b.y; z[6] += b.z; z[7] += b.w;
-    if (swiglu) {
-      const float4 d = __ldcg(s + 16), e = __ldcg(s + 17);
-      u[0] += d.x; u[1] += d.y; u[2] += d.z; u[3] += d.w;
-      u[4] += e.x; u[5] += e.y; u[6] += e.z; u[7] += e.w;
+  const float* first = p.parts + (size_t)(c0 * 2 + 1) * tile;  // the later ones are in their slot 0
+  uint16_t* out = p.act == kDecNone ? p.y : p.h;
+  for (int i = ftid; i < en.n * (cols / 4); i += DF_FIN) {
+    const int r = i / (cols / 4), cl = (i % (cols / 4)) * 4;
+    const int col = nb * cols + cl;
+    if (col >= p.N1) continue;  // N1 is a multiple of 8
+    const float* s = first + r * kDecBN + cl;
+    float4 z = __ldcg(reinterpret_cast<const float4*>(s));
+    float4 u = swiglu ? __ldcg(reinterpret_cast<const float4*>(s + 64)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int o = 1; o <= c1 - c0; ++o) {
+      const float* q = s + (size_t)(2 * o - 1) * tile;
+      const float4 d = __ldcg(reinterpret_cast<const float4*>(q));
+      add4(z, d);
+      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(q + 64)));
     }
+    if (swiglu) {
+      z = make_float4(dec_silu(z.x) * u.x, dec_silu(z.y) * u.y, dec_silu(z.z) * u.z, dec_silu(z.w) * u.w);
+    } else if (p.act == kDecGelu) {
+      z = make_float4(dec_gelu(z.x), dec_gelu(z.y), dec_gelu(z.z), dec_gelu(z.w));
+    }
+    *reinterpret_cast<uint2*>(out + (size_t)(en.row0 + r) * p.N1 + col) =
+        make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = swiglu ? dec_silu(z[i]) * u[i] : dec_gelu(z[i]);
-  return make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                    pack_bf16x2(z[6], z[7]));
 }
 
 // Warp-wide wait for every CTA's arrival at the grid barrier; false when it
@@ -699,33 +731,86 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 
       if (cached && x < end) {
         // ---- this CTA's part of h, chunk after chunk, once every CTA's is
-        // there: whole items as they are, shared ones summed from their tiles
-        grid_wait(p, G, c.abort_flag, lane);
-        named_sync(BAR_CONS, CTHREADS);  // no group reads rows of the first product any more
+        // there: whole items as they are, shared ones summed from their tiles.
+        // A thread's pieces are worked out before the wait, and their loads
+        // are in flight together.
+        constexpr int UN = 3;
         q2 = qi;
         const Split s1((uint32_t)n_ent * p.nb1 * p.kc1, G);
         const int total = (int)(end - x) * max_rows * PCS;
-        for (int i = ctid; i < total; i += CTHREADS) {
-          const int j = i % PCS, rc = i / PCS;
-          const int r = rc % max_rows;
-          const uint32_t xc = x + (uint32_t)(rc / max_rows);
-          const int item = (int)(xc / KCN);
-          const int ei = item % n_ent;
-          const DecEntry en = c.ent[ei];
-          const int kk = (int)(xc - (uint32_t)item * KCN) * C::KC + j * 8;
-          if (r >= en.n) continue;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (kk < p.K2) {
-            const uint32_t i0 = (uint32_t)(ei * p.nb1 + (swiglu ? kk >> 6 : kk >> 7)) * p.kc1;
-            const int o0 = s1.owner(i0), o1 = s1.owner(i0 + p.kc1 - 1);
-            v = o0 == o1 ? __ldcg(reinterpret_cast<const uint4*>(p.h + (size_t)(en.row0 + r) * p.K2 + kk))
-                         : sum_h_piece(p, o0, o1, r, kk, swiglu);
+        const size_t tile = (size_t)p.row_cap * kDecBN;
+        for (int i0 = ctid; i0 < total || i0 == ctid; i0 += UN * CTHREADS) {
+          const float* part[UN];     // first tile of a shared item's piece
+          const uint16_t* whole[UN]; // or the piece of h
+          int more[UN];
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            const int i = i0 + u * CTHREADS;
+            part[u] = nullptr;
+            whole[u] = nullptr;
+            more[u] = -1;            // nothing to store
+            if (i < total) {
+              const int j = i % PCS, rc = i / PCS;
+              const int r = rc % max_rows;
+              const uint32_t xc = x + (uint32_t)(rc / max_rows);
+              const int item = (int)(xc / KCN);
+              const int ei = item % n_ent;
+              const DecEntry en = c.ent[ei];
+              const int kk = (int)(xc - (uint32_t)item * KCN) * C::KC + j * 8;
+              if (r < en.n) {
+                more[u] = 0;         // zeros past the end of K
+                if (kk < p.K2) {
+                  const uint32_t f = (uint32_t)(ei * p.nb1 + (swiglu ? kk >> 6 : kk >> 7)) * p.kc1;
+                  const int o0 = s1.owner(f);
+                  more[u] = s1.owner(f + p.kc1 - 1) - o0;
+                  if (more[u] == 0)
+                    whole[u] = p.h + (size_t)(en.row0 + r) * p.K2 + kk;
+                  else
+                    part[u] = p.parts + (size_t)(o0 * 2 + 1) * tile + r * kDecBN + (swiglu ? kk & 63 : kk & 127);
+                }
+              }
+            }
           }
-          sts128(smem_u32(sB) + (uint32_t)rc * C::PITCH + (uint32_t)j * 16, v.x, v.y, v.z, v.w);
+          if (i0 == ctid) {
+            grid_wait(p, G, c.abort_flag, lane);
+            named_sync(BAR_CONS, CTHREADS);
+          }
+          float4 z[UN][2], g2[UN][2];
+          uint4 v[UN];
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            v[u] = make_uint4(0, 0, 0, 0);
+            if (whole[u]) v[u] = __ldcg(reinterpret_cast<const uint4*>(whole[u]));
+            if (part[u]) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                z[u][h] = __ldcg(reinterpret_cast<const float4*>(part[u]) + h);
+                if (swiglu) g2[u][h] = __ldcg(reinterpret_cast<const float4*>(part[u] + 64) + h);
+              }
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            if (part[u]) {
+#pragma unroll 2
+              for (int o = 1; o <= more[u]; ++o) {
+                const float* q = part[u] + (size_t)(2 * o - 1) * tile;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  add4(z[u][h], __ldcg(reinterpret_cast<const float4*>(q) + h));
+                  if (swiglu) add4(g2[u][h], __ldcg(reinterpret_cast<const float4*>(q + 64) + h));
+                }
+              }
+              v[u] = activated(z[u], g2[u], swiglu);
+            }
+            const int i = i0 + u * CTHREADS;
+            if (more[u] >= 0)
+              sts128(smem_u32(sB) + (uint32_t)(i / PCS) * C::PITCH + (uint32_t)(i % PCS) * 16, v[u].x, v[u].y,
+                     v[u].z, v[u].w);
+          }
         }
         named_sync(BAR_CONS, CTHREADS);
       }
-      if (ph == 0 && layer && x == end && ctid == 0) red_release(p.barrier, 1u);  // nothing to do
 
       while (x < end) {
         const int item = (int)(x / KCN);
@@ -805,11 +890,9 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
         const int bar_fin = BAR_FIN + kg;
 
-        const bool whole = k0 == 0 && k1 == KCN;
-        bool write = whole;
-        if (!whole) {
-          // partial tile of this CTA: slot 0 if the item began in an earlier
-          // CTA, else slot 1
+        if (k0 != 0 || k1 != KCN) {
+          // a shared item: this CTA's partial tile, slot 0 if the item began in
+          // an earlier CTA, else slot 1
           float* mine = (ph ? p.parts2 : p.parts) + (size_t)(cta * 2 + (k0 > 0 ? 0 : 1)) * p.row_cap * kDecBN;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
@@ -818,38 +901,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 #pragma unroll
               for (int r = 0; r < 4; ++r)
                 if (row_of(n, r) < en.n) mine[row_of(n, r) * kDecBN + col_of(m, r)] = acc[m][n][r];
-          if (ph == 0 && !reader) {
-            const uint32_t i0 = (uint32_t)item * KCN;
-            const int c0 = sp.owner(i0), c1 = sp.owner(i0 + KCN - 1);
-            named_sync(bar_fin, DF_FIN);
-            if (ftid == 0) {
-              __threadfence();
-              c.last[kg] = atomicAdd(p.item_tickets + c0, 1u) == (unsigned)(c1 - c0);
-              __threadfence();
-            }
-            named_sync(bar_fin, DF_FIN);
-            if (c.last[kg]) {
-              write = true;
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) acc[m][n][r] = 0.f;
-              for (int o = c0; o <= c1; ++o) {
-                const float* src = p.parts + (size_t)(o * 2 + (o == c0 ? 1 : 0)) * p.row_cap * kDecBN;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                      if (row_of(n, r) < en.n) acc[m][n][r] += __ldcg(src + row_of(n, r) * kDecBN + col_of(m, r));
-              }
-            }
-          }
-        }
-        if (write) {
+        } else {
           if (ph == 1) {  // whole items of the second product stay in fp32 for the combine
 #pragma unroll
             for (int m = 0; m < 2; ++m)
@@ -901,15 +953,8 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           }
         }
 
-        // The other group's items before this one are written too: it came to
-        // this item's barrier after them.
-        if (ph == 0 && layer && x == end) {  // this CTA's h is written: the grid barrier
-          named_sync(bar_fin, DF_FIN);
-          if (ftid == 0) {
-            __threadfence();
-            red_release(p.barrier, 1u);
-          }
-        }
+        // (The other groups' items before this one are written too: they came
+        // to this item's barrier after them.)
         if (ph == 1 && (x == end || (int)(x / ((uint32_t)n_ent * KCN)) != nb)) {
           // ---- this CTA's part of column block nb is written: count in, and
           // combine the block if it is the last part
@@ -922,46 +967,90 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           named_sync(bar_fin, DF_FIN);
           if (ftid == 0) {
             const int parts = owner[n_ent - 1].y - owner[0].x + 1;
-            __threadfence();
-            c.last[kg] = atomicAdd(p.col_tickets + nb, 1u) == (unsigned)(parts - 1);
-            __threadfence();
+            c.last[kg] = atom_acq_rel(p.col_tickets + nb) == (unsigned)(parts - 1);
           }
           named_sync(bar_fin, DF_FIN);
           if (c.last[kg]) {
             const int col0 = nb * kDecBN;
-            for (int i = ftid; i < p.T * (kDecBN / 2); i += DF_FIN) {
-              const int tok = i / (kDecBN / 2);
-              const int cl = (i % (kDecBN / 2)) * 2;
-              if (col0 + cl >= N) continue;
-              float y0 = 0.f, y1 = 0.f;
-#pragma unroll 4
-              for (int j = 0; j < p.k; ++j) {
-                const int row = c.slot[tok * p.k + j];
-                if (row < 0) continue;
-                const float w = c.gate[tok * p.k + j];
-                const int ei = c.row_entry[row];
-                const int2 own = owner[ei];
-                float2 v;
-                if (own.x == own.y) {
-                  v = __ldcg(reinterpret_cast<const float2*>(p.yfull + (size_t)row * N + col0 + cl));
-                } else {
-                  v = make_float2(0.f, 0.f);
-                  const int rr = row - c.ent[ei].row0;
-#pragma unroll 4
-                  for (int o = own.x; o <= own.y; ++o) {
-                    const float2 u = __ldcg(reinterpret_cast<const float2*>(
-                        p.parts2 + ((size_t)(o * 2 + (o == own.x ? 1 : 0)) * p.row_cap + rr) * kDecBN +
-                        cl));
-                    v.x += u.x;
-                    v.y += u.y;
+            for (int i = ftid; i < p.T * (kDecBN / 4); i += DF_FIN) {
+              const int tok = i / (kDecBN / 4);
+              const int cl = (i % (kDecBN / 4)) * 4;
+              if (col0 + cl >= N) continue;  // N is a multiple of 8: all 4 columns or none
+              float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int j0 = 0; j0 < p.k; j0 += 4) {  // 4 experts' loads in flight together
+                const float* src[4];
+                int more[4];
+                float w[4];
+                float4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const int row = j0 + u < p.k ? c.slot[tok * p.k + j0 + u] : -1;
+                  w[u] = 0.f;
+                  more[u] = 0;
+                  src[u] = nullptr;
+                  if (row >= 0) {
+                    w[u] = c.gate[tok * p.k + j0 + u];
+                    const int ei = c.row_entry[row];
+                    const int2 own = owner[ei];
+                    more[u] = own.y - own.x;
+                    src[u] = more[u] == 0 ? p.yfull + (size_t)row * N + col0 + cl
+                                          : p.parts2 + ((size_t)(own.x * 2 + 1) * p.row_cap + row - c.ent[ei].row0) * kDecBN + cl;
                   }
                 }
-                y0 = fmaf(w, v.x, y0);
-                y1 = fmaf(w, v.y, y1);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  v[u] = src[u] ? __ldcg(reinterpret_cast<const float4*>(src[u])) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const size_t tile = (size_t)p.row_cap * kDecBN;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {  // the later CTAs' parts are in their slot 0
+#pragma unroll 2
+                  for (int o = 1; o <= more[u]; ++o) {
+                    const float4 d = __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * o - 1) * tile));
+                    add4(v[u], d);
+                  }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (src[u]) {
+                    y.x = fmaf(w[u], v[u].x, y.x);
+                    y.y = fmaf(w[u], v[u].y, y.y);
+                    y.z = fmaf(w[u], v[u].z, y.z);
+                    y.w = fmaf(w[u], v[u].w, y.w);
+                  }
               }
-              *reinterpret_cast<uint32_t*>(p.y + (size_t)tok * N + col0 + cl) = pack_bf16x2(y0, y1);
+              *reinterpret_cast<uint2*>(p.y + (size_t)tok * N + col0 + cl) =
+                  make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
             }
           }
+        }
+      }
+
+      if (ph == 0) {
+        // ---- every group has written its items
+        named_sync(BAR_CONS, CTHREADS);
+        if (!reader) {
+          // shared items, at most the CTA's first and last: whoever counts in
+          // last puts the item together (group 0 the first, group 1 the last)
+          const uint32_t s0 = sp.start(cta);
+          const int first = s0 < end && s0 % KCN != 0 ? (int)(s0 / KCN) : -1;
+          const int last = s0 < end && end % KCN != 0 && (int)(end / KCN) != first ? (int)(end / KCN) : -1;
+          if (ctid < 2) {
+            const int it = ctid == 0 ? first : last;
+            c.last[ctid] = 0;
+            if (it >= 0) {
+              const uint32_t i0 = (uint32_t)it * KCN;
+              const int c0 = sp.owner(i0), c1 = sp.owner(i0 + KCN - 1);
+              if (atom_acq_rel(p.item_tickets + c0) == (unsigned)(c1 - c0)) c.last[ctid] = 1 + (c0 << 16 | c1);
+            }
+          }
+          named_sync(BAR_CONS, CTHREADS);
+          if (kg < 2 && c.last[kg])
+            finish_item(p, c.ent[(kg == 0 ? first : last) / NB], (kg == 0 ? first : last) % NB,
+                        (c.last[kg] - 1) >> 16, (c.last[kg] - 1) & 0xFFFF, ftid);
+        }
+        if (layer) {  // this CTA's h is there: the grid barrier
+          if (!reader) named_sync(BAR_CONS, CTHREADS);
+          if (ctid == 0) red_release(p.barrier, 1u);
         }
       }
     }
