@@ -40,7 +40,17 @@ struct Layout {
   int max_entries, row_cap;
 };
 
-int row_cap_of(int rows) { return rows >= kDecRows ? kDecRows : (rows + 7) / 8 * 8; }
+// Rows of an entry at most: the kernel is built for 8, 16, 32 and 64, and its
+// cost grows with it (registers, ring space, products), so experts or segments
+// that hold 4 times the average or less should fit and longer ones are cut into
+// several entries, whose weights are read once each (37 rows over 64 segments:
+// 33.3 us with entries of 64 rows, 17.6 with 8).  `most`: rows that one can hold.
+int row_block_of(int rows, int parts, int most) {
+  const int want = 4 * ((rows + parts - 1) / parts);
+  int rb = 8;
+  while (rb < kDecRows && rb < want && rb < most) rb *= 2;
+  return rb;
+}
 
 Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool layer) {
   Layout L;
@@ -57,18 +67,22 @@ Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool laye
   return L;
 }
 
+// ceil(n_e / block) summed over at most `parts` experts or segments with n_e
+// rows, `rows` in all
+int max_entries_of(int rows, int parts, int block) {
+  return rows < parts ? rows : parts + (rows - parts) / block;
+}
+
 Layout layer_layout(const moe_shape* s) {
-  const int n = s->T * s->k;
-  const int rows = n > 0 ? n : 1;
-  return layout_of(rows, row_cap_of(s->T > 0 ? s->T : 1), n < s->E ? (n > 0 ? n : 1) : s->E, s->H,
-                   s->F, true);
+  const int rows = s->T > 0 ? s->T * s->k : 1;
+  const int block = row_block_of(rows, s->E, s->T);
+  return layout_of(rows, block, max_entries_of(rows, s->E, block), s->H, s->F, true);
 }
 
 Layout matvec_layout(int rows, int n_segments) {
   const int r = rows > 0 ? rows : 1;
-  // a segment with n rows has ceil(n / kDecRows) entries
-  const int ent = n_segments < r ? n_segments + r / kDecRows : r;
-  return layout_of(r, row_cap_of(r), ent, 0, 0, false);
+  const int block = row_block_of(r, n_segments, r);
+  return layout_of(r, block, max_entries_of(r, n_segments, block), 0, 0, false);
 }
 
 template <typename T>
@@ -219,6 +233,7 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   ra.entries = at<DecEntry>(ws, L.entries);
   ra.col_tickets = at<int>(ws, L.col_tickets);
   ra.n_col_tickets = (s->H + kDecBN - 1) / kDecBN;
+  ra.row_block = L.row_cap;
   cudaError_t e = launch_decode_route(ra, st);
   if (e != cudaSuccess) return cuda_fail(e, "decode route launch");
 
@@ -348,6 +363,7 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   pa.ctrl = static_cast<int*>(ws);
   pa.entries = at<DecEntry>(ws, L.entries);
   pa.max_entries = L.max_entries;
+  pa.row_block = L.row_cap;
   cudaError_t e = launch_decode_prep(pa, st);
   if (e != cudaSuccess) return cuda_fail(e, "entry list launch");
 

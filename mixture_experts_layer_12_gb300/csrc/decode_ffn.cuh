@@ -221,31 +221,21 @@ __device__ __forceinline__ uint4 activated(const float4 (&z)[2], const float4 (&
                     pack_bf16x2(h[6], h[7]));
 }
 
-// A shared item of the first product, put together by one group (128 threads):
-// the sum of the partial tiles of CTAs c0..c1 in that order, 4 columns of a row
-// per thread and step.
-__device__ __forceinline__ void finish_item(const DecFfnArgs& p, const DecEntry& en, int nb, int c0, int c1,
-                                            int ftid) {
+// A whole item of the first product to h (or y), by one group (128 threads):
+// 4 columns of a row per thread and step; tile(r, c): its sums.
+template <typename Tile>
+__device__ __forceinline__ void write_item(const DecFfnArgs& p, const DecEntry& en, int nb, int ftid, Tile tile) {
   const bool swiglu = p.act == kDecSwiGLU;
   const int cols = swiglu ? 64 : kDecBN;
-  const size_t tile = (size_t)p.row_cap * kDecBN;
-  const float* first = p.parts + (size_t)(c0 * 2 + 1) * tile;  // the later ones are in their slot 0
   uint16_t* out = p.act == kDecNone ? p.y : p.h;
+#pragma unroll 1
   for (int i = ftid; i < en.n * (cols / 4); i += DF_FIN) {
     const int r = i / (cols / 4), cl = (i % (cols / 4)) * 4;
     const int col = nb * cols + cl;
     if (col >= p.N1) continue;  // N1 is a multiple of 8
-    const float* s = first + r * kDecBN + cl;
-    float4 z = __ldcg(reinterpret_cast<const float4*>(s));
-    float4 u = swiglu ? __ldcg(reinterpret_cast<const float4*>(s + 64)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int o = 1; o <= c1 - c0; ++o) {
-      const float* q = s + (size_t)(2 * o - 1) * tile;
-      const float4 d = __ldcg(reinterpret_cast<const float4*>(q));
-      add4(z, d);
-      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(q + 64)));
-    }
+    float4 z = tile(r, cl);
     if (swiglu) {
+      const float4 u = tile(r, cl + 64);
       z = make_float4(dec_silu(z.x) * u.x, dec_silu(z.y) * u.y, dec_silu(z.z) * u.z, dec_silu(z.w) * u.w);
     } else if (p.act == kDecGelu) {
       z = make_float4(dec_gelu(z.x), dec_gelu(z.y), dec_gelu(z.z), dec_gelu(z.w));
@@ -300,9 +290,9 @@ struct Cfg {
   static constexpr int PITCH = KC * 2 + 16;             // bytes of a row's chunk: no bank conflicts
   static constexpr int S_BYTES = Q4 ? 8 * 256 : 0;      // scales: up to 8 groups x 128 columns
   static constexpr int W_STAGE = DF_W_BYTES + S_BYTES;
-  static constexpr int RED_GROUP = DF_FIN * 2 * NT * 4;    // floats a group hands over
+  static constexpr int RED_GROUP = DF_FIN * 2 * NT * 4;    // floats a group hands over: 8 NT rows x 128
   static constexpr int RED = KG * (KG - 1) * RED_GROUP * 4;
-  static constexpr int CTRL = 18 * 1024;
+  static constexpr int CTRL = 15 * 1024;
   static constexpr int SPACE = DF_SMEM - 1024 - RED - CTRL;  // for the rings
   // reads of rows past an entry's last stay inside: RED and CTRL follow the rows
   static_assert(RED + CTRL >= 8 * PITCH, "room behind the rows");
@@ -316,13 +306,13 @@ struct Ctrl {
   int max_rows;
   int last[DF_MAX_KG];
   DecEntry ent[kDecMaxEntries];
-  int2 owner[DF_MAX_KG][kDecMaxEntries];     // combine: CTAs of the column block's items
+  short2 owner[DF_MAX_KG][kDecMaxEntries];   // combine: CTAs of the column block's items
   uint16_t row_entry[MOED_MAX_ROWS];  // layer: entry of a row
-  int tok[MOED_MAX_ROWS];             // row of x of a dispatch row
-  int slot[MOED_MAX_ROWS];            // layer: [T, k]
+  int16_t tok[MOED_MAX_ROWS];         // row of x of a dispatch row
+  int16_t slot[MOED_MAX_ROWS];        // layer: [T, k]
   float gate[MOED_MAX_ROWS];
 };
-static_assert(sizeof(Ctrl) <= 18 * 1024, "control area");
+static_assert(sizeof(Ctrl) <= 15 * 1024, "control area");
 
 // One product's chunks, in item order, dealt to the first G = min(CTAs, total)
 // CTAs: CTA c < G takes chunks [total c / G, total (c + 1) / G), at least one.
@@ -479,11 +469,11 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
   } else {
     for (int i = tid - 32; i < p.T * p.k; i += C::THREADS - 32) {
       if (layer) {
-        c.slot[i] = __ldcg(p.slot + i);
+        c.slot[i] = (int16_t)__ldcg(p.slot + i);
         c.gate[i] = __ldcg(p.gate + i);
-        c.tok[i] = min(max(__ldcg(p.perm + i), 0), p.T * p.k - 1) / p.k;
+        c.tok[i] = (int16_t)(min(max(__ldcg(p.perm + i), 0), p.T * p.k - 1) / p.k);
       } else {
-        c.tok[i] = i;
+        c.tok[i] = (int16_t)i;
       }
     }
     named_sync(BAR_SETUP, C::THREADS);
@@ -890,79 +880,48 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
         const int bar_fin = BAR_FIN + kg;
 
+        // The item's sums as rows of 128 columns in this group's own space (it
+        // is free while the group writes), so that only real rows cost
+        // anything and every access to memory is 4 columns wide.
+        float* tile_s = sRed + kg * (KG - 1) * C::RED_GROUP;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (row_of(n, r) < en.n) tile_s[row_of(n, r) * kDecBN + col_of(m, r)] = acc[m][n][r];
+        named_sync(bar_fin, DF_FIN);
         if (k0 != 0 || k1 != KCN) {
           // a shared item: this CTA's partial tile, slot 0 if the item began in
           // an earlier CTA, else slot 1
           float* mine = (ph ? p.parts2 : p.parts) + (size_t)(cta * 2 + (k0 > 0 ? 0 : 1)) * p.row_cap * kDecBN;
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if (row_of(n, r) < en.n) mine[row_of(n, r) * kDecBN + col_of(m, r)] = acc[m][n][r];
-        } else {
-          if (ph == 1) {  // whole items of the second product stay in fp32 for the combine
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const int col = nb * kDecBN + col_of(m, r);
-                  if (row_of(n, r) < en.n && col < N)
-                    p.yfull[(size_t)(en.row0 + row_of(n, r)) * N + col] = acc[m][n][r];
-                }
-          } else {
-            uint16_t* out = layer ? p.h : p.y;
-            // gated: gate columns meet up columns, warps 2, 3 hand over to 0, 1
-            // in this group's own space, which is free while it writes
-            float* red = sRed + kg * (KG - 1) * C::RED_GROUP;
-            if (sg) {
-              if (wn >= 2) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                      red[((m * NT + n) * 4 + r) * 64 + (wn - 2) * 32 + lane] = acc[m][n][r];
-              }
-              named_sync(bar_fin, DF_FIN);
-            }
-            if (!sg || wn < 2) {
-#pragma unroll
-              for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    const int col = nb * (sg ? 64 : kDecBN) + col_of(m, r);
-                    if (row_of(n, r) < en.n && col < N) {
-                      float v = acc[m][n][r];
-                      if (sg)
-                        v = dec_silu(v) * red[((m * NT + n) * 4 + r) * 64 + wn * 32 + lane];
-                      else if (layer)
-                        v = dec_gelu(v);
-                      out[(size_t)(en.row0 + row_of(n, r)) * N + col] =
-                          (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
-                    }
-                  }
-            }
-            if (sg) named_sync(bar_fin, DF_FIN);  // before this space is handed over again
+          for (int i = ftid * 4; i < en.n * kDecBN; i += DF_FIN * 4)
+            *reinterpret_cast<float4*>(mine + i) = *reinterpret_cast<const float4*>(tile_s + i);
+        } else if (ph == 1) {  // whole items of the second product stay in fp32 for the combine
+          for (int i = ftid * 4; i < en.n * kDecBN; i += DF_FIN * 4) {
+            const int col = nb * kDecBN + (i & (kDecBN - 1));
+            if (col < N)
+              *reinterpret_cast<float4*>(p.yfull + (size_t)(en.row0 + i / kDecBN) * N + col) =
+                  *reinterpret_cast<const float4*>(tile_s + i);
           }
+        } else {
+          write_item(p, en, nb, ftid, [&](int r, int c) {
+            return *reinterpret_cast<const float4*>(tile_s + r * kDecBN + c);
+          });
         }
+        named_sync(bar_fin, DF_FIN);  // before this space is handed over again
 
         // (The other groups' items before this one are written too: they came
         // to this item's barrier after them.)
         if (ph == 1 && (x == end || (int)(x / ((uint32_t)n_ent * KCN)) != nb)) {
           // ---- this CTA's part of column block nb is written: count in, and
           // combine the block if it is the last part
-          int2* owner = c.owner[kg];
+          short2* owner = c.owner[kg];
           const uint32_t b0 = (uint32_t)nb * n_ent * KCN;
           for (int i = ftid; i < n_ent; i += DF_FIN) {
             const uint32_t i0 = b0 + (uint32_t)i * KCN;
-            owner[i] = make_int2(sp.owner(i0), sp.owner(i0 + KCN - 1));
+            owner[i] = make_short2((short)sp.owner(i0), (short)sp.owner(i0 + KCN - 1));
           }
           named_sync(bar_fin, DF_FIN);
           if (ftid == 0) {
@@ -991,7 +950,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
                   if (row >= 0) {
                     w[u] = c.gate[tok * p.k + j0 + u];
                     const int ei = c.row_entry[row];
-                    const int2 own = owner[ei];
+                    const short2 own = owner[ei];
                     more[u] = own.y - own.x;
                     src[u] = more[u] == 0 ? p.yfull + (size_t)row * N + col0 + cl
                                           : p.parts2 + ((size_t)(own.x * 2 + 1) * p.row_cap + row - c.ent[ei].row0) * kDecBN + cl;
@@ -1044,9 +1003,22 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
           }
           named_sync(BAR_CONS, CTHREADS);
-          if (kg < 2 && c.last[kg])
-            finish_item(p, c.ent[(kg == 0 ? first : last) / NB], (kg == 0 ? first : last) % NB,
-                        (c.last[kg] - 1) >> 16, (c.last[kg] - 1) & 0xFFFF, ftid);
+          if (kg < 2 && c.last[kg]) {
+            // the sum of the CTAs' tiles in their order: the first one's slot
+            // 1, the later ones' slot 0
+            const int it = kg == 0 ? first : last;
+            const int c0 = (c.last[kg] - 1) >> 16, c1 = (c.last[kg] - 1) & 0xFFFF;
+            const size_t tile = (size_t)p.row_cap * kDecBN;
+            const float* t0 = p.parts + (size_t)(c0 * 2 + 1) * tile;
+            write_item(p, c.ent[it / NB], it % NB, ftid, [&](int r, int col) {
+              const float* t = t0 + r * kDecBN + col;
+              float4 z = __ldcg(reinterpret_cast<const float4*>(t));
+#pragma unroll 4
+              for (int o = 1; o <= c1 - c0; ++o)
+                add4(z, __ldcg(reinterpret_cast<const float4*>(t + (size_t)(2 * o - 1) * tile)));
+              return z;
+            });
+          }
         }
         if (layer) {  // this CTA's h is there: the grid barrier
           if (!reader) named_sync(BAR_CONS, CTHREADS);

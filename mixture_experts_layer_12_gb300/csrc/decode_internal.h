@@ -16,11 +16,11 @@ struct DecEntry {
   int32_t pad;
 };
 
-constexpr int kDecRows = MOED_MAX_TOKENS;  // rows of an entry at most
+constexpr int kDecRows = 64;               // rows of an entry at most
 constexpr int kDecMaxCtas = 152;           // CTAs of the streaming kernel
 // entries: at most one per expert or segment, plus the row blocks that long
-// segments are cut into
-constexpr int kDecMaxEntries = kMaxExperts + MOED_MAX_ROWS / kDecRows;
+// ones are cut into
+constexpr int kDecMaxEntries = kMaxExperts + MOED_MAX_ROWS / 8;
 
 // Control block at the start of a workspace, cleared by the first kernel of
 // every call.  bytes: [status 64 | barrier 64 | item tickets | n_entries].
@@ -48,6 +48,7 @@ struct DecRouteArgs {
   DecEntry* entries;
   int* col_tickets;    // [n_col_tickets], zeroed here
   int n_col_tickets;
+  int row_block;       // rows of an entry at most
 };
 cudaError_t launch_decode_route(const DecRouteArgs& a, cudaStream_t st);
 
@@ -58,6 +59,7 @@ struct DecPrepArgs {
   int* ctrl;
   DecEntry* entries;
   int max_entries;     // room in `entries`
+  int row_block;       // rows of an entry at most
 };
 cudaError_t launch_decode_prep(const DecPrepArgs& a, cudaStream_t st);
 

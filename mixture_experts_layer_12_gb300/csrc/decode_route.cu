@@ -115,7 +115,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   __shared__ int s_ids[DR_MAX_ASSIGN];
   __shared__ int s_wc[DR_CHUNKS][kMaxExperts];
   __shared__ int s_off[kMaxExperts + 1];
-  __shared__ int s_scan[3][DR_WARPS];
+  __shared__ int s_scan[2][DR_WARPS];
   __shared__ float s_log[DR_WARPS][kMaxExperts];
   __shared__ uint32_t s_key[DR_WARPS][kMaxExperts];
 
@@ -344,43 +344,40 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
     }
     kept = a.capacity >= 0 ? min(run, a.capacity) : run;
   }
-  // exclusive scans over the experts of the kept rows and of the experts hit
-  const unsigned hit = __ballot_sync(0xffffffffu, kept > 0);
-  int incl = kept;
+  // exclusive scans over the experts of the kept rows and of their row blocks
+  // (16 bits each: at most 512 of either)
+  const int blocks = (kept + a.row_block - 1) / a.row_block;
+  int incl = kept | blocks << 16;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += v;
   }
-  if (lane == 31) {
-    s_scan[0][warp] = incl;
-    s_scan[1][warp] = __popc(hit);
-  }
-  const int longest = __reduce_max_sync(0xffffffffu, kept);
-  if (lane == 0) s_scan[2][warp] = longest;
+  if (lane == 31) s_scan[0][warp] = incl;
+  const int longest = __reduce_max_sync(0xffffffffu, min(kept, a.row_block));
+  if (lane == 0) s_scan[1][warp] = longest;
   __syncthreads();
-  int base = 0, hbase = 0, total = 0, htotal = 0, max_rows = 0;
+  int before = 0, all = 0, max_rows = 0;
 #pragma unroll
   for (int w = 0; w < DR_WARPS; ++w) {
-    max_rows = max(max_rows, s_scan[2][w]);
-    if (w < warp) {
-      base += s_scan[0][w];
-      hbase += s_scan[1][w];
-    }
-    total += s_scan[0][w];
-    htotal += s_scan[1][w];
+    max_rows = max(max_rows, s_scan[1][w]);
+    if (w < warp) before += s_scan[0][w];
+    all += s_scan[0][w];
   }
+  const int total = all & 0xFFFF;
   if (tid < E) {
-    const int off = base + incl - kept;
+    const int excl = before + incl;
+    const int off = (excl & 0xFFFF) - kept;
     s_off[tid] = off;
     a.counts[tid] = kept;
     a.offsets[tid] = off;
-    if (kept > 0)
-      a.entries[hbase + __popc(hit & ((1u << lane) - 1u))] = DecEntry{tid, off, kept, 0};
+    for (int b = 0; b < blocks; ++b)
+      a.entries[(excl >> 16) - blocks + b] =
+          DecEntry{tid, off + b * a.row_block, min(a.row_block, kept - b * a.row_block), 0};
   }
   if (tid == 0) {
     a.offsets[E] = total;
-    a.ctrl[kDecCountOffset / 4] = htotal;
+    a.ctrl[kDecCountOffset / 4] = all >> 16;
     a.ctrl[kDecCountOffset / 4 + 1] = max_rows;
   }
   __syncthreads();
@@ -401,7 +398,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   for (int i = total + tid; i < n; i += DR_THREADS) a.perm[i] = -1;
 }
 
-// Entries of the grouped products: segment i's rows in blocks of kDecRows.
+// Entries of the grouped products: segment i's rows in blocks of row_block.
 __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
   __shared__ int s_scan[8], s_rows[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -416,14 +413,14 @@ __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
     const int o1 = a.seg_offsets ? min(max(__ldg(a.seg_offsets + tid + 1), 0), a.rows) : a.rows;
     n = max(o1 - o0, 0);
   }
-  const int blocks = (n + kDecRows - 1) / kDecRows;
+  const int blocks = (n + a.row_block - 1) / a.row_block;
   int incl = blocks;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += v;
   }
-  const int longest = __reduce_max_sync(0xffffffffu, min(n, kDecRows));
+  const int longest = __reduce_max_sync(0xffffffffu, min(n, a.row_block));
   if (lane == 31) {
     s_scan[warp] = incl;
     s_rows[warp] = longest;
@@ -438,7 +435,7 @@ __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
   }
   int at = base + incl - blocks;
   for (int b = 0; b < blocks && at < a.max_entries; ++b, ++at)
-    a.entries[at] = DecEntry{tid % a.E, o0 + b * kDecRows, min(kDecRows, n - b * kDecRows), 0};
+    a.entries[at] = DecEntry{tid % a.E, o0 + b * a.row_block, min(a.row_block, n - b * a.row_block), 0};
   if (tid == 0) {
     a.ctrl[kDecCountOffset / 4] = min(total, a.max_entries);
     a.ctrl[kDecCountOffset / 4 + 1] = max_rows;
