@@ -12,8 +12,6 @@ from __future__ import annotations
 
 import ctypes
 import threading
-from contextlib import nullcontext
-from dataclasses import dataclass
 
 import torch
 
@@ -35,9 +33,9 @@ _sig_lib = None
 def _lib():
     """The library with the decode entry points' signatures set."""
     global _sig_lib
+    if _sig_lib is not None:
+        return _sig_lib
     lib = load_library()
-    if lib is _sig_lib:
-        return lib
     with _sig_lock:
         P, S, I, Z = ctypes.c_void_p, ctypes.POINTER(moe_shape), ctypes.c_int32, ctypes.c_size_t
         sig = {
@@ -73,7 +71,8 @@ def moed_forward(shape, x, w_router, b_router, w1, w2, y, ids, weights, counts, 
 
 
 def _q4_ptrs(w, E, K, N, name):
-    """(codes, scales) pointers of `w` checked against W [E, K, N]."""
+    """(codes, scales) pointers of `w` checked against W [E, K, N] and the
+    current device."""
     if (w.E, w.K, w.N) != (E, K, N):
         raise ValueError(f"{name} is [{w.E}, {w.K}, {w.N}]; the shape needs [{E}, {K}, {N}]")
     return (_ptr(w.codes, _I32, f"{name}.codes", E * (K // 8) * N),
@@ -136,7 +135,7 @@ class Q4Weights:
     E they describe one matrix (E = 1).  The group size follows from the
     shapes."""
 
-    __slots__ = ("codes", "scales", "E", "K", "N", "group")
+    __slots__ = ("_codes", "_scales", "E", "K", "N", "group", "_device", "_args")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         if codes.dtype != _I32 or scales.dtype != _BF:
@@ -153,63 +152,126 @@ class Q4Weights:
             raise ValueError(f"groups of {group} rows: 32, 64 or 128 are supported")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales = codes, scales
         self.E, self.K, self.N, self.group = E, K8 * 8, N, group
+        # what the calls below pass for them
+        self._device = codes.get_device() if codes.device == scales.device else -1
+        self._args = (ctypes.c_void_p(codes.data_ptr()), ctypes.c_void_p(scales.data_ptr()))
+
+    # fixed for the object's life: the calls use their addresses
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
 
 
 def _on(stream):
-    """Allocation context: memory used on `stream` is allocated for it."""
-    if stream is None:
-        return nullcontext()
+    """`stream` (a torch stream or a raw handle) as the current stream."""
     if isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)
     return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
 
 
+def _here():
+    """(current device, its current stream's handle)."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _addr(t: torch.Tensor, dtype, name: str, numel: int, dev: int) -> int:
+    """Address of `t` after the binding's checks (see check_tensor)."""
+    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= numel):
+        check_tensor(t, dtype, name, numel, dev)
+    return t.data_ptr()
+
+
+def _q4_here(w: Q4Weights, dev: int):
+    if w._device != dev:
+        raise ValueError(f"the 4-bit weights' codes are on {w.codes.device} and their scales on "
+                         f"{w.scales.device}, the current device is cuda:{dev}")
+    return w._args
+
+
 def quantize_q4(w: torch.Tensor, group: int = 128, stream=None) -> Q4Weights:
     """bf16 w [E, K, N] or [K, N] -> :class:`Q4Weights`."""
-    w3 = w.unsqueeze(0) if w.dim() == 2 else w
-    if w3.dim() != 3:
+    if stream is not None:
+        with _on(stream):
+            return quantize_q4(w, group)
+    if w.dim() not in (2, 3):
         raise ValueError(f"w must be [E, K, N] or [K, N], got {tuple(w.shape)}")
-    E, K, N = w3.shape
+    E, (K, N) = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2:]
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"group = {group}: need 32, 64 or 128, dividing K = {K}")
-    with _on(stream):
-        codes = torch.empty(E, K // 8, N, dtype=_I32, device=w.device)
-        scales = torch.empty(E, K // group, N, dtype=_BF, device=w.device)
-    moed_quantize_q4(w3, codes, scales, group, stream)
-    return Q4Weights(codes, scales)
+    dev, raw = _here()
+    src = _addr(w, _BF, "w", E * K * N, dev)
+    codes = torch.empty((E, K // 8, N), dtype=_I32, device=w.device)
+    scales = torch.empty((E, K // group, N), dtype=_BF, device=w.device)
+    q = Q4Weights(codes, scales)
+    _check(_lib().moed_quantize_q4(E, K, N, group, src, *q._args, raw))
+    return q
 
 
 def dequantize_q4(w: Q4Weights, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The bf16 matrices [E, K, N] that `w` stands for."""
-    if out is None:
+    if stream is not None:
         with _on(stream):
-            out = torch.empty(w.E, w.K, w.N, dtype=_BF, device=w.codes.device)
-    moed_dequantize_q4(w, out, stream)
+            return dequantize_q4(w, out)
+    dev, raw = _here()
+    q = _q4_here(w, dev)
+    if out is None:
+        out = torch.empty((w.E, w.K, w.N), dtype=_BF, device=w.codes.device)
+    dst = _addr(out, _BF, "out", w.E * w.K * w.N, dev)
+    _check(_lib().moed_dequantize_q4(w.E, w.K, w.N, w.group, *q, dst, raw))
     return out
+
+
+# Workspaces of matvec_q4: one per stream, grown as needed.  Calls on one
+# stream run one after the other and may share it; a call that is captured
+# into a CUDA graph gets its own.
+_matvec_bytes: dict = {}
+_matvec_ws: dict = {}
+
+
+def _matvec_workspace(rows: int, n_segments: int, K: int, N: int, dev: int, raw: int) -> torch.Tensor:
+    n = _matvec_bytes.get((rows, n_segments))
+    if n is None:
+        n = _matvec_bytes[rows, n_segments] = moed_matvec_q4_workspace_size(rows, n_segments, K, N)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    ws = _matvec_ws.get((dev, raw))
+    if ws is None or ws.numel() < n:
+        ws = _matvec_ws[dev, raw] = torch.empty(n, dtype=torch.uint8, device=dev)
+    return ws
 
 
 def matvec_q4(x: torch.Tensor, w: Q4Weights, seg_offsets: torch.Tensor | None = None,
               out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[r] = x[r] W[i % E] for the rows r of segment i (rows [seg_offsets[i],
-    seg_offsets[i+1]) of x); without seg_offsets all rows use W[0].  Rows of y
-    outside every segment are not written."""
-    if x.dim() != 2 or x.shape[1] != w.K:
-        raise ValueError(f"x must be [rows, {w.K}], got {tuple(x.shape)}")
+    seg_offsets[i+1]) of x); without seg_offsets all rows use a single matrix.
+    Rows of y outside every segment are not written."""
+    if stream is not None:
+        with _on(stream):
+            return matvec_q4(x, w, seg_offsets, out)
+    E, K, N = w.E, w.K, w.N
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [rows, {K}], got {tuple(x.shape)}")
     rows = x.shape[0]
+    dev, raw = _here()
     if seg_offsets is None:
-        if w.E != 1:
-            raise ValueError(f"seg_offsets is needed with {w.E} matrices")
-    elif seg_offsets.dim() != 1 or seg_offsets.numel() < 2:
-        raise ValueError("seg_offsets must be [n_segments + 1]")
-    n_segments = 1 if seg_offsets is None else seg_offsets.numel() - 1
-    n = moed_matvec_q4_workspace_size(rows, n_segments, w.K, w.N)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(rows, w.N, dtype=_BF, device=x.device)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    moed_matvec_q4(x, w, seg_offsets, out, ws, stream)
+        if E != 1:
+            raise ValueError(f"seg_offsets is needed with {E} matrices")
+        n_segments, seg = 1, None
+    else:
+        if seg_offsets.dim() != 1 or seg_offsets.numel() < 2:
+            raise ValueError("seg_offsets must be [n_segments + 1]")
+        n_segments = seg_offsets.numel() - 1
+        seg = _addr(seg_offsets, _I32, "seg_offsets", n_segments + 1, dev)
+    q = _q4_here(w, dev)
+    src = _addr(x, _BF, "x", rows * K, dev)
+    ws = _matvec_workspace(rows, n_segments, K, N, dev, raw)
+    if out is None:
+        out = torch.empty((rows, N), dtype=_BF, device=x.device)
+    dst = _addr(out, _BF, "out", rows * N, dev)
+    _check(_lib().moed_matvec_q4(rows, K, N, E, w.group, n_segments, src, *q, seg, dst, ws.data_ptr(),
+                                 ws.numel(), raw))
     return out
 
 
@@ -272,7 +334,7 @@ class MoEDecodeLayer:
         if bias is not None:
             check_tensor(bias, _F32, "bias", self.E, dev)
         self._w_router, self._w1, self._w2, self._bias = w_router, w1, w2, bias
-        self._device = w_router.device
+        self._device, self._index = w_router.device, dev
         self._held = weights  # the tensors behind the pointers below
         self._ptrs = (ctypes.c_void_p(w_router.data_ptr()),
                       ctypes.c_void_p(None if bias is None else bias.data_ptr()),
@@ -297,22 +359,21 @@ class MoEDecodeLayer:
         if stream is not None:  # as if it were the current stream
             with _on(stream):
                 return self(x)
-        dev = torch.cuda.current_device()
-        if x.dtype is not _BF or x.dim() != 2 or x.shape[1] != self.H or not x.is_contiguous():
-            raise ValueError(f"x must be a contiguous bfloat16 [T, {self.H}], got {x.dtype} {tuple(x.shape)}")
-        if self._device.index != dev or x.device != self._device:
-            raise ValueError(f"x is on {x.device} and the weights on {self._device}; the current device is "
-                             f"cuda:{dev}")
+        dev, raw = _here()
+        if x.dim() != 2 or x.shape[1] != self.H:
+            raise ValueError(f"x must be [T, {self.H}], got {tuple(x.shape)}")
+        if self._index != dev:
+            raise ValueError(f"the layer's weights are on {self._device}, the current device is cuda:{dev}")
         T = x.shape[0]
-        raw = torch.cuda.current_stream().cuda_stream
-        b = self._buffers.get((T, raw))
-        if b is None or torch.cuda.is_current_stream_capturing():
+        src = _addr(x, _BF, "x", T * self.H, dev)
+        capturing = torch.cuda.is_current_stream_capturing()
+        b = None if capturing else self._buffers.get((T, raw))
+        if b is None:
             b = _Buffers(self, T, raw)
-            if not torch.cuda.is_current_stream_capturing():
+            if not capturing:
                 self._buffers[T, raw] = b
-        y = torch.empty(x.shape, dtype=_BF, device=self._device)
-        p = self._ptrs
-        _check(self._fn(*b.head, x.data_ptr(), *p, y.data_ptr(), *b.tail))
+        y = torch.empty((T, self.H), dtype=_BF, device=self._device)
+        _check(self._fn(*b.head, src, *self._ptrs, y.data_ptr(), *b.tail))
         self._last = b
         return y
 
