@@ -40,15 +40,21 @@ struct Layout {
   int max_entries, row_cap;
 };
 
-// Rows of an entry at most: the kernel is built for 8, 16, 32 and 64, and its
-// cost grows with it (registers, ring space, products), so experts or segments
-// that hold 4 times the average or less should fit and longer ones are cut into
-// several entries, whose weights are read once each (37 rows over 64 segments:
-// 33.3 us with entries of 64 rows, 17.6 with 8).  `most`: rows that one can hold.
-int row_block_of(int rows, int parts, int most) {
-  const int want = 4 * ((rows + parts - 1) / parts);
+// Rows of an entry at most.  The kernel is built for 8, 16, 32 and 64 rows; an
+// expert or segment with more is cut into several entries, which read its
+// weights once each.  With 4-bit weights the cost of an entry grows with the
+// rows it has room for (registers, ring space, products): room for the average
+// and 1.4 times its square root more, what an even choice of experts hardly
+// exceeds (37 rows over 64 segments: 33 us with entries of up to 64 rows, 19
+// with 8; 32 rows over 8 experts: 121 us with 16, 118 with 8).  With bf16
+// weights reading them twice costs more than room does: 3 square roots.
+// `most`: rows that one can hold.
+int row_block_of(bool q4, int rows, int parts, int most) {
+  const int avg = (rows + parts - 1) / parts;
+  int root = 0;
+  while ((root + 1) * (root + 1) <= (q4 ? 2 : 9) * avg) ++root;
   int rb = 8;
-  while (rb < kDecRows && rb < want && rb < most) rb *= 2;
+  while (rb < kDecRows && rb < avg + root && rb < most) rb *= 2;
   return rb;
 }
 
@@ -73,15 +79,15 @@ int max_entries_of(int rows, int parts, int block) {
   return rows < parts ? rows : parts + (rows - parts) / block;
 }
 
-Layout layer_layout(const moe_shape* s) {
+Layout layer_layout(const moe_shape* s, bool q4) {
   const int rows = s->T > 0 ? s->T * s->k : 1;
-  const int block = row_block_of(rows, s->E, s->T);
+  const int block = row_block_of(q4, rows, s->E, s->T);
   return layout_of(rows, block, max_entries_of(rows, s->E, block), s->H, s->F, true);
 }
 
 Layout matvec_layout(int rows, int n_segments) {
   const int r = rows > 0 ? rows : 1;
-  const int block = row_block_of(r, n_segments, r);
+  const int block = row_block_of(true, r, n_segments, r);
   return layout_of(r, block, max_entries_of(r, n_segments, block), 0, 0, false);
 }
 
@@ -172,7 +178,7 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
             void* stream) {
   int rc;
   REQUIRE_PTR(ws);
-  const Layout L = layer_layout(s);
+  const Layout L = layer_layout(s, wt.q4);
   if (ws_bytes < L.total)
     return fail(MOE_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed (moed_workspace_size)",
                 ws_bytes, L.total);
@@ -282,7 +288,8 @@ extern "C" {
 
 size_t moed_workspace_size(const moe_shape* s) {
   if (check_layer(s) != MOE_OK) return 0;
-  return layer_layout(s).total;
+  const size_t a = layer_layout(s, false).total, b = layer_layout(s, true).total;
+  return a > b ? a : b;
 }
 
 int moed_forward(const moe_shape* s, const uint16_t* x, const uint16_t* w_router,

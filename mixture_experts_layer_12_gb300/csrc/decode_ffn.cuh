@@ -63,7 +63,14 @@ constexpr int DF_MAX_STAGES = 12;
 constexpr int DF_SMEM = 227 * 1024;
 constexpr int DF_CACHE = 24 * 1024; // h kept whole by its readers: at most this much of it
 
-constexpr int DF_MAX_KG = 3;   // consumer groups at most
+// Consumer warps: KG groups of 4 across the columns; group i takes every KG-th
+// chunk, so that a warp has a chunk's whole K to keep its pipes full between two
+// waits, and writes out every KG-th item while the other goes on multiplying.
+// 2 groups unpack and multiply a 4-bit chunk in 680 clocks, 3 in 660; one SM's
+// share of the memory brings it in 700.  With 3 the registers spill and the
+// ring is shorter, and the layers take as long.
+constexpr int KG = 2;
+constexpr int DF_BLOCKS = 64;  // column blocks combined at a time
 constexpr int DF_LOADERS = 3;  // row loaders: 12 warps in all, 3 to a scheduler
 
 // named barriers: set-up; all consumers; the writers of an item (one per group); an
@@ -71,7 +78,7 @@ constexpr int DF_LOADERS = 3;  // row loaders: 12 warps in all, 3 to a scheduler
 constexpr int BAR_SETUP = 0;
 constexpr int BAR_CONS = 1;
 constexpr int BAR_FIN = 2;
-constexpr int BAR_ITEM = BAR_FIN + DF_MAX_KG;
+constexpr int BAR_ITEM = BAR_FIN + KG;
 
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -202,6 +209,36 @@ __device__ __forceinline__ float dec_gelu(float z) {
 }
 __device__ __forceinline__ float dec_silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
 
+struct Ctrl {
+  uint64_t full[DF_MAX_STAGES], empty[DF_MAX_STAGES];
+  int abort_flag;
+  int n_entries;
+  int max_rows;
+  int last[2];
+  DecEntry ent[kDecMaxEntries];
+  int block_last[DF_BLOCKS];          // combine: this CTA came last
+  uint16_t row_entry[MOED_MAX_ROWS];  // layer: entry of a row
+  int16_t tok[MOED_MAX_ROWS];         // row of x of a dispatch row
+  int16_t slot[MOED_MAX_ROWS];        // layer: [T, k]
+  float gate[MOED_MAX_ROWS];
+};
+static_assert(sizeof(Ctrl) <= 12 * 1024, "control area");
+
+// One product's chunks, in item order, dealt to the first G = min(CTAs, total)
+// CTAs: CTA c < G takes chunks [total c / G, total (c + 1) / G), at least one.
+// The host keeps total * CTAs below 2^32.
+struct Split {
+  uint32_t total, G;
+  __device__ __forceinline__ Split(uint32_t n, uint32_t ctas) : total(n), G(min(ctas, n)) {}
+  __device__ __forceinline__ uint32_t start(uint32_t c) const {
+    return c < G ? total * c / G : total;
+  }
+  // the CTA that holds chunk x: the largest c with total c / G < x + 1
+  __device__ __forceinline__ int owner(uint32_t x) const {
+    return (int)(((x + 1) * G - 1) / total);
+  }
+};
+
 __device__ __forceinline__ void add4(float4& a, const float4 b) {
   a.x += b.x;
   a.y += b.y;
@@ -221,27 +258,137 @@ __device__ __forceinline__ uint4 activated(const float4 (&z)[2], const float4 (&
                     pack_bf16x2(h[6], h[7]));
 }
 
-// A whole item of the first product to h (or y), by one group (128 threads):
-// 4 columns of a row per thread and step; tile(r, c): its sums.
-template <typename Tile>
-__device__ __forceinline__ void write_item(const DecFfnArgs& p, const DecEntry& en, int nb, int ftid, Tile tile) {
+// 4 columns of the first product, activated, to h (or y)
+__device__ __forceinline__ void write_piece(const DecFfnArgs& p, size_t at, float4 z, const float4& u) {
+  if (p.act == kDecSwiGLU) {
+    z = make_float4(dec_silu(z.x) * u.x, dec_silu(z.y) * u.y, dec_silu(z.z) * u.z, dec_silu(z.w) * u.w);
+  } else if (p.act == kDecGelu) {
+    z = make_float4(dec_gelu(z.x), dec_gelu(z.y), dec_gelu(z.z), dec_gelu(z.w));
+  }
+  *reinterpret_cast<uint2*>((p.act == kDecNone ? p.y : p.h) + at) =
+      make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
+}
+
+// A whole item of the first product, from its sums in shared memory, by one
+// group (128 threads): 4 columns of a row per thread and step.
+__device__ __forceinline__ void write_item(const DecFfnArgs& p, const DecEntry& en, int nb, int ftid,
+                                           const float* tile) {
   const bool swiglu = p.act == kDecSwiGLU;
   const int cols = swiglu ? 64 : kDecBN;
-  uint16_t* out = p.act == kDecNone ? p.y : p.h;
 #pragma unroll 1
   for (int i = ftid; i < en.n * (cols / 4); i += DF_FIN) {
     const int r = i / (cols / 4), cl = (i % (cols / 4)) * 4;
     const int col = nb * cols + cl;
     if (col >= p.N1) continue;  // N1 is a multiple of 8
-    float4 z = tile(r, cl);
-    if (swiglu) {
-      const float4 u = tile(r, cl + 64);
-      z = make_float4(dec_silu(z.x) * u.x, dec_silu(z.y) * u.y, dec_silu(z.z) * u.z, dec_silu(z.w) * u.w);
-    } else if (p.act == kDecGelu) {
-      z = make_float4(dec_gelu(z.x), dec_gelu(z.y), dec_gelu(z.z), dec_gelu(z.w));
+    const float4* t = reinterpret_cast<const float4*>(tile + r * kDecBN + cl);
+    write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, t[0], swiglu ? t[16] : t[0]);
+  }
+}
+
+// The shared items of the first product that this CTA came last to (at most
+// two), by all consumer threads: the sums of the tiles of CTAs c0..c1 in that
+// order (the first one's slot 1, the later ones' slot 0), 2 pieces' loads in
+// flight together.
+struct Finish {
+  int row0, n, nb, c0, c1;  // n = 0: nothing
+};
+template <int CTHREADS>
+__device__ __forceinline__ void finish_items(const DecFfnArgs& p, const Finish (&f)[2], int ctid) {
+  const bool swiglu = p.act == kDecSwiGLU;
+  const int q = swiglu ? 16 : kDecBN / 4;  // pieces of a row
+  const size_t tile = (size_t)p.row_cap * kDecBN;
+  constexpr int UN = 2;
+  const int total0 = f[0].n * q, total = total0 + f[1].n * q;
+#pragma unroll 1
+  for (int i0 = ctid; i0 < total; i0 += UN * CTHREADS) {
+    float4 z[UN], u[UN];
+    const float* src[UN];
+    int more[UN];
+    size_t at[UN];
+#pragma unroll
+    for (int v = 0; v < UN; ++v) {
+      const int i = i0 + v * CTHREADS;
+      more[v] = -1;
+      if (i < total) {
+        const bool second = i >= total0;
+        const int pc = second ? i - total0 : i;
+        const int r = pc / q, cl = (pc % q) * 4;
+        const int c0 = second ? f[1].c0 : f[0].c0;
+        const int col = (second ? f[1].nb : f[0].nb) * q * 4 + cl;
+        if (col < p.N1) {  // N1 is a multiple of 8
+          more[v] = (second ? f[1].c1 : f[0].c1) - c0;
+          at[v] = (size_t)((second ? f[1].row0 : f[0].row0) + r) * p.N1 + col;
+          src[v] = p.parts + (size_t)(c0 * 2 + 1) * tile + r * kDecBN + cl;
+          z[v] = __ldcg(reinterpret_cast<const float4*>(src[v]));
+          u[v] = swiglu ? __ldcg(reinterpret_cast<const float4*>(src[v] + 64)) : z[v];
+        }
+      }
     }
-    *reinterpret_cast<uint2*>(out + (size_t)(en.row0 + r) * p.N1 + col) =
-        make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
+#pragma unroll
+    for (int v = 0; v < UN; ++v)
+      if (more[v] >= 0) {
+#pragma unroll 4
+        for (int o = 1; o <= more[v]; ++o) {
+          const float* s = src[v] + (size_t)(2 * o - 1) * tile;
+          add4(z[v], __ldcg(reinterpret_cast<const float4*>(s)));
+          if (swiglu) add4(u[v], __ldcg(reinterpret_cast<const float4*>(s + 64)));
+        }
+        write_piece(p, at[v], z[v], u[v]);
+      }
+  }
+}
+
+// Column block nb of y by all consumer threads: 4 columns of a token each, its
+// experts summed in slot order, their rows whole from yfull or, where CTAs
+// share the item, from their tiles in order (the first one's slot 1, the later
+// ones' slot 0).
+template <int CTHREADS>
+__device__ __forceinline__ void combine_block(const DecFfnArgs& p, const Ctrl& c, const Split& sp, int nb,
+                                              int ctid) {
+  const int N = p.N2, col0 = nb * kDecBN;
+  const size_t tile = (size_t)p.row_cap * kDecBN;
+#pragma unroll 1
+  for (int i = ctid; i < p.T * (kDecBN / 4); i += CTHREADS) {
+    const int tok = i / (kDecBN / 4), cl = (i % (kDecBN / 4)) * 4;
+    if (col0 + cl >= N) continue;  // N is a multiple of 8: all 4 columns or none
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < p.k; j0 += 4) {  // 4 experts' loads in flight together
+      const float* src[4];
+      int more[4];
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = j0 + u < p.k ? c.slot[tok * p.k + j0 + u] : -1;
+        more[u] = 0;
+        src[u] = nullptr;
+        if (row >= 0) {
+          const int ei = c.row_entry[row];
+          const uint32_t i0 = ((uint32_t)nb * c.n_entries + ei) * p.kc2;
+          const int o0 = sp.owner(i0);
+          more[u] = sp.owner(i0 + p.kc2 - 1) - o0;
+          src[u] = more[u] == 0 ? p.yfull + (size_t)row * N + col0 + cl
+                                : p.parts2 + (size_t)(o0 * 2 + 1) * tile + (row - c.ent[ei].row0) * kDecBN + cl;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        v[u] = src[u] ? __ldcg(reinterpret_cast<const float4*>(src[u])) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll 2
+        for (int o = 1; o <= more[u]; ++o)
+          add4(v[u], __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * o - 1) * tile)));
+        if (src[u]) {
+          const float w = c.gate[tok * p.k + j0 + u];
+          y.x = fmaf(w, v[u].x, y.x);
+          y.y = fmaf(w, v[u].y, y.y);
+          y.z = fmaf(w, v[u].z, y.z);
+          y.w = fmaf(w, v[u].w, y.w);
+        }
+      }
+    }
+    *reinterpret_cast<uint2*>(p.y + (size_t)tok * N + col0 + cl) =
+        make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
   }
 }
 
@@ -277,13 +424,6 @@ struct Int {
 
 template <bool Q4, int NT>
 struct Cfg {
-  // consumer warps: KG groups of 4 across the columns; group i takes every
-  // KG-th chunk, so that a warp has a chunk's whole K to keep its pipes full
-  // between two waits, and writes out every KG-th item while the others go on
-  // multiplying.  2 groups of 4 warps unpack and multiply a 4-bit chunk in 615
-  // clocks, 3 in 600, and one SM's share of the memory brings it in 700; the
-  // third group fills the pipes while another waits or writes.
-  static constexpr int KG = Q4 && NT <= 2 ? 3 : 2;
   static constexpr int CONSUMERS = DF_WN * KG;
   static constexpr int THREADS = 32 * (1 + DF_LOADERS + CONSUMERS);
   static constexpr int KC = Q4 ? kDecKC4 : kDecKC16;    // K rows of a chunk
@@ -291,102 +431,69 @@ struct Cfg {
   static constexpr int S_BYTES = Q4 ? 8 * 256 : 0;      // scales: up to 8 groups x 128 columns
   static constexpr int W_STAGE = DF_W_BYTES + S_BYTES;
   static constexpr int RED_GROUP = DF_FIN * 2 * NT * 4;    // floats a group hands over: 8 NT rows x 128
-  static constexpr int RED = KG * (KG - 1) * RED_GROUP * 4;
-  static constexpr int CTRL = 15 * 1024;
+  static constexpr int RED = KG * RED_GROUP * 4;
+  static constexpr int CTRL = 12 * 1024;
   static constexpr int SPACE = DF_SMEM - 1024 - RED - CTRL;  // for the rings
   // reads of rows past an entry's last stay inside: RED and CTRL follow the rows
   static_assert(RED + CTRL >= 8 * PITCH, "room behind the rows");
   static_assert(SPACE >= 2 * KG * W_STAGE, "weight ring");
 };
 
-struct Ctrl {
-  uint64_t full[DF_MAX_STAGES], empty[DF_MAX_STAGES];
-  int abort_flag;
-  int n_entries;
-  int max_rows;
-  int last[DF_MAX_KG];
-  DecEntry ent[kDecMaxEntries];
-  short2 owner[DF_MAX_KG][kDecMaxEntries];   // combine: CTAs of the column block's items
-  uint16_t row_entry[MOED_MAX_ROWS];  // layer: entry of a row
-  int16_t tok[MOED_MAX_ROWS];         // row of x of a dispatch row
-  int16_t slot[MOED_MAX_ROWS];        // layer: [T, k]
-  float gate[MOED_MAX_ROWS];
-};
-static_assert(sizeof(Ctrl) <= 15 * 1024, "control area");
-
-// One product's chunks, in item order, dealt to the first G = min(CTAs, total)
-// CTAs: CTA c < G takes chunks [total c / G, total (c + 1) / G), at least one.
-// The host keeps total * CTAs below 2^32.
-struct Split {
-  uint32_t total, G;
-  __device__ __forceinline__ Split(uint32_t n, uint32_t ctas) : total(n), G(min(ctas, n)) {}
-  __device__ __forceinline__ uint32_t start(uint32_t c) const {
-    return c < G ? total * c / G : total;
-  }
-  // the CTA that holds chunk x: the largest c with total c / G < x + 1
-  __device__ __forceinline__ int owner(uint32_t x) const {
-    return (int)(((x + 1) * G - 1) / total);
-  }
-};
-
 // One chunk of 4-bit weights for a warp's 32 columns and the first NTA 8-row
 // tiles: acc += W^T x.  w0: the weight stage, wofs: this lane's place in it at
-// even and odd steps; bl, bofs: the same in the rows; sl: its 4 columns' scales.  Everything is
-// unrolled and nothing branches, so that loads, unpacking and products of
-// different steps overlap.
+// even and odd steps of 32 rows of K; bl, bofs: the same in the rows; sl: its 4
+// columns' scales.  Nothing branches and, as far as the registers go, everything
+// is unrolled, so that loads, unpacking and products of different steps overlap.
+// A step's sum begins at zero and is scaled and added in fp32: a chain of products
+// through a whole group of 128 rows runs 3 times slower (717 -> 2612 clocks a
+// chunk on one warp per scheduler).
 template <int NT, int NTA, int GRP>
 __device__ __forceinline__ void chunk_q4(float (&acc)[2][NT][4], uint32_t w0, const uint32_t (&wofs)[2],
                                          uint32_t bl, const uint32_t (&bofs)[2], uint32_t sl) {
-  constexpr int STEPS = GRP / 32;  // 32 rows of K each
+  constexpr int UNROLL = NTA == 1 ? kDecKC4 / 64 : NTA == 2 ? 2 : 1;
+#pragma unroll UNROLL
+  for (uint32_t blk = 0; blk < kDecKC4 / 64; ++blk) {  // 64 rows of K
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int grp = 0; grp < kDecKC4 / GRP; ++grp) {
-    uint32_t s01, s23;
-    lds64(sl + grp * 256, s01, s23);
-    const float s[4] = {64.f * bf16_lo(s01), 64.f * bf16_hi(s01), 64.f * bf16_lo(s23), 64.f * bf16_hi(s23)};
-#pragma unroll
-    for (int st = 0; st < STEPS; ++st) {
-      const uint32_t blk = (uint32_t)(grp * STEPS + st) >> 1, i = (uint32_t)(grp * STEPS + st) & 1;
+    for (uint32_t i = 0; i < 2; ++i) {
+      if (GRP == 32 || i == 0) {
+        uint32_t s01, s23;
+        lds64(sl + (blk * 64 + i * 32) / GRP * 256, s01, s23);
+        s[0] = 64.f * bf16_lo(s01);
+        s[1] = 64.f * bf16_hi(s01);
+        s[2] = 64.f * bf16_lo(s23);
+        s[3] = 64.f * bf16_hi(s23);
+      }
       uint32_t v[4];  // columns 4g .. 4g + 3 of 8 rows of K
       lds128(w0 + blk * 1024 + wofs[i], v);
-      uint32_t b[NTA][4];
-#pragma unroll
-      for (int n = 0; n < NTA; ++n) {  // the same 8 rows of K, paired as the codes are
-        uint32_t x[4];
-        lds128(bl + n * 8 * (kDecKC4 * 2 + 16) + blk * 128 + bofs[i], x);
-        b[n][0] = __byte_perm(x[0], x[2], 0x5410);
-        b[n][1] = __byte_perm(x[0], x[2], 0x7632);
-        b[n][2] = __byte_perm(x[1], x[3], 0x5410);
-        b[n][3] = __byte_perm(x[1], x[3], 0x7632);
-      }
-      // a step's sum begins at zero and is scaled and added in fp32: a chain
-      // of products through a whole group of 128 rows runs 3 times slower
-      // (717 -> 2612 clocks a chunk on one warp per scheduler)
-      float part[2][NTA][4];
+      uint32_t a[2][8];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const uint32_t va = v[2 * m], vb = v[2 * m + 1];
-        uint32_t a[8];
-        a[0] = q4_pair<0>(va);
-        a[1] = q4_pair<0>(vb);
-        a[2] = q4_pair<1>(va);
-        a[3] = q4_pair<1>(vb);
-        a[4] = q4_pair<2>(va);
-        a[5] = q4_pair<2>(vb);
-        a[6] = q4_pair<3>(va);
-        a[7] = q4_pair<3>(vb);
-#pragma unroll
-        for (int n = 0; n < NTA; ++n) {
-          mma_bf16_zero(part[m][n], a[0], a[1], a[2], a[3], b[n][0], b[n][1]);
-          mma_bf16(part[m][n], a[4], a[5], a[6], a[7], b[n][2], b[n][3]);
-        }
+        a[m][0] = q4_pair<0>(va);
+        a[m][1] = q4_pair<0>(vb);
+        a[m][2] = q4_pair<1>(va);
+        a[m][3] = q4_pair<1>(vb);
+        a[m][4] = q4_pair<2>(va);
+        a[m][5] = q4_pair<2>(vb);
+        a[m][6] = q4_pair<3>(va);
+        a[m][7] = q4_pair<3>(vb);
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int n = 0; n < NTA; ++n) {
+        uint32_t x[4];  // the same 8 rows of K, paired as the codes are
+        lds128(bl + n * 8 * (kDecKC4 * 2 + 16) + blk * 128 + bofs[i], x);
+        const uint32_t b0 = __byte_perm(x[0], x[2], 0x5410), b1 = __byte_perm(x[0], x[2], 0x7632);
+        const uint32_t b2 = __byte_perm(x[1], x[3], 0x5410), b3 = __byte_perm(x[1], x[3], 0x7632);
 #pragma unroll
-        for (int n = 0; n < NTA; ++n)
+        for (int m = 0; m < 2; ++m) {
+          float part[4];
+          mma_bf16_zero(part, a[m][0], a[m][1], a[m][2], a[m][3], b0, b1);
+          mma_bf16(part, a[m][4], a[m][5], a[m][6], a[m][7], b2, b3);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[m][n][r] = fmaf(s[2 * m + (r >> 1)], part[m][n][r], acc[m][n][r]);
+          for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(s[2 * m + (r >> 1)], part[r], acc[m][n][r]);
+        }
+      }
     }
   }
 }
@@ -421,7 +528,6 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     decode_ffn_kernel(const __grid_constant__ DecFfnMaps maps, const DecFfnArgs p) {
   constexpr bool Q4 = GRP > 0;
   using C = Cfg<Q4, NT>;
-  constexpr int KG = C::KG;
   constexpr int CTHREADS = 32 * C::CONSUMERS;
   constexpr int PCS = C::KC / 8;  // 16-byte pieces of a row's chunk
   extern __shared__ uint8_t smem_raw[];
@@ -714,7 +820,6 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
       const int N = ph ? p.N2 : p.N1;
       const Split sp((uint32_t)n_ent * NB * KCN, G);
-      const bool sg = ph == 0 && swiglu;
       uint32_t x = sp.start(cta);
       const uint32_t end = sp.start(cta + 1);
       const bool cached = ph == 1 && reader;
@@ -848,13 +953,12 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         qi += (uint32_t)(k1 - k0);
         x += (uint32_t)(k1 - k0);
 
-        // ---- one group, in turn, sums all groups' parts and writes the item
-        // out; the others hand over and go on.  A group has a place for each
-        // of the KG - 1 items between two of its own: at its own item it meets
-        // the groups that wrote those, which have read them by then.
+        // ---- the groups in turn sum both parts and write the item out; the
+        // other hands over and goes on.  It hands over again only after an item
+        // of its own, for which the first has come to a barrier after this
+        // reading.
         const int writer = (int)(n_items % KG);
-        const int place = (int)(n_items % (KG - 1));
-        float* mine_red = sRed + (kg * (KG - 1) + place) * C::RED_GROUP;
+        float* mine_red = sRed + kg * C::RED_GROUP;
         ++n_items;
         if (kg != writer) {
 #pragma unroll
@@ -867,10 +971,8 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           continue;
         }
         named_sync(BAR_ITEM + writer, CTHREADS);
-#pragma unroll
-        for (int u = 1; u < KG; ++u) {
-          const int from = kg + u < KG ? kg + u : kg + u - KG;
-          const float* red = sRed + (from * (KG - 1) + place) * C::RED_GROUP;
+        {
+          const float* red = sRed + (1 - kg) * C::RED_GROUP;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -883,7 +985,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         // The item's sums as rows of 128 columns in this group's own space (it
         // is free while the group writes), so that only real rows cost
         // anything and every access to memory is 4 columns wide.
-        float* tile_s = sRed + kg * (KG - 1) * C::RED_GROUP;
+        float* tile_s = sRed + kg * C::RED_GROUP;
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -906,93 +1008,24 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
                   *reinterpret_cast<const float4*>(tile_s + i);
           }
         } else {
-          write_item(p, en, nb, ftid, [&](int r, int c) {
-            return *reinterpret_cast<const float4*>(tile_s + r * kDecBN + c);
-          });
+          write_item(p, en, nb, ftid, tile_s);
         }
         named_sync(bar_fin, DF_FIN);  // before this space is handed over again
 
-        // (The other groups' items before this one are written too: they came
-        // to this item's barrier after them.)
-        if (ph == 1 && (x == end || (int)(x / ((uint32_t)n_ent * KCN)) != nb)) {
-          // ---- this CTA's part of column block nb is written: count in, and
-          // combine the block if it is the last part
-          short2* owner = c.owner[kg];
-          const uint32_t b0 = (uint32_t)nb * n_ent * KCN;
-          for (int i = ftid; i < n_ent; i += DF_FIN) {
-            const uint32_t i0 = b0 + (uint32_t)i * KCN;
-            owner[i] = make_short2((short)sp.owner(i0), (short)sp.owner(i0 + KCN - 1));
-          }
-          named_sync(bar_fin, DF_FIN);
-          if (ftid == 0) {
-            const int parts = owner[n_ent - 1].y - owner[0].x + 1;
-            c.last[kg] = atom_acq_rel(p.col_tickets + nb) == (unsigned)(parts - 1);
-          }
-          named_sync(bar_fin, DF_FIN);
-          if (c.last[kg]) {
-            const int col0 = nb * kDecBN;
-            for (int i = ftid; i < p.T * (kDecBN / 4); i += DF_FIN) {
-              const int tok = i / (kDecBN / 4);
-              const int cl = (i % (kDecBN / 4)) * 4;
-              if (col0 + cl >= N) continue;  // N is a multiple of 8: all 4 columns or none
-              float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int j0 = 0; j0 < p.k; j0 += 4) {  // 4 experts' loads in flight together
-                const float* src[4];
-                int more[4];
-                float w[4];
-                float4 v[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const int row = j0 + u < p.k ? c.slot[tok * p.k + j0 + u] : -1;
-                  w[u] = 0.f;
-                  more[u] = 0;
-                  src[u] = nullptr;
-                  if (row >= 0) {
-                    w[u] = c.gate[tok * p.k + j0 + u];
-                    const int ei = c.row_entry[row];
-                    const short2 own = owner[ei];
-                    more[u] = own.y - own.x;
-                    src[u] = more[u] == 0 ? p.yfull + (size_t)row * N + col0 + cl
-                                          : p.parts2 + ((size_t)(own.x * 2 + 1) * p.row_cap + row - c.ent[ei].row0) * kDecBN + cl;
-                  }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  v[u] = src[u] ? __ldcg(reinterpret_cast<const float4*>(src[u])) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const size_t tile = (size_t)p.row_cap * kDecBN;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {  // the later CTAs' parts are in their slot 0
-#pragma unroll 2
-                  for (int o = 1; o <= more[u]; ++o) {
-                    const float4 d = __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * o - 1) * tile));
-                    add4(v[u], d);
-                  }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  if (src[u]) {
-                    y.x = fmaf(w[u], v[u].x, y.x);
-                    y.y = fmaf(w[u], v[u].y, y.y);
-                    y.z = fmaf(w[u], v[u].z, y.z);
-                    y.w = fmaf(w[u], v[u].w, y.w);
-                  }
-              }
-              *reinterpret_cast<uint2*>(p.y + (size_t)tok * N + col0 + cl) =
-                  make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-            }
-          }
-        }
       }
 
+      // ---- every group has written its items: what they share with other
+      // CTAs is counted in and, by whoever comes last, put together, by all
+      // consumer threads (more loads in flight, and the multiplying loop's
+      // registers are free: a spill costs this kernel a trip to memory behind
+      // the weights, as shared memory leaves no L1 to speak of)
+      named_sync(BAR_CONS, CTHREADS);
+      const uint32_t begin = sp.start(cta);
       if (ph == 0) {
-        // ---- every group has written its items
-        named_sync(BAR_CONS, CTHREADS);
         if (!reader) {
-          // shared items, at most the CTA's first and last: whoever counts in
-          // last puts the item together (group 0 the first, group 1 the last)
-          const uint32_t s0 = sp.start(cta);
-          const int first = s0 < end && s0 % KCN != 0 ? (int)(s0 / KCN) : -1;
-          const int last = s0 < end && end % KCN != 0 && (int)(end / KCN) != first ? (int)(end / KCN) : -1;
+          // shared items are at most the CTA's first and last
+          const int first = begin < end && begin % KCN != 0 ? (int)(begin / KCN) : -1;
+          const int last = begin < end && end % KCN != 0 && (int)(end / KCN) != first ? (int)(end / KCN) : -1;
           if (ctid < 2) {
             const int it = ctid == 0 ? first : last;
             c.last[ctid] = 0;
@@ -1003,26 +1036,39 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
           }
           named_sync(BAR_CONS, CTHREADS);
-          if (kg < 2 && c.last[kg]) {
-            // the sum of the CTAs' tiles in their order: the first one's slot
-            // 1, the later ones' slot 0
-            const int it = kg == 0 ? first : last;
-            const int c0 = (c.last[kg] - 1) >> 16, c1 = (c.last[kg] - 1) & 0xFFFF;
-            const size_t tile = (size_t)p.row_cap * kDecBN;
-            const float* t0 = p.parts + (size_t)(c0 * 2 + 1) * tile;
-            write_item(p, c.ent[it / NB], it % NB, ftid, [&](int r, int col) {
-              const float* t = t0 + r * kDecBN + col;
-              float4 z = __ldcg(reinterpret_cast<const float4*>(t));
-#pragma unroll 4
-              for (int o = 1; o <= c1 - c0; ++o)
-                add4(z, __ldcg(reinterpret_cast<const float4*>(t + (size_t)(2 * o - 1) * tile)));
-              return z;
-            });
+          if (c.last[0] | c.last[1]) {
+            Finish f[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int it = h == 0 ? first : last;
+              f[h] = Finish{0, 0, 0, 0, 0};
+              if (c.last[h]) {
+                const DecEntry en = c.ent[it / NB];
+                f[h] = Finish{en.row0, en.n, it % NB, (c.last[h] - 1) >> 16, (c.last[h] - 1) & 0xFFFF};
+              }
+            }
+            finish_items<CTHREADS>(p, f, ctid);
           }
         }
         if (layer) {  // this CTA's h is there: the grid barrier
           if (!reader) named_sync(BAR_CONS, CTHREADS);
           if (ctid == 0) red_release(p.barrier, 1u);
+        }
+      } else if (begin < end) {
+        // column blocks, up to DF_BLOCKS at a time
+        const uint32_t per = (uint32_t)n_ent * KCN;  // chunks of a block
+        const int nb0 = (int)(begin / per), nb1 = (int)((end - 1) / per);
+        for (int b = nb0; b <= nb1; b += DF_BLOCKS) {
+          const int n = min(DF_BLOCKS, nb1 + 1 - b);
+          if (ctid < n) {
+            const uint32_t i0 = (uint32_t)(b + ctid) * per;
+            const int parts = sp.owner(i0 + per - 1) - sp.owner(i0) + 1;
+            c.block_last[ctid] = atom_acq_rel(p.col_tickets + b + ctid) == (unsigned)(parts - 1);
+          }
+          named_sync(BAR_CONS, CTHREADS);
+          for (int i = 0; i < n; ++i)
+            if (c.block_last[i]) combine_block<CTHREADS>(p, c, sp, b + i, ctid);
+          named_sync(BAR_CONS, CTHREADS);
         }
       }
     }
