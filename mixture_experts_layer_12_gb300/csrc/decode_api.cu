@@ -32,11 +32,11 @@ cudaError_t launch_decode_ffn(const DecFfnMaps& m, const DecFfnArgs& a, int ctas
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Workspace: [control block | entries | column tickets | partial tiles |
-// expert outputs of whole items, fp32 | h].  The control block and the
-// tickets are cleared by the first kernel of every call.
+// Workspace: [control block | entries | partial tiles of both products | expert
+// outputs of whole items, fp32 | h].  The control block is cleared by the first
+// kernel of every call.
 struct Layout {
-  size_t entries, col_tickets, parts, parts2, yfull, h, total;
+  size_t entries, parts, parts2, yfull, h, total;
   int max_entries, row_cap;
 };
 
@@ -63,8 +63,7 @@ Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool laye
   L.max_entries = max_entries;
   L.row_cap = row_cap;
   L.entries = kDecEntryOffset;
-  L.col_tickets = L.entries + up((size_t)max_entries * sizeof(DecEntry), 1024);
-  L.parts = L.col_tickets + (layer ? up((size_t)((H + kDecBN - 1) / kDecBN) * 4, 1024) : 0);
+  L.parts = L.entries + up((size_t)max_entries * sizeof(DecEntry), 1024);
   const size_t tiles = (size_t)kDecMaxCtas * 2 * row_cap * kDecBN * 4;
   L.parts2 = L.parts + tiles;
   L.yfull = L.parts2 + (layer ? tiles : 0);
@@ -158,6 +157,15 @@ int empty_call(void* ws, int32_t* counts, int32_t* offsets, int E, cudaStream_t 
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "clearing an empty call's outputs");
 }
 
+// Chunks worth a CTA of their own where a product is too small for all CTAs: a
+// chunk is read in ~0.37 us and a partial tile added in ~0.25, so n chunks per
+// CTA and K-chunks / n tiles per item cost least at n = sqrt(0.7 K-chunks).
+int least_chunks(int kc) {
+  int n = 1;
+  while (10 * (n + 1) * (n + 1) <= 7 * kc && n < 64) ++n;
+  return n;
+}
+
 // The streaming kernel counts a product's chunks, times its CTAs, in 32 bits.
 int check_chunks(int64_t entries, int64_t nb, int64_t kc) {
   if (nb * kc > ((int64_t)1 << 32) / kDecMaxCtas || entries * nb * kc >= ((int64_t)1 << 32) / kDecMaxCtas)
@@ -237,8 +245,6 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   ra.slot = slot;
   ra.ctrl = static_cast<int*>(ws);
   ra.entries = at<DecEntry>(ws, L.entries);
-  ra.col_tickets = at<int>(ws, L.col_tickets);
-  ra.n_col_tickets = (s->H + kDecBN - 1) / kDecBN;
   ra.row_block = L.row_cap;
   cudaError_t e = launch_decode_route(ra, st);
   if (e != cudaSuccess) return cuda_fail(e, "decode route launch");
@@ -249,7 +255,6 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.max_entries = L.max_entries;
   fa.barrier = at<unsigned>(ws, kDecBarrierOffset);
   fa.item_tickets = at<unsigned>(ws, kDecTicketOffset);
-  fa.col_tickets = at<unsigned>(ws, L.col_tickets);
   fa.parts = at<float>(ws, L.parts);
   fa.row_cap = L.row_cap;
   fa.parts2 = at<float>(ws, L.parts2);
@@ -272,6 +277,8 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.N1 = s->F;
   fa.nb1 = nb1;
   fa.kc1 = kc1;
+  fa.least1 = least_chunks(kc1);
+  fa.least2 = least_chunks(kc2);
   fa.K2 = s->F;
   fa.N2 = s->H;
   fa.nb2 = nb2;
@@ -394,6 +401,8 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   fa.N1 = N;
   fa.nb1 = nb;
   fa.kc1 = kc;
+  fa.least1 = least_chunks(kc);
+  fa.least2 = 1;
   fa.status = static_cast<int*>(ws);
   fa.wait_limit_ns = kWaitLimitNs;
   e = launch_decode_ffn(maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);

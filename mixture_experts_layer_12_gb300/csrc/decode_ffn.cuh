@@ -40,14 +40,13 @@
 //   bound: one m16n8k16 per 256 weights is a tenth of the tensor rate at 8
 //   rows.
 //   * Between the products h goes through memory.  An item shared by several
-//     CTAs is put together either by its last CTA (a ticket) or, where a CTA's
-//     part of the second product needs little of h, by every CTA for the
-//     elements it needs, after the grid barrier, with all its threads at once:
-//     one trip to memory instead of three before the barrier.
-//   * Combine: a CTA that has finished its part of a column block counts
-//     itself in; the last one sums every token's experts in slot order.
-// The grid barrier needs all CTAs resident, which the cooperative launch
-// guarantees; it and every other wait is bounded.
+//     CTAs is put together by its last CTA (a ticket); by all CTAs, after a grid
+//     barrier, where it has many rows; or, where a CTA's part of the second
+//     product needs little of h, by every CTA for the elements it needs.
+//   * Combine: after a grid barrier all CTAs sum the tokens' experts in slot
+//     order, 128 columns of a token per warp.
+// The grid barriers need all CTAs resident, which the cooperative launch
+// guarantees; they and every other wait are bounded.
 #pragma once
 
 #include "decode_internal.h"
@@ -70,8 +69,10 @@ constexpr int DF_CACHE = 24 * 1024; // h kept whole by its readers: at most this
 // share of the memory brings it in 700.  With 3 the registers spill and the
 // ring is shorter, and the layers take as long.
 constexpr int KG = 2;
-constexpr int DF_BLOCKS = 64;  // column blocks combined at a time
 constexpr int DF_LOADERS = 3;  // row loaders: 12 warps in all, 3 to a scheduler
+
+// grid barriers: the first product's tiles are written, h is, the second's are
+constexpr int kGridTiles = 0, kGridH = 1, kGridY = 2;
 
 // named barriers: set-up; all consumers; the writers of an item (one per group); an
 // item's hand-over between the groups (one per writing group)
@@ -216,7 +217,6 @@ struct Ctrl {
   int max_rows;
   int last[2];
   DecEntry ent[kDecMaxEntries];
-  int block_last[DF_BLOCKS];          // combine: this CTA came last
   uint16_t row_entry[MOED_MAX_ROWS];  // layer: entry of a row
   int16_t tok[MOED_MAX_ROWS];         // row of x of a dispatch row
   int16_t slot[MOED_MAX_ROWS];        // layer: [T, k]
@@ -224,12 +224,14 @@ struct Ctrl {
 };
 static_assert(sizeof(Ctrl) <= 12 * 1024, "control area");
 
-// One product's chunks, in item order, dealt to the first G = min(CTAs, total)
-// CTAs: CTA c < G takes chunks [total c / G, total (c + 1) / G), at least one.
-// The host keeps total * CTAs below 2^32.
+// One product's chunks, in item order, dealt to the first G CTAs: CTA c < G takes
+// chunks [total c / G, total (c + 1) / G), at least one.  `least`: chunks that are
+// worth a CTA of their own (a small product cut finer is read faster than its
+// many partial tiles are added).  The host keeps total * CTAs below 2^32.
 struct Split {
   uint32_t total, G;
-  __device__ __forceinline__ Split(uint32_t n, uint32_t ctas) : total(n), G(min(ctas, n)) {}
+  __device__ __forceinline__ Split(uint32_t n, uint32_t ctas, uint32_t least)
+      : total(n), G(max(1u, min(ctas, n / least))) {}
   __device__ __forceinline__ uint32_t start(uint32_t c) const {
     return c < G ? total * c / G : total;
   }
@@ -338,68 +340,14 @@ __device__ __forceinline__ void finish_items(const DecFfnArgs& p, const Finish (
   }
 }
 
-// Column block nb of y by all consumer threads: 4 columns of a token each, its
-// experts summed in slot order, their rows whole from yfull or, where CTAs
-// share the item, from their tiles in order (the first one's slot 1, the later
-// ones' slot 0).
-template <int CTHREADS>
-__device__ __forceinline__ void combine_block(const DecFfnArgs& p, const Ctrl& c, const Split& sp, int nb,
-                                              int ctid) {
-  const int N = p.N2, col0 = nb * kDecBN;
-  const size_t tile = (size_t)p.row_cap * kDecBN;
-#pragma unroll 1
-  for (int i = ctid; i < p.T * (kDecBN / 4); i += CTHREADS) {
-    const int tok = i / (kDecBN / 4), cl = (i % (kDecBN / 4)) * 4;
-    if (col0 + cl >= N) continue;  // N is a multiple of 8: all 4 columns or none
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < p.k; j0 += 4) {  // 4 experts' loads in flight together
-      const float* src[4];
-      int more[4];
-      float4 v[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int row = j0 + u < p.k ? c.slot[tok * p.k + j0 + u] : -1;
-        more[u] = 0;
-        src[u] = nullptr;
-        if (row >= 0) {
-          const int ei = c.row_entry[row];
-          const uint32_t i0 = ((uint32_t)nb * c.n_entries + ei) * p.kc2;
-          const int o0 = sp.owner(i0);
-          more[u] = sp.owner(i0 + p.kc2 - 1) - o0;
-          src[u] = more[u] == 0 ? p.yfull + (size_t)row * N + col0 + cl
-                                : p.parts2 + (size_t)(o0 * 2 + 1) * tile + (row - c.ent[ei].row0) * kDecBN + cl;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        v[u] = src[u] ? __ldcg(reinterpret_cast<const float4*>(src[u])) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-#pragma unroll 2
-        for (int o = 1; o <= more[u]; ++o)
-          add4(v[u], __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * o - 1) * tile)));
-        if (src[u]) {
-          const float w = c.gate[tok * p.k + j0 + u];
-          y.x = fmaf(w, v[u].x, y.x);
-          y.y = fmaf(w, v[u].y, y.y);
-          y.z = fmaf(w, v[u].z, y.z);
-          y.w = fmaf(w, v[u].w, y.w);
-        }
-      }
-    }
-    *reinterpret_cast<uint2*>(p.y + (size_t)tok * N + col0 + cl) =
-        make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-  }
-}
-
-// Warp-wide wait for every CTA's arrival at the grid barrier; false when it
+// Warp-wide wait for every CTA's arrival at a grid barrier; false when it
 // ran out or another role of the CTA gave up.
-__device__ __forceinline__ bool grid_wait(const DecFfnArgs& p, uint32_t G, int& abort_flag, int lane) {
+__device__ __forceinline__ bool grid_wait(const DecFfnArgs& p, int which, uint32_t G, int& abort_flag, int lane) {
   volatile int* abort = &abort_flag;
   int got = 1;
   if (lane == 0) {
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1; ld_acquire(p.barrier) < G; ++it) {
+    for (uint32_t it = 1; ld_acquire(p.barrier + which) < G; ++it) {
       if ((it & 63u) == 0) {
         if (*abort) {
           got = 0;
@@ -414,7 +362,106 @@ __device__ __forceinline__ bool grid_wait(const DecFfnArgs& p, uint32_t G, int& 
       }
     }
   }
-  return __shfl_sync(0xffffffffu, got, 0) != 0;
+  got = __shfl_sync(0xffffffffu, got, 0);
+  __syncwarp();  // orders the other lanes' reads after lane 0's acquire
+  return got != 0;
+}
+
+// y by the consumer warps of all CTAs, once every CTA's parts of it are there:
+// 128 columns of a token per warp and step, 4 per lane, its experts summed in slot
+// order, their rows whole from yfull or, where CTAs share the item, from their
+// tiles in order (the first one's slot 1, the later ones' slot 0).
+__device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, uint32_t G, int gw,
+                                        int warps, int lane) {
+  const int N = p.N2;
+  const size_t tile = (size_t)p.row_cap * kDecBN;
+  const int tasks = p.T * p.nb2;
+  bool waited = false;
+#pragma unroll 1
+  for (int task = gw; task < tasks; task += warps) {
+    const int tok = task / p.nb2, nb = task % p.nb2;
+    const int col = nb * kDecBN + lane * 4;  // N is a multiple of 8: all 4 columns or none
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.k; j0 += 4) {  // 4 experts' loads in flight together
+      const float* src[4];
+      int more[4];
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = j0 + u < p.k ? c.slot[tok * p.k + j0 + u] : -1;
+        more[u] = 0;
+        src[u] = nullptr;
+        if (row >= 0) {
+          const int ei = c.row_entry[row];
+          const uint32_t i0 = ((uint32_t)nb * c.n_entries + ei) * p.kc2;
+          const int o0 = sp.owner(i0);
+          more[u] = sp.owner(i0 + p.kc2 - 1) - o0;
+          src[u] = more[u] == 0 ? p.yfull + (size_t)row * N + col
+                                : p.parts2 + (size_t)(o0 * 2 + 1) * tile + (row - c.ent[ei].row0) * kDecBN + lane * 4;
+        }
+      }
+      if (!waited) {
+        grid_wait(p, kGridY, G, c.abort_flag, lane);
+        waited = true;
+      }
+      if (col < N) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          v[u] = src[u] ? __ldcg(reinterpret_cast<const float4*>(src[u])) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll 4
+          for (int o = 1; o <= more[u]; ++o)
+            add4(v[u], __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * o - 1) * tile)));
+          if (src[u]) {
+            const float w = c.gate[tok * p.k + j0 + u];
+            y.x = fmaf(w, v[u].x, y.x);
+            y.y = fmaf(w, v[u].y, y.y);
+            y.z = fmaf(w, v[u].z, y.z);
+            y.w = fmaf(w, v[u].w, y.w);
+          }
+        }
+      }
+    }
+    if (col < N)
+      *reinterpret_cast<uint2*>(p.y + (size_t)tok * N + col) =
+          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  }
+}
+
+// All shared items of the first product by the consumer warps of all CTAs, once
+// every CTA's tiles are there: a row of an item per warp and step.
+__device__ __forceinline__ void finish_all(const DecFfnArgs& p, Ctrl& c, const Split& sp, int gw, int warps,
+                                           int lane) {
+  const bool swiglu = p.act == kDecSwiGLU;
+  const size_t tile = (size_t)p.row_cap * kDecBN;
+  const int KCN = p.kc1, rows = c.max_rows;
+  const int tasks = ((int)sp.G - 1) * rows;  // an item belongs to the first border of CTAs inside it
+#pragma unroll 1
+  for (int task = gw; task < tasks; task += warps) {
+    const uint32_t b = (uint32_t)(task / rows) + 1;
+    const int r = task % rows;
+    const uint32_t x = sp.start(b);
+    const int item = (int)(x / KCN);
+    const uint32_t i0 = (uint32_t)item * KCN;
+    if (x == i0 || sp.owner(i0) != (int)b - 1) continue;
+    const DecEntry en = c.ent[item / p.nb1];
+    if (r >= en.n) continue;
+    const int more = sp.owner(i0 + KCN - 1) - ((int)b - 1);
+    const int col = (item % p.nb1) * (swiglu ? 64 : kDecBN) + lane * 4;
+    if (col >= p.N1 || (swiglu && lane >= 16)) continue;
+    const float* s = p.parts + (size_t)((b - 1) * 2 + 1) * tile + r * kDecBN + lane * 4;
+    float4 z = __ldcg(reinterpret_cast<const float4*>(s));
+    float4 u = swiglu ? __ldcg(reinterpret_cast<const float4*>(s + 64)) : z;
+#pragma unroll 4
+    for (int o = 1; o <= more; ++o) {
+      const float* q = s + (size_t)(2 * o - 1) * tile;
+      add4(z, __ldcg(reinterpret_cast<const float4*>(q)));
+      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(q + 64)));
+    }
+    write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, z, u);
+  }
 }
 
 template <int V>
@@ -598,7 +645,9 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
   // fit beside the rows' chunks and, where it is small, this CTA's part of h
   const int max_rows = c.max_rows;
   const int row_bytes = max_rows * C::PITCH;
-  const uint32_t cpc = ((uint32_t)n_ent * p.nb2 * p.kc2 + G - 1) / G;  // second product's chunks, at most
+  // the second product's chunks of a CTA, at most
+  const Split s2((uint32_t)n_ent * p.nb2 * p.kc2, G, p.least2);
+  const uint32_t cpc = (s2.total + s2.G - 1) / s2.G;
   const bool reader = layer && cpc * (uint32_t)row_bytes <= (uint32_t)DF_CACHE;
   int S = DF_MAX_STAGES / KG * KG;
   for (; S > KG; S -= KG) {
@@ -625,7 +674,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       bool ok = true;
       for (int ph = 0; ph < phases && ok; ++ph) {
         const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
-        const Split sp((uint32_t)n_ent * NB * KCN, G);
+        const Split sp((uint32_t)n_ent * NB * KCN, G, ph ? p.least2 : p.least1);
         const CUtensorMap* mw = ph ? &maps.w2 : &maps.w1;
         const bool blocked = ph ? p.blocked2 : p.blocked1;
         uint32_t x = sp.start(cta);
@@ -694,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
       const int K = ph ? p.K2 : p.K1;
       const uint16_t* src = ph ? p.h : p.x;
-      const Split sp((uint32_t)n_ent * NB * KCN, G);
+      const Split sp((uint32_t)n_ent * NB * KCN, G, ph ? p.least2 : p.least1);
       uint32_t x = sp.start(cta);
       const uint32_t end = sp.start(cta + 1);
       const bool copies = ph == 0 || !reader;
@@ -702,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const int N = ph ? p.N2 : p.N1;
       const bool sg = ph == 0 && swiglu;
       const int ncols = sg ? 2 * N : N;  // columns of W
-      if (ph == 1 && copies && x < end) ok = grid_wait(p, G, c.abort_flag, lane);
+      if (ph == 1 && copies && x < end) ok = grid_wait(p, kGridH, G, c.abort_flag, lane);
       while (x < end && ok) {
         const int item = (int)(x / KCN);
         const int k0 = (int)(x - (uint32_t)item * KCN);
@@ -819,7 +868,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     for (int ph = 0; ph < phases; ++ph) {
       const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
       const int N = ph ? p.N2 : p.N1;
-      const Split sp((uint32_t)n_ent * NB * KCN, G);
+      const Split sp((uint32_t)n_ent * NB * KCN, G, ph ? p.least2 : p.least1);
       uint32_t x = sp.start(cta);
       const uint32_t end = sp.start(cta + 1);
       const bool cached = ph == 1 && reader;
@@ -831,7 +880,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         // are in flight together.
         constexpr int UN = 3;
         q2 = qi;
-        const Split s1((uint32_t)n_ent * p.nb1 * p.kc1, G);
+        const Split s1((uint32_t)n_ent * p.nb1 * p.kc1, G, p.least1);
         const int total = (int)(end - x) * max_rows * PCS;
         const size_t tile = (size_t)p.row_cap * kDecBN;
         for (int i0 = ctid; i0 < total || i0 == ctid; i0 += UN * CTHREADS) {
@@ -867,7 +916,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
           }
           if (i0 == ctid) {
-            grid_wait(p, G, c.abort_flag, lane);
+            grid_wait(p, kGridH, G, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
           }
           float4 z[UN][2], g2[UN][2];
@@ -1014,16 +1063,22 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 
       }
 
-      // ---- every group has written its items: what they share with other
-      // CTAs is counted in and, by whoever comes last, put together, by all
-      // consumer threads (more loads in flight, and the multiplying loop's
-      // registers are free: a spill costs this kernel a trip to memory behind
-      // the weights, as shared memory leaves no L1 to speak of)
+      // ---- every group has written its items: now what they share with other
+      // CTAs, by all consumer threads (more loads in flight, and the multiplying
+      // loop's registers are free: a spill costs this kernel a trip to memory
+      // behind the weights, as shared memory leaves no L1 to speak of)
       named_sync(BAR_CONS, CTHREADS);
-      const uint32_t begin = sp.start(cta);
+      const int gw = cw * (int)G + cta, warps = C::CONSUMERS * (int)G;
       if (ph == 0) {
-        if (!reader) {
-          // shared items are at most the CTA's first and last
+        if (!reader && NT >= 4) {
+          // many rows: by all CTAs, after a grid barrier
+          if (ctid == 0) red_release(p.barrier + kGridTiles, 1u);
+          grid_wait(p, kGridTiles, G, c.abort_flag, lane);
+          finish_all(p, c, sp, gw, warps, lane);
+        } else if (!reader) {
+          // few rows: an item (at most the CTA's first and its last) by the
+          // CTA that comes last to it
+          const uint32_t begin = sp.start(cta);
           const int first = begin < end && begin % KCN != 0 ? (int)(begin / KCN) : -1;
           const int last = begin < end && end % KCN != 0 && (int)(end / KCN) != first ? (int)(end / KCN) : -1;
           if (ctid < 2) {
@@ -1050,26 +1105,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             finish_items<CTHREADS>(p, f, ctid);
           }
         }
-        if (layer) {  // this CTA's h is there: the grid barrier
+        if (layer) {  // this CTA's h is there
           if (!reader) named_sync(BAR_CONS, CTHREADS);
-          if (ctid == 0) red_release(p.barrier, 1u);
+          if (ctid == 0) red_release(p.barrier + kGridH, 1u);
         }
-      } else if (begin < end) {
-        // column blocks, up to DF_BLOCKS at a time
-        const uint32_t per = (uint32_t)n_ent * KCN;  // chunks of a block
-        const int nb0 = (int)(begin / per), nb1 = (int)((end - 1) / per);
-        for (int b = nb0; b <= nb1; b += DF_BLOCKS) {
-          const int n = min(DF_BLOCKS, nb1 + 1 - b);
-          if (ctid < n) {
-            const uint32_t i0 = (uint32_t)(b + ctid) * per;
-            const int parts = sp.owner(i0 + per - 1) - sp.owner(i0) + 1;
-            c.block_last[ctid] = atom_acq_rel(p.col_tickets + b + ctid) == (unsigned)(parts - 1);
-          }
-          named_sync(BAR_CONS, CTHREADS);
-          for (int i = 0; i < n; ++i)
-            if (c.block_last[i]) combine_block<CTHREADS>(p, c, sp, b + i, ctid);
-          named_sync(BAR_CONS, CTHREADS);
-        }
+      } else {
+        if (ctid == 0) red_release(p.barrier + kGridY, 1u);
+        combine(p, c, sp, G, gw, warps, lane);
       }
     }
   }

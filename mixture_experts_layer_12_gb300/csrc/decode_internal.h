@@ -23,11 +23,11 @@ constexpr int kDecMaxCtas = 152;           // CTAs of the streaming kernel
 constexpr int kDecMaxEntries = kMaxExperts + MOED_MAX_ROWS / 8;
 
 // Control block at the start of a workspace, cleared by the first kernel of
-// every call.  bytes: [status 64 | barrier 64 | item tickets | n_entries].
+// every call.  bytes: [status 64 | grid barriers 64 | item tickets | n_entries].
 constexpr size_t kDecBarrierOffset = 64;
 constexpr size_t kDecTicketOffset = 128;    // kDecMaxCtas ints (<= 152 * 4 = 608 bytes)
 constexpr size_t kDecCountOffset = 960;     // number of entries, rows of the longest
-constexpr size_t kDecEntryOffset = 1024;    // entries, then the column tickets
+constexpr size_t kDecEntryOffset = 1024;    // entries
 constexpr int kDecCtrlInts = 240;           // ints zeroed: everything before n_entries
 
 // ---- kernel 1 of the layer: routing and dispatch by one cluster of 8 CTAs
@@ -46,8 +46,6 @@ struct DecRouteArgs {
   int32_t* slot;
   int* ctrl;           // control block
   DecEntry* entries;
-  int* col_tickets;    // [n_col_tickets], zeroed here
-  int n_col_tickets;
   int row_block;       // rows of an entry at most
 };
 cudaError_t launch_decode_route(const DecRouteArgs& a, cudaStream_t st);
@@ -71,9 +69,8 @@ struct DecFfnArgs {
   const int* ctrl;
   const DecEntry* entries;
   int max_entries;       // host bound on the number of entries
-  unsigned* barrier;
+  unsigned* barrier;     // 3 grid barriers
   unsigned* item_tickets;
-  unsigned* col_tickets;
   float* parts;          // [CTAs][2][row_cap][128] partial tiles of the first product's split items
   float* parts2;         // the second product's: the first's are still being read
   int row_cap;           // rows of an entry at most, rounded up to 8
@@ -92,6 +89,7 @@ struct DecFfnArgs {
   int group;             // 4-bit: rows per scale; 0: bf16
   int K1, N1;            // first product: x [., K1] -> N1 columns of h (or y)
   int nb1, kc1;          // its column blocks and K chunks
+  int least1, least2;    // chunks worth a CTA of their own
   int K2, N2, nb2, kc2;  // second product (layer)
   int* status;
   uint64_t wait_limit_ns;

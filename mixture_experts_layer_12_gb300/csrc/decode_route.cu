@@ -133,13 +133,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   pdl_wait();
 
   // the counters of the second kernel
-  for (int i = rank * DR_THREADS + tid; i < kDecCtrlInts + a.n_col_tickets;
-       i += DR_RANKS * DR_THREADS) {
-    if (i < kDecCtrlInts)
-      a.ctrl[i] = 0;
-    else
-      a.col_tickets[i - kDecCtrlInts] = 0;
-  }
+  if (rank == 0 && tid < kDecCtrlInts) a.ctrl[tid] = 0;
 
   // ---- partial logits of rows [h0, h1) of H
   const int h0 = min(rank * L.hs, H), h1 = min(h0 + L.hs, H);
