@@ -32,8 +32,7 @@ constexpr int DR_THREADS = 256;
 constexpr int DR_WARPS = DR_THREADS / 32;
 constexpr int DR_RANKS = 8;
 constexpr int DR_MAX_ASSIGN = MOED_MAX_TOKENS * kMaxTopK;  // 512
-constexpr int DR_CHUNKS = DR_MAX_ASSIGN / 32;
-constexpr int DR_STAGE_BYTES = 112 * 1024;  // W_router and x rows staged at a time
+constexpr int DR_STAGE_BYTES = 140 * 1024;  // W_router and x rows staged at a time
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -75,13 +74,17 @@ struct RouteLayout {
   size_t stage, part, total;
 };
 
+// Row pitches of the staged W_router and x: odd multiples of 16 bytes, so that
+// the 8 rows of an ldmatrix fall into different banks.
+__host__ __device__ inline int w_pitch(int E) { return 16 * ((E * 2 + 15) / 16 | 1); }
+__host__ __device__ inline int token_tile(int T) { return T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64; }
+
 __host__ __device__ inline RouteLayout route_layout(int T, int H, int E) {
   RouteLayout L;
   L.ep = (E + 15) / 16 * 16;
-  L.tp = 8;
-  while (L.tp < T) L.tp *= 2;
+  L.tp = token_tile(T);
   L.hs = (H + DR_RANKS * 16 - 1) / (DR_RANKS * 16) * 16;
-  L.pw = L.ep * 2 + 16;
+  L.pw = w_pitch(E);  // (the columns up to ep belong to the next row: of no expert)
   // kb rows of W_router (pw bytes) and of every token (2 kb + 16 bytes)
   int kb = (DR_STAGE_BYTES - 16 * L.tp) / (L.pw + 2 * L.tp) / 16 * 16;
   if (kb > L.hs) kb = L.hs;
@@ -95,6 +98,8 @@ __host__ __device__ inline RouteLayout route_layout(int T, int H, int E) {
   // partial logits of the tokens a rank owns, from all ranks
   const size_t own = T <= DR_RANKS ? (size_t)L.tp : (size_t)(T + DR_RANKS - 1) / DR_RANKS;
   L.stage = tiles > red ? tiles : red;
+  const size_t wc = T * 8 > 32 ? (size_t)(T * 8 + 31) / 32 * kMaxExperts * 4 : 0;  // the dispatch's counts
+  if (L.stage < wc) L.stage = wc;
   L.stage = (L.stage + 127) / 128 * 128;
   L.part = DR_RANKS * own * L.ep * 4;
   L.total = L.stage + L.part;
@@ -113,10 +118,10 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
     decode_route_kernel(const DecRouteArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_ids[DR_MAX_ASSIGN];
-  __shared__ int s_wc[DR_CHUNKS][kMaxExperts];
   __shared__ int s_off[kMaxExperts + 1];
   __shared__ int s_scan[2][DR_WARPS];
   __shared__ float s_log[DR_WARPS][kMaxExperts];
+  __shared__ float s_bias[kMaxExperts];
   __shared__ uint32_t s_key[DR_WARPS][kMaxExperts];
 
   const int tid = threadIdx.x;
@@ -129,11 +134,13 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   uint8_t* sX = smem + (size_t)L.kb * L.pw;
   float* sRed = reinterpret_cast<float*>(smem);
   float* sPart = reinterpret_cast<float*>(smem + L.stage);
+  int* s_wc = reinterpret_cast<int*>(smem);  // dispatch: [chunk][expert], over the stage
   pdl_launch_dependents();
   pdl_wait();
 
   // the counters of the second kernel
   if (rank == 0 && tid < kDecCtrlInts) a.ctrl[tid] = 0;
+  if (tid < E) s_bias[tid] = a.bias ? __ldg(a.bias + tid) : 0.f;  // read behind the barriers below
 
   // ---- partial logits of rows [h0, h1) of H
   const int h0 = min(rank * L.hs, H), h1 = min(h0 + L.hs, H);
@@ -172,8 +179,8 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
       cp_async16(smem_u32(sX + (size_t)t * L.px + c * 16), a.x + (size_t)t * H + hb + c * 8);
     }
     if (rows16 != rows) {  // zero the half step past the end in both operands
-      for (int i = tid; i < 8 * (L.ep / 8); i += DR_THREADS) {
-        const int r = rows + i / (L.ep / 8), c = i % (L.ep / 8);
+      for (int i = tid; i < 8 * (L.pw / 16); i += DR_THREADS) {
+        const int r = rows + i / (L.pw / 16), c = i % (L.pw / 16);
         *reinterpret_cast<uint4*>(sW + (size_t)r * L.pw + c * 16) = make_uint4(0, 0, 0, 0);
       }
       for (int t = tid; t < T; t += DR_THREADS)
@@ -245,7 +252,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
       float v = 0.f;
 #pragma unroll
       for (int r = 0; r < DR_RANKS; ++r) v += sPart[((size_t)r * own + tl) * L.ep + e];
-      if (a.bias) v += __ldg(a.bias + e);
+      if (a.bias) v += s_bias[e];
       if (isnan(v)) v = -INFINITY;
       lg[e] = v;
       key[e] = order_key(v);
@@ -308,8 +315,55 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
 
   // ---- dispatch of all T*k assignments, in (token, slot) order
   const int n = T * k;
+  if (n <= 32) {
+    // one assignment per lane, the same in every warp: ranks by match, sums
+    // over the assignments by shuffles, no barrier.  Lane i's `word`: expert,
+    // kept or not, and for the first kept one of an expert its row blocks.
+    const int id = lane < n ? s_ids[lane] : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    const int rank_e = __popc(same & ((1u << lane) - 1u));
+    const bool kept = lane < n && (a.capacity < 0 || rank_e < a.capacity);
+    const unsigned kept_mask = __ballot_sync(0xffffffffu, kept);
+    const int cnt = __popc(same & kept_mask);
+    const int blocks = kept && rank_e == 0 ? (cnt + a.row_block - 1) / a.row_block : 0;
+    const int word = lane < n ? id | (kept ? 256 : 0) | blocks << 16 : 1 << 12;
+    int my_off = 0, e_cnt = 0, e_off = 0, e_blk = 0, e_own = 0, all = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int w = __shfl_sync(0xffffffffu, word, i);
+      const int e = w & 255, on = (w >> 8) & 1, b = w >> 16;
+      my_off += on & (e < id);
+      e_cnt += on & (e == tid);
+      e_off += on & (e < tid);
+      e_blk += e < tid ? b : 0;
+      e_own += e == tid ? b : 0;
+      all += b;
+    }
+    const int total = __popc(kept_mask);
+    if (tid < E) {
+      a.counts[tid] = e_cnt;
+      a.offsets[tid] = e_off;
+      for (int b = 0; b < e_own; ++b)
+        a.entries[e_blk + b] =
+            DecEntry{tid, e_off + b * a.row_block, min(a.row_block, e_cnt - b * a.row_block), 0};
+    }
+    const int longest = __reduce_max_sync(0xffffffffu, min(cnt, a.row_block));
+    if (warp == 0) {
+      if (lane < n) {
+        a.slot[lane] = kept ? my_off + rank_e : -1;
+        if (kept) a.perm[my_off + rank_e] = lane;
+      }
+      if (lane >= total && lane < n) a.perm[lane] = -1;
+      if (lane == 0) {
+        a.offsets[E] = total;
+        a.ctrl[kDecCountOffset / 4] = all;
+        a.ctrl[kDecCountOffset / 4 + 1] = longest;
+      }
+    }
+    return;
+  }
   const int chunks = (n + 31) / 32;
-  for (int i = tid; i < chunks * kMaxExperts; i += DR_THREADS) (&s_wc[0][0])[i] = 0;
+  for (int i = tid; i < chunks * kMaxExperts; i += DR_THREADS) s_wc[i] = 0;
   __syncthreads();
   int my_e[2], below[2];
 #pragma unroll
@@ -323,7 +377,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
       if (e < 0 || e >= E) e = -1;
       const unsigned m = __match_any_sync(0xffffffffu, e);
       below[u] = __popc(m & ((1u << lane) - 1u));
-      if (e >= 0 && below[u] == 0) s_wc[c][e] = __popc(m);
+      if (e >= 0 && below[u] == 0) s_wc[c * kMaxExperts + e] = __popc(m);
       my_e[u] = e;
     }
   }
@@ -332,8 +386,8 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   if (tid < E) {
     int run = 0;
     for (int c = 0; c < chunks; ++c) {
-      const int v = s_wc[c][tid];
-      s_wc[c][tid] = run;
+      const int v = s_wc[c * kMaxExperts + tid];
+      s_wc[c * kMaxExperts + tid] = run;
       run += v;
     }
     kept = a.capacity >= 0 ? min(run, a.capacity) : run;
@@ -381,7 +435,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
     const int i = c * 32 + lane;
     if (c >= chunks || i >= n) continue;
     const int e = my_e[u];
-    const int pos = e >= 0 ? s_wc[c][e] + below[u] : -1;
+    const int pos = e >= 0 ? s_wc[c * kMaxExperts + e] + below[u] : -1;
     if (pos >= 0 && (a.capacity < 0 || pos < a.capacity)) {
       a.slot[i] = s_off[e] + pos;
       a.perm[s_off[e] + pos] = i;
@@ -452,7 +506,7 @@ cudaError_t route_launch(const DecRouteArgs& a, cudaStream_t st) {
 
 template <int NT>
 cudaError_t route_attr() {
-  // stage plus partial logits at the largest shapes: 112 KB + 64 KB
+  // stage plus partial logits at the largest shapes: 140 KB + 64 KB
   return cudaFuncSetAttribute(decode_route_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               DR_STAGE_BYTES + MOED_MAX_TOKENS * kMaxExperts * 4);
 }
