@@ -152,11 +152,15 @@ class Q4Weights:
             raise ValueError(f"groups of {group} rows: 32, 64 or 128 are supported")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
+        self._set(codes, scales, E, K8 * 8, N, group,
+                  codes.get_device() if codes.device == scales.device else -1)
+
+    def _set(self, codes, scales, E, K, N, group, dev):
         self._codes, self._scales = codes, scales
-        self.E, self.K, self.N, self.group = E, K8 * 8, N, group
+        self.E, self.K, self.N, self.group = E, K, N, group
         # what the calls below pass for them
-        self._device = codes.get_device() if codes.device == scales.device else -1
-        self._args = (ctypes.c_void_p(codes.data_ptr()), ctypes.c_void_p(scales.data_ptr()))
+        self._device = dev
+        self._args = (codes.data_ptr(), scales.data_ptr())
 
     # fixed for the object's life: the calls use their addresses
     codes = property(lambda self: self._codes)
@@ -197,14 +201,15 @@ def quantize_q4(w: torch.Tensor, group: int = 128, stream=None) -> Q4Weights:
             return quantize_q4(w, group)
     if w.dim() not in (2, 3):
         raise ValueError(f"w must be [E, K, N] or [K, N], got {tuple(w.shape)}")
-    E, (K, N) = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2:]
+    E, K, N = w.shape if w.dim() == 3 else (1, *w.shape)
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"group = {group}: need 32, 64 or 128, dividing K = {K}")
     dev, raw = _here()
     src = _addr(w, _BF, "w", E * K * N, dev)
     codes = torch.empty((E, K // 8, N), dtype=_I32, device=w.device)
     scales = torch.empty((E, K // group, N), dtype=_BF, device=w.device)
-    q = Q4Weights(codes, scales)
+    q = Q4Weights.__new__(Q4Weights)  # of tensors that need no checks
+    q._set(codes, scales, E, K, N, group, dev)
     _check(_lib().moed_quantize_q4(E, K, N, group, src, *q._args, raw))
     return q
 
