@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
           }
           if (i0 == ctid) {
-            grid_wait(p, kGridH, G, c.abort_flag, lane);
+            if (cw == 0) grid_wait(p, kGridH, G, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
           }
           float4 z[UN][2], g2[UN][2];
