@@ -83,6 +83,7 @@ constexpr int BAR_SETUP = 0;
 constexpr int BAR_CONS = 1;
 constexpr int BAR_FIN = 2;
 constexpr int BAR_ITEM = BAR_FIN + KG;
+constexpr int BAR_ROWS = BAR_ITEM + KG;  // the row loaders
 
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -343,43 +344,39 @@ __device__ __forceinline__ void finish_items(const DecFfnArgs& p, const Finish (
   }
 }
 
-// Warp-wide wait for every CTA's arrival at a grid barrier; false when it
-// ran out or another role of the CTA gave up.
-__device__ __forceinline__ bool grid_wait(const DecFfnArgs& p, int which, uint32_t G, int& abort_flag, int lane) {
+// Warp-wide wait for every CTA's arrival at a grid barrier; gives up when another
+// role of the CTA did, or makes the others give up when it ran out.  One warp of a
+// CTA waits and the others wait for it: 152 polls at a time delay the arrivals and
+// everybody's data less than 1216 (one token's layer of narrow experts 27.5 -> 26.7 us).
+__device__ __forceinline__ void grid_wait(const DecFfnArgs& p, int which, uint32_t G, int& abort_flag, int lane) {
   volatile int* abort = &abort_flag;
-  int got = 1;
   if (lane == 0) {
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1; ld_acquire(p.barrier + which) < G; ++it) {
       if ((it & 63u) == 0) {
-        if (*abort) {
-          got = 0;
-          break;
-        }
+        if (*abort) break;
         if (global_timer_ns() - t0 > p.wait_limit_ns) {
           *abort = 1;
           record_status(p.status, MOE_DEV_TIMEOUT);
-          got = 0;
           break;
         }
       }
     }
   }
-  got = __shfl_sync(0xffffffffu, got, 0);
   __syncwarp();  // orders the other lanes' reads after lane 0's acquire
-  return got != 0;
 }
 
 // y by the consumer warps of all CTAs, once every CTA's parts of it are there:
 // 128 columns of a token per warp and step, 4 per lane, its experts summed in slot
 // order, their rows whole from yfull or, where CTAs share the item, from their
 // tiles in order (the first one's slot 1, the later ones' slot 0).
-__device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, uint32_t G, int gw,
-                                        int warps, int lane) {
+__device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, uint32_t G, int cw,
+                                        int gw, int warps, int threads, int lane) {
   const int N = p.N2;
   const size_t tile = (size_t)p.row_cap * kDecBN;
   const int tasks = p.T * p.nb2;
   bool waited = false;
+  if (gw >= tasks && (int)blockIdx.x < tasks) named_sync(BAR_CONS, threads);  // another warp's wait, below
 #pragma unroll 1
   for (int task = gw; task < tasks; task += warps) {
     const int tok = task / p.nb2, nb = task % p.nb2;
@@ -405,7 +402,8 @@ __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Spli
         }
       }
       if (!waited) {
-        grid_wait(p, kGridY, G, c.abort_flag, lane);
+        if (cw == 0) grid_wait(p, kGridY, G, c.abort_flag, lane);
+        named_sync(BAR_CONS, threads);
         waited = true;
       }
       if (col < N) {
@@ -749,7 +747,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int ph = 0; ph < phases && ok; ++ph) {
+    for (int ph = 0; ph < phases; ++ph) {
       const int NB = ph ? p.nb2 : p.nb1, KCN = ph ? p.kc2 : p.kc1;
       const int K = ph ? p.K2 : p.K1;
       const uint16_t* src = ph ? p.h : p.x;
@@ -761,7 +759,12 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const int N = ph ? p.N2 : p.N1;
       const bool sg = ph == 0 && swiglu;
       const int ncols = sg ? 2 * N : N;  // columns of W
-      if (ph == 1 && copies && x < end) ok = grid_wait(p, kGridH, G, c.abort_flag, lane);
+      if (ph == 1 && copies && x < end) {
+        // a loader that gave up before comes here too
+        if (lw == 0 && ok) grid_wait(p, kGridH, G, c.abort_flag, lane);
+        named_sync(BAR_ROWS, 32 * DF_LOADERS);
+        ok = ok && *const_cast<volatile int*>(&c.abort_flag) == 0;
+      }
       while (x < end && ok) {
         const int item = (int)(x / KCN);
         const int k0 = (int)(x - (uint32_t)item * KCN);
@@ -1083,7 +1086,8 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         if (!reader && NT >= 4) {
           // many rows: by all CTAs, after a grid barrier
           if (ctid == 0) red_release(p.barrier + kGridTiles, 1u);
-          grid_wait(p, kGridTiles, G, c.abort_flag, lane);
+          if (cw == 0) grid_wait(p, kGridTiles, G, c.abort_flag, lane);
+          named_sync(BAR_CONS, CTHREADS);
           finish_all(p, c, sp, gw, warps, lane);
         } else if (!reader) {
           // few rows: an item (at most the CTA's first and its last) by the
@@ -1121,7 +1125,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
       } else {
         if (ctid == 0) red_release(p.barrier + kGridY, 1u);
-        combine(p, c, sp, G, gw, warps, lane);
+        combine(p, c, sp, G, cw, gw, warps, CTHREADS, lane);
       }
     }
   }
