@@ -183,7 +183,7 @@ __device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32
 }
 
 // codes i and i + 4 of a word (rows i and i + 4 of its 8) as a bf16 pair
-// (c - 8) / 64, exactly (the scale is multiplied by 64).  A code at bits 0-3
+// (c - 8) / 64, exactly (an item's sums are multiplied by 64 at its end).  A code at bits 0-3
 // or 4-7 of a half word is, read as bf16, c or 16 c times 2^-133 (the numbers
 // below 2^-125 are evenly spaced), so one masked word and one fused
 // multiply-add make a pair, and a word needs one shift: 9 instructions for 8
@@ -510,10 +510,10 @@ __device__ __forceinline__ void chunk_q4(float (&acc)[2][NT][4], uint32_t w0, co
       if (GRP < 128 ? step % (GRP / 32) == 0 : first && i == 0) {
         uint32_t s01, s23;
         lds64(sl + (blk * 64 + i * 32) / GRP * 256, s01, s23);
-        s[0] = 64.f * bf16_lo(s01);
-        s[1] = 64.f * bf16_hi(s01);
-        s[2] = 64.f * bf16_lo(s23);
-        s[3] = 64.f * bf16_hi(s23);
+        s[0] = bf16_lo(s01);
+        s[1] = bf16_hi(s01);
+        s[2] = bf16_lo(s23);
+        s[3] = bf16_hi(s23);
       }
       uint32_t v[4];  // columns 4g .. 4g + 3 of 8 rows of K
       lds128(w0 + blk * 1024 + wofs[i], v);
@@ -1014,6 +1014,14 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
         qi += (uint32_t)(k1 - k0);
         x += (uint32_t)(k1 - k0);
+        if constexpr (Q4) {  // the codes were taken as (c - 8) / 64
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[m][n][r] *= 64.f;
+        }
 
         // ---- the groups in turn sum both parts and write the item out; the
         // other hands over and goes on.  It hands over again only after an item

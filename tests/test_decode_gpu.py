@@ -324,6 +324,20 @@ def test_matvec_nan_scale_and_inf_rows():
     assert torch.equal(y[[0, 2]][:, cols], clean[[0, 2]][:, cols])
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_matvec_largest_and_smallest_scales(group):
+    """Scales near the ends of bf16's range, with rows that bring the result
+    back inside: nothing on the way overflows or vanishes."""
+    g = gen(34)
+    for scale, xs in ((2.0 ** 125, 2.0 ** -60), (2.0 ** -118, 2.0 ** 60)):
+        w = random_q4(g, 1, 384, 72, group)
+        w.scales.copy_((w.scales.double().sign() * scale).bfloat16())
+        x = (randn(g, 5, 384).double() * xs).bfloat16().to(DEV)
+        y = moe.matvec_q4(x, w)
+        assert torch.isfinite(y).all() and (y != 0).any()
+        check_matvec(x, w, group, [0, 5], y)
+
+
 def test_matvec_past_32_bit_offsets():
     E, K, N = 150, 4096, 4096                        # 2.5e9 weights
     codes = torch.full((E, K // 8, N), -1, dtype=torch.int32, device=DEV)
