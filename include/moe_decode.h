@@ -54,7 +54,8 @@ MOE_API size_t moed_workspace_size(const moe_shape* s);
  * bf16.  The result does not depend on how the work is split over the SMs'
  * timing: the same inputs give the same bits.
  * Calls on different streams may overlap if they share no workspace and no
- * output.  T = 0 clears counts / offsets, as moe_forward does.
+ * output; host threads that call on one stream with one workspace have to
+ * take turns (a call enqueues two kernels).  y may be x.  T = 0 clears counts / offsets, as moe_forward does.
  */
 MOE_API int moed_forward(const moe_shape* s, const uint16_t* x, const uint16_t* w_router,
                          const float* b_router, const uint16_t* w1, const uint16_t* w2,
@@ -85,8 +86,8 @@ MOE_API size_t moed_matvec_q4_workspace_size(int32_t rows, int32_t n_segments, i
  *   x [rows, K] bf16, codes [E, K/8, N], scales [E, K/group, N],
  *   seg_offsets [n_segments+1] int32 (device, non-decreasing, at most rows;
  *   clamped to [0, rows], never followed out of range) or NULL with
- *   n_segments = 1: all rows, 1 <= n_segments <= 256, y [rows, N] bf16; rows
- *   of y outside every segment are not written.
+ *   n_segments = 1: all rows, 1 <= n_segments <= 256, y [rows, N] bf16, which
+ *   must not overlap x; rows of y outside every segment are not written.
  * rows = 0 enqueues nothing but the status clear.
  */
 MOE_API int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,

@@ -356,6 +356,9 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
     REQUIRE_PTR(scales);
     if (seg_offsets || n_segments != 1) REQUIRE_PTR(seg_offsets);  // null: one segment, all rows
     REQUIRE_PTR(y);
+    // rows of y are finished while others of x are still being read
+    if (x < y + (size_t)rows * N && y < x + (size_t)rows * K)
+      return fail(MOE_ERR_INVALID_ARG, "y overlaps x");
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int sms = 0;

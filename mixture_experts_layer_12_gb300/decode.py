@@ -152,7 +152,8 @@ class Q4Weights:
             raise ValueError(f"groups of {group} rows: 32, 64 or 128 are supported")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        self._set(codes, scales, E, K8 * 8, N, group,
+        # aliases, so that the memory stays even if the caller's tensors get other data
+        self._set(codes.detach(), scales.detach(), E, K8 * 8, N, group,
                   codes.get_device() if codes.device == scales.device else -1)
 
     def _set(self, codes, scales, E, K, N, group, dev):
@@ -161,6 +162,9 @@ class Q4Weights:
         # what the calls below pass for them
         self._device = dev
         self._args = (codes.data_ptr(), scales.data_ptr())
+
+    def __reduce__(self):  # a copy has addresses of its own
+        return Q4Weights, (self._codes, self._scales)
 
     # fixed for the object's life: the calls use their addresses
     codes = property(lambda self: self._codes)
@@ -229,10 +233,12 @@ def dequantize_q4(w: Q4Weights, out: torch.Tensor | None = None, stream=None) ->
 
 
 # Workspaces of matvec_q4: one per stream, grown as needed.  Calls on one
-# stream run one after the other and may share it; a call that is captured
-# into a CUDA graph gets its own.
+# stream run one after the other and may share it, if the two kernels of a call
+# are enqueued together (the lock); a call that is captured into a CUDA graph
+# gets its own.
 _matvec_bytes: dict = {}
 _matvec_ws: dict = {}
+_enqueue = threading.Lock()
 
 
 def _matvec_workspace(rows: int, n_segments: int, K: int, N: int, dev: int, raw: int) -> torch.Tensor:
@@ -271,23 +277,26 @@ def matvec_q4(x: torch.Tensor, w: Q4Weights, seg_offsets: torch.Tensor | None = 
         seg = _addr(seg_offsets, _I32, "seg_offsets", n_segments + 1, dev)
     q = _q4_here(w, dev)
     src = _addr(x, _BF, "x", rows * K, dev)
-    ws = _matvec_workspace(rows, n_segments, K, N, dev, raw)
     if out is None:
         out = torch.empty((rows, N), dtype=_BF, device=x.device)
     dst = _addr(out, _BF, "out", rows * N, dev)
-    _check(_lib().moed_matvec_q4(rows, K, N, E, w.group, n_segments, src, *q, seg, dst, ws.data_ptr(),
-                                 ws.numel(), raw))
+    with _enqueue:
+        ws = _matvec_workspace(rows, n_segments, K, N, dev, raw)
+        rc = _lib().moed_matvec_q4(rows, K, N, E, w.group, n_segments, src, *q, seg, dst, ws.data_ptr(),
+                                   ws.numel(), raw)
+    _check(rc)
     return out
 
 
 class _Buffers:
-    """Routing outputs and workspace of the calls with T tokens on one stream,
-    and the call's arguments that stay the same."""
+    """Routing outputs of the calls with T tokens on one stream, their workspace
+    (`ws`, or a new one) and the call's arguments that stay the same."""
 
-    def __init__(self, layer, T: int, stream: int):
+    def __init__(self, layer, T: int, stream: int, ws: torch.Tensor | None):
         shape = layer._shape(T)
         dev = layer.w_router.device
-        self.ws = torch.empty(moed_workspace_size(shape), dtype=torch.uint8, device=dev)
+        need = moed_workspace_size(shape)
+        self.ws = ws if ws is not None and ws.numel() >= need else torch.empty(need, dtype=torch.uint8, device=dev)
         n, i32 = T * layer.k, dict(dtype=_I32, device=dev)
         self.routing = r = RoutingBuffers(
             ids=torch.empty(T, layer.k, **i32), weights=torch.empty(T, layer.k, dtype=_F32, device=dev),
@@ -307,9 +316,10 @@ class MoEDecodeLayer:
     stream (or `stream`) and returns a new y [T, H].
 
     ``routing`` and ``ws`` are those of the last call; the next call with as
-    many tokens on the same stream writes them again.  Calls on different
-    streams have buffers of their own, and so has every call that is captured
-    into a CUDA graph, so they may overlap."""
+    many tokens on the same stream writes the routing again, and the next call
+    on the same stream the workspace.  Calls on different streams have buffers
+    of their own, and so has every call that is captured into a CUDA graph, so
+    they may overlap."""
 
     def __init__(self, w_router, w1, w2, k: int, bias=None, capacity_factor=None,
                  gating: int = MOE_GATE_TOPK_SOFTMAX, act: str = "gelu"):
@@ -338,16 +348,23 @@ class MoEDecodeLayer:
             check_tensor(t, dt, name, 0, dev)
         if bias is not None:
             check_tensor(bias, _F32, "bias", self.E, dev)
-        self._w_router, self._w1, self._w2, self._bias = w_router, w1, w2, bias
+        # aliases, so that the memory stays even if the caller's tensors get other data
+        self._w_router, self._bias = w_router.detach(), None if bias is None else bias.detach()
+        self._w1, self._w2 = (w1, w2) if self.q4 else (w1.detach(), w2.detach())
         self._device, self._index = w_router.device, dev
-        self._held = weights  # the tensors behind the pointers below
         self._ptrs = (ctypes.c_void_p(w_router.data_ptr()),
                       ctypes.c_void_p(None if bias is None else bias.data_ptr()),
                       *(ctypes.c_void_p(t.data_ptr()) for t in weights))
         self._shape(1)
         self._fn = _lib().moed_forward_q4 if self.q4 else _lib().moed_forward
-        self._buffers = {}
+        self._buffers = {}   # (T, stream) -> _Buffers
+        self._streams = {}   # stream -> its workspace, as large as any T needed so far
+        self._lock = threading.Lock()  # a call's two kernels are enqueued together
         self._last = None
+
+    def __reduce__(self):  # a copy has addresses and buffers of its own
+        return MoEDecodeLayer, (self._w_router, self._w1, self._w2, self.k, self._bias, self.capacity_factor,
+                                self.gating, self.act)
 
     # fixed for the layer's life: the calls use their addresses
     w_router = property(lambda self: self._w_router)
@@ -371,16 +388,24 @@ class MoEDecodeLayer:
             raise ValueError(f"the layer's weights are on {self._device}, the current device is cuda:{dev}")
         T = x.shape[0]
         src = _addr(x, _BF, "x", T * self.H, dev)
-        capturing = torch.cuda.is_current_stream_capturing()
-        b = None if capturing else self._buffers.get((T, raw))
-        if b is None:
-            b = _Buffers(self, T, raw)
-            if not capturing:
-                self._buffers[T, raw] = b
         y = torch.empty((T, self.H), dtype=_BF, device=self._device)
-        _check(self._fn(*b.head, src, *self._ptrs, y.data_ptr(), *b.tail))
-        self._last = b
+        capturing = torch.cuda.is_current_stream_capturing()
+        with self._lock:
+            b = _Buffers(self, T, raw, None) if capturing else self._buffers.get((T, raw)) or self._new(T, raw)
+            rc = self._fn(*b.head, src, *self._ptrs, y.data_ptr(), *b.tail)
+            self._last = b
+        _check(rc)
         return y
+
+    def _new(self, T: int, raw: int) -> _Buffers:
+        """Buffers of a first call with T tokens on a stream."""
+        b = _Buffers(self, T, raw, self._streams.get(raw))
+        if b.ws is not self._streams.get(raw):  # the smaller one goes
+            for key in [key for key in self._buffers if key[1] == raw]:
+                del self._buffers[key]
+            self._streams[raw] = b.ws
+        self._buffers[T, raw] = b
+        return b
 
     @property
     def ws(self) -> torch.Tensor:

@@ -2,8 +2,10 @@
 symbols, what the calls refuse (all before the library touches CUDA), the
 workspace sizes, the 4-bit layout's shape rules, and the reference the GPU
 tests use, against brute force."""
+import copy
 import ctypes
 import os
+import pickle
 import re
 
 import pytest
@@ -117,6 +119,23 @@ def test_matvec_refuses_null_misaligned_and_small_buffers(lib):
             args[i] = bad
             assert lib.moed_matvec_q4(3, 128, 64, 4, 64, 4, *args, need, None) == moe.MOE_ERR_INVALID_ARG
     assert lib.moed_matvec_q4(3, 128, 64, 4, 64, 4, *good, need - 1, None) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_matvec_refuses_a_y_that_overlaps_x(lib):
+    P = ctypes.c_void_p
+    need = lib.moed_matvec_q4_workspace_size(3, 1, 128, 64)
+    x, nx, ny = 0x10000, 3 * 128 * 2, 3 * 64 * 2
+    for y in (x, x + nx - 16, x - ny + 16):
+        rc = lib.moed_matvec_q4(3, 128, 64, 1, 64, 1, P(x), P(0x1000), P(0x2000), None, P(y), P(0x3000), need, None)
+        assert rc == moe.MOE_ERR_INVALID_ARG and b"overlaps" in lib.moe_last_error_string()
+
+
+def test_a_copied_q4weights_has_addresses_of_its_own():
+    w = moe.Q4Weights(torch.zeros(2, 16, 8, dtype=torch.int32), torch.ones(2, 4, 8, dtype=torch.bfloat16))
+    for c in (copy.deepcopy(w), pickle.loads(pickle.dumps(w))):
+        assert c._args == (c.codes.data_ptr(), c.scales.data_ptr())
+        assert not set(c._args) & set(w._args)
+        assert (c.E, c.K, c.N, c.group) == (2, 128, 8, 32) and torch.equal(c.scales, w.scales)
 
 
 def test_conversions_refuse(lib):

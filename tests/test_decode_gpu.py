@@ -1,7 +1,9 @@
 """The decode operators on the GPU against their definition in 64 bits
 (tests/decode_reference.py, whose bounds count roundings), at the sizes where
 they can go wrong, and a run of them together."""
+import copy
 import math
+import threading
 
 import pytest
 import torch
@@ -478,6 +480,62 @@ def test_results_of_earlier_calls_stay():
     keep = y1.clone()
     layer(torch.randn_like(x))
     assert torch.equal(y1, keep)
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_batches_of_changing_size_share_a_streams_workspace(group):
+    _, layer = make_layer(56, 1, 256, 128, 8, 2, group=group)
+    g = gen(57)
+    for T in (2, 64, 2, 5, 64):
+        check_layer(randn(g, T, 256).to(DEV), layer)
+        if T == 64:
+            large = layer.ws
+    check_layer(randn(g, 1, 256).to(DEV), layer)
+    assert layer.ws is large
+
+
+def test_host_threads_on_one_stream():
+    """Calls of several host threads land on the default stream, each with its
+    two kernels together."""
+    x, layer = make_layer(58, 6, 512, 256, 8, 2)
+    q = random_q4(gen(59), 1, 512, 256, 32)
+    xs = [torch.randn_like(x) for _ in range(4)]
+    wants = [(layer(v).clone(), moe.matvec_q4(v, q).clone()) for v in xs]
+    bad = []
+
+    def work(v, want):
+        for _ in range(50):
+            got = layer(v), moe.matvec_q4(v, q)
+            if not (torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])):
+                bad.append(v)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(xs, wants)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_copies_and_replaced_tensors(group):
+    """A copied layer works on its own memory; a weight whose tensor is given
+    other data stays what it was for the layer."""
+    x, layer = make_layer(60, 3, 256, 128, 4, 2, group=group)
+    want = layer(x).clone()
+    twin = copy.deepcopy(layer)
+    if group:
+        layer.w1.scales.zero_()
+    else:
+        layer.w1.zero_()
+    assert torch.equal(twin(x), want) and not torch.equal(layer(x), want)
+    w = torch.randn(128, 64, device=DEV).to(BF)
+    q = moe.quantize_q4(w, 64)
+    codes, scales = q.codes.clone(), q.scales.clone()
+    held = moe.Q4Weights(codes, scales)
+    codes.data, scales.data = torch.zeros_like(codes), torch.zeros_like(scales)
+    torch.cuda.empty_cache()
+    assert torch.equal(moe.dequantize_q4(held), moe.dequantize_q4(q))
 
 
 def test_wrong_device_types_and_strides_are_refused():
