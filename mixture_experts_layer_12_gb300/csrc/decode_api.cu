@@ -254,7 +254,7 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.entries = ra.entries;
   fa.max_entries = L.max_entries;
   fa.barrier = at<unsigned>(ws, kDecBarrierOffset);
-  fa.item_tickets = at<unsigned>(ws, kDecTicketOffset);
+  fa.item_counts = at<unsigned>(ws, kDecItemOffset);
   fa.parts = at<float>(ws, L.parts);
   fa.row_cap = L.row_cap;
   fa.parts2 = at<float>(ws, L.parts2);
@@ -389,7 +389,7 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   fa.entries = pa.entries;
   fa.max_entries = L.max_entries;
   fa.barrier = at<unsigned>(ws, kDecBarrierOffset);
-  fa.item_tickets = at<unsigned>(ws, kDecTicketOffset);
+  fa.item_counts = at<unsigned>(ws, kDecItemOffset);
   fa.parts = at<float>(ws, L.parts);
   fa.row_cap = L.row_cap;
   fa.s1 = scales;

@@ -16,9 +16,8 @@
 //     contiguous ranges, one CTA per SM.  Every SM reads the same number of
 //     bytes whatever the shape, and at most its first and last item are
 //     shared with other CTAs.  A CTA's sum of a shared item goes to a partial
-//     tile in the workspace; the CTA that finishes the item last (a ticket
-//     counter, nobody waits) adds the tiles in CTA order, so the sum has one
-//     order whoever comes last.
+//     tile in the workspace, and the tiles are added in CTA order, so the sum
+//     has one order whoever comes last.
 //   * One warp issues TMA loads of weights into a ring of stages and runs ahead
 //     of everything: while the CTAs meet at the grid barrier between the two
 //     products, the ring already fills with W2.
@@ -40,7 +39,8 @@
 //   bound: one m16n8k16 per 256 weights is a tenth of the tensor rate at 8
 //   rows.
 //   * Between the products h goes through memory.  An item shared by several
-//     CTAs is put together by its last CTA (a ticket); by all CTAs, after a grid
+//     CTAs is put together by its first CTA, whose last it is, while the later
+//     ones begin with it and have counted in by then; by all CTAs, after a grid
 //     barrier, where it has many rows; or, where a CTA's part of the second
 //     product needs little of h, by every CTA for the elements it needs.
 //   * Combine: after a grid barrier all CTAs sum the tokens' experts in slot
@@ -128,13 +128,8 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-// counts in on a ticket: earlier writes of the CTA (a barrier before it) are
-// visible to whoever sees the count, and theirs to this CTA
-__device__ __forceinline__ unsigned atom_acq_rel(unsigned* p) {
-  unsigned v;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
+// counts in: earlier writes of the CTA (a barrier before it) are visible to whoever
+// sees the count
 __device__ __forceinline__ void red_release(unsigned* p, unsigned v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
@@ -219,7 +214,6 @@ struct Ctrl {
   int abort_flag;
   int n_entries;
   int max_rows;
-  int last[2];
   DecEntry ent[kDecMaxEntries];
   uint16_t row_entry[MOED_MAX_ROWS];  // layer: entry of a row
   int16_t tok[MOED_MAX_ROWS];         // row of x of a dispatch row
@@ -291,68 +285,43 @@ __device__ __forceinline__ void write_item(const DecFfnArgs& p, const DecEntry& 
   }
 }
 
-// The shared items of the first product that this CTA came last to (at most
-// two), by all consumer threads: the sums of the tiles of CTAs c0..c1 in that
-// order (the first one's slot 1, the later ones' slot 0), 2 pieces' loads in
-// flight together.
-struct Finish {
-  int row0, n, nb, c0, c1;  // n = 0: nothing
-};
+// A shared item of the first product by its first CTA, all consumer threads: its
+// own sums, from shared memory, and the tiles of the `more` CTAs after it in that
+// order (their slot 0).
 template <int CTHREADS>
-__device__ __forceinline__ void finish_items(const DecFfnArgs& p, const Finish (&f)[2], int ctid) {
+__device__ __forceinline__ void finish_item(const DecFfnArgs& p, const DecEntry& en, int nb, const float* own,
+                                            int cta, int more, int ctid) {
   const bool swiglu = p.act == kDecSwiGLU;
-  const int q = swiglu ? 16 : kDecBN / 4;  // pieces of a row
+  const int sh = swiglu ? 4 : 5;  // pieces of a row: 64 or 128 columns
   const size_t tile = (size_t)p.row_cap * kDecBN;
-  constexpr int UN = 2;
-  const int total0 = f[0].n * q, total = total0 + f[1].n * q;
 #pragma unroll 1
-  for (int i0 = ctid; i0 < total; i0 += UN * CTHREADS) {
-    float4 z[UN], u[UN];
-    const float* src[UN];
-    int more[UN];
-    size_t at[UN];
-#pragma unroll
-    for (int v = 0; v < UN; ++v) {
-      const int i = i0 + v * CTHREADS;
-      more[v] = -1;
-      if (i < total) {
-        const bool second = i >= total0;
-        const int pc = second ? i - total0 : i;
-        const int r = pc / q, cl = (pc % q) * 4;
-        const int c0 = second ? f[1].c0 : f[0].c0;
-        const int col = (second ? f[1].nb : f[0].nb) * q * 4 + cl;
-        if (col < p.N1) {  // N1 is a multiple of 8
-          more[v] = (second ? f[1].c1 : f[0].c1) - c0;
-          at[v] = (size_t)((second ? f[1].row0 : f[0].row0) + r) * p.N1 + col;
-          src[v] = p.parts + (size_t)(c0 * 2 + 1) * tile + r * kDecBN + cl;
-          z[v] = __ldcg(reinterpret_cast<const float4*>(src[v]));
-          u[v] = swiglu ? __ldcg(reinterpret_cast<const float4*>(src[v] + 64)) : z[v];
-        }
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < UN; ++v)
-      if (more[v] >= 0) {
+  for (int i = ctid; i < en.n << sh; i += CTHREADS) {
+    const int r = i >> sh, cl = (i - (r << sh)) * 4;
+    const int col = (nb << (sh + 2)) + cl;
+    if (col >= p.N1) continue;  // N1 is a multiple of 8
+    const int at = r * kDecBN + cl;
+    const float* s = p.parts + (size_t)(cta * 2) * tile + at;
+    float4 z = *reinterpret_cast<const float4*>(own + at);
+    float4 u = swiglu ? *reinterpret_cast<const float4*>(own + at + 64) : z;
 #pragma unroll 4
-        for (int o = 1; o <= more[v]; ++o) {
-          const float* s = src[v] + (size_t)(2 * o - 1) * tile;
-          add4(z[v], __ldcg(reinterpret_cast<const float4*>(s)));
-          if (swiglu) add4(u[v], __ldcg(reinterpret_cast<const float4*>(s + 64)));
-        }
-        write_piece(p, at[v], z[v], u[v]);
-      }
+    for (int o = 1; o <= more; ++o) {
+      add4(z, __ldcg(reinterpret_cast<const float4*>(s + (size_t)(2 * o) * tile)));
+      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(s + (size_t)(2 * o) * tile + 64)));
+    }
+    write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, z, u);
   }
 }
 
-// Warp-wide wait for every CTA's arrival at a grid barrier; gives up when another
+// Warp-wide wait until a counter in memory has reached `value`; gives up when another
 // role of the CTA did, or makes the others give up when it ran out.  One warp of a
 // CTA waits and the others wait for it: 152 polls at a time delay the arrivals and
 // everybody's data less than 1216 (one token's layer of narrow experts 27.5 -> 26.7 us).
-__device__ __forceinline__ void grid_wait(const DecFfnArgs& p, int which, uint32_t G, int& abort_flag, int lane) {
+__device__ __forceinline__ void count_wait(const DecFfnArgs& p, const unsigned* at, uint32_t value, int& abort_flag,
+                                           int lane) {
   volatile int* abort = &abort_flag;
   if (lane == 0) {
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1; ld_acquire(p.barrier + which) < G; ++it) {
+    for (uint32_t it = 1; ld_acquire(at) < value; ++it) {
       if ((it & 63u) == 0) {
         if (*abort) break;
         if (global_timer_ns() - t0 > p.wait_limit_ns) {
@@ -402,7 +371,7 @@ __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Spli
         }
       }
       if (!waited) {
-        if (cw == 0) grid_wait(p, kGridY, G, c.abort_flag, lane);
+        if (cw == 0) count_wait(p, p.barrier + kGridY, G, c.abort_flag, lane);
         named_sync(BAR_CONS, threads);
         waited = true;
       }
@@ -761,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const int ncols = sg ? 2 * N : N;  // columns of W
       if (ph == 1 && copies && x < end) {
         // a loader that gave up before comes here too
-        if (lw == 0 && ok) grid_wait(p, kGridH, G, c.abort_flag, lane);
+        if (lw == 0 && ok) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
         named_sync(BAR_ROWS, 32 * DF_LOADERS);
         ok = ok && *const_cast<volatile int*>(&c.abort_flag) == 0;
       }
@@ -929,7 +898,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
           }
           if (i0 == ctid) {
-            if (cw == 0) grid_wait(p, kGridH, G, c.abort_flag, lane);
+            if (cw == 0) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
           }
           float4 z[UN][2], g2[UN][2];
@@ -1064,6 +1033,10 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             for (int r = 0; r < 4; ++r)
               if (row_of(n, r) < en.n) tile_s[row_of(n, r) * kDecBN + col_of(m, r)] = acc[m][n][r];
         named_sync(bar_fin, DF_FIN);
+        // the first product's shared items by their first CTA, where it has no
+        // readers and few rows: its own sums stay here until the loop ends
+        const bool by_first = NT < 4 && ph == 0 && !reader;
+        if (by_first && k0 == 0 && k1 != KCN) continue;
         if (k0 != 0 || k1 != KCN) {
           // a shared item: this CTA's partial tile, slot 0 if the item began in
           // an earlier CTA, else slot 1
@@ -1081,7 +1054,8 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           write_item(p, en, nb, ftid, tile_s);
         }
         named_sync(bar_fin, DF_FIN);  // before this space is handed over again
-
+        if (by_first && k0 != 0 && ftid == 0)
+          red_release(p.item_counts + sp.owner((uint32_t)item * KCN), 1u);
       }
 
       // ---- every group has written its items: now what they share with other
@@ -1094,37 +1068,20 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         if (!reader && NT >= 4) {
           // many rows: by all CTAs, after a grid barrier
           if (ctid == 0) red_release(p.barrier + kGridTiles, 1u);
-          if (cw == 0) grid_wait(p, kGridTiles, G, c.abort_flag, lane);
+          if (cw == 0) count_wait(p, p.barrier + kGridTiles, G, c.abort_flag, lane);
           named_sync(BAR_CONS, CTHREADS);
           finish_all(p, c, sp, gw, warps, lane);
         } else if (!reader) {
-          // few rows: an item (at most the CTA's first and its last) by the
-          // CTA that comes last to it
-          const uint32_t begin = sp.start(cta);
-          const int first = begin < end && begin % KCN != 0 ? (int)(begin / KCN) : -1;
-          const int last = begin < end && end % KCN != 0 && (int)(end / KCN) != first ? (int)(end / KCN) : -1;
-          if (ctid < 2) {
-            const int it = ctid == 0 ? first : last;
-            c.last[ctid] = 0;
-            if (it >= 0) {
-              const uint32_t i0 = (uint32_t)it * KCN;
-              const int c0 = sp.owner(i0), c1 = sp.owner(i0 + KCN - 1);
-              if (atom_acq_rel(p.item_tickets + c0) == (unsigned)(c1 - c0)) c.last[ctid] = 1 + (c0 << 16 | c1);
-            }
-          }
-          named_sync(BAR_CONS, CTHREADS);
-          if (c.last[0] | c.last[1]) {
-            Finish f[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int it = h == 0 ? first : last;
-              f[h] = Finish{0, 0, 0, 0, 0};
-              if (c.last[h]) {
-                const DecEntry en = c.ent[it / NB];
-                f[h] = Finish{en.row0, en.n, it % NB, (c.last[h] - 1) >> 16, (c.last[h] - 1) & 0xFFFF};
-              }
-            }
-            finish_items<CTHREADS>(p, f, ctid);
+          // few rows: the item that goes on in later CTAs, once they have counted
+          // in.  They begin with it, so they have done so long ago.
+          const uint32_t i0 = end / KCN * KCN;
+          if (i0 != end && i0 >= sp.start(cta) && end > sp.start(cta)) {
+            const int more = sp.owner(i0 + KCN - 1) - cta;
+            if (cw == 0) count_wait(p, p.item_counts + cta, (uint32_t)more, c.abort_flag, lane);
+            named_sync(BAR_CONS, CTHREADS);
+            const int it = (int)(end / KCN);
+            finish_item<CTHREADS>(p, c.ent[it / NB], it % NB, sRed + (n_items - 1) % KG * C::RED_GROUP, cta, more,
+                                  ctid);
           }
         }
         if (layer) {  // this CTA's h is there

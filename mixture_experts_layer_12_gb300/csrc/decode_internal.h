@@ -23,9 +23,9 @@ constexpr int kDecMaxCtas = 152;           // CTAs of the streaming kernel
 constexpr int kDecMaxEntries = kMaxExperts + MOED_MAX_ROWS / 8;
 
 // Control block at the start of a workspace, cleared by the first kernel of
-// every call.  bytes: [status 64 | grid barriers 64 | item tickets | n_entries].
+// every call.  bytes: [status 64 | grid barriers 64 | item counters | n_entries].
 constexpr size_t kDecBarrierOffset = 64;
-constexpr size_t kDecTicketOffset = 128;    // kDecMaxCtas ints (<= 152 * 4 = 608 bytes)
+constexpr size_t kDecItemOffset = 128;    // kDecMaxCtas ints (<= 152 * 4 = 608 bytes)
 constexpr size_t kDecCountOffset = 960;     // number of entries, rows of the longest
 constexpr size_t kDecEntryOffset = 1024;    // entries
 constexpr int kDecCtrlInts = 240;           // ints zeroed: everything before n_entries
@@ -70,7 +70,7 @@ struct DecFfnArgs {
   const DecEntry* entries;
   int max_entries;       // host bound on the number of entries
   unsigned* barrier;     // 3 grid barriers
-  unsigned* item_tickets;
+  unsigned* item_counts;
   float* parts;          // [CTAs][2][row_cap][128] partial tiles of the first product's split items
   float* parts2;         // the second product's: the first's are still being read
   int row_cap;           // rows of an entry at most, rounded up to 8
