@@ -214,7 +214,9 @@ def quantize_q4(w: torch.Tensor, group: int = 128, stream=None) -> Q4Weights:
     scales = torch.empty((E, K // group, N), dtype=_BF, device=w.device)
     q = Q4Weights.__new__(Q4Weights)  # of tensors that need no checks
     q._set(codes, scales, E, K, N, group, dev)
-    _check(_lib().moed_quantize_q4(E, K, N, group, src, *q._args, raw))
+    rc = (_sig_lib or _lib()).moed_quantize_q4(E, K, N, group, src, *q._args, raw)
+    if rc:
+        _check(rc)
     return q
 
 
@@ -225,10 +227,15 @@ def dequantize_q4(w: Q4Weights, out: torch.Tensor | None = None, stream=None) ->
             return dequantize_q4(w, out)
     dev, raw = _here()
     q = _q4_here(w, dev)
+    E, K, N = w.E, w.K, w.N
     if out is None:
-        out = torch.empty((w.E, w.K, w.N), dtype=_BF, device=w.codes.device)
-    dst = _addr(out, _BF, "out", w.E * w.K * w.N, dev)
-    _check(_lib().moed_dequantize_q4(w.E, w.K, w.N, w.group, *q, dst, raw))
+        out = torch.empty((E, K, N), dtype=_BF, device=w._codes.device)
+        dst = out.data_ptr()
+    else:
+        dst = _addr(out, _BF, "out", E * K * N, dev)
+    rc = (_sig_lib or _lib()).moed_dequantize_q4(E, K, N, w.group, *q, dst, raw)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -279,12 +286,15 @@ def matvec_q4(x: torch.Tensor, w: Q4Weights, seg_offsets: torch.Tensor | None = 
     src = _addr(x, _BF, "x", rows * K, dev)
     if out is None:
         out = torch.empty((rows, N), dtype=_BF, device=x.device)
-    dst = _addr(out, _BF, "out", rows * N, dev)
+        dst = out.data_ptr()
+    else:
+        dst = _addr(out, _BF, "out", rows * N, dev)
     with _enqueue:
         ws = _matvec_workspace(rows, n_segments, K, N, dev, raw)
-        rc = _lib().moed_matvec_q4(rows, K, N, E, w.group, n_segments, src, *q, seg, dst, ws.data_ptr(),
-                                   ws.numel(), raw)
-    _check(rc)
+        rc = (_sig_lib or _lib()).moed_matvec_q4(rows, K, N, E, w.group, n_segments, src, *q, seg, dst, ws.data_ptr(),
+                                                 ws.numel(), raw)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -394,7 +404,8 @@ class MoEDecodeLayer:
             b = _Buffers(self, T, raw, None) if capturing else self._buffers.get((T, raw)) or self._new(T, raw)
             rc = self._fn(*b.head, src, *self._ptrs, y.data_ptr(), *b.tail)
             self._last = b
-        _check(rc)
+        if rc:
+            _check(rc)
         return y
 
     def _new(self, T: int, raw: int) -> _Buffers:
