@@ -740,45 +740,69 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         const int k1 = (int)min((uint32_t)KCN, k0 + (end - x));
         const DecEntry en = c.ent[ph ? item % n_ent : item / NB];
         const int nb = ph ? item / n_ent : item % NB;
+        // What a chunk costs its loader paces the stream (1000 clocks a chunk of 4
+        // bits, 300 of them computing addresses, where memory takes 700), so
+        // everything that does not change between chunks is worked out here.
+        constexpr int RPP = 32 / PCS;                          // rows per pass of the warp
+        constexpr int RSTEP = RPP * DF_LOADERS;                // of all loaders
+        constexpr int PASSES = (8 * NT + RSTEP - 1) / RSTEP;
+        constexpr int HELD = PASSES <= 3 ? PASSES : 0;         // rows whose addresses are kept
+        const int r0 = lw * RPP + lane / PCS;
+        int kk = k0 * C::KC + lane % PCS * 8;
+        const uint16_t* rows[HELD > 0 ? HELD : 1];
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+          const int r = r0 + i * RSTEP;
+          rows[i] = src + kk;
+          if (r < en.n) rows[i] += (size_t)(ph ? en.row0 + r : c.tok[en.row0 + r]) * K;
+        }
+        // 4 bits: a chunk's scales, [256 / GRP rows][128 columns], by the last
+        // loader: 8 columns of every second row per lane
+        constexpr int GRP1 = Q4 ? GRP : 256;
+        constexpr int SROWS = 256 / GRP1;
+        const bool scaling = Q4 && lw == DF_LOADERS - 1;
+        const int c8 = (lane & 15) * 8;
+        const int scol = sg ? nb * 64 + (c8 & 63) : nb * kDecBN + c8;
+        int sr = k0 * SROWS + (lane >> 4);
+        const int send = scaling && scol < N ? K / GRP1 : 0;   // zeros past the end of K or of the columns
+        const uint16_t* sp = scales;
+        if (scaling) sp += ((size_t)en.expert * (K / GRP1) + sr) * ncols + scol + (sg && c8 >= 64 ? N : 0);
+        const bool any = scaling || (copies && lw * RPP < en.n);
         for (int kc = k0; kc < k1; ++kc) {
           if (!mbar_wait(&c.empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
           uint64_t* bar = &c.full[stage];
-          bool any = false;
-          if (Q4 && lw == DF_LOADERS - 1) {
-            any = true;
-            // the chunk's scales, [256 / GRP rows][128 columns]: 8 columns per
-            // copy, zeros past the end of K or of the columns
-            constexpr int GRP1 = Q4 ? GRP : 1;
-            constexpr int SROWS = kDecKC4 / GRP1;
-            const int c8 = (lane & 15) * 8;
-            const int col = sg ? nb * 64 + (c8 & 63) : nb * kDecBN + c8;
-            const bool in = col < N;
-            const uint32_t dst = smem_u32(sS + stage * C::S_BYTES) + (uint32_t)c8 * 2;
+          if (scaling) {
+            const uint32_t dst = smem_u32(sS) + (uint32_t)(stage * C::S_BYTES + (lane >> 4) * 256 + c8 * 2);
 #pragma unroll
-            for (int r = lane >> 4; r < SROWS; r += 2) {
-              const int sr = kc * SROWS + r;
-              const bool ok_row = in && sr * GRP1 < K;
-              const uint16_t* from = scales + ((size_t)en.expert * (K / GRP1) + (ok_row ? sr : 0)) * ncols +
-                                     (ok_row ? col + (sg && c8 >= 64 ? N : 0) : 0);
-              cp_async16(dst + (uint32_t)r * 256, from, ok_row ? 16u : 0u);
+            for (int m = 0; m < SROWS / 2; ++m) {
+              const bool in = sr + 2 * m < send;
+              cp_async16(dst + m * 512, in ? sp + (size_t)(2 * m) * ncols : scales, in ? 16u : 0u);
             }
+            sr += SROWS;
+            sp += (size_t)SROWS * ncols;
           }
-          if (copies && lw * (32 / PCS) < en.n) {
-            any = true;
-            constexpr int RPP = 32 / PCS;  // rows per pass of the warp
-            const int j = lane % PCS;
-            const int kk = kc * C::KC + j * 8;
-            const uint32_t dst = smem_u32(sB + stage * row_bytes) + (uint32_t)j * 16;
-            const uint32_t n = kk < K ? 16u : 0u;   // zeros past the end of K
-            const uint16_t* s = src + (kk < K ? kk : 0);
+          if (copies) {
+            const uint32_t dst = smem_u32(sB) + (uint32_t)(stage * row_bytes + r0 * C::PITCH + lane % PCS * 16);
+            const uint32_t n = kk < K ? 16u : 0u;              // zeros past the end of K
+            if constexpr (HELD > 0) {
+#pragma unroll
+              for (int i = 0; i < HELD; ++i) {
+                if (r0 + i * RSTEP < en.n)
+                  cp_async16(dst + i * (RSTEP * C::PITCH), kk < K ? rows[i] : src, n);
+                rows[i] += C::KC;
+              }
+            } else {
+              const uint16_t* s = src + (kk < K ? kk : 0);
 #pragma unroll 4
-            for (int r = lw * RPP + lane / PCS; r < en.n; r += RPP * DF_LOADERS) {
-              const int row = ph ? en.row0 + r : c.tok[en.row0 + r];
-              cp_async16(dst + (uint32_t)(r * C::PITCH), s + (size_t)row * K, n);
+              for (int r = r0; r < en.n; r += RSTEP) {
+                const int row = ph ? en.row0 + r : c.tok[en.row0 + r];
+                cp_async16(dst + (uint32_t)((r - r0) * C::PITCH), s + (size_t)row * K, n);
+              }
             }
+            kk += C::KC;
           }
           if (any)
             cp_async_arrive(bar);
