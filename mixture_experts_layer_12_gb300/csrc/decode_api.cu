@@ -45,8 +45,8 @@ struct Layout {
 // weights once each.  With 4-bit weights the cost of an entry grows with the
 // rows it has room for (registers, ring space, products): room for the average
 // and 1.4 times its square root more, what an even choice of experts hardly
-// exceeds (37 rows over 64 segments: 33 us with entries of up to 64 rows, 19
-// with 8; 32 rows over 8 experts: 121 us with 16, 118 with 8).  With bf16
+// exceeds (37 rows over 64 segments: 27 us with entries of up to 64 rows, 18
+// with 8; 32 rows over 8 experts: 108 us with 16, 100 with 8).  With bf16
 // weights reading them twice costs more than room does: 3 square roots.
 // `most`: rows that one can hold.
 int row_block_of(bool q4, int rows, int parts, int most) {
