@@ -152,9 +152,8 @@ class Q4Weights:
             raise ValueError(f"groups of {group} rows: 32, 64 or 128 are supported")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        # aliases, so that the memory stays even if the caller's tensors get other data
-        self._set(codes.detach(), scales.detach(), E, K8 * 8, N, group,
-                  codes.get_device() if codes.device == scales.device else -1)
+        dev = codes.get_device()
+        self._set(codes, scales, E, K8 * 8, N, group, dev if scales.get_device() == dev else -1)
 
     def _set(self, codes, scales, E, K, N, group, dev):
         self._codes, self._scales = codes, scales
@@ -195,6 +194,8 @@ def _q4_here(w: Q4Weights, dev: int):
     if w._device != dev:
         raise ValueError(f"the 4-bit weights' codes are on {w.codes.device} and their scales on "
                          f"{w.scales.device}, the current device is cuda:{dev}")
+    if (w._codes.data_ptr(), w._scales.data_ptr()) != w._args:
+        raise ValueError("the 4-bit weights' tensors were given other memory")
     return w._args
 
 
@@ -358,9 +359,9 @@ class MoEDecodeLayer:
             check_tensor(t, dt, name, 0, dev)
         if bias is not None:
             check_tensor(bias, _F32, "bias", self.E, dev)
-        # aliases, so that the memory stays even if the caller's tensors get other data
-        self._w_router, self._bias = w_router.detach(), None if bias is None else bias.detach()
-        self._w1, self._w2 = (w1, w2) if self.q4 else (w1.detach(), w2.detach())
+        self._w_router, self._w1, self._w2, self._bias = w_router, w1, w2, bias
+        # aliases, so that the memory stays even if those tensors are given other
+        self._held = [t.detach() for t in (w_router, bias, *weights) if t is not None]
         self._device, self._index = w_router.device, dev
         self._ptrs = (ctypes.c_void_p(w_router.data_ptr()),
                       ctypes.c_void_p(None if bias is None else bias.data_ptr()),

@@ -520,7 +520,7 @@ def test_host_threads_on_one_stream():
 @pytest.mark.parametrize("group", [0, 64])
 def test_copies_and_replaced_tensors(group):
     """A copied layer works on its own memory; a weight whose tensor is given
-    other data stays what it was for the layer."""
+    other memory stays what it was for the layer."""
     x, layer = make_layer(60, 3, 256, 128, 4, 2, group=group)
     want = layer(x).clone()
     twin = copy.deepcopy(layer)
@@ -529,13 +529,17 @@ def test_copies_and_replaced_tensors(group):
     else:
         layer.w1.zero_()
     assert torch.equal(twin(x), want) and not torch.equal(layer(x), want)
-    w = torch.randn(128, 64, device=DEV).to(BF)
-    q = moe.quantize_q4(w, 64)
-    codes, scales = q.codes.clone(), q.scales.clone()
-    held = moe.Q4Weights(codes, scales)
-    codes.data, scales.data = torch.zeros_like(codes), torch.zeros_like(scales)
+    want = layer(x).clone()
+    for t in (layer.w1.codes, layer.w1.scales) if group else (layer.w1,):
+        t.data = torch.zeros_like(t)
     torch.cuda.empty_cache()
-    assert torch.equal(moe.dequantize_q4(held), moe.dequantize_q4(q))
+    assert torch.equal(layer(x), want)
+    if group:                                        # the weights by themselves are refused
+        with pytest.raises(ValueError, match="other memory"):
+            moe.dequantize_q4(layer.w1)
+        seg = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+        with pytest.raises(ValueError, match="other memory"):
+            moe.matvec_q4(x, layer.w1, seg)
 
 
 def test_wrong_device_types_and_strides_are_refused():
