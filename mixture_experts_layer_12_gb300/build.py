@@ -1,7 +1,7 @@
 """Builds libmoe.so in-tree with nvcc for sm_103a (no torch extension, no cmake).
 
 Each .cu translation unit compiles in parallel; the shared library links the
-CUDA runtime statically and exports only the C ABI of include/moe.h.
+CUDA runtime statically and exports only the C ABI of include/moe.h and moe_decode.h.
 """
 from __future__ import annotations
 
