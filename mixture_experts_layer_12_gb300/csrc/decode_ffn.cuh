@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         // there: whole items as they are, shared ones summed from their tiles.
         // A thread's pieces are worked out before the wait, and their loads
         // are in flight together.
-        constexpr int UN = 3;
+        constexpr int UN = 2;
         q2 = qi;
         const Split s1((uint32_t)n_ent * p.nb1 * p.kc1, G, p.least1);
         const int total = (int)(end - x) * max_rows * PCS;
@@ -932,8 +932,10 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             if (cw == 0) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
           }
-          float4 z[UN][2], g2[UN][2];
+          // the first two tiles of all pieces at once, hardly ever there are more
+          float4 z[UN][2], g2[UN][2], z1[UN][2], g1[UN][2];
           uint4 v[UN];
+          const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int u = 0; u < UN; ++u) {
             v[u] = make_uint4(0, 0, 0, 0);
@@ -941,16 +943,25 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             if (part[u]) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                z[u][h] = __ldcg(reinterpret_cast<const float4*>(part[u]) + h);
-                if (swiglu) g2[u][h] = __ldcg(reinterpret_cast<const float4*>(part[u] + 64) + h);
+                const float4* t0 = reinterpret_cast<const float4*>(part[u]) + h;
+                const float4* t1 = reinterpret_cast<const float4*>(part[u] + tile) + h;
+                z[u][h] = __ldcg(t0);
+                z1[u][h] = __ldcg(t1);
+                g2[u][h] = swiglu ? __ldcg(t0 + 16) : none;
+                g1[u][h] = swiglu ? __ldcg(t1 + 16) : none;
               }
             }
           }
 #pragma unroll
           for (int u = 0; u < UN; ++u) {
             if (part[u]) {
-#pragma unroll 2
-              for (int o = 1; o <= more[u]; ++o) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                add4(z[u][h], z1[u][h]);
+                add4(g2[u][h], g1[u][h]);
+              }
+#pragma unroll 1
+              for (int o = 2; o <= more[u]; ++o) {
                 const float* q = part[u] + (size_t)(2 * o - 1) * tile;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
