@@ -346,6 +346,9 @@ __device__ __forceinline__ void count_wait(const DecFfnArgs& p, const unsigned* 
 // 128 columns of a token per warp and step, 4 per lane, its experts summed in slot
 // order, their rows whole from yfull or, where CTAs share the item, from their
 // tiles in order (the first one's slot 1, the later ones' slot 0).
+// DEEP: tiles of each of 4 experts whose loads are in flight together, as many as the
+// registers of the kernel leave room for.
+template <int DEEP>
 __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, uint32_t G, int cw,
                                         int gw, int warps, int threads, int lane) {
   const int N = p.N2;
@@ -386,11 +389,24 @@ __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Spli
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           v[u] = src[u] ? __ldcg(reinterpret_cast<const float4*>(src[u])) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int most = max(max(more[0], more[1]), max(more[2], more[3]));
+#pragma unroll 1
+        for (int o0 = 1; o0 <= most; o0 += DEEP) {
+          float4 t[DEEP][4];
+#pragma unroll
+          for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              t[d][u] = o0 + d <= more[u]
+                            ? __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * (o0 + d) - 1) * tile))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add4(v[u], t[d][u]);
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-#pragma unroll 4
-          for (int o = 1; o <= more[u]; ++o)
-            add4(v[u], __ldcg(reinterpret_cast<const float4*>(src[u] + (size_t)(2 * o - 1) * tile)));
           if (src[u]) {
             const float w = c.gate[tok * p.k + j0 + u];
             y.x = fmaf(w, v[u].x, y.x);
@@ -1132,7 +1148,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
       } else {
         if (ctid == 0) red_release(p.barrier + kGridY, 1u);
-        combine(p, c, sp, G, cw, gw, warps, CTHREADS, lane);
+        combine<(Q4 || NT > 2 ? 1 : 3)>(p, c, sp, G, cw, gw, warps, CTHREADS, lane);
       }
     }
   }
