@@ -161,9 +161,8 @@ __device__ __forceinline__ void lds128(uint32_t a, uint32_t (&r)[4]) {
 __device__ __forceinline__ void lds64(uint32_t a, uint32_t& r0, uint32_t& r1) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(a) : "memory");
 }
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -253,27 +252,18 @@ __device__ __forceinline__ void add4(float4& a, const float4 b) {
   a.w += b.w;
 }
 
-// 8 elements of h, rounded to bf16, from x W1 (or the gate's, and the up
-// projection's)
-__device__ __forceinline__ uint4 activated(const float4 (&z)[2], const float4 (&u)[2], bool swiglu) {
-  const float a[8] = {z[0].x, z[0].y, z[0].z, z[0].w, z[1].x, z[1].y, z[1].z, z[1].w};
-  const float b[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
-  float h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = swiglu ? dec_silu(a[i]) * b[i] : dec_gelu(a[i]);
-  return make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]),
-                    pack_bf16x2(h[6], h[7]));
-}
-
-// 4 columns of the first product, activated, to h (or y)
-__device__ __forceinline__ void write_piece(const DecFfnArgs& p, size_t at, float4 z, const float4& u) {
-  if (p.act == kDecSwiGLU) {
+// 4 columns of the first product (and of the up projection), activated and rounded
+// to bf16
+__device__ __forceinline__ uint2 activated(int act, float4 z, const float4& u) {
+  if (act == kDecSwiGLU) {
     z = make_float4(dec_silu(z.x) * u.x, dec_silu(z.y) * u.y, dec_silu(z.z) * u.z, dec_silu(z.w) * u.w);
-  } else if (p.act == kDecGelu) {
+  } else if (act == kDecGelu) {
     z = make_float4(dec_gelu(z.x), dec_gelu(z.y), dec_gelu(z.z), dec_gelu(z.w));
   }
-  *reinterpret_cast<uint2*>((p.act == kDecNone ? p.y : p.h) + at) =
-      make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
+  return make_uint2(pack_bf16x2(z.x, z.y), pack_bf16x2(z.z, z.w));
+}
+__device__ __forceinline__ void write_piece(const DecFfnArgs& p, size_t at, const float4& z, const float4& u) {
+  *reinterpret_cast<uint2*>((p.act == kDecNone ? p.y : p.h) + at) = activated(p.act, z, u);
 }
 
 // A whole item of the first product, from its sums in shared memory, by one
@@ -948,49 +938,49 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             if (cw == 0) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
           }
-          // the first two tiles of all pieces at once, hardly ever there are more
-          float4 z[UN][2], g2[UN][2], z1[UN][2], g1[UN][2];
-          uint4 v[UN];
+          // the same tile of all pieces (their halves) at once
+          float4 z[2 * UN], g2[2 * UN];
+          uint2 v[2 * UN];
           const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+          int most = 0;
 #pragma unroll
-          for (int u = 0; u < UN; ++u) {
-            v[u] = make_uint4(0, 0, 0, 0);
-            if (whole[u]) v[u] = __ldcg(reinterpret_cast<const uint4*>(whole[u]));
+          for (int i = 0; i < 2 * UN; ++i) {
+            const int u = i / 2, h = i % 2;
+            most = max(most, more[u]);
+            v[i] = make_uint2(0, 0);
+            z[i] = g2[i] = none;
+            if (whole[u]) v[i] = __ldcg(reinterpret_cast<const uint2*>(whole[u]) + h);
             if (part[u]) {
+              z[i] = __ldcg(reinterpret_cast<const float4*>(part[u]) + h);
+              if (swiglu) g2[i] = __ldcg(reinterpret_cast<const float4*>(part[u] + 64) + h);
+            }
+          }
+#pragma unroll 1
+          for (int o = 1; o <= most; ++o) {
+            float4 z1[2 * UN], g1[2 * UN];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float4* t0 = reinterpret_cast<const float4*>(part[u]) + h;
-                const float4* t1 = reinterpret_cast<const float4*>(part[u] + tile) + h;
-                z[u][h] = __ldcg(t0);
-                z1[u][h] = __ldcg(t1);
-                g2[u][h] = swiglu ? __ldcg(t0 + 16) : none;
-                g1[u][h] = swiglu ? __ldcg(t1 + 16) : none;
+            for (int i = 0; i < 2 * UN; ++i) {
+              const int u = i / 2, h = i % 2;
+              z1[i] = g1[i] = none;
+              if (o <= more[u]) {
+                const float* t = part[u] + (size_t)(2 * o - 1) * tile;
+                z1[i] = __ldcg(reinterpret_cast<const float4*>(t) + h);
+                if (swiglu) g1[i] = __ldcg(reinterpret_cast<const float4*>(t + 64) + h);
               }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * UN; ++i) {
+              add4(z[i], z1[i]);
+              add4(g2[i], g1[i]);
             }
           }
 #pragma unroll
-          for (int u = 0; u < UN; ++u) {
-            if (part[u]) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                add4(z[u][h], z1[u][h]);
-                add4(g2[u][h], g1[u][h]);
-              }
-#pragma unroll 1
-              for (int o = 2; o <= more[u]; ++o) {
-                const float* q = part[u] + (size_t)(2 * o - 1) * tile;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  add4(z[u][h], __ldcg(reinterpret_cast<const float4*>(q) + h));
-                  if (swiglu) add4(g2[u][h], __ldcg(reinterpret_cast<const float4*>(q + 64) + h));
-                }
-              }
-              v[u] = activated(z[u], g2[u], swiglu);
-            }
-            const int i = i0 + u * CTHREADS;
+          for (int i = 0; i < 2 * UN; ++i) {
+            const int u = i / 2, h = i % 2, piece = i0 + u * CTHREADS;
+            if (more[u] > 0) v[i] = activated(p.act, z[i], g2[i]);
             if (more[u] >= 0)
-              sts128(smem_u32(sB) + (uint32_t)(i / PCS) * C::PITCH + (uint32_t)(i % PCS) * 16, v[u].x, v[u].y,
-                     v[u].z, v[u].w);
+              sts64(smem_u32(sB) + (uint32_t)(piece / PCS) * C::PITCH + (uint32_t)(piece % PCS) * 16 + h * 8, v[i].x,
+                    v[i].y);
           }
         }
         named_sync(BAR_CONS, CTHREADS);
