@@ -48,12 +48,12 @@
 // The grid barriers need all CTAs resident, which the cooperative launch
 // guarantees; they and every other wait are bounded.
 // Measured with the first kernel, GPU time of a call: one token, 8 experts of 4096 x
-// 14336, 2 of them: 80 us in bf16 (5.9 TB/s, 0.87 of the copy bandwidth), 48 us gated
-// in 4 bits; 16 tokens in 4 bits 100 us (4.8 TB/s); 64 experts of 2048 x 1408, 4 of
-// them, gated: 27 us in bf16, of which 10 are the weights; 4096 x 14336 in 4 bits
-// times a row: 12.6 us, 4.5 of them the weights.  What is left beside the stream is a
+// 14336, 2 of them: 80 us in bf16 (5.9 TB/s, 0.87 of the copy bandwidth), 47 us gated
+// in 4 bits; 16 tokens in 4 bits 97 us (4.9 TB/s); 64 experts of 2048 x 1408, 4 of
+// them, gated: 25 us in bf16, of which 10 are the weights; 4096 x 14336 in 4 bits
+// times a row: 12.4 us, 4.5 of them the weights.  What is left beside the stream is a
 // chain of trips to memory: the list (1 us) and the first chunk (2 us), partial tiles
-// and h between the products (4-5 us) and the combine (3 us).
+// and h between the products (4-5 us) and the combine (2-3 us).
 #pragma once
 
 #include "decode_internal.h"
@@ -336,8 +336,10 @@ __device__ __forceinline__ void count_wait(const DecFfnArgs& p, const unsigned* 
 // 128 columns of a token per warp and step, 4 per lane, its experts summed in slot
 // order, their rows whole from yfull or, where CTAs share the item, from their
 // tiles in order (the first one's slot 1, the later ones' slot 0).
-// DEEP: tiles of each of 4 experts whose loads are in flight together, as many as the
-// registers of the kernel leave room for.
+// The same tile of 4 experts is asked for at once: one expert after the other is 4
+// trips to memory in a row (narrow experts, one token: 26.8 us instead of 25.1).
+// DEEP: tiles of each of them in flight together, as many as the registers of the
+// kernel leave room for.
 template <int DEEP>
 __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, uint32_t G, int cw,
                                         int gw, int warps, int threads, int lane) {
