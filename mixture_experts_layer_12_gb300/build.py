@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "router.cu", "route_fused.cu", "dispatch_combine.cu", "ffn_gemm.cu",
-           "ffn_gemm_small.cu", "decode_api.cu", "decode_route.cu", "decode_ffn_bf16.cu",
+           "ffn_gemm_small.cu", "decode_api.cu", "decode_route.cu", "decode_ffn_bf16.cu", "decode_ffn_pair.cu",
            "decode_ffn_q4_32.cu", "decode_ffn_q4_64.cu", "decode_ffn_q4_128.cu", "q4.cu"]
 HEADERS = ["tc_common.cuh", "moe_internal.h", "api_internal.h", "decode_internal.h", "decode_ffn.cuh",
            "route_topk.cuh"]

@@ -11,6 +11,7 @@ namespace moe {
 cudaError_t decode_set_attributes() {
   cudaError_t e = decode_route_set_attributes();
   if (e == cudaSuccess) e = decode_ffn_bf16_set_attributes();
+  if (e == cudaSuccess) e = decode_ffn_pair_set_attributes();
   if (e == cudaSuccess) e = decode_ffn_q4_32_set_attributes();
   if (e == cudaSuccess) e = decode_ffn_q4_64_set_attributes();
   if (e == cudaSuccess) e = decode_ffn_q4_128_set_attributes();
@@ -24,6 +25,7 @@ namespace {
 cudaError_t launch_decode_ffn(const DecFfnMaps& m, const DecFfnArgs& a, int ctas, cudaStream_t st) {
   switch (a.group) {
     case 0: return launch_decode_ffn_bf16(m, a, ctas, st);
+    case kDecPair: return launch_decode_ffn_pair(m, a, ctas, st);
     case 32: return launch_decode_ffn_q4_32(m, a, ctas, st);
     case 64: return launch_decode_ffn_q4_64(m, a, ctas, st);
     default: return launch_decode_ffn_q4_128(m, a, ctas, st);
@@ -58,14 +60,15 @@ int row_block_of(bool q4, int rows, int parts, int most) {
   return rb;
 }
 
-Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool layer) {
+// pair: the first product's partial tiles are a gate's and an up projection's
+Layout layout_of(int rows, int row_cap, int max_entries, int H, int F, bool layer, bool pair) {
   Layout L;
   L.max_entries = max_entries;
   L.row_cap = row_cap;
   L.entries = kDecEntryOffset;
   L.parts = L.entries + up((size_t)max_entries * sizeof(DecEntry), 1024);
   const size_t tiles = (size_t)kDecMaxCtas * 2 * row_cap * kDecBN * 4;
-  L.parts2 = L.parts + tiles;
+  L.parts2 = L.parts + tiles * (pair ? 2 : 1);
   L.yfull = L.parts2 + (layer ? tiles : 0);
   L.h = L.yfull + (layer ? up((size_t)rows * H * 4, 1024) : 0);
   L.total = L.h + (layer ? up((size_t)rows * F * 2, 1024) : 0);
@@ -78,16 +81,31 @@ int max_entries_of(int rows, int parts, int block) {
   return rows < parts ? rows : parts + (rows - parts) / block;
 }
 
+// How the first product of gated bf16 experts is cut (kDecPair).
+// Chunks of 64 gate and 64 up columns are rows of 128 bytes, which memory delivers
+// a quarter more slowly than the 256 of 128 columns (64 experts of 2048 x 1408, 32
+// tokens: 204 us, with alternating chunks of 128 columns 157); but those are dealt
+// out in pairs, 32 KB, and where a CTA has few of them one more or less is what
+// counts (one token, 9 pairs per CTA: 24.8 us, 25.3 with pairs; 2 tokens, 18 pairs:
+// 35.8, 34.5).  With 4 bits 64 columns are 256 bytes.
+bool pair_of(const moe_shape* s, bool q4) {
+  if (q4 || s->expert_act != MOE_EXPERT_SWIGLU) return false;
+  const int64_t hit = (int64_t)s->T * s->k < s->E ? s->T * s->k : s->E;
+  const int64_t nb = (s->F + kDecBN - 1) / kDecBN, kc = (s->H + kDecKC16 - 1) / kDecKC16;
+  return hit * nb * kc >= 12 * kDecMaxCtas;
+}
+
 Layout layer_layout(const moe_shape* s, bool q4) {
   const int rows = s->T > 0 ? s->T * s->k : 1;
   const int block = row_block_of(q4, rows, s->E, s->T);
-  return layout_of(rows, block, max_entries_of(rows, s->E, block), s->H, s->F, true);
+  return layout_of(rows, block, max_entries_of(rows, s->E, block), s->H, s->F, true,
+                   pair_of(s, q4));
 }
 
 Layout matvec_layout(int rows, int n_segments) {
   const int r = rows > 0 ? rows : 1;
   const int block = row_block_of(true, r, n_segments, r);
-  return layout_of(r, block, max_entries_of(r, n_segments, block), 0, 0, false);
+  return layout_of(r, block, max_entries_of(r, n_segments, block), 0, 0, false, false);
 }
 
 template <typename T>
@@ -129,7 +147,7 @@ int check_q4(int32_t E, int32_t K, int32_t N, int32_t group) {
 
 // The weights' tensor map (see DecFfnMaps): W [E, K, N] bf16, or words
 // [E, K/8, N]; `half`: columns of a gate / up half (N where there is none).
-int map_weights(CUtensorMap* m, int* blocked, const void* w, bool q4, int E, int K, int N, int half,
+int map_weights(CUtensorMap* m, int* blocked, const void* w, bool q4, int E, int K, int N, int half, bool pair,
                 const char* what) {
   const uint64_t rows = q4 ? K / 8 : K;
   const uint64_t esize = q4 ? 4 : 2;
@@ -141,7 +159,7 @@ int map_weights(CUtensorMap* m, int* blocked, const void* w, bool q4, int E, int
   if (*blocked) {
     const uint64_t dims[4] = {blk, rows, (uint64_t)N / blk, (uint64_t)E};
     const uint64_t strides[3] = {(uint64_t)N * esize, 128, rows * N * esize};
-    const uint32_t box[4] = {(uint32_t)blk, box_rows, (uint32_t)((gated ? 64 : kDecBN) / blk), 1};
+    const uint32_t box[4] = {(uint32_t)blk, box_rows, (uint32_t)((gated && !pair ? 64 : kDecBN) / blk), 1};
     return encode_map_as(m, type, CU_TENSOR_MAP_SWIZZLE_128B, w, 4, dims, strides, box, what);
   }
   const uint64_t dims[3] = {(uint64_t)N, rows, (uint64_t)E};
@@ -217,11 +235,12 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   const int N1 = swiglu ? 2 * s->F : s->F;
   DecFfnMaps maps;
   int blocked1 = 0, blocked2 = 0;
-  if ((rc = map_weights(&maps.w1, &blocked1, wt.w1, wt.q4, s->E, s->H, N1, s->F, "W1")) != MOE_OK) return rc;
-  if ((rc = map_weights(&maps.w2, &blocked2, wt.w2, wt.q4, s->E, s->F, s->H, s->H, "W2")) != MOE_OK) return rc;
+  const bool pair = pair_of(s, wt.q4);
+  if ((rc = map_weights(&maps.w1, &blocked1, wt.w1, wt.q4, s->E, s->H, N1, s->F, pair, "W1")) != MOE_OK) return rc;
+  if ((rc = map_weights(&maps.w2, &blocked2, wt.w2, wt.q4, s->E, s->F, s->H, s->H, false, "W2")) != MOE_OK) return rc;
 
   const int kc = wt.q4 ? kDecKC4 : kDecKC16;
-  const int cols1 = swiglu ? 64 : kDecBN;  // columns of h per item
+  const int cols1 = swiglu && !pair ? 64 : kDecBN;  // columns of h per item
   const int nb1 = (s->F + cols1 - 1) / cols1, kc1 = (s->H + kc - 1) / kc;
   const int nb2 = (s->H + kDecBN - 1) / kDecBN, kc2 = (s->F + kc - 1) / kc;
   if ((rc = check_chunks(L.max_entries, nb1, kc1)) != MOE_OK) return rc;
@@ -272,12 +291,12 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.T = s->T;
   fa.k = s->k;
   fa.act = swiglu ? kDecSwiGLU : kDecGelu;
-  fa.group = wt.group;
+  fa.group = pair ? kDecPair : wt.group;
   fa.K1 = s->H;
   fa.N1 = s->F;
   fa.nb1 = nb1;
   fa.kc1 = kc1;
-  fa.least1 = least_chunks(kc1);
+  fa.least1 = least_chunks(pair ? kc1 / 2 : kc1);  // (a pair takes twice the time)
   fa.least2 = least_chunks(kc2);
   fa.K2 = s->F;
   fa.N2 = s->H;
@@ -369,7 +388,7 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   if ((rc = check_chunks(L.max_entries, nb, kc)) != MOE_OK) return rc;
   DecFfnMaps maps;
   int blocked = 0;
-  if ((rc = map_weights(&maps.w1, &blocked, codes, true, E, K, N, N, "W")) != MOE_OK) return rc;
+  if ((rc = map_weights(&maps.w1, &blocked, codes, true, E, K, N, N, false, "W")) != MOE_OK) return rc;
   maps.w2 = maps.w1;  // not used
 
   DecPrepArgs pa;

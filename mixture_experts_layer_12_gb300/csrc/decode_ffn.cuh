@@ -266,19 +266,26 @@ __device__ __forceinline__ void write_piece(const DecFfnArgs& p, size_t at, cons
   *reinterpret_cast<uint2*>((p.act == kDecNone ? p.y : p.h) + at) = activated(p.act, z, u);
 }
 
-// A whole item of the first product, from its sums in shared memory, by one
-// group (128 threads): 4 columns of a row per thread and step.
-__device__ __forceinline__ void write_item(const DecFfnArgs& p, const DecEntry& en, int nb, int ftid,
-                                           const float* tile) {
+// The first product's items and partial tiles: 2^sh columns of h each, rows of 128
+// floats; `up`: from a gate's column to the up projection's; `tile`: floats of a tile.
+struct Items {
+  int sh, up;
+  size_t tile;
+};
+
+// A whole item of the first product, from its sums in shared memory (z, and u where
+// gated), by one group (128 threads): 4 columns of a row per thread and step.
+__device__ __forceinline__ void write_item(const DecFfnArgs& p, const Items& g, const DecEntry& en, int nb,
+                                           int ftid, const float* z, const float* u) {
   const bool swiglu = p.act == kDecSwiGLU;
-  const int cols = swiglu ? 64 : kDecBN;
 #pragma unroll 1
-  for (int i = ftid; i < en.n * (cols / 4); i += DF_FIN) {
-    const int r = i / (cols / 4), cl = (i % (cols / 4)) * 4;
-    const int col = nb * cols + cl;
+  for (int i = ftid; i < en.n << (g.sh - 2); i += DF_FIN) {
+    const int r = i >> (g.sh - 2), cl = (i - (r << (g.sh - 2))) * 4;
+    const int col = (nb << g.sh) + cl;
     if (col >= p.N1) continue;  // N1 is a multiple of 8
-    const float4* t = reinterpret_cast<const float4*>(tile + r * kDecBN + cl);
-    write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, t[0], swiglu ? t[16] : t[0]);
+    const float4 a = *reinterpret_cast<const float4*>(z + r * kDecBN + cl);
+    write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, a,
+                swiglu ? *reinterpret_cast<const float4*>(u + r * kDecBN + cl) : a);
   }
 }
 
@@ -286,24 +293,22 @@ __device__ __forceinline__ void write_item(const DecFfnArgs& p, const DecEntry& 
 // own sums, from shared memory, and the tiles of the `more` CTAs after it in that
 // order (their slot 0).
 template <int CTHREADS>
-__device__ __forceinline__ void finish_item(const DecFfnArgs& p, const DecEntry& en, int nb, const float* own,
-                                            int cta, int more, int ctid) {
+__device__ __forceinline__ void finish_item(const DecFfnArgs& p, const Items& g, const DecEntry& en, int nb,
+                                            const float* own_z, const float* own_u, int cta, int more, int ctid) {
   const bool swiglu = p.act == kDecSwiGLU;
-  const int sh = swiglu ? 4 : 5;  // pieces of a row: 64 or 128 columns
-  const size_t tile = (size_t)p.row_cap * kDecBN;
 #pragma unroll 1
-  for (int i = ctid; i < en.n << sh; i += CTHREADS) {
-    const int r = i >> sh, cl = (i - (r << sh)) * 4;
-    const int col = (nb << (sh + 2)) + cl;
+  for (int i = ctid; i < en.n << (g.sh - 2); i += CTHREADS) {
+    const int r = i >> (g.sh - 2), cl = (i - (r << (g.sh - 2))) * 4;
+    const int col = (nb << g.sh) + cl;
     if (col >= p.N1) continue;  // N1 is a multiple of 8
     const int at = r * kDecBN + cl;
-    const float* s = p.parts + (size_t)(cta * 2) * tile + at;
-    float4 z = *reinterpret_cast<const float4*>(own + at);
-    float4 u = swiglu ? *reinterpret_cast<const float4*>(own + at + 64) : z;
+    const float* s = p.parts + (size_t)(cta * 2) * g.tile + at;
+    float4 z = *reinterpret_cast<const float4*>(own_z + at);
+    float4 u = swiglu ? *reinterpret_cast<const float4*>(own_u + at) : z;
 #pragma unroll 4
     for (int o = 1; o <= more; ++o) {
-      add4(z, __ldcg(reinterpret_cast<const float4*>(s + (size_t)(2 * o) * tile)));
-      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(s + (size_t)(2 * o) * tile + 64)));
+      add4(z, __ldcg(reinterpret_cast<const float4*>(s + (size_t)(2 * o) * g.tile)));
+      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(s + (size_t)(2 * o) * g.tile + g.up)));
     }
     write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, z, u);
   }
@@ -417,10 +422,9 @@ __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Spli
 
 // All shared items of the first product by the consumer warps of all CTAs, once
 // every CTA's tiles are there: a row of an item per warp and step.
-__device__ __forceinline__ void finish_all(const DecFfnArgs& p, Ctrl& c, const Split& sp, int gw, int warps,
+__device__ __forceinline__ void finish_all(const DecFfnArgs& p, const Items& g, Ctrl& c, const Split& sp, int gw, int warps,
                                            int lane) {
   const bool swiglu = p.act == kDecSwiGLU;
-  const size_t tile = (size_t)p.row_cap * kDecBN;
   const int KCN = p.kc1, rows = c.max_rows;
   const int tasks = ((int)sp.G - 1) * rows;  // an item belongs to the first border of CTAs inside it
 #pragma unroll 1
@@ -434,16 +438,16 @@ __device__ __forceinline__ void finish_all(const DecFfnArgs& p, Ctrl& c, const S
     const DecEntry en = c.ent[item / p.nb1];
     if (r >= en.n) continue;
     const int more = sp.owner(i0 + KCN - 1) - ((int)b - 1);
-    const int col = (item % p.nb1) * (swiglu ? 64 : kDecBN) + lane * 4;
-    if (col >= p.N1 || (swiglu && lane >= 16)) continue;
-    const float* s = p.parts + (size_t)((b - 1) * 2 + 1) * tile + r * kDecBN + lane * 4;
+    const int col = (item % p.nb1 << g.sh) + lane * 4;
+    if (col >= p.N1 || lane * 4 >= 1 << g.sh) continue;
+    const float* s = p.parts + (size_t)((b - 1) * 2 + 1) * g.tile + r * kDecBN + lane * 4;
     float4 z = __ldcg(reinterpret_cast<const float4*>(s));
-    float4 u = swiglu ? __ldcg(reinterpret_cast<const float4*>(s + 64)) : z;
+    float4 u = swiglu ? __ldcg(reinterpret_cast<const float4*>(s + g.up)) : z;
 #pragma unroll 4
     for (int o = 1; o <= more; ++o) {
-      const float* q = s + (size_t)(2 * o - 1) * tile;
+      const float* q = s + (size_t)(2 * o - 1) * g.tile;
       add4(z, __ldcg(reinterpret_cast<const float4*>(q)));
-      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(q + 64)));
+      if (swiglu) add4(u, __ldcg(reinterpret_cast<const float4*>(q + g.up)));
     }
     write_piece(p, (size_t)(en.row0 + r) * p.N1 + col, z, u);
   }
@@ -561,7 +565,8 @@ __device__ __forceinline__ void chunk_bf16(float (&acc)[2][NT][4], uint32_t w0,
   }
 }
 
-// GRP: rows per scale of 4-bit weights; 0: bf16 weights.
+// GRP: rows per scale of 4-bit weights; 0: bf16 weights; kDecPair: bf16, gated, and
+// the chunks of the gate and of the up projection alternate.
 template <int GRP, int NT>
 __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     decode_ffn_kernel(const __grid_constant__ DecFfnMaps maps, const DecFfnArgs p) {
@@ -584,6 +589,12 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
   const uint32_t G = gridDim.x;
   const bool layer = p.act != kDecNone;
   const bool swiglu = p.act == kDecSwiGLU;
+  // Gated experts: an item is 64 columns of the gate and 64 of the up projection, and
+  // a chunk holds both; or (pair) 128 of either, whose chunks alternate, so that one
+  // group of consumers sums the gate and the other the up projection.
+  constexpr bool pair = GRP == kDecPair;
+  const Items g1{swiglu && !pair ? 6 : 7, pair ? p.row_cap * kDecBN : 64,
+                 (size_t)p.row_cap * kDecBN * (pair ? 2 : 1)};
 
   if (tid == 0) {
     for (int i = 0; i < DF_MAX_STAGES; ++i) {
@@ -680,10 +691,12 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           const int e = c.ent[ei].expert;
           // first columns of the tile's two 64-column halves: gated, the
           // gate's 64 columns and the up projection's
-          const bool sg = ph == 0 && swiglu;
+          const bool sg = ph == 0 && swiglu && !pair;
           const int ca = sg ? nb * 64 : nb * kDecBN;
           const int cb = sg ? p.N1 + nb * 64 : ca + 64;
-          for (int kc = k0; kc < k1; ++kc) {
+          const int two = pair && ph == 0 ? 1 : 0;  // the chunks of gate and up in turn
+          for (int i2 = k0 << two; i2 < k1 << two; ++i2) {
+            const int kc = i2 >> two, up = (i2 & two) * p.N1;
             if (!mbar_wait(&c.empty[stage], phase ^ 1u, wc)) {
               ok = false;
               break;
@@ -692,13 +705,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             uint8_t* dst = sW + stage * DF_W_BYTES;
             mbar_arrive_expect_tx(bar, DF_W_BYTES);
             if (blocked) {
-              tma_load_4d_hint(dst, mw, bar, 0, kc * KROWS, ca / BLK, e, pol);
+              tma_load_4d_hint(dst, mw, bar, 0, kc * KROWS, (ca + up) / BLK, e, pol);
               if (sg) tma_load_4d_hint(dst + DF_W_BYTES / 2, mw, bar, 0, kc * KROWS, cb / BLK, e, pol);
             } else {
 #pragma unroll
               for (int i = 0; i < kDecBN / BLK; ++i)
                 tma_load_3d_hint(dst + i * BLK_BYTES, mw, bar,
-                                 (i < kDecBN / BLK / 2 ? ca : cb - 64) + i * BLK, kc * KROWS, e, pol);
+                                 (i < kDecBN / BLK / 2 ? ca : cb - 64) + up + i * BLK, kc * KROWS, e, pol);
             }
             ++issued;
             if (++stage == S) {
@@ -741,8 +754,9 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const bool copies = ph == 0 || !reader;
       const uint16_t* scales = ph ? p.s2 : p.s1;
       const int N = ph ? p.N2 : p.N1;
-      const bool sg = ph == 0 && swiglu;
+      const bool sg = Q4 && ph == 0 && swiglu;
       const int ncols = sg ? 2 * N : N;  // columns of W
+      const int two = pair && ph == 0 ? 1 : 0;  // a chunk of rows for the gate's and the up projection's weights
       if (ph == 1 && copies && x < end) {
         // a loader that gave up before comes here too
         if (lw == 0 && ok) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
@@ -783,11 +797,12 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         const uint16_t* sp = scales;
         if (scaling) sp += ((size_t)en.expert * (K / GRP1) + sr) * ncols + scol + (sg && c8 >= 64 ? N : 0);
         const bool any = scaling || (copies && lw * RPP < en.n);
-        for (int kc = k0; kc < k1; ++kc) {
+        for (int i2 = k0 << two; i2 < k1 << two; ++i2) {
           if (!mbar_wait(&c.empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
+          const int step = (i2 & two) == two ? C::KC : 0;
           uint64_t* bar = &c.full[stage];
           if (scaling) {
             const uint32_t dst = smem_u32(sS) + (uint32_t)(stage * C::S_BYTES + (lane >> 4) * 256 + c8 * 2);
@@ -807,7 +822,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
               for (int i = 0; i < HELD; ++i) {
                 if (r0 + i * RSTEP < en.n)
                   cp_async16(dst + i * (RSTEP * C::PITCH), kk < K ? rows[i] : src, n);
-                rows[i] += C::KC;
+                rows[i] += step;
               }
             } else {
               const uint16_t* s = src + (kk < K ? kk : 0);
@@ -817,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
                 cp_async16(dst + (uint32_t)((r - r0) * C::PITCH), s + (size_t)row * K, n);
               }
             }
-            kk += C::KC;
+            kk += step;
           }
           if (any)
             cp_async_arrive(bar);
@@ -903,7 +918,6 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         q2 = qi;
         const Split s1((uint32_t)n_ent * p.nb1 * p.kc1, G, p.least1);
         const int total = (int)(end - x) * max_rows * PCS;
-        const size_t tile = (size_t)p.row_cap * kDecBN;
         for (int i0 = ctid; i0 < total || i0 == ctid; i0 += UN * CTHREADS) {
           const float* part[UN];     // first tile of a shared item's piece
           const uint16_t* whole[UN]; // or the piece of h
@@ -925,13 +939,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
               if (r < en.n) {
                 more[u] = 0;         // zeros past the end of K
                 if (kk < p.K2) {
-                  const uint32_t f = (uint32_t)(ei * p.nb1 + (swiglu ? kk >> 6 : kk >> 7)) * p.kc1;
+                  const uint32_t f = (uint32_t)(ei * p.nb1 + (kk >> g1.sh)) * p.kc1;
                   const int o0 = s1.owner(f);
                   more[u] = s1.owner(f + p.kc1 - 1) - o0;
                   if (more[u] == 0)
                     whole[u] = p.h + (size_t)(en.row0 + r) * p.K2 + kk;
                   else
-                    part[u] = p.parts + (size_t)(o0 * 2 + 1) * tile + r * kDecBN + (swiglu ? kk & 63 : kk & 127);
+                    part[u] = p.parts + (size_t)(o0 * 2 + 1) * g1.tile + r * kDecBN + (kk & ((1 << g1.sh) - 1));
                 }
               }
             }
@@ -954,26 +968,26 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             if (whole[u]) v[i] = __ldcg(reinterpret_cast<const uint2*>(whole[u]) + h);
             if (part[u]) {
               z[i] = __ldcg(reinterpret_cast<const float4*>(part[u]) + h);
-              if (swiglu) g2[i] = __ldcg(reinterpret_cast<const float4*>(part[u] + 64) + h);
+              if (swiglu) g2[i] = __ldcg(reinterpret_cast<const float4*>(part[u] + g1.up) + h);
             }
           }
 #pragma unroll 1
           for (int o = 1; o <= most; ++o) {
-            float4 z1[2 * UN], g1[2 * UN];
+            float4 z1[2 * UN], u1[2 * UN];
 #pragma unroll
             for (int i = 0; i < 2 * UN; ++i) {
               const int u = i / 2, h = i % 2;
-              z1[i] = g1[i] = none;
+              z1[i] = u1[i] = none;
               if (o <= more[u]) {
-                const float* t = part[u] + (size_t)(2 * o - 1) * tile;
+                const float* t = part[u] + (size_t)(2 * o - 1) * g1.tile;
                 z1[i] = __ldcg(reinterpret_cast<const float4*>(t) + h);
-                if (swiglu) g1[i] = __ldcg(reinterpret_cast<const float4*>(t + 64) + h);
+                if (swiglu) u1[i] = __ldcg(reinterpret_cast<const float4*>(t + g1.up) + h);
               }
             }
 #pragma unroll
             for (int i = 0; i < 2 * UN; ++i) {
               add4(z[i], z1[i]);
-              add4(g2[i], g1[i]);
+              add4(g2[i], u1[i]);
             }
           }
 #pragma unroll
@@ -1003,7 +1017,8 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[m][n][r] = 0.f;
 
-        for (; q < qi + (uint32_t)(k1 - k0); q += KG) {
+        const uint32_t chunks = (uint32_t)(k1 - k0) << (pair && ph == 0 ? 1 : 0);
+        for (; q < qi + chunks; q += KG) {
           const bool got = mbar_wait(&c.full[stage], par, wc);
           const uint32_t w0 = smem_u32(sW + stage * DF_W_BYTES);
           const uint32_t b0 = smem_u32(sB) + bl + (cached ? q - q2 : (uint32_t)stage) * (uint32_t)row_bytes;
@@ -1031,7 +1046,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             par ^= 1u;
           }
         }
-        qi += (uint32_t)(k1 - k0);
+        qi += chunks;
         x += (uint32_t)(k1 - k0);
         if constexpr (Q4) {  // the codes were taken as (c - 8) / 64
 #pragma unroll
@@ -1060,8 +1075,34 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           continue;
         }
         named_sync(BAR_ITEM + writer, CTHREADS);
-        {
-          const float* red = sRed + (1 - kg) * C::RED_GROUP;
+        const int bar_fin = BAR_FIN + kg;
+        float* tile_s = sRed + kg * C::RED_GROUP;
+        float* red = sRed + (1 - kg) * C::RED_GROUP;
+        // The item's sums as rows of 128 columns in this group's own space (it
+        // is free while the group writes), so that only real rows cost
+        // anything and every access to memory is 4 columns wide.
+        const auto lay_down = [&](float* to, const float (&v)[2][NT][4]) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (row_of(n, r) < en.n) to[row_of(n, r) * kDecBN + col_of(m, r)] = v[m][n][r];
+        };
+        if (pair && ph == 0) {
+          // the other's sums are of other columns: as rows too, in its space, once
+          // everybody has taken his own
+          float other[2][NT][4];
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) other[m][n][r] = red[((m * NT + n) * 4 + r) * DF_FIN + ftid];
+          named_sync(bar_fin, DF_FIN);
+          lay_down(red, other);
+        } else {
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -1069,20 +1110,11 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 #pragma unroll
               for (int r = 0; r < 4; ++r) acc[m][n][r] += red[((m * NT + n) * 4 + r) * DF_FIN + ftid];
         }
-        const int bar_fin = BAR_FIN + kg;
-
-        // The item's sums as rows of 128 columns in this group's own space (it
-        // is free while the group writes), so that only real rows cost
-        // anything and every access to memory is 4 columns wide.
-        float* tile_s = sRed + kg * C::RED_GROUP;
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (row_of(n, r) < en.n) tile_s[row_of(n, r) * kDecBN + col_of(m, r)] = acc[m][n][r];
+        lay_down(tile_s, acc);
         named_sync(bar_fin, DF_FIN);
+        // group 0 has summed the gate, group 1 the up projection
+        const float* tile_z = pair && ph == 0 ? sRed : tile_s;
+        const float* tile_u = pair ? sRed + C::RED_GROUP : tile_s + 64;
         // the first product's shared items by their first CTA, where it has no
         // readers and few rows: its own sums stay here until the loop ends
         const bool by_first = NT < 4 && ph == 0 && !reader;
@@ -1090,9 +1122,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         if (k0 != 0 || k1 != KCN) {
           // a shared item: this CTA's partial tile, slot 0 if the item began in
           // an earlier CTA, else slot 1
-          float* mine = (ph ? p.parts2 : p.parts) + (size_t)(cta * 2 + (k0 > 0 ? 0 : 1)) * p.row_cap * kDecBN;
-          for (int i = ftid * 4; i < en.n * kDecBN; i += DF_FIN * 4)
-            *reinterpret_cast<float4*>(mine + i) = *reinterpret_cast<const float4*>(tile_s + i);
+          float* mine = (ph ? p.parts2 : p.parts) + (size_t)(cta * 2 + (k0 > 0 ? 0 : 1)) *
+                                                        (ph ? (size_t)p.row_cap * kDecBN : g1.tile);
+          for (int i = ftid * 4; i < en.n * kDecBN; i += DF_FIN * 4) {
+            *reinterpret_cast<float4*>(mine + i) = *reinterpret_cast<const float4*>(tile_z + i);
+            if (pair && ph == 0)
+              *reinterpret_cast<float4*>(mine + g1.up + i) = *reinterpret_cast<const float4*>(tile_u + i);
+          }
         } else if (ph == 1) {  // whole items of the second product stay in fp32 for the combine
           for (int i = ftid * 4; i < en.n * kDecBN; i += DF_FIN * 4) {
             const int col = nb * kDecBN + (i & (kDecBN - 1));
@@ -1101,7 +1137,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
                   *reinterpret_cast<const float4*>(tile_s + i);
           }
         } else {
-          write_item(p, en, nb, ftid, tile_s);
+          write_item(p, g1, en, nb, ftid, tile_z, tile_u);
         }
         named_sync(bar_fin, DF_FIN);  // before this space is handed over again
         if (by_first && k0 != 0 && ftid == 0)
@@ -1120,7 +1156,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           if (ctid == 0) red_release(p.barrier + kGridTiles, 1u);
           if (cw == 0) count_wait(p, p.barrier + kGridTiles, G, c.abort_flag, lane);
           named_sync(BAR_CONS, CTHREADS);
-          finish_all(p, c, sp, gw, warps, lane);
+          finish_all(p, g1, c, sp, gw, warps, lane);
         } else if (!reader) {
           // few rows: the item that goes on in later CTAs, once they have counted
           // in.  They begin with it, so they have done so long ago.
@@ -1130,8 +1166,9 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             if (cw == 0) count_wait(p, p.item_counts + cta, (uint32_t)more, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
             const int it = (int)(end / KCN);
-            finish_item<CTHREADS>(p, c.ent[it / NB], it % NB, sRed + (n_items - 1) % KG * C::RED_GROUP, cta, more,
-                                  ctid);
+            const float* own = sRed + (n_items - 1) % KG * C::RED_GROUP;
+            finish_item<CTHREADS>(p, g1, c.ent[it / NB], it % NB, pair ? sRed : own,
+                                  pair ? sRed + C::RED_GROUP : own + 64, cta, more, ctid);
           }
         }
         if (layer) {  // this CTA's h is there

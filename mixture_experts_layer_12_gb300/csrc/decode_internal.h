@@ -71,7 +71,7 @@ struct DecFfnArgs {
   int max_entries;       // host bound on the number of entries
   unsigned* barrier;     // 3 grid barriers
   unsigned* item_counts;
-  float* parts;          // [CTAs][2][row_cap][128] partial tiles of the first product's split items
+  float* parts;          // [CTAs][2][row_cap][128] partial tiles of the first product's split items (kDecPair: two)
   float* parts2;         // the second product's: the first's are still being read
   int row_cap;           // rows of an entry at most, rounded up to 8
   float* yfull;          // layer: [T*k, H] fp32 expert outputs of whole items
@@ -86,7 +86,7 @@ struct DecFfnArgs {
   uint16_t* y;
   int T, k;
   int act;               // kDec*
-  int group;             // 4-bit: rows per scale; 0: bf16
+  int group;             // 4-bit: rows per scale; 0: bf16; kDecPair
   int K1, N1;            // first product: x [., K1] -> N1 columns of h (or y)
   int nb1, kc1;          // its column blocks and K chunks
   int least1, least2;    // chunks worth a CTA of their own
@@ -98,20 +98,23 @@ struct DecFfnArgs {
 // columns divide into blocks of 128 bytes (64 bf16, 32 words), gate and up
 // separately: dimensions [E, blocks, K, block], a box of one expert, as many
 // blocks as a 128- (gated: 64-) column half takes and one chunk's rows.
-// Elsewhere: dimensions [E, K, N], a box of one block.
+// Elsewhere: dimensions [E, K, N], a box of one block.  (kDecPair: the box is 128 columns.)
 struct DecFfnMaps {
   CUtensorMap w1, w2;
 };
 constexpr int kDecBN = 128;    // columns of an item's weight tile
 constexpr int kDecKC16 = 64;   // K rows of a chunk, bf16 weights
 constexpr int kDecKC4 = 256;   // K rows of a chunk, 4-bit weights
-// one translation unit per weight type (bf16; 4 bits with a scale per 32, 64
-// or 128 rows)
+// a `group` that says: bf16, gated, chunks of the gate and of the up projection in turn
+constexpr int kDecPair = -1;
+// one translation unit per weight type (bf16, the same in pairs; 4 bits with a scale
+// per 32, 64 or 128 rows)
 #define DECODE_FFN_UNIT(name)                                                                    \
   cudaError_t launch_decode_ffn_##name(const DecFfnMaps& m, const DecFfnArgs& a, int ctas,       \
                                        cudaStream_t st);                                         \
   cudaError_t decode_ffn_##name##_set_attributes();
 DECODE_FFN_UNIT(bf16)
+DECODE_FFN_UNIT(pair)
 DECODE_FFN_UNIT(q4_32)
 DECODE_FFN_UNIT(q4_64)
 DECODE_FFN_UNIT(q4_128)

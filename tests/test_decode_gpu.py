@@ -126,6 +126,22 @@ def test_layer_against_the_definition(T, H, F, E, k, act, gating, cf, bias):
     check_layer(*make_layer(T + H + E, T, H, F, E, k, act, gating, cf, bias))
 
 
+@pytest.mark.parametrize("T,H,F,E,k,gating,cf,bias", [
+    (1, 2048, 2816, 8, 4, 0, None, False),              # one token
+    (5, 1000, 1352, 24, 4, 1, None, True),              # columns in no blocks, a last item of 72
+    (16, 1024, 1408, 16, 4, 2, 1.0, False),             # 16 rows to an entry
+    (64, 1032, 2176, 8, 2, 0, None, True),              # 32
+    (64, 2056, 2176, 4, 3, 0, None, False),             # 64
+])
+def test_gated_layer_with_many_chunks(T, H, F, E, k, gating, cf, bias):
+    """Large enough for the gate's and the up projection's chunks to alternate."""
+    x, layer = make_layer(T + H, T, H, F, E, k, "swiglu", gating=gating, cf=cf, bias=bias)
+    check_layer(x, layer)
+    first = layer(x).clone()
+    for _ in range(5):
+        assert torch.equal(layer(x), first)
+
+
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("T,H,F,E,k,act,gating,cf,bias", [
     (1, 128, 128, 1, 1, "gelu", 0, None, False),
