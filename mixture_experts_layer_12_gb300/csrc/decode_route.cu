@@ -139,6 +139,10 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   float* sRed = reinterpret_cast<float*>(smem);
   float* sPart = reinterpret_cast<float*>(smem + L.stage);
   int* s_wc = reinterpret_cast<int*>(smem);  // dispatch: [chunk][expert], over the stage
+  // counted here, waited for before the first store to another rank's shared memory:
+  // only the cluster barrier says that all ranks have started, and ranks past the
+  // end of H come to that store almost at once
+  cluster_arrive();
   pdl_launch_dependents();
   pdl_wait();
 
@@ -230,6 +234,7 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
   const bool one_owner = T <= DR_RANKS;
   const int own = one_owner ? L.tp : (T + DR_RANKS - 1) / DR_RANKS;  // tokens of an owner
   const uint32_t part0 = smem_u32(sPart);
+  cluster_wait();
   for (int i = tid; i < T * (L.ep / 4); i += DR_THREADS) {
     const int t = i / (L.ep / 4), c4 = i - t * (L.ep / 4);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
