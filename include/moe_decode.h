@@ -76,6 +76,23 @@ MOE_API int moed_forward_q4(const moe_shape* s, int32_t group, const uint16_t* x
                             int32_t* perm, int32_t* slot, void* ws, size_t ws_bytes,
                             void* stream);
 
+/*
+ * Self-test of the streaming kernel's bounded waits, beside
+ * moe_selftest_wait_timeout: the layer (group = 0: bf16 weights, no scales;
+ * else as moed_forward_q4) with waits of at most limit_ns nanoseconds
+ * (1e3 .. 1e9), between its products for one CTA more than there are.  Those
+ * waits run out, every CTA gives up and leaves, and MOE_DEV_TIMEOUT is set in
+ * the workspace's status word.  The routing outputs are the layer's, y is void; the next call
+ * with the workspace is an ordinary one.  Nothing traps or hangs.
+ */
+MOE_API int moed_selftest_wait_timeout(const moe_shape* s, int32_t group, const uint16_t* x,
+                                       const uint16_t* w_router, const float* b_router,
+                                       const void* w1, const uint16_t* w1_scales, const void* w2,
+                                       const uint16_t* w2_scales, uint16_t* y, int32_t* ids,
+                                       float* weights, int32_t* counts, int32_t* offsets,
+                                       int32_t* perm, int32_t* slot, void* ws, size_t ws_bytes,
+                                       uint64_t limit_ns, void* stream);
+
 /* Workspace bytes of moed_matvec_q4; 0 for sizes it does not take. */
 MOE_API size_t moed_matvec_q4_workspace_size(int32_t rows, int32_t n_segments, int32_t K,
                                              int32_t N);

@@ -448,7 +448,7 @@ __all__ = [n for n in EXPORTS] + ["MoEError", "moe_shape", "make_shape", "load_l
 from .decode import (DECODE_EXPORTS, MOED_MAX_ROWS, MOED_MAX_TOKENS, MoEDecodeLayer,  # noqa: E402
                      Q4Weights, dequantize_q4, matvec_q4, moed_dequantize_q4, moed_forward,
                      moed_forward_q4, moed_matvec_q4, moed_matvec_q4_workspace_size,
-                     moed_quantize_q4, moed_workspace_size, quantize_q4)
+                     moed_quantize_q4, moed_selftest_wait_timeout, moed_workspace_size, quantize_q4)
 
 __all__ += [n for n in DECODE_EXPORTS] + ["DECODE_EXPORTS", "MOED_MAX_ROWS", "MOED_MAX_TOKENS",
                                           "MoEDecodeLayer", "Q4Weights", "dequantize_q4",

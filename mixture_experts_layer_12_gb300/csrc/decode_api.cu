@@ -130,6 +130,14 @@ int check_group(int32_t group) {
   return MOE_OK;
 }
 
+int check_q4_layer(const moe_shape* s, int32_t group) {
+  int rc = check_group(group);
+  if (rc != MOE_OK) return rc;
+  if (s->H % group != 0 || s->F % group != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "H = %d, F = %d: need multiples of the group (%d)", s->H, s->F, group);
+  return MOE_OK;
+}
+
 int check_q4(int32_t E, int32_t K, int32_t N, int32_t group) {
   int rc = check_group(group);
   if (rc != MOE_OK) return rc;
@@ -198,10 +206,11 @@ struct Weights {
   const void *w1, *s1, *w2, *s2;
 };
 
+// missing: CTAs that the grid barriers wait for in vain (the self-test)
 int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint16_t* w_router,
             const float* b_router, uint16_t* y, int32_t* ids, float* weights, int32_t* counts,
             int32_t* offsets, int32_t* perm, int32_t* slot, void* ws, size_t ws_bytes,
-            void* stream) {
+            void* stream, uint64_t wait_limit_ns = kWaitLimitNs, int missing = 0) {
   int rc;
   REQUIRE_PTR(ws);
   const Layout L = layer_layout(s, wt.q4);
@@ -303,8 +312,10 @@ int forward(const moe_shape* s, const Weights& wt, const uint16_t* x, const uint
   fa.nb2 = nb2;
   fa.kc2 = kc2;
   fa.status = static_cast<int*>(ws);
-  fa.wait_limit_ns = kWaitLimitNs;
-  e = launch_decode_ffn(maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
+  fa.wait_limit_ns = wait_limit_ns;
+  const int ctas = sms < kDecMaxCtas ? sms : kDecMaxCtas;
+  fa.arrivals = (uint32_t)(ctas + missing);
+  e = launch_decode_ffn(maps, fa, ctas, st);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "decode expert launch");
 }
 
@@ -336,12 +347,26 @@ int moed_forward_q4(const moe_shape* s, int32_t group, const uint16_t* x, const 
                     int32_t* slot, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_layer(s);
   if (rc != MOE_OK) return rc;
-  if ((rc = check_group(group)) != MOE_OK) return rc;
-  if (s->H % group != 0 || s->F % group != 0)
-    return fail(MOE_ERR_UNSUPPORTED, "H = %d, F = %d: need multiples of the group (%d)", s->H, s->F, group);
+  if ((rc = check_q4_layer(s, group)) != MOE_OK) return rc;
   const Weights wt{true, group, w1_codes, w1_scales, w2_codes, w2_scales};
   return forward(s, wt, x, w_router, b_router, y, ids, weights, counts, offsets, perm, slot, ws,
                  ws_bytes, stream);
+}
+
+int moed_selftest_wait_timeout(const moe_shape* s, int32_t group, const uint16_t* x,
+                               const uint16_t* w_router, const float* b_router, const void* w1,
+                               const uint16_t* w1_scales, const void* w2, const uint16_t* w2_scales,
+                               uint16_t* y, int32_t* ids, float* weights, int32_t* counts,
+                               int32_t* offsets, int32_t* perm, int32_t* slot, void* ws,
+                               size_t ws_bytes, uint64_t limit_ns, void* stream) {
+  int rc = check_layer(s);
+  if (rc != MOE_OK) return rc;
+  if (group != 0 && (rc = check_q4_layer(s, group)) != MOE_OK) return rc;
+  if (limit_ns < 1000 || limit_ns > kWaitLimitNs)
+    return fail(MOE_ERR_INVALID_ARG, "limit_ns = %llu: need 1e3 .. 1e9", (unsigned long long)limit_ns);
+  const Weights wt{group != 0, group, w1, w1_scales, w2, w2_scales};
+  return forward(s, wt, x, w_router, b_router, y, ids, weights, counts, offsets, perm, slot, ws,
+                 ws_bytes, stream, limit_ns, 1);
 }
 
 size_t moed_matvec_q4_workspace_size(int32_t rows, int32_t n_segments, int32_t K, int32_t N) {
@@ -427,7 +452,9 @@ int moed_matvec_q4(int32_t rows, int32_t K, int32_t N, int32_t E, int32_t group,
   fa.least2 = 1;
   fa.status = static_cast<int*>(ws);
   fa.wait_limit_ns = kWaitLimitNs;
-  e = launch_decode_ffn(maps, fa, sms < kDecMaxCtas ? sms : kDecMaxCtas, st);
+  const int ctas = sms < kDecMaxCtas ? sms : kDecMaxCtas;
+  fa.arrivals = (uint32_t)ctas;
+  e = launch_decode_ffn(maps, fa, ctas, st);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e, "matrix-vector launch");
 }
 

@@ -346,7 +346,7 @@ __device__ __forceinline__ void count_wait(const DecFfnArgs& p, const unsigned* 
 // DEEP: tiles of each of them in flight together, as many as the registers of the
 // kernel leave room for.
 template <int DEEP>
-__device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, uint32_t G, int cw,
+__device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Split& sp, int cw,
                                         int gw, int warps, int threads, int lane) {
   const int N = p.N2;
   const size_t tile = (size_t)p.row_cap * kDecBN;
@@ -378,7 +378,7 @@ __device__ __forceinline__ void combine(const DecFfnArgs& p, Ctrl& c, const Spli
         }
       }
       if (!waited) {
-        if (cw == 0) count_wait(p, p.barrier + kGridY, G, c.abort_flag, lane);
+        if (cw == 0) count_wait(p, p.barrier + kGridY, p.arrivals, c.abort_flag, lane);
         named_sync(BAR_CONS, threads);
         waited = true;
       }
@@ -722,16 +722,17 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
           x += k1 - k0;
         }
       }
-      // A CTA that gave up must not leave with copies in flight.  The barriers
-      // also count the row loaders, so wait a bounded while for each stage that
-      // was issued and not seen full.
-      if (!ok || *const_cast<volatile int*>(&c.abort_flag)) {
-        for (int m = max(0, issued - S); m < issued; ++m) {
-          const uint32_t a = smem_u32(&c.full[m % S]);
-          const uint32_t par = (uint32_t)((m / S) & 1);
-          const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(a, par) && global_timer_ns() - t0 < 1000000ull) {
-          }
+      // The CTA must not leave with copies in flight.  The barriers also count the
+      // row loaders, which do not arrive any more after a wait ran out: then a
+      // bounded while for each stage that was issued and not seen full.  A stage is
+      // issued again only after its copies before were seen full by all its consumers
+      // (they free nothing else), so the parity names the last ones.
+      for (int m = max(0, issued - S); m < issued; ++m) {
+        const uint32_t par = (uint32_t)((m / S) & 1);
+        if (mbar_wait(&c.full[m % S], par, wc)) continue;
+        const uint32_t a = smem_u32(&c.full[m % S]);
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(a, par) && global_timer_ns() - t0 < 1000000ull) {
         }
       }
     }
@@ -758,10 +759,13 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
       const int ncols = sg ? 2 * N : N;  // columns of W
       const int two = pair && ph == 0 ? 1 : 0;  // a chunk of rows for the gate's and the up projection's weights
       if (ph == 1 && copies && x < end) {
-        // a loader that gave up before comes here too
-        if (lw == 0 && ok) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
+        // a loader that gave up before comes here too; its lanes may have done so one
+        // by one, what follows is the whole warp's (a vote per chunk costs the 4-bit
+        // layer of 16 tokens 1.5 us)
+        ok = __all_sync(0xffffffffu, ok);
+        if (lw == 0 && ok) count_wait(p, p.barrier + kGridH, p.arrivals, c.abort_flag, lane);
         named_sync(BAR_ROWS, 32 * DF_LOADERS);
-        ok = ok && *const_cast<volatile int*>(&c.abort_flag) == 0;
+        ok = __all_sync(0xffffffffu, ok && *const_cast<volatile int*>(&c.abort_flag) == 0);
       }
       while (x < end && ok) {
         const int item = (int)(x / KCN);
@@ -860,9 +864,14 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
     // barrier apart by parity only, so whoever waits for a stage's phase must
     // know the one before it to be over; groups and copies in flight overtake
     // each other, so every stage belongs to one group (S mod KG = 0).
-    // After a wait that ran out the consumers go through all their barriers
-    // and counters as before, only without data: nobody else hangs, and the
-    // status word says that the result is void.
+    // After a wait that ran out the consumers go through all their barriers and
+    // counters as before, multiplying whatever the stages hold (a branch around the
+    // products would need the warp's lanes to agree: a vote per chunk, 1.5 us of the
+    // 4-bit layer of 16 tokens): nobody else hangs, and the status word says that the
+    // result is void.  They free no stage any more: copies into it may still be on
+    // their way, and new ones would leave its barrier a phase behind what everybody
+    // takes it for.
+    bool ok = true;
     uint32_t q = (uint32_t)kg, qi = 0, q2 = 0;
     int stage = kg;
     uint32_t par = 0;
@@ -951,7 +960,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             }
           }
           if (i0 == ctid) {
-            if (cw == 0) count_wait(p, p.barrier + kGridH, G, c.abort_flag, lane);
+            if (cw == 0) count_wait(p, p.barrier + kGridH, p.arrivals, c.abort_flag, lane);
             named_sync(BAR_CONS, CTHREADS);
           }
           // the same tile of all pieces (their halves) at once
@@ -1019,7 +1028,8 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
 
         const uint32_t chunks = (uint32_t)(k1 - k0) << (pair && ph == 0 ? 1 : 0);
         for (; q < qi + chunks; q += KG) {
-          const bool got = mbar_wait(&c.full[stage], par, wc);
+          ok = ok && mbar_wait(&c.full[stage], par, wc);
+          __syncwarp();
           const uint32_t w0 = smem_u32(sW + stage * DF_W_BYTES);
           const uint32_t b0 = smem_u32(sB) + bl + (cached ? q - q2 : (uint32_t)stage) * (uint32_t)row_bytes;
           const auto chunk = [&](auto nta) {
@@ -1029,18 +1039,16 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
             else
               chunk_bf16<NT, NTA>(acc, w0, wofs, b0);
           };
-          if (got) {
-            if (NT == 1 || en.n <= 8)
-              chunk(Int<1>{});
-            else if (NT == 2 || en.n <= 16)
-              chunk(Int<NT < 2 ? NT : 2>{});
-            else if (NT == 4 || en.n <= 32)
-              chunk(Int<NT < 4 ? NT : 4>{});
-            else
-              chunk(Int<NT>{});
-          }
+          if (NT == 1 || en.n <= 8)
+            chunk(Int<1>{});
+          else if (NT == 2 || en.n <= 16)
+            chunk(Int<NT < 2 ? NT : 2>{});
+          else if (NT == 4 || en.n <= 32)
+            chunk(Int<NT < 4 ? NT : 4>{});
+          else
+            chunk(Int<NT>{});
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c.empty[stage]);
+          if (ok && lane == 0) mbar_arrive(&c.empty[stage]);
           if ((stage += KG) >= S) {
             stage -= S;
             par ^= 1u;
@@ -1154,7 +1162,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         if (!reader && NT >= 4) {
           // many rows: by all CTAs, after a grid barrier
           if (ctid == 0) red_release(p.barrier + kGridTiles, 1u);
-          if (cw == 0) count_wait(p, p.barrier + kGridTiles, G, c.abort_flag, lane);
+          if (cw == 0) count_wait(p, p.barrier + kGridTiles, p.arrivals, c.abort_flag, lane);
           named_sync(BAR_CONS, CTHREADS);
           finish_all(p, g1, c, sp, gw, warps, lane);
         } else if (!reader) {
@@ -1177,7 +1185,7 @@ __global__ void __launch_bounds__(Cfg<(GRP > 0), NT>::THREADS, 1)
         }
       } else {
         if (ctid == 0) red_release(p.barrier + kGridY, 1u);
-        combine<(Q4 || NT > 2 ? 1 : 3)>(p, c, sp, G, cw, gw, warps, CTHREADS, lane);
+        combine<(Q4 || NT > 2 ? 1 : 3)>(p, c, sp, cw, gw, warps, CTHREADS, lane);
       }
     }
   }

@@ -70,6 +70,7 @@ struct DecFfnArgs {
   const DecEntry* entries;
   int max_entries;       // host bound on the number of entries
   unsigned* barrier;     // 3 grid barriers
+  uint32_t arrivals;     // CTAs that they wait for: all (the self-test: one more than there are)
   unsigned* item_counts;
   float* parts;          // [CTAs][2][row_cap][128] partial tiles of the first product's split items (kDecPair: two)
   float* parts2;         // the second product's: the first's are still being read

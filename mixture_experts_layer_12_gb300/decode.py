@@ -24,7 +24,7 @@ MOED_MAX_ROWS = 512
 # Every symbol include/moe_decode.h declares.
 DECODE_EXPORTS = ("moed_workspace_size", "moed_forward", "moed_forward_q4",
                   "moed_matvec_q4_workspace_size", "moed_matvec_q4", "moed_quantize_q4",
-                  "moed_dequantize_q4")
+                  "moed_dequantize_q4", "moed_selftest_wait_timeout")
 
 _sig_lock = threading.Lock()
 _sig_lib = None
@@ -42,6 +42,7 @@ def _lib():
             "moed_workspace_size": ([S], Z),
             "moed_forward": ([S] + [P] * 13 + [Z, P], ctypes.c_int),
             "moed_forward_q4": ([S, I] + [P] * 15 + [Z, P], ctypes.c_int),
+            "moed_selftest_wait_timeout": ([S, I] + [P] * 15 + [Z, ctypes.c_uint64, P], ctypes.c_int),
             "moed_matvec_q4_workspace_size": ([I] * 4, Z),
             "moed_matvec_q4": ([I] * 6 + [P] * 6 + [Z, P], ctypes.c_int),
             "moed_quantize_q4": ([I] * 4 + [P] * 4, ctypes.c_int),
@@ -79,17 +80,34 @@ def _q4_ptrs(w, E, K, N, name):
             _ptr(w.scales, _BF, f"{name}.scales", E * (K // w.group) * N))
 
 
-def moed_forward_q4(shape, x, w_router, b_router, w1, w2, y, ids, weights, counts, offsets, perm, slot,
-                    ws, stream=None):
-    """moed_forward with w1, w2 as :class:`Q4Weights` of one group size."""
+def _q4_layer_ptrs(shape, w1, w2):
+    """(w1, w1_scales, w2, w2_scales) pointers of a layer's :class:`Q4Weights`."""
     if w1.group != w2.group:
         raise ValueError(f"w1 has groups of {w1.group} rows, w2 of {w2.group}")
     f1 = 2 * shape.F if shape.expert_act else shape.F
-    q = _q4_ptrs(w1, shape.E, shape.H, f1, "w1") + _q4_ptrs(w2, shape.E, shape.F, shape.H, "w2")
+    return _q4_ptrs(w1, shape.E, shape.H, f1, "w1") + _q4_ptrs(w2, shape.E, shape.F, shape.H, "w2")
+
+
+def moed_forward_q4(shape, x, w_router, b_router, w1, w2, y, ids, weights, counts, offsets, perm, slot,
+                    ws, stream=None):
+    """moed_forward with w1, w2 as :class:`Q4Weights` of one group size."""
+    q = _q4_layer_ptrs(shape, w1, w2)
     specs = _forward_specs(x, w_router, b_router, None, None, y, ids, weights, counts, offsets, perm, slot)
     p = _args(shape, *specs)
     _check(_lib().moed_forward_q4(ctypes.byref(shape), w1.group, *p[:3], *q, *p[5:], *_ws(ws),
                                   _stream(stream)))
+
+
+def moed_selftest_wait_timeout(shape, x, w_router, b_router, w1, w2, y, ids, weights, counts, offsets, perm,
+                               slot, ws, limit_ns: int, stream=None):
+    """The layer (w1, w2 tensors or :class:`Q4Weights`) with waits that run out."""
+    q4 = isinstance(w1, Q4Weights)
+    specs = _forward_specs(x, w_router, b_router, None if q4 else w1, None if q4 else w2, y, ids, weights,
+                           counts, offsets, perm, slot)
+    p = _args(shape, *specs)
+    q = _q4_layer_ptrs(shape, w1, w2) if q4 else (p[3], None, p[4], None)
+    _check(_lib().moed_selftest_wait_timeout(ctypes.byref(shape), w1.group if q4 else 0, *p[:3], *q, *p[5:],
+                                             *_ws(ws), int(limit_ns), _stream(stream)))
 
 
 def moed_matvec_q4_workspace_size(rows: int, n_segments: int, K: int, N: int) -> int:

@@ -1,10 +1,10 @@
 """The decode operators on the GPU where other tests do not go: batches whose
-cluster ranks have no rows of H."""
+cluster ranks have no rows of H, waits that run out."""
 import pytest
 import torch
 
 import mixture_experts_layer_12_gb300 as moe
-from test_decode_gpu import check_layer, make_layer
+from test_decode_gpu import check_layer, check_routing, make_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +27,36 @@ def test_ranks_without_rows_of_h(H, T, E, k):
     for _ in range(50):
         y = layer(x)
         assert torch.equal(y, first) and torch.equal(layer.routing.ids, ids)
+
+
+@pytest.mark.parametrize("limit_ns", [2_000_000, 1000])
+@pytest.mark.parametrize("T,H,F,E,k,act,group", [
+    (1, 256, 256, 8, 2, "gelu", 0),          # h read by whoever needs it
+    (16, 4096, 4096, 4, 1, "gelu", 0),       # h copied, shared items by their first CTA
+    (64, 4096, 4096, 4, 2, "gelu", 0),       # h copied, shared items by all CTAs
+    (16, 1024, 1408, 16, 4, "swiglu", 0),    # gate's and up projection's chunks in turn
+    (1, 512, 768, 8, 2, "swiglu", 128),
+    (6, 4096, 4096, 8, 2, "gelu", 64),
+    (64, 2048, 2048, 4, 2, "swiglu", 32),    # two stages, one per consumer group
+])
+def test_waits_that_run_out(T, H, F, E, k, act, group, limit_ns):
+    """Every CTA gives up and leaves, the status says so, the routing is the
+    layer's, and the next call with the same workspace is right.  With 1 us
+    the waits for the weights run out too."""
+    x, layer = make_layer(T + H + F, T, H, F, E, k, act, group=group)
+    want = check_layer(x, layer).clone()
+    r, ws = layer.routing, layer.ws
+    s = moe.make_shape(T, H, F, E, k, act=act)
+    for t in (r.ids, r.weights, r.counts, r.offsets, r.perm, r.slot):
+        t.zero_()
+    y = torch.empty_like(x)
+    for _ in range(3):
+        moe.moed_selftest_wait_timeout(s, x, layer.w_router, None, layer.w1, layer.w2, y, r.ids, r.weights,
+                                       r.counts, r.offsets, r.perm, r.slot, ws, limit_ns)
+        with pytest.raises(moe.MoEError) as e:
+            moe.moe_get_device_status(ws)
+        assert e.value.code == moe.MOE_ERR_TIMEOUT
+        check_routing(x, layer, r)
+        for _ in range(2):
+            assert torch.equal(layer(x), want)
+            assert layer.ws is ws and moe.moe_get_device_status(ws) == 0
