@@ -102,7 +102,8 @@ MOE_API size_t moed_matvec_q4_workspace_size(int32_t rows, int32_t n_segments, i
  * seg_offsets[i+1] (as in moe_expert_ffn); fp32 sums, y rounded to bf16 once.
  *   x [rows, K] bf16, codes [E, K/8, N], scales [E, K/group, N],
  *   seg_offsets [n_segments+1] int32 (device, non-decreasing, at most rows;
- *   clamped to [0, rows], never followed out of range) or NULL with
+ *   clamped to [0, rows] and to the largest before them, never followed out of
+ *   range: a row belongs to the first segment that reaches it) or NULL with
  *   n_segments = 1: all rows, 1 <= n_segments <= 256, y [rows, N] bf16, which
  *   must not overlap x; rows of y outside every segment are not written.
  * rows = 0 enqueues nothing but the status clear.

@@ -457,19 +457,30 @@ __global__ void __cluster_dims__(DR_RANKS, 1, 1) __launch_bounds__(DR_THREADS, 1
 
 // Entries of the grouped products: segment i's rows in blocks of row_block.
 __global__ void __launch_bounds__(256) decode_prep_kernel(const DecPrepArgs a) {
-  __shared__ int s_scan[8], s_rows[8];
+  __shared__ int s_scan[8], s_rows[8], s_max[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   pdl_wait();
   for (int i = tid; i < kDecCtrlInts; i += 256) a.ctrl[i] = 0;
-  int o0 = 0, n = 0;
+  // each row belongs to one entry at most, and the entries have room: offsets are
+  // clamped to [0, rows] and to the largest before them (a scan), so that a
+  // decreasing one gives an empty segment
+  int o0 = 0, o1 = 0;
   if (tid < a.n_segments) {
-    // each row belongs to one entry at most: offsets are clamped, and a
-    // decreasing one gives an empty segment
     o0 = a.seg_offsets ? min(max(__ldg(a.seg_offsets + tid), 0), a.rows) : 0;
-    const int o1 = a.seg_offsets ? min(max(__ldg(a.seg_offsets + tid + 1), 0), a.rows) : a.rows;
-    n = max(o1 - o0, 0);
+    o1 = a.seg_offsets ? min(max(__ldg(a.seg_offsets + tid + 1), 0), a.rows) : a.rows;
   }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, o0, off);
+    if (lane >= off) o0 = max(o0, v);
+  }
+  if (lane == 31) s_max[warp] = o0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w)
+    if (w < warp) o0 = max(o0, s_max[w]);
+  const int n = max(o1 - o0, 0);
   const int blocks = (n + a.row_block - 1) / a.row_block;
   int incl = blocks;
 #pragma unroll

@@ -1,10 +1,13 @@
 """The decode operators on the GPU where other tests do not go: batches whose
-cluster ranks have no rows of H, waits that run out."""
+cluster ranks have no rows of H, waits that run out, offsets that decrease."""
+import random
+
 import pytest
 import torch
 
 import mixture_experts_layer_12_gb300 as moe
-from test_decode_gpu import check_layer, check_routing, make_layer
+from test_decode_gpu import (BF, DEV, check_layer, check_matvec, check_routing, gen, make_layer, random_q4,
+                             randn)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +63,23 @@ def test_waits_that_run_out(T, H, F, E, k, act, group, limit_ns):
         for _ in range(2):
             assert torch.equal(layer(x), want)
             assert layer.ws is ws and moe.moe_get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("rows,n_segments,E", [(12, 3, 3), (100, 33, 5), (512, 256, 7), (37, 100, 64), (512, 40, 3)])
+def test_matvec_decreasing_offsets_give_disjoint_segments(rows, n_segments, E):
+    """Offsets against the contract: every row is computed once, by the first
+    segment that reaches it, and rows that none reaches stay."""
+    w = random_q4(gen(rows + E), E, 256, 136, 64)
+    x = randn(gen(rows), rows, 256).to(DEV)
+    rng = random.Random(rows + n_segments)
+    for offsets in ([-5, 4, 2, 1000][:n_segments + 1] + [0, rows] * n_segments,
+                    [rng.randint(-20, rows + 20) for _ in range(n_segments + 1)],
+                    [rows // 3 + rng.randint(-2, 2) + i * rows // (2 * n_segments) for i in range(n_segments + 1)],
+                    [rows] + [0] * n_segments):
+        offsets = offsets[:n_segments + 1]
+        rising = [max(min(max(o, 0), rows) for o in offsets[:i + 1]) for i in range(n_segments + 1)]
+        out = torch.full((rows, 136), 3.0, dtype=BF, device=DEV)
+        moe.matvec_q4(x, w, torch.tensor(offsets, dtype=torch.int32, device=DEV), out=out)
+        done = check_matvec(x, w, 64, rising, out)
+        assert done.tolist() == [rising[0] <= r < rising[-1] for r in range(rows)]
+        assert (out[~done.to(DEV)] == 3.0).all()
