@@ -53,6 +53,11 @@ MOE_API size_t moed_workspace_size(const moe_shape* s);
  * weighted sum (moe_forward rounds them to bf16 when k > 1).  h is rounded to
  * bf16.  The result does not depend on how the work is split over the SMs'
  * timing: the same inputs give the same bits.
+ * Experts may be masked by a bias of -inf (a NaN logit counts as one): they
+ * are chosen after all others, lower index first, with weight 0.  Where that
+ * leaves a token no expert the softmax has no value: it goes to experts
+ * 0 .. k-1, and its weights and its row of y are NaN.  All of this is
+ * moe_forward's too.  Non-finite values of x stay in their token's row.
  * Calls on different streams may overlap if they share no workspace and no
  * output; host threads that call on one stream with one workspace have to
  * take turns (a call enqueues two kernels).  y may be x.  T = 0 clears counts / offsets, as moe_forward does.

@@ -1,10 +1,13 @@
 """The decode operators on the GPU where other tests do not go: batches whose
-cluster ranks have no rows of H, waits that run out, offsets that decrease."""
+cluster ranks have no rows of H, waits that run out, offsets that decrease,
+rows whose mask leaves few experts or none."""
+import math
 import random
 
 import pytest
 import torch
 
+import decode_reference as ref
 import mixture_experts_layer_12_gb300 as moe
 from test_decode_gpu import (BF, DEV, check_layer, check_matvec, check_routing, gen, make_layer, random_q4,
                              randn)
@@ -83,3 +86,73 @@ def test_matvec_decreasing_offsets_give_disjoint_segments(rows, n_segments, E):
         done = check_matvec(x, w, 64, rising, out)
         assert done.tolist() == [rising[0] <= r < rising[-1] for r in range(rows)]
         assert (out[~done.to(DEV)] == 3.0).all()
+
+
+def masked_layer(T, E, k, gating, bias, group=0):
+    x, layer = make_layer(T + E + k, T, 128, 64, E, k, gating=gating, group=group)
+    return x, moe.MoEDecodeLayer(layer.w_router, layer.w1, layer.w2, k, bias=bias.to(DEV), gating=gating)
+
+
+def same_as_forward(x, layer):
+    """The routing, NaN included, is that of moe_forward."""
+    full = moe.MoELayer(layer.w_router, layer.w1, layer.w2, layer.k, bias=layer.bias, gating=layer.gating)
+    want = full(x)
+    r, f = layer.routing, full.routing
+    for n in ("ids", "counts", "offsets", "slot", "perm"):
+        assert torch.equal(getattr(r, n), getattr(f, n)), n
+    torch.testing.assert_close(r.weights, f.weights, rtol=0, atol=1e-5, equal_nan=True)
+    return want
+
+
+@pytest.mark.parametrize("gating", [0, 1, 2])
+@pytest.mark.parametrize("T,E,k,allowed", [(1, 8, 4, [3]), (5, 40, 8, [39, 7]), (9, 8, 8, [1, 2, 5]), (64, 6, 5, [4])])
+def test_more_choices_than_experts_that_are_not_masked(T, E, k, allowed, gating):
+    """Masked experts come last, in index order and with weight 0."""
+    bias = torch.full((E,), -math.inf)
+    bias[allowed] = 0.0
+    x, layer = masked_layer(T, E, k, gating, bias)
+    y = layer(x)
+    r = layer.routing
+    n = len(allowed)
+    masked = [e for e in range(E) if e not in allowed][:k - n]
+    for row in r.ids.tolist():
+        assert sorted(row[:n]) == sorted(allowed) and row[n:] == masked
+    assert (r.weights[:, n:] == 0).all() and ((r.weights[:, :n].sum(1) - 1).abs() <= 1e-5).all()
+    same_as_forward(x, layer)
+    # the sum over the allowed experts alone: masked ones add 0 times a finite row
+    ids = r.ids.cpu().long()
+    lg, _, _ = ref.route(x, layer.w_router, layer.bias, k, gating)
+    want, err = ref.experts(x, lambda e: layer.w1[e].cpu().double(), lambda e: layer.w2[e].cpu().double(), ids,
+                            ref.gate(lg, ids, gating), r.slot.cpu(), "gelu")
+    assert ((y.cpu().double() - want).abs() <= err).all()
+
+
+@pytest.mark.parametrize("gating", [0, 1, 2])
+@pytest.mark.parametrize("T,E,k,group", [(1, 8, 4, 0), (7, 40, 2, 32), (64, 6, 6, 0), (33, 16, 1, 64)])
+def test_no_expert_left(T, E, k, group, gating):
+    """Every expert masked: experts 0..k-1, a valid dispatch, NaN weights and y."""
+    x, layer = masked_layer(T, E, k, gating, torch.full((E,), -math.inf), group)
+    y = layer(x)
+    r = layer.routing
+    ids = torch.arange(k).expand(T, k)
+    assert torch.equal(r.ids.cpu().long(), ids)
+    assert torch.isnan(r.weights).all() and torch.isnan(y).all()
+    for got, want in zip((r.counts, r.offsets, r.perm, r.slot), ref.dispatch(ids, E, T * k)):
+        assert torch.equal(got.cpu(), want)
+    assert moe.moe_get_device_status(layer.ws) == 0
+    if not group:
+        assert torch.isnan(same_as_forward(x, layer)).all()
+
+
+@pytest.mark.parametrize("gating", [0, 1, 2])
+def test_lowest_value_masks_are_no_infinities(gating):
+    """Every expert at the type's lowest value: the logits round to it, all are
+    equal, and the weights are those of equal logits."""
+    low = torch.finfo(torch.float32).min
+    x, layer = masked_layer(3, 8, 3, gating, torch.full((8,), low))
+    y = layer(x)
+    r = layer.routing
+    assert r.ids.tolist() == [[0, 1, 2]] * 3
+    want = 1 / 8 if gating == 1 else 1 / 3
+    assert ((r.weights - want).abs() <= 1e-6).all() and torch.isfinite(y).all()
+    same_as_forward(x, layer)
