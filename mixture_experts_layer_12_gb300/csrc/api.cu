@@ -19,7 +19,6 @@ cudaError_t small_gemm_set_attributes();
 cudaError_t router_set_attributes();
 cudaError_t route_fused_set_attributes();
 cudaError_t dispatch_combine_set_attributes();
-cudaError_t decode_set_attributes();
 }  // namespace moe
 
 using namespace moe;
@@ -50,7 +49,6 @@ namespace {
 
 // ---------------------------------------------------------------- device --
 
-constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   bool ready;
   int sms;
@@ -83,7 +81,6 @@ int device_setup(int* sms) {
     if ((e = small_gemm_set_attributes()) != cudaSuccess) return cuda_fail(e, "gemm attributes");
     if ((e = dispatch_combine_set_attributes()) != cudaSuccess)
       return cuda_fail(e, "dispatch/combine attributes");
-    if ((e = decode_set_attributes()) != cudaSuccess) return cuda_fail(e, "decode attributes");
     if (!g_encode) {
       void* fn = nullptr;
       cudaDriverEntryPointQueryResult q;

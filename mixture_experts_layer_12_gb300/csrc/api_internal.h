@@ -15,8 +15,10 @@ namespace moe {
 int fail(int code, const char* fmt, ...);
 int cuda_fail(cudaError_t e, const char* what);
 
-// Sets the current device up on its first use (kernel attributes, the
-// tensor-map encoder) and yields its SM count.
+constexpr int kMaxDevices = 64;
+
+// Sets the current device up on its first use (attributes of moe.h's kernels,
+// the tensor-map encoder) and yields its SM count.
 int device_setup(int* sms);
 
 // Tensor map of `rank` dimensions, zero fill out of bounds.  Needs a

@@ -1,5 +1,8 @@
-"""What the decode operators' self-test refuses, before the library touches CUDA."""
+"""What the decode operators' self-test refuses, before the library touches CUDA,
+and what the other entry points load of them."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -40,3 +43,14 @@ def test_wait_selftest_refuses_null_and_small_buffers(lib):
             moe.MOE_ERR_INVALID_ARG, i
     assert lib.moed_selftest_wait_timeout(ctypes.byref(s), 0, *good, need - 1, 10 ** 6, None) == \
         moe.MOE_ERR_INVALID_ARG
+
+
+def test_other_entry_points_do_not_load_the_decode_kernels(lib):
+    """What sets a device up for moe.h's calls refers to nothing of the decode
+    operators: their kernels' code is loaded by their own first call."""
+    objs = [s.replace(".cu", ".o") for s in moe_build.SOURCES if not s.startswith(("decode", "q4"))]
+    assert "api.o" in objs
+    for o in objs:
+        path = os.path.join(moe_build.BUILD_DIR, o)
+        syms = subprocess.run(["nm", "-u", path], capture_output=True, text=True, check=True).stdout
+        assert "decode" not in syms and "q4" not in syms, o
