@@ -342,7 +342,8 @@ class MoEDecodeLayer:
     """A layer's weights for decode steps of at most MOED_MAX_TOKENS tokens:
     w1 / w2 as bf16 tensors ([E, H, F] or [E, H, 2F] for "swiglu", [E, F, H])
     or as :class:`Q4Weights`.  Calling it runs moed_forward(_q4) on the current
-    stream (or `stream`) and returns a new y [T, H].
+    stream (or `stream`) and returns a new y [T, H].  What it was made with
+    cannot be set later.
 
     ``routing`` and ``ws`` are those of the last call; the next call with as
     many tokens on the same stream writes the routing again, and the next call
@@ -352,14 +353,14 @@ class MoEDecodeLayer:
 
     def __init__(self, w_router, w1, w2, k: int, bias=None, capacity_factor=None,
                  gating: int = MOE_GATE_TOPK_SOFTMAX, act: str = "gelu"):
-        self.q4 = isinstance(w1, Q4Weights)
+        self._q4 = isinstance(w1, Q4Weights)
         if self.q4 != isinstance(w2, Q4Weights):
             raise TypeError("w1 and w2 must both be tensors or both Q4Weights")
         if not self.q4 and w2.dim() != 3:
             raise ValueError(f"w2 must be [E, F, H], got {tuple(w2.shape)}")
-        self.E, self.F, self.H = (w2.E, w2.K, w2.N) if self.q4 else w2.shape
-        self.k, self.act = int(k), act
-        self.capacity_factor, self.gating = capacity_factor, int(gating)
+        self._E, self._F, self._H = (w2.E, w2.K, w2.N) if self.q4 else w2.shape
+        self._k, self._act = int(k), act
+        self._capacity_factor, self._gating = capacity_factor, int(gating)
         f1 = 2 * self.F if act == "swiglu" else self.F
         if self.q4:
             if (w1.E, w1.K, w1.N) != (self.E, self.H, f1) or w1.group != w2.group:
@@ -395,11 +396,20 @@ class MoEDecodeLayer:
         return MoEDecodeLayer, (self._w_router, self._w1, self._w2, self.k, self._bias, self.capacity_factor,
                                 self.gating, self.act)
 
-    # fixed for the layer's life: the calls use their addresses
+    # fixed for the layer's life: the calls use the tensors' addresses and keep the
+    # shape of every batch size they have seen
     w_router = property(lambda self: self._w_router)
     w1 = property(lambda self: self._w1)
     w2 = property(lambda self: self._w2)
     bias = property(lambda self: self._bias)
+    q4 = property(lambda self: self._q4)
+    E = property(lambda self: self._E)
+    F = property(lambda self: self._F)
+    H = property(lambda self: self._H)
+    k = property(lambda self: self._k)
+    act = property(lambda self: self._act)
+    capacity_factor = property(lambda self: self._capacity_factor)
+    gating = property(lambda self: self._gating)
 
     def _shape(self, T: int) -> moe_shape:
         s = make_shape(T, self.H, self.F, self.E, self.k, self.capacity_factor, self.gating, self.act)
@@ -411,13 +421,13 @@ class MoEDecodeLayer:
             with _on(stream):
                 return self(x)
         dev, raw = _here()
-        if x.dim() != 2 or x.shape[1] != self.H:
+        if x.dim() != 2 or x.shape[1] != self._H:
             raise ValueError(f"x must be [T, {self.H}], got {tuple(x.shape)}")
         if self._index != dev:
             raise ValueError(f"the layer's weights are on {self._device}, the current device is cuda:{dev}")
         T = x.shape[0]
-        src = _addr(x, _BF, "x", T * self.H, dev)
-        y = torch.empty((T, self.H), dtype=_BF, device=self._device)
+        src = _addr(x, _BF, "x", T * self._H, dev)
+        y = torch.empty((T, self._H), dtype=_BF, device=self._device)
         capturing = torch.cuda.is_current_stream_capturing()
         with self._lock:
             b = _Buffers(self, T, raw, None) if capturing else self._buffers.get((T, raw)) or self._new(T, raw)

@@ -54,3 +54,11 @@ def test_other_entry_points_do_not_load_the_decode_kernels(lib):
         path = os.path.join(moe_build.BUILD_DIR, o)
         syms = subprocess.run(["nm", "-u", path], capture_output=True, text=True, check=True).stdout
         assert "decode" not in syms and "q4" not in syms, o
+
+
+@pytest.mark.parametrize("name", ["w_router", "w1", "w2", "bias", "q4", "E", "F", "H", "k", "act", "capacity_factor",
+                                  "gating"])
+def test_what_a_layer_was_made_with_cannot_be_set(name):
+    """It would hold for batch sizes not seen yet and be ignored for the others."""
+    with pytest.raises(AttributeError):
+        setattr(object.__new__(moe.MoEDecodeLayer), name, 1)
