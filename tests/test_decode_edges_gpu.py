@@ -1,6 +1,6 @@
 """The decode operators on the GPU where other tests do not go: batches whose
 cluster ranks have no rows of H, waits that run out, offsets that decrease,
-rows whose mask leaves few experts or none."""
+rows whose mask leaves few experts or none, the calls by their C names."""
 import math
 import random
 
@@ -156,3 +156,68 @@ def test_lowest_value_masks_are_no_infinities(gating):
     want = 1 / 8 if gating == 1 else 1 / 3
     assert ((r.weights - want).abs() <= 1e-6).all() and torch.isfinite(y).all()
     same_as_forward(x, layer)
+
+
+def buffers(layer, T):
+    s = moe.make_shape(T, layer.H, layer.F, layer.E, layer.k, layer.capacity_factor, layer.gating, layer.act)
+    r = moe.alloc_routing(T, layer.E, layer.k, DEV)
+    ws = torch.empty(moe.moed_workspace_size(s), dtype=torch.uint8, device=DEV)
+    return s, (r.ids, r.weights, r.counts, r.offsets, r.perm, r.slot), ws
+
+
+@pytest.mark.parametrize("T,H,F,E,k,act,group", [
+    (1, 256, 256, 8, 2, "gelu", 0), (40, 512, 384, 6, 3, "swiglu", 0), (16, 1024, 1408, 16, 4, "swiglu", 0),
+    (9, 256, 640, 64, 4, "swiglu", 64), (64, 2048, 2048, 4, 2, "gelu", 32)])
+def test_y_may_be_x(T, H, F, E, k, act, group):
+    """moed_forward and moed_forward_q4 by name, written over their input, on
+    another stream, eager and replayed."""
+    x, layer = make_layer(T + H + E, T, H, F, E, k, act, bias=True, group=group)
+    want = check_layer(x, layer).clone()
+    s, r, ws = buffers(layer, T)
+    fwd = moe.moed_forward_q4 if group else moe.moed_forward
+    call = lambda v, st: fwd(s, v, layer.w_router, layer.bias, layer.w1, layer.w2, v, *r, ws, st)  # noqa: E731
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        with torch.cuda.stream(st):
+            v = x.clone()
+        call(v, st)
+        st.synchronize()
+        assert torch.equal(v, want) and moe.moe_get_device_status(ws, st) == 0
+    static, g = x.clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        call(static, st)
+    for _ in range(3):
+        static.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(static, want)
+    for got, ref_ in zip(r, (layer.routing.ids, layer.routing.weights, layer.routing.counts, layer.routing.offsets,
+                             layer.routing.perm, layer.routing.slot)):
+        assert torch.equal(got, ref_)
+
+
+def test_products_and_conversions_by_name():
+    g = gen(71)
+    w = randn(g, 3, 256, 72).to(DEV)
+    q = moe.quantize_q4(w, 64)
+    codes, scales = torch.empty_like(q.codes), torch.empty_like(q.scales)
+    moe.moed_quantize_q4(w, codes, scales, 64)
+    assert torch.equal(codes, q.codes) and torch.equal(scales.view(torch.int16), q.scales.view(torch.int16))
+    out = torch.empty_like(w)
+    moe.moed_dequantize_q4(q, out)
+    assert torch.equal(out, moe.dequantize_q4(q))
+    x = randn(g, 21, 256).to(DEV)
+    offsets = [0, 4, 4, 21]
+    seg = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+    y = torch.empty(21, 72, dtype=BF, device=DEV)
+    ws = torch.empty(moe.moed_matvec_q4_workspace_size(21, 3, 256, 72), dtype=torch.uint8, device=DEV)
+    moe.moed_matvec_q4(x, q, seg, y, ws)
+    check_matvec(x, q, 64, offsets, y)
+    assert torch.equal(y, moe.matvec_q4(x, q, seg)) and moe.moe_get_device_status(ws) == 0
+    # no offsets: one segment of all rows, the first matrix
+    with pytest.raises(moe.MoEError, match="moed_matvec_q4_workspace_size"):
+        moe.moed_matvec_q4(x, q, None, y, ws)       # one segment of 21 rows needs more than three
+    ws = torch.empty(moe.moed_matvec_q4_workspace_size(21, 1, 256, 72), dtype=torch.uint8, device=DEV)
+    moe.moed_matvec_q4(x, q, None, y, ws)
+    check_matvec(x, q, 64, [0, 21], y)
