@@ -2,7 +2,10 @@
 cluster ranks have no rows of H, waits that run out, offsets that decrease,
 rows whose mask leaves few experts or none, the calls by their C names."""
 import math
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -13,6 +16,8 @@ from test_decode_gpu import (BF, DEV, check_layer, check_matvec, check_routing, 
                              randn)
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -221,3 +226,45 @@ def test_products_and_conversions_by_name():
     ws = torch.empty(moe.moed_matvec_q4_workspace_size(21, 1, 256, 72), dtype=torch.uint8, device=DEV)
     moe.moed_matvec_q4(x, q, None, y, ws)
     check_matvec(x, q, 64, [0, 21], y)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import mixture_experts_layer_12_gb300 as moe
+bf = dict(dtype=torch.bfloat16, device="cuda")
+g = torch.Generator(device="cuda").manual_seed(1)
+rnd = lambda *s: (torch.randn(*s, generator=g, device="cuda") / 16).bfloat16()
+w1, w2, wr = rnd(8, 256, 384), rnd(8, 384, 256), rnd(256, 8)
+x = rnd(5, 256)
+seg = torch.tensor([0, 1, 1, 2, 3, 3, 4, 4, 5], dtype=torch.int32, device="cuda")
+layer = moe.MoEDecodeLayer(wr, w1, w2, 2)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = layer(x)
+    none = layer(x[:0])
+    q = moe.quantize_q4(w1, 64)
+    back = moe.dequantize_q4(q)
+    z = moe.matvec_q4(x, q, seg)
+    z0 = moe.matvec_q4(x[:0], q, seg)
+for _ in range(2):
+    for t in (y, q.codes, q.scales, back, z):
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    e = moe.quantize_q4(w1, 64)
+    assert torch.equal(y, layer(x)) and torch.equal(q.codes, e.codes) and torch.equal(q.scales, e.scales)
+    assert torch.equal(back, moe.dequantize_q4(e)) and torch.equal(z, moe.matvec_q4(x, e, seg))
+    assert y.abs().sum() > 0 and z.abs().sum() > 0
+print("ok")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Nothing of the library has run before the capture: kernels are loaded and
+    set up inside it."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=ROOT)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
