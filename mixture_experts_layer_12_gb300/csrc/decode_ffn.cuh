@@ -33,11 +33,13 @@
 //     come out of the 128-byte-swizzled stage by ldmatrix.trans.  4-bit codes
 //     are turned into bf16 in registers; the products are exact in fp32, 32
 //     rows of K are summed in fp32 and multiplied by their scale in fp32.
-//   tcgen05 is not used: it would want the 4-bit weights expanded to bf16 in
-//   shared memory (94 bytes per clock written and read where the SM's shared
-//   memory moves 128), and for bf16 the stream, not the multiply, is the
-//   bound: one m16n8k16 per 256 weights is a tenth of the tensor rate at 8
-//   rows.
+//   tcgen05 is not used: for bf16 the stream, not the multiply, is the bound (one
+//   m16n8k16 per 256 weights is a tenth of the tensor rate at 8 rows), and 4-bit
+//   weights expanded to bf16 in shared memory would write and read 94 bytes per
+//   clock there, of the 128 it moves.  Both hold for few rows: from 17 rows of an
+//   expert on, with 4 bits, the products and their scaling take more clocks than
+//   the memory (860 and 1560 a chunk for 16 and 32 rows, where it takes 700).
+//   Weights unpacked into tensor memory as the A operand have not been tried.
 //   * Between the products h goes through memory.  An item shared by several
 //     CTAs is put together by its first CTA, whose last it is, while the later
 //     ones begin with it and have counted in by then; by all CTAs, after a grid
@@ -49,9 +51,9 @@
 // guarantees; they and every other wait are bounded.
 // Measured with the first kernel, GPU time of a call: one token, 8 experts of 4096 x
 // 14336, 2 of them: 80 us in bf16 (5.9 TB/s, 0.87 of the copy bandwidth), 47 us gated
-// in 4 bits; 16 tokens in 4 bits 97 us (4.9 TB/s); 64 experts of 2048 x 1408, 4 of
-// them, gated: 25 us in bf16, of which 10 are the weights; 4096 x 14336 in 4 bits
-// times a row: 12.4 us, 4.5 of them the weights.  What is left beside the stream is a
+// in 4 bits; 16 tokens in 4 bits 97 us (4.9 TB/s), 64 tokens 231; 64 experts of 2048 x
+// 1408, 4 of them, gated: 25 us in bf16, of which 10 are the weights; 4096 x 14336 in
+// 4 bits times a row: 12.4 us, 4.5 of them the weights.  What is left beside the stream is a
 // chain of trips to memory: the list (1 us) and the first chunk (2 us), partial tiles
 // and h between the products (4-5 us) and the combine (2-3 us).
 #pragma once
@@ -253,7 +255,10 @@ __device__ __forceinline__ void add4(float4& a, const float4 b) {
 }
 
 // 4 columns of the first product (and of the up projection), activated and rounded
-// to bf16
+// to bf16: h is the operand of the second product, whose weights are bf16 or exact in
+// it, and moe_forward rounds it too; two halves of it would double that product.
+// It is most of what a layer's y is off beyond its own rounding (2.3e-3 of y against 64
+// bits, 1.7e-3 from the rounding of y).
 __device__ __forceinline__ uint2 activated(int act, float4 z, const float4& u) {
   if (act == kDecSwiGLU) {
     z = make_float4(dec_silu(z.x) * u.x, dec_silu(z.y) * u.y, dec_silu(z.z) * u.z, dec_silu(z.w) * u.w);
@@ -470,8 +475,10 @@ struct Cfg {
   static constexpr int RED = KG * RED_GROUP * 4;
   static constexpr int CTRL = 12 * 1024;
   static constexpr int SPACE = DF_SMEM - 1024 - RED - CTRL;  // for the rings
-  // reads of rows past an entry's last stay inside: RED and CTRL follow the rows
-  static_assert(RED + CTRL >= 8 * PITCH, "room behind the rows");
+  // Reads of rows past an entry's last stay inside: RED and CTRL follow the rows.  An
+  // entry is multiplied in tiles of 8, 16, 32 or 64 rows, of which it has more than
+  // half, or has 1 of 8.
+  static_assert(RED + CTRL >= (NT == 1 ? 7 : 4 * NT - 1) * PITCH, "room behind the rows");
   static_assert(SPACE >= 2 * KG * W_STAGE, "weight ring");
 };
 

@@ -61,7 +61,7 @@ struct DecPrepArgs {
 };
 cudaError_t launch_decode_prep(const DecPrepArgs& a, cudaStream_t st);
 
-// ---- kernel 2: the weight stream (decode_ffn.cu)
+// ---- kernel 2: the weight stream (decode_ffn.cuh)
 constexpr int kDecNone = 0;    // y = x W (grouped products)
 constexpr int kDecGelu = 1;    // the layer, GELU experts
 constexpr int kDecSwiGLU = 2;  // the layer, gated experts

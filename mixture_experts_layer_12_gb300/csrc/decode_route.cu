@@ -14,7 +14,9 @@
 // order (warps of a CTA, then ranks 0..7).  Every rank stores its partial
 // logits into the shared memory of the rank that owns the token (rank 0 owns
 // all of up to 8 tokens, else t mod 8), so that the owner reads its own
-// memory after the barrier.  A warp per token then takes the k largest, one
+// memory after the barrier; a cluster barrier that ends before the first of these
+// stores says that all ranks run.  Logits are fp32, as moe_forward's: two that are
+// closer than the rounding of such a sum may be chosen in either order.  A warp per token then takes the k largest, one
 // per round (two warp-wide integer reductions: the largest, then the lowest
 // index that has it).  This code runs once per launch and comes cold from
 // memory, so its size is its cost: the loops stay loops.  Rank 0 then holds
