@@ -87,8 +87,10 @@ MOE_API int moed_forward_q4(const moe_shape* s, int32_t group, const uint16_t* x
  * else as moed_forward_q4) with waits of at most limit_ns nanoseconds
  * (1e3 .. 1e9), between its products for one CTA more than there are.  Those
  * waits run out, every CTA gives up and leaves, and MOE_DEV_TIMEOUT is set in
- * the workspace's status word.  The routing outputs are the layer's, y is void; the next call
- * with the workspace is an ordinary one.  Nothing traps or hangs.
+ * the workspace's status word (not in a call without rows, which does not
+ * wait: T = 0, or every assignment dropped).  The routing outputs are the
+ * layer's, y is void; the next call with the workspace is an ordinary one.
+ * Nothing traps or hangs.
  */
 MOE_API int moed_selftest_wait_timeout(const moe_shape* s, int32_t group, const uint16_t* x,
                                        const uint16_t* w_router, const float* b_router,
