@@ -453,3 +453,11 @@ from .decode import (DECODE_EXPORTS, MOED_MAX_ROWS, MOED_MAX_TOKENS, MoEDecodeLa
 __all__ += [n for n in DECODE_EXPORTS] + ["DECODE_EXPORTS", "MOED_MAX_ROWS", "MOED_MAX_TOKENS",
                                           "MoEDecodeLayer", "Q4Weights", "dequantize_q4",
                                           "matvec_q4", "quantize_q4"]
+
+from .train import (TRAIN_EXPORTS, A8Tensor, Gradients, MoETrainLayer, Saved, combine_backward,  # noqa: E402
+                    dequantize_a8, dispatch_rows_backward, expert_ffn, expert_ffn_backward, quantize_a8,
+                    route_backward, router_probs, train_status)
+
+__all__ += ["TRAIN_EXPORTS", "A8Tensor", "Gradients", "MoETrainLayer", "Saved", "combine_backward",
+            "dequantize_a8", "dispatch_rows_backward", "expert_ffn", "expert_ffn_backward", "quantize_a8",
+            "route_backward", "router_probs", "train_status"]

@@ -1,7 +1,8 @@
 """Builds libmoe.so in-tree with nvcc for sm_103a (no torch extension, no cmake).
 
 Each .cu translation unit compiles in parallel; the shared library links the
-CUDA runtime statically and exports only the C ABI of include/moe.h and moe_decode.h.
+CUDA runtime statically and exports only the C ABI of include/moe.h,
+moe_decode.h and moe_train.h.
 """
 from __future__ import annotations
 
@@ -19,10 +20,11 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
 SOURCES = ["api.cu", "router.cu", "route_fused.cu", "dispatch_combine.cu", "ffn_gemm.cu",
            "ffn_gemm_small.cu", "decode_api.cu", "decode_route.cu", "decode_ffn_bf16.cu", "decode_ffn_pair.cu",
-           "decode_ffn_q4_32.cu", "decode_ffn_q4_64.cu", "decode_ffn_q4_128.cu", "q4.cu"]
+           "decode_ffn_q4_32.cu", "decode_ffn_q4_64.cu", "decode_ffn_q4_128.cu", "q4.cu",
+           "train_api.cu", "train_gemm_fwd.cu", "train_gemm_bwd.cu", "train_gemm_wgrad.cu", "train_rows.cu"]
 HEADERS = ["tc_common.cuh", "moe_internal.h", "api_internal.h", "decode_internal.h", "decode_ffn.cuh",
-           "route_topk.cuh"]
-INCLUDES = ["moe.h", "moe_decode.h"]
+           "route_topk.cuh", "train_internal.h", "train_seg.cuh", "train_gemm.cuh"]
+INCLUDES = ["moe.h", "moe_decode.h", "moe_train.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,744 @@
+// train_api.cu -- the C ABI declared in include/moe_train.h: argument checks,
+// workspace layouts, tensor maps and the launches of each call on the caller's
+// stream.  No allocation and no host synchronisation.
+#include <mutex>
+
+#include "api_internal.h"
+#include "moe_train.h"
+#include "train_internal.h"
+
+using namespace moe;
+
+namespace {
+
+std::mutex g_mu;
+bool g_ready[kMaxDevices];
+
+// device_setup() and, on a device's first use here, the attributes of these
+// kernels (callers of the other entry points do not load them).
+int train_setup(int* sms) {
+  int rc = device_setup(sms);
+  if (rc != MOE_OK) return rc;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_ready[dev]) {
+    if ((e = train_gemm_set_attributes()) != cudaSuccess) return cuda_fail(e, "training attributes");
+    g_ready[dev] = true;
+  }
+  return MOE_OK;
+}
+
+#define CUDA_TRY(call, what)                          \
+  do {                                                \
+    const cudaError_t err_ = (call);                  \
+    if (err_ != cudaSuccess) return cuda_fail(err_, what); \
+  } while (0)
+#define TRY(call)                 \
+  do {                            \
+    const int rc_ = (call);       \
+    if (rc_ != MOE_OK) return rc_; \
+  } while (0)
+
+size_t up(size_t v) { return (v + 1023) / 1024 * 1024; }
+
+bool gated(const moe_shape* s) { return s->expert_act == MOE_EXPERT_SWIGLU; }
+int halves(const moe_shape* s) { return gated(s) ? 2 : 1; }
+size_t rows_of(const moe_shape* s) { return (size_t)s->T * s->k; }
+int ep_of(const moe_shape* s) { return (s->E + 7) / 8 * 8; }
+size_t pad_of(const moe_shape* s) { return padded_rows_cap(rows_of(s), s->E); }
+
+// Regions of a workspace, handed out one after the other.
+struct Carve {
+  char* base;
+  size_t used = 0;
+  explicit Carve(void* p) : base(static_cast<char*>(p)) {}
+  template <typename T>
+  T* take(size_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += up(n * sizeof(T));
+    return p;
+  }
+};
+
+int bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint32_t* box,
+             const char* what) {
+  uint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
+  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims,
+                       strides, box, what);
+}
+int map_rows(CUtensorMap* m, const void* base, size_t cols, size_t rows, uint32_t box_rows, const char* what) {
+  const uint64_t dims[2] = {cols, rows};
+  const uint32_t box[2] = {64, box_rows};
+  return bf16_map(m, base, 2, dims, box, what);
+}
+int map_weights(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t n, uint32_t box_rows,
+                const char* what) {
+  const uint64_t dims[3] = {cols, rows, n};
+  const uint32_t box[3] = {64, box_rows, 1};
+  return bf16_map(m, base, 3, dims, box, what);
+}
+
+SegArgs segments(const moe_shape* s, const int32_t* offsets) {
+  SegArgs g;
+  g.offsets = offsets;
+  g.E = s->E;
+  g.rows = (int)rows_of(s);
+  g.rows_pad = (int)pad_of(s);
+  g.chunk = 0;
+  return g;
+}
+// `rows` rows in chunks of `chunk`, not padded
+SegArgs chunks(int rows, int chunk) {
+  SegArgs g;
+  g.offsets = nullptr;
+  g.E = (rows + chunk - 1) / chunk;
+  g.rows = rows;
+  g.rows_pad = (rows + kSegPad - 1) / kSegPad * kSegPad;
+  g.chunk = chunk;
+  return g;
+}
+TrainGemmArgs gemm_args(const SegArgs& seg, int M, int N, int K, void* status) {
+  TrainGemmArgs a = {};
+  a.seg = seg;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.status = static_cast<int*>(status);
+  a.wait_limit_ns = kWaitLimitNs;
+  return a;
+}
+int64_t row_tiles(size_t rows, int E, int cols, int per) {
+  return (int64_t)((rows + 255) / 256 + (rows < (size_t)E ? rows : (size_t)E)) * ((cols + per - 1) / per);
+}
+int64_t blocks256(int n) { return ((int64_t)n + 255) / 256; }
+
+// ------------------------------------------------------------------ products --
+
+int fwd_product(const moe_shape* s, int bits, const uint16_t* xp, const uint16_t* w1, const int32_t* offsets,
+                uint16_t* h, void* z, uint8_t* z_scales, const int* merge, void* status, cudaStream_t st) {
+  const size_t rows = rows_of(s);
+  CUtensorMap ta, tb, ta64;
+  TRY(map_rows(&ta, xp, s->H, rows, 128, "xp"));
+  TRY(map_rows(&ta64, xp, s->H, rows, 64, "xp"));
+  TRY(map_weights(&tb, w1, (size_t)s->F * halves(s), s->H, s->E, 64, "W1"));
+  TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->F, s->H, status);
+  a.out = h;
+  a.keep_bits = bits;
+  a.z = z;
+  a.z_scales = z_scales;
+  a.merge_status = merge;
+  CUDA_TRY(launch_train_gemm(gated(s) ? kTrainFwdSwiGLU : kTrainFwdGelu, ta, tb, ta64, a,
+                             row_tiles(rows, s->E, s->F, gated(s) ? 128 : 256), st),
+           "expert GEMM1 launch");
+  return MOE_OK;
+}
+
+// Y = h W2 by the forward's own kernel
+int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, const int32_t* offsets, uint16_t* Y,
+                  void* status, cudaStream_t st) {
+  const size_t rows = rows_of(s);
+  CUtensorMap ta, tb, ta64;
+  TRY(map_rows(&ta, h, s->F, rows, 128, "h"));
+  TRY(map_rows(&ta64, h, s->F, rows, 64, "h"));
+  TRY(map_weights(&tb, w2, s->H, s->F, s->E, 64, "W2"));
+  GemmArgs g = {};
+  g.offsets = offsets;
+  g.E = g.E_w = s->E;
+  g.N = s->H;
+  g.K = s->F;
+  g.out = Y;
+  g.T = s->T;
+  g.splits = 1;
+  g.status = static_cast<int*>(status);
+  g.wait_limit_ns = kWaitLimitNs;
+  const int64_t ub = row_tiles(rows, s->E, s->H, kGemmBN);
+  CUDA_TRY(launch_grouped_gemm(kGemmPlain, ta, tb, ta64, g, (int)(ub < (1 << 30) ? ub : (1 << 30)), st, true),
+           "expert GEMM2 launch");
+  return MOE_OK;
+}
+
+// The experts' gradients from padded xp and dyp; dxp compact, may be dyp.
+struct FfnGrad {
+  int bits;
+  const uint16_t *xp, *dyp, *w1, *w2;
+  const int32_t* offsets;
+  const void* z;
+  const uint8_t* z_scales;
+  const float* w;
+  const int32_t* perm;
+  float* part;
+  uint16_t *hw, *dz, *dxp, *dw1, *dw2;
+};
+int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream_t st) {
+  const size_t rows = rows_of(s), pad = pad_of(s);
+  const int f1 = s->F * halves(s);
+  const SegArgs seg = segments(s, f.offsets);
+  CUtensorMap ta, tb, ta64;
+  // g = dy W2^T; dz, w h, <g, h>
+  TRY(map_rows(&ta, f.dyp, s->H, pad, 128, "dy rows"));
+  TRY(map_rows(&ta64, f.dyp, s->H, pad, 64, "dy rows"));
+  TRY(map_weights(&tb, f.w2, s->H, s->F, s->E, 128, "W2"));
+  TrainGemmArgs a = gemm_args(seg, 0, s->F, s->H, status);
+  a.keep_bits = f.bits;
+  a.z = const_cast<void*>(f.z);
+  a.z_scales = const_cast<uint8_t*>(f.z_scales);
+  a.w = f.w;
+  a.perm = f.perm;
+  a.n_w = (int)rows;
+  a.dz = f.dz;
+  a.hw = f.hw;
+  a.part = f.part;
+  a.units = (s->F + 63) / 64;
+  CUDA_TRY(launch_train_gemm(gated(s) ? kTrainBwdSwiGLU : kTrainBwdGelu, ta, tb, ta64, a,
+                             row_tiles(rows, s->E, s->F, 256), st),
+           "h gradient launch");
+  // dW2 = (w h)^T dy
+  TRY(map_rows(&ta, f.hw, s->F, pad, 64, "w h"));
+  TRY(map_rows(&tb, f.dyp, s->H, pad, 64, "dy rows"));
+  a = gemm_args(seg, s->F, s->H, 0, status);
+  a.out = f.dw2;
+  CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta, a, s->E * blocks256(s->F) * blocks256(s->H), st),
+           "dW2 launch");
+  // dW1 = xp^T dz
+  TRY(map_rows(&ta, f.xp, s->H, pad, 64, "xp"));
+  TRY(map_rows(&tb, f.dz, f1, pad, 64, "dz"));
+  a = gemm_args(seg, s->H, f1, 0, status);
+  a.out = f.dw1;
+  CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta, a, s->E * blocks256(s->H) * blocks256(f1), st),
+           "dW1 launch");
+  // dxp = dz W1^T
+  TRY(map_rows(&ta, f.dz, f1, pad, 128, "dz"));
+  TRY(map_rows(&ta64, f.dz, f1, pad, 64, "dz"));
+  TRY(map_weights(&tb, f.w1, f1, s->H, s->E, 128, "W1"));
+  a = gemm_args(seg, 0, s->H, f1, status);
+  a.out = f.dxp;
+  CUDA_TRY(launch_train_gemm(kTrainRows, ta, tb, ta64, a, row_tiles(rows, s->E, s->H, 256), st),
+           "x gradient launch");
+  return MOE_OK;
+}
+
+// Splits of the router's weight gradient along the tokens: as many as give
+// every CTA pair of the device a tile, but at least 256 tokens each (its fp32
+// partial outputs are written and read again).
+int router_chunk(const moe_shape* s) {
+  const int64_t tiles = blocks256(s->H) * blocks256(2 * ep_of(s));
+  int64_t S = 76 / tiles;
+  if (S > s->T / 256) S = s->T / 256;
+  if (S < 1) S = 1;
+  if (S > kMaxExperts) S = kMaxExperts;
+  const int64_t c = (s->T + S - 1) / S;
+  return (int)((c + 63) / 64 * 64);
+}
+int router_splits(const moe_shape* s) {
+  const int c = router_chunk(s);
+  return (s->T + c - 1) / c;
+}
+
+struct RouteGradWs {
+  uint16_t *dl, *w2;
+  float *part, *db_part;
+};
+RouteGradWs route_grad_ws(const moe_shape* s, Carve& c) {
+  const size_t ep2 = 2 * (size_t)ep_of(s);
+  RouteGradWs r;
+  r.dl = c.take<uint16_t>(s->T * ep2);
+  r.w2 = c.take<uint16_t>(s->H * ep2);
+  r.part = c.take<float>(s->T > 0 ? router_splits(s) * (size_t)s->H * ep2 : 0);
+  r.db_part = c.take<float>((size_t)((s->T + kGateTokens - 1) / kGateTokens) * s->E);
+  return r;
+}
+int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackwardArgs& gate, const uint16_t* x,
+                    const uint16_t* w_router, uint16_t* dx, uint16_t* dw_router, float* db, void* status,
+                    cudaStream_t st) {
+  const int ep = ep_of(s);
+  CUDA_TRY(launch_gate_backward(gate, st), "gate gradient launch");
+  CUDA_TRY(launch_router_twice(w_router, s->H, s->E, ep, r.w2, st), "router weights launch");
+  CUtensorMap ta, tb, ta64;
+  // dW_router's partial sums = x^T dlogits over chunks of tokens
+  TRY(map_rows(&ta, x, s->H, s->T, 64, "x"));
+  TRY(map_rows(&tb, r.dl, 2 * ep, s->T, 64, "dlogits"));
+  TrainGemmArgs a = gemm_args(chunks(s->T, router_chunk(s)), s->H, 2 * ep, 0, status);
+  a.out32 = r.part;
+  CUDA_TRY(launch_train_gemm(kTrainWgradF32, ta, tb, ta, a, a.seg.E * blocks256(s->H) * blocks256(2 * ep), st),
+           "dW_router launch");
+  RouterReduceArgs ra;
+  ra.H = s->H;
+  ra.E = s->E;
+  ra.ep = ep;
+  ra.S = a.seg.E;
+  ra.part = r.part;
+  ra.dw_router = dw_router;
+  ra.db_part = r.db_part;
+  ra.n_db = (s->T + kGateTokens - 1) / kGateTokens;
+  ra.db = db;
+  CUDA_TRY(launch_router_reduce(ra, st), "dW_router sums launch");
+  // dx = dlogits W_router^T
+  TRY(map_rows(&ta, r.dl, 2 * ep, s->T, 128, "dlogits"));
+  TRY(map_rows(&ta64, r.dl, 2 * ep, s->T, 64, "dlogits"));
+  TRY(map_weights(&tb, r.w2, 2 * ep, s->H, 1, 128, "W_router"));
+  a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, s->H, 2 * ep, status);
+  a.out = dx;
+  CUDA_TRY(launch_train_gemm(kTrainRows, ta, tb, ta64, a, blocks256(s->T) * blocks256(s->H), st),
+           "router x gradient launch");
+  return MOE_OK;
+}
+GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const int32_t* ids, const float* weights,
+                           const float* probs) {
+  GateBackwardArgs g = {};
+  g.T = s->T;
+  g.E = s->E;
+  g.k = s->k;
+  g.ep = ep_of(s);
+  g.gating = s->gating;
+  g.ids = ids;
+  g.weights = weights;
+  g.probs = probs;
+  g.dl = r.dl;
+  g.db_part = r.db_part;
+  return g;
+}
+
+struct ProbsWs {
+  uint16_t* wpad;
+  float* logits;
+};
+ProbsWs probs_ws(const moe_shape* s, Carve& c) {
+  ProbsWs p;
+  p.wpad = c.take<uint16_t>(s->E % 8 ? (size_t)s->H * ep_of(s) : 0);
+  p.logits = c.take<float>((size_t)s->T * ep_of(s));
+  return p;
+}
+int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* x, const uint16_t* w_router,
+                 const float* b_router, float* probs, void* status, cudaStream_t st) {
+  const int ep = ep_of(s);
+  if (s->E % 8) {
+    CUDA_TRY(launch_pad_router_weights(w_router, s->H, s->E, ep, p.wpad, sms, st, true),
+             "router weight padding launch");
+    w_router = p.wpad;
+  }
+  CUtensorMap ta, tb, ta64;
+  TRY(map_rows(&ta, x, s->H, s->T, 128, "x"));
+  TRY(map_rows(&ta64, x, s->H, s->T, 64, "x"));
+  TRY(map_weights(&tb, w_router, ep, s->H, 1, 64, "W_router"));
+  TrainGemmArgs a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, ep, s->H, status);
+  a.out32 = p.logits;
+  CUDA_TRY(launch_train_gemm(kTrainLogits, ta, tb, ta64, a, blocks256(s->T) * blocks256(ep), st),
+           "router logits launch");
+  CUDA_TRY(launch_router_softmax(p.logits, ep, b_router, s->T, s->E, probs, st), "router softmax launch");
+  return MOE_OK;
+}
+
+// ---------------------------------------------------------------- workspaces --
+
+struct FfnWs {
+  uint16_t* h;
+};
+FfnWs ffn_ws(const moe_shape* s, Carve& c) {
+  FfnWs w;
+  w.h = c.take<uint16_t>(rows_of(s) * s->F);
+  return w;
+}
+
+struct FfnGradWs {
+  uint16_t *xp, *dyp, *hw, *dz;
+};
+FfnGradWs ffn_grad_ws(const moe_shape* s, Carve& c) {
+  const size_t pad = pad_of(s);
+  FfnGradWs w;
+  w.xp = c.take<uint16_t>(pad * s->H);
+  w.dyp = c.take<uint16_t>(pad * s->H);
+  w.hw = c.take<uint16_t>(pad * s->F);
+  w.dz = c.take<uint16_t>(pad * s->F * halves(s));
+  return w;
+}
+
+struct ForwardWs {
+  void* route;
+  size_t route_bytes;
+  uint16_t* rows;  // xp, then the experts' outputs
+  FfnWs ffn;
+  ProbsWs probs;
+};
+ForwardWs forward_ws(const moe_shape* s, Carve& c) {
+  ForwardWs w = {};
+  w.route_bytes = moe_route_workspace_size(s);
+  w.route = c.take<char>(w.route_bytes);
+  w.rows = c.take<uint16_t>(rows_of(s) * s->H);
+  w.ffn = ffn_ws(s, c);
+  if (s->gating == MOE_GATE_SOFTMAX_TOPK) w.probs = probs_ws(s, c);
+  return w;
+}
+
+struct BackwardWs {
+  FfnGradWs ffn;
+  uint16_t* x;  // bf16 of x kept in 8 bits
+  float* part;
+  RouteGradWs route;
+  uint16_t* dxr;  // the router's part of dx
+};
+BackwardWs backward_ws(const moe_shape* s, int bits, Carve& c) {
+  BackwardWs w;
+  w.ffn = ffn_grad_ws(s, c);
+  w.x = c.take<uint16_t>(bits == 8 ? (size_t)s->T * s->H : 0);
+  w.part = c.take<float>(rows_of(s) * ((s->F + 63) / 64));
+  w.route = route_grad_ws(s, c);
+  w.dxr = c.take<uint16_t>((size_t)s->T * s->H);
+  return w;
+}
+
+int check_bits(int32_t bits) {
+  if (bits != 8 && bits != 16) return fail(MOE_ERR_INVALID_ARG, "keep_bits = %d: 8 or 16", bits);
+  return MOE_OK;
+}
+
+#define CHECK_WS(need, name)                                                                        \
+  do {                                                                                              \
+    REQUIRE_PTR(status);                                                                            \
+    REQUIRE_PTR(ws);                                                                                \
+    if (ws_bytes < (need))                                                                          \
+      return fail(MOE_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed (%s)", ws_bytes, (size_t)(need), \
+                  name);                                                                            \
+  } while (0)
+
+int check_a8(int64_t rows, int32_t cols) {
+  if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %lld, cols = %d", (long long)rows, cols);
+  if (cols < 8 || cols % 8) return fail(MOE_ERR_UNSUPPORTED, "cols = %d: need cols >= 8, cols %% 8 == 0", cols);
+  if (rows >= ((int64_t)1 << 46) / cols)
+    return fail(MOE_ERR_UNSUPPORTED, "rows * cols = %lld * %d: need less than 2^46", (long long)rows, cols);
+  return MOE_OK;
+}
+
+cudaStream_t stream_of(void* s) { return static_cast<cudaStream_t>(s); }
+
+int zero(void* p, size_t bytes, cudaStream_t st) {
+  CUDA_TRY(cudaMemsetAsync(p, 0, bytes, st), "cudaMemsetAsync");
+  return MOE_OK;
+}
+int zero_weights(const moe_shape* s, uint16_t* dw1, uint16_t* dw2, cudaStream_t st) {
+  const size_t n = (size_t)s->E * s->H * s->F * 2;
+  TRY(zero(dw1, n * halves(s), st));
+  return zero(dw2, n, st);
+}
+
+}  // namespace
+
+// =================================================================== C ABI
+
+extern "C" {
+
+int moet_quantize_a8(int64_t rows, int32_t cols, const uint16_t* x, int8_t* codes, uint8_t* scales,
+                     void* stream) {
+  TRY(check_a8(rows, cols));
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  int sms = 0;
+  TRY(device_setup(&sms));
+  CUDA_TRY(launch_quantize_a8(rows, cols, x, codes, scales, sms, stream_of(stream)), "quantize launch");
+  return MOE_OK;
+}
+
+int moet_dequantize_a8(int64_t rows, int32_t cols, const int8_t* codes, const uint8_t* scales, uint16_t* out,
+                       void* stream) {
+  TRY(check_a8(rows, cols));
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(codes);
+  REQUIRE_PTR(scales);
+  REQUIRE_PTR(out);
+  int sms = 0;
+  TRY(device_setup(&sms));
+  CUDA_TRY(launch_dequantize_a8(rows, cols, codes, scales, out, sms, stream_of(stream)), "dequantize launch");
+  return MOE_OK;
+}
+
+int moet_dispatch_rows_backward(const moe_shape* s, const uint16_t* dxp, const int32_t* slot, uint16_t* dx,
+                                void* stream) {
+  TRY(check_shape(s, false));
+  if (s->T == 0) return MOE_OK;
+  REQUIRE_PTR(dxp);
+  REQUIRE_PTR(slot);
+  REQUIRE_PTR(dx);
+  int sms = 0;
+  TRY(device_setup(&sms));
+  RowsSumArgs a = {dxp, slot, nullptr, s->T, s->H, s->k, dx};
+  CUDA_TRY(launch_rows_sum(a, stream_of(stream)), "row sums launch");
+  return MOE_OK;
+}
+
+int moet_combine_backward(const moe_shape* s, const uint16_t* dy, const uint16_t* Y, const float* weights,
+                          const int32_t* slot, uint16_t* dY, float* dweights, void* stream) {
+  TRY(check_shape(s, false));
+  if (s->T == 0) return MOE_OK;
+  REQUIRE_PTR(dy);
+  REQUIRE_PTR(Y);
+  REQUIRE_PTR(weights);
+  REQUIRE_PTR(slot);
+  REQUIRE_PTR(dY);
+  REQUIRE_PTR(dweights);
+  int sms = 0;
+  TRY(device_setup(&sms));
+  CombineBackwardArgs a = {dy, Y, weights, slot, s->T, s->H, s->k, dY, dweights};
+  CUDA_TRY(launch_combine_backward(a, stream_of(stream)), "combine gradient launch");
+  return MOE_OK;
+}
+
+size_t moet_expert_ffn_workspace_size(const moe_shape* s) {
+  if (check_shape(s, true) != MOE_OK) return 0;
+  Carve c(nullptr);
+  ffn_ws(s, c);
+  return c.used + 1024;
+}
+
+int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, const uint16_t* w1,
+                    const uint16_t* w2, const int32_t* offsets, uint16_t* Y, void* z, uint8_t* z_scales,
+                    void* status, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_shape(s, true));
+  TRY(check_bits(keep_bits));
+  CHECK_WS(moet_expert_ffn_workspace_size(s), "moet_expert_ffn_workspace_size");
+  if (s->T == 0) return MOE_OK;
+  REQUIRE_PTR(xp);
+  REQUIRE_PTR(w1);
+  REQUIRE_PTR(w2);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(Y);
+  REQUIRE_PTR(z);
+  if (keep_bits == 8) REQUIRE_PTR(z_scales);
+  int sms = 0;
+  TRY(train_setup(&sms));
+  Carve c(ws);
+  const FfnWs w = ffn_ws(s, c);
+  TRY(fwd_product(s, keep_bits, xp, w1, offsets, w.h, z, z_scales, nullptr, status, stream_of(stream)));
+  return plain_product(s, w.h, w2, offsets, Y, status, stream_of(stream));
+}
+
+size_t moet_expert_ffn_backward_workspace_size(const moe_shape* s) {
+  if (check_shape(s, true) != MOE_OK) return 0;
+  Carve c(nullptr);
+  ffn_grad_ws(s, c);
+  return c.used + 1024;
+}
+
+int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, const void* z,
+                             const uint8_t* z_scales, const uint16_t* w1, const uint16_t* w2,
+                             const int32_t* offsets, const uint16_t* dY, uint16_t* dxp, uint16_t* dw1,
+                             uint16_t* dw2, void* status, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_shape(s, true));
+  TRY(check_bits(keep_bits));
+  CHECK_WS(moet_expert_ffn_backward_workspace_size(s), "moet_expert_ffn_backward_workspace_size");
+  REQUIRE_PTR(dw1);
+  REQUIRE_PTR(dw2);
+  if (s->T > 0) {
+    REQUIRE_PTR(xp);
+    REQUIRE_PTR(z);
+    if (keep_bits == 8) REQUIRE_PTR(z_scales);
+    REQUIRE_PTR(w1);
+    REQUIRE_PTR(w2);
+    REQUIRE_PTR(offsets);
+    REQUIRE_PTR(dY);
+    REQUIRE_PTR(dxp);
+  }
+  cudaStream_t st = stream_of(stream);
+  int sms = 0;
+  TRY(train_setup(&sms));
+  if (s->T == 0) return zero_weights(s, dw1, dw2, st);
+  Carve c(ws);
+  const FfnGradWs w = ffn_grad_ws(s, c);
+  GatherArgs ga = {segments(s, offsets), nullptr, s->T, s->H, s->k, {xp, dY}, {w.xp, w.dyp}};
+  CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
+  FfnGrad f = {keep_bits, w.xp, w.dyp, w1, w2, offsets, z, z_scales, nullptr, nullptr, nullptr,
+               w.hw, w.dz, dxp, dw1, dw2};
+  return ffn_gradients(s, f, status, st);
+}
+
+size_t moet_router_probs_workspace_size(const moe_shape* s) {
+  if (check_shape(s, false) != MOE_OK) return 0;
+  Carve c(nullptr);
+  probs_ws(s, c);
+  return c.used + 1024;
+}
+
+int moet_router_probs(const moe_shape* s, const uint16_t* x, const uint16_t* w_router, const float* b_router,
+                      float* probs, void* status, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_shape(s, false));
+  CHECK_WS(moet_router_probs_workspace_size(s), "moet_router_probs_workspace_size");
+  if (b_router && !aligned16(b_router)) return fail(MOE_ERR_INVALID_ARG, "b_router is not 16-byte aligned");
+  if (s->T == 0) return MOE_OK;
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(w_router);
+  REQUIRE_PTR(probs);
+  int sms = 0;
+  TRY(train_setup(&sms));
+  Carve c(ws);
+  return router_probs(s, sms, probs_ws(s, c), x, w_router, b_router, probs, status, stream_of(stream));
+}
+
+size_t moet_route_backward_workspace_size(const moe_shape* s) {
+  if (check_shape(s, false) != MOE_OK) return 0;
+  Carve c(nullptr);
+  route_grad_ws(s, c);
+  return c.used + 1024;
+}
+
+int moet_route_backward(const moe_shape* s, const uint16_t* x, const uint16_t* w_router, const int32_t* ids,
+                        const float* weights, const float* probs, const float* dweights, uint16_t* dx,
+                        uint16_t* dw_router, float* db, void* status, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_shape(s, false));
+  CHECK_WS(moet_route_backward_workspace_size(s), "moet_route_backward_workspace_size");
+  REQUIRE_PTR(dw_router);
+  if (db && !aligned16(db)) return fail(MOE_ERR_INVALID_ARG, "db is not 16-byte aligned");
+  if (s->T > 0) {
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(w_router);
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(weights);
+    if (s->gating == MOE_GATE_SOFTMAX_TOPK) REQUIRE_PTR(probs);
+    REQUIRE_PTR(dweights);
+    REQUIRE_PTR(dx);
+  }
+  cudaStream_t st = stream_of(stream);
+  int sms = 0;
+  TRY(train_setup(&sms));
+  if (s->T == 0) {
+    TRY(zero(dw_router, (size_t)s->H * s->E * 2, st));
+    return db ? zero(db, (size_t)s->E * 4, st) : MOE_OK;
+  }
+  Carve c(ws);
+  const RouteGradWs r = route_grad_ws(s, c);
+  GateBackwardArgs g = gate_args(s, r, ids, weights, probs);
+  g.dw = dweights;
+  return route_gradients(s, r, g, x, w_router, dx, dw_router, db, status, st);
+}
+
+size_t moet_forward_workspace_size(const moe_shape* s) {
+  if (check_shape(s, true) != MOE_OK) return 0;
+  Carve c(nullptr);
+  forward_ws(s, c);
+  return c.used + 1024;
+}
+
+int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const uint16_t* w_router,
+                 const float* b_router, const uint16_t* w1, const uint16_t* w2, uint16_t* y, int32_t* ids,
+                 float* weights, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* slot, void* z,
+                 uint8_t* z_scales, int8_t* xk, uint8_t* xk_scales, float* probs, void* status, void* ws,
+                 size_t ws_bytes, void* stream) {
+  TRY(check_shape(s, true));
+  TRY(check_bits(keep_bits));
+  CHECK_WS(moet_forward_workspace_size(s), "moet_forward_workspace_size");
+  if (s->T > 0) {
+    REQUIRE_PTR(w1);
+    REQUIRE_PTR(w2);
+    REQUIRE_PTR(y);
+    REQUIRE_PTR(z);
+    if (keep_bits == 8) {
+      REQUIRE_PTR(z_scales);
+      REQUIRE_PTR(xk);
+      REQUIRE_PTR(xk_scales);
+    }
+    if (s->gating == MOE_GATE_SOFTMAX_TOPK) REQUIRE_PTR(probs);
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(w_router);
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(weights);
+    REQUIRE_PTR(perm);
+    REQUIRE_PTR(slot);
+  }
+  cudaStream_t st = stream_of(stream);
+  int sms = 0;
+  TRY(train_setup(&sms));
+  Carve c(ws);
+  const ForwardWs w = forward_ws(s, c);
+  TRY(moe_route(s, x, w_router, b_router, ids, weights, counts, offsets, perm, slot, w.route, w.route_bytes,
+                stream));
+  if (s->T == 0) return MOE_OK;
+  if (s->gating == MOE_GATE_SOFTMAX_TOPK)
+    TRY(router_probs(s, sms, w.probs, x, w_router, b_router, probs, status, st));
+  if (keep_bits == 8)
+    CUDA_TRY(launch_quantize_a8(s->T, s->H, x, xk, xk_scales, sms, st), "quantize launch");
+  PermuteArgs pa = {x, perm, offsets, s->T, s->H, s->k, s->E, w.rows, nullptr, nullptr};
+  CUDA_TRY(launch_permute(pa, sms, st, true), "permute launch");
+  // the route's own status word is taken over by the next product
+  TRY(fwd_product(s, keep_bits, w.rows, w1, offsets, w.ffn.h, z, z_scales, static_cast<const int*>(w.route),
+                  status, st));
+  TRY(plain_product(s, w.ffn.h, w2, offsets, w.rows, status, st));
+  CombineArgs ca = {w.rows, weights, slot, s->T, s->H, s->k, y, nullptr, 1, 0};
+  CUDA_TRY(launch_combine(ca, st, true), "combine launch");
+  return MOE_OK;
+}
+
+size_t moet_backward_workspace_size(const moe_shape* s, int32_t keep_bits) {
+  if (check_shape(s, true) != MOE_OK || check_bits(keep_bits) != MOE_OK) return 0;
+  Carve c(nullptr);
+  backward_ws(s, keep_bits, c);
+  return c.used + 1024;
+}
+
+int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, const void* x,
+                  const uint8_t* x_scales, const uint16_t* w_router, const uint16_t* w1, const uint16_t* w2,
+                  const int32_t* ids, const float* weights, const int32_t* offsets, const int32_t* perm,
+                  const int32_t* slot, const void* z, const uint8_t* z_scales, const float* probs,
+                  uint16_t* dx, uint16_t* dw_router, float* db, uint16_t* dw1, uint16_t* dw2, void* status,
+                  void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_shape(s, true));
+  TRY(check_bits(keep_bits));
+  CHECK_WS(moet_backward_workspace_size(s, keep_bits), "moet_backward_workspace_size");
+  REQUIRE_PTR(dw_router);
+  REQUIRE_PTR(dw1);
+  REQUIRE_PTR(dw2);
+  if (db && !aligned16(db)) return fail(MOE_ERR_INVALID_ARG, "db is not 16-byte aligned");
+  if (s->T > 0) {
+    REQUIRE_PTR(dy);
+    REQUIRE_PTR(x);
+    REQUIRE_PTR(w_router);
+    REQUIRE_PTR(w1);
+    REQUIRE_PTR(w2);
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(weights);
+    REQUIRE_PTR(offsets);
+    REQUIRE_PTR(perm);
+    REQUIRE_PTR(slot);
+    REQUIRE_PTR(z);
+    if (keep_bits == 8) {
+      REQUIRE_PTR(z_scales);
+      REQUIRE_PTR(x_scales);
+    }
+    if (s->gating == MOE_GATE_SOFTMAX_TOPK) REQUIRE_PTR(probs);
+    REQUIRE_PTR(dx);
+  }
+  cudaStream_t st = stream_of(stream);
+  int sms = 0;
+  TRY(train_setup(&sms));
+  if (s->T == 0) {
+    TRY(zero(dw_router, (size_t)s->H * s->E * 2, st));
+    if (db) TRY(zero(db, (size_t)s->E * 4, st));
+    return zero_weights(s, dw1, dw2, st);
+  }
+  Carve c(ws);
+  const BackwardWs w = backward_ws(s, keep_bits, c);
+  const uint16_t* xb = static_cast<const uint16_t*>(x);
+  if (keep_bits == 8) {
+    CUDA_TRY(launch_dequantize_a8(s->T, s->H, static_cast<const int8_t*>(x), x_scales, w.x, sms, st),
+             "dequantize launch");
+    xb = w.x;
+  }
+  GatherArgs ga = {segments(s, offsets), perm, s->T, s->H, s->k, {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
+  CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
+  // dxp takes dyp's place: its product is the last of the four
+  uint16_t* dxp = w.ffn.dyp;
+  FfnGrad f = {keep_bits, w.ffn.xp, w.ffn.dyp, w1, w2, offsets, z, z_scales, weights, perm, w.part,
+               w.ffn.hw, w.ffn.dz, dxp, dw1, dw2};
+  TRY(ffn_gradients(s, f, status, st));
+  GateBackwardArgs g = gate_args(s, w.route, ids, weights, probs);
+  g.part = w.part;
+  g.slot = slot;
+  g.rows = (int)rows_of(s);
+  g.units = (s->F + 63) / 64;
+  TRY(route_gradients(s, w.route, g, xb, w_router, w.dxr, dw_router, db, status, st));
+  RowsSumArgs ra = {dxp, slot, w.dxr, s->T, s->H, s->k, dx};
+  CUDA_TRY(launch_rows_sum(ra, st), "row sums launch");
+  return MOE_OK;
+}
+
+}  // extern "C"

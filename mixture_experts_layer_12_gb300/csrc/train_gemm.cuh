@@ -1,0 +1,687 @@
+// train_gemm.cuh -- the products of a training step on the 5th-generation
+// tensor cores, grouped by expert.
+//
+// For the rows r of expert e (A_e = its rows of A):
+//   Fwd    z = A_e W1[e], kept in bf16 or 8 bits; h = act(z)
+//   Bwd    g = A_e W2[e]^T with A the rows' dy; from the kept z:
+//          dz = w g act'(z), w h, and <g, h> (the gate weight's gradient)
+//   Rows   out = A_e W[e]^T                     (dxp = dz W1^T)
+//   Wgrad  out[e] = A_e^T B_e                   (dW2 = (w h)^T dy, dW1 = xp^T dz)
+//   Logits out = A W in fp32                    (the router's)
+//
+// One design serves all (as the forward's expert GEMM): CTA pairs run the
+// 2-SM tcgen05.mma (M = 256, N = 256, K = 16, fp32 in TMEM), each CTA holding
+// 128 rows of A and 128 columns of B per 64-deep stage, six stages fed by one
+// TMA thread, one MMA thread in the leader, and an epilogue double-buffered
+// against the next tile.  What differs is the operands' major and the
+// epilogue:
+//   * transposed weights are K-major operands of the same bytes: W2 [E, F, H]
+//     read as [N = F rows, K = H] needs no transposed copy;
+//   * Wgrad's operands are both MN-major ([K = rows, M] and [K = rows, N]):
+//     row-major activations as they are.  Its K is an expert's row count, any
+//     number: rows are padded to 16 with zeros (SegTable), the box of a stage
+//     may reach past them, but only the K steps of the expert's own 16-row
+//     groups are issued, so a neighbour's infinities or NaN stay its own;
+//   * the Bwd epilogue never writes g: it reads the kept z, one 32-column
+//     chunk ahead, and leaves the two operands that the remaining products
+//     need.  <g, h> makes dw without the experts' output Y, which therefore is
+//     not kept: dw = dy . (h W2) = (dy W2^T) . h.
+// Two epilogue warps per TMEM lane quadrant share a tile's columns: the Bwd
+// epilogue reads and writes 8 to 16 bytes a column and is the longer half of a
+// tile with K below 2000.
+// Every mbarrier wait is bounded (MOE_DEV_TIMEOUT on expiry).
+#pragma once
+
+#include <atomic>
+
+#include "train_seg.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int TBM = 128;            // rows per CTA
+constexpr int TPAIR_M = 2 * TBM;    // rows per pair tile
+constexpr int TBN = 256;            // columns per pair tile
+constexpr int TBK = 64;
+constexpr int TSTAGES = 6;
+constexpr int TACC = 2;
+constexpr int T_OP_BYTES = 128 * TBK * 2;  // a CTA's half of either operand: 16 KB
+constexpr int T_BOX = 64 * TBK * 2;        // one 64-column MN-major box: 8 KB
+constexpr int T_STAGE_BYTES = 2 * T_OP_BYTES;
+constexpr int T_MMA_WARP = 1;
+constexpr int T_EPI_WARP0 = 2;
+constexpr int T_EPI_WARPS = 8;  // two per TMEM lane quadrant (warp % 4)
+constexpr int T_THREADS = 32 * (T_EPI_WARP0 + T_EPI_WARPS);
+constexpr int T_TMEM_COLS = TACC * TBN;
+constexpr uint16_t T_PAIR_MASK = 0x3;
+
+struct TrainCtrl {
+  uint64_t full[TSTAGES];
+  uint64_t empty[TSTAGES];
+  uint64_t tfull[TACC];
+  uint64_t tempty[TACC];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int tile_start[kMaxExperts + 1];
+  SegTable seg;
+};
+constexpr size_t T_SMEM_BYTES = 1024 + (size_t)TSTAGES * T_STAGE_BYTES + sizeof(TrainCtrl);
+static_assert(T_SMEM_BYTES <= 232448, "shared memory of one CTA");
+
+template <int OP>
+struct TrainTraits {
+  static constexpr bool FWD = OP == kTrainFwdGelu || OP == kTrainFwdSwiGLU;
+  static constexpr bool BWD = OP == kTrainBwdGelu || OP == kTrainBwdSwiGLU;
+  static constexpr bool GATED = OP == kTrainFwdSwiGLU || OP == kTrainBwdSwiGLU;
+  static constexpr bool PAIRED = OP == kTrainFwdSwiGLU;  // a tile holds 128 gate and 128 up columns
+  static constexpr bool WGRAD = OP == kTrainWgrad || OP == kTrainWgradF32;
+  static constexpr bool A_MN = WGRAD;
+  static constexpr bool B_MN = !(BWD || OP == kTrainRows);
+  static constexpr bool A_PADDED = !(FWD || OP == kTrainLogits);
+  static constexpr int BN_OUT = PAIRED ? TBN / 2 : TBN;
+};
+
+struct TrainTile {
+  int e, nb;
+  int base;    // the tile's first row within the segment (Wgrad: row of out)
+  int kb;      // stages
+  int k16;     // Wgrad: K steps of 16 in all
+  bool half;   // M = 128 tile: 64 rows per CTA
+  bool nhalf;  // N = 128 tile
+};
+
+// Tiles run segment-major, row-block fastest, so that pairs at work at the
+// same time share the columns of B through L2.  An M block with at most 128
+// rows runs as an M = 128 MMA (TMEM lanes 0-63: the CTA's 64 rows, columns
+// 0..127; lanes 64-127: the same rows, columns 128..255), else an N block
+// with at most 128 columns as N = 128; not for paired gate and up columns.
+template <int OP>
+__device__ __forceinline__ TrainTile train_tile(const TrainCtrl& c, const TrainGemmArgs& p, int tile,
+                                                int& e) {
+  using TT = TrainTraits<OP>;
+  while (tile >= c.tile_start[e + 1]) ++e;
+  const int local = tile - c.tile_start[e];
+  const int m = TT::WGRAD ? p.M : c.seg.rows[e];
+  const int mbs = (m + TPAIR_M - 1) / TPAIR_M;
+  const int mb = local % mbs;
+  TrainTile t;
+  t.e = e;
+  t.nb = local / mbs;
+  t.base = mb * TPAIR_M;
+  if constexpr (TT::WGRAD) {
+    t.k16 = (c.seg.rows[e] + 15) / 16;
+    t.kb = (t.k16 + 3) / 4;
+  } else {
+    t.k16 = 0;
+    t.kb = (p.K + TBK - 1) / TBK;
+  }
+  t.half = !TT::PAIRED && m - t.base <= TPAIR_M / 2;
+  t.nhalf = !TT::PAIRED && !t.half && p.N - t.nb * TBN <= TBN / 2;
+  return t;
+}
+
+__device__ __forceinline__ bool train_wait_drain(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                 int* status) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait(a, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) {
+      record_status(status, MOE_DEV_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// erfc(|z| / sqrt 2) and exp(-z^2 / 2): Abramowitz & Stegun, Handbook of
+// Mathematical Functions, formula 7.1.26 (|error| <= 1.5e-7); the exponential
+// it needs is the normal density's.
+__device__ __forceinline__ float train_erfc(float z, float& ex) {
+  const float ax = fabsf(z) * 0.70710678118654752440f;
+  const float t = __fdividef(1.0f, fmaf(0.3275911f, ax, 1.0f));
+  const float poly =
+      t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+               0.254829592f);
+  ex = __expf(-ax * ax);
+  return poly * ex;
+}
+// GELU(z) = z Phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2, without cancellation
+__device__ __forceinline__ float train_gelu(float z) {
+  float ex;
+  const float c = train_erfc(z, ex);
+  return 0.5f * z * (z >= 0.0f ? 2.0f - c : c);
+}
+// GELU and GELU'(z) = Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi); an infinite z
+// has a density of 0, not 0 times infinity
+__device__ __forceinline__ void train_gelu_grad(float z, float& h, float& d) {
+  float ex;
+  const float c = train_erfc(z, ex);
+  const float phi = z >= 0.0f ? 1.0f - 0.5f * c : 0.5f * c;
+  h = z * phi;
+  d = phi + (ex == 0.0f ? 0.0f : z * ex * 0.39894228040143267794f);
+}
+__device__ __forceinline__ float train_sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
+
+// eight columns as bf16, 16 bytes
+__device__ __forceinline__ void train_store8(uint16_t* dst, const float* f) {
+  uint4 pk;
+  pk.x = pack_bf16x2(f[0], f[1]);
+  pk.y = pack_bf16x2(f[2], f[3]);
+  pk.z = pack_bf16x2(f[4], f[5]);
+  pk.w = pack_bf16x2(f[6], f[7]);
+  *reinterpret_cast<uint4*>(dst) = pk;
+}
+
+// Keeps 32 columns of z (those below `valid`, a multiple of 8, exist) at
+// column `col` of half `hf` of row `row`.
+__device__ __forceinline__ void train_keep(const TrainGemmArgs& p, bool gated, size_t row, int hf, int col,
+                                           int valid, const uint32_t (&v)[32]) {
+  const int halves = gated ? 2 : 1;
+  const size_t at = (row * halves + hf) * (size_t)p.N + col;
+  if (p.keep_bits == 16) {
+    uint16_t* dst = static_cast<uint16_t*>(p.z) + at;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (g * 8 < valid) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[g * 8 + i]);
+        train_store8(dst + g * 8, f);
+      }
+    return;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = max(m, i < valid ? v[i] & 0x7fffffffu : 0u);
+  const uint32_t b = a8_scale_byte(m);
+  const float inv = a8_inverse(b);
+  int8_t* dst = static_cast<int8_t*>(p.z) + at;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    if (g * 8 < valid) {
+      uint32_t q[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[i / 4] |= ((uint32_t)a8_code(__uint_as_float(v[g * 8 + i]), inv, b) & 0xffu) << (8 * (i % 4));
+      *reinterpret_cast<uint2*>(dst + g * 8) = make_uint2(q[0], q[1]);
+    }
+  const int groups = (p.N + 31) / 32;
+  p.z_scales[(row * halves + hf) * (size_t)groups + (col >> 5)] = (uint8_t)b;
+}
+
+// 32 kept columns on their way from memory: 16 words of bf16, or 8 words of
+// codes and the group's scale byte.
+struct KeptChunk {
+  uint32_t w[16];
+  uint32_t b;
+};
+__device__ __forceinline__ void train_load_kept(const TrainGemmArgs& p, int halves, size_t row, int hf,
+                                                int col, bool ok, KeptChunk& k) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) k.w[i] = 0u;
+  k.b = 127u;
+  if (!ok || col >= p.N) return;
+  const size_t at = (row * halves + hf) * (size_t)p.N + col;
+  const int valid = p.N - col;
+  if (p.keep_bits == 16) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + at);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (g * 8 < valid) {
+        const uint4 u = __ldg(src + g);
+        k.w[4 * g] = u.x;
+        k.w[4 * g + 1] = u.y;
+        k.w[4 * g + 2] = u.z;
+        k.w[4 * g + 3] = u.w;
+      }
+  } else {
+    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.z) + at);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if (g * 8 < valid) {
+        const uint2 u = __ldg(src + g);
+        k.w[2 * g] = u.x;
+        k.w[2 * g + 1] = u.y;
+      }
+    const int groups = (p.N + 31) / 32;
+    k.b = __ldg(p.z_scales + (row * halves + hf) * (size_t)groups + (col >> 5));
+  }
+}
+// columns 8 g .. 8 g + 7 of a chunk
+__device__ __forceinline__ void train_kept8(const TrainGemmArgs& p, const KeptChunk& k, int g, float* f) {
+  if (p.keep_bits == 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(k.w[4 * g + i]);
+      f[2 * i + 1] = bf16_hi(k.w[4 * g + i]);
+    }
+  } else {
+    const float s = a8_scale(k.b);
+    a8_values(k.w[2 * g], s, f);
+    a8_values(k.w[2 * g + 1], s, f + 4);
+  }
+}
+
+template <int OP>
+__global__ void __launch_bounds__(T_THREADS, 1)
+    train_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                      const __grid_constant__ CUtensorMap tm_a64, const TrainGemmArgs p) {
+  using TT = TrainTraits<OP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + TSTAGES * T_OP_BYTES;
+  TrainCtrl& c = *reinterpret_cast<TrainCtrl*>(smem + TSTAGES * T_STAGE_BYTES);
+  constexpr uint32_t IDESC = idesc_bf16_f32(TPAIR_M, TBN, TT::A_MN, TT::B_MN);
+  constexpr uint32_t IDESC_HALF = idesc_bf16_f32(TPAIR_M / 2, TBN, TT::A_MN, TT::B_MN);
+  constexpr uint32_t IDESC_NHALF = idesc_bf16_f32(TPAIR_M, TBN / 2, TT::A_MN, TT::B_MN);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();  // 0 = leader of the pair
+  const int pair = blockIdx.x >> 1;
+  const int n_pairs = gridDim.x >> 1;
+  const int NB = (p.N + TT::BN_OUT - 1) / TT::BN_OUT;
+  pdl_launch_dependents();
+  pdl_wait();  // offsets, operands and output buffers belong to earlier kernels
+
+  if (warp == 0) {
+    seg_scan(p.seg, c.seg, c.tile_start, lane, [&](int n) {
+      const int m = TT::WGRAD ? p.M : n;
+      return (m + TPAIR_M - 1) / TPAIR_M * NB;
+    });
+  } else if (threadIdx.x == 32) {
+    for (int i = 0; i < TSTAGES; ++i) {
+      mbar_init(&c.full[i], 2);
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < TACC; ++i) {
+      mbar_init(&c.tfull[i], 1);
+      mbar_init(&c.tempty[i], 2 * T_EPI_WARPS);
+    }
+    mbar_init(&c.drain, 1);
+    c.abort_flag = 0;
+    fence_mbar_init();
+    if (p.merge_status && blockIdx.x == 0) {
+      const int s = *p.merge_status;
+      if (s) record_status(p.status, s);
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // the leader's barriers exist before the peer signals them
+  const int n_tiles = c.tile_start[p.seg.E];
+  if (pair >= n_tiles) return;  // uniform across the pair: nothing allocated yet
+
+  if (warp == T_MMA_WARP) {
+    tmem_alloc_pair(&c.tmem_base, T_TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem_base;
+  const WaitCtl wc{&c.abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer (one thread)
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_a);
+      tma_prefetch_desc(&tm_b);
+      const uint32_t full0 = dsmem_map(smem_u32(&c.full[0]), 0);  // leader's barriers
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      int e = 0;
+      bool ok = true;
+      for (int tile = pair; tile < n_tiles && ok; tile += n_pairs) {
+        const TrainTile t = train_tile<OP>(c, p, tile, e);
+        const int off = TT::A_PADDED ? c.seg.pad_off[t.e] : c.seg.row_off[t.e];
+        // this CTA's first row of A's M and column of B's N
+        const int arow = t.base + rank * (t.half ? TBM / 2 : TBM);
+        const int bcol = TT::PAIRED  ? rank * p.N + t.nb * TT::BN_OUT
+                         : t.nhalf   ? t.nb * TBN + rank * (TBN / 4)
+                                     : t.nb * TBN + rank * (TBN / 2);
+        const uint32_t a_bytes = t.half ? T_OP_BYTES / 2 : T_OP_BYTES;
+        const int b_boxes = t.nhalf ? 1 : 2;  // MN-major: 64-column boxes
+        const uint32_t bytes = a_bytes + (TT::B_MN ? b_boxes * T_BOX : T_OP_BYTES);
+        for (int kb = 0; kb < t.kb; ++kb) {
+          if (!mbar_wait(&c.empty[stage], phase ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_cl = full0 + (uint32_t)(stage * sizeof(uint64_t));
+          uint8_t* a = sA + stage * T_OP_BYTES;
+          uint8_t* b = sB + stage * T_OP_BYTES;
+          mbar_arrive_expect_tx_cluster(full_cl, bytes);
+          if constexpr (TT::WGRAD) {
+            const int krow = off + kb * TBK;
+            tma_load_2d_pair(a, &tm_a, full_cl, arow, krow);
+            if (!t.half) tma_load_2d_pair(a + T_BOX, &tm_a, full_cl, arow + 64, krow);
+            tma_load_2d_pair(b, &tm_b, full_cl, bcol, krow);
+            if (!t.nhalf) tma_load_2d_pair(b + T_BOX, &tm_b, full_cl, bcol + 64, krow);
+          } else {
+            // rows past the segment's end are computed but never stored
+            tma_load_2d_pair(a, t.half ? &tm_a64 : &tm_a, full_cl, kb * TBK, off + arow);
+            if constexpr (TT::B_MN) {
+              tma_load_3d_pair(b, &tm_b, full_cl, bcol, kb * TBK, t.e);
+              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol + 64, kb * TBK, t.e);
+            } else {
+              tma_load_3d_pair(b, &tm_b, full_cl, kb * TBK, bcol, t.e);
+            }
+          }
+          ++issued;
+          if (++stage == TSTAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the bytes of the last armed stages of both CTAs have landed before
+      // shared memory is released (at once on the normal path)
+      if (rank == 0) {
+        for (int m = max(0, issued - TSTAGES); m < issued; ++m)
+          train_wait_drain(&c.full[m % TSTAGES], (uint32_t)((m / TSTAGES) & 1), p.wait_limit_ns, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == T_MMA_WARP) {
+    // ------------------------------------------------ MMA issuer (leader)
+    if (rank == 0 && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      int e = 0;
+      for (int tile = pair; tile < n_tiles && ok; tile += n_pairs) {
+        const TrainTile t = train_tile<OP>(c, p, tile, e);
+        if (t.kb == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const uint32_t idesc = t.half ? IDESC_HALF : t.nhalf ? IDESC_NHALF : IDESC;
+        if (!mbar_wait(&c.tempty[acc], acc_phase ^ 1u, wc)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * TBN);
+        for (int kb = 0; kb < t.kb; ++kb) {
+          if (!mbar_wait(&c.full[stage], phase, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + stage * T_OP_BYTES);
+          const uint32_t b0 = smem_u32(sB + stage * T_OP_BYTES);
+          const int steps = TT::WGRAD ? min(4, t.k16 - 4 * kb) : 4;
+#pragma unroll
+          for (int j = 0; j < TBK / 16; ++j) {
+            if (TT::WGRAD && j >= steps) break;
+            // K-major: 16 elements = 32 bytes inside the swizzle row;
+            // MN-major: 16 K rows = two 1024-byte atoms
+            const uint64_t ad = TT::A_MN ? sdesc_sw128(a0 + j * 2048, T_BOX, 1024)
+                                         : sdesc_sw128(a0 + j * 32, 16, 1024);
+            const uint64_t bd = TT::B_MN ? sdesc_sw128(b0 + j * 2048, T_BOX, 1024)
+                                         : sdesc_sw128(b0 + j * 32, 16, 1024);
+            umma_bf16_pair(d, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
+          }
+          umma_commit_pair_mc(&c.empty[stage], T_PAIR_MASK);
+          if (++stage == TSTAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_mc(&c.tfull[acc], T_PAIR_MASK);
+        if (++acc == TACC) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      umma_commit_pair_mc(&c.drain, 0x1);  // all MMAs of this thread have completed
+      train_wait_drain(&c.drain, 0, p.wait_limit_ns, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue warps
+    const int q = warp & 3;                     // TMEM lane quadrant this warp may read
+    const int wh = (warp - T_EPI_WARP0) >> 2;   // which half of the tile's chunks
+    const uint32_t tempty0 = dsmem_map(smem_u32(&c.tempty[0]), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    int e = 0;
+    for (int tile = pair; tile < n_tiles; tile += n_pairs) {
+      const TrainTile t = train_tile<OP>(c, p, tile, e);
+      const int row = t.base + (t.half ? rank * (TBM / 2) + (q & 1) * 32 + lane
+                                       : rank * TBM + q * 32 + lane);  // within segment (Wgrad: of out)
+      const int col_base = t.nb * TT::BN_OUT + (t.half ? (q >> 1) * 128 : 0);
+      const int n_chunks = t.half || t.nhalf || TT::PAIRED ? 4 : 8;  // of 32 columns, both warps'
+      const int ch0 = wh * (n_chunks / 2);
+      const int ch1 = ch0 + n_chunks / 2;
+      const int n_rows = TT::WGRAD ? p.M : c.seg.rows[t.e];
+      const bool row_ok = row < n_rows;
+
+      [[maybe_unused]] KeptChunk next[TT::GATED ? 2 : 1];
+      [[maybe_unused]] size_t crow = 0;
+      [[maybe_unused]] float gw = 0.0f;
+      if constexpr (TT::BWD) {
+        // z of the first chunk and the gate weight, before the accumulator
+        crow = (size_t)c.seg.row_off[t.e] + row;
+#pragma unroll
+        for (int hf = 0; hf < (TT::GATED ? 2 : 1); ++hf)
+          train_load_kept(p, TT::GATED ? 2 : 1, crow, hf, col_base + ch0 * 32, row_ok, next[hf]);
+        if (row_ok) {
+          gw = 1.0f;
+          if (p.w) {
+            const int a = __ldg(p.perm + crow);
+            gw = a >= 0 && a < p.n_w ? __ldg(p.w + a) : 0.0f;
+          }
+        }
+      }
+      if (t.kb > 0) {
+        int got = 1;
+        if (lane == 0) got = mbar_wait(&c.tfull[acc], acc_phase, wc);
+        got = __shfl_sync(0xffffffffu, got, 0);
+        if (!got) break;
+        tc_fence_after();
+      }
+      const uint32_t tbase = tmem + (uint32_t)(acc * TBN) + ((uint32_t)(q * 32) << 16);
+
+      if constexpr (TT::PAIRED) {
+        const size_t orow = (size_t)c.seg.row_off[t.e] + row;
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1; ++ch) {
+          uint32_t gv[32], uv[32];
+          tmem_ld_x32(tbase + (uint32_t)(ch * 32), gv);
+          tmem_ld_x32(tbase + (uint32_t)(TT::BN_OUT + ch * 32), uv);
+          tmem_ld_wait();
+          const int gcol = col_base + ch * 32;
+          if (row_ok && gcol < p.N) {
+            const int valid = min(32, p.N - gcol);
+            train_keep(p, true, orow, 0, gcol, valid, gv);
+            train_keep(p, true, orow, 1, gcol, valid, uv);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (g * 8 < valid) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float a = __uint_as_float(gv[g * 8 + i]);
+                  f[i] = __fdividef(a, 1.0f + __expf(-a)) * __uint_as_float(uv[g * 8 + i]);
+                }
+                train_store8(p.out + orow * (size_t)p.N + gcol + g * 8, f);
+              }
+          }
+        }
+      } else if constexpr (TT::BWD) {
+        const int n16 = (n_rows + 15) / 16 * 16;
+        const size_t prow = (size_t)c.seg.pad_off[t.e] + row;
+        constexpr int HALVES = TT::GATED ? 2 : 1;
+        float dot = 0.0f;
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1; ++ch) {
+          KeptChunk cur[HALVES];
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf) cur[hf] = next[hf];
+          const int gcol = col_base + ch * 32;
+          if (ch + 1 < ch1) {
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+              train_load_kept(p, HALVES, crow, hf, gcol + 32, row_ok, next[hf]);
+          }
+          uint32_t v[32];
+          tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
+          tmem_ld_wait();
+          if (row < n16 && gcol < p.N) {
+            const int valid = p.N - gcol;
+            uint16_t* dz = p.dz + prow * (size_t)(HALVES * p.N) + gcol;
+            uint16_t* hw = p.hw + prow * (size_t)p.N + gcol;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (g * 8 < valid) {
+                float z[8], hv[8], d0[8];
+                [[maybe_unused]] float u[8], d1[8];
+                train_kept8(p, cur[0], g, z);
+                if constexpr (TT::GATED) train_kept8(p, cur[HALVES - 1], g, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float gr = __uint_as_float(v[g * 8 + i]);
+                  float h;
+                  if constexpr (TT::GATED) {
+                    // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
+                    const float s = train_sigmoid(z[i]);
+                    const float as = z[i] * s;
+                    h = as * u[i];
+                    d0[i] = gw * gr * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
+                    d1[i] = gw * gr * as;
+                  } else {
+                    float d;
+                    train_gelu_grad(z[i], h, d);
+                    d0[i] = gw * gr * d;
+                  }
+                  dot = fmaf(gr, h, dot);
+                  hv[i] = gw * h;
+                }
+                if (!row_ok) {  // a padding row
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    d0[i] = hv[i] = 0.0f;
+                    if constexpr (TT::GATED) d1[i] = 0.0f;
+                  }
+                }
+                train_store8(dz + g * 8, d0);
+                if constexpr (TT::GATED) train_store8(dz + p.N + g * 8, d1);
+                train_store8(hw + g * 8, hv);
+              }
+            if (p.part && row_ok && ((ch & 1) || gcol + 32 >= p.N)) {
+              p.part[crow * (size_t)p.units + (gcol >> 6)] = dot;
+              dot = 0.0f;
+            }
+          }
+        }
+      } else {
+        // Fwd GELU, Rows, Logits, Wgrad
+        size_t orow;
+        if constexpr (TT::WGRAD)
+          orow = (size_t)t.e * p.M + row;
+        else
+          orow = (size_t)c.seg.row_off[t.e] + row;
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1; ++ch) {
+          uint32_t v[32];
+          if (t.kb > 0) {
+            tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+          const int gcol = col_base + ch * 32;
+          if (row_ok && gcol < p.N) {
+            const int valid = min(32, p.N - gcol);
+            if constexpr (OP == kTrainFwdGelu) train_keep(p, false, orow, 0, gcol, valid, v);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (g * 8 < valid) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  f[i] = __uint_as_float(v[g * 8 + i]);
+                  if constexpr (OP == kTrainFwdGelu) f[i] = train_gelu(f[i]);
+                }
+                if constexpr (OP == kTrainLogits || OP == kTrainWgradF32) {
+                  float4* dst = reinterpret_cast<float4*>(p.out32 + orow * (size_t)p.N + gcol + g * 8);
+                  dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                  dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+                } else {
+                  train_store8(p.out + orow * (size_t)p.N + gcol + g * 8, f);
+                }
+              }
+          }
+        }
+      }
+      if (t.kb > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(acc * sizeof(uint64_t)));
+        if (++acc == TACC) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+  }
+
+  // Both CTAs finish all remote signalling and the leader's MMAs before TMEM
+  // is released and before either CTA's shared memory goes away.
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == T_MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, T_TMEM_COLS);
+  }
+  cluster_sync_all();
+}
+
+template <int OP>
+cudaError_t train_set_attributes() {
+  return cudaFuncSetAttribute(train_gemm_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)T_SMEM_BYTES);
+}
+
+// Persistent pairs: as many as are resident at once, at most one per tile.
+template <int OP>
+cudaError_t train_launch(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_a64,
+                         const TrainGemmArgs& a, int64_t max_tiles, cudaStream_t st) {
+  static std::atomic<int> pairs_of[64];
+  if (max_tiles <= 0) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(T_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = T_SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = dev >= 0 && dev < 64 ? pairs_of[dev].load() : 0;
+  if (pairs == 0) {
+    e = cudaOccupancyMaxActiveClusters(&pairs, train_gemm_kernel<OP>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    if (dev >= 0 && dev < 64) pairs_of[dev] = pairs;
+  }
+  if (pairs > max_tiles) pairs = (int)max_tiles;
+  cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+  set_pdl_attr(attr[1]);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, train_gemm_kernel<OP>, tm_a, tm_b, tm_a64, a);
+}
+
+}  // namespace
+}  // namespace moe

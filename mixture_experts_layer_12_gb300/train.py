@@ -1,0 +1,552 @@
+"""Training operators of the MoE layer: Python binding of include/moe_train.h.
+
+The layer's forward that keeps what its gradients need and the gradients
+themselves (:class:`MoETrainLayer`), the same for single steps
+(:func:`expert_ffn`, :func:`expert_ffn_backward`, :func:`route_backward`,
+:func:`combine_backward`, :func:`dispatch_rows_backward`,
+:func:`router_probs`), and activations kept in 8 bits
+(:func:`quantize_a8`, :func:`dequantize_a8`).  Gradients are explicit calls, as
+every other step of this package; all of them run in the library's CUDA kernels
+on the current stream (or `stream`), allocate their outputs and workspace there
+and keep nothing between calls.
+"""
+from __future__ import annotations
+
+import ctypes
+import threading
+from typing import NamedTuple
+
+import torch
+
+from . import (_BF, _F32, _I32, _check, MOE_ERR_UNSUPPORTED, MOE_GATE_SOFTMAX_TOPK, MOE_GATE_TOPK_SOFTMAX,
+               MOE_WS_MIN_BYTES, RoutingBuffers, check_tensor, load_library, make_shape, moe_get_device_status,
+               moe_shape)
+from .decode import _addr, _here, _on
+
+# Every symbol include/moe_train.h declares.
+TRAIN_EXPORTS = ("moet_quantize_a8", "moet_dequantize_a8", "moet_dispatch_rows_backward",
+                 "moet_combine_backward", "moet_expert_ffn_workspace_size", "moet_expert_ffn",
+                 "moet_expert_ffn_backward_workspace_size", "moet_expert_ffn_backward",
+                 "moet_router_probs_workspace_size", "moet_router_probs",
+                 "moet_route_backward_workspace_size", "moet_route_backward",
+                 "moet_forward_workspace_size", "moet_forward", "moet_backward_workspace_size",
+                 "moet_backward")
+
+_I8, _U8 = torch.int8, torch.uint8
+_sig_lock = threading.Lock()
+_sig_lib = None
+
+
+def _lib():
+    """The library with the training entry points' signatures set."""
+    global _sig_lib
+    if _sig_lib is not None:
+        return _sig_lib
+    lib = load_library()
+    with _sig_lock:
+        P, S, I, Z = ctypes.c_void_p, ctypes.POINTER(moe_shape), ctypes.c_int32, ctypes.c_size_t
+        L = ctypes.c_int64
+        call = [P, P, Z, P]  # status, ws, ws_bytes, stream
+        sig = {
+            "moet_quantize_a8": ([L, I] + [P] * 4, ctypes.c_int),
+            "moet_dequantize_a8": ([L, I] + [P] * 4, ctypes.c_int),
+            "moet_dispatch_rows_backward": ([S] + [P] * 4, ctypes.c_int),
+            "moet_combine_backward": ([S] + [P] * 7, ctypes.c_int),
+            "moet_expert_ffn_workspace_size": ([S], Z),
+            "moet_expert_ffn": ([S, I] + [P] * 7 + call, ctypes.c_int),
+            "moet_expert_ffn_backward_workspace_size": ([S], Z),
+            "moet_expert_ffn_backward": ([S, I] + [P] * 10 + call, ctypes.c_int),
+            "moet_router_probs_workspace_size": ([S], Z),
+            "moet_router_probs": ([S] + [P] * 4 + call, ctypes.c_int),
+            "moet_route_backward_workspace_size": ([S], Z),
+            "moet_route_backward": ([S] + [P] * 9 + call, ctypes.c_int),
+            "moet_forward_workspace_size": ([S], Z),
+            "moet_forward": ([S, I] + [P] * 17 + call, ctypes.c_int),
+            "moet_backward_workspace_size": ([S, I], Z),
+            "moet_backward": ([S, I] + [P] * 19 + call, ctypes.c_int),
+        }
+        for name, (args, res) in sig.items():
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = args, res
+        _sig_lib = lib
+    return lib
+
+
+# ------------------------------------------------------------------- shared --
+
+_status: dict = {}  # device -> the status block of the calls that have no layer
+
+
+def _status_block(dev: int) -> torch.Tensor:
+    return torch.zeros(MOE_WS_MIN_BYTES, dtype=_U8, device=torch.device("cuda", dev))
+
+
+def _shared_status(dev: int) -> torch.Tensor:
+    t = _status.get(dev)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the status block of this device is made by the first call on it, which cannot be "
+                               "one that is captured: call train_status() before the capture")
+        t = _status_block(dev)
+        torch.cuda.synchronize(dev)  # zeroed before a call on any stream
+        t = _status.setdefault(dev, t)
+    return t
+
+
+def train_status(stream=None) -> int:
+    """Synchronises the stream, returns and clears the status word of this
+    module's functions on the current device (0 if all is well).  Raises
+    MoEError if a status bit is set.  A layer's calls have a word of their own
+    (``moe_get_device_status(layer.status)``)."""
+    return moe_get_device_status(_shared_status(torch.cuda.current_device()), stream)
+
+
+def _workspace(size_fn, shape, dev: int, *extra) -> torch.Tensor:
+    n = int(size_fn(ctypes.byref(shape), *extra))
+    if n == 0:
+        _check(MOE_ERR_UNSUPPORTED)
+    return torch.empty(n, dtype=_U8, device=torch.device("cuda", dev))
+
+
+def _out(t, shape, dtype, name: str, dev: int) -> torch.Tensor:
+    """`t` checked against a shape, or a new tensor of it."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    _addr(t, dtype, name, t.numel(), dev)
+    return t
+
+
+def _need(cond: bool, message: str) -> None:
+    if not cond:
+        raise ValueError(message)
+
+
+def _shaped(t, shape, dtype, name: str, dev: int) -> int:
+    """Address of `t`, which must have just this shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return _addr(t, dtype, name, t.numel(), dev)
+
+
+# --------------------------------------------------- activations in 8 bits --
+
+class A8Tensor:
+    """bf16 values [..., C] kept in 8 bits: codes int8 of that shape and scales
+    uint8 [..., ceil(C / 32)], the exponents (biased by 127) of the power of two
+    that 32 columns share (layout and rounding: include/moe_train.h)."""
+
+    __slots__ = ("codes", "scales")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
+        if codes.dtype != _I8 or scales.dtype != _U8:
+            raise TypeError(f"codes must be int8 and scales uint8, got {codes.dtype} and {scales.dtype}")
+        if codes.dim() < 1 or tuple(scales.shape) != (*codes.shape[:-1], -(-codes.shape[-1] // 32)):
+            raise ValueError(f"scales {tuple(scales.shape)} do not match codes {tuple(codes.shape)}")
+        self.codes, self.scales = codes, scales
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def _a8_new(shape, dev: int) -> A8Tensor:
+    q = A8Tensor.__new__(A8Tensor)
+    d = torch.device("cuda", dev)
+    q.codes = torch.empty(shape, dtype=_I8, device=d)
+    q.scales = torch.empty((*shape[:-1], -(-shape[-1] // 32)), dtype=_U8, device=d)
+    return q
+
+
+def _rows(shape) -> int:
+    n = 1
+    for v in shape[:-1]:
+        n *= v
+    return n
+
+
+def quantize_a8(x: torch.Tensor, stream=None) -> A8Tensor:
+    """bf16 x [..., C] (C % 8 == 0) -> :class:`A8Tensor`."""
+    if stream is not None:
+        with _on(stream):
+            return quantize_a8(x)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    dev, raw = _here()
+    src = _addr(x, _BF, "x", x.numel(), dev)
+    q = _a8_new(tuple(x.shape), dev)
+    rc = _lib().moet_quantize_a8(_rows(x.shape), x.shape[-1], src, q.codes.data_ptr(), q.scales.data_ptr(), raw)
+    if rc:
+        _check(rc)
+    return q
+
+
+def dequantize_a8(q: A8Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The bf16 values that `q` stands for."""
+    if stream is not None:
+        with _on(stream):
+            return dequantize_a8(q, out)
+    dev, raw = _here()
+    codes = _addr(q.codes, _I8, "codes", q.codes.numel(), dev)
+    scales = _addr(q.scales, _U8, "scales", q.scales.numel(), dev)
+    out = _out(out, q.codes.shape, _BF, "out", dev)
+    rc = _lib().moet_dequantize_a8(_rows(q.shape), q.shape[-1], codes, scales, out.data_ptr(), raw)
+    if rc:
+        _check(rc)
+    return out
+
+
+def _kept_ptrs(z, shape, name: str, dev: int):
+    """(keep_bits, address, scales' address) of bf16 values or an A8Tensor."""
+    if isinstance(z, A8Tensor):
+        a = _shaped(z.codes, shape, _I8, f"{name}.codes", dev)
+        return 8, a, _addr(z.scales, _U8, f"{name}.scales", z.scales.numel(), dev)
+    return 16, _shaped(z, shape, _BF, name, dev), None
+
+
+# ------------------------------------------------------- rows there and back --
+
+def _slot_shape(rows: torch.Tensor, slot: torch.Tensor, name: str) -> moe_shape:
+    _need(slot.dim() == 2, f"slot must be [T, k], got {tuple(slot.shape)}")
+    T, k = slot.shape
+    _need(rows.dim() == 2 and rows.shape[0] >= T * k, f"{name} must be [T * k, H] with T * k = {T * k}, got "
+          f"{tuple(rows.shape)}")
+    return make_shape(T, rows.shape[1], 8, max(k, 1), k)
+
+
+def dispatch_rows_backward(dxp: torch.Tensor, slot: torch.Tensor, out: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """The gradient of moe_dispatch_rows: dx[t] = sum of dxp[slot[t, j]] over
+    the kept slots (slot >= 0); dxp [T * k, H] in dispatch order."""
+    if stream is not None:
+        with _on(stream):
+            return dispatch_rows_backward(dxp, slot, out)
+    s = _slot_shape(dxp, slot, "dxp")
+    dev, raw = _here()
+    src, sl = _addr(dxp, _BF, "dxp", dxp.numel(), dev), _addr(slot, _I32, "slot", slot.numel(), dev)
+    out = _out(out, (s.T, s.H), _BF, "out", dev)
+    rc = _lib().moet_dispatch_rows_backward(ctypes.byref(s), src, sl, out.data_ptr(), raw)
+    if rc:
+        _check(rc)
+    return out
+
+
+def combine_backward(dy: torch.Tensor, Y: torch.Tensor, weights: torch.Tensor, slot: torch.Tensor,
+                     dY: torch.Tensor | None = None, dweights: torch.Tensor | None = None, stream=None):
+    """The gradients of moe_combine, (dY, dweights): dY[slot[t, j]] =
+    weights[t, j] dy[t], dweights[t, j] = <dy[t], Y[slot[t, j]]>, 0 for a dropped
+    slot.  Rows of dY that no slot names are not written."""
+    if stream is not None:
+        with _on(stream):
+            return combine_backward(dy, Y, weights, slot, dY, dweights)
+    s = _slot_shape(Y, slot, "Y")
+    dev, raw = _here()
+    p = (_shaped(dy, (s.T, s.H), _BF, "dy", dev), _addr(Y, _BF, "Y", Y.numel(), dev),
+         _shaped(weights, (s.T, s.k), _F32, "weights", dev), _addr(slot, _I32, "slot", slot.numel(), dev))
+    dY = _out(dY, Y.shape, _BF, "dY", dev)
+    dweights = _out(dweights, (s.T, s.k), _F32, "dweights", dev)
+    rc = _lib().moet_combine_backward(ctypes.byref(s), *p, dY.data_ptr(), dweights.data_ptr(), raw)
+    if rc:
+        _check(rc)
+    return dY, dweights
+
+
+# ------------------------------------------------------------- experts' FFN --
+
+def _ffn_shape(xp, w1, w2, act: str) -> moe_shape:
+    _need(w2.dim() == 3, f"w2 must be [E, F, H], got {tuple(w2.shape)}")
+    E, F, H = w2.shape
+    _need(xp.dim() == 2 and xp.shape[1] == H, f"xp must be [rows, {H}], got {tuple(xp.shape)}")
+    s = make_shape(xp.shape[0], H, F, E, 1, None, MOE_GATE_TOPK_SOFTMAX, act)
+    f1 = 2 * F if s.expert_act else F
+    _need(tuple(w1.shape) == (E, H, f1), f"w1 must be {(E, H, f1)} for act = {act!r}, got {tuple(w1.shape)}")
+    return s
+
+
+def _z_shape(rows: int, s: moe_shape):
+    return (rows, 2, s.F) if s.expert_act else (rows, s.F)
+
+
+def expert_ffn(xp: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, offsets: torch.Tensor, act: str = "gelu",
+               keep_bits: int = 16, stream=None):
+    """The experts' FFN on rows grouped by expert (rows [offsets[e], offsets[e + 1])
+    of xp belong to expert e): (Y, z), z the pre-activations xp W1 for the
+    backward pass, bf16 (keep_bits 16) or :class:`A8Tensor` (8), of shape
+    [rows, F] or [rows, 2, F] for "swiglu".  Rows outside every segment are not
+    written."""
+    if stream is not None:
+        with _on(stream):
+            return expert_ffn(xp, w1, w2, offsets, act, keep_bits)
+    s = _ffn_shape(xp, w1, w2, act)
+    dev, raw = _here()
+    rows = xp.shape[0]
+    p = (_addr(xp, _BF, "xp", xp.numel(), dev), _addr(w1, _BF, "w1", w1.numel(), dev),
+         _addr(w2, _BF, "w2", w2.numel(), dev), _shaped(offsets, (s.E + 1,), _I32, "offsets", dev))
+    Y = _out(None, (rows, s.H), _BF, "Y", dev)
+    if keep_bits == 8:
+        z = _a8_new(_z_shape(rows, s), dev)
+        zp = z.codes.data_ptr(), z.scales.data_ptr()
+    else:
+        z = _out(None, _z_shape(rows, s), _BF, "z", dev)
+        zp = z.data_ptr(), None
+    lib = _lib()
+    ws = _workspace(lib.moet_expert_ffn_workspace_size, s, dev)
+    rc = lib.moet_expert_ffn(ctypes.byref(s), keep_bits, *p, Y.data_ptr(), *zp, _shared_status(dev).data_ptr(),
+                             ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
+    return Y, z
+
+
+def expert_ffn_backward(xp: torch.Tensor, z, w1: torch.Tensor, w2: torch.Tensor, offsets: torch.Tensor,
+                        dY: torch.Tensor, act: str = "gelu", stream=None):
+    """The gradients of :func:`expert_ffn`, (dxp, dw1, dw2), from its inputs, the
+    kept z and dY.  Rows of dxp outside every segment are not written; experts
+    without rows get zeros."""
+    if stream is not None:
+        with _on(stream):
+            return expert_ffn_backward(xp, z, w1, w2, offsets, dY, act)
+    s = _ffn_shape(xp, w1, w2, act)
+    dev, raw = _here()
+    rows = xp.shape[0]
+    bits, zp, zs = _kept_ptrs(z, _z_shape(rows, s), "z", dev)
+    src = _addr(xp, _BF, "xp", xp.numel(), dev)
+    p = (_addr(w1, _BF, "w1", w1.numel(), dev), _addr(w2, _BF, "w2", w2.numel(), dev),
+         _shaped(offsets, (s.E + 1,), _I32, "offsets", dev), _shaped(dY, (rows, s.H), _BF, "dY", dev))
+    dxp, dw1, dw2 = (_out(None, t.shape, _BF, "gradient", dev) for t in (xp, w1, w2))
+    lib = _lib()
+    ws = _workspace(lib.moet_expert_ffn_backward_workspace_size, s, dev)
+    rc = lib.moet_expert_ffn_backward(ctypes.byref(s), bits, src, zp, zs, *p, dxp.data_ptr(), dw1.data_ptr(),
+                                      dw2.data_ptr(), _shared_status(dev).data_ptr(), ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
+    return dxp, dw1, dw2
+
+
+# ---------------------------------------------------------- router and gate --
+
+def _route_shape(x, w_router, k: int, gating: int) -> moe_shape:
+    _need(w_router.dim() == 2, f"w_router must be [H, E], got {tuple(w_router.shape)}")
+    H, E = w_router.shape
+    _need(x.dim() == 2 and x.shape[1] == H, f"x must be [T, {H}], got {tuple(x.shape)}")
+    return make_shape(x.shape[0], H, 8, E, k, None, gating)
+
+
+def router_probs(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """softmax(x W_router + bias) over all experts, fp32 [T, E]: what the
+    gradient of MOE_GATE_SOFTMAX_TOPK needs of the forward."""
+    if stream is not None:
+        with _on(stream):
+            return router_probs(x, w_router, bias)
+    s = _route_shape(x, w_router, 1, MOE_GATE_TOPK_SOFTMAX)
+    dev, raw = _here()
+    p = (_addr(x, _BF, "x", x.numel(), dev), _addr(w_router, _BF, "w_router", w_router.numel(), dev),
+         None if bias is None else _shaped(bias, (s.E,), _F32, "bias", dev))
+    probs = _out(None, (s.T, s.E), _F32, "probs", dev)
+    lib = _lib()
+    ws = _workspace(lib.moet_router_probs_workspace_size, s, dev)
+    rc = lib.moet_router_probs(ctypes.byref(s), *p, probs.data_ptr(), _shared_status(dev).data_ptr(),
+                               ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
+    return probs
+
+
+def route_backward(x: torch.Tensor, w_router: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                   dweights: torch.Tensor, gating: int = MOE_GATE_TOPK_SOFTMAX,
+                   probs: torch.Tensor | None = None, stream=None):
+    """The gradients of router and gate, (dx, dw_router, dbias), from those of the
+    gate weights [T, k]: dx the router's part alone, dbias that of a router bias.
+    probs (:func:`router_probs`) is needed for MOE_GATE_SOFTMAX_TOPK."""
+    if stream is not None:
+        with _on(stream):
+            return route_backward(x, w_router, ids, weights, dweights, gating, probs)
+    _need(ids.dim() == 2, f"ids must be [T, k], got {tuple(ids.shape)}")
+    s = _route_shape(x, w_router, ids.shape[1], gating)
+    dev, raw = _here()
+    tk = (s.T, s.k)
+    if gating == MOE_GATE_SOFTMAX_TOPK:
+        _need(probs is not None, "MOE_GATE_SOFTMAX_TOPK needs probs")
+        pp = _shaped(probs, (s.T, s.E), _F32, "probs", dev)
+    else:
+        pp = None
+    p = (_addr(x, _BF, "x", x.numel(), dev), _addr(w_router, _BF, "w_router", w_router.numel(), dev),
+         _shaped(ids, tk, _I32, "ids", dev), _shaped(weights, tk, _F32, "weights", dev), pp,
+         _shaped(dweights, tk, _F32, "dweights", dev))
+    dx = _out(None, x.shape, _BF, "dx", dev)
+    dw = _out(None, w_router.shape, _BF, "dw_router", dev)
+    db = _out(None, (s.E,), _F32, "dbias", dev)
+    lib = _lib()
+    ws = _workspace(lib.moet_route_backward_workspace_size, s, dev)
+    rc = lib.moet_route_backward(ctypes.byref(s), *p, dx.data_ptr(), dw.data_ptr(), db.data_ptr(),
+                                 _shared_status(dev).data_ptr(), ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------- the layer --
+
+class Gradients(NamedTuple):
+    """What :meth:`MoETrainLayer.backward` returns; dbias is None unless asked for."""
+    dx: torch.Tensor
+    dw_router: torch.Tensor
+    dbias: torch.Tensor | None
+    dw1: torch.Tensor
+    dw2: torch.Tensor
+
+
+def _version(t: torch.Tensor):
+    return None if t.is_inference() else t._version
+
+
+class Saved:
+    """What a forward keeps for its backward: z and, with keep_bits 8, x in 8
+    bits (else x itself), the routing (``routing``) and, for
+    MOE_GATE_SOFTMAX_TOPK, the router's probabilities."""
+
+    __slots__ = ("shape", "x", "z", "routing", "probs", "versions")
+
+    def nbytes(self) -> int:
+        """Device bytes held (x itself not counted with keep_bits 16)."""
+        ts = [self.routing.ids, self.routing.weights, self.routing.counts, self.routing.offsets, self.routing.perm,
+              self.routing.slot]
+        for t in (self.z, self.x, self.probs):
+            if isinstance(t, A8Tensor):
+                ts += [t.codes, t.scales]
+            elif t is not None and t is not self.x:
+                ts.append(t)
+        return sum(t.numel() * t.element_size() for t in ts)
+
+
+class MoETrainLayer:
+    """A layer's weights for training: bf16 w_router [H, E], w1 [E, H, F] ([E, H,
+    2F] = [gate | up] for "swiglu"), w2 [E, F, H] and an optional fp32 bias [E]
+    on the logits, all updated in place by the caller's optimizer.
+
+    ``y, saved = layer(x)`` runs the forward and keeps what its gradients need, in
+    16 or in 8 bits (`keep_bits`); ``layer.backward(saved, dy)`` returns
+    :class:`Gradients`.  A `saved` may be used once or several times, as long as
+    x (with keep_bits 16) and the weights are what they were.  Both calls run on
+    the current stream (or `stream`), allocate what they return and their
+    workspace, and may be captured into CUDA graphs; several forwards may be in
+    flight before their backwards.  ``moe_get_device_status(layer.status)`` reads
+    the device status of all calls so far."""
+
+    def __init__(self, w_router, w1, w2, k: int, bias=None, capacity_factor=None,
+                 gating: int = MOE_GATE_TOPK_SOFTMAX, act: str = "gelu", keep_bits: int = 16):
+        _need(w2.dim() == 3, f"w2 must be [E, F, H], got {tuple(w2.shape)}")
+        _need(keep_bits in (8, 16), f"keep_bits = {keep_bits}: 8 or 16")
+        self.E, self.F, self.H = w2.shape
+        self.k, self.act, self.keep_bits = int(k), act, int(keep_bits)
+        self.capacity_factor, self.gating = capacity_factor, int(gating)
+        self.w_router, self.w1, self.w2, self.bias = w_router, w1, w2, bias
+        s = self._shape(1)
+        dev = w_router.device.index
+        for (t, dt, shape, name) in self._params(s):
+            check_tensor(t, dt, name, 0, dev)
+            _need(tuple(t.shape) == shape, f"{name} must be {shape}, got {tuple(t.shape)}")
+        if int(_lib().moet_forward_workspace_size(ctypes.byref(s))) == 0:
+            _check(MOE_ERR_UNSUPPORTED)
+        self.status = _status_block(dev)
+        torch.cuda.synchronize(dev)  # zeroed before a call on any stream
+
+    def _params(self, s):
+        f1 = 2 * self.F if s.expert_act else self.F
+        p = [(self.w_router, _BF, (self.H, self.E), "w_router"), (self.w1, _BF, (self.E, self.H, f1), "w1"),
+             (self.w2, _BF, (self.E, self.F, self.H), "w2")]
+        if self.bias is not None:
+            p.append((self.bias, _F32, (self.E,), "bias"))
+        return p
+
+    def _shape(self, T: int) -> moe_shape:
+        return make_shape(T, self.H, self.F, self.E, self.k, self.capacity_factor, self.gating, self.act)
+
+    def _weights(self, s, dev: int):
+        p = [_shaped(t, shape, dt, name, dev) for t, dt, shape, name in self._params(s)]
+        return p if self.bias is not None else p + [None]
+
+    def __call__(self, x: torch.Tensor, stream=None):
+        """(y, saved)"""
+        if stream is not None:
+            with _on(stream):
+                return self(x)
+        _need(x.dim() == 2 and x.shape[1] == self.H, f"x must be [T, {self.H}], got {tuple(x.shape)}")
+        dev, raw = _here()
+        T, k, E = x.shape[0], self.k, self.E
+        s = self._shape(T)
+        wr, w1, w2, b = self._weights(s, dev)
+        src = _addr(x, _BF, "x", T * self.H, dev)
+        d = torch.device("cuda", dev)
+        lib = _lib()
+        ws = _workspace(lib.moet_forward_workspace_size, s, dev)
+        y = torch.empty((T, self.H), dtype=_BF, device=d)
+        n = T * k
+        # the routing's tensors in one allocation, each on a 16-byte boundary
+        n4, e4 = (n + 3) // 4 * 4, (E + 4) // 4 * 4
+        ints = torch.empty(3 * n4 + 2 * e4, dtype=_I32, device=d)
+        r = RoutingBuffers(ids=ints[:n].view(T, k), weights=torch.empty((T, k), dtype=_F32, device=d),
+                           counts=ints[3 * n4:3 * n4 + E], offsets=ints[3 * n4 + e4:3 * n4 + e4 + E + 1],
+                           perm=ints[n4:n4 + n], slot=ints[2 * n4:2 * n4 + n].view(T, k))
+        v = Saved()
+        v.shape, v.routing, v.probs = s, r, None
+        if self.keep_bits == 8:
+            v.z, v.x = _a8_new(_z_shape(n, s), dev), _a8_new((T, self.H), dev)
+            kept = v.z.codes.data_ptr(), v.z.scales.data_ptr(), v.x.codes.data_ptr(), v.x.scales.data_ptr()
+        else:
+            v.z, v.x = torch.empty(_z_shape(n, s), dtype=_BF, device=d), x
+            kept = v.z.data_ptr(), None, None, None
+        if self.gating == MOE_GATE_SOFTMAX_TOPK:
+            v.probs = torch.empty((T, E), dtype=_F32, device=d)
+        v.versions = self._versions(v)
+        rc = lib.moet_forward(ctypes.byref(s), self.keep_bits, src, wr, b, w1, w2, y.data_ptr(), r.ids.data_ptr(),
+                              r.weights.data_ptr(), r.counts.data_ptr(), r.offsets.data_ptr(), r.perm.data_ptr(),
+                              r.slot.data_ptr(), *kept, None if v.probs is None else v.probs.data_ptr(),
+                              self.status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+        if rc:
+            _check(rc)
+        return y, v
+
+    def _versions(self, saved):
+        ts = [self.w_router, self.w1, self.w2]
+        if not isinstance(saved.x, A8Tensor):
+            ts.append(saved.x)
+        return [(t.data_ptr(), _version(t)) for t in ts]
+
+    def backward(self, saved: Saved, dy: torch.Tensor, bias_grad: bool = False, stream=None) -> Gradients:
+        """The gradients of the forward that `saved` comes from, for the gradient
+        dy [T, H] of its y; bias_grad: dbias too (fp32 [E])."""
+        if stream is not None:
+            with _on(stream):
+                return self.backward(saved, dy, bias_grad)
+        if not isinstance(saved, Saved):
+            raise TypeError("saved must be what a forward of this layer returned")
+        s, r = saved.shape, saved.routing
+        _need((s.H, s.F, s.E, s.k) == (self.H, self.F, self.E, self.k), "saved is of a layer of another shape")
+        _need(self._versions(saved) == saved.versions,
+              "x or a weight was changed or replaced after the forward that saved is of")
+        dev, raw = _here()
+        T = s.T
+        wr, w1, w2, _ = self._weights(s, dev)
+        g = _shaped(dy, (T, s.H), _BF, "dy", dev)
+        bits, zp, zs = _kept_ptrs(saved.z, saved.z.shape, "z", dev)
+        _, xp, xs = _kept_ptrs(saved.x, (T, s.H), "x", dev)
+        d = torch.device("cuda", dev)
+        lib = _lib()
+        ws = _workspace(lib.moet_backward_workspace_size, s, dev, bits)
+        out = Gradients(torch.empty((T, s.H), dtype=_BF, device=d), torch.empty_like(self.w_router),
+                        torch.empty(s.E, dtype=_F32, device=d) if bias_grad else None,
+                        torch.empty_like(self.w1), torch.empty_like(self.w2))
+        rc = lib.moet_backward(ctypes.byref(s), bits, g, xp, xs, wr, w1, w2, r.ids.data_ptr(), r.weights.data_ptr(),
+                               r.offsets.data_ptr(), r.perm.data_ptr(), r.slot.data_ptr(), zp, zs,
+                               None if saved.probs is None else saved.probs.data_ptr(), out.dx.data_ptr(),
+                               out.dw_router.data_ptr(), None if out.dbias is None else out.dbias.data_ptr(),
+                               out.dw1.data_ptr(), out.dw2.data_ptr(), self.status.data_ptr(), ws.data_ptr(),
+                               ws.numel(), raw)
+        if rc:
+            _check(rc)
+        return out
