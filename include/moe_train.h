@@ -22,8 +22,10 @@
  * SwiGLU z = (x W_gate, x W_up).
  *
  * Precision: bf16 operands, fp32 accumulation and epilogues; w h and dz are
- * rounded to bf16 once, as the tensor cores' operands; dlogits travel as two
- * bf16 numbers (16 bits and the rest); every output is rounded once.  No
+ * rounded to bf16 once, as the tensor cores' operands, and so is the forward's
+ * h; dlogits travel as two bf16 numbers (16 bits and the rest); expert outputs
+ * and their rows' gradients stay in fp32 inside a layer's call; every output is
+ * rounded once.  No
  * atomics: results do not depend on timing.
  *
  * Conventions are moe.h's (device pointers, 16-byte aligned, row-major and
@@ -130,8 +132,8 @@ MOE_API int moet_route_backward(const moe_shape* s, const uint16_t* x, const uin
  * The layer's forward for training: moe_forward's outputs, z (as
  * moet_expert_ffn), with keep_bits 8 also x in 8 bits (xk [T, H] codes,
  * xk_scales; else ignored) and with MOE_GATE_SOFTMAX_TOPK probs (else ignored).
- * y may differ from moe_forward's by roundings: h is rounded from the same fp32
- * z, but small batches sum it in another order there.
+ * y may differ from moe_forward's by roundings: expert outputs are not rounded to
+ * bf16 before they are combined.
  */
 MOE_API size_t moet_forward_workspace_size(const moe_shape* s);
 MOE_API int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x,

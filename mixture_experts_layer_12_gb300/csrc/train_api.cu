@@ -135,14 +135,21 @@ int fwd_product(const moe_shape* s, int bits, const uint16_t* xp, const uint16_t
   return MOE_OK;
 }
 
-// Y = h W2 by the forward's own kernel
+// Y = h W2: rounded to bf16 by the forward's own kernel, or kept in fp32
 int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, const int32_t* offsets, uint16_t* Y,
-                  void* status, cudaStream_t st) {
+                  float* Y32, void* status, cudaStream_t st) {
   const size_t rows = rows_of(s);
   CUtensorMap ta, tb, ta64;
   TRY(map_rows(&ta, h, s->F, rows, 128, "h"));
   TRY(map_rows(&ta64, h, s->F, rows, 64, "h"));
   TRY(map_weights(&tb, w2, s->H, s->F, s->E, 64, "W2"));
+  const int64_t ub = row_tiles(rows, s->E, s->H, kGemmBN);
+  if (Y32) {
+    TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->H, s->F, status);
+    a.out32 = Y32;
+    CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, ub, st), "expert GEMM2 launch");
+    return MOE_OK;
+  }
   GemmArgs g = {};
   g.offsets = offsets;
   g.E = g.E_w = s->E;
@@ -153,13 +160,13 @@ int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, con
   g.splits = 1;
   g.status = static_cast<int*>(status);
   g.wait_limit_ns = kWaitLimitNs;
-  const int64_t ub = row_tiles(rows, s->E, s->H, kGemmBN);
   CUDA_TRY(launch_grouped_gemm(kGemmPlain, ta, tb, ta64, g, (int)(ub < (1 << 30) ? ub : (1 << 30)), st, true),
            "expert GEMM2 launch");
   return MOE_OK;
 }
 
-// The experts' gradients from padded xp and dyp; dxp compact, may be dyp.
+// The experts' gradients from padded xp and dyp; dxp compact, in bf16 or (dxp32)
+// in fp32.
 struct FfnGrad {
   int bits;
   const uint16_t *xp, *dyp, *w1, *w2;
@@ -170,6 +177,7 @@ struct FfnGrad {
   const int32_t* perm;
   float* part;
   uint16_t *hw, *dz, *dxp, *dw1, *dw2;
+  float* dxp32;
 };
 int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream_t st) {
   const size_t rows = rows_of(s), pad = pad_of(s);
@@ -214,7 +222,8 @@ int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream
   TRY(map_weights(&tb, f.w1, f1, s->H, s->E, 128, "W1"));
   a = gemm_args(seg, 0, s->H, f1, status);
   a.out = f.dxp;
-  CUDA_TRY(launch_train_gemm(kTrainRows, ta, tb, ta64, a, row_tiles(rows, s->E, s->H, 256), st),
+  a.out32 = f.dxp32;
+  CUDA_TRY(launch_train_gemm(f.dxp32 ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a, row_tiles(rows, s->E, s->H, 256), st),
            "x gradient launch");
   return MOE_OK;
 }
@@ -250,8 +259,8 @@ RouteGradWs route_grad_ws(const moe_shape* s, Carve& c) {
   return r;
 }
 int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackwardArgs& gate, const uint16_t* x,
-                    const uint16_t* w_router, uint16_t* dx, uint16_t* dw_router, float* db, void* status,
-                    cudaStream_t st) {
+                    const uint16_t* w_router, uint16_t* dx, float* dx32, uint16_t* dw_router, float* db,
+                    void* status, cudaStream_t st) {
   const int ep = ep_of(s);
   CUDA_TRY(launch_gate_backward(gate, st), "gate gradient launch");
   CUDA_TRY(launch_router_twice(w_router, s->H, s->E, ep, r.w2, st), "router weights launch");
@@ -280,7 +289,8 @@ int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackward
   TRY(map_weights(&tb, r.w2, 2 * ep, s->H, 1, 128, "W_router"));
   a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, s->H, 2 * ep, status);
   a.out = dx;
-  CUDA_TRY(launch_train_gemm(kTrainRows, ta, tb, ta64, a, blocks256(s->T) * blocks256(s->H), st),
+  a.out32 = dx32;
+  CUDA_TRY(launch_train_gemm(dx32 ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a, blocks256(s->T) * blocks256(s->H), st),
            "router x gradient launch");
   return MOE_OK;
 }
@@ -324,7 +334,7 @@ int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* 
   TRY(map_weights(&tb, w_router, ep, s->H, 1, 64, "W_router"));
   TrainGemmArgs a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, ep, s->H, status);
   a.out32 = p.logits;
-  CUDA_TRY(launch_train_gemm(kTrainLogits, ta, tb, ta64, a, blocks256(s->T) * blocks256(ep), st),
+  CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, blocks256(s->T) * blocks256(ep), st),
            "router logits launch");
   CUDA_TRY(launch_router_softmax(p.logits, ep, b_router, s->T, s->E, probs, st), "router softmax launch");
   return MOE_OK;
@@ -357,7 +367,8 @@ FfnGradWs ffn_grad_ws(const moe_shape* s, Carve& c) {
 struct ForwardWs {
   void* route;
   size_t route_bytes;
-  uint16_t* rows;  // xp, then the experts' outputs
+  uint16_t* xp;
+  float* Y;
   FfnWs ffn;
   ProbsWs probs;
 };
@@ -365,7 +376,8 @@ ForwardWs forward_ws(const moe_shape* s, Carve& c) {
   ForwardWs w = {};
   w.route_bytes = moe_route_workspace_size(s);
   w.route = c.take<char>(w.route_bytes);
-  w.rows = c.take<uint16_t>(rows_of(s) * s->H);
+  w.Y = c.take<float>(rows_of(s) * s->H);
+  w.xp = reinterpret_cast<uint16_t*>(w.Y);  // read before Y is written
   w.ffn = ffn_ws(s, c);
   if (s->gating == MOE_GATE_SOFTMAX_TOPK) w.probs = probs_ws(s, c);
   return w;
@@ -376,7 +388,8 @@ struct BackwardWs {
   uint16_t* x;  // bf16 of x kept in 8 bits
   float* part;
   RouteGradWs route;
-  uint16_t* dxr;  // the router's part of dx
+  float* dxp;
+  float* dxr;  // the router's part of dx
 };
 BackwardWs backward_ws(const moe_shape* s, int bits, Carve& c) {
   BackwardWs w;
@@ -384,7 +397,8 @@ BackwardWs backward_ws(const moe_shape* s, int bits, Carve& c) {
   w.x = c.take<uint16_t>(bits == 8 ? (size_t)s->T * s->H : 0);
   w.part = c.take<float>(rows_of(s) * ((s->F + 63) / 64));
   w.route = route_grad_ws(s, c);
-  w.dxr = c.take<uint16_t>((size_t)s->T * s->H);
+  w.dxp = c.take<float>(rows_of(s) * s->H);
+  w.dxr = c.take<float>((size_t)s->T * s->H);
   return w;
 }
 
@@ -463,7 +477,7 @@ int moet_dispatch_rows_backward(const moe_shape* s, const uint16_t* dxp, const i
   REQUIRE_PTR(dx);
   int sms = 0;
   TRY(device_setup(&sms));
-  RowsSumArgs a = {dxp, slot, nullptr, s->T, s->H, s->k, dx};
+  RowsSumArgs a = {dxp, nullptr, nullptr, slot, nullptr, s->T, s->H, s->k, dx};
   CUDA_TRY(launch_rows_sum(a, stream_of(stream)), "row sums launch");
   return MOE_OK;
 }
@@ -511,7 +525,7 @@ int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, c
   Carve c(ws);
   const FfnWs w = ffn_ws(s, c);
   TRY(fwd_product(s, keep_bits, xp, w1, offsets, w.h, z, z_scales, nullptr, status, stream_of(stream)));
-  return plain_product(s, w.h, w2, offsets, Y, status, stream_of(stream));
+  return plain_product(s, w.h, w2, offsets, Y, nullptr, status, stream_of(stream));
 }
 
 size_t moet_expert_ffn_backward_workspace_size(const moe_shape* s) {
@@ -549,7 +563,7 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
   GatherArgs ga = {segments(s, offsets), nullptr, s->T, s->H, s->k, {xp, dY}, {w.xp, w.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.xp, w.dyp, w1, w2, offsets, z, z_scales, nullptr, nullptr, nullptr,
-               w.hw, w.dz, dxp, dw1, dw2};
+               w.hw, w.dz, dxp, dw1, dw2, nullptr};
   return ffn_gradients(s, f, status, st);
 }
 
@@ -609,7 +623,7 @@ int moet_route_backward(const moe_shape* s, const uint16_t* x, const uint16_t* w
   const RouteGradWs r = route_grad_ws(s, c);
   GateBackwardArgs g = gate_args(s, r, ids, weights, probs);
   g.dw = dweights;
-  return route_gradients(s, r, g, x, w_router, dx, dw_router, db, status, st);
+  return route_gradients(s, r, g, x, w_router, dx, nullptr, dw_router, db, status, st);
 }
 
 size_t moet_forward_workspace_size(const moe_shape* s) {
@@ -657,14 +671,15 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
     TRY(router_probs(s, sms, w.probs, x, w_router, b_router, probs, status, st));
   if (keep_bits == 8)
     CUDA_TRY(launch_quantize_a8(s->T, s->H, x, xk, xk_scales, sms, st), "quantize launch");
-  PermuteArgs pa = {x, perm, offsets, s->T, s->H, s->k, s->E, w.rows, nullptr, nullptr};
+  PermuteArgs pa = {x, perm, offsets, s->T, s->H, s->k, s->E, w.xp, nullptr, nullptr};
   CUDA_TRY(launch_permute(pa, sms, st, true), "permute launch");
   // the route's own status word is taken over by the next product
-  TRY(fwd_product(s, keep_bits, w.rows, w1, offsets, w.ffn.h, z, z_scales, static_cast<const int*>(w.route),
+  TRY(fwd_product(s, keep_bits, w.xp, w1, offsets, w.ffn.h, z, z_scales, static_cast<const int*>(w.route),
                   status, st));
-  TRY(plain_product(s, w.ffn.h, w2, offsets, w.rows, status, st));
-  CombineArgs ca = {w.rows, weights, slot, s->T, s->H, s->k, y, nullptr, 1, 0};
-  CUDA_TRY(launch_combine(ca, st, true), "combine launch");
+  // the experts' outputs stay in fp32: y is rounded once
+  TRY(plain_product(s, w.ffn.h, w2, offsets, nullptr, w.Y, status, st));
+  RowsSumArgs ca = {nullptr, w.Y, weights, slot, nullptr, s->T, s->H, s->k, y};
+  CUDA_TRY(launch_rows_sum(ca, st), "combine launch");
   return MOE_OK;
 }
 
@@ -725,18 +740,16 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
   }
   GatherArgs ga = {segments(s, offsets), perm, s->T, s->H, s->k, {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
-  // dxp takes dyp's place: its product is the last of the four
-  uint16_t* dxp = w.ffn.dyp;
   FfnGrad f = {keep_bits, w.ffn.xp, w.ffn.dyp, w1, w2, offsets, z, z_scales, weights, perm, w.part,
-               w.ffn.hw, w.ffn.dz, dxp, dw1, dw2};
+               w.ffn.hw, w.ffn.dz, nullptr, dw1, dw2, w.dxp};
   TRY(ffn_gradients(s, f, status, st));
   GateBackwardArgs g = gate_args(s, w.route, ids, weights, probs);
   g.part = w.part;
   g.slot = slot;
   g.rows = (int)rows_of(s);
   g.units = (s->F + 63) / 64;
-  TRY(route_gradients(s, w.route, g, xb, w_router, w.dxr, dw_router, db, status, st));
-  RowsSumArgs ra = {dxp, slot, w.dxr, s->T, s->H, s->k, dx};
+  TRY(route_gradients(s, w.route, g, xb, w_router, nullptr, w.dxr, dw_router, db, status, st));
+  RowsSumArgs ra = {nullptr, w.dxp, nullptr, slot, w.dxr, s->T, s->H, s->k, dx};
   CUDA_TRY(launch_rows_sum(ra, st), "row sums launch");
   return MOE_OK;
 }

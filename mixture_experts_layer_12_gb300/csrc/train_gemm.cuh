@@ -7,7 +7,7 @@
 //          dz = w g act'(z), w h, and <g, h> (the gate weight's gradient)
 //   Rows   out = A_e W[e]^T                     (dxp = dz W1^T)
 //   Wgrad  out[e] = A_e^T B_e                   (dW2 = (w h)^T dy, dW1 = xp^T dz)
-//   Logits out = A W in fp32                    (the router's)
+//   Plain  out = A_e W[e] in fp32               (Y = h W2, the router's logits)
 //
 // One design serves all (as the forward's expert GEMM): CTA pairs run the
 // 2-SM tcgen05.mma (M = 256, N = 256, K = 16, fp32 in TMEM), each CTA holding
@@ -66,7 +66,9 @@ struct TrainCtrl {
   int tile_start[kMaxExperts + 1];
   SegTable seg;
 };
-constexpr size_t T_SMEM_BYTES = 1024 + (size_t)TSTAGES * T_STAGE_BYTES + sizeof(TrainCtrl);
+constexpr int T_TURN = 2048;  // a warp's 32 rows x 64 bytes between threads and memory
+constexpr size_t T_SMEM_BYTES =
+    1024 + (size_t)TSTAGES * T_STAGE_BYTES + T_EPI_WARPS * T_TURN + sizeof(TrainCtrl);
 static_assert(T_SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 template <int OP>
@@ -77,8 +79,9 @@ struct TrainTraits {
   static constexpr bool PAIRED = OP == kTrainFwdSwiGLU;  // a tile holds 128 gate and 128 up columns
   static constexpr bool WGRAD = OP == kTrainWgrad || OP == kTrainWgradF32;
   static constexpr bool A_MN = WGRAD;
-  static constexpr bool B_MN = !(BWD || OP == kTrainRows);
-  static constexpr bool A_PADDED = !(FWD || OP == kTrainLogits);
+  static constexpr bool B_MN = !(BWD || OP == kTrainRows || OP == kTrainRowsF32);
+  static constexpr bool A_PADDED = !(FWD || OP == kTrainPlain);
+  static constexpr bool OUT32 = OP == kTrainPlain || OP == kTrainWgradF32 || OP == kTrainRowsF32;
   static constexpr int BN_OUT = PAIRED ? TBN / 2 : TBN;
 };
 
@@ -164,32 +167,109 @@ __device__ __forceinline__ void train_gelu_grad(float z, float& h, float& d) {
 }
 __device__ __forceinline__ float train_sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
 
-// eight columns as bf16, 16 bytes
-__device__ __forceinline__ void train_store8(uint16_t* dst, const float* f) {
+// A warp's 32 rows x 32 columns between threads (one row each, as TMEM gives
+// them) and memory (where 4 lanes together read or write a row's 64 bytes, or 32
+// of 8-bit codes): 2 KB of shared memory per warp, rows of four 16-byte pieces
+// whose places are turned so that neither side meets a bank twice.  Straight from
+// the threads a warp's access met 32 rows at once, 16 bytes each: the weight
+// gradients of 64 experts of 2048 x 2816 took 325 us.
+struct Turn {
+  uint32_t base;  // shared-memory address of the warp's buffer
+  int lane;
+  __device__ __forceinline__ uint32_t own(int j) const {  // piece j of this thread's row
+    return base + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+  }
+  __device__ __forceinline__ uint32_t at(int row, int j) const {
+    return base + row * 64 + ((j ^ ((row >> 1) & 3)) << 4);
+  }
+};
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts8(uint32_t a, const uint2& v) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 train_pack8(const float* f) {
   uint4 pk;
   pk.x = pack_bf16x2(f[0], f[1]);
   pk.y = pack_bf16x2(f[2], f[3]);
   pk.z = pack_bf16x2(f[4], f[5]);
   pk.w = pack_bf16x2(f[6], f[7]);
-  *reinterpret_cast<uint4*>(dst) = pk;
+  return pk;
 }
 
-// Keeps 32 columns of z (those below `valid`, a multiple of 8, exist) at
-// column `col` of half `hf` of row `row`.
-__device__ __forceinline__ void train_keep(const TrainGemmArgs& p, bool gated, size_t row, int hf, int col,
-                                           int valid, const uint32_t (&v)[32]) {
-  const int halves = gated ? 2 : 1;
-  const size_t at = (row * halves + hf) * (size_t)p.N + col;
-  if (p.keep_bits == 16) {
-    uint16_t* dst = static_cast<uint16_t*>(p.z) + at;
+// The warp's block to memory: rows 0 .. n_rows - 1 of 32 at dst + row * pitch
+// (bytes), the first `pieces` 16-byte pieces of each.
+__device__ __forceinline__ void turn_store(const Turn& t, uint8_t* dst, size_t pitch, int n_rows, int pieces) {
+  __syncwarp();
+  const int j = t.lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (t.lane >> 2);
+    const uint4 v = lds16(t.at(row, j));
+    if (row < n_rows && j < pieces) *reinterpret_cast<uint4*>(dst + row * pitch + j * 16) = v;
+  }
+  __syncwarp();
+}
+// 32 fp32 or bf16 values of every thread's row.
+__device__ __forceinline__ void turn_store_bf16(const Turn& t, const float (&f)[32], uint16_t* dst, size_t cols,
+                                                int n_rows, int valid) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) sts16(t.own(g), train_pack8(f + 8 * g));
+  turn_store(t, reinterpret_cast<uint8_t*>(dst), cols * 2, n_rows, valid >> 3);
+}
+__device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v)[32], float* dst, size_t cols,
+                                               int n_rows, int valid) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
-      if (g * 8 < valid) {
-        float f[8];
+      sts16(t.own(g), make_uint4(v[16 * h + 4 * g], v[16 * h + 4 * g + 1], v[16 * h + 4 * g + 2],
+                                 v[16 * h + 4 * g + 3]));
+    turn_store(t, reinterpret_cast<uint8_t*>(dst + 16 * h), cols * 4, n_rows, (valid >> 2) - 4 * h);
+  }
+}
+// 32 codes of every thread's row: 8-byte pieces, as rows start on 8 bytes only.
+__device__ __forceinline__ void turn_store_codes(const Turn& t, const uint2 (&q)[4], int8_t* dst, size_t cols,
+                                                 int n_rows, int valid) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[g * 8 + i]);
-        train_store8(dst + g * 8, f);
-      }
+  for (int g = 0; g < 4; ++g) sts8(t.own(g), q[g]);
+  __syncwarp();
+  const int j = t.lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (t.lane >> 2);
+    const uint2 v = lds8(t.at(row, j));
+    if (row < n_rows && j * 8 < valid) *reinterpret_cast<uint2*>(dst + row * cols + j * 8) = v;
+  }
+  __syncwarp();
+}
+
+// Keeps a warp's 32 columns of z (those below `valid`, a multiple of 8, exist)
+// at column `col` of half `hf` of rows row0 ..
+__device__ __forceinline__ void train_keep(const TrainGemmArgs& p, const Turn& t, int halves, size_t row0, int hf,
+                                           int col, int n_rows, int valid, const uint32_t (&v)[32]) {
+  const size_t pitch = (size_t)halves * p.N;
+  const size_t at = row0 * pitch + (size_t)hf * p.N + col;
+  if (p.keep_bits == 16) {
+    float f[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+    turn_store_bf16(t, f, static_cast<uint16_t*>(p.z) + at, pitch, n_rows, valid);
     return;
   }
   uint32_t m = 0;
@@ -197,71 +277,79 @@ __device__ __forceinline__ void train_keep(const TrainGemmArgs& p, bool gated, s
   for (int i = 0; i < 32; ++i) m = max(m, i < valid ? v[i] & 0x7fffffffu : 0u);
   const uint32_t b = a8_scale_byte(m);
   const float inv = a8_inverse(b);
-  int8_t* dst = static_cast<int8_t*>(p.z) + at;
+  uint2 q[4];
 #pragma unroll
-  for (int g = 0; g < 4; ++g)
-    if (g * 8 < valid) {
-      uint32_t q[2] = {0u, 0u};
+  for (int g = 0; g < 4; ++g) {
+    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        q[i / 4] |= ((uint32_t)a8_code(__uint_as_float(v[g * 8 + i]), inv, b) & 0xffu) << (8 * (i % 4));
-      *reinterpret_cast<uint2*>(dst + g * 8) = make_uint2(q[0], q[1]);
-    }
+    for (int i = 0; i < 8; ++i)
+      w[i / 4] |= ((uint32_t)a8_code(__uint_as_float(v[g * 8 + i]), inv, b) & 0xffu) << (8 * (i % 4));
+    q[g] = make_uint2(w[0], w[1]);
+  }
+  turn_store_codes(t, q, static_cast<int8_t*>(p.z) + at, pitch, n_rows, valid);
   const int groups = (p.N + 31) / 32;
-  p.z_scales[(row * halves + hf) * (size_t)groups + (col >> 5)] = (uint8_t)b;
+  if (t.lane < n_rows)
+    p.z_scales[((row0 + t.lane) * halves + hf) * (size_t)groups + (col >> 5)] = (uint8_t)b;
 }
 
-// 32 kept columns on their way from memory: 16 words of bf16, or 8 words of
-// codes and the group's scale byte.
+// 32 kept columns of a warp's rows on their way from memory: four pieces of
+// other threads' rows (16 bytes of bf16 or 8 of codes), and this thread's scale.
 struct KeptChunk {
-  uint32_t w[16];
+  uint4 w[4];
   uint32_t b;
 };
-__device__ __forceinline__ void train_load_kept(const TrainGemmArgs& p, int halves, size_t row, int hf,
-                                                int col, bool ok, KeptChunk& k) {
+__device__ __forceinline__ void train_load_kept(const TrainGemmArgs& p, int lane, int halves, size_t row0, int hf,
+                                                int col, int n_rows, KeptChunk& k) {
+  const size_t pitch = (size_t)halves * p.N;
+  const size_t at = row0 * pitch + (size_t)hf * p.N + col;
+  const int j = lane & 3;
+  const bool col_ok = col + j * 8 < p.N;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) k.w[i] = 0u;
-  k.b = 127u;
-  if (!ok || col >= p.N) return;
-  const size_t at = (row * halves + hf) * (size_t)p.N + col;
-  const int valid = p.N - col;
-  if (p.keep_bits == 16) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + at);
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (g * 8 < valid) {
-        const uint4 u = __ldg(src + g);
-        k.w[4 * g] = u.x;
-        k.w[4 * g + 1] = u.y;
-        k.w[4 * g + 2] = u.z;
-        k.w[4 * g + 3] = u.w;
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (lane >> 2);
+    k.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < n_rows && col_ok) {
+      const size_t o = at + row * pitch + j * 8;
+      if (p.keep_bits == 16) {
+        k.w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + o));
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.z) + o));
+        k.w[i].x = u.x;
+        k.w[i].y = u.y;
       }
-  } else {
-    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.z) + at);
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      if (g * 8 < valid) {
-        const uint2 u = __ldg(src + g);
-        k.w[2 * g] = u.x;
-        k.w[2 * g + 1] = u.y;
-      }
-    const int groups = (p.N + 31) / 32;
-    k.b = __ldg(p.z_scales + (row * halves + hf) * (size_t)groups + (col >> 5));
-  }
-}
-// columns 8 g .. 8 g + 7 of a chunk
-__device__ __forceinline__ void train_kept8(const TrainGemmArgs& p, const KeptChunk& k, int g, float* f) {
-  if (p.keep_bits == 16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_lo(k.w[4 * g + i]);
-      f[2 * i + 1] = bf16_hi(k.w[4 * g + i]);
     }
-  } else {
-    const float s = a8_scale(k.b);
-    a8_values(k.w[2 * g], s, f);
-    a8_values(k.w[2 * g + 1], s, f + 4);
   }
+  k.b = 127u;
+  if (p.keep_bits == 8 && lane < n_rows && col < p.N)
+    k.b = __ldg(p.z_scales + ((row0 + lane) * halves + hf) * (size_t)((p.N + 31) / 32) + (col >> 5));
+}
+// ... and as 32 values of this thread's row.
+__device__ __forceinline__ void train_kept(const TrainGemmArgs& p, const Turn& t, const KeptChunk& k,
+                                           float (&f)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = t.at(i * 8 + (t.lane >> 2), t.lane & 3);
+    if (p.keep_bits == 16) sts16(a, k.w[i]); else sts8(a, make_uint2(k.w[i].x, k.w[i].y));
+  }
+  __syncwarp();
+  const float s = a8_scale(k.b);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (p.keep_bits == 16) {
+      const uint4 u = lds16(t.own(g));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[8 * g + 2 * i] = bf16_lo(w[i]);
+        f[8 * g + 2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+      const uint2 u = lds8(t.own(g));
+      a8_values(u.x, s, f + 8 * g);
+      a8_values(u.y, s, f + 8 * g + 4);
+    }
+  }
+  __syncwarp();
 }
 
 template <int OP>
@@ -274,7 +362,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + TSTAGES * T_OP_BYTES;
-  TrainCtrl& c = *reinterpret_cast<TrainCtrl*>(smem + TSTAGES * T_STAGE_BYTES);
+  uint8_t* sTurn = smem + TSTAGES * T_STAGE_BYTES;
+  TrainCtrl& c = *reinterpret_cast<TrainCtrl*>(sTurn + T_EPI_WARPS * T_TURN);
   constexpr uint32_t IDESC = idesc_bf16_f32(TPAIR_M, TBN, TT::A_MN, TT::B_MN);
   constexpr uint32_t IDESC_HALF = idesc_bf16_f32(TPAIR_M / 2, TBN, TT::A_MN, TT::B_MN);
   constexpr uint32_t IDESC_NHALF = idesc_bf16_f32(TPAIR_M, TBN / 2, TT::A_MN, TT::B_MN);
@@ -444,34 +533,35 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     // ------------------------------------------------ epilogue warps
     const int q = warp & 3;                     // TMEM lane quadrant this warp may read
     const int wh = (warp - T_EPI_WARP0) >> 2;   // which half of the tile's chunks
+    const Turn turn{smem_u32(sTurn + (warp - T_EPI_WARP0) * T_TURN), lane};
     const uint32_t tempty0 = dsmem_map(smem_u32(&c.tempty[0]), 0);
+    constexpr int HALVES = TT::GATED ? 2 : 1;
     int acc = 0;
     uint32_t acc_phase = 0;
     int e = 0;
     for (int tile = pair; tile < n_tiles; tile += n_pairs) {
       const TrainTile t = train_tile<OP>(c, p, tile, e);
-      const int row = t.base + (t.half ? rank * (TBM / 2) + (q & 1) * 32 + lane
-                                       : rank * TBM + q * 32 + lane);  // within segment (Wgrad: of out)
+      // this warp's first row, within the segment (Wgrad: of out)
+      const int row0 = t.base + (t.half ? rank * (TBM / 2) + (q & 1) * 32 : rank * TBM + q * 32);
       const int col_base = t.nb * TT::BN_OUT + (t.half ? (q >> 1) * 128 : 0);
       const int n_chunks = t.half || t.nhalf || TT::PAIRED ? 4 : 8;  // of 32 columns, both warps'
       const int ch0 = wh * (n_chunks / 2);
       const int ch1 = ch0 + n_chunks / 2;
-      const int n_rows = TT::WGRAD ? p.M : c.seg.rows[t.e];
-      const bool row_ok = row < n_rows;
+      const int n_seg = TT::WGRAD ? p.M : c.seg.rows[t.e];
+      const int n_rows = min(max(n_seg - row0, 0), 32);  // of this warp
 
-      [[maybe_unused]] KeptChunk next[TT::GATED ? 2 : 1];
-      [[maybe_unused]] size_t crow = 0;
+      [[maybe_unused]] KeptChunk next[HALVES];
       [[maybe_unused]] float gw = 0.0f;
       if constexpr (TT::BWD) {
         // z of the first chunk and the gate weight, before the accumulator
-        crow = (size_t)c.seg.row_off[t.e] + row;
+        const size_t crow0 = (size_t)c.seg.row_off[t.e] + row0;
 #pragma unroll
-        for (int hf = 0; hf < (TT::GATED ? 2 : 1); ++hf)
-          train_load_kept(p, TT::GATED ? 2 : 1, crow, hf, col_base + ch0 * 32, row_ok, next[hf]);
-        if (row_ok) {
+        for (int hf = 0; hf < HALVES; ++hf)
+          train_load_kept(p, lane, HALVES, crow0, hf, col_base + ch0 * 32, n_rows, next[hf]);
+        if (lane < n_rows) {
           gw = 1.0f;
           if (p.w) {
-            const int a = __ldg(p.perm + crow);
+            const int a = __ldg(p.perm + crow0 + lane);
             gw = a >= 0 && a < p.n_w ? __ldg(p.w + a) : 0.0f;
           }
         }
@@ -485,136 +575,96 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       }
       const uint32_t tbase = tmem + (uint32_t)(acc * TBN) + ((uint32_t)(q * 32) << 16);
 
-      if constexpr (TT::PAIRED) {
-        const size_t orow = (size_t)c.seg.row_off[t.e] + row;
-#pragma unroll 1
-        for (int ch = ch0; ch < ch1; ++ch) {
-          uint32_t gv[32], uv[32];
-          tmem_ld_x32(tbase + (uint32_t)(ch * 32), gv);
-          tmem_ld_x32(tbase + (uint32_t)(TT::BN_OUT + ch * 32), uv);
-          tmem_ld_wait();
-          const int gcol = col_base + ch * 32;
-          if (row_ok && gcol < p.N) {
-            const int valid = min(32, p.N - gcol);
-            train_keep(p, true, orow, 0, gcol, valid, gv);
-            train_keep(p, true, orow, 1, gcol, valid, uv);
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (g * 8 < valid) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float a = __uint_as_float(gv[g * 8 + i]);
-                  f[i] = __fdividef(a, 1.0f + __expf(-a)) * __uint_as_float(uv[g * 8 + i]);
-                }
-                train_store8(p.out + orow * (size_t)p.N + gcol + g * 8, f);
-              }
-          }
-        }
-      } else if constexpr (TT::BWD) {
-        const int n16 = (n_rows + 15) / 16 * 16;
-        const size_t prow = (size_t)c.seg.pad_off[t.e] + row;
-        constexpr int HALVES = TT::GATED ? 2 : 1;
+      if constexpr (TT::BWD) {
+        const size_t crow0 = (size_t)c.seg.row_off[t.e] + row0;
+        // padded rows: zeros behind the segment's last one, up to 16
+        const int n_pad = min(max((n_seg + 15) / 16 * 16 - row0, 0), 32);
+        const size_t prow0 = (size_t)c.seg.pad_off[t.e] + row0;
+        const bool row_ok = lane < n_rows;
         float dot = 0.0f;
 #pragma unroll 1
         for (int ch = ch0; ch < ch1; ++ch) {
-          KeptChunk cur[HALVES];
-#pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf) cur[hf] = next[hf];
           const int gcol = col_base + ch * 32;
+          if (gcol >= p.N) break;  // uniform: no columns from here on
+          const int valid = min(32, p.N - gcol);
+          float z[32];
+          [[maybe_unused]] float u[32];
+          train_kept(p, turn, next[0], z);
+          if constexpr (TT::GATED) train_kept(p, turn, next[HALVES - 1], u);
           if (ch + 1 < ch1) {
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
-              train_load_kept(p, HALVES, crow, hf, gcol + 32, row_ok, next[hf]);
+              train_load_kept(p, lane, HALVES, crow0, hf, gcol + 32, n_rows, next[hf]);
           }
           uint32_t v[32];
           tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
           tmem_ld_wait();
-          if (row < n16 && gcol < p.N) {
-            const int valid = p.N - gcol;
-            uint16_t* dz = p.dz + prow * (size_t)(HALVES * p.N) + gcol;
-            uint16_t* hw = p.hw + prow * (size_t)p.N + gcol;
+          if (n_pad == 0) continue;
+          // z becomes dz (of the gate), u becomes dz of the up projection
+          float hv[32];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (g * 8 < valid) {
-                float z[8], hv[8], d0[8];
-                [[maybe_unused]] float u[8], d1[8];
-                train_kept8(p, cur[0], g, z);
-                if constexpr (TT::GATED) train_kept8(p, cur[HALVES - 1], g, u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float gr = __uint_as_float(v[g * 8 + i]);
-                  float h;
-                  if constexpr (TT::GATED) {
-                    // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
-                    const float s = train_sigmoid(z[i]);
-                    const float as = z[i] * s;
-                    h = as * u[i];
-                    d0[i] = gw * gr * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
-                    d1[i] = gw * gr * as;
-                  } else {
-                    float d;
-                    train_gelu_grad(z[i], h, d);
-                    d0[i] = gw * gr * d;
-                  }
-                  dot = fmaf(gr, h, dot);
-                  hv[i] = gw * h;
-                }
-                if (!row_ok) {  // a padding row
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    d0[i] = hv[i] = 0.0f;
-                    if constexpr (TT::GATED) d1[i] = 0.0f;
-                  }
-                }
-                train_store8(dz + g * 8, d0);
-                if constexpr (TT::GATED) train_store8(dz + p.N + g * 8, d1);
-                train_store8(hw + g * 8, hv);
-              }
-            if (p.part && row_ok && ((ch & 1) || gcol + 32 >= p.N)) {
-              p.part[crow * (size_t)p.units + (gcol >> 6)] = dot;
-              dot = 0.0f;
+          for (int i = 0; i < 32; ++i) {
+            const float gr = row_ok && i < valid ? __uint_as_float(v[i]) : 0.0f;
+            float h;
+            if constexpr (TT::GATED) {
+              // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
+              const float s = train_sigmoid(z[i]);
+              const float as = z[i] * s;
+              h = as * u[i];
+              z[i] = gw * gr * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
+              u[i] = gw * gr * as;
+            } else {
+              float d;
+              train_gelu_grad(z[i], h, d);
+              z[i] = gw * gr * d;
             }
+            dot = fmaf(gr, h, dot);
+            hv[i] = gw * h;
+          }
+          uint16_t* dz = p.dz + prow0 * (size_t)(HALVES * p.N) + gcol;
+          turn_store_bf16(turn, z, dz, (size_t)HALVES * p.N, n_pad, valid);
+          if constexpr (TT::GATED) turn_store_bf16(turn, u, dz + p.N, (size_t)HALVES * p.N, n_pad, valid);
+          turn_store_bf16(turn, hv, p.hw + prow0 * (size_t)p.N + gcol, (size_t)p.N, n_pad, valid);
+          if (p.part && ((ch & 1) || gcol + 32 >= p.N)) {
+            if (row_ok) p.part[(crow0 + lane) * (size_t)p.units + (gcol >> 6)] = dot;
+            dot = 0.0f;
           }
         }
       } else {
-        // Fwd GELU, Rows, Logits, Wgrad
-        size_t orow;
-        if constexpr (TT::WGRAD)
-          orow = (size_t)t.e * p.M + row;
-        else
-          orow = (size_t)c.seg.row_off[t.e] + row;
+        // Fwd, Rows, Plain, Wgrad
+        const size_t orow0 = TT::WGRAD ? (size_t)t.e * p.M + row0 : (size_t)c.seg.row_off[t.e] + row0;
 #pragma unroll 1
         for (int ch = ch0; ch < ch1; ++ch) {
+          const int gcol = col_base + ch * 32;
+          if (gcol >= p.N) break;
           uint32_t v[32];
+          [[maybe_unused]] uint32_t uv[32];
           if (t.kb > 0) {
             tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
+            // gate columns are the accumulator's first 128, up columns the others
+            if constexpr (TT::PAIRED) tmem_ld_x32(tbase + (uint32_t)(TT::BN_OUT + ch * 32), uv);
             tmem_ld_wait();
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          const int gcol = col_base + ch * 32;
-          if (row_ok && gcol < p.N) {
-            const int valid = min(32, p.N - gcol);
-            if constexpr (OP == kTrainFwdGelu) train_keep(p, false, orow, 0, gcol, valid, v);
+          if (n_rows == 0) continue;
+          const int valid = min(32, p.N - gcol);
+          if constexpr (TT::FWD) {
+            train_keep(p, turn, HALVES, orow0, 0, gcol, n_rows, valid, v);
+            if constexpr (TT::GATED) train_keep(p, turn, HALVES, orow0, 1, gcol, n_rows, valid, uv);
+          }
+          if constexpr (TT::OUT32) {
+            turn_store_f32(turn, v, p.out32 + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
+          } else {
+            float f[32];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (g * 8 < valid) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  f[i] = __uint_as_float(v[g * 8 + i]);
-                  if constexpr (OP == kTrainFwdGelu) f[i] = train_gelu(f[i]);
-                }
-                if constexpr (OP == kTrainLogits || OP == kTrainWgradF32) {
-                  float4* dst = reinterpret_cast<float4*>(p.out32 + orow * (size_t)p.N + gcol + g * 8);
-                  dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-                  dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-                } else {
-                  train_store8(p.out + orow * (size_t)p.N + gcol + g * 8, f);
-                }
-              }
+            for (int i = 0; i < 32; ++i) {
+              f[i] = __uint_as_float(v[i]);
+              if constexpr (OP == kTrainFwdGelu) f[i] = train_gelu(f[i]);
+              if constexpr (OP == kTrainFwdSwiGLU) f[i] = __fdividef(f[i], 1.0f + __expf(-f[i])) * __uint_as_float(uv[i]);
+            }
+            turn_store_bf16(turn, f, p.out + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
           }
         }
       }

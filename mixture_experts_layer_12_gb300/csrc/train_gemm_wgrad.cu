@@ -17,10 +17,11 @@ cudaError_t launch_train_gemm(int op, const CUtensorMap& tm_a, const CUtensorMap
   switch (op) {
     case kTrainFwdGelu:
     case kTrainFwdSwiGLU:
-    case kTrainLogits: return launch_train_gemm_fwd(op, tm_a, tm_b, tm_a64, a, max_tiles, st);
+    case kTrainPlain: return launch_train_gemm_fwd(op, tm_a, tm_b, tm_a64, a, max_tiles, st);
     case kTrainBwdGelu:
     case kTrainBwdSwiGLU:
-    case kTrainRows: return launch_train_gemm_bwd(op, tm_a, tm_b, tm_a64, a, max_tiles, st);
+    case kTrainRows:
+    case kTrainRowsF32: return launch_train_gemm_bwd(op, tm_a, tm_b, tm_a64, a, max_tiles, st);
     case kTrainWgrad: return train_launch<kTrainWgrad>(tm_a, tm_b, tm_a64, a, max_tiles, st);
     default: return train_launch<kTrainWgradF32>(tm_a, tm_b, tm_a64, a, max_tiles, st);
   }

@@ -42,9 +42,10 @@ enum TrainOp {
   kTrainBwdGelu = 2,    // g = A W2[e]^T; dz, w h and <g, h> from the kept z
   kTrainBwdSwiGLU = 3,
   kTrainRows = 4,       // out = A W[e]^T
-  kTrainLogits = 5,     // out32 = A W
+  kTrainPlain = 5,      // out32 = A W[e]
   kTrainWgrad = 6,      // out[e] = A_e^T B_e over a segment's rows
-  kTrainWgradF32 = 7    // the same in fp32
+  kTrainWgradF32 = 7,   // the same in fp32
+  kTrainRowsF32 = 8     // out32 = A W[e]^T
 };
 
 struct TrainGemmArgs {
@@ -74,7 +75,7 @@ struct TrainGemmArgs {
   uint64_t wait_limit_ns;
 };
 // Operand boxes: A of row products {64, 128} and {64, 64} (tm_a64), of Wgrad
-// {64, 64}; B of Fwd and Logits W [E, K, N] {64, 64, 1}, of Bwd and Rows W
+// {64, 64}; B of Fwd and Plain W [E, K, N] {64, 64, 1}, of Bwd and Rows W
 // [E, N, K] {64, 128, 1}, of Wgrad {64, 64} (2D, as A).  max_tiles bounds the
 // number of 256 x 256 tiles.
 cudaError_t launch_train_gemm(int op, const CUtensorMap& tm_a, const CUtensorMap& tm_b,
@@ -94,13 +95,16 @@ struct GatherArgs {
 };
 cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st);
 
-// dx[t] = (add ? add[t] : 0) + sum_j rows[slot[t, j]] (fp32, j ascending)
+// out[t] = (add ? add[t] : 0) + sum_j (w ? w[t, j] : 1) * rows[slot[t, j]]
+// (fp32, j ascending), rounded to bf16 once; rows in bf16 or fp32, add in fp32.
 struct RowsSumArgs {
   const uint16_t* rows;
+  const float* rows32;  // used where set
+  const float* w;
   const int32_t* slot;
-  const uint16_t* add;
+  const float* add;
   int T, H, k;
-  uint16_t* dx;
+  uint16_t* out;
 };
 cudaError_t launch_rows_sum(const RowsSumArgs& a, cudaStream_t st);
 
@@ -121,8 +125,8 @@ cudaError_t launch_dequantize_a8(int64_t rows, int cols, const int8_t* codes, co
                                  uint16_t* out, int sms, cudaStream_t st);
 
 // The gate's gradient: dlogits as two bf16 numbers (the second is what the
-// first one's rounding left), dl [T, 2 ep], and sums of 64 tokens' dlogits.
-constexpr int kGateTokens = 64;
+// first one's rounding left), dl [T, 2 ep], and sums of 16 tokens' dlogits.
+constexpr int kGateTokens = 16;
 struct GateBackwardArgs {
   int T, E, k, ep;
   int gating;
@@ -134,7 +138,7 @@ struct GateBackwardArgs {
   const int32_t* slot;
   int rows, units;
   uint16_t* dl;
-  float* db_part;      // [ceil(T / 64), E]
+  float* db_part;      // [ceil(T / 16), E]
 };
 cudaError_t launch_gate_backward(const GateBackwardArgs& a, cudaStream_t st);
 

@@ -89,51 +89,78 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
   }
 }
 
-// ------------------------------------------------------- dispatch's gradient --
-// dx[t] = add[t] + sum_j rows[slot[t, j]]: a thread takes two 16-byte chunks
-// of one token and asks for all k rows' before the sums.
+// ------------------------------------------------------- sums of a token's rows --
+// out[t] = add[t] + sum_j w[t, j] rows[slot[t, j]]: a thread takes two 8-column
+// chunks of one token (one where rows are in fp32: the same bytes) and asks for
+// all k rows' before the sums.
 constexpr int RTHREADS = 128;
-constexpr int RCPT = 2;
-template <int KMAX>
+template <int KMAX, bool F32>
 __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a) {
+  constexpr int RCPT = F32 ? 1 : 2;
   pdl_launch_dependents();
   pdl_wait();
   const int t = blockIdx.x;
   const int col0 = (blockIdx.y * RTHREADS * RCPT + threadIdx.x) * 8;
   if (col0 >= a.H) return;
   int r[KMAX];
+  float w[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
     r[j] = j < a.k ? __ldg(a.slot + (size_t)t * a.k + j) : -1;
     if (r[j] >= a.T * a.k) r[j] = -1;  // slot is not re-validated: nothing outside rows
+    w[j] = a.w && r[j] >= 0 ? __ldg(a.w + (size_t)t * a.k + j) : 1.0f;
   }
-  uint4 v[KMAX][RCPT], ad[RCPT];
+  if constexpr (F32) {
+    float4 v[KMAX][2], s[2];
 #pragma unroll
-  for (int c = 0; c < RCPT; ++c) {
-    const int col = col0 + c * RTHREADS * 8;
-    ad[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (col < a.H) {
-      if (a.add) ad[c] = __ldg(reinterpret_cast<const uint4*>(a.add + (size_t)t * a.H + col));
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j)
-        if (r[j] >= 0) v[j][c] = __ldg(reinterpret_cast<const uint4*>(a.rows + (size_t)r[j] * a.H + col));
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < RCPT; ++c) {
-    const int col = col0 + c * RTHREADS * 8;
-    if (col >= a.H) break;
-    float s[8];
-    unpack8(ad[c], s);
+    for (int h = 0; h < 2; ++h)
+      s[h] = a.add ? __ldg(reinterpret_cast<const float4*>(a.add + (size_t)t * a.H + col0) + h)
+                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
-      if (r[j] >= 0) {
-        float f[8];
-        unpack8(v[j][c], f);
+      if (r[j] >= 0)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += f[i];
-      }
-    *reinterpret_cast<uint4*>(a.dx + (size_t)t * a.H + col) = pack8(s);
+        for (int h = 0; h < 2; ++h)
+          v[j][h] = __ldg(reinterpret_cast<const float4*>(a.rows32 + (size_t)r[j] * a.H + col0) + h);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (r[j] >= 0)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          s[h].x = fmaf(w[j], v[j][h].x, s[h].x);
+          s[h].y = fmaf(w[j], v[j][h].y, s[h].y);
+          s[h].z = fmaf(w[j], v[j][h].z, s[h].z);
+          s[h].w = fmaf(w[j], v[j][h].w, s[h].w);
+        }
+    const float f[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+    *reinterpret_cast<uint4*>(a.out + (size_t)t * a.H + col0) = pack8(f);
+  } else {
+    uint4 v[KMAX][RCPT];
+#pragma unroll
+    for (int c = 0; c < RCPT; ++c) {
+      const int col = col0 + c * RTHREADS * 8;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j)
+        if (r[j] >= 0 && col < a.H)
+          v[j][c] = __ldg(reinterpret_cast<const uint4*>(a.rows + (size_t)r[j] * a.H + col));
+    }
+#pragma unroll
+    for (int c = 0; c < RCPT; ++c) {
+      const int col = col0 + c * RTHREADS * 8;
+      if (col >= a.H) break;
+      float s[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = a.add ? __ldg(a.add + (size_t)t * a.H + col + i) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j)
+        if (r[j] >= 0) {
+          float f[8];
+          unpack8(v[j][c], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(w[j], f[i], s[i]);
+        }
+      *reinterpret_cast<uint4*>(a.out + (size_t)t * a.H + col) = pack8(s);
+    }
   }
 }
 
@@ -300,7 +327,8 @@ __global__ void __launch_bounds__(QTHREADS) dequantize_a8_kernel(int64_t chunks,
 }
 
 // ------------------------------------------------------------ the gate's gradient --
-// A block takes 64 tokens, a warp one token at a time; lane l holds experts
+// A block takes 16 tokens (64: 26 us for 8192 tokens of 64 experts), a warp one
+// at a time; lane l holds experts
 // l, l + 32, ...  With the weights of a softmax over the chosen experts,
 // dlogit_j = w_j (dw_j - sum_i w_i dw_i) for the chosen and 0 for the others;
 // with those of a softmax over all experts, dlogit_e = p_e ([e chosen] dw_e -
@@ -481,13 +509,17 @@ cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st) {
   return launch(train_gather_kernel, dim3(gx, a.src[1] ? 2 : 1), GTHREADS, st, a);
 }
 
-cudaError_t launch_rows_sum(const RowsSumArgs& a, cudaStream_t st) {
-  const int per = RTHREADS * 8 * RCPT;
+template <bool F32>
+static cudaError_t rows_sum(const RowsSumArgs& a, cudaStream_t st) {
+  const int per = RTHREADS * 8 * (F32 ? 1 : 2);
   const dim3 grid((unsigned)a.T, (unsigned)((a.H + per - 1) / per), 1);
-  if (a.k <= 1) return launch(rows_sum_kernel<1>, grid, RTHREADS, st, a);
-  if (a.k <= 2) return launch(rows_sum_kernel<2>, grid, RTHREADS, st, a);
-  if (a.k <= 4) return launch(rows_sum_kernel<4>, grid, RTHREADS, st, a);
-  return launch(rows_sum_kernel<8>, grid, RTHREADS, st, a);
+  if (a.k <= 1) return launch(rows_sum_kernel<1, F32>, grid, RTHREADS, st, a);
+  if (a.k <= 2) return launch(rows_sum_kernel<2, F32>, grid, RTHREADS, st, a);
+  if (a.k <= 4) return launch(rows_sum_kernel<4, F32>, grid, RTHREADS, st, a);
+  return launch(rows_sum_kernel<8, F32>, grid, RTHREADS, st, a);
+}
+cudaError_t launch_rows_sum(const RowsSumArgs& a, cudaStream_t st) {
+  return a.rows32 ? rows_sum<true>(a, st) : rows_sum<false>(a, st);
 }
 
 template <int W>
