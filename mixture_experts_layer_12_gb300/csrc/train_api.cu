@@ -641,6 +641,9 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
   TRY(check_shape(s, true));
   TRY(check_bits(keep_bits));
   CHECK_WS(moet_forward_workspace_size(s), "moet_forward_workspace_size");
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(offsets);
+  if (b_router && !aligned16(b_router)) return fail(MOE_ERR_INVALID_ARG, "b_router is not 16-byte aligned");
   if (s->T > 0) {
     REQUIRE_PTR(w1);
     REQUIRE_PTR(w2);

@@ -1,0 +1,218 @@
+"""The training operators' C ABI and binding without a GPU: the header's symbols,
+what the calls refuse (all before the library touches CUDA), workspace sizes, and
+the reference the GPU tests use, against differences and brute force."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import mixture_experts_layer_12_gb300 as moe
+import train_reference as ref
+from mixture_experts_layer_12_gb300 import build as moe_build, train
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    moe_build.build()
+    return train._lib()
+
+
+def test_exports_match_header(lib):
+    with open(os.path.join(ROOT, "include", "moe_train.h")) as f:
+        decl = set(re.findall(r"MOE_API\s+[\w\s\*]+?\b(moet_\w+)\s*\(", f.read()))
+    assert decl == set(moe.TRAIN_EXPORTS)
+    import subprocess
+    out = subprocess.run(["nm", "-D", "--defined-only", moe.LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    assert {w.split()[-1] for w in out.splitlines() if w.split()[-1].startswith("moet_")} == decl
+
+
+# name -> (arguments between the shape and the pointers, pointers before status, which may be null)
+CALLS = {
+    "moet_expert_ffn": ((16,), 7, {6}), "moet_expert_ffn_backward": ((16,), 10, {2}),
+    "moet_router_probs": ((), 4, {2}), "moet_route_backward": ((), 9, {4, 8}),
+    "moet_forward": ((16,), 17, {2, 13, 14, 15, 16}), "moet_backward": ((16,), 19, {2, 12, 13, 16}),
+}
+SHAPE = dict(T=4, H=128, F=256, E=8, k=2)
+
+
+def size_of(lib, name, s, bits=16):
+    fn = getattr(lib, name + "_workspace_size")
+    return fn(ctypes.byref(s), bits) if name == "moet_backward" else fn(ctypes.byref(s))
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), moe.MOE_ERR_INVALID_ARG), (dict(E=0), moe.MOE_ERR_UNSUPPORTED),
+    (dict(E=257), moe.MOE_ERR_UNSUPPORTED), (dict(k=0), moe.MOE_ERR_UNSUPPORTED),
+    (dict(k=9, E=16), moe.MOE_ERR_UNSUPPORTED), (dict(H=100), moe.MOE_ERR_UNSUPPORTED),
+    (dict(gating=3), moe.MOE_ERR_INVALID_ARG), (dict(T=1 << 23, k=4), moe.MOE_ERR_UNSUPPORTED)])
+def test_bad_shapes_are_refused(lib, name, kw, code):
+    s = moe.make_shape(**{**SHAPE, **kw})
+    mid, n, _ = CALLS[name]
+    assert size_of(lib, name, s) == 0
+    assert getattr(lib, name)(ctypes.byref(s), *mid, *([P(0x1000)] * n), P(0x1000), P(0x1000), 1 << 50, None) == code
+    assert lib.moe_last_error_string()
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_null_misaligned_and_small_buffers_are_refused(lib, name):
+    mid, n, optional = CALLS[name]
+    s = moe.make_shape(**SHAPE)
+    need = size_of(lib, name, s)
+    fn = getattr(lib, name)
+    good = [P(0x1000 * (i + 1)) for i in range(n + 2)]
+    for i in range(n + 2):
+        for bad in (P(None), P(0x1008)):
+            if i in optional:
+                continue
+            args = list(good)
+            args[i] = bad
+            assert fn(ctypes.byref(s), *mid, *args, need, None) == moe.MOE_ERR_INVALID_ARG, (i, bad)
+    assert fn(ctypes.byref(s), *mid, *good, need - 1, None) == moe.MOE_ERR_INVALID_ARG
+    assert b"_workspace_size" in lib.moe_last_error_string()
+    assert fn(None, *mid, *good, need, None) == moe.MOE_ERR_INVALID_ARG
+    if mid:
+        assert fn(ctypes.byref(s), 4, *good, need, None) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_what_8_bits_and_the_softmax_over_all_need(lib):
+    s = moe.make_shape(**SHAPE)
+    need = size_of(lib, "moet_backward", s, 8)
+    assert need > size_of(lib, "moet_backward", s, 16) and size_of(lib, "moet_backward", s, 4) == 0
+    # positions of the scales of z and of x (and of x's codes)
+    for name, at in (("moet_expert_ffn", (6,)), ("moet_expert_ffn_backward", (2,)), ("moet_forward", (13, 14, 15)),
+                     ("moet_backward", (2, 12))):
+        _, n, _ = CALLS[name]
+        good = [P(0x1000 * (i + 1)) for i in range(n + 2)]
+        for i in at:
+            args = list(good)
+            args[i] = P(None)
+            assert getattr(lib, name)(ctypes.byref(s), 8, *args, 1 << 40, None) == moe.MOE_ERR_INVALID_ARG, (name, i)
+    s1 = moe.make_shape(**SHAPE, gating=1)
+    for name, i in (("moet_forward", 16), ("moet_backward", 13), ("moet_route_backward", 4)):
+        mid, n, _ = CALLS[name]
+        args = [P(0x1000 * (j + 1)) for j in range(n + 2)]
+        args[i] = P(None)
+        assert getattr(lib, name)(ctypes.byref(s1), *mid, *args, 1 << 40, None) == moe.MOE_ERR_INVALID_ARG, name
+
+
+@pytest.mark.parametrize("rows,cols,code", [(-1, 8, moe.MOE_ERR_INVALID_ARG), (4, 12, moe.MOE_ERR_UNSUPPORTED),
+                                            (4, 0, moe.MOE_ERR_UNSUPPORTED), (1 << 43, 8, moe.MOE_ERR_UNSUPPORTED),
+                                            (4, -8, moe.MOE_ERR_INVALID_ARG)])
+def test_a8_refuses(lib, rows, cols, code):
+    for fn in (lib.moet_quantize_a8, lib.moet_dequantize_a8):
+        assert fn(rows, cols, P(0x1000), P(0x2000), P(0x3000), None) == code
+        assert fn(0, 8, None, None, None, None) == moe.MOE_OK
+        for i in range(3):
+            for bad in (P(None), P(0x1008)):
+                args = [P(0x1000), P(0x2000), P(0x3000)]
+                args[i] = bad
+                assert fn(4, 8, *args, None) == moe.MOE_ERR_INVALID_ARG
+
+
+def test_rows_refuse(lib):
+    s = moe.make_shape(4, 128, 8, 8, 2)
+    for fn, n in ((lib.moet_dispatch_rows_backward, 3), (lib.moet_combine_backward, 6)):
+        for i in range(n):
+            for bad in (P(None), P(0x1008)):
+                args = [P(0x1000 * (j + 1)) for j in range(n)]
+                args[i] = bad
+                assert fn(ctypes.byref(s), *args, None) == moe.MOE_ERR_INVALID_ARG
+        assert fn(ctypes.byref(moe.make_shape(4, 100, 8, 8, 2)), *([P(0x1000)] * n), None) == moe.MOE_ERR_UNSUPPORTED
+        assert fn(ctypes.byref(moe.make_shape(0, 128, 8, 8, 2)), *([None] * n), None) == moe.MOE_OK
+
+
+def test_workspaces_hold_what_a_call_needs(lib):
+    s = moe.make_shape(4096, 4096, 14336, 8, 2)
+    n, pad = 8192, 8192 + 8 * 15
+    assert size_of(lib, "moet_backward", s) >= 2 * pad * (2 * 4096 + 2 * 14336) + 4 * n * 4096
+    assert size_of(lib, "moet_expert_ffn", s) >= 2 * n * 14336
+
+
+def test_a8_tensor_checks_shapes():
+    c = torch.zeros(3, 40, dtype=torch.int8)
+    moe.A8Tensor(c, torch.zeros(3, 2, dtype=torch.uint8))
+    for bad in (torch.zeros(3, 1, dtype=torch.uint8), torch.zeros(2, 2, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            moe.A8Tensor(c, bad)
+    with pytest.raises(TypeError):
+        moe.A8Tensor(c.int(), torch.zeros(3, 2, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        moe.A8Tensor(c, torch.zeros(3, 2))
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    bf = torch.bfloat16
+    x = torch.zeros(4, 16, dtype=bf)
+    slot = torch.zeros(4, 2, dtype=torch.int32)
+    w1, w2 = torch.zeros(2, 16, 8, dtype=bf), torch.zeros(2, 8, 16, dtype=bf)
+    o = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match=r"dxp must be \[T \* k, H\]"):
+        moe.dispatch_rows_backward(x, slot)
+    with pytest.raises(ValueError, match="w1 must be"):
+        moe.expert_ffn(x, w1, w2, o, act="swiglu")
+    with pytest.raises(ValueError, match="xp must be"):
+        moe.expert_ffn_backward(x[:, :8], x, w1, w2, o, x)
+    with pytest.raises(ValueError, match="x must be"):
+        moe.route_backward(x, torch.zeros(8, 4, dtype=bf), slot, torch.zeros(4, 2), torch.zeros(4, 2))
+    if not torch.cuda.is_available():
+        return
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.quantize_a8(x)
+
+
+# ------------------------------------------------------ the tests' reference --
+
+@pytest.mark.parametrize("gating", [0, 1, 2])
+@pytest.mark.parametrize("act", ["gelu", "swiglu"])
+def test_reference_gradients_match_differences(act, gating):
+    """Directional derivatives of sum(y dy) by central differences with step h:
+    off by h^2 times a third derivative (below 1e4 at these sizes: 1e-8) and by
+    2^-52 |f| / h (1e-9)."""
+    g = torch.Generator().manual_seed(5)
+    T, H, F, E, k = 9, 16, 24, 5, 3
+    gated = act == "swiglu"
+    rnd = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    x, wr, b = rnd(T, H), rnd(H, E) / 4, rnd(E)
+    w1, w2, dy = rnd(E, H, (2 if gated else 1) * F) / 4, rnd(E, F, H) / 5, rnd(T, H)
+    lg = x @ wr + b
+    ids = torch.topk(lg, k, dim=1).indices
+    counts, offsets, perm, slot = ref.dispatch(ids, E, ref.capacity(T, k, E, 0.8))
+    assert (slot < 0).any()
+    n = int(offsets[-1])
+    z = torch.cat([x[perm[int(offsets[e]):int(offsets[e + 1])] // k] @ w1[e] for e in range(E)])
+    z = z.view(n, 2, F) if gated else z
+    r = ref.layer_backward(x, z, wr, w1, w2, ids, ref.gate(lg, ids, gating), torch.softmax(lg, 1), offsets, perm, slot,
+                           dy, gating, gated)
+    h = 1e-6
+    args = dict(x=x, wr=wr, b=b, w1=w1, w2=w2)
+    for name, key in (("x", "dx"), ("wr", "dw_router"), ("b", "dbias"), ("w1", "dw1"), ("w2", "dw2")):
+        for _ in range(3):
+            d = rnd(*args[name].shape)
+            f = [float((ref.layer(*[a + s * h * d if n2 == name else a for n2, a in args.items()], ids, slot, gating,
+                                  gated) * dy).sum()) for s in (1, -1)]
+            want = (f[0] - f[1]) / (2 * h)
+            got = float((r[key][0] * d).sum())
+            assert abs(got - want) <= 1e-7 * (1 + abs(want)) * 10, (name, got, want)
+
+
+def test_reference_8_bits_by_brute_force():
+    v = torch.tensor([[127.0, 63.5, 0.5, 1.5, -127.0] + [0.0] * 27, [127.5] * 32, [0.0] * 32, [2.0 ** -130] * 32])
+    b = ref.a8_scales(v)
+    assert b[:, 0].tolist() == [127, 128, 1, 1]
+    assert ref.a8_codes(v, b)[0, :5].tolist() == [127, 64, 0, 2, -127]
+    assert ref.a8_codes(v, b)[1, 0] == 64 and ref.a8_codes(v, b)[3, 0] == 0
+    x = torch.randn(50, 72, generator=torch.Generator().manual_seed(1)).bfloat16()
+    b = ref.a8_scales(x)
+    q = ref.a8_codes(x, b)
+    assert int(q.abs().max()) <= 127
+    s = torch.exp2((b - 127).double()).repeat_interleave(32, 1)[:, :72]
+    assert ((ref.a8_values(q, b) - x.double()).abs() <= s / 2).all()
+    m = torch.nn.functional.pad(x.double().abs(), (0, 24)).view(50, 3, 32).amax(2)
+    assert (m > 127 * torch.exp2((b - 128).double())).all()  # no smaller scale would do
