@@ -43,7 +43,7 @@ constexpr int TBM = 128;            // rows per CTA
 constexpr int TPAIR_M = 2 * TBM;    // rows per pair tile
 constexpr int TBN = 256;            // columns per pair tile
 constexpr int TBK = 64;
-constexpr int TSTAGES = 6;
+constexpr int TSTAGES = 6;          // at most (TrainTraits)
 constexpr int TACC = 2;
 constexpr int T_OP_BYTES = 128 * TBK * 2;  // a CTA's half of either operand: 16 KB
 constexpr int T_BOX = 64 * TBK * 2;        // one 64-column MN-major box: 8 KB
@@ -66,10 +66,7 @@ struct TrainCtrl {
   int tile_start[kMaxExperts + 1];
   SegTable seg;
 };
-constexpr int T_TURN = 2048;  // a warp's 32 rows x 64 bytes between threads and memory
-constexpr size_t T_SMEM_BYTES =
-    1024 + (size_t)TSTAGES * T_STAGE_BYTES + T_EPI_WARPS * T_TURN + sizeof(TrainCtrl);
-static_assert(T_SMEM_BYTES <= 232448, "shared memory of one CTA");
+constexpr int T_TURN = 2048;  // 32 rows x 64 bytes between a warp's threads and memory
 
 template <int OP>
 struct TrainTraits {
@@ -83,6 +80,14 @@ struct TrainTraits {
   static constexpr bool A_PADDED = !(FWD || OP == kTrainPlain);
   static constexpr bool OUT32 = OP == kTrainPlain || OP == kTrainWgradF32 || OP == kTrainRowsF32;
   static constexpr int BN_OUT = PAIRED ? TBN / 2 : TBN;
+  // the epilogue's buffers per warp (FWD: z and h, BWD: z turned into dz, and
+  // w h), and the stages that fit beside them
+  static constexpr int HALVES = GATED ? 2 : 1;
+  static constexpr int BUFS = FWD || BWD ? HALVES + 1 : 1;
+  static constexpr int STAGES = FWD || BWD ? 5 : TSTAGES;
+  static constexpr size_t SMEM =
+      1024 + (size_t)STAGES * T_STAGE_BYTES + T_EPI_WARPS * BUFS * T_TURN + sizeof(TrainCtrl);
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
 struct TrainTile {
@@ -138,41 +143,58 @@ __device__ __forceinline__ bool train_wait_drain(uint64_t* bar, uint32_t parity,
   return true;
 }
 
+// The epilogues' instructions bound the products with short K (a gated Bwd tile
+// of 256 x 256 took 22 us of them beside 11 of MMAs with K = 2048), so they use
+// the special-function unit's own exponential and reciprocal.
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // erfc(|z| / sqrt 2) and exp(-z^2 / 2): Abramowitz & Stegun, Handbook of
 // Mathematical Functions, formula 7.1.26 (|error| <= 1.5e-7); the exponential
 // it needs is the normal density's.
 __device__ __forceinline__ float train_erfc(float z, float& ex) {
-  const float ax = fabsf(z) * 0.70710678118654752440f;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, ax, 1.0f));
+  const float t = rcp_fast(fmaf(0.3275911f * 0.70710678118654752440f, fabsf(z), 1.0f));
   const float poly =
       t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
                0.254829592f);
-  ex = __expf(-ax * ax);
+  ex = exp2_fast(z * z * -0.72134752044448170368f);  // -z^2 / (2 ln 2)
   return poly * ex;
 }
 // GELU(z) = z Phi(z), Phi(z) = (1 + erf(z / sqrt 2)) / 2, without cancellation
 __device__ __forceinline__ float train_gelu(float z) {
   float ex;
-  const float c = train_erfc(z, ex);
-  return 0.5f * z * (z >= 0.0f ? 2.0f - c : c);
+  const float c = 0.5f * train_erfc(z, ex);
+  return z * (z >= 0.0f ? 1.0f - c : c);
 }
 // GELU and GELU'(z) = Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi); an infinite z
 // has a density of 0, not 0 times infinity
 __device__ __forceinline__ void train_gelu_grad(float z, float& h, float& d) {
   float ex;
-  const float c = train_erfc(z, ex);
-  const float phi = z >= 0.0f ? 1.0f - 0.5f * c : 0.5f * c;
+  const float c = 0.5f * train_erfc(z, ex);
+  const float phi = z >= 0.0f ? 1.0f - c : c;
   h = z * phi;
-  d = phi + (ex == 0.0f ? 0.0f : z * ex * 0.39894228040143267794f);
+  d = ex == 0.0f ? phi : fmaf(z * ex, 0.39894228040143267794f, phi);
 }
-__device__ __forceinline__ float train_sigmoid(float a) { return __fdividef(1.0f, 1.0f + __expf(-a)); }
+// 1 / (1 + exp(-a)): exp overflows to infinity below -88, its reciprocal is 0
+__device__ __forceinline__ float train_sigmoid(float a) {
+  return rcp_fast(1.0f + exp2_fast(a * -1.44269504088896340736f));
+}
 
 // A warp's 32 rows x 32 columns between threads (one row each, as TMEM gives
 // them) and memory (where 4 lanes together read or write a row's 64 bytes, or 32
-// of 8-bit codes): 2 KB of shared memory per warp, rows of four 16-byte pieces
-// whose places are turned so that neither side meets a bank twice.  Straight from
-// the threads a warp's access met 32 rows at once, 16 bytes each: the weight
-// gradients of 64 experts of 2048 x 2816 took 325 us.
+// of 8-bit codes): 2 KB of shared memory, rows of four 16-byte pieces whose
+// places are turned so that neither side meets a bank twice.  Straight from the
+// threads a warp's access met 32 rows at once, 16 bytes each: the weight
+// gradients of 64 experts of 2048 x 2816 took 325 us, so 240.  Outputs of one
+// chunk are put down in buffers of their own and leave together: with one
+// buffer and ten warp barriers a chunk, a gated Bwd tile took 22 us.
 struct Turn {
   uint32_t base;  // shared-memory address of the warp's buffer
   int lane;
@@ -182,6 +204,7 @@ struct Turn {
   __device__ __forceinline__ uint32_t at(int row, int j) const {
     return base + row * 64 + ((j ^ ((row >> 1) & 3)) << 4);
   }
+  __device__ __forceinline__ Turn buffer(int b) const { return Turn{base + (uint32_t)(b * T_TURN), lane}; }
 };
 __device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -211,27 +234,44 @@ __device__ __forceinline__ uint4 train_pack8(const float* f) {
   pk.w = pack_bf16x2(f[6], f[7]);
   return pk;
 }
+__device__ __forceinline__ void train_unpack8(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
 
-// The warp's block to memory: rows 0 .. n_rows - 1 of 32 at dst + row * pitch
-// (bytes), the first `pieces` 16-byte pieces of each.
-__device__ __forceinline__ void turn_store(const Turn& t, uint8_t* dst, size_t pitch, int n_rows, int pieces) {
-  __syncwarp();
+// A buffer to memory, after a warp barrier: rows 0 .. n_rows - 1 of 32 at dst +
+// row * pitch (bytes), the first `pieces` 16-byte pieces of each; rows from
+// n_full on as zeros.
+__device__ __forceinline__ void turn_out(const Turn& t, uint8_t* dst, size_t pitch, int n_rows, int pieces,
+                                         int n_full = 32) {
   const int j = t.lane & 3;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = i * 8 + (t.lane >> 2);
-    const uint4 v = lds16(t.at(row, j));
+    uint4 v = lds16(t.at(row, j));
+    if (row >= n_full) v = make_uint4(0u, 0u, 0u, 0u);
     if (row < n_rows && j < pieces) *reinterpret_cast<uint4*>(dst + row * pitch + j * 16) = v;
   }
-  __syncwarp();
 }
-// 32 fp32 or bf16 values of every thread's row.
-__device__ __forceinline__ void turn_store_bf16(const Turn& t, const float (&f)[32], uint16_t* dst, size_t cols,
-                                                int n_rows, int valid) {
+__device__ __forceinline__ void turn_out_bf16(const Turn& t, uint16_t* dst, size_t cols, int n_rows, int valid,
+                                              int n_full = 32) {
+  turn_out(t, reinterpret_cast<uint8_t*>(dst), cols * 2, n_rows, valid >> 3, n_full);
+}
+// Codes: 8-byte pieces, as rows start on 8 bytes only.
+__device__ __forceinline__ void turn_out_codes(const Turn& t, int8_t* dst, size_t cols, int n_rows, int valid) {
+  const int j = t.lane & 3;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) sts16(t.own(g), train_pack8(f + 8 * g));
-  turn_store(t, reinterpret_cast<uint8_t*>(dst), cols * 2, n_rows, valid >> 3);
+  for (int i = 0; i < 4; ++i) {
+    const int row = i * 8 + (t.lane >> 2);
+    const uint2 v = lds8(t.at(row, j));
+    if (row < n_rows && j * 8 < valid) *reinterpret_cast<uint2*>(dst + row * cols + j * 8) = v;
+  }
 }
+// 32 fp32 values of every thread's row, 16 at a time.
 __device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v)[32], float* dst, size_t cols,
                                                int n_rows, int valid) {
 #pragma unroll
@@ -240,116 +280,112 @@ __device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v
     for (int g = 0; g < 4; ++g)
       sts16(t.own(g), make_uint4(v[16 * h + 4 * g], v[16 * h + 4 * g + 1], v[16 * h + 4 * g + 2],
                                  v[16 * h + 4 * g + 3]));
-    turn_store(t, reinterpret_cast<uint8_t*>(dst + 16 * h), cols * 4, n_rows, (valid >> 2) - 4 * h);
+    __syncwarp();
+    turn_out(t, reinterpret_cast<uint8_t*>(dst + 16 * h), cols * 4, n_rows, (valid >> 2) - 4 * h);
+    __syncwarp();
   }
-}
-// 32 codes of every thread's row: 8-byte pieces, as rows start on 8 bytes only.
-__device__ __forceinline__ void turn_store_codes(const Turn& t, const uint2 (&q)[4], int8_t* dst, size_t cols,
-                                                 int n_rows, int valid) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) sts8(t.own(g), q[g]);
-  __syncwarp();
-  const int j = t.lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = i * 8 + (t.lane >> 2);
-    const uint2 v = lds8(t.at(row, j));
-    if (row < n_rows && j * 8 < valid) *reinterpret_cast<uint2*>(dst + row * cols + j * 8) = v;
-  }
-  __syncwarp();
 }
 
-// Keeps a warp's 32 columns of z (those below `valid`, a multiple of 8, exist)
-// at column `col` of half `hf` of rows row0 ..
-__device__ __forceinline__ void train_keep(const TrainGemmArgs& p, const Turn& t, int halves, size_t row0, int hf,
-                                           int col, int n_rows, int valid, const uint32_t (&v)[32]) {
+// This thread's 32 columns of z (those below `valid` exist) into buffer t as
+// bf16, or as codes with the group's scale byte as the result.
+__device__ __forceinline__ uint32_t train_keep(const TrainGemmArgs& p, const Turn& t, int valid,
+                                               const uint32_t (&v)[32]) {
+  if (p.keep_bits == 16) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * g + i]);
+      sts16(t.own(g), train_pack8(f));
+    }
+    return 0u;
+  }
+  uint32_t m = 0;
+  if (valid == 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, v[i] & 0x7fffffffu);
+  } else {  // gate columns past the last one are up columns
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, i < valid ? v[i] & 0x7fffffffu : 0u);
+  }
+  const uint32_t b = a8_scale_byte(m);
+  const float inv = a8_inverse(b);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[g * 8 + i]);
+    sts8(t.own(g), a8_codes8(f, inv, b));
+  }
+  return b;
+}
+// ... and from there to half `hf` of rows row0 .., column col.
+__device__ __forceinline__ void train_kept_out(const TrainGemmArgs& p, const Turn& t, int halves, size_t row0,
+                                               int hf, int col, int n_rows, int valid, uint32_t b) {
   const size_t pitch = (size_t)halves * p.N;
   const size_t at = row0 * pitch + (size_t)hf * p.N + col;
   if (p.keep_bits == 16) {
-    float f[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-    turn_store_bf16(t, f, static_cast<uint16_t*>(p.z) + at, pitch, n_rows, valid);
+    turn_out_bf16(t, static_cast<uint16_t*>(p.z) + at, pitch, n_rows, valid);
     return;
   }
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) m = max(m, i < valid ? v[i] & 0x7fffffffu : 0u);
-  const uint32_t b = a8_scale_byte(m);
-  const float inv = a8_inverse(b);
-  uint2 q[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i / 4] |= ((uint32_t)a8_code(__uint_as_float(v[g * 8 + i]), inv, b) & 0xffu) << (8 * (i % 4));
-    q[g] = make_uint2(w[0], w[1]);
-  }
-  turn_store_codes(t, q, static_cast<int8_t*>(p.z) + at, pitch, n_rows, valid);
+  turn_out_codes(t, static_cast<int8_t*>(p.z) + at, pitch, n_rows, valid);
   const int groups = (p.N + 31) / 32;
   if (t.lane < n_rows)
     p.z_scales[((row0 + t.lane) * halves + hf) * (size_t)groups + (col >> 5)] = (uint8_t)b;
 }
 
 // 32 kept columns of a warp's rows on their way from memory: four pieces of
-// other threads' rows (16 bytes of bf16 or 8 of codes), and this thread's scale.
+// other threads' rows, 16 bytes of bf16 or 8 of codes with the group's scale.
 struct KeptChunk {
   uint4 w[4];
-  uint32_t b;
 };
 __device__ __forceinline__ void train_load_kept(const TrainGemmArgs& p, int lane, int halves, size_t row0, int hf,
                                                 int col, int n_rows, KeptChunk& k) {
   const size_t pitch = (size_t)halves * p.N;
-  const size_t at = row0 * pitch + (size_t)hf * p.N + col;
   const int j = lane & 3;
   const bool col_ok = col + j * 8 < p.N;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = i * 8 + (lane >> 2);
-    k.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    k.w[i] = make_uint4(0u, 0u, 127u, 0u);
     if (row < n_rows && col_ok) {
-      const size_t o = at + row * pitch + j * 8;
+      const size_t o = (row0 + row) * pitch + (size_t)hf * p.N + col + j * 8;
       if (p.keep_bits == 16) {
         k.w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + o));
       } else {
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.z) + o));
         k.w[i].x = u.x;
         k.w[i].y = u.y;
+        k.w[i].z = __ldg(p.z_scales + ((row0 + row) * halves + hf) * (size_t)((p.N + 31) / 32) + (col >> 5));
       }
+    } else if (p.keep_bits == 16) {
+      k.w[i].z = 0u;
     }
   }
-  k.b = 127u;
-  if (p.keep_bits == 8 && lane < n_rows && col < p.N)
-    k.b = __ldg(p.z_scales + ((row0 + lane) * halves + hf) * (size_t)((p.N + 31) / 32) + (col >> 5));
 }
-// ... and as 32 values of this thread's row.
-__device__ __forceinline__ void train_kept(const TrainGemmArgs& p, const Turn& t, const KeptChunk& k,
-                                           float (&f)[32]) {
+// ... and into buffer t as bf16 (which codes times scales are exactly).
+__device__ __forceinline__ void train_kept_in(const TrainGemmArgs& p, const Turn& t, const KeptChunk& k) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t a = t.at(i * 8 + (t.lane >> 2), t.lane & 3);
-    if (p.keep_bits == 16) sts16(a, k.w[i]); else sts8(a, make_uint2(k.w[i].x, k.w[i].y));
-  }
-  __syncwarp();
-  const float s = a8_scale(k.b);
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    if (p.keep_bits == 16) {
-      const uint4 u = lds16(t.own(g));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[8 * g + 2 * i] = bf16_lo(w[i]);
-        f[8 * g + 2 * i + 1] = bf16_hi(w[i]);
-      }
-    } else {
-      const uint2 u = lds8(t.own(g));
-      a8_values(u.x, s, f + 8 * g);
-      a8_values(u.y, s, f + 8 * g + 4);
+    uint4 v = k.w[i];
+    if (p.keep_bits == 8) {
+      float f[8];
+      const float s = a8_scale(v.z);
+      a8_values(v.x, s, f);
+      a8_values(v.y, s, f + 4);
+      v = train_pack8(f);
     }
+    sts16(t.at(i * 8 + (t.lane >> 2), t.lane & 3), v);
   }
-  __syncwarp();
+}
+
+// 32 lanes x 32 bits, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
 }
 
 template <int OP>
@@ -361,9 +397,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
-  uint8_t* sB = smem + TSTAGES * T_OP_BYTES;
-  uint8_t* sTurn = smem + TSTAGES * T_STAGE_BYTES;
-  TrainCtrl& c = *reinterpret_cast<TrainCtrl*>(sTurn + T_EPI_WARPS * T_TURN);
+  constexpr int STAGES = TT::STAGES;
+  uint8_t* sB = smem + STAGES * T_OP_BYTES;
+  uint8_t* sTurn = smem + STAGES * T_STAGE_BYTES;
+  TrainCtrl& c = *reinterpret_cast<TrainCtrl*>(sTurn + T_EPI_WARPS * TT::BUFS * T_TURN);
   constexpr uint32_t IDESC = idesc_bf16_f32(TPAIR_M, TBN, TT::A_MN, TT::B_MN);
   constexpr uint32_t IDESC_HALF = idesc_bf16_f32(TPAIR_M / 2, TBN, TT::A_MN, TT::B_MN);
   constexpr uint32_t IDESC_NHALF = idesc_bf16_f32(TPAIR_M, TBN / 2, TT::A_MN, TT::B_MN);
@@ -383,7 +420,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       return (m + TPAIR_M - 1) / TPAIR_M * NB;
     });
   } else if (threadIdx.x == 32) {
-    for (int i = 0; i < TSTAGES; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       mbar_init(&c.full[i], 2);
       mbar_init(&c.empty[i], 1);
     }
@@ -462,7 +499,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             }
           }
           ++issued;
-          if (++stage == TSTAGES) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -471,8 +508,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       // the bytes of the last armed stages of both CTAs have landed before
       // shared memory is released (at once on the normal path)
       if (rank == 0) {
-        for (int m = max(0, issued - TSTAGES); m < issued; ++m)
-          train_wait_drain(&c.full[m % TSTAGES], (uint32_t)((m / TSTAGES) & 1), p.wait_limit_ns, p.status);
+        for (int m = max(0, issued - STAGES); m < issued; ++m)
+          train_wait_drain(&c.full[m % STAGES], (uint32_t)((m / STAGES) & 1), p.wait_limit_ns, p.status);
       }
     }
     __syncwarp();
@@ -513,7 +550,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             umma_bf16_pair(d, ad, bd, idesc, (kb | j) != 0 ? 1u : 0u);
           }
           umma_commit_pair_mc(&c.empty[stage], T_PAIR_MASK);
-          if (++stage == TSTAGES) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -533,35 +570,50 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     // ------------------------------------------------ epilogue warps
     const int q = warp & 3;                     // TMEM lane quadrant this warp may read
     const int wh = (warp - T_EPI_WARP0) >> 2;   // which half of the tile's chunks
-    const Turn turn{smem_u32(sTurn + (warp - T_EPI_WARP0) * T_TURN), lane};
+    const Turn turn{smem_u32(sTurn + (warp - T_EPI_WARP0) * TT::BUFS * T_TURN), lane};
     const uint32_t tempty0 = dsmem_map(smem_u32(&c.tempty[0]), 0);
-    constexpr int HALVES = TT::GATED ? 2 : 1;
+    constexpr int HALVES = TT::HALVES;
     int acc = 0;
     uint32_t acc_phase = 0;
     int e = 0;
+    // what this warp does of a tile
+    struct Part {
+      TrainTile t;
+      int row0;      // its first row, within the segment (Wgrad: of out)
+      int n_seg;     // rows of the segment (Wgrad: of out)
+      int n_rows;    // its rows
+      int col_base, ch0, ch1;  // first column of the tile's half, its chunks of 32
+    };
+    const auto part_of = [&](int tile) {
+      Part a;
+      a.t = train_tile<OP>(c, p, tile, e);
+      a.row0 = a.t.base + (a.t.half ? rank * (TBM / 2) + (q & 1) * 32 : rank * TBM + q * 32);
+      a.col_base = a.t.nb * TT::BN_OUT + (a.t.half ? (q >> 1) * 128 : 0);
+      const int n_chunks = a.t.half || a.t.nhalf || TT::PAIRED ? 4 : 8;  // both warps'
+      a.ch0 = wh * (n_chunks / 2);
+      a.ch1 = a.ch0 + n_chunks / 2;
+      a.n_seg = TT::WGRAD ? p.M : c.seg.rows[a.t.e];
+      a.n_rows = min(max(a.n_seg - a.row0, 0), 32);
+      return a;
+    };
+    [[maybe_unused]] KeptChunk next[HALVES];
+    [[maybe_unused]] const auto load_kept = [&](const Part& a, int ch) {
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf)
+        train_load_kept(p, lane, HALVES, (size_t)c.seg.row_off[a.t.e] + a.row0, hf, a.col_base + ch * 32, a.n_rows,
+                        next[hf]);
+    };
+    Part w = part_of(pair);
+    if constexpr (TT::BWD) load_kept(w, w.ch0);
     for (int tile = pair; tile < n_tiles; tile += n_pairs) {
-      const TrainTile t = train_tile<OP>(c, p, tile, e);
-      // this warp's first row, within the segment (Wgrad: of out)
-      const int row0 = t.base + (t.half ? rank * (TBM / 2) + (q & 1) * 32 : rank * TBM + q * 32);
-      const int col_base = t.nb * TT::BN_OUT + (t.half ? (q >> 1) * 128 : 0);
-      const int n_chunks = t.half || t.nhalf || TT::PAIRED ? 4 : 8;  // of 32 columns, both warps'
-      const int ch0 = wh * (n_chunks / 2);
-      const int ch1 = ch0 + n_chunks / 2;
-      const int n_seg = TT::WGRAD ? p.M : c.seg.rows[t.e];
-      const int n_rows = min(max(n_seg - row0, 0), 32);  // of this warp
-
-      [[maybe_unused]] KeptChunk next[HALVES];
+      const TrainTile t = w.t;
+      const int n_rows = w.n_rows;
       [[maybe_unused]] float gw = 0.0f;
       if constexpr (TT::BWD) {
-        // z of the first chunk and the gate weight, before the accumulator
-        const size_t crow0 = (size_t)c.seg.row_off[t.e] + row0;
-#pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf)
-          train_load_kept(p, lane, HALVES, crow0, hf, col_base + ch0 * 32, n_rows, next[hf]);
         if (lane < n_rows) {
           gw = 1.0f;
           if (p.w) {
-            const int a = __ldg(p.perm + crow0 + lane);
+            const int a = __ldg(p.perm + c.seg.row_off[t.e] + w.row0 + lane);
             gw = a >= 0 && a < p.n_w ? __ldg(p.w + a) : 0.0f;
           }
         }
@@ -576,67 +628,86 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       const uint32_t tbase = tmem + (uint32_t)(acc * TBN) + ((uint32_t)(q * 32) << 16);
 
       if constexpr (TT::BWD) {
-        const size_t crow0 = (size_t)c.seg.row_off[t.e] + row0;
+        const size_t crow0 = (size_t)c.seg.row_off[t.e] + w.row0;
         // padded rows: zeros behind the segment's last one, up to 16
-        const int n_pad = min(max((n_seg + 15) / 16 * 16 - row0, 0), 32);
-        const size_t prow0 = (size_t)c.seg.pad_off[t.e] + row0;
-        const bool row_ok = lane < n_rows;
+        const int n_pad = min(max((w.n_seg + 15) / 16 * 16 - w.row0, 0), 32);
+        const size_t prow0 = (size_t)c.seg.pad_off[t.e] + w.row0;
+        const Turn b_hw = turn.buffer(HALVES);
         float dot = 0.0f;
 #pragma unroll 1
-        for (int ch = ch0; ch < ch1; ++ch) {
-          const int gcol = col_base + ch * 32;
+        for (int ch = w.ch0; ch < w.ch1; ++ch) {
+          const int gcol = w.col_base + ch * 32;
           if (gcol >= p.N) break;  // uniform: no columns from here on
           const int valid = min(32, p.N - gcol);
-          float z[32];
-          [[maybe_unused]] float u[32];
-          train_kept(p, turn, next[0], z);
-          if constexpr (TT::GATED) train_kept(p, turn, next[HALVES - 1], u);
-          if (ch + 1 < ch1) {
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf) train_kept_in(p, turn.buffer(hf), next[hf]);
+          if (ch + 1 < w.ch1) load_kept(w, ch + 1);
+          __syncwarp();
+          if (n_pad > 0) {
+            uint32_t v[8], vn[8];
+            tmem_ld_x8(tbase + (uint32_t)(ch * 32), v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              if (g < 3) tmem_ld_x8(tbase + (uint32_t)(ch * 32 + 8 * g + 8), vn);
+              float z[8], hv[8];
+              [[maybe_unused]] float u[8];
+              train_unpack8(lds16(turn.own(g)), z);
+              if constexpr (TT::GATED) train_unpack8(lds16(turn.buffer(1).own(g)), u);
+              // z becomes dz (of the gate), u becomes dz of the up projection
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                // columns past the last one: g and z are 0
+                const float gr = __uint_as_float(v[i]);
+                const float wg = gw * gr;
+                float h;
+                if constexpr (TT::GATED) {
+                  // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
+                  const float s = train_sigmoid(z[i]);
+                  const float as = z[i] * s;
+                  h = as * u[i];
+                  z[i] = wg * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
+                  u[i] = wg * as;
+                } else {
+                  float d;
+                  train_gelu_grad(z[i], h, d);
+                  z[i] = wg * d;
+                }
+                dot = fmaf(gr, h, dot);
+                hv[i] = gw * h;
+              }
+              sts16(turn.own(g), train_pack8(z));
+              if constexpr (TT::GATED) sts16(turn.buffer(1).own(g), train_pack8(u));
+              sts16(b_hw.own(g), train_pack8(hv));
+              if (g < 3) {
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = vn[i];
+              }
+            }
+          }
+          __syncwarp();
+          if (n_pad > 0) {
+            uint16_t* dz = p.dz + prow0 * (size_t)(HALVES * p.N) + gcol;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
-              train_load_kept(p, lane, HALVES, crow0, hf, gcol + 32, n_rows, next[hf]);
-          }
-          uint32_t v[32];
-          tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
-          tmem_ld_wait();
-          if (n_pad == 0) continue;
-          // z becomes dz (of the gate), u becomes dz of the up projection
-          float hv[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float gr = row_ok && i < valid ? __uint_as_float(v[i]) : 0.0f;
-            float h;
-            if constexpr (TT::GATED) {
-              // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
-              const float s = train_sigmoid(z[i]);
-              const float as = z[i] * s;
-              h = as * u[i];
-              z[i] = gw * gr * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
-              u[i] = gw * gr * as;
-            } else {
-              float d;
-              train_gelu_grad(z[i], h, d);
-              z[i] = gw * gr * d;
+              turn_out_bf16(turn.buffer(hf), dz + hf * (size_t)p.N, (size_t)HALVES * p.N, n_pad, valid, n_rows);
+            turn_out_bf16(b_hw, p.hw + prow0 * (size_t)p.N + gcol, (size_t)p.N, n_pad, valid, n_rows);
+            if (p.part && ((ch & 1) || gcol + 32 >= p.N)) {
+              if (lane < n_rows) p.part[(crow0 + lane) * (size_t)p.units + (gcol >> 6)] = dot;
+              dot = 0.0f;
             }
-            dot = fmaf(gr, h, dot);
-            hv[i] = gw * h;
           }
-          uint16_t* dz = p.dz + prow0 * (size_t)(HALVES * p.N) + gcol;
-          turn_store_bf16(turn, z, dz, (size_t)HALVES * p.N, n_pad, valid);
-          if constexpr (TT::GATED) turn_store_bf16(turn, u, dz + p.N, (size_t)HALVES * p.N, n_pad, valid);
-          turn_store_bf16(turn, hv, p.hw + prow0 * (size_t)p.N + gcol, (size_t)p.N, n_pad, valid);
-          if (p.part && ((ch & 1) || gcol + 32 >= p.N)) {
-            if (row_ok) p.part[(crow0 + lane) * (size_t)p.units + (gcol >> 6)] = dot;
-            dot = 0.0f;
-          }
+          __syncwarp();
         }
       } else {
         // Fwd, Rows, Plain, Wgrad
-        const size_t orow0 = TT::WGRAD ? (size_t)t.e * p.M + row0 : (size_t)c.seg.row_off[t.e] + row0;
+        const size_t orow0 = TT::WGRAD ? (size_t)t.e * p.M + w.row0 : (size_t)c.seg.row_off[t.e] + w.row0;
 #pragma unroll 1
-        for (int ch = ch0; ch < ch1; ++ch) {
-          const int gcol = col_base + ch * 32;
-          if (gcol >= p.N) break;
+        for (int ch = w.ch0; ch < w.ch1; ++ch) {
+          const int gcol = w.col_base + ch * 32;
+          if (gcol >= p.N || n_rows == 0) break;
+          const int valid = min(32, p.N - gcol);
           uint32_t v[32];
           [[maybe_unused]] uint32_t uv[32];
           if (t.kb > 0) {
@@ -648,25 +719,38 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          if (n_rows == 0) continue;
-          const int valid = min(32, p.N - gcol);
-          if constexpr (TT::FWD) {
-            train_keep(p, turn, HALVES, orow0, 0, gcol, n_rows, valid, v);
-            if constexpr (TT::GATED) train_keep(p, turn, HALVES, orow0, 1, gcol, n_rows, valid, uv);
-          }
           if constexpr (TT::OUT32) {
             turn_store_f32(turn, v, p.out32 + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
           } else {
-            float f[32];
+            [[maybe_unused]] uint32_t b0 = 0u, b1 = 0u;
+            if constexpr (TT::FWD) b0 = train_keep(p, turn, valid, v);
+            if constexpr (TT::PAIRED) b1 = train_keep(p, turn.buffer(1), valid, uv);
+            const Turn out = turn.buffer(TT::BUFS - 1);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              f[i] = __uint_as_float(v[i]);
-              if constexpr (OP == kTrainFwdGelu) f[i] = train_gelu(f[i]);
-              if constexpr (OP == kTrainFwdSwiGLU) f[i] = __fdividef(f[i], 1.0f + __expf(-f[i])) * __uint_as_float(uv[i]);
+            for (int g = 0; g < 4; ++g) {
+              float f[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                f[i] = __uint_as_float(v[8 * g + i]);
+                if constexpr (OP == kTrainFwdGelu) f[i] = train_gelu(f[i]);
+                if constexpr (OP == kTrainFwdSwiGLU)
+                  f[i] = f[i] * train_sigmoid(f[i]) * __uint_as_float(uv[8 * g + i]);
+              }
+              sts16(out.own(g), train_pack8(f));
             }
-            turn_store_bf16(turn, f, p.out + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
+            __syncwarp();
+            if constexpr (TT::FWD) train_kept_out(p, turn, HALVES, orow0, 0, gcol, n_rows, valid, b0);
+            if constexpr (TT::PAIRED) train_kept_out(p, turn.buffer(1), HALVES, orow0, 1, gcol, n_rows, valid, b1);
+            turn_out_bf16(out, p.out + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
+            __syncwarp();
           }
         }
+      }
+      // the next tile's part, and its first kept columns while this one's
+      // accumulator is handed back
+      if (tile + n_pairs < n_tiles) {
+        w = part_of(tile + n_pairs);
+        if constexpr (TT::BWD) load_kept(w, w.ch0);
       }
       if (t.kb > 0) {
         tc_fence_before();
@@ -695,7 +779,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 template <int OP>
 cudaError_t train_set_attributes() {
   return cudaFuncSetAttribute(train_gemm_kernel<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)T_SMEM_BYTES);
+                              (int)TrainTraits<OP>::SMEM);
 }
 
 // Persistent pairs: as many as are resident at once, at most one per tile.
@@ -710,7 +794,7 @@ cudaError_t train_launch(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(T_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = T_SMEM_BYTES;
+  cfg.dynamicSmemBytes = TrainTraits<OP>::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

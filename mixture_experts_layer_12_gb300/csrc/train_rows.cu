@@ -274,10 +274,7 @@ __global__ void __launch_bounds__(QTHREADS) quantize_a8_kernel(int64_t chunks, i
       if (at[u] >= 0) {
         float f[8];
         unpack8(v[u], f);
-        uint32_t q[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i / 4] |= ((uint32_t)a8_code(f[i], inv, b) & 0xffu) << (8 * (i % 4));
-        *reinterpret_cast<uint2*>(codes + at[u]) = make_uint2(q[0], q[1]);
+        *reinterpret_cast<uint2*>(codes + at[u]) = a8_codes8(f, inv, b);
       }
       const int64_t i = i0 + u * step;
       if (i < chunks && (threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)b;

@@ -108,10 +108,29 @@ __device__ __forceinline__ int a8_code(float v, float inv, uint32_t b) {
 __device__ __forceinline__ float a8_scale(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
 }
-// four codes of a word as floats times s
+// Four codes of a word as floats times s: a byte under the exponent of 2^23 is
+// 2^23 + 128 + code once its sign bit is turned, and needs no conversion.
 __device__ __forceinline__ void a8_values(uint32_t w, float s, float* f) {
+  const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = (float)(int8_t)(w >> (8 * i)) * s;
+  for (int i = 0; i < 4; ++i) f[i] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 | i)) - 8388736.0f) * s;
+}
+// 8 values as codes.  v / scale is exact and at most 127, so adding 1.5 * 2^23
+// rounds it half to even into the low byte; only a scale byte of 249 or more
+// (the largest magnitudes, infinities, NaN) needs limits.
+__device__ __forceinline__ uint2 a8_codes8(const float* v, float inv, uint32_t b) {
+  uint32_t t[8];
+  if (b < 249u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = __float_as_uint(fmaf(v[i], inv, 12582912.0f));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = (uint32_t)a8_code(v[i], inv, b);
+  }
+  uint2 q;
+  q.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+  q.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+  return q;
 }
 
 }  // namespace moe
