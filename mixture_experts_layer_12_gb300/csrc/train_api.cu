@@ -80,6 +80,16 @@ int map_weights(CUtensorMap* m, const void* base, size_t cols, size_t rows, size
   return bf16_map(m, base, 3, dims, box, what);
 }
 
+// Output [n, rows, cols] of a weight gradient.
+int map_out(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t n, bool f32) {
+  const uint64_t size = f32 ? 4 : 2;
+  const uint64_t dims[3] = {cols, rows, n};
+  const uint64_t strides[2] = {cols * size, cols * rows * size};
+  const uint32_t box[3] = {(uint32_t)(64 / size), 32, 1};
+  return encode_map_as(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       CU_TENSOR_MAP_SWIZZLE_64B, base, 3, dims, strides, box, "weight gradient");
+}
+
 SegArgs segments(const moe_shape* s, const int32_t* offsets) {
   SegArgs g;
   g.offsets = offsets;
@@ -206,15 +216,15 @@ int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream
   TRY(map_rows(&ta, f.hw, s->F, pad, 64, "w h"));
   TRY(map_rows(&tb, f.dyp, s->H, pad, 64, "dy rows"));
   a = gemm_args(seg, s->F, s->H, 0, status);
-  a.out = f.dw2;
-  CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta, a, s->E * blocks256(s->F) * blocks256(s->H), st),
+  TRY(map_out(&ta64, f.dw2, s->H, s->F, s->E, false));
+  CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta64, a, s->E * blocks256(s->F) * blocks256(s->H), st),
            "dW2 launch");
   // dW1 = xp^T dz
   TRY(map_rows(&ta, f.xp, s->H, pad, 64, "xp"));
   TRY(map_rows(&tb, f.dz, f1, pad, 64, "dz"));
   a = gemm_args(seg, s->H, f1, 0, status);
-  a.out = f.dw1;
-  CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta, a, s->E * blocks256(s->H) * blocks256(f1), st),
+  TRY(map_out(&ta64, f.dw1, f1, s->H, s->E, false));
+  CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta64, a, s->E * blocks256(s->H) * blocks256(f1), st),
            "dW1 launch");
   // dxp = dz W1^T
   TRY(map_rows(&ta, f.dz, f1, pad, 128, "dz"));
@@ -269,8 +279,8 @@ int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackward
   TRY(map_rows(&ta, x, s->H, s->T, 64, "x"));
   TRY(map_rows(&tb, r.dl, 2 * ep, s->T, 64, "dlogits"));
   TrainGemmArgs a = gemm_args(chunks(s->T, router_chunk(s)), s->H, 2 * ep, 0, status);
-  a.out32 = r.part;
-  CUDA_TRY(launch_train_gemm(kTrainWgradF32, ta, tb, ta, a, a.seg.E * blocks256(s->H) * blocks256(2 * ep), st),
+  TRY(map_out(&ta64, r.part, 2 * ep, s->H, a.seg.E, true));
+  CUDA_TRY(launch_train_gemm(kTrainWgradF32, ta, tb, ta64, a, a.seg.E * blocks256(s->H) * blocks256(2 * ep), st),
            "dW_router launch");
   RouterReduceArgs ra;
   ra.H = s->H;

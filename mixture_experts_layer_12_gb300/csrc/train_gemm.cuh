@@ -81,10 +81,10 @@ struct TrainTraits {
   static constexpr bool OUT32 = OP == kTrainPlain || OP == kTrainWgradF32 || OP == kTrainRowsF32;
   static constexpr int BN_OUT = PAIRED ? TBN / 2 : TBN;
   // the epilogue's buffers per warp (FWD: z and h, BWD: z turned into dz, and
-  // w h), and the stages that fit beside them
+  // w h, Wgrad: a ring), and the stages that fit beside them
   static constexpr int HALVES = GATED ? 2 : 1;
-  static constexpr int BUFS = FWD || BWD ? HALVES + 1 : 1;
-  static constexpr int STAGES = FWD || BWD ? 5 : TSTAGES;
+  static constexpr int BUFS = FWD || BWD ? HALVES + 1 : WGRAD ? 3 : 1;
+  static constexpr int STAGES = FWD || BWD || WGRAD ? 5 : TSTAGES;
   static constexpr size_t SMEM =
       1024 + (size_t)STAGES * T_STAGE_BYTES + T_EPI_WARPS * BUFS * T_TURN + sizeof(TrainCtrl);
   static_assert(SMEM <= 232448, "shared memory of one CTA");
@@ -271,6 +271,26 @@ __device__ __forceinline__ void turn_out_codes(const Turn& t, int8_t* dst, size_
     if (row < n_rows && j * 8 < valid) *reinterpret_cast<uint2*>(dst + row * cols + j * 8) = v;
   }
 }
+// A buffer to memory by a TMA store (its pieces lie as the 64-byte swizzle lays
+// them; what is outside the tensor is left out): the ring's next buffer is free
+// once at most BUFS - 1 earlier stores still read theirs.
+__device__ __forceinline__ void turn_tma(const Turn& t, const CUtensorMap* m, int c0, int c1, int c2) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (t.lane == 0) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(t.base), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void turn_tma_wait(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+  __syncwarp();
+}
+
 // 32 fp32 values of every thread's row, 16 at a time.
 __device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v)[32], float* dst, size_t cols,
                                                int n_rows, int valid) {
@@ -399,7 +419,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   uint8_t* sA = smem;
   constexpr int STAGES = TT::STAGES;
   uint8_t* sB = smem + STAGES * T_OP_BYTES;
-  uint8_t* sTurn = smem + STAGES * T_STAGE_BYTES;
+  uint8_t* sTurn = smem + STAGES * T_STAGE_BYTES;  // 1024-byte aligned, buffers of 2 KB
   TrainCtrl& c = *reinterpret_cast<TrainCtrl*>(sTurn + T_EPI_WARPS * TT::BUFS * T_TURN);
   constexpr uint32_t IDESC = idesc_bf16_f32(TPAIR_M, TBN, TT::A_MN, TT::B_MN);
   constexpr uint32_t IDESC_HALF = idesc_bf16_f32(TPAIR_M / 2, TBN, TT::A_MN, TT::B_MN);
@@ -603,6 +623,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         train_load_kept(p, lane, HALVES, (size_t)c.seg.row_off[a.t.e] + a.row0, hf, a.col_base + ch * 32, a.n_rows,
                         next[hf]);
     };
+    [[maybe_unused]] int ring = 0;
     Part w = part_of(pair);
     if constexpr (TT::BWD) load_kept(w, w.ch0);
     for (int tile = pair; tile < n_tiles; tile += n_pairs) {
@@ -719,7 +740,29 @@ __global__ void __launch_bounds__(T_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          if constexpr (TT::OUT32) {
+          if constexpr (TT::WGRAD) {
+            // 64 bytes of every row at a time: 32 columns of bf16, 16 of fp32
+            constexpr int OUTS = TT::OUT32 ? 2 : 1;
+#pragma unroll
+            for (int o = 0; o < OUTS; ++o) {
+              turn_tma_wait<TT::BUFS - 1>(lane);
+              const Turn out = turn.buffer(ring);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                if constexpr (TT::OUT32) {
+                  const int i = 16 * o + 4 * g;
+                  sts16(out.own(g), make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                } else {
+                  float f[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * g + i]);
+                  sts16(out.own(g), train_pack8(f));
+                }
+              }
+              if (gcol + 16 * o < p.N) turn_tma(out, &tm_a64, gcol + 16 * o, w.row0, t.e);
+              ring = ring == TT::BUFS - 1 ? 0 : ring + 1;
+            }
+          } else if constexpr (TT::OUT32) {
             turn_store_f32(turn, v, p.out32 + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
           } else {
             [[maybe_unused]] uint32_t b0 = 0u, b1 = 0u;
@@ -764,6 +807,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     }
   }
 
+  // A warp's stores have read its buffers (and are complete) before they go.
+  if constexpr (TT::WGRAD) {
+    if (warp >= T_EPI_WARP0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
   // Both CTAs finish all remote signalling and the leader's MMAs before TMEM
   // is released and before either CTA's shared memory goes away.
   tc_fence_before();

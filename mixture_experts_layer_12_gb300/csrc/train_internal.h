@@ -76,8 +76,9 @@ struct TrainGemmArgs {
 };
 // Operand boxes: A of row products {64, 128} and {64, 64} (tm_a64), of Wgrad
 // {64, 64}; B of Fwd and Plain W [E, K, N] {64, 64, 1}, of Bwd and Rows W
-// [E, N, K] {64, 128, 1}, of Wgrad {64, 64} (2D, as A).  max_tiles bounds the
-// number of 256 x 256 tiles.
+// [E, N, K] {64, 128, 1}, of Wgrad {64, 64} (2D, as A).  Wgrad's third map is its
+// output [E, M, N], box of 64 bytes x 32 rows, 64-byte swizzle.  max_tiles
+// bounds the number of 256 x 256 tiles.
 cudaError_t launch_train_gemm(int op, const CUtensorMap& tm_a, const CUtensorMap& tm_b,
                               const CUtensorMap& tm_a64, const TrainGemmArgs& a, int64_t max_tiles,
                               cudaStream_t st);
