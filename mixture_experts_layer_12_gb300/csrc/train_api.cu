@@ -256,29 +256,37 @@ int router_splits(const moe_shape* s) {
 }
 
 struct RouteGradWs {
-  uint16_t *dl, *w2;
-  float *part, *db_part;
+  uint16_t *dl, *w;
+  float *part, *db_part, *dlk;
 };
 RouteGradWs route_grad_ws(const moe_shape* s, Carve& c) {
   const size_t ep2 = 2 * (size_t)ep_of(s);
   RouteGradWs r;
   r.dl = c.take<uint16_t>(s->T * ep2);
-  r.w2 = c.take<uint16_t>(s->H * ep2);
+  r.w = c.take<uint16_t>(s->H * ep2);
+  r.dlk = c.take<float>(rows_of(s));
   r.part = c.take<float>(s->T > 0 ? router_splits(s) * (size_t)s->H * ep2 : 0);
   r.db_part = c.take<float>((size_t)((s->T + kGateTokens - 1) / kGateTokens) * s->E);
   return r;
 }
+// Whether dx's router part is a product over all experts: with a softmax over all
+// every expert has one; else only a token's k chosen ones, which the sum over its
+// rows takes along while they are few (2048 tokens of 4096 columns, k = 8: 22 us,
+// 12 as a product; 8192 of 2048, k = 4, with the rows: see rows_sum_kernel).
+bool router_product(const moe_shape* s) { return s->gating == MOE_GATE_SOFTMAX_TOPK || s->k > 4; }
+
+// dW_router, db and dx, whose other parts `sum` has; the router's as a product
+// goes into dx, or in fp32 into `add`.
 int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackwardArgs& gate, const uint16_t* x,
-                    const uint16_t* w_router, uint16_t* dx, float* dx32, uint16_t* dw_router, float* db,
-                    void* status, cudaStream_t st) {
+                    uint16_t* dw_router, float* db, float* add, RowsSumArgs sum, void* status, cudaStream_t st) {
   const int ep = ep_of(s);
   CUDA_TRY(launch_gate_backward(gate, st), "gate gradient launch");
-  CUDA_TRY(launch_router_twice(w_router, s->H, s->E, ep, r.w2, st), "router weights launch");
   CUtensorMap ta, tb, ta64;
   // dW_router's partial sums = x^T dlogits over chunks of tokens
   TRY(map_rows(&ta, x, s->H, s->T, 64, "x"));
   TRY(map_rows(&tb, r.dl, 2 * ep, s->T, 64, "dlogits"));
   TrainGemmArgs a = gemm_args(chunks(s->T, router_chunk(s)), s->H, 2 * ep, 0, status);
+  a.out32 = r.part;
   TRY(map_out(&ta64, r.part, 2 * ep, s->H, a.seg.E, true));
   CUDA_TRY(launch_train_gemm(kTrainWgradF32, ta, tb, ta64, a, a.seg.E * blocks256(s->H) * blocks256(2 * ep), st),
            "dW_router launch");
@@ -293,19 +301,29 @@ int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackward
   ra.n_db = (s->T + kGateTokens - 1) / kGateTokens;
   ra.db = db;
   CUDA_TRY(launch_router_reduce(ra, st), "dW_router sums launch");
-  // dx = dlogits W_router^T
-  TRY(map_rows(&ta, r.dl, 2 * ep, s->T, 128, "dlogits"));
-  TRY(map_rows(&ta64, r.dl, 2 * ep, s->T, 64, "dlogits"));
-  TRY(map_weights(&tb, r.w2, 2 * ep, s->H, 1, 128, "W_router"));
-  a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, s->H, 2 * ep, status);
-  a.out = dx;
-  a.out32 = dx32;
-  CUDA_TRY(launch_train_gemm(dx32 ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a, blocks256(s->T) * blocks256(s->H), st),
-           "router x gradient launch");
+  if (router_product(s)) {
+    TRY(map_rows(&ta, r.dl, 2 * ep, s->T, 128, "dlogits"));
+    TRY(map_rows(&ta64, r.dl, 2 * ep, s->T, 64, "dlogits"));
+    TRY(map_weights(&tb, r.w, 2 * ep, s->H, 1, 128, "W_router"));
+    a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, s->H, 2 * ep, status);
+    a.out = sum.out;
+    a.out32 = add;
+    CUDA_TRY(launch_train_gemm(add ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a,
+                               blocks256(s->T) * blocks256(s->H), st),
+             "router x gradient launch");
+    if (!add) return MOE_OK;
+    sum.add = add;
+  } else {
+    sum.dl = r.dlk;
+    sum.ids = gate.ids;
+    sum.wt = r.w;
+    sum.E = s->E;
+  }
+  CUDA_TRY(launch_rows_sum(sum, st), "row sums launch");
   return MOE_OK;
 }
-GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const int32_t* ids, const float* weights,
-                           const float* probs) {
+GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const uint16_t* w_router, const int32_t* ids,
+                           const float* weights, const float* probs) {
   GateBackwardArgs g = {};
   g.T = s->T;
   g.E = s->E;
@@ -317,6 +335,14 @@ GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const int32
   g.probs = probs;
   g.dl = r.dl;
   g.db_part = r.db_part;
+  g.w_router = w_router;
+  g.H = s->H;
+  if (router_product(s)) {
+    g.w2 = r.w;
+  } else {
+    g.wt = r.w;
+    g.dlk = r.dlk;
+  }
   return g;
 }
 
@@ -408,7 +434,7 @@ BackwardWs backward_ws(const moe_shape* s, int bits, Carve& c) {
   w.part = c.take<float>(rows_of(s) * ((s->F + 63) / 64));
   w.route = route_grad_ws(s, c);
   w.dxp = c.take<float>(rows_of(s) * s->H);
-  w.dxr = c.take<float>((size_t)s->T * s->H);
+  w.dxr = c.take<float>(router_product(s) ? (size_t)s->T * s->H : 0);
   return w;
 }
 
@@ -487,7 +513,13 @@ int moet_dispatch_rows_backward(const moe_shape* s, const uint16_t* dxp, const i
   REQUIRE_PTR(dx);
   int sms = 0;
   TRY(device_setup(&sms));
-  RowsSumArgs a = {dxp, nullptr, nullptr, slot, nullptr, s->T, s->H, s->k, dx};
+  RowsSumArgs a = {};
+  a.rows = dxp;
+  a.slot = slot;
+  a.T = s->T;
+  a.H = s->H;
+  a.k = s->k;
+  a.out = dx;
   CUDA_TRY(launch_rows_sum(a, stream_of(stream)), "row sums launch");
   return MOE_OK;
 }
@@ -631,9 +663,14 @@ int moet_route_backward(const moe_shape* s, const uint16_t* x, const uint16_t* w
   }
   Carve c(ws);
   const RouteGradWs r = route_grad_ws(s, c);
-  GateBackwardArgs g = gate_args(s, r, ids, weights, probs);
+  GateBackwardArgs g = gate_args(s, r, w_router, ids, weights, probs);
   g.dw = dweights;
-  return route_gradients(s, r, g, x, w_router, dx, nullptr, dw_router, db, status, st);
+  RowsSumArgs sum = {};
+  sum.T = s->T;
+  sum.H = s->H;
+  sum.k = s->k;
+  sum.out = dx;
+  return route_gradients(s, r, g, x, dw_router, db, nullptr, sum, status, st);
 }
 
 size_t moet_forward_workspace_size(const moe_shape* s) {
@@ -691,7 +728,14 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
                   status, st));
   // the experts' outputs stay in fp32: y is rounded once
   TRY(plain_product(s, w.ffn.h, w2, offsets, nullptr, w.Y, status, st));
-  RowsSumArgs ca = {nullptr, w.Y, weights, slot, nullptr, s->T, s->H, s->k, y};
+  RowsSumArgs ca = {};
+  ca.rows32 = w.Y;
+  ca.w = weights;
+  ca.slot = slot;
+  ca.T = s->T;
+  ca.H = s->H;
+  ca.k = s->k;
+  ca.out = y;
   CUDA_TRY(launch_rows_sum(ca, st), "combine launch");
   return MOE_OK;
 }
@@ -756,15 +800,19 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
   FfnGrad f = {keep_bits, w.ffn.xp, w.ffn.dyp, w1, w2, offsets, z, z_scales, weights, perm, w.part,
                w.ffn.hw, w.ffn.dz, nullptr, dw1, dw2, w.dxp};
   TRY(ffn_gradients(s, f, status, st));
-  GateBackwardArgs g = gate_args(s, w.route, ids, weights, probs);
+  GateBackwardArgs g = gate_args(s, w.route, w_router, ids, weights, probs);
   g.part = w.part;
   g.slot = slot;
   g.rows = (int)rows_of(s);
   g.units = (s->F + 63) / 64;
-  TRY(route_gradients(s, w.route, g, xb, w_router, nullptr, w.dxr, dw_router, db, status, st));
-  RowsSumArgs ra = {nullptr, w.dxp, nullptr, slot, w.dxr, s->T, s->H, s->k, dx};
-  CUDA_TRY(launch_rows_sum(ra, st), "row sums launch");
-  return MOE_OK;
+  RowsSumArgs sum = {};
+  sum.rows32 = w.dxp;
+  sum.slot = slot;
+  sum.T = s->T;
+  sum.H = s->H;
+  sum.k = s->k;
+  sum.out = dx;
+  return route_gradients(s, w.route, g, xb, dw_router, db, w.dxr, sum, status, st);
 }
 
 }  // extern "C"

@@ -432,14 +432,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   const int n_pairs = gridDim.x >> 1;
   const int NB = (p.N + TT::BN_OUT - 1) / TT::BN_OUT;
   pdl_launch_dependents();
-  pdl_wait();  // offsets, operands and output buffers belong to earlier kernels
-
-  if (warp == 0) {
-    seg_scan(p.seg, c.seg, c.tile_start, lane, [&](int n) {
-      const int m = TT::WGRAD ? p.M : n;
-      return (m + TPAIR_M - 1) / TPAIR_M * NB;
-    });
-  } else if (threadIdx.x == 32) {
+  // barriers and TMEM before the earlier kernels have ended
+  if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&c.full[i], 2);
       mbar_init(&c.empty[i], 1);
@@ -451,31 +445,35 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     mbar_init(&c.drain, 1);
     c.abort_flag = 0;
     fence_mbar_init();
-    if (p.merge_status && blockIdx.x == 0) {
-      const int s = *p.merge_status;
-      if (s) record_status(p.status, s);
-    }
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
   }
-  __syncthreads();
-  cluster_sync_all();  // the leader's barriers exist before the peer signals them
-  const int n_tiles = c.tile_start[p.seg.E];
-  if (pair >= n_tiles) return;  // uniform across the pair: nothing allocated yet
-
   if (warp == T_MMA_WARP) {
     tmem_alloc_pair(&c.tmem_base, T_TMEM_COLS);
     tmem_relinquish_pair();
   }
+  pdl_wait();  // offsets, operands and output buffers belong to earlier kernels
+  if (warp == 0) {
+    seg_scan(p.seg, c.seg, c.tile_start, lane, [&](int n) {
+      const int m = TT::WGRAD ? p.M : n;
+      return (m + TPAIR_M - 1) / TPAIR_M * NB;
+    });
+  }
+  if (p.merge_status && blockIdx.x == 0 && threadIdx.x == 32) {
+    const int s = *p.merge_status;
+    if (s) record_status(p.status, s);
+  }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // the leader's barriers exist before the peer signals them
   tc_fence_after();
+  const int n_tiles = c.tile_start[p.seg.E];
   const uint32_t tmem = c.tmem_base;
   const WaitCtl wc{&c.abort_flag, p.status, p.wait_limit_ns};
 
   if (warp == 0) {
     // ------------------------------------------------ producer (one thread)
     if (lane == 0) {
-      tma_prefetch_desc(&tm_a);
-      tma_prefetch_desc(&tm_b);
       const uint32_t full0 = dsmem_map(smem_u32(&c.full[0]), 0);  // leader's barriers
       int stage = 0;
       uint32_t phase = 0;
@@ -624,8 +622,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                         next[hf]);
     };
     [[maybe_unused]] int ring = 0;
-    Part w = part_of(pair);
-    if constexpr (TT::BWD) load_kept(w, w.ch0);
+    Part w = {};
+    if (pair < n_tiles) {
+      w = part_of(pair);
+      if constexpr (TT::BWD) load_kept(w, w.ch0);
+    }
     for (int tile = pair; tile < n_tiles; tile += n_pairs) {
       const TrainTile t = w.t;
       const int n_rows = w.n_rows;

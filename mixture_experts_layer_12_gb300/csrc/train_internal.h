@@ -97,15 +97,21 @@ struct GatherArgs {
 cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st);
 
 // out[t] = (add ? add[t] : 0) + sum_j (w ? w[t, j] : 1) * rows[slot[t, j]]
-// (fp32, j ascending), rounded to bf16 once; rows in bf16 or fp32, add in fp32.
+//          + (dl ? sum_j dl[t, j] * wt[ids[t, j]] : 0)
+// (fp32, in that order, j ascending), rounded to bf16 once; rows in bf16 or fp32
+// (both null: none), add in fp32, wt [E, H] bf16.
 struct RowsSumArgs {
   const uint16_t* rows;
-  const float* rows32;  // used where set
+  const float* rows32;
   const float* w;
   const int32_t* slot;
   const float* add;
   int T, H, k;
   uint16_t* out;
+  const float* dl;
+  const int32_t* ids;
+  const uint16_t* wt;
+  int E;
 };
 cudaError_t launch_rows_sum(const RowsSumArgs& a, cudaStream_t st);
 
@@ -139,7 +145,14 @@ struct GateBackwardArgs {
   const int32_t* slot;
   int rows, units;
   uint16_t* dl;
+  float* dlk;          // [T, k], the chosen experts' dlogits in fp32, or null
   float* db_part;      // [ceil(T / 16), E]
+  // W_router [H, E] on the way: transposed into wt [E, H] bf16, or (wt null)
+  // twice side by side into w2 [H, 2 ep], zeros between
+  const uint16_t* w_router;
+  int H;
+  uint16_t* wt;
+  uint16_t* w2;
 };
 cudaError_t launch_gate_backward(const GateBackwardArgs& a, cudaStream_t st);
 
@@ -155,8 +168,6 @@ struct RouterReduceArgs {
 };
 cudaError_t launch_router_reduce(const RouterReduceArgs& a, cudaStream_t st);
 
-// w2 [H, 2 ep]: W_router's rows twice, zero between
-cudaError_t launch_router_twice(const uint16_t* w, int H, int E, int ep, uint16_t* w2, cudaStream_t st);
 // probs[t] = softmax(logits[t] + bias) over E of ldl columns
 cudaError_t launch_router_softmax(const float* logits, int ldl, const float* bias, int T, int E,
                                   float* probs, cudaStream_t st);

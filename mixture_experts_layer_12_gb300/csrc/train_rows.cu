@@ -94,6 +94,35 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
 // chunks of one token (one where rows are in fp32: the same bytes) and asks for
 // all k rows' before the sums.
 constexpr int RTHREADS = 128;
+// The router's part of a token's gradient, k rows of W_router^T out of L2: as a
+// product of its own into an fp32 [T, H] it took 21 us more for 8192 tokens of
+// 2048 columns (and where every expert has a part it still is one: `add`).
+template <int KMAX>
+__device__ __forceinline__ void add_router_rows(const RowsSumArgs& a, int t, int col, float* s) {
+  if (!a.dl) return;
+  uint4 v[KMAX];
+  float d[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    d[j] = 0.0f;
+    v[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (j < a.k) {
+      const int e = __ldg(a.ids + (size_t)t * a.k + j);
+      if (e >= 0 && e < a.E) {
+        d[j] = __ldg(a.dl + (size_t)t * a.k + j);
+        v[j] = __ldg(reinterpret_cast<const uint4*>(a.wt + (size_t)e * a.H + col));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    float f[8];
+    unpack8(v[j], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = fmaf(d[j], f[i], s[i]);
+  }
+}
+
 template <int KMAX, bool F32>
 __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a) {
   constexpr int RCPT = F32 ? 1 : 2;
@@ -106,7 +135,7 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
   float w[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
-    r[j] = j < a.k ? __ldg(a.slot + (size_t)t * a.k + j) : -1;
+    r[j] = a.slot && j < a.k ? __ldg(a.slot + (size_t)t * a.k + j) : -1;
     if (r[j] >= a.T * a.k) r[j] = -1;  // slot is not re-validated: nothing outside rows
     w[j] = a.w && r[j] >= 0 ? __ldg(a.w + (size_t)t * a.k + j) : 1.0f;
   }
@@ -132,7 +161,8 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
           s[h].z = fmaf(w[j], v[j][h].z, s[h].z);
           s[h].w = fmaf(w[j], v[j][h].w, s[h].w);
         }
-    const float f[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+    float f[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
+    add_router_rows<KMAX>(a, t, col0, f);
     *reinterpret_cast<uint4*>(a.out + (size_t)t * a.H + col0) = pack8(f);
   } else {
     uint4 v[KMAX][RCPT];
@@ -159,6 +189,7 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
 #pragma unroll
           for (int i = 0; i < 8; ++i) s[i] = fmaf(w[j], f[i], s[i]);
         }
+      add_router_rows<KMAX>(a, t, col, s);
       *reinterpret_cast<uint4*>(a.out + (size_t)t * a.H + col) = pack8(s);
     }
   }
@@ -339,6 +370,31 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_backward_kernel(const Ga
   pdl_wait();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int token_blocks = (a.T + kGateTokens - 1) / kGateTokens;
+  if ((int)blockIdx.x >= token_blocks) {  // W_router for the products to come
+    const int64_t nt = (int64_t)(gridDim.x - token_blocks) * blockDim.x;
+    const int64_t i0 = (int64_t)(blockIdx.x - token_blocks) * blockDim.x + threadIdx.x;
+    if (a.wt) {
+      for (int64_t i = i0; i < (int64_t)a.H / 8 * a.E; i += nt) {
+        const int64_t h = i / a.E * 8;
+        const int e = (int)(i % a.E);
+        uint16_t v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = __ldg(a.w_router + (h + u) * a.E + e);
+        *reinterpret_cast<uint4*>(a.wt + (size_t)e * a.H + h) =
+            make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16, v[4] | (uint32_t)v[5] << 16,
+                       v[6] | (uint32_t)v[7] << 16);
+      }
+    } else {
+      for (int64_t i = i0; i < (int64_t)a.H * 2 * a.ep; i += nt) {
+        const int64_t h = i / (2 * a.ep);
+        int e = (int)(i - h * 2 * a.ep);
+        if (e >= a.ep) e -= a.ep;
+        a.w2[i] = e < a.E ? __ldg(a.w_router + h * a.E + e) : (uint16_t)0;
+      }
+    }
+    return;
+  }
   float acc[kMaxExperts / 32];
 #pragma unroll
   for (int i = 0; i < kMaxExperts / 32; ++i) acc[i] = 0.0f;
@@ -371,6 +427,7 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_backward_kernel(const Ga
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) S += __shfl_xor_sync(0xffffffffu, S, off);
     const float mine = w * (dw - S);
+    if (a.dlk && lane < a.k) a.dlk[tk + lane] = mine;
     uint16_t* out = a.dl + (size_t)t * 2 * a.ep;
 #pragma unroll
     for (int u = 0; u < kMaxExperts / 32; ++u) {
@@ -414,50 +471,56 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_backward_kernel(const Ga
 }
 
 // ----------------------------------------------------------- the router's sums --
-// Block 0 sums the token blocks' dlogits (one expert per thread, block after
-// block), the others the K splits of dW_router.
+// The first blocks sum the token blocks' dlogits, a warp per expert (one thread
+// per expert took 11 us for 128 blocks), the others the K splits of dW_router.
 constexpr int SUM_THREADS = 256;
-__global__ void __launch_bounds__(SUM_THREADS) router_reduce_kernel(const RouterReduceArgs a) {
+__global__ void __launch_bounds__(SUM_THREADS) router_reduce_kernel(const RouterReduceArgs a, int db_blocks) {
   pdl_launch_dependents();
   pdl_wait();
-  if (blockIdx.x == 0) {
-    if (a.db)
-      for (int e = threadIdx.x; e < a.E; e += SUM_THREADS) {
-        float s = 0.0f;
-#pragma unroll 8
-        for (int b = 0; b < a.n_db; ++b) s += __ldg(a.db_part + (size_t)b * a.E + e);
-        a.db[e] = s;
-      }
+  if ((int)blockIdx.x < db_blocks) {
+    const int lane = threadIdx.x & 31;
+    const int e = blockIdx.x * (SUM_THREADS / 32) + (threadIdx.x >> 5);
+    if (e >= a.E) return;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int b = lane; b < a.n_db; b += 32) s += __ldg(a.db_part + (size_t)b * a.E + e);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (lane == 0) a.db[e] = s;
     return;
   }
+  // eight columns of a row of the partial sums: their first and second halves
   const size_t plane = (size_t)a.H * 2 * a.ep;
-  const int64_t n = (int64_t)a.H * a.E;
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * SUM_THREADS + threadIdx.x; i < n;
-       i += (int64_t)(gridDim.x - 1) * SUM_THREADS) {
-    const int h = (int)(i / a.E);
-    const int e = (int)(i - (int64_t)h * a.E);
-    const float* src = a.part + (size_t)h * 2 * a.ep + e;
-    float hi = 0.0f, lo = 0.0f;
-#pragma unroll 4
+  const int per = a.ep / 8;
+  const int64_t n = (int64_t)a.H * per;
+  for (int64_t i = (int64_t)(blockIdx.x - db_blocks) * SUM_THREADS + threadIdx.x; i < n;
+       i += (int64_t)(gridDim.x - db_blocks) * SUM_THREADS) {
+    const int64_t h = i / per;
+    const int e0 = (int)(i - h * per) * 8;
+    const float* src = a.part + h * 2 * a.ep + e0;
+    float hi[8], lo[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) hi[u] = lo[u] = 0.0f;
+#pragma unroll 2
     for (int s = 0; s < a.S; ++s) {
-      hi += __ldg(src + s * plane);
-      lo += __ldg(src + s * plane + a.ep);
+      const float4* p = reinterpret_cast<const float4*>(src + s * plane);
+      const float4* q = reinterpret_cast<const float4*>(src + s * plane + a.ep);
+      const float4 p0 = __ldg(p), p1 = __ldg(p + 1), q0 = __ldg(q), q1 = __ldg(q + 1);
+      hi[0] += p0.x, hi[1] += p0.y, hi[2] += p0.z, hi[3] += p0.w;
+      hi[4] += p1.x, hi[5] += p1.y, hi[6] += p1.z, hi[7] += p1.w;
+      lo[0] += q0.x, lo[1] += q0.y, lo[2] += q0.z, lo[3] += q0.w;
+      lo[4] += q1.x, lo[5] += q1.y, lo[6] += q1.z, lo[7] += q1.w;
     }
-    a.dw_router[i] = __bfloat16_as_ushort(__float2bfloat16_rn(hi + lo));
-  }
-}
-
-__global__ void __launch_bounds__(SUM_THREADS) router_twice_kernel(const uint16_t* w, int H, int E, int ep,
-                                                                   uint16_t* w2) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t n = (int64_t)H * 2 * ep;
-  for (int64_t i = (int64_t)blockIdx.x * SUM_THREADS + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * SUM_THREADS) {
-    const int64_t h = i / (2 * ep);
-    int e = (int)(i - h * 2 * ep);
-    if (e >= ep) e -= ep;
-    w2[i] = e < E ? __ldg(w + h * E + e) : (uint16_t)0;
+    uint16_t* dst = a.dw_router + h * a.E + e0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) hi[u] += lo[u];
+    if (a.E % 8 == 0) {
+      *reinterpret_cast<uint4*>(dst) = pack8(hi);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (e0 + u < a.E) dst[u] = __bfloat16_as_ushort(__float2bfloat16_rn(hi[u]));
+    }
   }
 }
 
@@ -551,17 +614,15 @@ cudaError_t launch_dequantize_a8(int64_t rows, int cols, const int8_t* codes, co
 }
 
 cudaError_t launch_gate_backward(const GateBackwardArgs& a, cudaStream_t st) {
-  return launch(gate_backward_kernel, dim3((unsigned)((a.T + kGateTokens - 1) / kGateTokens)), GATE_WARPS * 32, st, a);
+  const int64_t items = a.wt ? (int64_t)a.H / 8 * a.E : (int64_t)a.H * 2 * a.ep;
+  const unsigned grid = (unsigned)((a.T + kGateTokens - 1) / kGateTokens) + blocks_for(items, GATE_WARPS * 32, 512);
+  return launch(gate_backward_kernel, dim3(grid), GATE_WARPS * 32, st, a);
 }
 
 cudaError_t launch_router_reduce(const RouterReduceArgs& a, cudaStream_t st) {
-  const unsigned g = 1 + blocks_for((int64_t)a.H * a.E, SUM_THREADS, 1024);
-  return launch(router_reduce_kernel, dim3(g), SUM_THREADS, st, a);
-}
-
-cudaError_t launch_router_twice(const uint16_t* w, int H, int E, int ep, uint16_t* w2, cudaStream_t st) {
-  return launch(router_twice_kernel, dim3(blocks_for((int64_t)H * 2 * ep, SUM_THREADS, 1024)), SUM_THREADS, st,
-                w, H, E, ep, w2);
+  const int db_blocks = a.db ? (a.E + SUM_THREADS / 32 - 1) / (SUM_THREADS / 32) : 0;
+  const unsigned g = db_blocks + blocks_for((int64_t)a.H * a.ep / 8, SUM_THREADS, 1024);
+  return launch(router_reduce_kernel, dim3(g), SUM_THREADS, st, a, db_blocks);
 }
 
 cudaError_t launch_router_softmax(const float* logits, int ldl, const float* bias, int T, int E, float* probs,

@@ -13,6 +13,7 @@ and keep nothing between calls.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 from typing import NamedTuple
 
@@ -101,17 +102,34 @@ def train_status(stream=None) -> int:
     return moe_get_device_status(_shared_status(torch.cuda.current_device()), stream)
 
 
-def _workspace(size_fn, shape, dev: int, *extra) -> torch.Tensor:
-    n = int(size_fn(ctypes.byref(shape), *extra))
-    if n == 0:
-        _check(MOE_ERR_UNSUPPORTED)
-    return torch.empty(n, dtype=_U8, device=torch.device("cuda", dev))
+class _Call:
+    """A shape as the calls pass it, and the workspace each needs for it."""
+
+    __slots__ = ("shape", "ref", "_sizes")
+
+    def __init__(self, *args):
+        self.shape = make_shape(*args)
+        self.ref = ctypes.byref(self.shape)
+        self._sizes = {}
+
+    def workspace(self, name: str, device, *extra) -> torch.Tensor:
+        n = self._sizes.get((name, extra))
+        if n is None:
+            n = int(getattr(_lib(), name + "_workspace_size")(self.ref, *extra))
+            if n == 0:
+                _check(MOE_ERR_UNSUPPORTED)
+            self._sizes[name, extra] = n
+        return torch.empty(n, dtype=_U8, device=device)
 
 
-def _out(t, shape, dtype, name: str, dev: int) -> torch.Tensor:
+# T, H, F, E, k, capacity_factor, gating, act -> _Call
+_call = functools.lru_cache(maxsize=1024)(_Call)
+
+
+def _out(t, shape, dtype, name: str, dev: int, device) -> torch.Tensor:
     """`t` checked against a shape, or a new tensor of it."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return torch.empty(shape, dtype=dtype, device=device)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     _addr(t, dtype, name, t.numel(), dev)
@@ -153,11 +171,10 @@ class A8Tensor:
         return self.codes.shape
 
 
-def _a8_new(shape, dev: int) -> A8Tensor:
+def _a8_new(shape, device) -> A8Tensor:
     q = A8Tensor.__new__(A8Tensor)
-    d = torch.device("cuda", dev)
-    q.codes = torch.empty(shape, dtype=_I8, device=d)
-    q.scales = torch.empty((*shape[:-1], -(-shape[-1] // 32)), dtype=_U8, device=d)
+    q.codes = torch.empty(shape, dtype=_I8, device=device)
+    q.scales = torch.empty((*shape[:-1], -(-shape[-1] // 32)), dtype=_U8, device=device)
     return q
 
 
@@ -177,7 +194,7 @@ def quantize_a8(x: torch.Tensor, stream=None) -> A8Tensor:
         raise ValueError("x must have at least one dimension")
     dev, raw = _here()
     src = _addr(x, _BF, "x", x.numel(), dev)
-    q = _a8_new(tuple(x.shape), dev)
+    q = _a8_new(tuple(x.shape), x.device)
     rc = _lib().moet_quantize_a8(_rows(x.shape), x.shape[-1], src, q.codes.data_ptr(), q.scales.data_ptr(), raw)
     if rc:
         _check(rc)
@@ -192,7 +209,7 @@ def dequantize_a8(q: A8Tensor, out: torch.Tensor | None = None, stream=None) -> 
     dev, raw = _here()
     codes = _addr(q.codes, _I8, "codes", q.codes.numel(), dev)
     scales = _addr(q.scales, _U8, "scales", q.scales.numel(), dev)
-    out = _out(out, q.codes.shape, _BF, "out", dev)
+    out = _out(out, q.codes.shape, _BF, "out", dev, q.codes.device)
     rc = _lib().moet_dequantize_a8(_rows(q.shape), q.shape[-1], codes, scales, out.data_ptr(), raw)
     if rc:
         _check(rc)
@@ -209,12 +226,12 @@ def _kept_ptrs(z, shape, name: str, dev: int):
 
 # ------------------------------------------------------- rows there and back --
 
-def _slot_shape(rows: torch.Tensor, slot: torch.Tensor, name: str) -> moe_shape:
+def _slot_shape(rows: torch.Tensor, slot: torch.Tensor, name: str) -> _Call:
     _need(slot.dim() == 2, f"slot must be [T, k], got {tuple(slot.shape)}")
     T, k = slot.shape
     _need(rows.dim() == 2 and rows.shape[0] >= T * k, f"{name} must be [T * k, H] with T * k = {T * k}, got "
           f"{tuple(rows.shape)}")
-    return make_shape(T, rows.shape[1], 8, max(k, 1), k)
+    return _call(T, rows.shape[1], 8, max(k, 1), k)
 
 
 def dispatch_rows_backward(dxp: torch.Tensor, slot: torch.Tensor, out: torch.Tensor | None = None,
@@ -224,11 +241,11 @@ def dispatch_rows_backward(dxp: torch.Tensor, slot: torch.Tensor, out: torch.Ten
     if stream is not None:
         with _on(stream):
             return dispatch_rows_backward(dxp, slot, out)
-    s = _slot_shape(dxp, slot, "dxp")
+    c = _slot_shape(dxp, slot, "dxp")
     dev, raw = _here()
     src, sl = _addr(dxp, _BF, "dxp", dxp.numel(), dev), _addr(slot, _I32, "slot", slot.numel(), dev)
-    out = _out(out, (s.T, s.H), _BF, "out", dev)
-    rc = _lib().moet_dispatch_rows_backward(ctypes.byref(s), src, sl, out.data_ptr(), raw)
+    out = _out(out, (c.shape.T, c.shape.H), _BF, "out", dev, dxp.device)
+    rc = _lib().moet_dispatch_rows_backward(c.ref, src, sl, out.data_ptr(), raw)
     if rc:
         _check(rc)
     return out
@@ -242,13 +259,14 @@ def combine_backward(dy: torch.Tensor, Y: torch.Tensor, weights: torch.Tensor, s
     if stream is not None:
         with _on(stream):
             return combine_backward(dy, Y, weights, slot, dY, dweights)
-    s = _slot_shape(Y, slot, "Y")
+    c = _slot_shape(Y, slot, "Y")
+    s = c.shape
     dev, raw = _here()
     p = (_shaped(dy, (s.T, s.H), _BF, "dy", dev), _addr(Y, _BF, "Y", Y.numel(), dev),
          _shaped(weights, (s.T, s.k), _F32, "weights", dev), _addr(slot, _I32, "slot", slot.numel(), dev))
-    dY = _out(dY, Y.shape, _BF, "dY", dev)
-    dweights = _out(dweights, (s.T, s.k), _F32, "dweights", dev)
-    rc = _lib().moet_combine_backward(ctypes.byref(s), *p, dY.data_ptr(), dweights.data_ptr(), raw)
+    dY = _out(dY, Y.shape, _BF, "dY", dev, Y.device)
+    dweights = _out(dweights, (s.T, s.k), _F32, "dweights", dev, Y.device)
+    rc = _lib().moet_combine_backward(c.ref, *p, dY.data_ptr(), dweights.data_ptr(), raw)
     if rc:
         _check(rc)
     return dY, dweights
@@ -256,14 +274,14 @@ def combine_backward(dy: torch.Tensor, Y: torch.Tensor, weights: torch.Tensor, s
 
 # ------------------------------------------------------------- experts' FFN --
 
-def _ffn_shape(xp, w1, w2, act: str) -> moe_shape:
+def _ffn_shape(xp, w1, w2, act: str) -> _Call:
     _need(w2.dim() == 3, f"w2 must be [E, F, H], got {tuple(w2.shape)}")
     E, F, H = w2.shape
     _need(xp.dim() == 2 and xp.shape[1] == H, f"xp must be [rows, {H}], got {tuple(xp.shape)}")
-    s = make_shape(xp.shape[0], H, F, E, 1, None, MOE_GATE_TOPK_SOFTMAX, act)
-    f1 = 2 * F if s.expert_act else F
+    c = _call(xp.shape[0], H, F, E, 1, None, MOE_GATE_TOPK_SOFTMAX, act)
+    f1 = 2 * F if c.shape.expert_act else F
     _need(tuple(w1.shape) == (E, H, f1), f"w1 must be {(E, H, f1)} for act = {act!r}, got {tuple(w1.shape)}")
-    return s
+    return c
 
 
 def _z_shape(rows: int, s: moe_shape):
@@ -280,21 +298,22 @@ def expert_ffn(xp: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, offsets: to
     if stream is not None:
         with _on(stream):
             return expert_ffn(xp, w1, w2, offsets, act, keep_bits)
-    s = _ffn_shape(xp, w1, w2, act)
+    c = _ffn_shape(xp, w1, w2, act)
+    s, d = c.shape, xp.device
     dev, raw = _here()
     rows = xp.shape[0]
     p = (_addr(xp, _BF, "xp", xp.numel(), dev), _addr(w1, _BF, "w1", w1.numel(), dev),
          _addr(w2, _BF, "w2", w2.numel(), dev), _shaped(offsets, (s.E + 1,), _I32, "offsets", dev))
-    Y = _out(None, (rows, s.H), _BF, "Y", dev)
+    Y = torch.empty((rows, s.H), dtype=_BF, device=d)
     if keep_bits == 8:
-        z = _a8_new(_z_shape(rows, s), dev)
+        z = _a8_new(_z_shape(rows, s), d)
         zp = z.codes.data_ptr(), z.scales.data_ptr()
     else:
-        z = _out(None, _z_shape(rows, s), _BF, "z", dev)
+        z = torch.empty(_z_shape(rows, s), dtype=_BF, device=d)
         zp = z.data_ptr(), None
     lib = _lib()
-    ws = _workspace(lib.moet_expert_ffn_workspace_size, s, dev)
-    rc = lib.moet_expert_ffn(ctypes.byref(s), keep_bits, *p, Y.data_ptr(), *zp, _shared_status(dev).data_ptr(),
+    ws = c.workspace("moet_expert_ffn", d)
+    rc = lib.moet_expert_ffn(c.ref, keep_bits, *p, Y.data_ptr(), *zp, _shared_status(dev).data_ptr(),
                              ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
@@ -309,17 +328,18 @@ def expert_ffn_backward(xp: torch.Tensor, z, w1: torch.Tensor, w2: torch.Tensor,
     if stream is not None:
         with _on(stream):
             return expert_ffn_backward(xp, z, w1, w2, offsets, dY, act)
-    s = _ffn_shape(xp, w1, w2, act)
+    c = _ffn_shape(xp, w1, w2, act)
+    s, d = c.shape, xp.device
     dev, raw = _here()
     rows = xp.shape[0]
     bits, zp, zs = _kept_ptrs(z, _z_shape(rows, s), "z", dev)
     src = _addr(xp, _BF, "xp", xp.numel(), dev)
     p = (_addr(w1, _BF, "w1", w1.numel(), dev), _addr(w2, _BF, "w2", w2.numel(), dev),
          _shaped(offsets, (s.E + 1,), _I32, "offsets", dev), _shaped(dY, (rows, s.H), _BF, "dY", dev))
-    dxp, dw1, dw2 = (_out(None, t.shape, _BF, "gradient", dev) for t in (xp, w1, w2))
+    dxp, dw1, dw2 = (torch.empty(t.shape, dtype=_BF, device=d) for t in (xp, w1, w2))
     lib = _lib()
-    ws = _workspace(lib.moet_expert_ffn_backward_workspace_size, s, dev)
-    rc = lib.moet_expert_ffn_backward(ctypes.byref(s), bits, src, zp, zs, *p, dxp.data_ptr(), dw1.data_ptr(),
+    ws = c.workspace("moet_expert_ffn_backward", d)
+    rc = lib.moet_expert_ffn_backward(c.ref, bits, src, zp, zs, *p, dxp.data_ptr(), dw1.data_ptr(),
                                       dw2.data_ptr(), _shared_status(dev).data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
@@ -328,11 +348,11 @@ def expert_ffn_backward(xp: torch.Tensor, z, w1: torch.Tensor, w2: torch.Tensor,
 
 # ---------------------------------------------------------- router and gate --
 
-def _route_shape(x, w_router, k: int, gating: int) -> moe_shape:
+def _route_shape(x, w_router, k: int, gating: int) -> _Call:
     _need(w_router.dim() == 2, f"w_router must be [H, E], got {tuple(w_router.shape)}")
     H, E = w_router.shape
     _need(x.dim() == 2 and x.shape[1] == H, f"x must be [T, {H}], got {tuple(x.shape)}")
-    return make_shape(x.shape[0], H, 8, E, k, None, gating)
+    return _call(x.shape[0], H, 8, E, k, None, gating)
 
 
 def router_probs(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor | None = None,
@@ -342,14 +362,15 @@ def router_probs(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor | N
     if stream is not None:
         with _on(stream):
             return router_probs(x, w_router, bias)
-    s = _route_shape(x, w_router, 1, MOE_GATE_TOPK_SOFTMAX)
+    c = _route_shape(x, w_router, 1, MOE_GATE_TOPK_SOFTMAX)
+    s = c.shape
     dev, raw = _here()
     p = (_addr(x, _BF, "x", x.numel(), dev), _addr(w_router, _BF, "w_router", w_router.numel(), dev),
          None if bias is None else _shaped(bias, (s.E,), _F32, "bias", dev))
-    probs = _out(None, (s.T, s.E), _F32, "probs", dev)
+    probs = torch.empty((s.T, s.E), dtype=_F32, device=x.device)
     lib = _lib()
-    ws = _workspace(lib.moet_router_probs_workspace_size, s, dev)
-    rc = lib.moet_router_probs(ctypes.byref(s), *p, probs.data_ptr(), _shared_status(dev).data_ptr(),
+    ws = c.workspace("moet_router_probs", x.device)
+    rc = lib.moet_router_probs(c.ref, *p, probs.data_ptr(), _shared_status(dev).data_ptr(),
                                ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
@@ -366,7 +387,8 @@ def route_backward(x: torch.Tensor, w_router: torch.Tensor, ids: torch.Tensor, w
         with _on(stream):
             return route_backward(x, w_router, ids, weights, dweights, gating, probs)
     _need(ids.dim() == 2, f"ids must be [T, k], got {tuple(ids.shape)}")
-    s = _route_shape(x, w_router, ids.shape[1], gating)
+    c = _route_shape(x, w_router, ids.shape[1], gating)
+    s, d = c.shape, x.device
     dev, raw = _here()
     tk = (s.T, s.k)
     if gating == MOE_GATE_SOFTMAX_TOPK:
@@ -377,12 +399,12 @@ def route_backward(x: torch.Tensor, w_router: torch.Tensor, ids: torch.Tensor, w
     p = (_addr(x, _BF, "x", x.numel(), dev), _addr(w_router, _BF, "w_router", w_router.numel(), dev),
          _shaped(ids, tk, _I32, "ids", dev), _shaped(weights, tk, _F32, "weights", dev), pp,
          _shaped(dweights, tk, _F32, "dweights", dev))
-    dx = _out(None, x.shape, _BF, "dx", dev)
-    dw = _out(None, w_router.shape, _BF, "dw_router", dev)
-    db = _out(None, (s.E,), _F32, "dbias", dev)
+    dx = torch.empty(x.shape, dtype=_BF, device=d)
+    dw = torch.empty(w_router.shape, dtype=_BF, device=d)
+    db = torch.empty(s.E, dtype=_F32, device=d)
     lib = _lib()
-    ws = _workspace(lib.moet_route_backward_workspace_size, s, dev)
-    rc = lib.moet_route_backward(ctypes.byref(s), *p, dx.data_ptr(), dw.data_ptr(), db.data_ptr(),
+    ws = c.workspace("moet_route_backward", d)
+    rc = lib.moet_route_backward(c.ref, *p, dx.data_ptr(), dw.data_ptr(), db.data_ptr(),
                                  _shared_status(dev).data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
@@ -409,12 +431,36 @@ class Saved:
     bits (else x itself), the routing (``routing``) and, for
     MOE_GATE_SOFTMAX_TOPK, the router's probabilities."""
 
-    __slots__ = ("shape", "x", "z", "routing", "probs", "versions")
+    __slots__ = ("call", "x", "z", "probs", "versions", "_block")
+
+    # ids, perm, slot, gate weights, counts and offsets in one block of 32-bit
+    # words, each on a 16-byte boundary
+    @staticmethod
+    def _layout(T: int, k: int, E: int):
+        n4, e4 = (T * k + 3) // 4 * 4, (E + 4) // 4 * 4
+        return 0, n4, 2 * n4, 3 * n4, 4 * n4, 4 * n4 + e4, 4 * n4 + 2 * e4
+
+    def _addresses(self):
+        """Of ids, perm, slot, weights, counts, offsets."""
+        s, a = self.call.shape, self._block.data_ptr()
+        return [a + 4 * o for o in self._layout(s.T, s.k, s.E)[:6]]
+
+    @property
+    def routing(self) -> RoutingBuffers:
+        s, b = self.call.shape, self._block
+        n, (o_ids, o_perm, o_slot, o_w, o_cnt, o_off, _) = s.T * s.k, self._layout(s.T, s.k, s.E)
+        tk = (s.T, s.k)
+        return RoutingBuffers(ids=b[o_ids:o_ids + n].view(tk), weights=b[o_w:o_w + n].view(_F32).view(tk),
+                              counts=b[o_cnt:o_cnt + s.E], offsets=b[o_off:o_off + s.E + 1], perm=b[o_perm:o_perm + n],
+                              slot=b[o_slot:o_slot + n].view(tk))
+
+    @property
+    def shape(self) -> moe_shape:
+        return self.call.shape
 
     def nbytes(self) -> int:
         """Device bytes held (x itself not counted with keep_bits 16)."""
-        ts = [self.routing.ids, self.routing.weights, self.routing.counts, self.routing.offsets, self.routing.perm,
-              self.routing.slot]
+        ts = [self._block]
         for t in (self.z, self.x, self.probs):
             if isinstance(t, A8Tensor):
                 ts += [t.codes, t.scales]
@@ -445,7 +491,7 @@ class MoETrainLayer:
         self.k, self.act, self.keep_bits = int(k), act, int(keep_bits)
         self.capacity_factor, self.gating = capacity_factor, int(gating)
         self.w_router, self.w1, self.w2, self.bias = w_router, w1, w2, bias
-        s = self._shape(1)
+        s = self._call(1).shape
         dev = w_router.device.index
         for (t, dt, shape, name) in self._params(s):
             check_tensor(t, dt, name, 0, dev)
@@ -463,8 +509,8 @@ class MoETrainLayer:
             p.append((self.bias, _F32, (self.E,), "bias"))
         return p
 
-    def _shape(self, T: int) -> moe_shape:
-        return make_shape(T, self.H, self.F, self.E, self.k, self.capacity_factor, self.gating, self.act)
+    def _call(self, T: int) -> _Call:
+        return _call(T, self.H, self.F, self.E, self.k, self.capacity_factor, self.gating, self.act)
 
     def _weights(self, s, dev: int):
         p = [_shaped(t, shape, dt, name, dev) for t, dt, shape, name in self._params(s)]
@@ -477,36 +523,29 @@ class MoETrainLayer:
                 return self(x)
         _need(x.dim() == 2 and x.shape[1] == self.H, f"x must be [T, {self.H}], got {tuple(x.shape)}")
         dev, raw = _here()
-        T, k, E = x.shape[0], self.k, self.E
-        s = self._shape(T)
+        T, d = x.shape[0], x.device
+        c = self._call(T)
+        s = c.shape
         wr, w1, w2, b = self._weights(s, dev)
         src = _addr(x, _BF, "x", T * self.H, dev)
-        d = torch.device("cuda", dev)
-        lib = _lib()
-        ws = _workspace(lib.moet_forward_workspace_size, s, dev)
+        ws = c.workspace("moet_forward", d)
         y = torch.empty((T, self.H), dtype=_BF, device=d)
-        n = T * k
-        # the routing's tensors in one allocation, each on a 16-byte boundary
-        n4, e4 = (n + 3) // 4 * 4, (E + 4) // 4 * 4
-        ints = torch.empty(3 * n4 + 2 * e4, dtype=_I32, device=d)
-        r = RoutingBuffers(ids=ints[:n].view(T, k), weights=torch.empty((T, k), dtype=_F32, device=d),
-                           counts=ints[3 * n4:3 * n4 + E], offsets=ints[3 * n4 + e4:3 * n4 + e4 + E + 1],
-                           perm=ints[n4:n4 + n], slot=ints[2 * n4:2 * n4 + n].view(T, k))
         v = Saved()
-        v.shape, v.routing, v.probs = s, r, None
+        v.call, v.probs = c, None
+        v._block = torch.empty(v._layout(T, self.k, self.E)[-1], dtype=_I32, device=d)
+        ids, perm, slot, weights, counts, offsets = v._addresses()
         if self.keep_bits == 8:
-            v.z, v.x = _a8_new(_z_shape(n, s), dev), _a8_new((T, self.H), dev)
+            v.z, v.x = _a8_new(_z_shape(T * self.k, s), d), _a8_new((T, self.H), d)
             kept = v.z.codes.data_ptr(), v.z.scales.data_ptr(), v.x.codes.data_ptr(), v.x.scales.data_ptr()
         else:
-            v.z, v.x = torch.empty(_z_shape(n, s), dtype=_BF, device=d), x
+            v.z, v.x = torch.empty(_z_shape(T * self.k, s), dtype=_BF, device=d), x
             kept = v.z.data_ptr(), None, None, None
         if self.gating == MOE_GATE_SOFTMAX_TOPK:
-            v.probs = torch.empty((T, E), dtype=_F32, device=d)
+            v.probs = torch.empty((T, self.E), dtype=_F32, device=d)
         v.versions = self._versions(v)
-        rc = lib.moet_forward(ctypes.byref(s), self.keep_bits, src, wr, b, w1, w2, y.data_ptr(), r.ids.data_ptr(),
-                              r.weights.data_ptr(), r.counts.data_ptr(), r.offsets.data_ptr(), r.perm.data_ptr(),
-                              r.slot.data_ptr(), *kept, None if v.probs is None else v.probs.data_ptr(),
-                              self.status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+        rc = _lib().moet_forward(c.ref, self.keep_bits, src, wr, b, w1, w2, y.data_ptr(), ids, weights, counts,
+                                 offsets, perm, slot, *kept, None if v.probs is None else v.probs.data_ptr(),
+                                 self.status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
         if rc:
             _check(rc)
         return y, v
@@ -525,28 +564,26 @@ class MoETrainLayer:
                 return self.backward(saved, dy, bias_grad)
         if not isinstance(saved, Saved):
             raise TypeError("saved must be what a forward of this layer returned")
-        s, r = saved.shape, saved.routing
+        c, s = saved.call, saved.call.shape
         _need((s.H, s.F, s.E, s.k) == (self.H, self.F, self.E, self.k), "saved is of a layer of another shape")
         _need(self._versions(saved) == saved.versions,
               "x or a weight was changed or replaced after the forward that saved is of")
         dev, raw = _here()
-        T = s.T
         wr, w1, w2, _ = self._weights(s, dev)
-        g = _shaped(dy, (T, s.H), _BF, "dy", dev)
+        g = _shaped(dy, (s.T, s.H), _BF, "dy", dev)
         bits, zp, zs = _kept_ptrs(saved.z, saved.z.shape, "z", dev)
-        _, xp, xs = _kept_ptrs(saved.x, (T, s.H), "x", dev)
-        d = torch.device("cuda", dev)
-        lib = _lib()
-        ws = _workspace(lib.moet_backward_workspace_size, s, dev, bits)
-        out = Gradients(torch.empty((T, s.H), dtype=_BF, device=d), torch.empty_like(self.w_router),
+        _, xp, xs = _kept_ptrs(saved.x, (s.T, s.H), "x", dev)
+        ids, perm, slot, weights, _, offsets = saved._addresses()
+        d = dy.device
+        ws = c.workspace("moet_backward", d, bits)
+        out = Gradients(torch.empty((s.T, s.H), dtype=_BF, device=d), torch.empty_like(self.w_router),
                         torch.empty(s.E, dtype=_F32, device=d) if bias_grad else None,
                         torch.empty_like(self.w1), torch.empty_like(self.w2))
-        rc = lib.moet_backward(ctypes.byref(s), bits, g, xp, xs, wr, w1, w2, r.ids.data_ptr(), r.weights.data_ptr(),
-                               r.offsets.data_ptr(), r.perm.data_ptr(), r.slot.data_ptr(), zp, zs,
-                               None if saved.probs is None else saved.probs.data_ptr(), out.dx.data_ptr(),
-                               out.dw_router.data_ptr(), None if out.dbias is None else out.dbias.data_ptr(),
-                               out.dw1.data_ptr(), out.dw2.data_ptr(), self.status.data_ptr(), ws.data_ptr(),
-                               ws.numel(), raw)
+        rc = _lib().moet_backward(c.ref, bits, g, xp, xs, wr, w1, w2, ids, weights, offsets, perm, slot, zp, zs,
+                                  None if saved.probs is None else saved.probs.data_ptr(), out.dx.data_ptr(),
+                                  out.dw_router.data_ptr(), None if out.dbias is None else out.dbias.data_ptr(),
+                                  out.dw1.data_ptr(), out.dw2.data_ptr(), self.status.data_ptr(), ws.data_ptr(),
+                                  ws.numel(), raw)
         if rc:
             _check(rc)
         return out
