@@ -37,7 +37,8 @@
  *   - `ws` holds nothing before or after a call.
  *   - Outputs must not overlap inputs.
  *   - offsets, perm, slot and ids are a dispatch's (moe_route, moe_dispatch);
- *     entries outside their range are not followed outside a buffer.
+ *     entries outside their range are not followed outside a buffer, and
+ *     offsets that are not ascending within [0, T*k] set MOE_DEV_BAD_ID.
  */
 #ifndef MOE_GB300_MOE_TRAIN_H
 #define MOE_GB300_MOE_TRAIN_H

@@ -145,7 +145,7 @@ int fwd_product(const moe_shape* s, int bits, const uint16_t* xp, const uint16_t
   return MOE_OK;
 }
 
-// Y = h W2: rounded to bf16 by the forward's own kernel, or kept in fp32
+// Y = h W2 in bf16, or (Y32) in fp32
 int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, const int32_t* offsets, uint16_t* Y,
                   float* Y32, void* status, cudaStream_t st) {
   const size_t rows = rows_of(s);
@@ -153,24 +153,11 @@ int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, con
   TRY(map_rows(&ta, h, s->F, rows, 128, "h"));
   TRY(map_rows(&ta64, h, s->F, rows, 64, "h"));
   TRY(map_weights(&tb, w2, s->H, s->F, s->E, 64, "W2"));
-  const int64_t ub = row_tiles(rows, s->E, s->H, kGemmBN);
-  if (Y32) {
-    TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->H, s->F, status);
-    a.out32 = Y32;
-    CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, ub, st), "expert GEMM2 launch");
-    return MOE_OK;
-  }
-  GemmArgs g = {};
-  g.offsets = offsets;
-  g.E = g.E_w = s->E;
-  g.N = s->H;
-  g.K = s->F;
-  g.out = Y;
-  g.T = s->T;
-  g.splits = 1;
-  g.status = static_cast<int*>(status);
-  g.wait_limit_ns = kWaitLimitNs;
-  CUDA_TRY(launch_grouped_gemm(kGemmPlain, ta, tb, ta64, g, (int)(ub < (1 << 30) ? ub : (1 << 30)), st, true),
+  TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->H, s->F, status);
+  a.out = Y;
+  a.out32 = Y32;
+  CUDA_TRY(launch_train_gemm(Y32 ? kTrainPlain : kTrainPlainBf16, ta, tb, ta64, a,
+                             row_tiles(rows, s->E, s->H, 256), st),
            "expert GEMM2 launch");
   return MOE_OK;
 }

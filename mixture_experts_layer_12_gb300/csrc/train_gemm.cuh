@@ -7,7 +7,7 @@
 //          dz = w g act'(z), w h, and <g, h> (the gate weight's gradient)
 //   Rows   out = A_e W[e]^T                     (dxp = dz W1^T)
 //   Wgrad  out[e] = A_e^T B_e                   (dW2 = (w h)^T dy, dW1 = xp^T dz)
-//   Plain  out = A_e W[e] in fp32               (Y = h W2, the router's logits)
+//   Plain  out = A_e W[e], fp32 or bf16          (Y = h W2, the router's logits)
 //
 // One design serves all (as the forward's expert GEMM): CTA pairs run the
 // 2-SM tcgen05.mma (M = 256, N = 256, K = 16, fp32 in TMEM), each CTA holding
@@ -77,7 +77,7 @@ struct TrainTraits {
   static constexpr bool WGRAD = OP == kTrainWgrad || OP == kTrainWgradF32;
   static constexpr bool A_MN = WGRAD;
   static constexpr bool B_MN = !(BWD || OP == kTrainRows || OP == kTrainRowsF32);
-  static constexpr bool A_PADDED = !(FWD || OP == kTrainPlain);
+  static constexpr bool A_PADDED = !(FWD || OP == kTrainPlain || OP == kTrainPlainBf16);
   static constexpr bool OUT32 = OP == kTrainPlain || OP == kTrainWgradF32 || OP == kTrainRowsF32;
   static constexpr int BN_OUT = PAIRED ? TBN / 2 : TBN;
   // the epilogue's buffers per warp (FWD: z and h, BWD: z turned into dz, and
@@ -103,7 +103,9 @@ struct TrainTile {
 // same time share the columns of B through L2.  An M block with at most 128
 // rows runs as an M = 128 MMA (TMEM lanes 0-63: the CTA's 64 rows, columns
 // 0..127; lanes 64-127: the same rows, columns 128..255), else an N block
-// with at most 128 columns as N = 128; not for paired gate and up columns.
+// with at most 128 columns as N = 128.  With paired gate and up columns such an
+// M block's CTA loads 64 gate and 64 up columns of the same outputs, so that both
+// land in the same lanes; N blocks stay whole.
 template <int OP>
 __device__ __forceinline__ TrainTile train_tile(const TrainCtrl& c, const TrainGemmArgs& p, int tile,
                                                 int& e) {
@@ -124,7 +126,7 @@ __device__ __forceinline__ TrainTile train_tile(const TrainCtrl& c, const TrainG
     t.k16 = 0;
     t.kb = (p.K + TBK - 1) / TBK;
   }
-  t.half = !TT::PAIRED && m - t.base <= TPAIR_M / 2;
+  t.half = m - t.base <= TPAIR_M / 2;
   t.nhalf = !TT::PAIRED && !t.half && p.N - t.nb * TBN <= TBN / 2;
   return t;
 }
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   }
   pdl_wait();  // offsets, operands and output buffers belong to earlier kernels
   if (warp == 0) {
-    seg_scan(p.seg, c.seg, c.tile_start, lane, [&](int n) {
+    seg_scan(p.seg, c.seg, c.tile_start, lane, pair == 0 && rank == 0 ? p.status : nullptr, [&](int n) {
       const int m = TT::WGRAD ? p.M : n;
       return (m + TPAIR_M - 1) / TPAIR_M * NB;
     });
@@ -485,9 +487,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const int off = TT::A_PADDED ? c.seg.pad_off[t.e] : c.seg.row_off[t.e];
         // this CTA's first row of A's M and column of B's N
         const int arow = t.base + rank * (t.half ? TBM / 2 : TBM);
-        const int bcol = TT::PAIRED  ? rank * p.N + t.nb * TT::BN_OUT
+        const int bcol = TT::PAIRED  ? t.nb * TT::BN_OUT + (t.half ? rank * 64 : rank * p.N)
                          : t.nhalf   ? t.nb * TBN + rank * (TBN / 4)
                                      : t.nb * TBN + rank * (TBN / 2);
+        const int bcol2 = TT::PAIRED && t.half ? bcol + p.N : bcol + 64;  // of the second box
         const uint32_t a_bytes = t.half ? T_OP_BYTES / 2 : T_OP_BYTES;
         const int b_boxes = t.nhalf ? 1 : 2;  // MN-major: 64-column boxes
         const uint32_t bytes = a_bytes + (TT::B_MN ? b_boxes * T_BOX : T_OP_BYTES);
@@ -505,13 +508,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             tma_load_2d_pair(a, &tm_a, full_cl, arow, krow);
             if (!t.half) tma_load_2d_pair(a + T_BOX, &tm_a, full_cl, arow + 64, krow);
             tma_load_2d_pair(b, &tm_b, full_cl, bcol, krow);
-            if (!t.nhalf) tma_load_2d_pair(b + T_BOX, &tm_b, full_cl, bcol + 64, krow);
+            if (!t.nhalf) tma_load_2d_pair(b + T_BOX, &tm_b, full_cl, bcol2, krow);
           } else {
             // rows past the segment's end are computed but never stored
             tma_load_2d_pair(a, t.half ? &tm_a64 : &tm_a, full_cl, kb * TBK, off + arow);
             if constexpr (TT::B_MN) {
               tma_load_3d_pair(b, &tm_b, full_cl, bcol, kb * TBK, t.e);
-              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol + 64, kb * TBK, t.e);
+              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol2, kb * TBK, t.e);
             } else {
               tma_load_3d_pair(b, &tm_b, full_cl, kb * TBK, bcol, t.e);
             }
@@ -606,8 +609,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       Part a;
       a.t = train_tile<OP>(c, p, tile, e);
       a.row0 = a.t.base + (a.t.half ? rank * (TBM / 2) + (q & 1) * 32 : rank * TBM + q * 32);
-      a.col_base = a.t.nb * TT::BN_OUT + (a.t.half ? (q >> 1) * 128 : 0);
-      const int n_chunks = a.t.half || a.t.nhalf || TT::PAIRED ? 4 : 8;  // both warps'
+      a.col_base = a.t.nb * TT::BN_OUT + (a.t.half ? (q >> 1) * (TT::BN_OUT / 2) : 0);
+      const int n_chunks = (a.t.half || a.t.nhalf ? 4 : 8) / (TT::PAIRED ? 2 : 1);  // both warps'
       a.ch0 = wh * (n_chunks / 2);
       a.ch1 = a.ch0 + n_chunks / 2;
       a.n_seg = TT::WGRAD ? p.M : c.seg.rows[a.t.e];
@@ -734,8 +737,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
           [[maybe_unused]] uint32_t uv[32];
           if (t.kb > 0) {
             tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
-            // gate columns are the accumulator's first 128, up columns the others
-            if constexpr (TT::PAIRED) tmem_ld_x32(tbase + (uint32_t)(TT::BN_OUT + ch * 32), uv);
+            // gate columns are the accumulator's first 128 (64 with M = 128), up
+            // columns the others
+            if constexpr (TT::PAIRED) tmem_ld_x32(tbase + (uint32_t)((t.half ? 64 : 128) + ch * 32), uv);
             tmem_ld_wait();
           } else {
 #pragma unroll

@@ -8,6 +8,7 @@ cudaError_t launch_train_gemm_fwd(int op, const CUtensorMap& tm_a, const CUtenso
                                   cudaStream_t st) {
   if (op == kTrainFwdGelu) return train_launch<kTrainFwdGelu>(tm_a, tm_b, tm_a64, a, max_tiles, st);
   if (op == kTrainFwdSwiGLU) return train_launch<kTrainFwdSwiGLU>(tm_a, tm_b, tm_a64, a, max_tiles, st);
+  if (op == kTrainPlainBf16) return train_launch<kTrainPlainBf16>(tm_a, tm_b, tm_a64, a, max_tiles, st);
   return train_launch<kTrainPlain>(tm_a, tm_b, tm_a64, a, max_tiles, st);
 }
 
@@ -15,6 +16,7 @@ cudaError_t train_gemm_fwd_set_attributes() {
   cudaError_t e = train_set_attributes<kTrainFwdGelu>();
   if (e == cudaSuccess) e = train_set_attributes<kTrainFwdSwiGLU>();
   if (e == cudaSuccess) e = train_set_attributes<kTrainPlain>();
+  if (e == cudaSuccess) e = train_set_attributes<kTrainPlainBf16>();
   return e;
 }
 

@@ -17,7 +17,8 @@ cudaError_t launch_train_gemm(int op, const CUtensorMap& tm_a, const CUtensorMap
   switch (op) {
     case kTrainFwdGelu:
     case kTrainFwdSwiGLU:
-    case kTrainPlain: return launch_train_gemm_fwd(op, tm_a, tm_b, tm_a64, a, max_tiles, st);
+    case kTrainPlain:
+    case kTrainPlainBf16: return launch_train_gemm_fwd(op, tm_a, tm_b, tm_a64, a, max_tiles, st);
     case kTrainBwdGelu:
     case kTrainBwdSwiGLU:
     case kTrainRows:

@@ -25,8 +25,8 @@ inline size_t padded_rows_cap(size_t rows, int E) {
 // What a kernel knows of the segments: from `offsets` on the device, or
 // (offsets null) `E` chunks of `chunk` rows of the `rows` there are, laid out
 // without padding (chunk % 16 == 0).  Offsets that run backwards or past
-// `rows` are cut so that no row is outside [0, rows) and no padded row
-// outside the padded buffers.
+// `rows` or overlap are cut so that no row is outside [0, rows) and no padded row
+// outside the padded buffers, and set MOE_DEV_BAD_ID in the call's status.
 struct SegArgs {
   const int32_t* offsets;  // [E+1] or null
   int E;
@@ -45,7 +45,8 @@ enum TrainOp {
   kTrainPlain = 5,      // out32 = A W[e]
   kTrainWgrad = 6,      // out[e] = A_e^T B_e over a segment's rows
   kTrainWgradF32 = 7,   // the same in fp32
-  kTrainRowsF32 = 8     // out32 = A W[e]^T
+  kTrainRowsF32 = 8,    // out32 = A W[e]^T
+  kTrainPlainBf16 = 9   // out = A W[e]
 };
 
 struct TrainGemmArgs {

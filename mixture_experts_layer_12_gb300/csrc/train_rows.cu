@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) seg_scan(a.seg, t, nullptr, lane, [](int) { return 0; });
+  if (threadIdx.x < 32) seg_scan(a.seg, t, nullptr, lane, nullptr, [](int) { return 0; });
   __syncthreads();
   const int E = a.seg.E;
   const int total = t.pad_off[E];

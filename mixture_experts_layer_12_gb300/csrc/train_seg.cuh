@@ -15,12 +15,14 @@ struct SegTable {
 };
 
 // One warp: the table, and tile_start[0 .. E] = exclusive sums of
-// tiles_of(rows).  E <= 256: lane l holds segments 8 l .. 8 l + 7.
+// tiles_of(rows).  E <= 256: lane l holds segments 8 l .. 8 l + 7.  Offsets that
+// had to be cut set MOE_DEV_BAD_ID in *status.
 template <typename F>
 __device__ __forceinline__ void seg_scan(const SegArgs& s, SegTable& t, int* tile_start, int lane,
-                                         F tiles_of) {
+                                         int* status, F tiles_of) {
   int n[8], o[8];
   int pad_sum = 0;
+  bool bad = false;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int e = lane * 8 + u;
@@ -29,8 +31,10 @@ __device__ __forceinline__ void seg_scan(const SegArgs& s, SegTable& t, int* til
     if (e < s.E) {
       int hi;
       if (s.offsets) {
-        o[u] = min(max(__ldg(s.offsets + e), 0), s.rows);
-        hi = min(__ldg(s.offsets + e + 1), s.rows);
+        const int o0 = __ldg(s.offsets + e), o1 = __ldg(s.offsets + e + 1);
+        o[u] = min(max(o0, 0), s.rows);
+        hi = min(o1, s.rows);
+        bad |= o0 < 0 || o1 < o0 || o1 > s.rows;
       } else {
         o[u] = (int)min((long long)e * s.chunk, (long long)s.rows);
         hi = (int)min((long long)o[u] + s.chunk, (long long)s.rows);
@@ -57,7 +61,10 @@ __device__ __forceinline__ void seg_scan(const SegArgs& s, SegTable& t, int* til
     tn[u] = 0;
     if (e < s.E) {
       const long long end = (long long)run + (n[u] + kSegPad - 1) / kSegPad * kSegPad;
-      if (end > s.rows_pad) n[u] = 0;  // overlapping segments: nothing past the buffers
+      if (end > s.rows_pad) {  // overlapping segments: nothing past the buffers
+        n[u] = 0;
+        bad = true;
+      }
       t.row_off[e] = o[u];
       t.rows[e] = n[u];
       t.pad_off[e] = min(run, s.rows_pad);
@@ -67,6 +74,7 @@ __device__ __forceinline__ void seg_scan(const SegArgs& s, SegTable& t, int* til
     }
     tsum += tn[u];
   }
+  if (bad) record_status(status, MOE_DEV_BAD_ID);
   if (!tile_start) return;
   int ti = tsum;
 #pragma unroll

@@ -431,7 +431,17 @@ class Saved:
     bits (else x itself), the routing (``routing``) and, for
     MOE_GATE_SOFTMAX_TOPK, the router's probabilities."""
 
-    __slots__ = ("call", "x", "z", "probs", "versions", "_block")
+    __slots__ = ("call", "x", "z", "probs", "versions", "_block", "_stream")
+
+    def _tensors(self):
+        """What the forward allocated."""
+        ts = [self._block]
+        for t in (self.z, self.x, self.probs):
+            if isinstance(t, A8Tensor):
+                ts += [t.codes, t.scales]
+            elif t is not None and t is not self.x:
+                ts.append(t)
+        return ts
 
     # ids, perm, slot, gate weights, counts and offsets in one block of 32-bit
     # words, each on a 16-byte boundary
@@ -460,13 +470,7 @@ class Saved:
 
     def nbytes(self) -> int:
         """Device bytes held (x itself not counted with keep_bits 16)."""
-        ts = [self._block]
-        for t in (self.z, self.x, self.probs):
-            if isinstance(t, A8Tensor):
-                ts += [t.codes, t.scales]
-            elif t is not None and t is not self.x:
-                ts.append(t)
-        return sum(t.numel() * t.element_size() for t in ts)
+        return sum(t.numel() * t.element_size() for t in self._tensors())
 
 
 class MoETrainLayer:
@@ -531,7 +535,7 @@ class MoETrainLayer:
         ws = c.workspace("moet_forward", d)
         y = torch.empty((T, self.H), dtype=_BF, device=d)
         v = Saved()
-        v.call, v.probs = c, None
+        v.call, v.probs, v._stream = c, None, raw
         v._block = torch.empty(v._layout(T, self.k, self.E)[-1], dtype=_I32, device=d)
         ids, perm, slot, weights, counts, offsets = v._addresses()
         if self.keep_bits == 8:
@@ -586,4 +590,8 @@ class MoETrainLayer:
                                   ws.numel(), raw)
         if rc:
             _check(rc)
+        if raw != saved._stream:  # their memory is the forward's stream's: not before this call has run
+            stream = torch.cuda.current_stream()
+            for t in saved._tensors():
+                t.record_stream(stream)
         return out

@@ -641,3 +641,118 @@ def test_steps_lower_a_loss_like_the_definition_does():
         for m, t, d in zip(master, (layer.w_router, layer.w1, layer.w2), gr):
             t.copy_((t.double() - 50.0 * d.to(DEV)).to(BF))
             m.copy_(f64(t))
+
+
+# -------------------------------------------------------- where it can go wrong --
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import mixture_experts_layer_12_gb300 as moe
+g = torch.Generator(device="cuda").manual_seed(7)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+x, dy = r(40, 64), r(40, 64)
+layer = moe.MoETrainLayer(r(64, 6), r(6, 64, 96), r(6, 48, 64), 2, gating=1, act="swiglu", keep_bits=8)
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    y, saved = layer(x)
+    out = layer.backward(saved, dy, bias_grad=True)
+gr.replay()
+torch.cuda.synchronize()
+y2, s2 = layer(x)
+want = layer.backward(s2, dy, bias_grad=True)
+assert torch.equal(y, y2)
+for a, b in zip(out, want):
+    assert torch.equal(a, b)
+q = moe.quantize_a8(x)
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        moe.router_probs(x, layer.w_router)
+except RuntimeError as e:
+    assert "train_status" in str(e), e
+else:
+    raise AssertionError("not refused")
+torch.cuda.synchronize()
+assert moe.train_status() == 0
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    p = moe.router_probs(x, layer.w_router)
+gr.replay()
+torch.cuda.synchronize()
+assert torch.equal(p, moe.router_probs(x, layer.w_router))
+print("ok")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Nothing of the library has run before the capture: kernels are loaded and
+    set up inside it.  A function without a layer needs its status block first."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]
+
+
+def test_backward_on_another_stream_than_the_forward():
+    """What a forward kept is not given out again while another stream's backward
+    reads it."""
+    x, dy, layer = make_layer(43, T=500, H=512, F=512, E=8, k=2, act="swiglu", bits=8)
+    y, saved = layer(x)
+    want = all_of(y, saved, layer.backward(saved, dy, bias_grad=True))
+    want = [t.clone() for t in want]
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        y, saved = layer(x)
+        z = [saved.z.codes.numel(), saved.z.scales.numel()]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+            g = layer.backward(saved, dy, bias_grad=True)
+        del saved  # its memory goes back to the first stream's pool
+        junk = [torch.full((n,), 77, dtype=torch.uint8, device=DEV) for n in z for _ in range(2)]
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(want[1:6], (g.dx, g.dw_router, g.dbias, g.dw1, g.dw2)):
+            assert bits_equal(a, b)
+        del junk
+
+
+def test_offsets_that_are_no_dispatch_are_an_error():
+    """Offsets that run backwards, overlap or pass the rows are cut on the device
+    and reported."""
+    rows, H, F, E = 64, 64, 96, 6
+    g = gen(44)
+    xp, dY = randn(g, rows, H).to(DEV), randn(g, rows, H).to(DEV)
+    w1, w2 = randn(g, E, H, F, std=0.1).to(DEV), randn(g, E, F, H, std=0.1).to(DEV)
+    z = randn(g, rows, F).to(DEV)
+    for o in ([0, 70, 80, 90, 100, 110, 120], [0, 64, 0, 64, 0, 64, 0], [-5, 3, 3, 2, 9, 1, 64], [5, 4, 3, 2, 1, 0, -1]):
+        o = torch.tensor(o, dtype=torch.int32, device=DEV)
+        for call in (lambda: moe.expert_ffn_backward(xp, z, w1, w2, o, dY),
+                     lambda: moe.expert_ffn(xp, w1, w2, o, keep_bits=8)):
+            out = call()
+            with pytest.raises(moe.MoEError):
+                moe.train_status()
+        dxp, dw1, dw2 = moe.expert_ffn_backward(xp, z, w1, w2, o, dY)
+        assert torch.isfinite(dw1.float()).all() and torch.isfinite(dw2.float()).all()
+        with pytest.raises(moe.MoEError):
+            moe.train_status()
+    assert moe.train_status() == 0
+
+
+def test_wide_rows_of_codes_past_two_to_the_31():
+    """Element offsets past 32 bits."""
+    rows, cols = 70000, 32768
+    x = torch.zeros(rows, cols, dtype=BF, device=DEV)
+    x[-1] = torch.arange(cols, device=DEV).to(BF)
+    x[66000, :64] = 3.0
+    q = moe.quantize_a8(x)
+    assert int(q.codes[66000, :64].float().sum()) == 64 * 96 and int(q.codes[65999].abs().max()) == 0
+    b = ref.a8_scales(x[-1:].cpu())
+    assert torch.equal(q.scales[-1:].cpu().long(), b)
+    assert torch.equal(q.codes[-1:].cpu().long(), ref.a8_codes(x[-1:].cpu(), b))
+    v = moe.dequantize_a8(q)
+    assert torch.equal(f64(v[-1:]), ref.a8_values(ref.a8_codes(x[-1:].cpu(), b), b))
+    assert float(v[66000, 0]) == 3.0 and float(v[:66000].abs().max()) == 0.0
