@@ -434,7 +434,9 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   const int n_pairs = gridDim.x >> 1;
   const int NB = (p.N + TT::BN_OUT - 1) / TT::BN_OUT;
   pdl_launch_dependents();
-  // barriers and TMEM before the earlier kernels have ended
+  // barriers before the earlier kernels have ended; TMEM after them, or a CTA of an
+  // earlier kernel on this SM that has yet to allocate its own would wait for
+  // this one, and this one for it
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&c.full[i], 2);
@@ -450,11 +452,11 @@ __global__ void __launch_bounds__(T_THREADS, 1)
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
   }
+  pdl_wait();  // offsets, operands and output buffers belong to earlier kernels
   if (warp == T_MMA_WARP) {
     tmem_alloc_pair(&c.tmem_base, T_TMEM_COLS);
     tmem_relinquish_pair();
   }
-  pdl_wait();  // offsets, operands and output buffers belong to earlier kernels
   if (warp == 0) {
     seg_scan(p.seg, c.seg, c.tile_start, lane, pair == 0 && rank == 0 ? p.status : nullptr, [&](int n) {
       const int m = TT::WGRAD ? p.M : n;

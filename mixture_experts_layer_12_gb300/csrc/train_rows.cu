@@ -46,23 +46,25 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 }
 
 // ------------------------------------------------- rows in padded order --
-// One warp per padded row: its segment by bisection of the padded offsets,
-// then a copy with eight 16-byte loads in flight per lane.
+// LPR lanes per padded row (a warp where a row has 256 columns or more): its
+// segment by bisection of the padded offsets, then a copy with eight 16-byte
+// loads in flight per lane.
 constexpr int GTHREADS = 256;
+template <int LPR>
 __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs a) {
   __shared__ SegTable t;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) seg_scan(a.seg, t, nullptr, lane, nullptr, [](int) { return 0; });
+  if (threadIdx.x < 32) seg_scan(a.seg, t, nullptr, threadIdx.x, nullptr, [](int) { return 0; });
   __syncthreads();
   const int E = a.seg.E;
   const int total = t.pad_off[E];
   const int vec = a.H / 8;
+  const int lane = threadIdx.x % LPR;
   const uint16_t* src0 = a.src[blockIdx.y];
   uint16_t* dst0 = a.dst[blockIdx.y];
-  const int nw = gridDim.x * (GTHREADS / 32);
-  for (int pr = blockIdx.x * (GTHREADS / 32) + (threadIdx.x >> 5); pr < total; pr += nw) {
+  constexpr int ROWS = GTHREADS / LPR;
+  for (int pr = blockIdx.x * ROWS + threadIdx.x / LPR; pr < total; pr += gridDim.x * ROWS) {
     int lo = 0, hi = E;  // the last segment that starts at or before pr
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -71,21 +73,21 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
     const int i = pr - t.pad_off[lo];
     uint4* dst = reinterpret_cast<uint4*>(dst0 + (size_t)pr * a.H);
     if (i >= t.rows[lo]) {
-      for (int c = lane; c < vec; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+      for (int c = lane; c < vec; c += LPR) dst[c] = make_uint4(0u, 0u, 0u, 0u);
       continue;
     }
     int r = t.row_off[lo] + i;
     if (a.perm) r = min(max(__ldg(a.perm + r) / a.k, 0), a.T - 1);
     const uint4* src = reinterpret_cast<const uint4*>(src0 + (size_t)r * a.H);
     int c = lane;
-    for (; c + 224 < vec; c += 256) {
+    for (; c + 7 * LPR < vec; c += 8 * LPR) {
       uint4 v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = __ldg(src + c + 32 * u);
+      for (int u = 0; u < 8; ++u) v[u] = __ldg(src + c + LPR * u);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) dst[c + 32 * u] = v[u];
+      for (int u = 0; u < 8; ++u) dst[c + LPR * u] = v[u];
     }
-    for (; c < vec; c += 32) dst[c] = __ldg(src + c);
+    for (; c < vec; c += LPR) dst[c] = __ldg(src + c);
   }
 }
 
@@ -355,8 +357,9 @@ __global__ void __launch_bounds__(QTHREADS) dequantize_a8_kernel(int64_t chunks,
 }
 
 // ------------------------------------------------------------ the gate's gradient --
-// A block takes 16 tokens (64: 26 us for 8192 tokens of 64 experts), a warp one
-// at a time; lane l holds experts
+// A block takes 16 tokens, a warp two (with 64 a block and one row of partial
+// sums at a time 26 us for 8192 tokens of 64 experts, k = 4, and 20 for 4096 of
+// 14336 columns; so 8 and 11); lane l holds experts
 // l, l + 32, ...  With the weights of a softmax over the chosen experts,
 // dlogit_j = w_j (dw_j - sum_i w_i dw_i) for the chosen and 0 for the others;
 // with those of a softmax over all experts, dlogit_e = p_e ([e chosen] dw_e -
@@ -386,11 +389,22 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_backward_kernel(const Ga
                        v[6] | (uint32_t)v[7] << 16);
       }
     } else {
-      for (int64_t i = i0; i < (int64_t)a.H * 2 * a.ep; i += nt) {
-        const int64_t h = i / (2 * a.ep);
-        int e = (int)(i - h * 2 * a.ep);
+      const int per = a.ep / 4;  // 16-byte pieces of a row of w2
+      for (int64_t i = i0; i < (int64_t)a.H * per; i += nt) {
+        const int64_t h = i / per;
+        int e = (int)(i - h * per) * 8;
         if (e >= a.ep) e -= a.ep;
-        a.w2[i] = e < a.E ? __ldg(a.w_router + h * a.E + e) : (uint16_t)0;
+        const uint16_t* src = a.w_router + h * a.E + e;
+        uint4 v;
+        if (a.E % 8 == 0) {
+          v = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+          uint32_t u[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) u[c] = e + c < a.E ? __ldg(src + c) : 0u;
+          v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+        }
+        *reinterpret_cast<uint4*>(a.w2 + i * 8) = v;
       }
     }
     return;
@@ -410,17 +424,28 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_backward_kernel(const Ga
       if (a.dw) dw = __ldg(a.dw + tk + lane);
     }
     if (!a.dw) {
+      // all k rows' partial sums at once: their latency is this kernel's time
       const int sl = lane < a.k ? __ldg(a.slot + tk + lane) : -1;
-      for (int j = 0; j < a.k; ++j) {
-        const int r = __shfl_sync(0xffffffffu, sl, j);
-        float s = 0.0f;
-        if (r >= 0 && r < a.rows) {
-          const float* src = a.part + (size_t)r * a.units;
-          for (int u = lane; u < a.units; u += 32) s += __ldg(src + u);
-        }
+      float s[kMaxTopK];
+      int r[kMaxTopK];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == j) dw = s;
+      for (int j = 0; j < kMaxTopK; ++j) {
+        r[j] = __shfl_sync(0xffffffffu, sl, j);
+        if (j >= a.k || r[j] >= a.rows) r[j] = -1;
+        s[j] = 0.0f;
+      }
+#pragma unroll 4
+      for (int u = lane; u < a.units; u += 32) {
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+          if (r[j] >= 0) s[j] += __ldg(a.part + (size_t)r[j] * a.units + u);
+      }
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j) {
+        if (j >= a.k) break;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], off);
+        if (lane == j) dw = s[j];
       }
     }
     float S = lane < a.k ? w * dw : 0.0f;
@@ -435,13 +460,14 @@ __global__ void __launch_bounds__(GATE_WARPS * 32) gate_backward_kernel(const Ga
       if (32 * u >= a.ep) break;
       float d = 0.0f;
       if (a.gating == MOE_GATE_SOFTMAX_TOPK) {
+        const float pe = e < a.E ? __ldg(a.probs + (size_t)t * a.E + e) : 0.0f;
         float up = -S;
         for (int j = 0; j < a.k; ++j) {
           const int ej = __shfl_sync(0xffffffffu, id, j);
           const float dj = __shfl_sync(0xffffffffu, dw, j);
           if (ej == e) up += dj;
         }
-        if (e < a.E) d = __ldg(a.probs + (size_t)t * a.E + e) * up;
+        d = e < a.E ? pe * up : 0.0f;
       } else {
         for (int j = 0; j < a.k; ++j) {
           const int ej = __shfl_sync(0xffffffffu, id, j);
@@ -501,7 +527,7 @@ __global__ void __launch_bounds__(SUM_THREADS) router_reduce_kernel(const Router
     float hi[8], lo[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) hi[u] = lo[u] = 0.0f;
-#pragma unroll 2
+#pragma unroll 8
     for (int s = 0; s < a.S; ++s) {
       const float4* p = reinterpret_cast<const float4*>(src + s * plane);
       const float4* q = reinterpret_cast<const float4*>(src + s * plane + a.ep);
@@ -564,9 +590,15 @@ __global__ void __launch_bounds__(256) router_softmax_kernel(const float* logits
 
 }  // namespace
 
+template <int LPR>
+static cudaError_t gather(const GatherArgs& a, int sms, cudaStream_t st) {
+  const int planes = a.src[1] ? 2 : 1;
+  const unsigned gx = blocks_for(a.seg.rows_pad, GTHREADS / LPR,
+                                 (int64_t)(sms > 0 ? sms : 1) * (2048 / GTHREADS) / planes);
+  return launch(train_gather_kernel<LPR>, dim3(gx, planes), GTHREADS, st, a);
+}
 cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st) {
-  const unsigned gx = blocks_for(a.seg.rows_pad, GTHREADS / 32, (int64_t)(sms > 0 ? sms : 1) * (2048 / GTHREADS));
-  return launch(train_gather_kernel, dim3(gx, a.src[1] ? 2 : 1), GTHREADS, st, a);
+  return a.H >= 256 ? gather<32>(a, sms, st) : gather<8>(a, sms, st);
 }
 
 template <bool F32>
@@ -614,7 +646,7 @@ cudaError_t launch_dequantize_a8(int64_t rows, int cols, const int8_t* codes, co
 }
 
 cudaError_t launch_gate_backward(const GateBackwardArgs& a, cudaStream_t st) {
-  const int64_t items = a.wt ? (int64_t)a.H / 8 * a.E : (int64_t)a.H * 2 * a.ep;
+  const int64_t items = a.wt ? (int64_t)a.H / 8 * a.E : (int64_t)a.H * a.ep / 4;
   const unsigned grid = (unsigned)((a.T + kGateTokens - 1) / kGateTokens) + blocks_for(items, GATE_WARPS * 32, 512);
   return launch(gate_backward_kernel, dim3(grid), GATE_WARPS * 32, st, a);
 }
