@@ -466,7 +466,8 @@ class Saved:
 
     @property
     def shape(self) -> moe_shape:
-        return self.call.shape
+        """For the moe_* functions (a copy)."""
+        return moe_shape.from_buffer_copy(self.call.shape)
 
     def nbytes(self) -> int:
         """Device bytes held (x itself not counted with keep_bits 16)."""

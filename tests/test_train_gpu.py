@@ -742,6 +742,52 @@ def test_offsets_that_are_no_dispatch_are_an_error():
     assert moe.train_status() == 0
 
 
+def test_eager_forward_and_captured_backward():
+    x, dy, layer = make_layer(45, T=100, H=128, F=96, E=8, k=2, bits=8, gating=1)
+    y, saved = layer(x)
+    want = layer.backward(saved, dy, bias_grad=True)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        g = layer.backward(saved, dy, bias_grad=True)
+    gr.replay()
+    gr.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, g):
+        assert bits_equal(a, b)
+    saved.shape.T = 3  # a copy: the next call of this size is not touched
+    y2, _ = layer(x)
+    assert bits_equal(y, y2)
+
+
+class Layer(torch.autograd.Function):
+    """What a program that uses torch's autograd puts around the calls."""
+
+    @staticmethod
+    def forward(ctx, x, w_router, w1, w2, layer):
+        y, ctx.saved = layer(x.detach())
+        ctx.layer = layer
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        g = ctx.layer.backward(ctx.saved, dy.contiguous())
+        return g.dx, g.dw_router, g.dw1, g.dw2, None
+
+
+def test_calls_inside_an_autograd_function():
+    x, dy, layer = make_layer(46, T=64, H=128, F=96, E=8, k=2, act="swiglu")
+    y, saved = layer(x)
+    want = layer.backward(saved, dy)
+    leaves = [t.clone().requires_grad_() for t in (x, layer.w_router, layer.w1, layer.w2)]
+    layer2 = moe.MoETrainLayer(*[t.detach() for t in leaves[1:]], 2, act="swiglu")
+    out = Layer.apply(*leaves, layer2)
+    assert bits_equal(out.detach(), y)
+    out.backward(dy)
+    for t, g in zip(leaves, (want.dx, want.dw_router, want.dw1, want.dw2)):
+        assert bits_equal(t.grad, g)
+
+
 def test_wide_rows_of_codes_past_two_to_the_31():
     """Element offsets past 32 bits."""
     rows, cols = 70000, 32768
