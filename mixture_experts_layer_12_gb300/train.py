@@ -136,11 +136,6 @@ def _out(t, shape, dtype, name: str, dev: int, device) -> torch.Tensor:
     return t
 
 
-def _need(cond: bool, message: str) -> None:
-    if not cond:
-        raise ValueError(message)
-
-
 def _shaped(t, shape, dtype, name: str, dev: int) -> int:
     """Address of `t`, which must have just this shape."""
     if not isinstance(t, torch.Tensor):
@@ -227,10 +222,11 @@ def _kept_ptrs(z, shape, name: str, dev: int):
 # ------------------------------------------------------- rows there and back --
 
 def _slot_shape(rows: torch.Tensor, slot: torch.Tensor, name: str) -> _Call:
-    _need(slot.dim() == 2, f"slot must be [T, k], got {tuple(slot.shape)}")
+    if slot.dim() != 2:
+        raise ValueError(f"slot must be [T, k], got {tuple(slot.shape)}")
     T, k = slot.shape
-    _need(rows.dim() == 2 and rows.shape[0] >= T * k, f"{name} must be [T * k, H] with T * k = {T * k}, got "
-          f"{tuple(rows.shape)}")
+    if rows.dim() != 2 or rows.shape[0] < T * k:
+        raise ValueError(f"{name} must be [T * k, H] with T * k = {T * k}, got {tuple(rows.shape)}")
     return _call(T, rows.shape[1], 8, max(k, 1), k)
 
 
@@ -275,12 +271,15 @@ def combine_backward(dy: torch.Tensor, Y: torch.Tensor, weights: torch.Tensor, s
 # ------------------------------------------------------------- experts' FFN --
 
 def _ffn_shape(xp, w1, w2, act: str) -> _Call:
-    _need(w2.dim() == 3, f"w2 must be [E, F, H], got {tuple(w2.shape)}")
+    if w2.dim() != 3:
+        raise ValueError(f"w2 must be [E, F, H], got {tuple(w2.shape)}")
     E, F, H = w2.shape
-    _need(xp.dim() == 2 and xp.shape[1] == H, f"xp must be [rows, {H}], got {tuple(xp.shape)}")
+    if xp.dim() != 2 or xp.shape[1] != H:
+        raise ValueError(f"xp must be [rows, {H}], got {tuple(xp.shape)}")
     c = _call(xp.shape[0], H, F, E, 1, None, MOE_GATE_TOPK_SOFTMAX, act)
     f1 = 2 * F if c.shape.expert_act else F
-    _need(tuple(w1.shape) == (E, H, f1), f"w1 must be {(E, H, f1)} for act = {act!r}, got {tuple(w1.shape)}")
+    if tuple(w1.shape) != (E, H, f1):
+        raise ValueError(f"w1 must be {(E, H, f1)} for act = {act!r}, got {tuple(w1.shape)}")
     return c
 
 
@@ -349,9 +348,11 @@ def expert_ffn_backward(xp: torch.Tensor, z, w1: torch.Tensor, w2: torch.Tensor,
 # ---------------------------------------------------------- router and gate --
 
 def _route_shape(x, w_router, k: int, gating: int) -> _Call:
-    _need(w_router.dim() == 2, f"w_router must be [H, E], got {tuple(w_router.shape)}")
+    if w_router.dim() != 2:
+        raise ValueError(f"w_router must be [H, E], got {tuple(w_router.shape)}")
     H, E = w_router.shape
-    _need(x.dim() == 2 and x.shape[1] == H, f"x must be [T, {H}], got {tuple(x.shape)}")
+    if x.dim() != 2 or x.shape[1] != H:
+        raise ValueError(f"x must be [T, {H}], got {tuple(x.shape)}")
     return _call(x.shape[0], H, 8, E, k, None, gating)
 
 
@@ -386,13 +387,15 @@ def route_backward(x: torch.Tensor, w_router: torch.Tensor, ids: torch.Tensor, w
     if stream is not None:
         with _on(stream):
             return route_backward(x, w_router, ids, weights, dweights, gating, probs)
-    _need(ids.dim() == 2, f"ids must be [T, k], got {tuple(ids.shape)}")
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be [T, k], got {tuple(ids.shape)}")
     c = _route_shape(x, w_router, ids.shape[1], gating)
     s, d = c.shape, x.device
     dev, raw = _here()
     tk = (s.T, s.k)
     if gating == MOE_GATE_SOFTMAX_TOPK:
-        _need(probs is not None, "MOE_GATE_SOFTMAX_TOPK needs probs")
+        if probs is None:
+            raise ValueError("MOE_GATE_SOFTMAX_TOPK needs probs")
         pp = _shaped(probs, (s.T, s.E), _F32, "probs", dev)
     else:
         pp = None
@@ -490,8 +493,10 @@ class MoETrainLayer:
 
     def __init__(self, w_router, w1, w2, k: int, bias=None, capacity_factor=None,
                  gating: int = MOE_GATE_TOPK_SOFTMAX, act: str = "gelu", keep_bits: int = 16):
-        _need(w2.dim() == 3, f"w2 must be [E, F, H], got {tuple(w2.shape)}")
-        _need(keep_bits in (8, 16), f"keep_bits = {keep_bits}: 8 or 16")
+        if w2.dim() != 3:
+            raise ValueError(f"w2 must be [E, F, H], got {tuple(w2.shape)}")
+        if keep_bits not in (8, 16):
+            raise ValueError(f"keep_bits = {keep_bits}: 8 or 16")
         self.E, self.F, self.H = w2.shape
         self.k, self.act, self.keep_bits = int(k), act, int(keep_bits)
         self.capacity_factor, self.gating = capacity_factor, int(gating)
@@ -500,7 +505,8 @@ class MoETrainLayer:
         dev = w_router.device.index
         for (t, dt, shape, name) in self._params(s):
             check_tensor(t, dt, name, 0, dev)
-            _need(tuple(t.shape) == shape, f"{name} must be {shape}, got {tuple(t.shape)}")
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
         if int(_lib().moet_forward_workspace_size(ctypes.byref(s))) == 0:
             _check(MOE_ERR_UNSUPPORTED)
         self.status = _status_block(dev)
@@ -518,15 +524,19 @@ class MoETrainLayer:
         return _call(T, self.H, self.F, self.E, self.k, self.capacity_factor, self.gating, self.act)
 
     def _weights(self, s, dev: int):
-        p = [_shaped(t, shape, dt, name, dev) for t, dt, shape, name in self._params(s)]
-        return p if self.bias is not None else p + [None]
+        """Addresses of w_router, w1, w2 and the bias (or None)."""
+        b = None if self.bias is None else _shaped(self.bias, (self.E,), _F32, "bias", dev)
+        return (_shaped(self.w_router, (self.H, self.E), _BF, "w_router", dev),
+                _shaped(self.w1, (self.E, self.H, 2 * self.F if s.expert_act else self.F), _BF, "w1", dev),
+                _shaped(self.w2, (self.E, self.F, self.H), _BF, "w2", dev), b)
 
     def __call__(self, x: torch.Tensor, stream=None):
         """(y, saved)"""
         if stream is not None:
             with _on(stream):
                 return self(x)
-        _need(x.dim() == 2 and x.shape[1] == self.H, f"x must be [T, {self.H}], got {tuple(x.shape)}")
+        if x.dim() != 2 or x.shape[1] != self.H:
+            raise ValueError(f"x must be [T, {self.H}], got {tuple(x.shape)}")
         dev, raw = _here()
         T, d = x.shape[0], x.device
         c = self._call(T)
@@ -570,9 +580,10 @@ class MoETrainLayer:
         if not isinstance(saved, Saved):
             raise TypeError("saved must be what a forward of this layer returned")
         c, s = saved.call, saved.call.shape
-        _need((s.H, s.F, s.E, s.k) == (self.H, self.F, self.E, self.k), "saved is of a layer of another shape")
-        _need(self._versions(saved) == saved.versions,
-              "x or a weight was changed or replaced after the forward that saved is of")
+        if (s.H, s.F, s.E, s.k) != (self.H, self.F, self.E, self.k):
+            raise ValueError("saved is of a layer of another shape")
+        if self._versions(saved) != saved.versions:
+            raise ValueError("x or a weight was changed or replaced after the forward that saved is of")
         dev, raw = _here()
         wr, w1, w2, _ = self._weights(s, dev)
         g = _shaped(dy, (s.T, s.H), _BF, "dy", dev)
