@@ -333,6 +333,20 @@ GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const uint1
   return g;
 }
 
+// K splits of the router's logits: as many as give every CTA pair a tile, at least
+// four stages each (one wave of 8 tiles with K = 4096 took 28 us).
+int probs_stages(const moe_shape* s) {
+  const int kb = (s->H + 63) / 64;
+  int64_t S = 76 / (blocks256(s->T) * blocks256(ep_of(s)));
+  if (S > kb / 4) S = kb / 4;
+  if (S < 1) S = 1;
+  return (int)((kb + S - 1) / S);
+}
+int probs_splits(const moe_shape* s) {
+  const int kb = (s->H + 63) / 64, n = s->T > 0 ? probs_stages(s) : kb;
+  return (kb + n - 1) / n;
+}
+
 struct ProbsWs {
   uint16_t* wpad;
   float* logits;
@@ -340,7 +354,7 @@ struct ProbsWs {
 ProbsWs probs_ws(const moe_shape* s, Carve& c) {
   ProbsWs p;
   p.wpad = c.take<uint16_t>(s->E % 8 ? (size_t)s->H * ep_of(s) : 0);
-  p.logits = c.take<float>((size_t)s->T * ep_of(s));
+  p.logits = c.take<float>(probs_splits(s) * (size_t)s->T * ep_of(s));
   return p;
 }
 int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* x, const uint16_t* w_router,
@@ -355,11 +369,17 @@ int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* 
   TRY(map_rows(&ta, x, s->H, s->T, 128, "x"));
   TRY(map_rows(&ta64, x, s->H, s->T, 64, "x"));
   TRY(map_weights(&tb, w_router, ep, s->H, 1, 64, "W_router"));
-  TrainGemmArgs a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, ep, s->H, status);
+  const int S = probs_splits(s);
+  SegArgs seg = chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad);
+  seg.E = S;
+  seg.chunk = 0;
+  seg.rows_pad *= S;
+  TrainGemmArgs a = gemm_args(seg, 0, ep, s->H, status);
   a.out32 = p.logits;
-  CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, blocks256(s->T) * blocks256(ep), st),
+  a.ksplit = probs_stages(s);
+  CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, S * blocks256(s->T) * blocks256(ep), st),
            "router logits launch");
-  CUDA_TRY(launch_router_softmax(p.logits, ep, b_router, s->T, s->E, probs, st), "router softmax launch");
+  CUDA_TRY(launch_router_softmax(p.logits, S, ep, b_router, s->T, s->E, probs, st), "router softmax launch");
   return MOE_OK;
 }
 

@@ -125,6 +125,7 @@ __device__ __forceinline__ TrainTile train_tile(const TrainCtrl& c, const TrainG
   } else {
     t.k16 = 0;
     t.kb = (p.K + TBK - 1) / TBK;
+    if (OP == kTrainPlain && p.ksplit) t.kb = min(p.ksplit, t.kb - t.e * p.ksplit);
   }
   t.half = m - t.base <= TPAIR_M / 2;
   t.nhalf = !TT::PAIRED && !t.half && p.N - t.nb * TBN <= TBN / 2;
@@ -513,12 +514,15 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (!t.nhalf) tma_load_2d_pair(b + T_BOX, &tm_b, full_cl, bcol2, krow);
           } else {
             // rows past the segment's end are computed but never stored
-            tma_load_2d_pair(a, t.half ? &tm_a64 : &tm_a, full_cl, kb * TBK, off + arow);
+            const bool split = OP == kTrainPlain && p.ksplit;
+            const int k0 = (kb + (split ? t.e * p.ksplit : 0)) * TBK;
+            const int we = split ? 0 : t.e;
+            tma_load_2d_pair(a, t.half ? &tm_a64 : &tm_a, full_cl, k0, off + arow);
             if constexpr (TT::B_MN) {
-              tma_load_3d_pair(b, &tm_b, full_cl, bcol, kb * TBK, t.e);
-              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol2, kb * TBK, t.e);
+              tma_load_3d_pair(b, &tm_b, full_cl, bcol, k0, we);
+              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol2, k0, we);
             } else {
-              tma_load_3d_pair(b, &tm_b, full_cl, kb * TBK, bcol, t.e);
+              tma_load_3d_pair(b, &tm_b, full_cl, k0, bcol, we);
             }
           }
           ++issued;
@@ -729,7 +733,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
       } else {
         // Fwd, Rows, Plain, Wgrad
-        const size_t orow0 = TT::WGRAD ? (size_t)t.e * p.M + w.row0 : (size_t)c.seg.row_off[t.e] + w.row0;
+        size_t orow0 = (size_t)c.seg.row_off[t.e] + w.row0;
+        if (OP == kTrainPlain && p.ksplit) orow0 += (size_t)t.e * p.seg.rows;
 #pragma unroll 1
         for (int ch = w.ch0; ch < w.ch1; ++ch) {
           const int gcol = w.col_base + ch * 32;

@@ -24,7 +24,7 @@ inline size_t padded_rows_cap(size_t rows, int E) {
 
 // What a kernel knows of the segments: from `offsets` on the device, or
 // (offsets null) `E` chunks of `chunk` rows of the `rows` there are, laid out
-// without padding (chunk % 16 == 0).  Offsets that run backwards or past
+// without padding (chunk % 16 == 0), or (chunk 0) all `rows` E times.  Offsets that run backwards or past
 // `rows` or overlap are cut so that no row is outside [0, rows) and no padded row
 // outside the padded buffers, and set MOE_DEV_BAD_ID in the call's status.
 struct SegArgs {
@@ -54,6 +54,8 @@ struct TrainGemmArgs {
   int M;        // Wgrad: rows of out (columns of A)
   int N;        // output columns (FwdSwiGLU, Bwd*: F)
   int K;        // reduction length (not Wgrad)
+  int ksplit;   // Plain of one matrix: segment e sums stages [e, e + 1) * ksplit of K
+                // for all rows into out32[e]; 0: not split
   uint16_t* out;
   float* out32;
   // kept pre-activations, compact rows: bf16 [rows, halves * N], or int8
@@ -169,8 +171,8 @@ struct RouterReduceArgs {
 };
 cudaError_t launch_router_reduce(const RouterReduceArgs& a, cudaStream_t st);
 
-// probs[t] = softmax(logits[t] + bias) over E of ldl columns
-cudaError_t launch_router_softmax(const float* logits, int ldl, const float* bias, int T, int E,
+// probs[t] = softmax(sum over S of logits[s, t] + bias) over E of ldl columns
+cudaError_t launch_router_softmax(const float* logits, int S, int ldl, const float* bias, int T, int E,
                                   float* probs, cudaStream_t st);
 
 }  // namespace moe

@@ -551,9 +551,9 @@ __global__ void __launch_bounds__(SUM_THREADS) router_reduce_kernel(const Router
 }
 
 // One warp per token; lane l holds experts l, l + 32, ...
-__global__ void __launch_bounds__(256) router_softmax_kernel(const float* logits, int ldl,
-                                                             const float* bias, int T, int E,
-                                                             float* probs) {
+__global__ void __launch_bounds__(256) router_softmax_kernel(const float* logits, int S,
+                                                             int ldl, const float* bias, int T,
+                                                             int E, float* probs) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(256) router_softmax_kernel(const float* logits
     v[u] = -INFINITY;
     if (e < E) {
       v[u] = __ldg(logits + (size_t)t * ldl + e);
+      for (int i = 1; i < S; ++i) v[u] += __ldg(logits + ((size_t)i * T + t) * ldl + e);
       if (bias) v[u] += __ldg(bias + e);
     }
     m = fmaxf(m, v[u]);
@@ -657,9 +658,10 @@ cudaError_t launch_router_reduce(const RouterReduceArgs& a, cudaStream_t st) {
   return launch(router_reduce_kernel, dim3(g), SUM_THREADS, st, a, db_blocks);
 }
 
-cudaError_t launch_router_softmax(const float* logits, int ldl, const float* bias, int T, int E, float* probs,
-                                  cudaStream_t st) {
-  return launch(router_softmax_kernel, dim3((unsigned)((T + 7) / 8)), 256, st, logits, ldl, bias, T, E, probs);
+cudaError_t launch_router_softmax(const float* logits, int S, int ldl, const float* bias, int T, int E,
+                                  float* probs, cudaStream_t st) {
+  return launch(router_softmax_kernel, dim3((unsigned)((T + 7) / 8)), 256, st, logits, S, ldl, bias, T, E,
+                probs);
 }
 
 }  // namespace moe
