@@ -58,8 +58,8 @@ extern "C" {
  * within 63, as 64 of them would be infinite.  A group that holds an infinity
  * or a NaN has b = 255, codes 0, and stands for 32 NaN.  code * scale is exact
  * in bf16, so products take kept values as they are; the error is at most half
- * a scale: 2^-7 of the group's largest magnitude (more only below 2^-120,
- * where b = 1, and within b = 249).
+ * a scale: 1/127 of the group's largest magnitude (more only below 2^-119,
+ * where b = 1, and up to a whole scale with b = 249).
  * cols % 8 == 0; rows * cols < 2^46.
  */
 MOE_API int moet_quantize_a8(int64_t rows, int32_t cols, const uint16_t* x, int8_t* codes,
