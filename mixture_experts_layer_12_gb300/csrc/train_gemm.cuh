@@ -246,32 +246,53 @@ __device__ __forceinline__ void train_unpack8(const uint4& u, float* f) {
   }
 }
 
-// A buffer to memory, after a warp barrier: rows 0 .. n_rows - 1 of 32 at dst +
-// row * pitch (bytes), the first `pieces` 16-byte pieces of each; rows from
-// n_full on as zeros.
-__device__ __forceinline__ void turn_out(const Turn& t, uint8_t* dst, size_t pitch, int n_rows, int pieces,
-                                         int n_full = 32) {
-  const int j = t.lane & 3;
+// Where a warp's 32 rows of an output are: this lane's piece of its first row,
+// and how many of the rows exist.  Addresses are made once per tile: as index
+// arithmetic of every access they were a third of the epilogue's instructions.
+struct RowsOut {
+  uint8_t* p;    // row lane / 4, piece lane % 4 of the first chunk
+  size_t step;   // 8 rows
+  int left;      // rows from lane / 4 on
+};
+template <int PIECE, typename T>
+__device__ __forceinline__ RowsOut rows_out(T* base, size_t row0, size_t cols, size_t col, int lane, int n_rows) {
+  RowsOut o;
+  o.p = reinterpret_cast<uint8_t*>(base + (row0 + (lane >> 2)) * cols + col) + (lane & 3) * PIECE;
+  o.step = 8 * cols * sizeof(T);
+  o.left = n_rows - (lane >> 2);
+  return o;
+}
+
+// A buffer to memory, after a warp barrier, `off` bytes from its first chunk: the
+// pieces that exist (`ok`) of the rows that do; rows from n_full on as zeros.
+__device__ __forceinline__ void turn_out(const Turn& t, const RowsOut& o, size_t off, bool ok, int n_full) {
+  uint8_t* p = o.p + off;
+  const int full_left = n_full - (t.lane >> 2);
+  if (__all_sync(0xffffffffu, min(o.left, full_left) > 24)) {  // 32 rows
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = i * 8 + (t.lane >> 2);
-    uint4 v = lds16(t.at(row, j));
-    if (row >= n_full) v = make_uint4(0u, 0u, 0u, 0u);
-    if (row < n_rows && j < pieces) *reinterpret_cast<uint4*>(dst + row * pitch + j * 16) = v;
+    for (int i = 0; i < 4; ++i) {
+      const uint4 v = lds16(t.at(i * 8 + (t.lane >> 2), t.lane & 3));
+      if (ok) *reinterpret_cast<uint4*>(p) = v;
+      p += o.step;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 v = lds16(t.at(i * 8 + (t.lane >> 2), t.lane & 3));
+      if (i * 8 >= full_left) v = make_uint4(0u, 0u, 0u, 0u);
+      if (ok && i * 8 < o.left) *reinterpret_cast<uint4*>(p) = v;
+      p += o.step;
+    }
   }
 }
-__device__ __forceinline__ void turn_out_bf16(const Turn& t, uint16_t* dst, size_t cols, int n_rows, int valid,
-                                              int n_full = 32) {
-  turn_out(t, reinterpret_cast<uint8_t*>(dst), cols * 2, n_rows, valid >> 3, n_full);
-}
 // Codes: 8-byte pieces, as rows start on 8 bytes only.
-__device__ __forceinline__ void turn_out_codes(const Turn& t, int8_t* dst, size_t cols, int n_rows, int valid) {
-  const int j = t.lane & 3;
+__device__ __forceinline__ void turn_out_codes(const Turn& t, const RowsOut& o, size_t off, bool ok) {
+  uint8_t* p = o.p + off;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = i * 8 + (t.lane >> 2);
-    const uint2 v = lds8(t.at(row, j));
-    if (row < n_rows && j * 8 < valid) *reinterpret_cast<uint2*>(dst + row * cols + j * 8) = v;
+    const uint2 v = lds8(t.at(i * 8 + (t.lane >> 2), t.lane & 3));
+    if (ok && i * 8 < o.left) *reinterpret_cast<uint2*>(p) = v;
+    p += o.step;
   }
 }
 // A buffer to memory by a TMA store (its pieces lie as the 64-byte swizzle lays
@@ -295,8 +316,8 @@ __device__ __forceinline__ void turn_tma_wait(int lane) {
 }
 
 // 32 fp32 values of every thread's row, 16 at a time.
-__device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v)[32], float* dst, size_t cols,
-                                               int n_rows, int valid) {
+__device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v)[32], const RowsOut& o,
+                                               size_t off, int valid) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -304,7 +325,7 @@ __device__ __forceinline__ void turn_store_f32(const Turn& t, const uint32_t (&v
       sts16(t.own(g), make_uint4(v[16 * h + 4 * g], v[16 * h + 4 * g + 1], v[16 * h + 4 * g + 2],
                                  v[16 * h + 4 * g + 3]));
     __syncwarp();
-    turn_out(t, reinterpret_cast<uint8_t*>(dst + 16 * h), cols * 4, n_rows, (valid >> 2) - 4 * h);
+    turn_out(t, o, off + 64 * h, 16 * h + (t.lane & 3) * 4 < valid, 32);
     __syncwarp();
   }
 }
@@ -342,62 +363,108 @@ __device__ __forceinline__ uint32_t train_keep(const TrainGemmArgs& p, const Tur
   }
   return b;
 }
-// ... and from there to half `hf` of rows row0 .., column col.
-__device__ __forceinline__ void train_kept_out(const TrainGemmArgs& p, const Turn& t, int halves, size_t row0,
-                                               int hf, int col, int n_rows, int valid, uint32_t b) {
-  const size_t pitch = (size_t)halves * p.N;
-  const size_t at = row0 * pitch + (size_t)hf * p.N + col;
+// Kept z of a warp's rows: in memory as rows of `halves` N columns, and a scale
+// byte per half and 32 columns.
+struct KeptOut {
+  RowsOut z;
+  uint8_t* scales;  // of this lane's row, first chunk, or null
+};
+__device__ __forceinline__ KeptOut kept_out(const TrainGemmArgs& p, int halves, size_t row0, int hf, int col,
+                                            int lane, int n_rows) {
+  KeptOut k;
+  const size_t pitch = (size_t)halves * p.N, at = (size_t)hf * p.N + col;
+  k.scales = nullptr;
   if (p.keep_bits == 16) {
-    turn_out_bf16(t, static_cast<uint16_t*>(p.z) + at, pitch, n_rows, valid);
+    k.z = rows_out<16>(static_cast<uint16_t*>(p.z), row0, pitch, at, lane, n_rows);
+  } else {
+    k.z = rows_out<8>(static_cast<int8_t*>(p.z), row0, pitch, at, lane, n_rows);
+    if (lane < n_rows)
+      k.scales = p.z_scales + ((row0 + lane) * halves + hf) * (size_t)((p.N + 31) / 32) + (col >> 5);
+  }
+  return k;
+}
+// ... from the buffer, chunk ch of the part, scale byte b.
+__device__ __forceinline__ void train_kept_out(const TrainGemmArgs& p, const Turn& t, const KeptOut& k, int ch,
+                                               bool ok, uint32_t b) {
+  if (p.keep_bits == 16) {
+    turn_out(t, k.z, (size_t)ch * 64, ok, 32);
     return;
   }
-  turn_out_codes(t, static_cast<int8_t*>(p.z) + at, pitch, n_rows, valid);
-  const int groups = (p.N + 31) / 32;
-  if (t.lane < n_rows)
-    p.z_scales[((row0 + t.lane) * halves + hf) * (size_t)groups + (col >> 5)] = (uint8_t)b;
+  turn_out_codes(t, k.z, (size_t)ch * 32, ok);
+  if (k.scales) k.scales[ch] = (uint8_t)b;
 }
 
 // 32 kept columns of a warp's rows on their way from memory: four pieces of
 // other threads' rows, 16 bytes of bf16 or 8 of codes with the group's scale.
+// Rows past the last one are read as the last one (nothing of them is stored, or
+// zeros are), columns past the last one are zeros.
+struct KeptIn {
+  const uint8_t* z;       // this lane's piece of the segment's row row0, first chunk
+  const uint8_t* scales;
+  uint32_t row[4];        // rows of this lane's four pieces, from row0
+};
 struct KeptChunk {
   uint4 w[4];
 };
-__device__ __forceinline__ void train_load_kept(const TrainGemmArgs& p, int lane, int halves, size_t row0, int hf,
-                                                int col, int n_rows, KeptChunk& k) {
-  const size_t pitch = (size_t)halves * p.N;
-  const int j = lane & 3;
-  const bool col_ok = col + j * 8 < p.N;
+__device__ __forceinline__ KeptIn kept_in(const TrainGemmArgs& p, int halves, size_t row0, int hf, int col,
+                                          int lane, int n_rows) {
+  KeptIn k;
+  const size_t at = row0 * halves * p.N + (size_t)hf * p.N + col + (lane & 3) * 8;
+  k.z = static_cast<const uint8_t*>(p.z) + at * (p.keep_bits / 8);
+  k.scales = p.z_scales + (row0 * halves + hf) * (size_t)((p.N + 31) / 32) + (col >> 5);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = i * 8 + (lane >> 2);
-    k.w[i] = make_uint4(0u, 0u, 127u, 0u);
-    if (row < n_rows && col_ok) {
-      const size_t o = (row0 + row) * pitch + (size_t)hf * p.N + col + j * 8;
-      if (p.keep_bits == 16) {
-        k.w[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.z) + o));
-      } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(p.z) + o));
-        k.w[i].x = u.x;
-        k.w[i].y = u.y;
-        k.w[i].z = __ldg(p.z_scales + ((row0 + row) * halves + hf) * (size_t)((p.N + 31) / 32) + (col >> 5));
-      }
-    } else if (p.keep_bits == 16) {
-      k.w[i].z = 0u;
+  for (int i = 0; i < 4; ++i) k.row[i] = (uint32_t)min(i * 8 + (lane >> 2), n_rows - 1);
+  return k;
+}
+__device__ __forceinline__ void train_load_kept(const TrainGemmArgs& p, const KeptIn& k, int halves, int ch,
+                                                bool ok, KeptChunk& c) {
+  if (p.keep_bits == 16) {
+    const uint32_t pitch = (uint32_t)(halves * 2) * (uint32_t)p.N;
+    const uint8_t* z = k.z + (size_t)ch * 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c.w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (ok) c.w[i] = __ldg(reinterpret_cast<const uint4*>(z + (uint64_t)k.row[i] * pitch));
+    }
+  } else {
+    const uint32_t pitch = (uint32_t)halves * (uint32_t)p.N;
+    const uint32_t groups = (uint32_t)halves * (uint32_t)((p.N + 31) / 32);
+    const uint8_t* z = k.z + (size_t)ch * 32;
+    const uint8_t* s = k.scales + ch;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint2 u = make_uint2(0u, 0u);
+      if (ok) u = __ldg(reinterpret_cast<const uint2*>(z + (uint64_t)k.row[i] * pitch));
+      c.w[i].x = u.x;
+      c.w[i].y = u.y;
+      c.w[i].z = __ldg(s + (uint64_t)k.row[i] * groups);
     }
   }
 }
-// ... and into buffer t as bf16 (which codes times scales are exactly).
+// 8 codes as bf16 times a power of two, exactly: a code c is (128 + its low seven
+// bits) - (128, or 256 if it is negative), both bf16 with a code's bits in the
+// mantissa.
+__device__ __forceinline__ uint4 a8_bf16x8(uint2 q, uint32_t b) {
+  const uint32_t sb = b == 255u ? 0x7fc0u : b == 0u ? 0x0040u : b << 7;
+  const uint32_t s2 = sb | sb << 16;
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = __byte_perm(i < 2 ? q.x : q.y, 0x43434343u, i & 1 ? 0x4342 : 0x4140);
+    const uint32_t lo = w & 0xff7fff7fu, hi = w & 0xff80ff80u;
+    const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&hi)), s);
+    r[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// ... and into buffer t as bf16.
 __device__ __forceinline__ void train_kept_in(const TrainGemmArgs& p, const Turn& t, const KeptChunk& k) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint4 v = k.w[i];
-    if (p.keep_bits == 8) {
-      float f[8];
-      const float s = a8_scale(v.z);
-      a8_values(v.x, s, f);
-      a8_values(v.y, s, f + 4);
-      v = train_pack8(f);
-    }
+    if (p.keep_bits == 8) v = a8_bf16x8(make_uint2(v.x, v.y), v.z);
     sts16(t.at(i * 8 + (t.lane >> 2), t.lane & 3), v);
   }
 }
@@ -624,17 +691,22 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       return a;
     };
     [[maybe_unused]] KeptChunk next[HALVES];
-    [[maybe_unused]] const auto load_kept = [&](const Part& a, int ch) {
+    [[maybe_unused]] KeptIn kin[HALVES];
+    // this warp's kept rows, and the first chunk of them on its way
+    [[maybe_unused]] const auto load_first = [&](const Part& a) {
+      if (a.n_rows == 0 || a.col_base + a.ch0 * 32 >= p.N) return;
 #pragma unroll
-      for (int hf = 0; hf < HALVES; ++hf)
-        train_load_kept(p, lane, HALVES, (size_t)c.seg.row_off[a.t.e] + a.row0, hf, a.col_base + ch * 32, a.n_rows,
-                        next[hf]);
+      for (int hf = 0; hf < HALVES; ++hf) {
+        kin[hf] = kept_in(p, HALVES, (size_t)c.seg.row_off[a.t.e] + a.row0, hf, a.col_base + a.ch0 * 32, lane,
+                          a.n_rows);
+        train_load_kept(p, kin[hf], HALVES, 0, a.col_base + a.ch0 * 32 + (lane & 3) * 8 < p.N, next[hf]);
+      }
     };
     [[maybe_unused]] int ring = 0;
     Part w = {};
     if (pair < n_tiles) {
       w = part_of(pair);
-      if constexpr (TT::BWD) load_kept(w, w.ch0);
+      if constexpr (TT::BWD) load_first(w);
     }
     for (int tile = pair; tile < n_tiles; tile += n_pairs) {
       const TrainTile t = w.t;
@@ -657,77 +729,81 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         tc_fence_after();
       }
       const uint32_t tbase = tmem + (uint32_t)(acc * TBN) + ((uint32_t)(q * 32) << 16);
+      const int gcol0 = w.col_base + w.ch0 * 32;
+      // chunks of 32 columns that exist, and whether this lane's piece of one does
+      const int n_ch = n_rows == 0 ? 0 : min(w.ch1 - w.ch0, (p.N - gcol0 + 31) / 32);
 
       if constexpr (TT::BWD) {
         const size_t crow0 = (size_t)c.seg.row_off[t.e] + w.row0;
-        // padded rows: zeros behind the segment's last one, up to 16
+        // padded rows: zeros behind the segment's last one, up to 16 (they share
+        // this warp with at least one row of the segment)
         const int n_pad = min(max((w.n_seg + 15) / 16 * 16 - w.row0, 0), 32);
         const size_t prow0 = (size_t)c.seg.pad_off[t.e] + w.row0;
         const Turn b_hw = turn.buffer(HALVES);
+        const RowsOut o_dz = rows_out<16>(p.dz, prow0, (size_t)HALVES * p.N, gcol0, lane, n_pad);
+        const RowsOut o_hw = rows_out<16>(p.hw, prow0, (size_t)p.N, gcol0, lane, n_pad);
+        float* part = p.part && lane < n_rows ? p.part + (crow0 + lane) * (size_t)p.units + (gcol0 >> 6) : nullptr;
         float dot = 0.0f;
 #pragma unroll 1
-        for (int ch = w.ch0; ch < w.ch1; ++ch) {
-          const int gcol = w.col_base + ch * 32;
-          if (gcol >= p.N) break;  // uniform: no columns from here on
-          const int valid = min(32, p.N - gcol);
+        for (int ch = 0; ch < n_ch; ++ch) {
+          const bool piece = gcol0 + ch * 32 + (lane & 3) * 8 < p.N;
 #pragma unroll
           for (int hf = 0; hf < HALVES; ++hf) train_kept_in(p, turn.buffer(hf), next[hf]);
-          if (ch + 1 < w.ch1) load_kept(w, ch + 1);
+          if (ch + 1 < n_ch) {
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+              train_load_kept(p, kin[hf], HALVES, ch + 1, gcol0 + (ch + 1) * 32 + (lane & 3) * 8 < p.N, next[hf]);
+          }
           __syncwarp();
-          if (n_pad > 0) {
-            uint32_t v[8], vn[8];
-            tmem_ld_x8(tbase + (uint32_t)(ch * 32), v);
-            tmem_ld_wait();
+          uint32_t v[8], vn[8];
+          const uint32_t tcol = tbase + (uint32_t)((w.ch0 + ch) * 32);
+          tmem_ld_x8(tcol, v);
+          tmem_ld_wait();
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (g < 3) tmem_ld_x8(tbase + (uint32_t)(ch * 32 + 8 * g + 8), vn);
-              float z[8], hv[8];
-              [[maybe_unused]] float u[8];
-              train_unpack8(lds16(turn.own(g)), z);
-              if constexpr (TT::GATED) train_unpack8(lds16(turn.buffer(1).own(g)), u);
-              // z becomes dz (of the gate), u becomes dz of the up projection
+          for (int g = 0; g < 4; ++g) {
+            if (g < 3) tmem_ld_x8(tcol + (uint32_t)(8 * g + 8), vn);
+            float z[8], hv[8];
+            [[maybe_unused]] float u[8];
+            train_unpack8(lds16(turn.own(g)), z);
+            if constexpr (TT::GATED) train_unpack8(lds16(turn.buffer(1).own(g)), u);
+            // z becomes dz (of the gate), u becomes dz of the up projection
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                // columns past the last one: g and z are 0
-                const float gr = __uint_as_float(v[i]);
-                const float wg = gw * gr;
-                float h;
-                if constexpr (TT::GATED) {
-                  // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
-                  const float s = train_sigmoid(z[i]);
-                  const float as = z[i] * s;
-                  h = as * u[i];
-                  z[i] = wg * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
-                  u[i] = wg * as;
-                } else {
-                  float d;
-                  train_gelu_grad(z[i], h, d);
-                  z[i] = wg * d;
-                }
-                dot = fmaf(gr, h, dot);
-                hv[i] = gw * h;
+            for (int i = 0; i < 8; ++i) {
+              // columns past the last one: g and z are 0
+              const float gr = __uint_as_float(v[i]);
+              const float wg = gw * gr;
+              float h;
+              if constexpr (TT::GATED) {
+                // h = a s(a) u; dh/da = u s (1 + a (1 - s)), dh/du = a s
+                const float s = train_sigmoid(z[i]);
+                const float as = z[i] * s;
+                h = as * u[i];
+                z[i] = wg * u[i] * s * fmaf(z[i], 1.0f - s, 1.0f);
+                u[i] = wg * as;
+              } else {
+                float d;
+                train_gelu_grad(z[i], h, d);
+                z[i] = wg * d;
               }
-              sts16(turn.own(g), train_pack8(z));
-              if constexpr (TT::GATED) sts16(turn.buffer(1).own(g), train_pack8(u));
-              sts16(b_hw.own(g), train_pack8(hv));
-              if (g < 3) {
-                tmem_ld_wait();
+              dot = fmaf(gr, h, dot);
+              hv[i] = gw * h;
+            }
+            sts16(turn.own(g), train_pack8(z));
+            if constexpr (TT::GATED) sts16(turn.buffer(1).own(g), train_pack8(u));
+            sts16(b_hw.own(g), train_pack8(hv));
+            if (g < 3) {
+              tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = vn[i];
-              }
+              for (int i = 0; i < 8; ++i) v[i] = vn[i];
             }
           }
           __syncwarp();
-          if (n_pad > 0) {
-            uint16_t* dz = p.dz + prow0 * (size_t)(HALVES * p.N) + gcol;
-#pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf)
-              turn_out_bf16(turn.buffer(hf), dz + hf * (size_t)p.N, (size_t)HALVES * p.N, n_pad, valid, n_rows);
-            turn_out_bf16(b_hw, p.hw + prow0 * (size_t)p.N + gcol, (size_t)p.N, n_pad, valid, n_rows);
-            if (p.part && ((ch & 1) || gcol + 32 >= p.N)) {
-              if (lane < n_rows) p.part[(crow0 + lane) * (size_t)p.units + (gcol >> 6)] = dot;
-              dot = 0.0f;
-            }
+          turn_out(turn, o_dz, (size_t)ch * 64, piece, n_rows);
+          if constexpr (TT::GATED) turn_out(turn.buffer(1), o_dz, (size_t)ch * 64 + (size_t)p.N * 2, piece, n_rows);
+          turn_out(b_hw, o_hw, (size_t)ch * 64, piece, n_rows);
+          if ((ch & 1) || ch + 1 == n_ch) {  // 64 columns, or the last
+            if (part) part[ch >> 1] = dot;
+            dot = 0.0f;
           }
           __syncwarp();
         }
@@ -735,23 +811,35 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         // Fwd, Rows, Plain, Wgrad
         size_t orow0 = (size_t)c.seg.row_off[t.e] + w.row0;
         if (OP == kTrainPlain && p.ksplit) orow0 += (size_t)t.e * p.seg.rows;
+        [[maybe_unused]] KeptOut kout[HALVES];
+        [[maybe_unused]] RowsOut o;
+        if constexpr (!TT::WGRAD) {
+          if constexpr (TT::OUT32)
+            o = rows_out<16>(p.out32, orow0, (size_t)p.N, gcol0, lane, n_rows);
+          else
+            o = rows_out<16>(p.out, orow0, (size_t)p.N, gcol0, lane, n_rows);
+        }
+        if constexpr (TT::FWD) {
+#pragma unroll
+          for (int hf = 0; hf < HALVES; ++hf) kout[hf] = kept_out(p, HALVES, orow0, hf, gcol0, lane, n_rows);
+        }
 #pragma unroll 1
-        for (int ch = w.ch0; ch < w.ch1; ++ch) {
-          const int gcol = w.col_base + ch * 32;
-          if (gcol >= p.N || n_rows == 0) break;
-          const int valid = min(32, p.N - gcol);
+        for (int ch = 0; ch < n_ch; ++ch) {
+          const int gcol = gcol0 + ch * 32;
           uint32_t v[32];
           [[maybe_unused]] uint32_t uv[32];
           if (t.kb > 0) {
-            tmem_ld_x32(tbase + (uint32_t)(ch * 32), v);
+            const uint32_t tcol = tbase + (uint32_t)((w.ch0 + ch) * 32);
+            tmem_ld_x32(tcol, v);
             // gate columns are the accumulator's first 128 (64 with M = 128), up
             // columns the others
-            if constexpr (TT::PAIRED) tmem_ld_x32(tbase + (uint32_t)((t.half ? 64 : 128) + ch * 32), uv);
+            if constexpr (TT::PAIRED) tmem_ld_x32(tcol + (uint32_t)(t.half ? 64 : 128), uv);
             tmem_ld_wait();
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
+          const int valid = min(32, p.N - gcol);
           if constexpr (TT::WGRAD) {
             // 64 bytes of every row at a time: 32 columns of bf16, 16 of fp32
             constexpr int OUTS = TT::OUT32 ? 2 : 1;
@@ -775,7 +863,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
               ring = ring == TT::BUFS - 1 ? 0 : ring + 1;
             }
           } else if constexpr (TT::OUT32) {
-            turn_store_f32(turn, v, p.out32 + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
+            turn_store_f32(turn, v, o, (size_t)ch * 128, valid);
           } else {
             [[maybe_unused]] uint32_t b0 = 0u, b1 = 0u;
             if constexpr (TT::FWD) b0 = train_keep(p, turn, valid, v);
@@ -794,9 +882,10 @@ __global__ void __launch_bounds__(T_THREADS, 1)
               sts16(out.own(g), train_pack8(f));
             }
             __syncwarp();
-            if constexpr (TT::FWD) train_kept_out(p, turn, HALVES, orow0, 0, gcol, n_rows, valid, b0);
-            if constexpr (TT::PAIRED) train_kept_out(p, turn.buffer(1), HALVES, orow0, 1, gcol, n_rows, valid, b1);
-            turn_out_bf16(out, p.out + orow0 * (size_t)p.N + gcol, (size_t)p.N, n_rows, valid);
+            const bool piece = (lane & 3) * 8 < valid;
+            if constexpr (TT::FWD) train_kept_out(p, turn, kout[0], ch, piece, b0);
+            if constexpr (TT::PAIRED) train_kept_out(p, turn.buffer(1), kout[HALVES - 1], ch, piece, b1);
+            turn_out(out, o, (size_t)ch * 64, piece, 32);
             __syncwarp();
           }
         }
@@ -805,7 +894,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
       // accumulator is handed back
       if (tile + n_pairs < n_tiles) {
         w = part_of(tile + n_pairs);
-        if constexpr (TT::BWD) load_kept(w, w.ch0);
+        if constexpr (TT::BWD) load_first(w);
       }
       if (t.kb > 0) {
         tc_fence_before();
