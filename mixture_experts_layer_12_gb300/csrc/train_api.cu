@@ -62,24 +62,28 @@ struct Carve {
   }
 };
 
-int bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint32_t* box,
+// Rows of a workspace matrix start on 128 bytes: TMA boxes of 128-byte rows then
+// read 4 sectors of one line, not 5 of two (8000 rows, 8 experts of 2872 x 9480:
+// a weight gradient 367 us against 306 with 2880 x 9472, which need none of this).
+size_t ld_of(size_t cols) { return (cols + 63) / 64 * 64; }
+
+// [rows, cols] bf16, rows `ld` columns apart
+int map_rows(CUtensorMap* m, const void* base, size_t cols, size_t ld, size_t rows, uint32_t box_rows,
              const char* what) {
-  uint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
-  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims,
-                       strides, box, what);
-}
-int map_rows(CUtensorMap* m, const void* base, size_t cols, size_t rows, uint32_t box_rows, const char* what) {
   const uint64_t dims[2] = {cols, rows};
+  const uint64_t strides[1] = {ld * 2};
   const uint32_t box[2] = {64, box_rows};
-  return bf16_map(m, base, 2, dims, box, what);
+  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 2, dims, strides, box,
+                       what);
 }
 int map_weights(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t n, uint32_t box_rows,
                 const char* what) {
   const uint64_t dims[3] = {cols, rows, n};
+  const uint64_t strides[2] = {cols * 2, cols * rows * 2};
   const uint32_t box[3] = {64, box_rows, 1};
-  return bf16_map(m, base, 3, dims, box, what);
+  return encode_map_as(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 3, dims, strides, box,
+                       what);
 }
-
 // Output [n, rows, cols] of a weight gradient.
 int map_out(CUtensorMap* m, const void* base, size_t cols, size_t rows, size_t n, bool f32) {
   const uint64_t size = f32 ? 4 : 2;
@@ -130,11 +134,12 @@ int fwd_product(const moe_shape* s, int bits, const uint16_t* xp, const uint16_t
                 uint16_t* h, void* z, uint8_t* z_scales, const int* merge, void* status, cudaStream_t st) {
   const size_t rows = rows_of(s);
   CUtensorMap ta, tb, ta64;
-  TRY(map_rows(&ta, xp, s->H, rows, 128, "xp"));
-  TRY(map_rows(&ta64, xp, s->H, rows, 64, "xp"));
+  TRY(map_rows(&ta, xp, s->H, s->H, rows, 128, "xp"));
+  TRY(map_rows(&ta64, xp, s->H, s->H, rows, 64, "xp"));
   TRY(map_weights(&tb, w1, (size_t)s->F * halves(s), s->H, s->E, 64, "W1"));
   TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->F, s->H, status);
   a.out = h;
+  a.ld_out = (int)ld_of(s->F);
   a.keep_bits = bits;
   a.z = z;
   a.z_scales = z_scales;
@@ -150,11 +155,12 @@ int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, con
                   float* Y32, void* status, cudaStream_t st) {
   const size_t rows = rows_of(s);
   CUtensorMap ta, tb, ta64;
-  TRY(map_rows(&ta, h, s->F, rows, 128, "h"));
-  TRY(map_rows(&ta64, h, s->F, rows, 64, "h"));
+  TRY(map_rows(&ta, h, s->F, ld_of(s->F), rows, 128, "h"));
+  TRY(map_rows(&ta64, h, s->F, ld_of(s->F), rows, 64, "h"));
   TRY(map_weights(&tb, w2, s->H, s->F, s->E, 64, "W2"));
   TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->H, s->F, status);
   a.out = Y;
+  a.ld_out = s->H;
   a.out32 = Y32;
   CUDA_TRY(launch_train_gemm(Y32 ? kTrainPlain : kTrainPlainBf16, ta, tb, ta64, a,
                              row_tiles(rows, s->E, s->H, 256), st),
@@ -182,8 +188,8 @@ int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream
   const SegArgs seg = segments(s, f.offsets);
   CUtensorMap ta, tb, ta64;
   // g = dy W2^T; dz, w h, <g, h>
-  TRY(map_rows(&ta, f.dyp, s->H, pad, 128, "dy rows"));
-  TRY(map_rows(&ta64, f.dyp, s->H, pad, 64, "dy rows"));
+  TRY(map_rows(&ta, f.dyp, s->H, ld_of(s->H), pad, 128, "dy rows"));
+  TRY(map_rows(&ta64, f.dyp, s->H, ld_of(s->H), pad, 64, "dy rows"));
   TRY(map_weights(&tb, f.w2, s->H, s->F, s->E, 128, "W2"));
   TrainGemmArgs a = gemm_args(seg, 0, s->F, s->H, status);
   a.keep_bits = f.bits;
@@ -194,31 +200,36 @@ int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream
   a.n_w = (int)rows;
   a.dz = f.dz;
   a.hw = f.hw;
+  a.ld_dz = (int)ld_of(f1);
+  a.ld_hw = (int)ld_of(s->F);
   a.part = f.part;
   a.units = (s->F + 63) / 64;
   CUDA_TRY(launch_train_gemm(gated(s) ? kTrainBwdSwiGLU : kTrainBwdGelu, ta, tb, ta64, a,
                              row_tiles(rows, s->E, s->F, 256), st),
            "h gradient launch");
   // dW2 = (w h)^T dy
-  TRY(map_rows(&ta, f.hw, s->F, pad, 64, "w h"));
-  TRY(map_rows(&tb, f.dyp, s->H, pad, 64, "dy rows"));
+  TRY(map_rows(&ta, f.hw, s->F, ld_of(s->F), pad, 64, "w h"));
+  TRY(map_rows(&tb, f.dyp, s->H, ld_of(s->H), pad, 64, "dy rows"));
   a = gemm_args(seg, s->F, s->H, 0, status);
+  a.out = f.dw2;
   TRY(map_out(&ta64, f.dw2, s->H, s->F, s->E, false));
   CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta64, a, s->E * blocks256(s->F) * blocks256(s->H), st),
            "dW2 launch");
   // dW1 = xp^T dz
-  TRY(map_rows(&ta, f.xp, s->H, pad, 64, "xp"));
-  TRY(map_rows(&tb, f.dz, f1, pad, 64, "dz"));
+  TRY(map_rows(&ta, f.xp, s->H, ld_of(s->H), pad, 64, "xp"));
+  TRY(map_rows(&tb, f.dz, f1, ld_of(f1), pad, 64, "dz"));
   a = gemm_args(seg, s->H, f1, 0, status);
+  a.out = f.dw1;
   TRY(map_out(&ta64, f.dw1, f1, s->H, s->E, false));
   CUDA_TRY(launch_train_gemm(kTrainWgrad, ta, tb, ta64, a, s->E * blocks256(s->H) * blocks256(f1), st),
            "dW1 launch");
   // dxp = dz W1^T
-  TRY(map_rows(&ta, f.dz, f1, pad, 128, "dz"));
-  TRY(map_rows(&ta64, f.dz, f1, pad, 64, "dz"));
+  TRY(map_rows(&ta, f.dz, f1, ld_of(f1), pad, 128, "dz"));
+  TRY(map_rows(&ta64, f.dz, f1, ld_of(f1), pad, 64, "dz"));
   TRY(map_weights(&tb, f.w1, f1, s->H, s->E, 128, "W1"));
   a = gemm_args(seg, 0, s->H, f1, status);
   a.out = f.dxp;
+  a.ld_out = s->H;
   a.out32 = f.dxp32;
   CUDA_TRY(launch_train_gemm(f.dxp32 ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a, row_tiles(rows, s->E, s->H, 256), st),
            "x gradient launch");
@@ -270,8 +281,8 @@ int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackward
   CUDA_TRY(launch_gate_backward(gate, st), "gate gradient launch");
   CUtensorMap ta, tb, ta64;
   // dW_router's partial sums = x^T dlogits over chunks of tokens
-  TRY(map_rows(&ta, x, s->H, s->T, 64, "x"));
-  TRY(map_rows(&tb, r.dl, 2 * ep, s->T, 64, "dlogits"));
+  TRY(map_rows(&ta, x, s->H, s->H, s->T, 64, "x"));
+  TRY(map_rows(&tb, r.dl, 2 * ep, 2 * ep, s->T, 64, "dlogits"));
   TrainGemmArgs a = gemm_args(chunks(s->T, router_chunk(s)), s->H, 2 * ep, 0, status);
   a.out32 = r.part;
   TRY(map_out(&ta64, r.part, 2 * ep, s->H, a.seg.E, true));
@@ -289,11 +300,12 @@ int route_gradients(const moe_shape* s, const RouteGradWs& r, const GateBackward
   ra.db = db;
   CUDA_TRY(launch_router_reduce(ra, st), "dW_router sums launch");
   if (router_product(s)) {
-    TRY(map_rows(&ta, r.dl, 2 * ep, s->T, 128, "dlogits"));
-    TRY(map_rows(&ta64, r.dl, 2 * ep, s->T, 64, "dlogits"));
+    TRY(map_rows(&ta, r.dl, 2 * ep, 2 * ep, s->T, 128, "dlogits"));
+    TRY(map_rows(&ta64, r.dl, 2 * ep, 2 * ep, s->T, 64, "dlogits"));
     TRY(map_weights(&tb, r.w, 2 * ep, s->H, 1, 128, "W_router"));
     a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, s->H, 2 * ep, status);
     a.out = sum.out;
+    a.ld_out = s->H;
     a.out32 = add;
     CUDA_TRY(launch_train_gemm(add ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a,
                                blocks256(s->T) * blocks256(s->H), st),
@@ -366,8 +378,8 @@ int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* 
     w_router = p.wpad;
   }
   CUtensorMap ta, tb, ta64;
-  TRY(map_rows(&ta, x, s->H, s->T, 128, "x"));
-  TRY(map_rows(&ta64, x, s->H, s->T, 64, "x"));
+  TRY(map_rows(&ta, x, s->H, s->H, s->T, 128, "x"));
+  TRY(map_rows(&ta64, x, s->H, s->H, s->T, 64, "x"));
   TRY(map_weights(&tb, w_router, ep, s->H, 1, 64, "W_router"));
   const int S = probs_splits(s);
   SegArgs seg = chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad);
@@ -390,7 +402,7 @@ struct FfnWs {
 };
 FfnWs ffn_ws(const moe_shape* s, Carve& c) {
   FfnWs w;
-  w.h = c.take<uint16_t>(rows_of(s) * s->F);
+  w.h = c.take<uint16_t>(rows_of(s) * ld_of(s->F));
   return w;
 }
 
@@ -400,10 +412,10 @@ struct FfnGradWs {
 FfnGradWs ffn_grad_ws(const moe_shape* s, Carve& c) {
   const size_t pad = pad_of(s);
   FfnGradWs w;
-  w.xp = c.take<uint16_t>(pad * s->H);
-  w.dyp = c.take<uint16_t>(pad * s->H);
-  w.hw = c.take<uint16_t>(pad * s->F);
-  w.dz = c.take<uint16_t>(pad * s->F * halves(s));
+  w.xp = c.take<uint16_t>(pad * ld_of(s->H));
+  w.dyp = c.take<uint16_t>(pad * ld_of(s->H));
+  w.hw = c.take<uint16_t>(pad * ld_of(s->F));
+  w.dz = c.take<uint16_t>(pad * ld_of((size_t)s->F * halves(s)));
   return w;
 }
 
@@ -609,7 +621,7 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
   if (s->T == 0) return zero_weights(s, dw1, dw2, st);
   Carve c(ws);
   const FfnGradWs w = ffn_grad_ws(s, c);
-  GatherArgs ga = {segments(s, offsets), nullptr, s->T, s->H, s->k, {xp, dY}, {w.xp, w.dyp}};
+  GatherArgs ga = {segments(s, offsets), nullptr, s->T, s->H, s->k, (int)ld_of(s->H), {xp, dY}, {w.xp, w.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.xp, w.dyp, w1, w2, offsets, z, z_scales, nullptr, nullptr, nullptr,
                w.hw, w.dz, dxp, dw1, dw2, nullptr};
@@ -802,7 +814,7 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
              "dequantize launch");
     xb = w.x;
   }
-  GatherArgs ga = {segments(s, offsets), perm, s->T, s->H, s->k, {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
+  GatherArgs ga = {segments(s, offsets), perm, s->T, s->H, s->k, (int)ld_of(s->H), {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.ffn.xp, w.ffn.dyp, w1, w2, offsets, z, z_scales, weights, perm, w.part,
                w.ffn.hw, w.ffn.dz, nullptr, dw1, dw2, w.dxp};

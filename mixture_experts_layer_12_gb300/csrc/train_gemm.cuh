@@ -740,8 +740,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         const int n_pad = min(max((w.n_seg + 15) / 16 * 16 - w.row0, 0), 32);
         const size_t prow0 = (size_t)c.seg.pad_off[t.e] + w.row0;
         const Turn b_hw = turn.buffer(HALVES);
-        const RowsOut o_dz = rows_out<16>(p.dz, prow0, (size_t)HALVES * p.N, gcol0, lane, n_pad);
-        const RowsOut o_hw = rows_out<16>(p.hw, prow0, (size_t)p.N, gcol0, lane, n_pad);
+        const RowsOut o_dz = rows_out<16>(p.dz, prow0, (size_t)p.ld_dz, gcol0, lane, n_pad);
+        const RowsOut o_hw = rows_out<16>(p.hw, prow0, (size_t)p.ld_hw, gcol0, lane, n_pad);
         float* part = p.part && lane < n_rows ? p.part + (crow0 + lane) * (size_t)p.units + (gcol0 >> 6) : nullptr;
         float dot = 0.0f;
 #pragma unroll 1
@@ -809,6 +809,20 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         }
       } else {
         // Fwd, Rows, Plain, Wgrad
+        const bool idle = OP == kTrainWgrad && t.kb == 0;
+        if (idle) {
+          // an expert without rows: its matrix is one block of memory, of which
+          // this tile clears a part in whole lines (36 experts of 2872 x 9480 by
+          // tiles, whose rows start inside a sector: 817 us, so 420)
+          const int64_t all = (int64_t)p.M * p.N / 8;
+          const int cnt = c.tile_start[t.e + 1] - c.tile_start[t.e], at = tile - c.tile_start[t.e];
+          const int64_t lo = all * at / cnt, hi = all * (at + 1) / cnt;
+          uint4* dst = reinterpret_cast<uint4*>(p.out) + (int64_t)t.e * all;
+          const int shift = (int)((reinterpret_cast<uintptr_t>(dst) >> 4) & 7);
+          for (int64_t i = ((lo + shift) & ~(int64_t)7) - shift + (rank * T_EPI_WARPS + warp - T_EPI_WARP0) * 32 + lane;
+               i < hi; i += 2 * T_EPI_WARPS * 32)
+            if (i >= lo) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
         size_t orow0 = (size_t)c.seg.row_off[t.e] + w.row0;
         if (OP == kTrainPlain && p.ksplit) orow0 += (size_t)t.e * p.seg.rows;
         [[maybe_unused]] KeptOut kout[HALVES];
@@ -817,28 +831,23 @@ __global__ void __launch_bounds__(T_THREADS, 1)
           if constexpr (TT::OUT32)
             o = rows_out<16>(p.out32, orow0, (size_t)p.N, gcol0, lane, n_rows);
           else
-            o = rows_out<16>(p.out, orow0, (size_t)p.N, gcol0, lane, n_rows);
+            o = rows_out<16>(p.out, orow0, (size_t)p.ld_out, gcol0, lane, n_rows);
         }
         if constexpr (TT::FWD) {
 #pragma unroll
           for (int hf = 0; hf < HALVES; ++hf) kout[hf] = kept_out(p, HALVES, orow0, hf, gcol0, lane, n_rows);
         }
 #pragma unroll 1
-        for (int ch = 0; ch < n_ch; ++ch) {
+        for (int ch = 0; ch < (idle ? 0 : n_ch); ++ch) {
           const int gcol = gcol0 + ch * 32;
           uint32_t v[32];
           [[maybe_unused]] uint32_t uv[32];
-          if (t.kb > 0) {
-            const uint32_t tcol = tbase + (uint32_t)((w.ch0 + ch) * 32);
-            tmem_ld_x32(tcol, v);
-            // gate columns are the accumulator's first 128 (64 with M = 128), up
-            // columns the others
-            if constexpr (TT::PAIRED) tmem_ld_x32(tcol + (uint32_t)(t.half ? 64 : 128), uv);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
-          }
+          const uint32_t tcol = tbase + (uint32_t)((w.ch0 + ch) * 32);
+          tmem_ld_x32(tcol, v);
+          // gate columns are the accumulator's first 128 (64 with M = 128), up
+          // columns the others
+          if constexpr (TT::PAIRED) tmem_ld_x32(tcol + (uint32_t)(t.half ? 64 : 128), uv);
+          tmem_ld_wait();
           const int valid = min(32, p.N - gcol);
           if constexpr (TT::WGRAD) {
             // 64 bytes of every row at a time: 32 columns of bf16, 16 of fp32

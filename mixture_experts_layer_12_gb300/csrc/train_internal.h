@@ -57,6 +57,7 @@ struct TrainGemmArgs {
   int ksplit;   // Plain of one matrix: segment e sums stages [e, e + 1) * ksplit of K
                 // for all rows into out32[e]; 0: not split
   uint16_t* out;
+  int ld_out;   // columns from one row of `out` to the next (not Wgrad)
   float* out32;
   // kept pre-activations, compact rows: bf16 [rows, halves * N], or int8
   // codes of that shape with scales [rows, halves * ceil(N / 32)]
@@ -64,13 +65,14 @@ struct TrainGemmArgs {
   void* z;
   uint8_t* z_scales;
   // Bwd: gate weight of compact row r is w[perm[r]] (w null: 1); dz [., halves
-  // * N] and hw [., N] padded rows; part [rows, units] the sums of g * h over
+  // * N] and hw [., N] padded rows, ld_dz and ld_hw columns apart; part [rows, units] the sums of g * h over
   // 64 columns (null: not wanted)
   const float* w;
   const int32_t* perm;
   int n_w;      // entries of w
   uint16_t* dz;
   uint16_t* hw;
+  int ld_dz, ld_hw;
   float* part;
   int units;
   const int* merge_status;  // a status word to take over, or null
@@ -94,6 +96,7 @@ struct GatherArgs {
   SegArgs seg;
   const int32_t* perm;
   int T, H, k;
+  int ld;  // columns from one row of dst to the next
   const uint16_t* src[2];
   uint16_t* dst[2];
 };

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
       if (t.pad_off[mid] <= pr) lo = mid; else hi = mid;
     }
     const int i = pr - t.pad_off[lo];
-    uint4* dst = reinterpret_cast<uint4*>(dst0 + (size_t)pr * a.H);
+    uint4* dst = reinterpret_cast<uint4*>(dst0 + (size_t)pr * a.ld);
     if (i >= t.rows[lo]) {
       for (int c = lane; c < vec; c += LPR) dst[c] = make_uint4(0u, 0u, 0u, 0u);
       continue;
