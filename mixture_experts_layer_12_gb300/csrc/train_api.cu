@@ -130,12 +130,12 @@ int64_t blocks256(int n) { return ((int64_t)n + 255) / 256; }
 
 // ------------------------------------------------------------------ products --
 
-int fwd_product(const moe_shape* s, int bits, const uint16_t* xp, const uint16_t* w1, const int32_t* offsets,
+int fwd_product(const moe_shape* s, int bits, const uint16_t* xp, size_t ld_xp, const uint16_t* w1, const int32_t* offsets,
                 uint16_t* h, void* z, uint8_t* z_scales, const int* merge, void* status, cudaStream_t st) {
   const size_t rows = rows_of(s);
   CUtensorMap ta, tb, ta64;
-  TRY(map_rows(&ta, xp, s->H, s->H, rows, 128, "xp"));
-  TRY(map_rows(&ta64, xp, s->H, s->H, rows, 64, "xp"));
+  TRY(map_rows(&ta, xp, s->H, ld_xp, rows, 128, "xp"));
+  TRY(map_rows(&ta64, xp, s->H, ld_xp, rows, 64, "xp"));
   TRY(map_weights(&tb, w1, (size_t)s->F * halves(s), s->H, s->E, 64, "W1"));
   TrainGemmArgs a = gemm_args(segments(s, offsets), 0, s->F, s->H, status);
   a.out = h;
@@ -431,7 +431,7 @@ ForwardWs forward_ws(const moe_shape* s, Carve& c) {
   ForwardWs w = {};
   w.route_bytes = moe_route_workspace_size(s);
   w.route = c.take<char>(w.route_bytes);
-  w.Y = c.take<float>(rows_of(s) * s->H);
+  w.Y = c.take<float>(rows_of(s) * ((size_t)s->H > ld_of(s->H) / 2 ? (size_t)s->H : ld_of(s->H) / 2));
   w.xp = reinterpret_cast<uint16_t*>(w.Y);  // read before Y is written
   w.ffn = ffn_ws(s, c);
   if (s->gating == MOE_GATE_SOFTMAX_TOPK) w.probs = probs_ws(s, c);
@@ -585,7 +585,7 @@ int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, c
   TRY(train_setup(&sms));
   Carve c(ws);
   const FfnWs w = ffn_ws(s, c);
-  TRY(fwd_product(s, keep_bits, xp, w1, offsets, w.h, z, z_scales, nullptr, status, stream_of(stream)));
+  TRY(fwd_product(s, keep_bits, xp, s->H, w1, offsets, w.h, z, z_scales, nullptr, status, stream_of(stream)));
   return plain_product(s, w.h, w2, offsets, Y, nullptr, status, stream_of(stream));
 }
 
@@ -621,7 +621,7 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
   if (s->T == 0) return zero_weights(s, dw1, dw2, st);
   Carve c(ws);
   const FfnGradWs w = ffn_grad_ws(s, c);
-  GatherArgs ga = {segments(s, offsets), nullptr, s->T, s->H, s->k, (int)ld_of(s->H), {xp, dY}, {w.xp, w.dyp}};
+  GatherArgs ga = {segments(s, offsets), false, nullptr, s->T, s->H, s->k, (int)ld_of(s->H), {xp, dY}, {w.xp, w.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.xp, w.dyp, w1, w2, offsets, z, z_scales, nullptr, nullptr, nullptr,
                w.hw, w.dz, dxp, dw1, dw2, nullptr};
@@ -740,10 +740,10 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
     TRY(router_probs(s, sms, w.probs, x, w_router, b_router, probs, status, st));
   if (keep_bits == 8)
     CUDA_TRY(launch_quantize_a8(s->T, s->H, x, xk, xk_scales, sms, st), "quantize launch");
-  PermuteArgs pa = {x, perm, offsets, s->T, s->H, s->k, s->E, w.xp, nullptr, nullptr};
-  CUDA_TRY(launch_permute(pa, sms, st, true), "permute launch");
+  GatherArgs ga = {segments(s, offsets), true, perm, s->T, s->H, s->k, (int)ld_of(s->H), {x, nullptr}, {w.xp, nullptr}};
+  CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   // the route's own status word is taken over by the next product
-  TRY(fwd_product(s, keep_bits, w.xp, w1, offsets, w.ffn.h, z, z_scales, static_cast<const int*>(w.route),
+  TRY(fwd_product(s, keep_bits, w.xp, ld_of(s->H), w1, offsets, w.ffn.h, z, z_scales, static_cast<const int*>(w.route),
                   status, st));
   // the experts' outputs stay in fp32: y is rounded once
   TRY(plain_product(s, w.ffn.h, w2, offsets, nullptr, w.Y, status, st));
@@ -814,7 +814,7 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
              "dequantize launch");
     xb = w.x;
   }
-  GatherArgs ga = {segments(s, offsets), perm, s->T, s->H, s->k, (int)ld_of(s->H), {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
+  GatherArgs ga = {segments(s, offsets), false, perm, s->T, s->H, s->k, (int)ld_of(s->H), {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.ffn.xp, w.ffn.dyp, w1, w2, offsets, z, z_scales, weights, perm, w.part,
                w.ffn.hw, w.ffn.dz, nullptr, dw1, dw2, w.dxp};

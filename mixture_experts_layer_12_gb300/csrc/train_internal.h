@@ -91,9 +91,11 @@ cudaError_t train_gemm_set_attributes();
 
 // ---- rows and elements (train_rows.cu).
 // dst[padded row] = src[perm ? perm[r] / k : r] for the rows r of every
-// segment, zeros behind each; two (src, dst) pairs at once (src1 may be null).
+// segment, zeros behind each (compact: dst[r], nothing behind); two (src, dst)
+// pairs at once (src1 may be null).
 struct GatherArgs {
   SegArgs seg;
+  bool compact;
   const int32_t* perm;
   int T, H, k;
   int ld;  // columns from one row of dst to the next

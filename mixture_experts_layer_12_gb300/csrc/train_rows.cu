@@ -55,28 +55,33 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
   __shared__ SegTable t;
   pdl_launch_dependents();
   pdl_wait();
-  if (threadIdx.x < 32) seg_scan(a.seg, t, nullptr, threadIdx.x, nullptr, [](int) { return 0; });
-  __syncthreads();
   const int E = a.seg.E;
-  const int total = t.pad_off[E];
+  if (!a.compact) {
+    if (threadIdx.x < 32) seg_scan(a.seg, t, nullptr, threadIdx.x, nullptr, [](int) { return 0; });
+    __syncthreads();
+  }
+  const int total = a.compact ? min(max(__ldg(a.seg.offsets + E), 0), a.seg.rows) : t.pad_off[E];
   const int vec = a.H / 8;
   const int lane = threadIdx.x % LPR;
   const uint16_t* src0 = a.src[blockIdx.y];
   uint16_t* dst0 = a.dst[blockIdx.y];
   constexpr int ROWS = GTHREADS / LPR;
   for (int pr = blockIdx.x * ROWS + threadIdx.x / LPR; pr < total; pr += gridDim.x * ROWS) {
-    int lo = 0, hi = E;  // the last segment that starts at or before pr
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (t.pad_off[mid] <= pr) lo = mid; else hi = mid;
-    }
-    const int i = pr - t.pad_off[lo];
     uint4* dst = reinterpret_cast<uint4*>(dst0 + (size_t)pr * a.ld);
-    if (i >= t.rows[lo]) {
-      for (int c = lane; c < vec; c += LPR) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-      continue;
+    int r = pr;
+    if (!a.compact) {
+      int lo = 0, hi = E;  // the last segment that starts at or before pr
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.pad_off[mid] <= pr) lo = mid; else hi = mid;
+      }
+      const int i = pr - t.pad_off[lo];
+      if (i >= t.rows[lo]) {
+        for (int c = lane; c < vec; c += LPR) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      r = t.row_off[lo] + i;
     }
-    int r = t.row_off[lo] + i;
     if (a.perm) r = min(max(__ldg(a.perm + r) / a.k, 0), a.T - 1);
     const uint4* src = reinterpret_cast<const uint4*>(src0 + (size_t)r * a.H);
     int c = lane;
