@@ -488,8 +488,9 @@ class MoETrainLayer:
     x (with keep_bits 16) and the weights are what they were.  Both calls run on
     the current stream (or `stream`), allocate what they return and their
     workspace, and may be captured into CUDA graphs; several forwards may be in
-    flight before their backwards.  ``moe_get_device_status(layer.status)`` reads
-    the device status of all calls so far."""
+    flight before their backwards.  The layer itself is made outside a capture (it
+    waits for its status block).  ``moe_get_device_status(layer.status)`` reads the
+    device status of all calls so far."""
 
     def __init__(self, w_router, w1, w2, k: int, bias=None, capacity_factor=None,
                  gating: int = MOE_GATE_TOPK_SOFTMAX, act: str = "gelu", keep_bits: int = 16):
