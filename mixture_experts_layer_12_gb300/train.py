@@ -498,6 +498,8 @@ class MoETrainLayer:
             raise ValueError(f"w2 must be [E, F, H], got {tuple(w2.shape)}")
         if keep_bits not in (8, 16):
             raise ValueError(f"keep_bits = {keep_bits}: 8 or 16")
+        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a layer is made outside a capture: it waits for its status block")
         self.E, self.F, self.H = w2.shape
         self.k, self.act, self.keep_bits = int(k), act, int(keep_bits)
         self.capacity_factor, self.gating = capacity_factor, int(gating)

@@ -423,6 +423,7 @@ LAYERS = [
     dict(T=130, H=72, F=72, E=256, k=8),
     dict(T=40, H=64, F=64, E=4, k=2, cf=1e-12, gating=1),  # everything dropped
     dict(T=700, H=512, F=320, E=4, k=2, act="swiglu"),
+    dict(T=16500, H=64, F=72, E=8, k=2, act="swiglu", gating=1),  # past the one-launch route
 ]
 
 
@@ -666,6 +667,13 @@ assert torch.equal(y, y2)
 for a, b in zip(out, want):
     assert torch.equal(a, b)
 q = moe.quantize_a8(x)
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        moe.MoETrainLayer(layer.w_router, layer.w1, layer.w2, 2, act="swiglu")
+except RuntimeError as e:
+    assert "outside a capture" in str(e), e
+else:
+    raise AssertionError("not refused")
 try:
     with torch.cuda.graph(torch.cuda.CUDAGraph()):
         moe.router_probs(x, layer.w_router)
