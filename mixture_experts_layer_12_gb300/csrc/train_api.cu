@@ -119,6 +119,8 @@ TrainGemmArgs gemm_args(const SegArgs& seg, int M, int N, int K, void* status) {
   a.M = M;
   a.N = N;
   a.K = K;
+  a.splits = 1;
+  a.ksplit = (K + 63) / 64;
   a.status = static_cast<int*>(status);
   a.wait_limit_ns = kWaitLimitNs;
   return a;
@@ -127,6 +129,30 @@ int64_t row_tiles(size_t rows, int E, int cols, int per) {
   return (int64_t)((rows + 255) / 256 + (rows < (size_t)E ? rows : (size_t)E)) * ((cols + per - 1) / per);
 }
 int64_t blocks256(int n) { return ((int64_t)n + 255) / 256; }
+
+// Parts of K for a product whose fp32 outputs are summed afterwards anyway: few
+// rows leave most CTA pairs without a tile, and a long K then takes its time on a
+// few of them (3 rows of 3 experts of 576 x 14096: 73 us).  At least eight stages a
+// part, at most eight parts, and together no more tiles than there are pairs.
+struct Split {
+  int parts, stages;
+};
+Split split_of(int64_t blocks, int cols, int K, int most, int least) {
+  const int kb = (K + 63) / 64;
+  const int64_t tiles = blocks * ((cols + 255) / 256);
+  int64_t S = tiles > 0 ? 76 / tiles : 1;
+  if (S > most) S = most;
+  if (S > kb / least) S = kb / least;
+  if (S < 1) S = 1;
+  Split p;
+  p.stages = (int)((kb + S - 1) / S);
+  p.parts = (kb + p.stages - 1) / p.stages;
+  return p;
+}
+Split row_split(size_t rows, int E, int cols, int K) {
+  const int64_t n = (int64_t)rows, hit = n < E ? n : E;
+  return split_of(hit > 0 ? hit * (((n + hit - 1) / hit + 255) / 256) : 0, cols, K, 8, 8);
+}
 
 // ------------------------------------------------------------------ products --
 
@@ -162,14 +188,17 @@ int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, con
   a.out = Y;
   a.ld_out = s->H;
   a.out32 = Y32;
+  const Split sp = row_split(rows, s->E, s->H, s->F);
+  a.splits = sp.parts;
+  a.ksplit = sp.stages;
   CUDA_TRY(launch_train_gemm(Y32 ? kTrainPlain : kTrainPlainBf16, ta, tb, ta64, a,
-                             row_tiles(rows, s->E, s->H, 256), st),
+                             row_tiles(rows, s->E, s->H, 256) * (Y32 ? sp.parts : 1), st),
            "expert GEMM2 launch");
   return MOE_OK;
 }
 
-// The experts' gradients from padded xp and dyp; dxp compact, in bf16 or (dxp32)
-// in fp32.
+// The experts' gradients from padded xp and dyp; dxp compact, in bf16 or (dxp
+// null) as the parts of row_split in dxp32.
 struct FfnGrad {
   int bits;
   const uint16_t *xp, *dyp, *w1, *w2;
@@ -231,8 +260,26 @@ int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream
   a.out = f.dxp;
   a.ld_out = s->H;
   a.out32 = f.dxp32;
-  CUDA_TRY(launch_train_gemm(f.dxp32 ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a, row_tiles(rows, s->E, s->H, 256), st),
+  const Split sp = row_split(rows, s->E, s->H, f1);
+  a.splits = sp.parts;
+  a.ksplit = sp.stages;
+  // (rounded at once where K is not split and nobody sums the rows)
+  const bool f32 = sp.parts > 1 || !f.dxp;
+  CUDA_TRY(launch_train_gemm(f32 ? kTrainRowsF32 : kTrainRows, ta, tb, ta64, a,
+                             row_tiles(rows, s->E, s->H, 256) * (f32 ? sp.parts : 1), st),
            "x gradient launch");
+  if (f32 && f.dxp) {
+    RowsSumArgs sum = {};
+    sum.rows32 = f.dxp32;
+    sum.splits = sp.parts;
+    sum.range = f.offsets;
+    sum.E = s->E;
+    sum.T = (int)rows;
+    sum.H = s->H;
+    sum.k = 1;
+    sum.out = f.dxp;
+    CUDA_TRY(launch_rows_sum(sum, st), "x gradient sums launch");
+  }
   return MOE_OK;
 }
 
@@ -345,18 +392,9 @@ GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const uint1
   return g;
 }
 
-// K splits of the router's logits: as many as give every CTA pair a tile, at least
-// four stages each (one wave of 8 tiles with K = 4096 took 28 us).
-int probs_stages(const moe_shape* s) {
-  const int kb = (s->H + 63) / 64;
-  int64_t S = 76 / (blocks256(s->T) * blocks256(ep_of(s)));
-  if (S > kb / 4) S = kb / 4;
-  if (S < 1) S = 1;
-  return (int)((kb + S - 1) / S);
-}
-int probs_splits(const moe_shape* s) {
-  const int kb = (s->H + 63) / 64, n = s->T > 0 ? probs_stages(s) : kb;
-  return (kb + n - 1) / n;
+// (one wave of 8 tiles with K = 4096 took 28 us, 11 in parts)
+Split probs_split(const moe_shape* s) {
+  return split_of(blocks256(s->T), ep_of(s), s->H, 64, 4);
 }
 
 struct ProbsWs {
@@ -366,7 +404,7 @@ struct ProbsWs {
 ProbsWs probs_ws(const moe_shape* s, Carve& c) {
   ProbsWs p;
   p.wpad = c.take<uint16_t>(s->E % 8 ? (size_t)s->H * ep_of(s) : 0);
-  p.logits = c.take<float>(probs_splits(s) * (size_t)s->T * ep_of(s));
+  p.logits = c.take<float>(probs_split(s).parts * (size_t)s->T * ep_of(s));
   return p;
 }
 int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* x, const uint16_t* w_router,
@@ -381,17 +419,14 @@ int router_probs(const moe_shape* s, int sms, const ProbsWs& p, const uint16_t* 
   TRY(map_rows(&ta, x, s->H, s->H, s->T, 128, "x"));
   TRY(map_rows(&ta64, x, s->H, s->H, s->T, 64, "x"));
   TRY(map_weights(&tb, w_router, ep, s->H, 1, 64, "W_router"));
-  const int S = probs_splits(s);
-  SegArgs seg = chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad);
-  seg.E = S;
-  seg.chunk = 0;
-  seg.rows_pad *= S;
-  TrainGemmArgs a = gemm_args(seg, 0, ep, s->H, status);
+  const Split sp = probs_split(s);
+  TrainGemmArgs a = gemm_args(chunks(s->T, (s->T + kSegPad - 1) / kSegPad * kSegPad), 0, ep, s->H, status);
   a.out32 = p.logits;
-  a.ksplit = probs_stages(s);
-  CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, S * blocks256(s->T) * blocks256(ep), st),
+  a.splits = sp.parts;
+  a.ksplit = sp.stages;
+  CUDA_TRY(launch_train_gemm(kTrainPlain, ta, tb, ta64, a, sp.parts * blocks256(s->T) * blocks256(ep), st),
            "router logits launch");
-  CUDA_TRY(launch_router_softmax(p.logits, S, ep, b_router, s->T, s->E, probs, st), "router softmax launch");
+  CUDA_TRY(launch_router_softmax(p.logits, sp.parts, ep, b_router, s->T, s->E, probs, st), "router softmax launch");
   return MOE_OK;
 }
 
@@ -408,14 +443,18 @@ FfnWs ffn_ws(const moe_shape* s, Carve& c) {
 
 struct FfnGradWs {
   uint16_t *xp, *dyp, *hw, *dz;
+  float* dxp;  // parts of row_split
 };
-FfnGradWs ffn_grad_ws(const moe_shape* s, Carve& c) {
+// layer: dxp is summed by token, in fp32 in any case
+FfnGradWs ffn_grad_ws(const moe_shape* s, bool layer, Carve& c) {
   const size_t pad = pad_of(s);
   FfnGradWs w;
   w.xp = c.take<uint16_t>(pad * ld_of(s->H));
   w.dyp = c.take<uint16_t>(pad * ld_of(s->H));
   w.hw = c.take<uint16_t>(pad * ld_of(s->F));
   w.dz = c.take<uint16_t>(pad * ld_of((size_t)s->F * halves(s)));
+  const int parts = row_split(rows_of(s), s->E, s->H, s->F * halves(s)).parts;
+  w.dxp = c.take<float>(parts > 1 || layer ? parts * rows_of(s) * s->H : 0);
   return w;
 }
 
@@ -431,7 +470,9 @@ ForwardWs forward_ws(const moe_shape* s, Carve& c) {
   ForwardWs w = {};
   w.route_bytes = moe_route_workspace_size(s);
   w.route = c.take<char>(w.route_bytes);
-  w.Y = c.take<float>(rows_of(s) * ((size_t)s->H > ld_of(s->H) / 2 ? (size_t)s->H : ld_of(s->H) / 2));
+  // xp and, once it has been read, the experts' outputs in row_split's parts
+  const size_t y = row_split(rows_of(s), s->E, s->H, s->F).parts * (size_t)s->H, x = (ld_of(s->H) + 1) / 2;
+  w.Y = c.take<float>(rows_of(s) * (y > x ? y : x));
   w.xp = reinterpret_cast<uint16_t*>(w.Y);  // read before Y is written
   w.ffn = ffn_ws(s, c);
   if (s->gating == MOE_GATE_SOFTMAX_TOPK) w.probs = probs_ws(s, c);
@@ -443,16 +484,14 @@ struct BackwardWs {
   uint16_t* x;  // bf16 of x kept in 8 bits
   float* part;
   RouteGradWs route;
-  float* dxp;
   float* dxr;  // the router's part of dx
 };
 BackwardWs backward_ws(const moe_shape* s, int bits, Carve& c) {
   BackwardWs w;
-  w.ffn = ffn_grad_ws(s, c);
+  w.ffn = ffn_grad_ws(s, true, c);
   w.x = c.take<uint16_t>(bits == 8 ? (size_t)s->T * s->H : 0);
   w.part = c.take<float>(rows_of(s) * ((s->F + 63) / 64));
   w.route = route_grad_ws(s, c);
-  w.dxp = c.take<float>(rows_of(s) * s->H);
   w.dxr = c.take<float>(router_product(s) ? (size_t)s->T * s->H : 0);
   return w;
 }
@@ -592,7 +631,7 @@ int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, c
 size_t moet_expert_ffn_backward_workspace_size(const moe_shape* s) {
   if (check_shape(s, true) != MOE_OK) return 0;
   Carve c(nullptr);
-  ffn_grad_ws(s, c);
+  ffn_grad_ws(s, false, c);
   return c.used + 1024;
 }
 
@@ -620,11 +659,11 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
   TRY(train_setup(&sms));
   if (s->T == 0) return zero_weights(s, dw1, dw2, st);
   Carve c(ws);
-  const FfnGradWs w = ffn_grad_ws(s, c);
+  const FfnGradWs w = ffn_grad_ws(s, false, c);
   GatherArgs ga = {segments(s, offsets), false, nullptr, s->T, s->H, s->k, (int)ld_of(s->H), {xp, dY}, {w.xp, w.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.xp, w.dyp, w1, w2, offsets, z, z_scales, nullptr, nullptr, nullptr,
-               w.hw, w.dz, dxp, dw1, dw2, nullptr};
+               w.hw, w.dz, dxp, dw1, dw2, w.dxp};
   return ffn_gradients(s, f, status, st);
 }
 
@@ -749,6 +788,7 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
   TRY(plain_product(s, w.ffn.h, w2, offsets, nullptr, w.Y, status, st));
   RowsSumArgs ca = {};
   ca.rows32 = w.Y;
+  ca.splits = row_split(rows_of(s), s->E, s->H, s->F).parts;
   ca.w = weights;
   ca.slot = slot;
   ca.T = s->T;
@@ -817,7 +857,7 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
   GatherArgs ga = {segments(s, offsets), false, perm, s->T, s->H, s->k, (int)ld_of(s->H), {xb, dy}, {w.ffn.xp, w.ffn.dyp}};
   CUDA_TRY(launch_train_gather(ga, sms, st), "row copy launch");
   FfnGrad f = {keep_bits, w.ffn.xp, w.ffn.dyp, w1, w2, offsets, z, z_scales, weights, perm, w.part,
-               w.ffn.hw, w.ffn.dz, nullptr, dw1, dw2, w.dxp};
+               w.ffn.hw, w.ffn.dz, nullptr, dw1, dw2, w.ffn.dxp};
   TRY(ffn_gradients(s, f, status, st));
   GateBackwardArgs g = gate_args(s, w.route, w_router, ids, weights, probs);
   g.part = w.part;
@@ -825,7 +865,8 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
   g.rows = (int)rows_of(s);
   g.units = (s->F + 63) / 64;
   RowsSumArgs sum = {};
-  sum.rows32 = w.dxp;
+  sum.rows32 = w.ffn.dxp;
+  sum.splits = row_split(rows_of(s), s->E, s->H, s->F * halves(s)).parts;
   sum.slot = slot;
   sum.T = s->T;
   sum.H = s->H;

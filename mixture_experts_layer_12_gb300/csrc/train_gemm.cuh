@@ -82,6 +82,7 @@ struct TrainTraits {
   static constexpr bool A_MN = WGRAD;
   static constexpr bool B_MN = !(BWD || OP == kTrainRows || OP == kTrainRowsF32);
   static constexpr bool A_PADDED = !(FWD || OP == kTrainPlain || OP == kTrainPlainBf16);
+  static constexpr bool SPLIT = OP == kTrainPlain || OP == kTrainRowsF32;
   static constexpr bool OUT32 = OP == kTrainPlain || OP == kTrainWgradF32 || OP == kTrainRowsF32;
   static constexpr int BN_OUT = PAIRED ? TBN / 2 : TBN;
   // the epilogue's buffers per warp (FWD: z and h, BWD: z turned into dz, and
@@ -98,6 +99,7 @@ struct TrainTile {
   int e, nb;
   int base;    // the tile's first row within the segment (Wgrad: row of out)
   int kb;      // stages
+  int ks, k0;  // part of K, its first stage
   int k16;     // Wgrad: K steps of 16 in all
   bool half;   // M = 128 tile: 64 rows per CTA
   bool nhalf;  // N = 128 tile
@@ -122,6 +124,13 @@ __device__ __forceinline__ TrainTile train_tile(const TrainCtrl& c, const TrainG
   TrainTile t;
   t.e = e;
   t.nb = local / mbs;
+  t.ks = 0;
+  t.k0 = 0;
+  if constexpr (TT::SPLIT) {
+    t.ks = t.nb % p.splits;
+    t.nb /= p.splits;
+    t.k0 = t.ks * p.ksplit;
+  }
   t.base = mb * TPAIR_M;
   if constexpr (TT::WGRAD) {
     t.k16 = (c.seg.rows[e] + 15) / 16;
@@ -129,7 +138,7 @@ __device__ __forceinline__ TrainTile train_tile(const TrainCtrl& c, const TrainG
   } else {
     t.k16 = 0;
     t.kb = (p.K + TBK - 1) / TBK;
-    if (OP == kTrainPlain && p.ksplit) t.kb = min(p.ksplit, t.kb - t.e * p.ksplit);
+    if constexpr (TT::SPLIT) t.kb = min(p.ksplit, t.kb - t.k0);
   }
   t.half = m - t.base <= TPAIR_M / 2;
   t.nhalf = !TT::PAIRED && !t.half && p.N - t.nb * TBN <= TBN / 2;
@@ -532,7 +541,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
   if (warp == 0) {
     seg_scan(p.seg, c.seg, c.tile_start, lane, pair == 0 && rank == 0 ? p.status : nullptr, [&](int n) {
       const int m = TT::WGRAD ? p.M : n;
-      return (m + TPAIR_M - 1) / TPAIR_M * NB;
+      return (m + TPAIR_M - 1) / TPAIR_M * NB * (TT::SPLIT ? p.splits : 1);
     });
   }
   if (p.merge_status && blockIdx.x == 0 && threadIdx.x == 32) {
@@ -585,15 +594,13 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (!t.nhalf) tma_load_2d_pair(b + T_BOX, &tm_b, full_cl, bcol2, krow);
           } else {
             // rows past the segment's end are computed but never stored
-            const bool split = OP == kTrainPlain && p.ksplit;
-            const int k0 = (kb + (split ? t.e * p.ksplit : 0)) * TBK;
-            const int we = split ? 0 : t.e;
+            const int k0 = (t.k0 + kb) * TBK;
             tma_load_2d_pair(a, t.half ? &tm_a64 : &tm_a, full_cl, k0, off + arow);
             if constexpr (TT::B_MN) {
-              tma_load_3d_pair(b, &tm_b, full_cl, bcol, k0, we);
-              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol2, k0, we);
+              tma_load_3d_pair(b, &tm_b, full_cl, bcol, k0, t.e);
+              if (!t.nhalf) tma_load_3d_pair(b + T_BOX, &tm_b, full_cl, bcol2, k0, t.e);
             } else {
-              tma_load_3d_pair(b, &tm_b, full_cl, k0, bcol, we);
+              tma_load_3d_pair(b, &tm_b, full_cl, k0, bcol, t.e);
             }
           }
           ++issued;
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             if (i >= lo) dst[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         size_t orow0 = (size_t)c.seg.row_off[t.e] + w.row0;
-        if (OP == kTrainPlain && p.ksplit) orow0 += (size_t)t.e * p.seg.rows;
+        if constexpr (TT::SPLIT) orow0 += (size_t)t.ks * p.seg.rows;
         [[maybe_unused]] KeptOut kout[HALVES];
         [[maybe_unused]] RowsOut o;
         if constexpr (!TT::WGRAD) {

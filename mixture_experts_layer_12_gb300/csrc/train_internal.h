@@ -24,7 +24,7 @@ inline size_t padded_rows_cap(size_t rows, int E) {
 
 // What a kernel knows of the segments: from `offsets` on the device, or
 // (offsets null) `E` chunks of `chunk` rows of the `rows` there are, laid out
-// without padding (chunk % 16 == 0), or (chunk 0) all `rows` E times.  Offsets that run backwards or past
+// without padding (chunk % 16 == 0).  Offsets that run backwards or past
 // `rows` or overlap are cut so that no row is outside [0, rows) and no padded row
 // outside the padded buffers, and set MOE_DEV_BAD_ID in the call's status.
 struct SegArgs {
@@ -54,8 +54,8 @@ struct TrainGemmArgs {
   int M;        // Wgrad: rows of out (columns of A)
   int N;        // output columns (FwdSwiGLU, Bwd*: F)
   int K;        // reduction length (not Wgrad)
-  int ksplit;   // Plain of one matrix: segment e sums stages [e, e + 1) * ksplit of K
-                // for all rows into out32[e]; 0: not split
+  int splits;   // Plain, RowsF32: parts of K, each a [rows, N] of out32
+  int ksplit;   // stages of 64 in each of them (the last may have fewer)
   uint16_t* out;
   int ld_out;   // columns from one row of `out` to the next (not Wgrad)
   float* out32;
@@ -107,10 +107,15 @@ cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st);
 // out[t] = (add ? add[t] : 0) + sum_j (w ? w[t, j] : 1) * rows[slot[t, j]]
 //          + (dl ? sum_j dl[t, j] * wt[ids[t, j]] : 0)
 // (fp32, in that order, j ascending), rounded to bf16 once; rows in bf16 or fp32
-// (both null: none), add in fp32, wt [E, H] bf16.
+// (both null: none), add in fp32, wt [E, H] bf16.  rows in fp32 may be `splits`
+// parts of T * k rows each, summed in their order.  With `range` (offsets of E
+// segments) slot[t, 0] is t for the rows t inside the segments, and the others
+// are not written.
 struct RowsSumArgs {
   const uint16_t* rows;
   const float* rows32;
+  int splits;
+  const int32_t* range;
   const float* w;
   const int32_t* slot;
   const float* add;

@@ -134,7 +134,7 @@ __device__ __forceinline__ void add_router_rows(const RowsSumArgs& a, int t, int
   }
 }
 
-template <int KMAX, bool F32>
+template <int KMAX, bool F32, bool PARTS>
 __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a) {
   constexpr int RCPT = F32 ? 1 : 2;
   pdl_launch_dependents();
@@ -142,12 +142,14 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
   const int t = blockIdx.x;
   const int col0 = (blockIdx.y * RTHREADS * RCPT + threadIdx.x) * 8;
   if (col0 >= a.H) return;
+  if (PARTS && a.range && (t < __ldg(a.range) || t >= __ldg(a.range + a.E))) return;
   int r[KMAX];
   float w[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
     r[j] = a.slot && j < a.k ? __ldg(a.slot + (size_t)t * a.k + j) : -1;
     if (r[j] >= a.T * a.k) r[j] = -1;  // slot is not re-validated: nothing outside rows
+    if (PARTS && a.range && j == 0) r[j] = t;
     w[j] = a.w && r[j] >= 0 ? __ldg(a.w + (size_t)t * a.k + j) : 1.0f;
   }
   if constexpr (F32) {
@@ -156,22 +158,26 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
     for (int h = 0; h < 2; ++h)
       s[h] = a.add ? __ldg(reinterpret_cast<const float4*>(a.add + (size_t)t * a.H + col0) + h)
                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const size_t part = (size_t)a.T * a.k * a.H;
+    for (int p = 0; p < (PARTS ? a.splits : 1); ++p) {
+      const float* rows = a.rows32 + p * part + col0;
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j)
-      if (r[j] >= 0)
+      for (int j = 0; j < KMAX; ++j)
+        if (r[j] >= 0)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          v[j][h] = __ldg(reinterpret_cast<const float4*>(a.rows32 + (size_t)r[j] * a.H + col0) + h);
+          for (int h = 0; h < 2; ++h)
+            v[j][h] = __ldg(reinterpret_cast<const float4*>(rows + (size_t)r[j] * a.H) + h);
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j)
-      if (r[j] >= 0)
+      for (int j = 0; j < KMAX; ++j)
+        if (r[j] >= 0)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s[h].x = fmaf(w[j], v[j][h].x, s[h].x);
-          s[h].y = fmaf(w[j], v[j][h].y, s[h].y);
-          s[h].z = fmaf(w[j], v[j][h].z, s[h].z);
-          s[h].w = fmaf(w[j], v[j][h].w, s[h].w);
-        }
+          for (int h = 0; h < 2; ++h) {
+            s[h].x = fmaf(w[j], v[j][h].x, s[h].x);
+            s[h].y = fmaf(w[j], v[j][h].y, s[h].y);
+            s[h].z = fmaf(w[j], v[j][h].z, s[h].z);
+            s[h].w = fmaf(w[j], v[j][h].w, s[h].w);
+          }
+    }
     float f[8] = {s[0].x, s[0].y, s[0].z, s[0].w, s[1].x, s[1].y, s[1].z, s[1].w};
     add_router_rows<KMAX>(a, t, col0, f);
     *reinterpret_cast<uint4*>(a.out + (size_t)t * a.H + col0) = pack8(f);
@@ -612,17 +618,19 @@ cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st) {
   return a.H >= 256 ? gather<32>(a, sms, st) : gather<8>(a, sms, st);
 }
 
-template <bool F32>
+template <bool F32, bool PARTS>
 static cudaError_t rows_sum(const RowsSumArgs& a, cudaStream_t st) {
   const int per = RTHREADS * 8 * (F32 ? 1 : 2);
   const dim3 grid((unsigned)a.T, (unsigned)((a.H + per - 1) / per), 1);
-  if (a.k <= 1) return launch(rows_sum_kernel<1, F32>, grid, RTHREADS, st, a);
-  if (a.k <= 2) return launch(rows_sum_kernel<2, F32>, grid, RTHREADS, st, a);
-  if (a.k <= 4) return launch(rows_sum_kernel<4, F32>, grid, RTHREADS, st, a);
-  return launch(rows_sum_kernel<8, F32>, grid, RTHREADS, st, a);
+  if (a.k <= 1) return launch(rows_sum_kernel<1, F32, PARTS>, grid, RTHREADS, st, a);
+  if (a.k <= 2) return launch(rows_sum_kernel<2, F32, PARTS>, grid, RTHREADS, st, a);
+  if (a.k <= 4) return launch(rows_sum_kernel<4, F32, PARTS>, grid, RTHREADS, st, a);
+  return launch(rows_sum_kernel<8, F32, PARTS>, grid, RTHREADS, st, a);
 }
 cudaError_t launch_rows_sum(const RowsSumArgs& a, cudaStream_t st) {
-  return a.rows32 ? rows_sum<true>(a, st) : rows_sum<false>(a, st);
+  if (!a.rows32) return rows_sum<false, false>(a, st);
+  // (a loop over one part takes 15% longer than none)
+  return a.splits > 1 || a.range ? rows_sum<true, true>(a, st) : rows_sum<true, false>(a, st);
 }
 
 template <int W>

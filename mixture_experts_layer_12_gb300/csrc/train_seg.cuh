@@ -37,7 +37,7 @@ __device__ __forceinline__ void seg_scan(const SegArgs& s, SegTable& t, int* til
         bad |= o0 < 0 || o1 < o0 || o1 > s.rows;
       } else {
         o[u] = (int)min((long long)e * s.chunk, (long long)s.rows);
-        hi = s.chunk ? (int)min((long long)o[u] + s.chunk, (long long)s.rows) : s.rows;
+        hi = (int)min((long long)o[u] + s.chunk, (long long)s.rows);
       }
       n[u] = max(hi - o[u], 0);
     }

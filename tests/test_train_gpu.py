@@ -173,6 +173,7 @@ FFN = [
     ([1], 8, 8), ([0], 8, 16), ([3, 0, 2], 64, 64), ([16, 17, 15, 1], 128, 256), ([130, 0, 257, 64], 72, 200),
     ([128, 129, 256, 255], 264, 136), ([300], 520, 392), ([0, 0, 0, 5], 1000, 88), ([2] * 40 + [0] * 3 + [70], 96, 40),
     ([65, 33], 256, 1032), ([600, 7], 128, 128),
+    ([2, 0, 1], 72, 4104), ([5], 264, 2056), ([40, 3], 64, 2600),  # K in parts
 ]
 
 
@@ -214,6 +215,20 @@ def test_expert_ffn_rows_outside_the_segments(act, bits):
     assert torch.isfinite(Y[3:n].float()).all()
     kept = moe.dequantize_a8(z) if bits == 8 else z
     assert torch.isfinite(kept[3:n].float()).all()
+
+
+def test_rows_outside_the_segments_with_k_in_parts():
+    counts, H, F = [2, 0, 3], 72, 4104
+    offsets, xp, dY, w1, w2, zk, zv = ffn_inputs(12, counts, H, F, "gelu", 16, lead=2, tail=4)
+    n = int(offsets[-1])
+    for t in (xp, dY, zk):
+        t[:2], t[n:] = math.nan, math.nan
+    dxp, dw1, dw2 = moe.expert_ffn_backward(xp.to(DEV), zk, w1.to(DEV), w2.to(DEV), offsets.int().to(DEV), dY.to(DEV))
+    clean = [torch.nan_to_num(f64(t)) for t in (xp, dY)]
+    r = ref.ffn_backward(clean[0], torch.nan_to_num(zv), f64(w1), f64(w2), offsets, clean[1], False)
+    ref.inside(dxp[2:n], tuple(v[2:n] for v in ref.to_bf16(*r["dxp"])), "dxp")
+    ref.inside(dw1, r["dw1"], "dw1")
+    ref.inside(dw2, r["dw2"], "dw2")
 
 
 def test_a_neighbours_nan_and_infinities_stay_its_own():
@@ -423,6 +438,8 @@ LAYERS = [
     dict(T=130, H=72, F=72, E=256, k=8),
     dict(T=40, H=64, F=64, E=4, k=2, cf=1e-12, gating=1),  # everything dropped
     dict(T=700, H=512, F=320, E=4, k=2, act="swiglu"),
+    dict(T=3, H=104, F=4136, E=5, k=2, act="swiglu", cf=1.2),  # products with K in parts
+    dict(T=2, H=1032, F=1100 // 8 * 8, E=9, k=1, gating=2),
     dict(T=16500, H=64, F=72, E=8, k=2, act="swiglu", gating=1),  # past the one-launch route
 ]
 
