@@ -827,3 +827,29 @@ def test_wide_rows_of_codes_past_two_to_the_31():
     v = moe.dequantize_a8(q)
     assert torch.equal(f64(v[-1:]), ref.a8_values(ref.a8_codes(x[-1:].cpu(), b), b))
     assert float(v[66000, 0]) == 3.0 and float(v[:66000].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_rows_whose_z_lies_past_two_to_the_31(bits):
+    """The last rows of a long batch, whose kept z is past 2^31 elements, come out
+    as they do alone."""
+    rows, H, F, n = 80000, 64, 14336, 200
+    g = gen(50)
+    w1 = randn(g, 1, H, 2 * F, std=H ** -0.5).to(DEV)
+    w2 = randn(g, 1, F, H, std=F ** -0.5).to(DEV)
+    tail_x, tail_d = randn(g, n, H).to(DEV), randn(g, n, H).to(DEV)
+    xp, dY = (torch.zeros(rows, H, dtype=BF, device=DEV) for _ in range(2))
+    xp[-n:], dY[-n:] = tail_x, tail_d
+    out = []
+    for x, d in ((xp, dY), (tail_x, tail_d)):
+        o = torch.tensor([0, x.shape[0]], dtype=torch.int32, device=DEV)
+        Y, z = moe.expert_ffn(x, w1, w2, o, act="swiglu", keep_bits=bits)
+        grads = moe.expert_ffn_backward(x, z, w1, w2, o, d, act="swiglu")
+        kept = z.codes if bits == 8 else z
+        assert kept.numel() > 1 << 31 or x is tail_x
+        out.append((Y[-n:].clone(), kept[-n:].clone(), grads[0][-n:].float(), grads[1].float(), grads[2].float()))
+    (Y, z, dx, dw1, dw2), (Y1, z1, dx1, e1, e2) = out
+    assert bits_equal(Y, Y1) and bits_equal(z, z1)
+    # dxp in another number of parts, the weights' over rows of zeros besides
+    for a, b in ((dx, dx1), (dw1, e1), (dw2, e2)):
+        assert float((a - b).norm() / b.norm()) < ref.U
