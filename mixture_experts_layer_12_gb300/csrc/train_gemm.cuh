@@ -310,7 +310,8 @@ __device__ __forceinline__ void turn_out_codes(const Turn& t, const RowsOut& o, 
 }
 // A buffer to memory by a TMA store (its pieces lie as the 64-byte swizzle lays
 // them; what is outside the tensor is left out): the ring's next buffer is free
-// once at most BUFS - 1 earlier stores still read theirs.
+// once at most BUFS - 1 earlier stores still read theirs, as every buffer that is
+// filled is stored.
 __device__ __forceinline__ void turn_tma(const Turn& t, const CUtensorMap* m, int c0, int c1, int c2) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
@@ -865,6 +866,8 @@ __global__ void __launch_bounds__(T_THREADS, 1)
             constexpr int OUTS = TT::OUT32 ? 2 : 1;
 #pragma unroll
             for (int o = 0; o < OUTS; ++o) {
+              // one store per buffer of the ring, or the wait would count too few
+              if (gcol + 16 * o >= p.N) break;
               turn_tma_wait<TT::BUFS - 1>(lane);
               const Turn out = turn.buffer(ring);
 #pragma unroll
@@ -879,7 +882,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
                   sts16(out.own(g), train_pack8(f));
                 }
               }
-              if (gcol + 16 * o < p.N) turn_tma(out, &tm_a64, gcol + 16 * o, w.row0, t.e);
+              turn_tma(out, &tm_a64, gcol + 16 * o, w.row0, t.e);
               ring = ring == TT::BUFS - 1 ? 0 : ring + 1;
             }
           } else if constexpr (TT::OUT32) {

@@ -354,6 +354,36 @@ def test_route_backward(T, H, E, k, gating):
         assert (dx == 0).all() and (dwr == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("T,H,E,k", [(64, 20480, 8, 2), (16, 40000, 24, 3), (5, 30008, 3, 1), (16, 10240, 132, 2)])
+def test_route_backward_of_wide_rows(T, H, E, k):
+    """More tiles of dW_router than CTA pairs, so that a pair stores several, of
+    numbers of columns that do and do not fill their last 32 (E rounded up to 8,
+    twice: 16, 48, 16 and 272)."""
+    g = gen(24)
+    x, wr = randn(g, T, H), randn(g, H, E, std=H ** -0.5)
+    dw = torch.randn(T, k, generator=g)
+    lg = f64(x) @ f64(wr)
+    ids = torch.topk(lg, k, dim=1).indices
+    w = ref.gate(lg, ids, 0).float()
+    dl, dle = ref.dlogits(ids, w.double(), dw.double(), torch.zeros(T, k).double(), 0, None, E)
+    if k == 1:  # weights of 1 have no gradient: of a softmax over all instead
+        p = torch.softmax(lg, 1).float()
+        dl, dle = ref.dlogits(ids, torch.gather(p, 1, ids).double(), dw.double(), torch.zeros(T, k).double(), 1,
+                              p.double(), E)
+        w = torch.gather(p, 1, ids)
+    r = ref.route_backward(f64(x), f64(wr), dl, dle)
+    args = [t.to(DEV) for t in (x, wr, ids.int(), w, dw)]
+    first = None
+    for _ in range(8):
+        got = moe.route_backward(*args, gating=int(k == 1), probs=p.to(DEV) if k == 1 else None)
+        ref.inside(got[1], r["dw_router"], "dw_router")
+        first = first or got
+        assert all(bits_equal(a, b) for a, b in zip(first, got))
+    ref.inside(first[0], ref.to_bf16(*r["dx"]), "dx")
+    ref.inside(first[2], r["db"], "dbias")
+    assert moe.train_status() == 0
+
+
 # ---------------------------------------------------------------- the layer --
 
 def make_layer(seed, T, H, F, E, k, act="gelu", gating=0, cf=None, bias=False, bits=16, skew=0.0):
