@@ -35,7 +35,8 @@
  *     before its first use: calls set bits in its first word and never clear
  *     them; moe_get_device_status(status, ...) reads and clears it.
  *   - `ws` holds nothing before or after a call.
- *   - Outputs must not overlap inputs.
+ *   - What a call writes (outputs, status, ws) must not overlap what it reads,
+ *     nor one output another: refused with MOE_ERR_INVALID_ARG.
  *   - offsets, perm, slot and ids are a dispatch's (moe_route, moe_dispatch);
  *     entries outside their range are not followed outside a buffer, and
  *     offsets that are not ascending within [0, T*k] set MOE_DEV_BAD_ID.

@@ -1,6 +1,7 @@
 // train_api.cu -- the C ABI declared in include/moe_train.h: argument checks,
 // workspace layouts, tensor maps and the launches of each call on the caller's
 // stream.  No allocation and no host synchronisation.
+#include <initializer_list>
 #include <mutex>
 
 #include "api_internal.h"
@@ -510,6 +511,39 @@ int check_bits(int32_t bits) {
                   name);                                                                            \
   } while (0)
 
+// The bytes that a call reads or writes of a buffer (null: none).
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+#define SPAN(p, n) Span{p, (size_t)(n) * sizeof(*(p)), #p}
+
+// What a call writes lies apart from what it reads and from the rest of what it
+// writes: blocks finish in any order, some while others still read.
+int check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  const auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && a.bytes && b.bytes && (x < y ? y - x < a.bytes : x - y < b.bytes);
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meet(*o, i)) return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", o->name, i.name);
+    for (const Span* q = o + 1; q != outs.end(); ++q)
+      if (meet(*o, *q)) return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", o->name, q->name);
+  }
+  return MOE_OK;
+}
+// Elements of the experts' weights, of kept z and of its scales.
+size_t w1_of(const moe_shape* s) { return (size_t)s->E * s->H * s->F * halves(s); }
+size_t w2_of(const moe_shape* s) { return (size_t)s->E * s->F * s->H; }
+Span kept_span(const moe_shape* s, int bits, const void* z) {
+  return Span{z, rows_of(s) * halves(s) * s->F * (bits / 8), "z"};
+}
+Span kept_scales_span(const moe_shape* s, int bits, const uint8_t* z_scales) {
+  return Span{z_scales, bits == 8 ? rows_of(s) * halves(s) * (((size_t)s->F + 31) / 32) : 0, "z_scales"};
+}
+
 int check_a8(int64_t rows, int32_t cols) {
   if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "rows = %lld, cols = %d", (long long)rows, cols);
   if (cols < 8 || cols % 8) return fail(MOE_ERR_UNSUPPORTED, "cols = %d: need cols >= 8, cols %% 8 == 0", cols);
@@ -543,6 +577,8 @@ int moet_quantize_a8(int64_t rows, int32_t cols, const uint16_t* x, int8_t* code
   REQUIRE_PTR(x);
   REQUIRE_PTR(codes);
   REQUIRE_PTR(scales);
+  const size_t n = (size_t)rows * cols, groups = (size_t)rows * ((cols + 31) / 32);
+  TRY(check_apart({SPAN(codes, n), SPAN(scales, groups)}, {SPAN(x, n)}));
   int sms = 0;
   TRY(device_setup(&sms));
   CUDA_TRY(launch_quantize_a8(rows, cols, x, codes, scales, sms, stream_of(stream)), "quantize launch");
@@ -556,6 +592,8 @@ int moet_dequantize_a8(int64_t rows, int32_t cols, const int8_t* codes, const ui
   REQUIRE_PTR(codes);
   REQUIRE_PTR(scales);
   REQUIRE_PTR(out);
+  const size_t n = (size_t)rows * cols, groups = (size_t)rows * ((cols + 31) / 32);
+  TRY(check_apart({SPAN(out, n)}, {SPAN(codes, n), SPAN(scales, groups)}));
   int sms = 0;
   TRY(device_setup(&sms));
   CUDA_TRY(launch_dequantize_a8(rows, cols, codes, scales, out, sms, stream_of(stream)), "dequantize launch");
@@ -569,6 +607,8 @@ int moet_dispatch_rows_backward(const moe_shape* s, const uint16_t* dxp, const i
   REQUIRE_PTR(dxp);
   REQUIRE_PTR(slot);
   REQUIRE_PTR(dx);
+  const size_t n = rows_of(s);
+  TRY(check_apart({SPAN(dx, (size_t)s->T * s->H)}, {SPAN(dxp, n * s->H), SPAN(slot, n)}));
   int sms = 0;
   TRY(device_setup(&sms));
   RowsSumArgs a = {};
@@ -592,6 +632,9 @@ int moet_combine_backward(const moe_shape* s, const uint16_t* dy, const uint16_t
   REQUIRE_PTR(slot);
   REQUIRE_PTR(dY);
   REQUIRE_PTR(dweights);
+  const size_t n = rows_of(s);
+  TRY(check_apart({SPAN(dY, n * s->H), SPAN(dweights, n)},
+                  {SPAN(dy, (size_t)s->T * s->H), SPAN(Y, n * s->H), SPAN(weights, n), SPAN(slot, n)}));
   int sms = 0;
   TRY(device_setup(&sms));
   CombineBackwardArgs a = {dy, Y, weights, slot, s->T, s->H, s->k, dY, dweights};
@@ -620,6 +663,10 @@ int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, c
   REQUIRE_PTR(Y);
   REQUIRE_PTR(z);
   if (keep_bits == 8) REQUIRE_PTR(z_scales);
+  const size_t n = rows_of(s);
+  TRY(check_apart({SPAN(Y, n * s->H), kept_span(s, keep_bits, z), kept_scales_span(s, keep_bits, z_scales),
+                   Span{status, MOE_WS_MIN_BYTES, "status"}, Span{ws, moet_expert_ffn_workspace_size(s), "ws"}},
+                  {SPAN(xp, n * s->H), SPAN(w1, w1_of(s)), SPAN(w2, w2_of(s)), SPAN(offsets, s->E + 1)}));
   int sms = 0;
   TRY(train_setup(&sms));
   Carve c(ws);
@@ -653,6 +700,11 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
     REQUIRE_PTR(offsets);
     REQUIRE_PTR(dY);
     REQUIRE_PTR(dxp);
+    const size_t n = rows_of(s);
+    TRY(check_apart({SPAN(dxp, n * s->H), SPAN(dw1, w1_of(s)), SPAN(dw2, w2_of(s)),
+                     Span{status, MOE_WS_MIN_BYTES, "status"}, Span{ws, moet_expert_ffn_backward_workspace_size(s), "ws"}},
+                    {SPAN(xp, n * s->H), kept_span(s, keep_bits, z), kept_scales_span(s, keep_bits, z_scales),
+                     SPAN(w1, w1_of(s)), SPAN(w2, w2_of(s)), SPAN(offsets, s->E + 1), SPAN(dY, n * s->H)}));
   }
   cudaStream_t st = stream_of(stream);
   int sms = 0;
@@ -683,6 +735,9 @@ int moet_router_probs(const moe_shape* s, const uint16_t* x, const uint16_t* w_r
   REQUIRE_PTR(x);
   REQUIRE_PTR(w_router);
   REQUIRE_PTR(probs);
+  TRY(check_apart({SPAN(probs, (size_t)s->T * s->E), Span{status, MOE_WS_MIN_BYTES, "status"},
+                   Span{ws, moet_router_probs_workspace_size(s), "ws"}},
+                  {SPAN(x, (size_t)s->T * s->H), SPAN(w_router, (size_t)s->H * s->E), SPAN(b_router, s->E)}));
   int sms = 0;
   TRY(train_setup(&sms));
   Carve c(ws);
@@ -711,6 +766,11 @@ int moet_route_backward(const moe_shape* s, const uint16_t* x, const uint16_t* w
     if (s->gating == MOE_GATE_SOFTMAX_TOPK) REQUIRE_PTR(probs);
     REQUIRE_PTR(dweights);
     REQUIRE_PTR(dx);
+    const size_t n = rows_of(s);
+    TRY(check_apart({SPAN(dx, (size_t)s->T * s->H), SPAN(dw_router, (size_t)s->H * s->E), SPAN(db, s->E),
+                     Span{status, MOE_WS_MIN_BYTES, "status"}, Span{ws, moet_route_backward_workspace_size(s), "ws"}},
+                    {SPAN(x, (size_t)s->T * s->H), SPAN(w_router, (size_t)s->H * s->E), SPAN(ids, n), SPAN(weights, n),
+                     SPAN(probs, s->gating == MOE_GATE_SOFTMAX_TOPK ? (size_t)s->T * s->E : 0), SPAN(dweights, n)}));
   }
   cudaStream_t st = stream_of(stream);
   int sms = 0;
@@ -766,6 +826,15 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
     REQUIRE_PTR(weights);
     REQUIRE_PTR(perm);
     REQUIRE_PTR(slot);
+    const size_t n = rows_of(s), x8 = keep_bits == 8 ? s->T : 0;
+    TRY(check_apart({SPAN(y, (size_t)s->T * s->H), SPAN(ids, n), SPAN(weights, n), SPAN(counts, s->E),
+                     SPAN(offsets, s->E + 1), SPAN(perm, n), SPAN(slot, n), kept_span(s, keep_bits, z),
+                     kept_scales_span(s, keep_bits, z_scales), SPAN(xk, x8 * s->H),
+                     SPAN(xk_scales, x8 * (((size_t)s->H + 31) / 32)),
+                     SPAN(probs, s->gating == MOE_GATE_SOFTMAX_TOPK ? (size_t)s->T * s->E : 0),
+                     Span{status, MOE_WS_MIN_BYTES, "status"}, Span{ws, moet_forward_workspace_size(s), "ws"}},
+                    {SPAN(x, (size_t)s->T * s->H), SPAN(w_router, (size_t)s->H * s->E), SPAN(b_router, s->E),
+                     SPAN(w1, w1_of(s)), SPAN(w2, w2_of(s))}));
   }
   cudaStream_t st = stream_of(stream);
   int sms = 0;
@@ -837,6 +906,16 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
     }
     if (s->gating == MOE_GATE_SOFTMAX_TOPK) REQUIRE_PTR(probs);
     REQUIRE_PTR(dx);
+    const size_t n = rows_of(s), th = (size_t)s->T * s->H;
+    TRY(check_apart({SPAN(dx, th), SPAN(dw_router, (size_t)s->H * s->E), SPAN(db, s->E), SPAN(dw1, w1_of(s)),
+                     SPAN(dw2, w2_of(s)), Span{status, MOE_WS_MIN_BYTES, "status"},
+                     Span{ws, moet_backward_workspace_size(s, keep_bits), "ws"}},
+                    {SPAN(dy, th), Span{x, th * (keep_bits / 8), "x"},
+                     SPAN(x_scales, keep_bits == 8 ? (size_t)s->T * ((s->H + 31) / 32) : 0),
+                     SPAN(w_router, (size_t)s->H * s->E), SPAN(w1, w1_of(s)), SPAN(w2, w2_of(s)), SPAN(ids, n),
+                     SPAN(weights, n), SPAN(offsets, s->E + 1), SPAN(perm, n), SPAN(slot, n),
+                     kept_span(s, keep_bits, z), kept_scales_span(s, keep_bits, z_scales),
+                     SPAN(probs, s->gating == MOE_GATE_SOFTMAX_TOPK ? (size_t)s->T * s->E : 0)}));
   }
   cudaStream_t st = stream_of(stream);
   int sms = 0;

@@ -8,7 +8,8 @@ themselves (:class:`MoETrainLayer`), the same for single steps
 (:func:`quantize_a8`, :func:`dequantize_a8`).  Gradients are explicit calls, as
 every other step of this package; all of them run in the library's CUDA kernels
 on the current stream (or `stream`), allocate their outputs and workspace there
-and keep nothing between calls.
+and keep nothing between calls.  An output that the caller gives must not overlap
+an input (MoEError).
 """
 from __future__ import annotations
 

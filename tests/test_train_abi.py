@@ -128,6 +128,91 @@ def test_rows_refuse(lib):
         assert fn(ctypes.byref(moe.make_shape(0, 128, 8, 8, 2)), *([None] * n), None) == moe.MOE_OK
 
 
+# name -> (pointers written, pointers read) with their bytes, in the order of the arguments; sizes for SHAPE, kept in
+# 8 bits, softmax over all, n = T k
+def buffers(name, bits):
+    T, H, F, E, k = (SHAPE[v] for v in "THFEk")
+    n = T * k
+    z, zs = n * F * bits // 8, n * F // 32 if bits == 8 else 0
+    x8, xs = (T * H, T * H // 32) if bits == 8 else (0, 0)
+    w1 = w2 = 2 * E * H * F
+    wr, p, th, nh, off = 2 * H * E, 4 * T * E, 2 * T * H, 2 * n * H, 4 * (E + 1)
+    r, w = "r", "w"  # read, written
+    return {
+        "moet_dispatch_rows_backward": [(r, nh), (r, 4 * n), (w, th)],
+        "moet_combine_backward": [(r, th), (r, nh), (r, 4 * n), (r, 4 * n), (w, nh), (w, 4 * n)],
+        "moet_expert_ffn": [(r, nh), (r, w1), (r, w2), (r, off), (w, nh), (w, z), (w, zs)],
+        "moet_expert_ffn_backward": [(r, nh), (r, z), (r, zs), (r, w1), (r, w2), (r, off), (r, nh), (w, nh), (w, w1),
+                                     (w, w2)],
+        "moet_router_probs": [(r, th), (r, wr), (r, 4 * E), (w, p)],
+        "moet_route_backward": [(r, th), (r, wr), (r, 4 * n), (r, 4 * n), (r, p), (r, 4 * n), (w, th), (w, wr),
+                                (w, 4 * E)],
+        "moet_forward": [(r, th), (r, wr), (r, 4 * E), (r, w1), (r, w2), (w, th), (w, 4 * n), (w, 4 * n), (w, 4 * E),
+                         (w, off), (w, 4 * n), (w, 4 * n), (w, z), (w, zs), (w, x8), (w, xs), (w, p)],
+        "moet_backward": [(r, th), (r, T * H * bits // 8), (r, xs), (r, wr), (r, w1), (r, w2), (r, 4 * n), (r, 4 * n),
+                          (r, off), (r, 4 * n), (r, 4 * n), (r, z), (r, zs), (r, p), (w, th), (w, wr), (w, 4 * E),
+                          (w, w1), (w, w2)],
+    }[name]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses, of which some calls are not refused")
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("name", ["moet_dispatch_rows_backward", "moet_combine_backward", *CALLS])
+def test_outputs_that_overlap_are_refused(lib, name, bits):
+    """Every output, the status block and the workspace one 16-byte piece into the
+    front or the end of every other buffer of the call; side by side they pass on
+    to the device, of which there is none."""
+    s = moe.make_shape(**SHAPE, gating=1)
+    bufs = buffers(name, bits)
+    mid = (bits,) if name in CALLS and CALLS[name][0] else ()
+    tail = []
+    if name in CALLS:
+        need = size_of(lib, name, s, bits)
+        bufs = bufs + [("w", moe.MOE_WS_MIN_BYTES), ("w", need)]
+        tail = [need]
+    step = 1 << 30
+    at = [step * (i + 1) for i in range(len(bufs))]
+
+    def call(addresses):
+        return getattr(lib, name)(ctypes.byref(s), *mid, *[P(a) for a in addresses], *tail, None)
+
+    assert call(at) == moe.MOE_ERR_CUDA
+    for i, (kind, size) in enumerate(bufs):
+        if kind == "r" or size == 0:
+            continue
+        for j, (_, other) in enumerate(bufs):
+            if i == j or other == 0:
+                continue
+            up = [-(-v // 16) * 16 for v in (other, size)]  # whole 16-byte pieces
+            for d, code in ((up[0] - 16, moe.MOE_ERR_INVALID_ARG), (16 - up[1], moe.MOE_ERR_INVALID_ARG),
+                            (up[0], moe.MOE_ERR_CUDA), (-up[1], moe.MOE_ERR_CUDA)):
+                a = list(at)
+                a[i] = at[j] + d
+                assert call(a) == code, (i, j, d)
+                if code == moe.MOE_ERR_INVALID_ARG:
+                    assert b"overlaps" in lib.moe_last_error_string()
+    for i, (kind, _) in enumerate(bufs):  # inputs may be one another's
+        for j, (other, _) in enumerate(bufs):
+            if kind == other == "r":
+                a = list(at)
+                a[i] = a[j]
+                assert call(a) == moe.MOE_ERR_CUDA
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses, of which some calls are not refused")
+def test_a8_outputs_that_overlap_are_refused(lib):
+    rows, cols = 4, 40  # 320 bytes of bf16, 160 of codes, 8 of scales
+    a, b, c = 1 << 30, 1 << 31, 1 << 32
+    q, d = lib.moet_quantize_a8, lib.moet_dequantize_a8
+    for fn, args in ((q, (a, b, c)), (q, (a, a + 320, a + 480)), (q, (a, a - 160, a - 176)), (d, (a, b, c)),
+                     (d, (a, a, b)), (d, (a, a + 160, a + 176)), (d, (a, a - 16, a - 336))):
+        assert fn(rows, cols, *[P(v) for v in args], None) == moe.MOE_ERR_CUDA, args
+    for fn, args in ((q, (a, a, c)), (q, (a, a + 304, c)), (q, (a, a - 144, c)), (q, (a, b, a + 16)),
+                     (q, (a, b, b + 144)), (d, (a, b, a)), (d, (a, b, b - 304)), (d, (a, b, b)), (d, (a, b, a + 144))):
+        assert fn(rows, cols, *[P(v) for v in args], None) == moe.MOE_ERR_INVALID_ARG, args
+        assert b"overlaps" in lib.moe_last_error_string()
+
+
 def test_workspaces_hold_what_a_call_needs(lib):
     s = moe.make_shape(4096, 4096, 14336, 8, 2)
     n, pad = 8192, 8192 + 8 * 15

@@ -151,6 +151,30 @@ def test_rows_of_dropped_slots_do_not_reach_the_gradients():
     assert (dx[1] == 0).all() and (dw[1] == 0).all()
 
 
+def test_outputs_over_inputs_are_refused():
+    T, H, k = 6, 64, 2
+    g = gen(6)
+    rows = torch.cat([randn(g, T * k, H), randn(g, T, H)]).to(DEV)  # dxp or Y, dy
+    Y, dy = rows[:T * k], rows[T * k:]
+    before = rows.clone()
+    slot = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k)
+    w = torch.full((T, k), 0.5, device=DEV)
+    for call in (lambda: moe.dispatch_rows_backward(Y, slot, out=Y[:T]),
+                 lambda: moe.dispatch_rows_backward(Y, slot, out=Y[-T:]),
+                 lambda: moe.combine_backward(dy, Y, w, slot, dY=Y),
+                 lambda: moe.combine_backward(dy, Y, w, slot, dY=rows[T:T + T * k]),
+                 lambda: moe.combine_backward(dy, Y, w, slot, dweights=w)):
+        with pytest.raises(moe.MoEError, match="overlaps"):
+            call()
+    q = moe.quantize_a8(Y)
+    memory = torch.empty(T * k * H * 2, dtype=torch.uint8, device=DEV)
+    q = moe.A8Tensor(memory[:T * k * H].view(torch.int8).view(T * k, H).copy_(q.codes), q.scales)
+    with pytest.raises(moe.MoEError, match="overlaps"):
+        moe.dequantize_a8(q, out=memory.view(BF).view(T * k, H))
+    assert torch.equal(rows, before)
+    moe.dispatch_rows_backward(Y, slot, out=dy)  # beside one another
+
+
 # ------------------------------------------------------------- experts' FFN --
 
 def ffn_inputs(seed, counts, H, F, act, bits, lead=0, tail=0):
