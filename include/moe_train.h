@@ -112,7 +112,9 @@ MOE_API int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, cons
 
 /*
  * probs [T, E] fp32 = softmax(x W_router + b_router) over all experts, what
- * MOE_GATE_SOFTMAX_TOPK's gradient needs of the forward.
+ * MOE_GATE_SOFTMAX_TOPK's gradient needs of the forward.  As in the route a
+ * logit of -inf or NaN masks its expert (probability 0); a token whose logits
+ * all do has NaN.
  */
 MOE_API size_t moet_router_probs_workspace_size(const moe_shape* s);
 MOE_API int moet_router_probs(const moe_shape* s, const uint16_t* x, const uint16_t* w_router,

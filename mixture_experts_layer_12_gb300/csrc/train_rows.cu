@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(256) router_softmax_kernel(const float* logits
       v[u] = __ldg(logits + (size_t)t * ldl + e);
       for (int i = 1; i < S; ++i) v[u] += __ldg(logits + ((size_t)i * T + t) * ldl + e);
       if (bias) v[u] += __ldg(bias + e);
+      if (isnan(v[u])) v[u] = -INFINITY;  // masked, as the route has it
     }
     m = fmaxf(m, v[u]);
   }

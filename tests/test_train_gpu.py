@@ -548,6 +548,30 @@ def test_forward_agrees_with_the_inference_layer():
     assert float((y.float() - y2.float()).norm() / y2.float().norm()) < 2 * ref.U
 
 
+@pytest.mark.parametrize("gating", [0, 1, 2])
+@pytest.mark.parametrize("T,E,k,masked", [(5, 4, 2, (1,)), (200, 13, 3, (0, 5, 12)), (64, 8, 3, (0, 1, 3, 4, 6, 7)),
+                                          (150, 130, 6, tuple(range(40, 128)))])
+def test_masked_experts(T, E, k, masked, gating):
+    """Experts masked by a bias of -inf or NaN, more of them than leave k: chosen
+    last, with a weight, a probability and gradients of the logits of 0."""
+    x, dy, layer = make_layer(47, T=T, H=128, F=72, E=E, k=k, gating=gating, bias=True)
+    runs = []
+    for value in (-math.inf, math.nan):
+        layer.bias[list(masked)] = value
+        y, saved = layer(x)
+        g = layer.backward(saved, dy, bias_grad=True)
+        if value == -math.inf:
+            check_layer(x, dy, layer, y, saved, g)
+            off = torch.isin(saved.routing.ids.cpu(), torch.tensor(masked))
+            assert (saved.routing.weights.cpu()[off] == 0).all() and off.any() == (E - len(masked) < k)
+        probs = moe.router_probs(x, layer.w_router, layer.bias)
+        assert (probs[:, list(masked)] == 0).all()
+        assert (g.dbias[list(masked)] == 0).all() and (g.dw_router[:, list(masked)] == 0).all()
+        runs.append([*all_of(y, saved, g), probs])
+    for a, b in zip(*runs):
+        assert bits_equal(a, b)
+
+
 def all_of(y, saved, g):
     z = (saved.z.codes, saved.z.scales) if isinstance(saved.z, moe.A8Tensor) else (saved.z,)
     return [y, g.dx, g.dw_router, g.dbias, g.dw1, g.dw2, *z]
