@@ -577,7 +577,7 @@ int moet_quantize_a8(int64_t rows, int32_t cols, const uint16_t* x, int8_t* code
   REQUIRE_PTR(x);
   REQUIRE_PTR(codes);
   REQUIRE_PTR(scales);
-  const size_t n = (size_t)rows * cols, groups = (size_t)rows * ((cols + 31) / 32);
+  const size_t n = (size_t)rows * cols, groups = (size_t)rows * (((size_t)cols + 31) / 32);
   TRY(check_apart({SPAN(codes, n), SPAN(scales, groups)}, {SPAN(x, n)}));
   int sms = 0;
   TRY(device_setup(&sms));
@@ -592,7 +592,7 @@ int moet_dequantize_a8(int64_t rows, int32_t cols, const int8_t* codes, const ui
   REQUIRE_PTR(codes);
   REQUIRE_PTR(scales);
   REQUIRE_PTR(out);
-  const size_t n = (size_t)rows * cols, groups = (size_t)rows * ((cols + 31) / 32);
+  const size_t n = (size_t)rows * cols, groups = (size_t)rows * (((size_t)cols + 31) / 32);
   TRY(check_apart({SPAN(out, n)}, {SPAN(codes, n), SPAN(scales, groups)}));
   int sms = 0;
   TRY(device_setup(&sms));
@@ -911,7 +911,7 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
                      SPAN(dw2, w2_of(s)), Span{status, MOE_WS_MIN_BYTES, "status"},
                      Span{ws, moet_backward_workspace_size(s, keep_bits), "ws"}},
                     {SPAN(dy, th), Span{x, th * (keep_bits / 8), "x"},
-                     SPAN(x_scales, keep_bits == 8 ? (size_t)s->T * ((s->H + 31) / 32) : 0),
+                     SPAN(x_scales, keep_bits == 8 ? (size_t)s->T * (((size_t)s->H + 31) / 32) : 0),
                      SPAN(w_router, (size_t)s->H * s->E), SPAN(w1, w1_of(s)), SPAN(w2, w2_of(s)), SPAN(ids, n),
                      SPAN(weights, n), SPAN(offsets, s->E + 1), SPAN(perm, n), SPAN(slot, n),
                      kept_span(s, keep_bits, z), kept_scales_span(s, keep_bits, z_scales),

@@ -648,7 +648,7 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, cudaStream_t s
 
 cudaError_t launch_quantize_a8(int64_t rows, int cols, const uint16_t* x, int8_t* codes, uint8_t* scales,
                                int sms, cudaStream_t st) {
-  const int per_row = (cols + 31) / 32 * 4;
+  const int per_row = (int)(((int64_t)cols + 31) / 32 * 4);
   const int64_t chunks = rows * per_row;
   const unsigned g = blocks_for(chunks, QTHREADS * QILP, (int64_t)(sms > 0 ? sms : 1) * (2048 / QTHREADS) * 4);
   if (cols % 32 == 0) return launch(quantize_a8_kernel<true>, dim3(g), QTHREADS, st, chunks, per_row, cols, x, codes, scales);
@@ -657,7 +657,7 @@ cudaError_t launch_quantize_a8(int64_t rows, int cols, const uint16_t* x, int8_t
 
 cudaError_t launch_dequantize_a8(int64_t rows, int cols, const int8_t* codes, const uint8_t* scales,
                                  uint16_t* out, int sms, cudaStream_t st) {
-  const int per_row = (cols + 31) / 32 * 4;
+  const int per_row = (int)(((int64_t)cols + 31) / 32 * 4);
   const int64_t chunks = rows * per_row;
   const unsigned g = blocks_for(chunks, QTHREADS * QILP, (int64_t)(sms > 0 ? sms : 1) * (2048 / QTHREADS) * 4);
   if (cols % 32 == 0)

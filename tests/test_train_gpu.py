@@ -907,6 +907,21 @@ def test_wide_rows_of_codes_past_two_to_the_31():
     assert float(v[66000, 0]) == 3.0 and float(v[:66000].abs().max()) == 0.0
 
 
+def test_the_longest_rows_of_codes():
+    """The largest number of columns that is a multiple of 8 and none of 32."""
+    cols = 2 ** 31 - 8
+    x = torch.zeros(cols, dtype=BF, device=DEV)
+    x[-24:] = torch.arange(24, device=DEV).to(BF)
+    x[:8] = 127.0
+    q = moe.quantize_a8(x)
+    assert q.scales.numel() == 2 ** 26
+    assert q.scales[-1] == 125 and q.scales[0] == 127  # 23 > 127 / 8
+    assert torch.equal(q.codes[-24:].float() * 2.0 ** (int(q.scales[-1]) - 127), x[-24:].float())
+    v = moe.dequantize_a8(q)
+    assert bits_equal(v[-24:], x[-24:]) and bits_equal(v[:32], x[:32])
+    assert int(torch.count_nonzero(v)) == 23 + 8
+
+
 @pytest.mark.parametrize("bits", [16, 8])
 def test_rows_whose_z_lies_past_two_to_the_31(bits):
     """The last rows of a long batch, whose kept z is past 2^31 elements, come out
