@@ -69,7 +69,10 @@ class moe_shape(ctypes.Structure):
 def make_shape(T: int, H: int, F: int, E: int, k: int, capacity_factor=None,
                gating: int = MOE_GATE_TOPK_SOFTMAX, act: str = "gelu") -> moe_shape:
     cf = -1.0 if capacity_factor is None else float(capacity_factor)
-    return moe_shape(int(T), int(H), int(F), int(E), int(k), cf, int(gating), _ACTS[act])
+    sizes = int(T), int(H), int(F), int(E), int(k)
+    if max(sizes) >= 2 ** 31 or min(sizes) < -2 ** 31:  # ctypes would drop the upper bits
+        raise ValueError(f"T, H, F, E, k = {sizes} do not fit in 32 bits")
+    return moe_shape(*sizes, cf, int(gating), _ACTS[act])
 
 
 _lock = threading.Lock()

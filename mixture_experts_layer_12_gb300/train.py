@@ -174,11 +174,14 @@ def _a8_new(shape, device) -> A8Tensor:
     return q
 
 
-def _rows(shape) -> int:
+def _matrix(shape):
+    """(rows, columns) of a tensor as the 8-bit calls take it."""
     n = 1
     for v in shape[:-1]:
         n *= v
-    return n
+    if shape[-1] >= 2 ** 31:  # ctypes would drop the upper bits
+        raise ValueError(f"a last dimension of {shape[-1]}: it must be below 2^31")
+    return n, shape[-1]
 
 
 def quantize_a8(x: torch.Tensor, stream=None) -> A8Tensor:
@@ -189,9 +192,10 @@ def quantize_a8(x: torch.Tensor, stream=None) -> A8Tensor:
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
     dev, raw = _here()
+    rows, cols = _matrix(x.shape)
     src = _addr(x, _BF, "x", x.numel(), dev)
     q = _a8_new(tuple(x.shape), x.device)
-    rc = _lib().moet_quantize_a8(_rows(x.shape), x.shape[-1], src, q.codes.data_ptr(), q.scales.data_ptr(), raw)
+    rc = _lib().moet_quantize_a8(rows, cols, src, q.codes.data_ptr(), q.scales.data_ptr(), raw)
     if rc:
         _check(rc)
     return q
@@ -203,10 +207,11 @@ def dequantize_a8(q: A8Tensor, out: torch.Tensor | None = None, stream=None) -> 
         with _on(stream):
             return dequantize_a8(q, out)
     dev, raw = _here()
+    rows, cols = _matrix(q.shape)
     codes = _addr(q.codes, _I8, "codes", q.codes.numel(), dev)
     scales = _addr(q.scales, _U8, "scales", q.scales.numel(), dev)
     out = _out(out, q.codes.shape, _BF, "out", dev, q.codes.device)
-    rc = _lib().moet_dequantize_a8(_rows(q.shape), q.shape[-1], codes, scales, out.data_ptr(), raw)
+    rc = _lib().moet_dequantize_a8(rows, cols, codes, scales, out.data_ptr(), raw)
     if rc:
         _check(rc)
     return out

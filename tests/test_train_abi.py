@@ -252,6 +252,24 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         moe.quantize_a8(x)
 
 
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """Not cut to their lower 32 bits (4 rows, 8 columns)."""
+    monkeypatch.setattr(train, "_here", lambda: (-1, None))  # tensors without memory, on no device
+    new = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    many = (1 << 32) + 4
+    for kw in (dict(T=many), dict(H=1 << 31), dict(F=1 << 32), dict(E=(1 << 32) + 8), dict(k=(1 << 32) + 2)):
+        with pytest.raises(ValueError, match="32 bits"):
+            moe.make_shape(**{**SHAPE, **kw})
+    with pytest.raises(ValueError, match=r"2\^31"):
+        moe.quantize_a8(new(1, (1 << 32) + 8))
+    with pytest.raises(ValueError, match=r"2\^31"):
+        moe.dequantize_a8(moe.A8Tensor(new((1 << 32) + 8, dtype=torch.int8), new((1 << 27) + 1, dtype=torch.uint8)))
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.dispatch_rows_backward(new(many, 8), new(many, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.expert_ffn(new(many, 8), new(1, 8, 8), new(1, 8, 8), new(2, dtype=torch.int32))
+
+
 # ------------------------------------------------------ the tests' reference --
 
 @pytest.mark.parametrize("gating", [0, 1, 2])
