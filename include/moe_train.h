@@ -35,6 +35,7 @@
  *     before its first use: calls set bits in its first word and never clear
  *     them; moe_get_device_status(status, ...) reads and clears it.
  *   - `ws` holds nothing before or after a call.
+ *   - H <= 2^25 and F <= 2^29 (MOE_ERR_UNSUPPORTED).
  *   - What a call writes (outputs, status, ws) must not overlap what it reads,
  *     nor one output another: refused with MOE_ERR_INVALID_ARG.
  *   - offsets, perm, slot and ids are a dispatch's (moe_route, moe_dispatch);

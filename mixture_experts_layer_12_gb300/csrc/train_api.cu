@@ -497,6 +497,15 @@ BackwardWs backward_ws(const moe_shape* s, int bits, Carve& c) {
   return w;
 }
 
+// moe.h's limits, and below the sizes whose grids (row sums: 1024 columns a block
+// of y, at most 65535) or numbers of columns (2 F) would not fit.
+int check_train_shape(const moe_shape* s, bool need_ffn) {
+  TRY(check_shape(s, need_ffn));
+  if (s->H > 1 << 25) return fail(MOE_ERR_UNSUPPORTED, "H = %d: at most 2^25", s->H);
+  if (need_ffn && s->F > 1 << 29) return fail(MOE_ERR_UNSUPPORTED, "F = %d: at most 2^29", s->F);
+  return MOE_OK;
+}
+
 int check_bits(int32_t bits) {
   if (bits != 8 && bits != 16) return fail(MOE_ERR_INVALID_ARG, "keep_bits = %d: 8 or 16", bits);
   return MOE_OK;
@@ -602,7 +611,7 @@ int moet_dequantize_a8(int64_t rows, int32_t cols, const int8_t* codes, const ui
 
 int moet_dispatch_rows_backward(const moe_shape* s, const uint16_t* dxp, const int32_t* slot, uint16_t* dx,
                                 void* stream) {
-  TRY(check_shape(s, false));
+  TRY(check_train_shape(s, false));
   if (s->T == 0) return MOE_OK;
   REQUIRE_PTR(dxp);
   REQUIRE_PTR(slot);
@@ -624,7 +633,7 @@ int moet_dispatch_rows_backward(const moe_shape* s, const uint16_t* dxp, const i
 
 int moet_combine_backward(const moe_shape* s, const uint16_t* dy, const uint16_t* Y, const float* weights,
                           const int32_t* slot, uint16_t* dY, float* dweights, void* stream) {
-  TRY(check_shape(s, false));
+  TRY(check_train_shape(s, false));
   if (s->T == 0) return MOE_OK;
   REQUIRE_PTR(dy);
   REQUIRE_PTR(Y);
@@ -643,7 +652,7 @@ int moet_combine_backward(const moe_shape* s, const uint16_t* dy, const uint16_t
 }
 
 size_t moet_expert_ffn_workspace_size(const moe_shape* s) {
-  if (check_shape(s, true) != MOE_OK) return 0;
+  if (check_train_shape(s, true) != MOE_OK) return 0;
   Carve c(nullptr);
   ffn_ws(s, c);
   return c.used + 1024;
@@ -652,7 +661,7 @@ size_t moet_expert_ffn_workspace_size(const moe_shape* s) {
 int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, const uint16_t* w1,
                     const uint16_t* w2, const int32_t* offsets, uint16_t* Y, void* z, uint8_t* z_scales,
                     void* status, void* ws, size_t ws_bytes, void* stream) {
-  TRY(check_shape(s, true));
+  TRY(check_train_shape(s, true));
   TRY(check_bits(keep_bits));
   CHECK_WS(moet_expert_ffn_workspace_size(s), "moet_expert_ffn_workspace_size");
   if (s->T == 0) return MOE_OK;
@@ -676,7 +685,7 @@ int moet_expert_ffn(const moe_shape* s, int32_t keep_bits, const uint16_t* xp, c
 }
 
 size_t moet_expert_ffn_backward_workspace_size(const moe_shape* s) {
-  if (check_shape(s, true) != MOE_OK) return 0;
+  if (check_train_shape(s, true) != MOE_OK) return 0;
   Carve c(nullptr);
   ffn_grad_ws(s, false, c);
   return c.used + 1024;
@@ -686,7 +695,7 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
                              const uint8_t* z_scales, const uint16_t* w1, const uint16_t* w2,
                              const int32_t* offsets, const uint16_t* dY, uint16_t* dxp, uint16_t* dw1,
                              uint16_t* dw2, void* status, void* ws, size_t ws_bytes, void* stream) {
-  TRY(check_shape(s, true));
+  TRY(check_train_shape(s, true));
   TRY(check_bits(keep_bits));
   CHECK_WS(moet_expert_ffn_backward_workspace_size(s), "moet_expert_ffn_backward_workspace_size");
   REQUIRE_PTR(dw1);
@@ -720,7 +729,7 @@ int moet_expert_ffn_backward(const moe_shape* s, int32_t keep_bits, const uint16
 }
 
 size_t moet_router_probs_workspace_size(const moe_shape* s) {
-  if (check_shape(s, false) != MOE_OK) return 0;
+  if (check_train_shape(s, false) != MOE_OK) return 0;
   Carve c(nullptr);
   probs_ws(s, c);
   return c.used + 1024;
@@ -728,7 +737,7 @@ size_t moet_router_probs_workspace_size(const moe_shape* s) {
 
 int moet_router_probs(const moe_shape* s, const uint16_t* x, const uint16_t* w_router, const float* b_router,
                       float* probs, void* status, void* ws, size_t ws_bytes, void* stream) {
-  TRY(check_shape(s, false));
+  TRY(check_train_shape(s, false));
   CHECK_WS(moet_router_probs_workspace_size(s), "moet_router_probs_workspace_size");
   if (b_router && !aligned16(b_router)) return fail(MOE_ERR_INVALID_ARG, "b_router is not 16-byte aligned");
   if (s->T == 0) return MOE_OK;
@@ -745,7 +754,7 @@ int moet_router_probs(const moe_shape* s, const uint16_t* x, const uint16_t* w_r
 }
 
 size_t moet_route_backward_workspace_size(const moe_shape* s) {
-  if (check_shape(s, false) != MOE_OK) return 0;
+  if (check_train_shape(s, false) != MOE_OK) return 0;
   Carve c(nullptr);
   route_grad_ws(s, c);
   return c.used + 1024;
@@ -754,7 +763,7 @@ size_t moet_route_backward_workspace_size(const moe_shape* s) {
 int moet_route_backward(const moe_shape* s, const uint16_t* x, const uint16_t* w_router, const int32_t* ids,
                         const float* weights, const float* probs, const float* dweights, uint16_t* dx,
                         uint16_t* dw_router, float* db, void* status, void* ws, size_t ws_bytes, void* stream) {
-  TRY(check_shape(s, false));
+  TRY(check_train_shape(s, false));
   CHECK_WS(moet_route_backward_workspace_size(s), "moet_route_backward_workspace_size");
   REQUIRE_PTR(dw_router);
   if (db && !aligned16(db)) return fail(MOE_ERR_INVALID_ARG, "db is not 16-byte aligned");
@@ -792,7 +801,7 @@ int moet_route_backward(const moe_shape* s, const uint16_t* x, const uint16_t* w
 }
 
 size_t moet_forward_workspace_size(const moe_shape* s) {
-  if (check_shape(s, true) != MOE_OK) return 0;
+  if (check_train_shape(s, true) != MOE_OK) return 0;
   Carve c(nullptr);
   forward_ws(s, c);
   return c.used + 1024;
@@ -803,7 +812,7 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
                  float* weights, int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* slot, void* z,
                  uint8_t* z_scales, int8_t* xk, uint8_t* xk_scales, float* probs, void* status, void* ws,
                  size_t ws_bytes, void* stream) {
-  TRY(check_shape(s, true));
+  TRY(check_train_shape(s, true));
   TRY(check_bits(keep_bits));
   CHECK_WS(moet_forward_workspace_size(s), "moet_forward_workspace_size");
   REQUIRE_PTR(counts);
@@ -869,7 +878,7 @@ int moet_forward(const moe_shape* s, int32_t keep_bits, const uint16_t* x, const
 }
 
 size_t moet_backward_workspace_size(const moe_shape* s, int32_t keep_bits) {
-  if (check_shape(s, true) != MOE_OK || check_bits(keep_bits) != MOE_OK) return 0;
+  if (check_train_shape(s, true) != MOE_OK || check_bits(keep_bits) != MOE_OK) return 0;
   Carve c(nullptr);
   backward_ws(s, keep_bits, c);
   return c.used + 1024;
@@ -881,7 +890,7 @@ int moet_backward(const moe_shape* s, int32_t keep_bits, const uint16_t* dy, con
                   const int32_t* slot, const void* z, const uint8_t* z_scales, const float* probs,
                   uint16_t* dx, uint16_t* dw_router, float* db, uint16_t* dw1, uint16_t* dw2, void* status,
                   void* ws, size_t ws_bytes, void* stream) {
-  TRY(check_shape(s, true));
+  TRY(check_train_shape(s, true));
   TRY(check_bits(keep_bits));
   CHECK_WS(moet_backward_workspace_size(s, keep_bits), "moet_backward_workspace_size");
   REQUIRE_PTR(dw_router);

@@ -60,6 +60,18 @@ def test_bad_shapes_are_refused(lib, name, kw, code):
     assert lib.moe_last_error_string()
 
 
+@pytest.mark.parametrize("name", list(CALLS) + ["moet_dispatch_rows_backward", "moet_combine_backward"])
+def test_widths_past_the_limits_are_refused(lib, name):
+    mid, n, _ = CALLS.get(name, ((), {"moet_dispatch_rows_backward": 3}.get(name, 6), None))
+    rest = [P(0x1000), P(0x1000), 1 << 62] if name in CALLS else []
+    ffn = "ffn" in name or name in ("moet_forward", "moet_backward")
+    for kw in (dict(H=(1 << 25) + 8), dict(H=2 ** 31 - 8)) + ((dict(F=(1 << 29) + 8), dict(F=2 ** 31 - 8)) if ffn else ()):
+        s = moe.make_shape(**{**SHAPE, **kw})
+        if name in CALLS:
+            assert size_of(lib, name, s) == 0
+        assert getattr(lib, name)(ctypes.byref(s), *mid, *([P(0x1000)] * n), *rest, None) == moe.MOE_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("name", list(CALLS))
 def test_null_misaligned_and_small_buffers_are_refused(lib, name):
     mid, n, optional = CALLS[name]
