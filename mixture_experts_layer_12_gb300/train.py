@@ -158,7 +158,7 @@ class A8Tensor:
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor):
         if codes.dtype != _I8 or scales.dtype != _U8:
             raise TypeError(f"codes must be int8 and scales uint8, got {codes.dtype} and {scales.dtype}")
-        if codes.dim() < 1 or tuple(scales.shape) != (*codes.shape[:-1], -(-codes.shape[-1] // 32)):
+        if codes.dim() < 1 or tuple(scales.shape) != _scales_shape(codes.shape):
             raise ValueError(f"scales {tuple(scales.shape)} do not match codes {tuple(codes.shape)}")
         self.codes, self.scales = codes, scales
 
@@ -167,10 +167,14 @@ class A8Tensor:
         return self.codes.shape
 
 
+def _scales_shape(shape):
+    return *shape[:-1], -(-shape[-1] // 32)
+
+
 def _a8_new(shape, device) -> A8Tensor:
     q = A8Tensor.__new__(A8Tensor)
     q.codes = torch.empty(shape, dtype=_I8, device=device)
-    q.scales = torch.empty((*shape[:-1], -(-shape[-1] // 32)), dtype=_U8, device=device)
+    q.scales = torch.empty(_scales_shape(shape), dtype=_U8, device=device)
     return q
 
 
@@ -209,7 +213,7 @@ def dequantize_a8(q: A8Tensor, out: torch.Tensor | None = None, stream=None) -> 
     dev, raw = _here()
     rows, cols = _matrix(q.shape)
     codes = _addr(q.codes, _I8, "codes", q.codes.numel(), dev)
-    scales = _addr(q.scales, _U8, "scales", q.scales.numel(), dev)
+    scales = _shaped(q.scales, _scales_shape(q.shape), _U8, "scales", dev)
     out = _out(out, q.codes.shape, _BF, "out", dev, q.codes.device)
     rc = _lib().moet_dequantize_a8(rows, cols, codes, scales, out.data_ptr(), raw)
     if rc:
@@ -221,7 +225,7 @@ def _kept_ptrs(z, shape, name: str, dev: int):
     """(keep_bits, address, scales' address) of bf16 values or an A8Tensor."""
     if isinstance(z, A8Tensor):
         a = _shaped(z.codes, shape, _I8, f"{name}.codes", dev)
-        return 8, a, _addr(z.scales, _U8, f"{name}.scales", z.scales.numel(), dev)
+        return 8, a, _shaped(z.scales, _scales_shape(shape), _U8, f"{name}.scales", dev)
     return 16, _shaped(z, shape, _BF, name, dev), None
 
 
@@ -596,8 +600,13 @@ class MoETrainLayer:
         dev, raw = _here()
         wr, w1, w2, _ = self._weights(s, dev)
         g = _shaped(dy, (s.T, s.H), _BF, "dy", dev)
-        bits, zp, zs = _kept_ptrs(saved.z, saved.z.shape, "z", dev)
-        _, xp, xs = _kept_ptrs(saved.x, (s.T, s.H), "x", dev)
+        bits, zp, zs = _kept_ptrs(saved.z, _z_shape(s.T * s.k, s), "z", dev)
+        x_bits, xp, xs = _kept_ptrs(saved.x, (s.T, s.H), "x", dev)
+        if x_bits != bits:
+            raise ValueError(f"z is kept in {bits} bits and x in {x_bits}")
+        probs = None
+        if s.gating == MOE_GATE_SOFTMAX_TOPK:
+            probs = _shaped(saved.probs, (s.T, s.E), _F32, "probs", dev)
         ids, perm, slot, weights, _, offsets = saved._addresses()
         d = dy.device
         ws = c.workspace("moet_backward", d, bits)
@@ -605,10 +614,9 @@ class MoETrainLayer:
                         torch.empty(s.E, dtype=_F32, device=d) if bias_grad else None,
                         torch.empty_like(self.w1), torch.empty_like(self.w2))
         rc = _lib().moet_backward(c.ref, bits, g, xp, xs, wr, w1, w2, ids, weights, offsets, perm, slot, zp, zs,
-                                  None if saved.probs is None else saved.probs.data_ptr(), out.dx.data_ptr(),
-                                  out.dw_router.data_ptr(), None if out.dbias is None else out.dbias.data_ptr(),
-                                  out.dw1.data_ptr(), out.dw2.data_ptr(), self.status.data_ptr(), ws.data_ptr(),
-                                  ws.numel(), raw)
+                                  probs, out.dx.data_ptr(), out.dw_router.data_ptr(),
+                                  None if out.dbias is None else out.dbias.data_ptr(), out.dw1.data_ptr(),
+                                  out.dw2.data_ptr(), self.status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
         if rc:
             _check(rc)
         if raw != saved._stream:  # their memory is the forward's stream's: not before this call has run

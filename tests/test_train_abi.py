@@ -264,6 +264,60 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         moe.quantize_a8(x)
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host tensors, which the calls would pass on")
+def test_kept_tensors_that_were_replaced_are_checked(lib, monkeypatch):
+    """The sizes of what a Saved or an A8Tensor holds are checked by the calls that
+    read them, not only when it is made: smaller ones would be read past their end."""
+    monkeypatch.setattr(train, "_here", lambda: (-1, None))  # host tensors pass for tensors of this device
+    bf, i8, u8 = torch.bfloat16, torch.int8, torch.uint8
+    q = moe.A8Tensor(torch.zeros(6, 64, dtype=i8), torch.zeros(6, 2, dtype=u8))
+    q.scales = q.scales[:3]
+    with pytest.raises(ValueError, match="scales must be"):
+        moe.dequantize_a8(q)
+    w1, w2, o = torch.zeros(2, 32, 64, dtype=bf), torch.zeros(2, 64, 32, dtype=bf), torch.zeros(3, dtype=torch.int32)
+    rows = torch.zeros(6, 32, dtype=bf)
+    with pytest.raises(ValueError, match="z.scales must be"):
+        moe.expert_ffn_backward(rows, q, w1, w2, o, rows)
+
+    layer = object.__new__(moe.MoETrainLayer)
+    layer.E, layer.F, layer.H, layer.k, layer.act, layer.capacity_factor, layer.gating = 2, 64, 32, 2, "gelu", None, 1
+    layer.w_router, layer.w1, layer.w2, layer.bias = torch.zeros(32, 2, dtype=bf), w1, w2, None
+    layer.status = torch.zeros(256, dtype=u8)
+
+    def saved(bits):
+        v = moe.Saved()
+        v.call, v._stream = layer._call(3), None
+        v.x = rows[:3] if bits == 16 else moe.A8Tensor(torch.zeros(3, 32, dtype=i8), torch.zeros(3, 1, dtype=u8))
+        v.z = torch.zeros(6, 64, dtype=bf) if bits == 16 else moe.A8Tensor(torch.zeros(6, 64, dtype=i8),
+                                                                            torch.zeros(6, 2, dtype=u8))
+        v.probs = torch.zeros(3, 2)
+        v._block = torch.zeros(64, dtype=torch.int32)
+        v.versions = layer._versions(v)
+        return v
+
+    dy = rows[3:]
+    for bits in (16, 8):
+        v = saved(bits)
+        v.z = v.z[:5] if bits == 16 else moe.A8Tensor(v.z.codes[:5], v.z.scales[:5])
+        with pytest.raises(ValueError, match="z(.codes)? must be"):
+            layer.backward(v, dy)
+        v = saved(bits)
+        v.probs = v.probs[:2]
+        with pytest.raises(ValueError, match="probs must be"):
+            layer.backward(v, dy)
+        v = saved(bits)
+        v.z = saved(24 - bits).z
+        with pytest.raises(ValueError, match="bits"):
+            layer.backward(v, dy)
+        with pytest.raises(moe.MoEError) as e:  # what was kept goes on to the library, which finds no device
+            layer.backward(saved(bits), dy)
+        assert e.value.code == moe.MOE_ERR_CUDA
+    v = saved(8)
+    v.x.scales = v.x.scales[:2]
+    with pytest.raises(ValueError, match="x.scales must be"):
+        layer.backward(v, dy)
+
+
 def test_sizes_past_32_bits_are_refused(monkeypatch):
     """Not cut to their lower 32 bits (4 rows, 8 columns)."""
     monkeypatch.setattr(train, "_here", lambda: (-1, None))  # tensors without memory, on no device
