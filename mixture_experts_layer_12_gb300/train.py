@@ -619,8 +619,13 @@ class MoETrainLayer:
                                   out.dw2.data_ptr(), self.status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
         if rc:
             _check(rc)
-        if raw != saved._stream:  # their memory is the forward's stream's: not before this call has run
+        # Not given out again before this call has run: what the forward allocated, if that was on another stream, and
+        # x, whatever stream it was made on (it may be saved's alone by now; a no-op on its own stream).
+        held = saved._tensors() if raw != saved._stream else []
+        if bits == 16:
+            held.append(saved.x)
+        if held:
             stream = torch.cuda.current_stream()
-            for t in saved._tensors():
+            for t in held:
                 t.record_stream(stream)
         return out

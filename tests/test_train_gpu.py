@@ -823,6 +823,32 @@ def test_backward_on_another_stream_than_the_forward():
         del junk
 
 
+@pytest.mark.parametrize("forward_beside", [False, True])
+def test_x_that_only_the_forward_still_holds(forward_beside):
+    """x kept as it is (16 bits) and dropped by its maker is what the forward kept
+    as well: not given out again while a backward on another stream than x's reads it."""
+    x, dy, layer = make_layer(48, T=500, H=512, F=128, E=8, k=2)
+    y, saved = layer(x)
+    want = [t.clone() for t in layer.backward(saved, dy, bias_grad=True)]
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        other = x.clone()
+        if not forward_beside:
+            y, saved = layer(other)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            if forward_beside:
+                y, saved = layer(other)
+            torch.cuda._sleep(2_000_000)
+            g = layer.backward(saved, dy, bias_grad=True)
+        del saved, other
+        junk = [torch.full_like(x, 77.0) for _ in range(2)]
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b in zip(want, g):
+            assert bits_equal(a, b)
+        del junk
+
+
 def test_offsets_that_are_no_dispatch_are_an_error():
     """Offsets that run backwards, overlap or pass the rows are cut on the device
     and reported."""
