@@ -189,11 +189,13 @@ int plain_product(const moe_shape* s, const uint16_t* h, const uint16_t* w2, con
   a.out = Y;
   a.ld_out = s->H;
   a.out32 = Y32;
-  const Split sp = row_split(rows, s->E, s->H, s->F);
-  a.splits = sp.parts;
-  a.ksplit = sp.stages;
+  if (Y32) {  // (bf16 outputs are rounded at once: K in one part)
+    const Split sp = row_split(rows, s->E, s->H, s->F);
+    a.splits = sp.parts;
+    a.ksplit = sp.stages;
+  }
   CUDA_TRY(launch_train_gemm(Y32 ? kTrainPlain : kTrainPlainBf16, ta, tb, ta64, a,
-                             row_tiles(rows, s->E, s->H, 256) * (Y32 ? sp.parts : 1), st),
+                             row_tiles(rows, s->E, s->H, 256) * a.splits, st),
            "expert GEMM2 launch");
   return MOE_OK;
 }

@@ -107,10 +107,10 @@ cudaError_t launch_train_gather(const GatherArgs& a, int sms, cudaStream_t st);
 // out[t] = (add ? add[t] : 0) + sum_j (w ? w[t, j] : 1) * rows[slot[t, j]]
 //          + (dl ? sum_j dl[t, j] * wt[ids[t, j]] : 0)
 // (fp32, in that order, j ascending), rounded to bf16 once; rows in bf16 or fp32
-// (both null: none), add in fp32, wt [E, H] bf16.  rows in fp32 may be `splits`
-// parts of T * k rows each, summed in their order.  With `range` (offsets of E
-// segments) slot[t, 0] is t for the rows t inside the segments, and the others
-// are not written.
+// (both null: none), wt [E, H] bf16.  add (fp32) and w go with rows in fp32 only,
+// which may be `splits` parts of T * k rows each, summed in their order.  With
+// `range` (offsets of E segments) slot[t, 0] is t for the rows t inside the
+// segments, and the others are not written.
 struct RowsSumArgs {
   const uint16_t* rows;
   const float* rows32;

@@ -99,11 +99,11 @@ __global__ void __launch_bounds__(GTHREADS) train_gather_kernel(const GatherArgs
 }
 
 // ------------------------------------------------------- sums of a token's rows --
-// out[t] = add[t] + sum_j w[t, j] rows[slot[t, j]]: a thread takes two 8-column
-// chunks of one token (one where rows are in fp32: the same bytes) and asks for
-// all k rows' before the sums.  8192 tokens of 2048 columns, k = 4 with drops: 22 us
-// in bf16 (6.2 TB/s), 34 in fp32 (7.1 TB/s, part of it out of L2), 40 with the
-// router's rows.
+// out[t] = add[t] + sum_j w[t, j] rows[slot[t, j]] (add and w with rows in fp32
+// only): a thread takes two 8-column chunks of one token (one where rows are in
+// fp32: the same bytes) and asks for all k rows' before the sums.  8192 tokens of
+// 2048 columns, k = 4 with drops: 22 us in bf16 (6.2 TB/s), 34 in fp32 (7.1 TB/s,
+// part of it out of L2), 40 with the router's rows.
 constexpr int RTHREADS = 128;
 // The router's part of a token's gradient, k rows of W_router^T out of L2: as a
 // product of its own into an fp32 [T, H] it took 21 us more for 8192 tokens of
@@ -144,13 +144,13 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
   if (col0 >= a.H) return;
   if (PARTS && a.range && (t < __ldg(a.range) || t >= __ldg(a.range + a.E))) return;
   int r[KMAX];
-  float w[KMAX];
+  [[maybe_unused]] float w[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
     r[j] = a.slot && j < a.k ? __ldg(a.slot + (size_t)t * a.k + j) : -1;
     if (r[j] >= a.T * a.k) r[j] = -1;  // slot is not re-validated: nothing outside rows
     if (PARTS && a.range && j == 0) r[j] = t;
-    w[j] = a.w && r[j] >= 0 ? __ldg(a.w + (size_t)t * a.k + j) : 1.0f;
+    if constexpr (F32) w[j] = a.w && r[j] >= 0 ? __ldg(a.w + (size_t)t * a.k + j) : 1.0f;
   }
   if constexpr (F32) {
     float4 v[KMAX][2], s[2];
@@ -197,14 +197,14 @@ __global__ void __launch_bounds__(RTHREADS) rows_sum_kernel(const RowsSumArgs a)
       if (col >= a.H) break;
       float s[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = a.add ? __ldg(a.add + (size_t)t * a.H + col + i) : 0.0f;
+      for (int i = 0; i < 8; ++i) s[i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if (r[j] >= 0) {
           float f[8];
           unpack8(v[j][c], f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = fmaf(w[j], f[i], s[i]);
+          for (int i = 0; i < 8; ++i) s[i] += f[i];
         }
       add_router_rows<KMAX>(a, t, col, s);
       *reinterpret_cast<uint4*>(a.out + (size_t)t * a.H + col) = pack8(s);
