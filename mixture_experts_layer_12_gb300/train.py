@@ -127,6 +127,13 @@ class _Call:
 _call = functools.lru_cache(maxsize=1024)(_Call)
 
 
+@functools.lru_cache(maxsize=64)
+def _current_stream(dev: int, raw: int) -> torch.cuda.Stream:
+    """torch's object for the current stream, whose handle is `raw` (kept, as making
+    one takes longer than the rest of a record_stream: 8 us of a backward's 55)."""
+    return torch.cuda.current_stream(dev)
+
+
 def _out(t, shape, dtype, name: str, dev: int, device) -> torch.Tensor:
     """`t` checked against a shape, or a new tensor of it."""
     if t is None:
@@ -621,11 +628,9 @@ class MoETrainLayer:
             _check(rc)
         # Not given out again before this call has run: what the forward allocated, if that was on another stream, and
         # x, whatever stream it was made on (it may be saved's alone by now; a no-op on its own stream).
-        held = saved._tensors() if raw != saved._stream else []
         if bits == 16:
-            held.append(saved.x)
-        if held:
-            stream = torch.cuda.current_stream()
-            for t in held:
-                t.record_stream(stream)
+            saved.x.record_stream(_current_stream(dev, raw))
+        if raw != saved._stream:
+            for t in saved._tensors():
+                t.record_stream(_current_stream(dev, raw))
         return out
