@@ -131,17 +131,23 @@ int64_t row_tiles(size_t rows, int E, int cols, int per) {
 }
 int64_t blocks256(int n) { return ((int64_t)n + 255) / 256; }
 
+// CTA pairs that plans count on: one per two of the part's 152 SMs.  A number and
+// not the device's count, so that workspace sizes, which are asked for without a
+// device, and the order of sums depend on the shape alone; where fewer pairs are
+// resident, what was planned as one round of tiles takes two.
+constexpr int kPlanPairs = 76;
+
 // Parts of K for a product whose fp32 outputs are summed afterwards anyway: few
 // rows leave most CTA pairs without a tile, and a long K then takes its time on a
-// few of them (3 rows of 3 experts of 576 x 14096: 73 us).  At least eight stages a
-// part, at most eight parts, and together no more tiles than there are pairs.
+// few of them (3 rows of 3 experts of 576 x 14096: 73 us).  At most `most` parts of
+// at least `least` stages, and together no more tiles than pairs.
 struct Split {
   int parts, stages;
 };
 Split split_of(int64_t blocks, int cols, int K, int most, int least) {
   const int kb = (K + 63) / 64;
   const int64_t tiles = blocks * ((cols + 255) / 256);
-  int64_t S = tiles > 0 ? 76 / tiles : 1;
+  int64_t S = tiles > 0 ? kPlanPairs / tiles : 1;
   if (S > most) S = most;
   if (S > kb / least) S = kb / least;
   if (S < 1) S = 1;
@@ -150,6 +156,8 @@ Split split_of(int64_t blocks, int cols, int K, int most, int least) {
   p.parts = (kb + p.stages - 1) / p.stages;
   return p;
 }
+// Products whose rows are summed by token: 8 parts of 8 stages or more (the sum
+// reads every part).
 Split row_split(size_t rows, int E, int cols, int K) {
   const int64_t n = (int64_t)rows, hit = n < E ? n : E;
   return split_of(hit > 0 ? hit * (((n + hit - 1) / hit + 255) / 256) : 0, cols, K, 8, 8);
@@ -286,12 +294,12 @@ int ffn_gradients(const moe_shape* s, const FfnGrad& f, void* status, cudaStream
   return MOE_OK;
 }
 
-// Splits of the router's weight gradient along the tokens: as many as give
-// every CTA pair of the device a tile, but at least 256 tokens each (its fp32
-// partial outputs are written and read again).
+// Splits of the router's weight gradient along the tokens: as many as give every
+// CTA pair a tile, but at least 256 tokens each (its fp32 partial outputs are
+// written and read again).
 int router_chunk(const moe_shape* s) {
   const int64_t tiles = blocks256(s->H) * blocks256(2 * ep_of(s));
-  int64_t S = 76 / tiles;
+  int64_t S = kPlanPairs / tiles;
   if (S > s->T / 256) S = s->T / 256;
   if (S < 1) S = 1;
   if (S > kMaxExperts) S = kMaxExperts;
@@ -395,7 +403,8 @@ GateBackwardArgs gate_args(const moe_shape* s, const RouteGradWs& r, const uint1
   return g;
 }
 
-// (one wave of 8 tiles with K = 4096 took 28 us, 11 in parts)
+// The router's logits, few columns: up to 64 parts of 4 stages or more (one wave
+// of 8 tiles with K = 4096 took 28 us, 11 in parts).
 Split probs_split(const moe_shape* s) {
   return split_of(blocks256(s->T), ep_of(s), s->H, 64, 4);
 }
