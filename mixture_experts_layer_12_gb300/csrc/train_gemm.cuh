@@ -14,7 +14,9 @@
 // 128 rows of A and 128 columns of B per 64-deep stage, five or six stages fed by
 // one TMA thread, one MMA thread in the leader, and an epilogue double-buffered
 // against the next tile.  8192 rows of 8 experts of 4096 x 14336: 600-625 us each
-// of the six products, 1.54-1.60 PFLOP/s; without any epilogue 2-5% less: the rest
+// of the six products while the card is cool, 1.54-1.60 PFLOP/s (back to back under
+// the power cap 1.35: the four of a backward and their row copies 2840-2910 us);
+// without any epilogue 2-5% less: the rest
 // is the main loop, 0.38 us a stage where the MMAs alone would take 0.27, with
 // shared memory filled and read at its rate meanwhile (a quarter less to read out
 // of L2, A shared by two pairs through multicast, changed nothing).  What differs
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(T_THREADS, 1)
         if (idle) {
           // an expert without rows: its matrix is one block of memory, of which
           // this tile clears a part in whole lines (36 experts of 2872 x 9480 by
-          // tiles, whose rows start inside a sector: 817 us, so 420)
+          // tiles, whose rows start inside a sector: 817 us, so 320-342)
           const int64_t all = (int64_t)p.M * p.N / 8;
           const int cnt = c.tile_start[t.e + 1] - c.tile_start[t.e], at = tile - c.tile_start[t.e];
           const int64_t lo = all * at / cnt, hi = all * (at + 1) / cnt;
