@@ -688,6 +688,36 @@ def test_captured_steps_replayed_with_other_inputs():
                 assert bits_equal(a, b)
 
 
+def test_captured_step_that_holds_x_in_16_bits():
+    """x from outside the capture and x made inside it, dropped there and later."""
+    x, dy, layer = make_layer(49, T=90, H=128, F=96, E=8, k=2)
+    x2 = (x * 1.5).contiguous()
+    wants = []
+    for a in (x, x2):
+        y, s = layer(a)
+        wants.append([t.clone() for t in all_of(y, s, layer.backward(s, dy, bias_grad=True))])
+    xb = x.clone()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        y, s = layer(xb)
+        outside = all_of(y, s, layer.backward(s, dy, bias_grad=True))
+        inner = xb * 1.5
+        y1, s1 = layer(inner)
+        del inner
+        inside = all_of(y1, s1, layer.backward(s1, dy, bias_grad=True))
+    for _ in range(2):
+        gr.replay()
+        torch.cuda.synchronize()
+        for want, got in zip(wants, (outside, inside)):
+            for a, b in zip(want, got):
+                assert bits_equal(a, b)
+    del gr, y, s, y1, s1, outside, inside, xb
+    junk = [torch.empty_like(x) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_status(layer.status) == 0
+    del junk
+
+
 def test_single_steps_make_the_layers_gradients():
     """dispatch -> expert FFN -> combine and back by the single steps, as a program
     that moves rows between ranks runs them, against the layer's own calls."""
